@@ -122,6 +122,75 @@ int pa_write_kv(const void *k, const void *v, const int64_t *slot_mapping, int32
                 const pa_kv_desc *kv, void *stream);
 
 /*
+ * Rotary position embedding with several axes, fused with the cache write:
+ * q rows are rotated into q_out, k rows are rotated into their slots, v rows
+ * are copied into theirs, in one pass over the step's new rows.  (The
+ * embedding precedes reshape_and_cache: the cache holds rotated keys.)
+ *
+ * A head's first rot_dim elements form rot_dim / 2 pairs; frequency i turns
+ * pair i = (a, b) by the angle t = positions[axis[i]][token] * inv_freq[i]:
+ *   a' = f (a cos t - b sin t),  b' = f (b cos t + a sin t),  f = attn_factor
+ * pair i is elements (i, i + rot_dim / 2), or (2 i, 2 i + 1) with `adjacent`.
+ * Elements from rot_dim on are copied.  One axis gives the plain rotary
+ * embedding of text; three (time, height, width) serve images and video,
+ * with any assignment of frequencies to axes.
+ *
+ * The angle is reduced exactly: position and inv_freq / 2 pi meet in 64-bit
+ * integer arithmetic, so far positions lose nothing.  The rotation runs in
+ * fp32 and is rounded once: to bf16 for q_out and a bf16 pool, and for an
+ * e4m3 pool straight to the code of (rotated x) / k_scale[h], as pa_write_kv
+ * rounds, without a bf16 step in between.
+ *
+ *   q, k, v       bf16 [num_tokens][heads][head_dim], token rows q_stride,
+ *                 k_stride, v_stride elements apart (multiples of 8, so the
+ *                 three may be slices of one fused projection), 16-B aligned
+ *   positions     int32 [num_axes][num_tokens], any value
+ *   slot_mapping  int64 [num_tokens], rules of pa_write_kv: a negative slot
+ *                 skips the token's k and v (its q is rotated all the same),
+ *                 a slot beyond the pool flags PA_DEV_BAD_SLOT
+ *   q_out         bf16 [num_tokens][num_q_heads][head_dim], 16-B aligned; it
+ *                 may be q itself (q_stride = num_q_heads * head_dim), and
+ *                 must not overlap any input otherwise
+ * num_q_heads may be 0 (q and q_out are then ignored).
+ */
+typedef struct pa_rope_desc {
+    const double *inv_freq;  /* device fp64 [rot_dim / 2], finite, radians per position */
+    const int32_t *axis;     /* device int32 [rot_dim / 2] in [0, num_axes); NULL: all 0.
+                              * A value outside is clamped and flags PA_DEV_BAD_METADATA */
+    int32_t rot_dim;         /* a multiple of 16, 16 .. head_dim */
+    int32_t num_axes;        /* 1 .. 8 */
+    int32_t adjacent;        /* 0 or 1 */
+    float attn_factor;       /* scales cos and sin (1 for none) */
+} pa_rope_desc;
+int pa_rope_write_kv(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                     const void *v, int64_t v_stride, const int32_t *positions,
+                     const pa_rope_desc *rope, const int64_t *slot_mapping, int32_t num_tokens,
+                     int32_t num_q_heads, const pa_kv_desc *kv, void *q_out, void *stream);
+
+/*
+ * Copies physical blocks, in every layer's pool: for each pair (src, dst),
+ * every kv head's block_size rows of K and of V of block src become those of
+ * block dst, bit for bit.  The copies of pa_bm_schedule (copy-on-write after
+ * a fork) and the moves of pa_bm_compact (pa_blocks.h) are such pairs.
+ *   kv         HOST array of num_layers descriptors of one geometry and
+ *              element type (the layers of a model; scales are not read and
+ *              may be NULL: a code keeps its meaning within its layer)
+ *   pairs      int32 [num_pairs][2] (src, dst)
+ * A dst appears once and is no other pair's src; a src may repeat.
+ * pa_validate_copies checks that on the host.  A pair with a negative id is
+ * padding and skipped (so one CUDA graph serves any smaller number of
+ * copies), as is src == dst; an id beyond the pool skips the pair and flags
+ * PA_DEV_BAD_BLOCK.
+ */
+int pa_copy_blocks(const pa_kv_desc *kv, int32_t num_layers, const int32_t *pairs,
+                   int32_t num_pairs, void *stream);
+
+/* Host-side check of pa_copy_blocks' pairs (HOST pointer): ids below
+ * num_blocks, each dst once and no other pair's src.  Returns PA_OK or
+ * PA_ERR_BAD_METADATA. */
+int pa_validate_copies(const int32_t *pairs, int32_t num_pairs, int32_t num_blocks);
+
+/*
  * Workspace bytes pa_attention / pa_attention_ex need for a step with these
  * sizes (independent of the lengths in the metadata).  The workspace holds
  * the device-built work list, split-KV partial states and completion
@@ -210,6 +279,29 @@ int pa_attention_ex(const void *q, const pa_kv_desc *kv, const int32_t *block_ta
                     int32_t num_q_tokens, int32_t num_q_heads, float scale, void *out, float *lse,
                     void *workspace, size_t workspace_bytes, int32_t short_q_max_rows,
                     int32_t split_keys, void *stream);
+
+/*
+ * pa_attention with a sliding window and sinks: query row i of request b (at
+ * position p = context_lens[b] + i) attends key j <= p if j > p - window (the
+ * last `window` keys, its own included) or j < num_sinks (the first tokens of
+ * the request, which stay visible).  Everything else is as in pa_attention:
+ * arguments, batches, empty and padding requests, workspace size, staging
+ * room of an e4m3 pool, errors.  window >= 1, num_sinks >= 0, scale > 0;
+ * max_blocks_per_seq * block_size must not exceed 2^30.
+ *
+ * Work and traffic go by the visible keys, not by seq_lens.  A block of which
+ * no row of its request sees a key is neither read nor looked up: its table
+ * entry may hold anything (pa_bm_release_window gives such blocks back and
+ * leaves -1), and keys that no row of the request sees may hold anything,
+ * even NaN.  Keys that one row sees and another does not must be finite.
+ * pa_fp8_staging_bytes counts a long request's visible blocks only.
+ */
+int pa_window_attention(const void *q, const pa_kv_desc *kv, const int32_t *block_tables,
+                        int32_t max_blocks_per_seq, const int32_t *query_start_loc,
+                        const int32_t *context_lens, const int32_t *seq_lens, int32_t num_seqs,
+                        int32_t num_q_tokens, int32_t num_q_heads, float scale, int32_t window,
+                        int32_t num_sinks, void *out, float *lse, void *workspace,
+                        size_t workspace_bytes, void *stream);
 
 /*
  * Merge operator of cascade inference ([AI] §02.1): combine two attention
@@ -318,6 +410,14 @@ int pa_validate_metadata(const int32_t *block_tables, int32_t max_blocks_per_seq
                          const int32_t *query_start_loc, const int32_t *context_lens,
                          const int32_t *seq_lens, int32_t num_seqs, int32_t num_q_tokens,
                          const int64_t *slot_mapping, int32_t num_blocks, int32_t block_size);
+
+/* pa_validate_metadata for pa_window_attention: only the blocks of which some
+ * row of the request sees a key need a valid id. */
+int pa_validate_window_metadata(const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                const int32_t *query_start_loc, const int32_t *context_lens,
+                                const int32_t *seq_lens, int32_t num_seqs, int32_t num_q_tokens,
+                                int32_t window, int32_t num_sinks, const int64_t *slot_mapping,
+                                int32_t num_blocks, int32_t block_size);
 
 /* Reason for the last PA_ERR_* returned on this host thread ("" if none). */
 const char *pa_last_error_message(void);

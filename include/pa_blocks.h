@@ -34,7 +34,8 @@
  *  - Copy-on-write: before a request writes into a partially filled block
  *    that other requests also reference (after pa_bm_fork), the block is
  *    replaced in its table by a fresh copy; the copy (src -> dst physical
- *    block) is reported to the caller, who copies the K/V bytes.
+ *    block) is reported to the caller, who copies the K/V bytes
+ *    (pa_copy_blocks).
  *
  * Errors: every call returns PA_OK (0) or a PA_ERR_* code (pa.h); on an
  * error nothing changes.  PA_ERR_WORKSPACE here means "not enough free
@@ -98,6 +99,31 @@ int pa_bm_schedule(pa_block_manager *bm, int32_t num_reqs, const int64_t *req_id
 /* Finish a request: its blocks are released (last block first); cached
  * blocks stay matchable until evicted, others become free. */
 int pa_bm_free_request(pa_block_manager *bm, int64_t req_id);
+
+/*
+ * Give back the blocks of a request that no later row of it can see under
+ * pa_window_attention(window, num_sinks): every block that ends at or before
+ * position (computed tokens) - window + 1 and starts at or after num_sinks.
+ * Their table entries become -1 (in the tables of later steps too), their
+ * references drop by one: a block that others reference stays theirs, a
+ * cached one stays matchable until evicted, any other becomes free.  Blocks
+ * are released last to first.  window >= 1, num_sinks >= 0; *num_released
+ * (optional) receives the number given back by this call.
+ * PA_ERR_WORKSPACE: out of host memory.
+ */
+int pa_bm_release_window(pa_block_manager *bm, int64_t req_id, int32_t window,
+                         int32_t num_sinks, int32_t *num_released);
+
+/*
+ * Compact the pool: moves the used blocks (referenced or cached) with the
+ * highest ids into the free blocks with the lowest ids until the used blocks
+ * are 0 .. used - 1 or max_moves moves are made.  moves (int32
+ * [max_moves][2], (src, dst)) are for pa_copy_blocks, before the next step
+ * reads the pool; *num_moves receives their count.  Tables, reference counts
+ * and the prefix cache follow at once.  No dst is another move's src.
+ * PA_ERR_WORKSPACE: out of host memory.
+ */
+int pa_bm_compact(pa_block_manager *bm, int32_t max_moves, int32_t *moves, int32_t *num_moves);
 
 /* Introspection (tests, schedulers). */
 int32_t pa_bm_num_free_blocks(const pa_block_manager *bm);      /* free + evictable */

@@ -105,7 +105,8 @@ class BlockManagerModel:
         r = Request(s.tokens)
         r.computed, r.table = s.computed, list(s.table)
         for b in r.table:
-            self.ref[b] += 1
+            if b >= 0:
+                self.ref[b] += 1
         self.reqs[dst] = r
         return OK
 
@@ -113,9 +114,44 @@ class BlockManagerModel:
         if rid not in self.reqs:
             return INVALID
         for b in reversed(self.reqs[rid].table):
-            self.release(b)
+            if b >= 0:
+                self.release(b)
         del self.reqs[rid]
         return OK
+
+    def release_window(self, rid, window, sinks):
+        """Returns (code, number of blocks given back): blocks whose every
+        position is neither a sink nor within the window of the next row."""
+        if rid not in self.reqs or window < 1 or sinks < 0:
+            return INVALID, 0
+        r, n = self.reqs[rid], 0
+        for j in reversed(range(len(r.table))):
+            hidden = all(p >= sinks and p <= r.computed - window
+                         for p in range(j * self.bs, (j + 1) * self.bs))
+            if hidden and r.table[j] >= 0:
+                self.release(r.table[j])
+                r.table[j] = -1
+                n += 1
+        return OK, n
+
+    def compact(self, max_moves):
+        """Highest used block to the lowest free one while that lowers it."""
+        moves = []
+        while len(moves) < max_moves:
+            free = self.free_blocks()
+            used = [b for b in range(self.n) if b not in free]
+            if not free or not used or max(used) < min(free):
+                break
+            src, dst = max(used), min(free)
+            moves.append((src, dst))
+            for field in (self.ref, self.key, self.released):
+                field[dst] = field[src]
+            self.ref[src], self.key[src], self.released[src] = 0, None, 0
+            if self.key[dst] is not None:
+                self.cache[self.key[dst]] = dst
+            for r in self.reqs.values():
+                r.table = [dst if b == src else b for b in r.table]
+        return moves
 
     def schedule(self, rids, num_new, max_blocks, max_copies):
         """Returns (code, metadata dict or None)."""

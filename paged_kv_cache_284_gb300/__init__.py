@@ -14,6 +14,10 @@ Calls (same names as the C ABI):
   pa_merge_states      the cascade merge operator
   pa_prefix_attention  cascade shared-prefix (multi-query) pass
   pa_cascade_decode    prefix pass + suffix decode + merge in one call
+  pa_window_attention  pa_attention with a sliding window and sinks
+  pa_rope_write_kv     rotary positions (several axes) on q and k, and the
+                       cache write, in one pass
+  pa_copy_blocks       block copies (copy-on-write, compaction) in all layers
 """
 from __future__ import annotations
 
@@ -42,7 +46,10 @@ EXPORTED = ["pa_write_kv", "pa_attention_workspace_size", "pa_attention", "pa_at
             "pa_bm_fork", "pa_bm_schedule", "pa_bm_free_request", "pa_bm_num_free_blocks",
             "pa_bm_num_cached_blocks", "pa_bm_block_ref_count", "pa_bm_request_blocks",
             "pa_bm_num_computed",
+            "pa_bm_release_window", "pa_bm_compact",
             "pa_set_test_stall", "pa_set_tile_counter",
+            "pa_window_attention", "pa_validate_window_metadata", "pa_rope_write_kv",
+            "pa_copy_blocks", "pa_validate_copies",
             # request router for sharded replicas (include/pa_shard.h)
             "pa_partition_requests"]
 PA_KERNEL_WRITE_KV, PA_KERNEL_PLAN, PA_KERNEL_SPLIT_KV, PA_KERNEL_TENSOR_CORE = range(4)
@@ -67,6 +74,12 @@ class KVDesc(ctypes.Structure):
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("kv_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("axis", ctypes.c_void_p),
+                ("rot_dim", ctypes.c_int32), ("num_axes", ctypes.c_int32),
+                ("adjacent", ctypes.c_int32), ("attn_factor", ctypes.c_float)]
 
 
 def _declare(lib):
@@ -111,6 +124,16 @@ def _declare(lib):
         "pa_bm_request_blocks": ([P, i64, P, i32], i32),
         "pa_bm_num_computed": ([P, i64], i32),
         "pa_partition_requests": ([P, i32, i32, P, P], ctypes.c_int),
+        "pa_bm_release_window": ([P, i64, i32, i32, P], ctypes.c_int),
+        "pa_bm_compact": ([P, i32, P, P], ctypes.c_int),
+        "pa_window_attention": ([P, KV, P, i32, P, P, P, i32, i32, i32, f32, i32, i32, P, P, P, sz,
+                                 P], ctypes.c_int),
+        "pa_validate_window_metadata": ([P, i32, P, P, P, i32, i32, i32, i32, P, i32, i32],
+                                        ctypes.c_int),
+        "pa_rope_write_kv": ([P, i64, P, i64, P, i64, P, ctypes.POINTER(RopeDesc), P, i32, i32, KV,
+                              P, P], ctypes.c_int),
+        "pa_copy_blocks": ([KV, i32, P, i32, P], ctypes.c_int),
+        "pa_validate_copies": ([P, i32, i32], ctypes.c_int),
         "pa_set_test_stall": ([i32], ctypes.c_int),
         "pa_set_tile_counter": ([P], ctypes.c_int),
     }
@@ -306,6 +329,173 @@ def pa_write_kv_attention(k, v, slot_mapping, q, k_cache, v_cache, block_tables,
     return workspace
 
 
+def _same_device(device: torch.device, tensors):
+    """The calls run on the current device: every tensor must live there."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    for name, t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def pa_window_attention(q, k_cache, v_cache, block_tables, query_start_loc, context_lens, seq_lens,
+                        scale, window, num_sinks, out, lse=None, workspace=None, stream=None,
+                        k_scale=None, v_scale=None, staging_blocks=0):
+    """pa_attention with a sliding window and sinks: the row at position p sees
+    key j <= p if j > p - window or j < num_sinks.  Arguments, workspace and
+    e4m3 pools as in pa_attention; blocks of which no row of their request
+    sees a key may have any table entry (staging_blocks counts the visible
+    blocks of the long requests).  Returns the workspace tensor used."""
+    _need(q, "q", torch.bfloat16)
+    _need(out, "out", torch.bfloat16)
+    for name, t in (("block_tables", block_tables), ("query_start_loc", query_start_loc),
+                    ("context_lens", context_lens), ("seq_lens", seq_lens)):
+        _need(t, name, torch.int32)
+    if lse is not None:
+        _need(lse, "lse", torch.float32)
+    kv = kv_desc(k_cache, v_cache, k_scale, v_scale)
+    T, hq, d = q.shape
+    B = int(seq_lens.shape[0])
+    if d != kv.head_dim or out.shape != q.shape or (lse is not None and lse.shape != q.shape[:2]):
+        raise ValueError("q and out must be [T, Hq, head_dim], lse [T, Hq]")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape[0] != B or \
+            query_start_loc.shape[0] != B + 1:
+        raise ValueError("block_tables [B, N], query_start_loc [B + 1], context_lens [B] and "
+                         "seq_lens [B] must agree")
+    _same_device(q.device, (("out", out), ("lse", lse), ("k_cache", k_cache),
+                            ("v_cache", v_cache), ("block_tables", block_tables),
+                            ("query_start_loc", query_start_loc), ("context_lens", context_lens),
+                            ("seq_lens", seq_lens), ("k_scale", k_scale), ("v_scale", v_scale),
+                            ("workspace", workspace)))
+    need = workspace_size(B, T, hq, kv.num_kv_heads, kv.head_dim)
+    if kv.kv_dtype == PA_KV_FP8_E4M3 and staging_blocks > 0:
+        need += fp8_staging_bytes(kv.num_kv_heads, kv.head_dim, kv.block_size, staging_blocks)
+    if workspace is None or workspace.numel() < need:
+        workspace = alloc_workspace(need, q.device)
+    _check(lib().pa_window_attention(_ptr(q), ctypes.byref(kv), _ptr(block_tables),
+                                     int(block_tables.shape[1]), _ptr(query_start_loc),
+                                     _ptr(context_lens), _ptr(seq_lens), B, T, hq, float(scale),
+                                     int(window), int(num_sinks), _ptr(out), _ptr(lse),
+                                     _ptr(workspace), workspace.numel(), _stream(stream)),
+           "pa_window_attention")
+    return workspace
+
+
+def _token_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between the token rows of a [T, H, d] tensor whose rows are
+    contiguous (a slice of a fused projection, or a whole tensor)."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} must be [T, H, d] with contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def pa_rope_write_kv(q, k, v, positions, inv_freq, axis, slot_mapping, k_cache, v_cache, q_out,
+                     adjacent=False, attn_factor=1.0, stream=None, k_scale=None, v_scale=None):
+    """Rotary positions on q (into q_out) and k, and the cache write of k and v,
+    in one pass.  q [T, Hq, d], k and v [T, Hkv, d] bf16, token rows at any
+    stride that is a multiple of 8; positions int32 [axes, T] (or [T] for
+    one axis); inv_freq float64 [rot_dim / 2]; axis int32 [rot_dim / 2], the
+    axis of each frequency, or None for axis 0; q_out bf16 [T, Hq, d] (may be
+    a contiguous q).  q and q_out may both be None."""
+    if positions.dim() == 1:
+        positions = positions[None]
+    T = int(k.shape[0])
+    ks, vs = _token_stride(k, "k"), _token_stride(v, "v")
+    hq, qs = 0, 0
+    if q is not None:
+        qs, hq = _token_stride(q, "q"), int(q.shape[1])
+        _need(q_out, "q_out", torch.bfloat16)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _need(positions, "positions", torch.int32)
+    _need(slot_mapping, "slot_mapping", torch.int64)
+    _need(inv_freq, "inv_freq", torch.float64)
+    if axis is not None:
+        _need(axis, "axis", torch.int32)
+        if axis.numel() != inv_freq.numel():
+            raise ValueError("axis and inv_freq must have one entry per frequency")
+    kv = kv_desc(k_cache, v_cache, k_scale, v_scale)
+    if k.shape != v.shape or k.shape[1] != kv.num_kv_heads or k.shape[2] != kv.head_dim or \
+            (q is not None and (q.shape[0] != T or q.shape[2] != kv.head_dim)):
+        raise ValueError("k and v must be [T, num_kv_heads, head_dim], q [T, Hq, head_dim]")
+    if positions.dim() != 2 or positions.shape[1] != T or slot_mapping.numel() != T:
+        raise ValueError("positions must be [axes, T], slot_mapping [T]")
+    _same_device(k.device, (("q", q), ("v", v), ("positions", positions), ("inv_freq", inv_freq),
+                            ("axis", axis), ("slot_mapping", slot_mapping), ("k_cache", k_cache),
+                            ("v_cache", v_cache), ("q_out", q_out), ("k_scale", k_scale),
+                            ("v_scale", v_scale)))
+    rope = RopeDesc(inv_freq.data_ptr(), None if axis is None else axis.data_ptr(),
+                    2 * inv_freq.numel(), int(positions.shape[0]), 1 if adjacent else 0,
+                    float(attn_factor))
+    _check(lib().pa_rope_write_kv(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(positions),
+                                  ctypes.byref(rope), _ptr(slot_mapping), T, hq, ctypes.byref(kv),
+                                  _ptr(q_out), _stream(stream)), "pa_rope_write_kv")
+
+
+class KVLayers:
+    """The pools of a model's layers, for pa_copy_blocks (see kv_layers)."""
+
+    def __init__(self, descs, tensors):
+        self.descs = descs
+        self.tensors = tensors  # keeps the pools alive
+        self.device = tensors[0].device if tensors else None
+
+    def __len__(self):
+        return len(self.descs)
+
+
+def kv_layers(k_caches, v_caches) -> KVLayers:
+    """Descriptors of the layers' pools (lists of k_cache and v_cache tensors of
+    one shape and type), made once and kept by the program."""
+    k_caches, v_caches = list(k_caches), list(v_caches)
+    if len(k_caches) != len(v_caches):
+        raise ValueError("as many k_caches as v_caches are needed")
+    descs = (KVDesc * len(k_caches))()
+    for i, (k, v) in enumerate(zip(k_caches, v_caches)):
+        fp8 = k.dtype in _FP8_DTYPES
+        for name, t in (("k_cache", k), ("v_cache", v)):
+            if t.dtype != k.dtype or not (fp8 or t.dtype == torch.bfloat16):
+                raise TypeError(f"{name} must be bf16, or uint8 / float8_e4m3fn codes")
+            if not t.is_contiguous() or not t.is_cuda:
+                raise ValueError(f"{name} must be a contiguous CUDA tensor")
+            if t.dim() != 4 or t.shape != k_caches[0].shape or t.dtype != k_caches[0].dtype or \
+                    t.device != k_caches[0].device:
+                raise ValueError("the layers' pools must all be alike, "
+                                 "[num_blocks, num_kv_heads, block_size, head_dim]")
+        nb, hkv, bs, d = k.shape
+        descs[i] = KVDesc(k.data_ptr(), v.data_ptr(), nb, bs, hkv, d,
+                          PA_KV_FP8_E4M3 if fp8 else PA_KV_BF16, 0, None, None)
+    return KVLayers(descs, k_caches + v_caches)
+
+
+def pa_copy_blocks(layers: KVLayers, pairs, stream=None):
+    """Copy physical blocks in every layer: pairs int32 [n, 2] of (src, dst) on
+    the device (BlockManager.schedule's copies, BlockManager.compact's moves).
+    A dst appears once and is no other pair's src; negative ids are padding."""
+    _need(pairs, "pairs", torch.int32)
+    if pairs.dim() != 2 or pairs.shape[1] != 2:
+        raise ValueError("pairs must be [n, 2]")
+    if len(layers) == 0:
+        return
+    _same_device(layers.device, (("pairs", pairs),))
+    _check(lib().pa_copy_blocks(layers.descs, len(layers), _ptr(pairs), int(pairs.shape[0]),
+                                _stream(stream)), "pa_copy_blocks")
+
+
+def pa_validate_copies(pairs, num_blocks):
+    """Host-side check of pa_copy_blocks' pairs.  Raises PaError on a problem."""
+    p = torch.as_tensor(pairs, dtype=torch.int32).detach().cpu().contiguous()
+    _check(lib().pa_validate_copies(_ptr(p) if p.numel() else None, int(p.shape[0]),
+                                    int(num_blocks)), "pa_validate_copies")
+
+
 def pa_merge_states(o_a, lse_a, o_b, lse_b, out, lse_out=None, stream=None):
     for name, t in (("o_a", o_a), ("o_b", o_b), ("out", out)):
         _need(t, name, torch.bfloat16)
@@ -363,14 +553,22 @@ def pa_cascade_decode(q, k_cache, v_cache, prefix_blocks, prefix_len, block_tabl
 
 
 def pa_validate_metadata(block_tables, query_start_loc, context_lens, seq_lens, num_blocks,
-                         block_size, slot_mapping=None):
-    """Host-side metadata check (CPU tensors).  Raises PaError on a problem."""
+                         block_size, slot_mapping=None, window=None, num_sinks=0):
+    """Host-side metadata check (CPU tensors).  Raises PaError on a problem.
+    With a window it checks a pa_window_attention step: only the visible
+    blocks' ids."""
     bt = block_tables.detach().cpu().to(torch.int32).contiguous()
     qsl = query_start_loc.detach().cpu().to(torch.int32).contiguous()
     ctx = context_lens.detach().cpu().to(torch.int32).contiguous()
     sl = seq_lens.detach().cpu().to(torch.int32).contiguous()
     sm = None if slot_mapping is None else slot_mapping.detach().cpu().to(torch.int64).contiguous()
     T = int(qsl[-1]) if qsl.numel() else 0
+    if window is not None:
+        _check(lib().pa_validate_window_metadata(
+            _ptr(bt), int(bt.shape[1]), _ptr(qsl), _ptr(ctx), _ptr(sl), int(sl.shape[0]), T,
+            int(window), int(num_sinks), _ptr(sm), int(num_blocks), int(block_size)),
+            "pa_validate_window_metadata")
+        return
     _check(lib().pa_validate_metadata(_ptr(bt), int(bt.shape[1]), _ptr(qsl), _ptr(ctx), _ptr(sl),
                                       int(sl.shape[0]), T, _ptr(sm), int(num_blocks),
                                       int(block_size)), "pa_validate_metadata")

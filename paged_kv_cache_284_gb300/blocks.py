@@ -61,6 +61,25 @@ class BlockManager:
     def free_request(self, req_id: int):
         self._check(lib().pa_bm_free_request(self._h, int(req_id)), "pa_bm_free_request")
 
+    def release_window(self, req_id: int, window: int, num_sinks: int) -> int:
+        """Give back the blocks no later row of the request can see under
+        pa_window_attention(window, num_sinks); returns how many."""
+        n = ctypes.c_int32(0)
+        self._check(lib().pa_bm_release_window(self._h, int(req_id), int(window), int(num_sinks),
+                                               ctypes.byref(n)), "pa_bm_release_window")
+        return n.value
+
+    def compact(self, max_moves: Optional[int] = None) -> np.ndarray:
+        """Move the used blocks to the pool's lower end; returns the (src, dst)
+        moves, which pa_copy_blocks has to make before the next step."""
+        if max_moves is None:
+            max_moves = self.num_blocks
+        moves = np.empty((max(int(max_moves), 1), 2), np.int32)
+        n = ctypes.c_int32(0)
+        self._check(lib().pa_bm_compact(self._h, int(max_moves), _ptr(moves), ctypes.byref(n)),
+                    "pa_bm_compact")
+        return moves[:n.value].copy()
+
     def schedule(self, req_ids: Sequence[int], num_new: Sequence[int], max_blocks_per_seq: int,
                  max_copies: Optional[int] = None) -> Dict[str, np.ndarray]:
         """One step's metadata: block_tables, query_start_loc, context_lens,

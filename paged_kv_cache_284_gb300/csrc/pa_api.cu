@@ -213,7 +213,8 @@ WsLayout make_layout(int num_seqs, int num_q_tokens, int num_q_heads, int num_kv
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-int check_kv(const pa_kv_desc *kv) {
+// need_scales: false for calls that move codes without their values.
+int check_kv(const pa_kv_desc *kv, bool need_scales = true) {
     if (!kv) return fail(PA_ERR_INVALID_ARG, "kv descriptor is NULL");
     if (!kv->k_cache || !kv->v_cache) return fail(PA_ERR_INVALID_ARG, "cache pointer is NULL");
     if (!aligned(kv->k_cache, 16) || !aligned(kv->v_cache, 16))
@@ -229,7 +230,8 @@ int check_kv(const pa_kv_desc *kv) {
     if (kv->kv_dtype == PA_KV_FP8_E4M3) {
         if (kv->head_dim != 128)
             return fail(PA_ERR_UNSUPPORTED, "fp8 KV pool: head_dim %d not built (128)", kv->head_dim);
-        if (!kv->k_scale || !kv->v_scale || !aligned(kv->k_scale, 4) || !aligned(kv->v_scale, 4))
+        if (need_scales &&
+            (!kv->k_scale || !kv->v_scale || !aligned(kv->k_scale, 4) || !aligned(kv->v_scale, 4)))
             return fail(PA_ERR_INVALID_ARG, "fp8 KV pool needs 4-byte aligned k_scale and v_scale");
     } else if (kv->kv_dtype != PA_KV_BF16) {
         return fail(PA_ERR_UNSUPPORTED, "kv_dtype %d unknown", kv->kv_dtype);
@@ -433,6 +435,19 @@ int check_new_rows(const NewRows &nr) {
     if (!nr.k || !nr.v || !nr.slots) return fail(PA_ERR_INVALID_ARG, "NULL input");
     if (!aligned(nr.k, 16) || !aligned(nr.v, 16))
         return fail(PA_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
+    return PA_OK;
+}
+
+// Longest block table of a windowed call, in keys (int32 arithmetic on keys
+// then never overflows), and most axes of a rotary embedding.
+constexpr int64_t kMaxWindowKeys = static_cast<int64_t>(1) << 30;
+constexpr int kMaxRopeAxes = 8;
+
+int check_window(int32_t window, int32_t num_sinks, float scale) {
+    if (window < 1) return fail(PA_ERR_INVALID_ARG, "window %d: need at least 1", window);
+    if (num_sinks < 0) return fail(PA_ERR_INVALID_ARG, "num_sinks < 0");
+    if (!(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f))
+        return fail(PA_ERR_INVALID_ARG, "scale must be positive and finite");
     return PA_OK;
 }
 
@@ -998,6 +1013,186 @@ int pa_attention(const void *q, const pa_kv_desc *kv, const int32_t *block_table
                            workspace, workspace_bytes, -1, 0, stream);
 }
 
+int pa_window_attention(const void *q, const pa_kv_desc *kv, const int32_t *block_tables,
+                        int32_t max_blocks_per_seq, const int32_t *query_start_loc,
+                        const int32_t *context_lens, const int32_t *seq_lens, int32_t num_seqs,
+                        int32_t num_q_tokens, int32_t num_q_heads, float scale, int32_t window,
+                        int32_t num_sinks, void *out, float *lse, void *workspace,
+                        size_t workspace_bytes, void *stream) {
+    g_err[0] = 0;
+    int rc = common_checks(q, kv, num_q_tokens, num_q_heads, scale, out, workspace);
+    if (rc != PA_OK) return rc;
+    if ((rc = check_window(window, num_sinks, scale)) != PA_OK) return rc;
+    if (num_seqs < 0) return fail(PA_ERR_INVALID_ARG, "num_seqs < 0");
+    if (num_seqs == 0 || num_q_tokens == 0) return PA_OK;
+    if (!block_tables || !query_start_loc || !context_lens || !seq_lens)
+        return fail(PA_ERR_INVALID_ARG, "metadata pointer is NULL");
+    if (max_blocks_per_seq <= 0) return fail(PA_ERR_INVALID_ARG, "max_blocks_per_seq <= 0");
+    if (static_cast<int64_t>(max_blocks_per_seq) * kv->block_size > kMaxWindowKeys)
+        return fail(PA_ERR_UNSUPPORTED, "block tables of more than 2^30 tokens per request");
+    const WsLayout L = make_layout(num_seqs, num_q_tokens, num_q_heads, kv->num_kv_heads,
+                                   kv->head_dim, 0, false);
+    if (!workspace || workspace_bytes < L.total)
+        return fail(PA_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", L.total,
+                    workspace_bytes);
+    DeviceInfo *dev;
+    if ((rc = device_info(&dev)) != PA_OK) return rc;
+    const bool fp8 = kv->kv_dtype == PA_KV_FP8_E4M3;
+    WindowParams p{};
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.lse = lse;
+    p.k_cache = kv->k_cache;
+    p.v_cache = kv->v_cache;
+    p.block_tables = block_tables;
+    p.bt_stride = max_blocks_per_seq;
+    p.qsl = query_start_loc;
+    p.ctx = context_lens;
+    p.seq_lens = seq_lens;
+    p.num_seqs = num_seqs;
+    p.num_q_tokens = num_q_tokens;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = kv->num_kv_heads;
+    p.group = num_q_heads / kv->num_kv_heads;
+    p.block_size = kv->block_size;
+    p.num_blocks = kv->num_blocks;
+    p.window = window;
+    p.sinks = num_sinks;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.k_scale = kv->k_scale;
+    p.v_scale = kv->v_scale;
+    p.status = dev->status;
+    rc = launch_window(p, kv->head_dim, fp8, static_cast<cudaStream_t>(stream));
+    return rc == PA_OK ? PA_OK : fail(rc, "window attention launch failed");
+}
+
+int pa_rope_write_kv(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                     const void *v, int64_t v_stride, const int32_t *positions,
+                     const pa_rope_desc *rope, const int64_t *slot_mapping, int32_t num_tokens,
+                     int32_t num_q_heads, const pa_kv_desc *kv, void *q_out, void *stream) {
+    g_err[0] = 0;
+    int rc = check_kv(kv);
+    if (rc != PA_OK) return rc;
+    if ((rc = check_new_rows(NewRows{k, v, slot_mapping, num_tokens})) != PA_OK) return rc;
+    if (!rope || !rope->inv_freq) return fail(PA_ERR_INVALID_ARG, "rope descriptor or inv_freq is NULL");
+    if (rope->rot_dim < 16 || rope->rot_dim % 16 != 0 || rope->rot_dim > kv->head_dim)
+        return fail(PA_ERR_UNSUPPORTED, "rot_dim %d: need a multiple of 16, at most head_dim %d",
+                    rope->rot_dim, kv->head_dim);
+    if (rope->num_axes < 1 || rope->num_axes > kMaxRopeAxes)
+        return fail(PA_ERR_UNSUPPORTED, "num_axes %d: need 1 .. %d", rope->num_axes, kMaxRopeAxes);
+    if (rope->adjacent != 0 && rope->adjacent != 1)
+        return fail(PA_ERR_INVALID_ARG, "pa_rope_desc.adjacent must be 0 or 1");
+    if (!std::isfinite(rope->attn_factor))
+        return fail(PA_ERR_INVALID_ARG, "attn_factor is not finite");
+    if (num_q_heads < 0) return fail(PA_ERR_INVALID_ARG, "num_q_heads < 0");
+    if (num_tokens == 0) return PA_OK;
+    if (!positions) return fail(PA_ERR_INVALID_ARG, "positions is NULL");
+    if (!aligned(positions, 4) || !aligned(slot_mapping, 8) || !aligned(rope->inv_freq, 8) ||
+        !aligned(rope->axis, 4))
+        return fail(PA_ERR_INVALID_ARG, "positions, axis, inv_freq or slot_mapping is misaligned");
+    if (num_q_heads > 0) {
+        if (!q || !q_out) return fail(PA_ERR_INVALID_ARG, "q or q_out is NULL");
+        if (!aligned(q, 16) || !aligned(q_out, 16))
+            return fail(PA_ERR_INVALID_ARG, "q and q_out must be 16-byte aligned");
+    }
+    const int64_t d = kv->head_dim;
+    const int64_t stride[3] = {num_q_heads > 0 ? q_stride : 0, k_stride, v_stride};
+    const int64_t least[3] = {num_q_heads * d, kv->num_kv_heads * d, kv->num_kv_heads * d};
+    for (int i = 0; i < 3; ++i)
+        if (stride[i] % 8 != 0 || (num_tokens > 1 && stride[i] < least[i]))
+            return fail(PA_ERR_INVALID_ARG,
+                        "%c_stride %lld: need a multiple of 8 that holds a token's heads", "qkv"[i],
+                        (long long)stride[i]);
+    if (num_q_heads > 0 && q == q_out && q_stride != least[0] && num_tokens > 1)
+        return fail(PA_ERR_INVALID_ARG, "q rotated in place must be contiguous");
+    DeviceInfo *dev;
+    if ((rc = device_info(&dev)) != PA_OK) return rc;
+    RopeParams p{};
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.k = static_cast<const __nv_bfloat16 *>(k);
+    p.v = static_cast<const __nv_bfloat16 *>(v);
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.positions = positions;
+    p.inv_freq = rope->inv_freq;
+    p.axis = rope->axis;
+    p.slots = slot_mapping;
+    p.q_out = static_cast<__nv_bfloat16 *>(q_out);
+    p.k_cache = kv->k_cache;
+    p.v_cache = kv->v_cache;
+    p.fp8 = kv->kv_dtype == PA_KV_FP8_E4M3 ? 1 : 0;
+    p.k_scale = kv->k_scale;
+    p.v_scale = kv->v_scale;
+    p.num_tokens = num_tokens;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = kv->num_kv_heads;
+    p.head_dim = kv->head_dim;
+    p.block_size = kv->block_size;
+    p.num_blocks = kv->num_blocks;
+    p.rot_dim = rope->rot_dim;
+    p.num_axes = rope->num_axes;
+    p.adjacent = rope->adjacent;
+    p.attn_factor = rope->attn_factor;
+    p.status = dev->status;
+    rc = launch_rope_write(p, static_cast<cudaStream_t>(stream));
+    return rc == PA_OK ? PA_OK : fail(rc, "rope_write_kv launch failed");
+}
+
+int pa_copy_blocks(const pa_kv_desc *kv, int32_t num_layers, const int32_t *pairs,
+                   int32_t num_pairs, void *stream) {
+    g_err[0] = 0;
+    if (num_layers < 0 || num_pairs < 0)
+        return fail(PA_ERR_INVALID_ARG, "num_layers or num_pairs < 0");
+    if (num_layers > 0 && !kv) return fail(PA_ERR_INVALID_ARG, "kv descriptors are NULL");
+    for (int l = 0; l < num_layers; ++l) {
+        const int rc = check_kv(&kv[l], false);
+        if (rc != PA_OK) return rc;
+        if (kv[l].num_blocks != kv->num_blocks || kv[l].block_size != kv->block_size ||
+            kv[l].num_kv_heads != kv->num_kv_heads || kv[l].head_dim != kv->head_dim ||
+            kv[l].kv_dtype != kv->kv_dtype)
+            return fail(PA_ERR_INVALID_ARG, "layer %d's pool differs from layer 0's in its geometry",
+                        l);
+    }
+    if (num_layers == 0 || num_pairs == 0) return PA_OK;
+    if (!pairs) return fail(PA_ERR_INVALID_ARG, "pairs is NULL");
+    if (!aligned(pairs, 8)) return fail(PA_ERR_INVALID_ARG, "pairs must be 8-byte aligned");
+    DeviceInfo *dev;
+    int rc = device_info(&dev);
+    if (rc != PA_OK) return rc;
+    rc = launch_copy_blocks(kv, num_layers, pairs, num_pairs, dev->sms, dev->status,
+                            static_cast<cudaStream_t>(stream));
+    return rc == PA_OK ? PA_OK : fail(rc, "copy_blocks launch failed");
+}
+
+int pa_validate_copies(const int32_t *pairs, int32_t num_pairs, int32_t num_blocks) {
+    g_err[0] = 0;
+    if (num_pairs < 0 || num_blocks <= 0 || (num_pairs > 0 && !pairs))
+        return fail(PA_ERR_INVALID_ARG, "bad sizes");
+    try {
+        std::vector<uint8_t> role(static_cast<size_t>(num_blocks), 0);  // 1: a src, 2: a dst
+        for (int pass = 0; pass < 2; ++pass)
+            for (int i = 0; i < num_pairs; ++i) {
+                const int32_t src = pairs[2 * i], dst = pairs[2 * i + 1];
+                if (src < 0 || dst < 0 || src == dst) continue;
+                if (src >= num_blocks || dst >= num_blocks)
+                    return fail(PA_ERR_BAD_METADATA, "pair %d (%d, %d) outside the pool", i, src,
+                                dst);
+                if (pass == 0) {
+                    role[static_cast<size_t>(src)] = 1;
+                    continue;
+                }
+                uint8_t &r = role[static_cast<size_t>(dst)];
+                if (r) return fail(PA_ERR_BAD_METADATA, "block %d is written by pair %d and %s", dst,
+                                   i, r == 1 ? "read by another" : "written by another");
+                r = 2;
+            }
+    } catch (...) {
+        return fail(PA_ERR_INVALID_ARG, "out of host memory");
+    }
+    return PA_OK;
+}
+
 int pa_merge_states(const void *o_a, const float *lse_a, const void *o_b, const float *lse_b,
                     int32_t n, int32_t num_heads, int32_t head_dim, void *out, float *lse_out,
                     void *stream) {
@@ -1111,10 +1306,13 @@ size_t pa_cascade_fp8_staging_bytes(int32_t num_kv_heads, int32_t head_dim,
     return prefix_stage_bytes(num_kv_heads, head_dim, block_size, prefix_len);
 }
 
-int pa_validate_metadata(const int32_t *block_tables, int32_t max_blocks_per_seq,
-                         const int32_t *query_start_loc, const int32_t *context_lens,
-                         const int32_t *seq_lens, int32_t num_seqs, int32_t num_q_tokens,
-                         const int64_t *slot_mapping, int32_t num_blocks, int32_t block_size) {
+// pa_validate_metadata; with window > 0 only the blocks of which some row of
+// the request sees a key are looked at.
+static int validate_metadata(const int32_t *block_tables, int32_t max_blocks_per_seq,
+                             const int32_t *query_start_loc, const int32_t *context_lens,
+                             const int32_t *seq_lens, int32_t num_seqs, int32_t num_q_tokens,
+                             int32_t window, int32_t num_sinks, const int64_t *slot_mapping,
+                             int32_t num_blocks, int32_t block_size) {
     g_err[0] = 0;
     if (num_seqs < 0 || num_q_tokens < 0 || block_size <= 0 || num_blocks <= 0)
         return fail(PA_ERR_INVALID_ARG, "bad sizes");
@@ -1133,7 +1331,13 @@ int pa_validate_metadata(const int32_t *block_tables, int32_t max_blocks_per_seq
         if (nblk > max_blocks_per_seq)
             return fail(PA_ERR_BAD_METADATA, "request %d needs %lld blocks > max_blocks_per_seq",
                         b, (long long)nblk);
+        if (window > 0 && n == 0) continue;
+        // blocks [hide_from, hide_to) lie between the sinks and the first row's window
+        const int64_t hide_from = (static_cast<int64_t>(num_sinks) + block_size - 1) / block_size;
+        const int64_t seen = static_cast<int64_t>(context_lens[b]) - window + 1;
+        const int64_t hide_to = window > 0 && seen > 0 ? seen / block_size : 0;
         for (int64_t j = 0; j < nblk; ++j) {
+            if (j >= hide_from && j < hide_to) continue;
             const int32_t blk = block_tables[static_cast<int64_t>(b) * max_blocks_per_seq + j];
             if (blk < 0 || blk >= num_blocks)
                 return fail(PA_ERR_BAD_METADATA, "block_tables[%d][%lld] = %d out of range", b,
@@ -1158,6 +1362,27 @@ int pa_validate_metadata(const int32_t *block_tables, int32_t max_blocks_per_seq
         }
     }
     return PA_OK;
+}
+
+int pa_validate_metadata(const int32_t *block_tables, int32_t max_blocks_per_seq,
+                         const int32_t *query_start_loc, const int32_t *context_lens,
+                         const int32_t *seq_lens, int32_t num_seqs, int32_t num_q_tokens,
+                         const int64_t *slot_mapping, int32_t num_blocks, int32_t block_size) {
+    return validate_metadata(block_tables, max_blocks_per_seq, query_start_loc, context_lens,
+                             seq_lens, num_seqs, num_q_tokens, 0, 0, slot_mapping, num_blocks,
+                             block_size);
+}
+
+int pa_validate_window_metadata(const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                const int32_t *query_start_loc, const int32_t *context_lens,
+                                const int32_t *seq_lens, int32_t num_seqs, int32_t num_q_tokens,
+                                int32_t window, int32_t num_sinks, const int64_t *slot_mapping,
+                                int32_t num_blocks, int32_t block_size) {
+    g_err[0] = 0;
+    if (window < 1 || num_sinks < 0) return fail(PA_ERR_INVALID_ARG, "bad window or num_sinks");
+    return validate_metadata(block_tables, max_blocks_per_seq, query_start_loc, context_lens,
+                             seq_lens, num_seqs, num_q_tokens, window, num_sinks, slot_mapping,
+                             num_blocks, block_size);
 }
 
 int pa_set_profile_events(int32_t which, void *start_event, void *end_event) {

@@ -68,7 +68,7 @@ struct Block {
 struct Request {
     std::vector<int32_t> tokens;
     int32_t computed = 0;
-    std::vector<int32_t> table;
+    std::vector<int32_t> table;   // -1: given back, behind every later row's window
     std::vector<Hash128> prefix;  // hash of each computed full block's prefix
 };
 
@@ -175,7 +175,8 @@ int pa_bm_fork(pa_block_manager *bm, int64_t src_id, int64_t dst_id) {
     auto it = bm->reqs.find(src_id);
     if (it == bm->reqs.end()) return PA_ERR_INVALID_ARG;
     Request r = it->second;
-    for (int32_t b : r.table) bm->take_ref(b);
+    for (int32_t b : r.table)
+        if (b >= 0) bm->take_ref(b);
     bm->reqs.emplace(dst_id, std::move(r));
     return PA_OK;
 }
@@ -264,8 +265,95 @@ int pa_bm_free_request(pa_block_manager *bm, int64_t req_id) {
     auto it = bm->reqs.find(req_id);
     if (it == bm->reqs.end()) return PA_ERR_INVALID_ARG;
     const std::vector<int32_t> &tab = it->second.table;
-    for (size_t j = tab.size(); j-- > 0;) bm->release(tab[j]);
+    for (size_t j = tab.size(); j-- > 0;)
+        if (tab[j] >= 0) bm->release(tab[j]);
     bm->reqs.erase(it);
+    return PA_OK;
+}
+
+int pa_bm_release_window(pa_block_manager *bm, int64_t req_id, int32_t window,
+                         int32_t num_sinks, int32_t *num_released) {
+    if (!bm || window < 1 || num_sinks < 0) return PA_ERR_INVALID_ARG;
+    auto it = bm->reqs.find(req_id);
+    if (it == bm->reqs.end()) return PA_ERR_INVALID_ARG;
+    std::vector<int32_t> &tab = it->second.table;
+    const int64_t bs = bm->bs;
+    // the next row sits at position `computed`: keys from here on stay visible
+    const int64_t keep_from = static_cast<int64_t>(it->second.computed) - window + 1;
+    const int64_t first = (static_cast<int64_t>(num_sinks) + bs - 1) / bs;
+    const int64_t last = keep_from > 0 ? keep_from / bs : 0;  // blocks [first, last) go
+    int32_t n = 0;
+    try {
+        // the set nodes are made before anything changes, so that running
+        // out of memory leaves the manager as it was
+        std::set<int32_t> freed;
+        std::set<std::pair<uint64_t, int32_t>> evict;
+        uint64_t clock = bm->clock;
+        for (int64_t j = last; j-- > first;) {
+            const int32_t b = tab[static_cast<size_t>(j)];
+            if (b < 0 || bm->blocks[b].ref > 1) continue;
+            if (bm->blocks[b].cached)
+                evict.insert({++clock, b});
+            else
+                freed.insert(b);
+        }
+        for (const auto &e : evict) bm->blocks[e.second].released = e.first;
+        bm->clock = clock;
+        bm->evictable.merge(evict);
+        bm->free_ids.merge(freed);
+    } catch (...) {
+        return PA_ERR_WORKSPACE;
+    }
+    for (int64_t j = first; j < last; ++j) {
+        int32_t &b = tab[static_cast<size_t>(j)];
+        if (b < 0) continue;
+        --bm->blocks[b].ref;
+        b = -1;
+        ++n;
+    }
+    if (num_released) *num_released = n;
+    return PA_OK;
+}
+
+int pa_bm_compact(pa_block_manager *bm, int32_t max_moves, int32_t *moves, int32_t *num_moves) {
+    if (!bm || max_moves < 0 || (max_moves > 0 && !moves) || !num_moves) return PA_ERR_INVALID_ARG;
+    std::vector<int32_t> to;  // new id of each block, -1: stays
+    int32_t used = 0, n = 0;
+    try {
+        to.assign(bm->blocks.size(), -1);
+    } catch (...) {
+        return PA_ERR_WORKSPACE;
+    }
+    for (const Block &b : bm->blocks) used += (b.ref > 0 || b.cached) ? 1 : 0;
+    for (int32_t src = static_cast<int32_t>(bm->blocks.size()) - 1; src >= used && n < max_moves;
+         --src) {
+        Block &from = bm->blocks[src];
+        if (from.ref == 0 && !from.cached) continue;
+        // as many free blocks lie below `used` as used ones above it
+        auto node = bm->free_ids.extract(bm->free_ids.begin());
+        const int32_t dst = node.value();
+        node.value() = src;
+        bm->free_ids.insert(std::move(node));
+        bm->blocks[dst] = from;
+        if (from.cached) {
+            bm->cache.find(from.h)->second = dst;
+            if (from.ref == 0) {
+                auto e = bm->evictable.extract({from.released, src});
+                e.value().second = dst;
+                bm->evictable.insert(std::move(e));
+            }
+        }
+        from = Block();
+        to[static_cast<size_t>(src)] = dst;
+        moves[2 * n] = src;
+        moves[2 * n + 1] = dst;
+        ++n;
+    }
+    if (n > 0)
+        for (auto &kv : bm->reqs)
+            for (int32_t &b : kv.second.table)
+                if (b >= 0 && to[static_cast<size_t>(b)] >= 0) b = to[static_cast<size_t>(b)];
+    *num_moves = n;
     return PA_OK;
 }
 

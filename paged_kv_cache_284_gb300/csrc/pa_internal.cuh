@@ -221,6 +221,46 @@ struct PrefixFoldParams {
     float *lse;          // may be NULL
 };
 
+// Windowed attention (one warp per row).
+struct WindowParams {
+    const __nv_bfloat16 *q;
+    __nv_bfloat16 *out;
+    float *lse;
+    const void *k_cache, *v_cache;
+    const int *block_tables;
+    int bt_stride;
+    const int *qsl, *ctx, *seq_lens;
+    int num_seqs, num_q_tokens, num_q_heads, num_kv_heads, group, block_size, num_blocks;
+    int window, sinks;
+    float scale_log2;
+    const float *k_scale, *v_scale;
+    unsigned *status;
+};
+
+// Rotary positions and cache write of a step's new rows.
+struct RopeParams {
+    const __nv_bfloat16 *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // elements between tokens
+    const int32_t *positions;              // [num_axes][num_tokens]
+    const double *inv_freq;                // [rot_dim / 2]
+    const int32_t *axis;                   // [rot_dim / 2], or NULL
+    const int64_t *slots;
+    __nv_bfloat16 *q_out;
+    void *k_cache, *v_cache;
+    const float *k_scale, *v_scale;  // fp8 pool only
+    int num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks;
+    int rot_dim, num_axes, adjacent, fp8;
+    float attn_factor;
+    unsigned *status;
+};
+
+// The cache arrays of one pa_copy_blocks launch: K and V of up to
+// kCopyLayers layers.
+constexpr int kCopyLayers = 64;
+struct CopyLayers {
+    void *p[2 * kCopyLayers];
+};
+
 // Launch configuration with the programmatic-stream-serialisation attribute
 // (programmatic dependent launch): the kernel may be scheduled while the
 // previous kernel of the stream is still running, and must call pdl_wait()
@@ -284,6 +324,10 @@ int launch_stage_fp8(const pa_kv_desc *kv, const int32_t *block_tables, int32_t 
 int launch_stage_prefix_fp8(const pa_kv_desc *kv, const int32_t *prefix_blocks, int n,
                             int32_t *ident, void *stage_k, void *stage_v, unsigned *status,
                             int grid, cudaStream_t s);
+int launch_rope_write(const RopeParams &p, cudaStream_t s);
+int launch_copy_blocks(const pa_kv_desc *kv, int num_layers, const int32_t *pairs, int num_pairs,
+                       int sms, unsigned *status, cudaStream_t s);
+int launch_window(const WindowParams &p, int head_dim, bool fp8, cudaStream_t s);
 int launch_plan(const PlanParams &p, cudaStream_t s);
 int launch_short(const ShortParams &p, const CUtensorMap &tk, const CUtensorMap &tv,
                  int head_dim, bool fp8, int grid, cudaStream_t s);

@@ -1,0 +1,273 @@
+"""pa_window_attention on the GPU against the float64 definition: every table
+entry and every key that no row sees is poisoned (-1 entries, NaN keys), so a
+read of anything hidden shows.
+
+Tolerances.  out is rounded to bf16 (at most 2^-8 of its value), and the
+probabilities are rounded once before P V (bf16 2^-8, f16 less), which moves
+out by at most 2^-8 sum_j p_j |v_j|; scores and sums in fp32 add less than
+2^-12 of that sum (a score of 128 products has an error below
+128 * 2^-24 * scale * sum |q k| < 2^-13 for the inputs here; the normaliser as
+much).  lse inherits the scores' error, 2^-13, and fp32's own 2^-22 of it."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_284_gb300 as pk
+from gpu_helpers import DEV, assert_status_clean
+from oracle import ops
+
+pytestmark = pytest.mark.gpu
+
+E4M3_NAN = 0x7F
+
+
+class Step:
+    """One windowed step: bf16 or e4m3 pool whose visible keys are normal values
+    and whose every other element is NaN; hidden blocks' table entries are -1."""
+
+    def __init__(self, requests, hq, hkv, d, bs, window, sinks, kv="bf16", seed=0, pad=0,
+                 keep_tables=False):
+        g = torch.Generator().manual_seed(seed)
+        self.window, self.sinks, self.bs, self.kv, self.hkv = window, sinks, bs, kv, hkv
+        self.requests = requests
+        width = max(1, max(-(-(c + n) // bs) for c, n in requests))
+        seen = [set(int(j) for p in range(c, c + n) for j in ops.visible_keys(p, window, sinks))
+                for c, n in requests]
+        need = [sorted({j // bs for j in s}) for s in seen]
+        used = sum(len(x) for x in need)
+        self.num_blocks = used + 3
+        perm = torch.randperm(self.num_blocks, generator=g).tolist()
+        table = torch.full((len(requests), width), -1, dtype=torch.int32)
+        live = torch.zeros(self.num_blocks, bs, dtype=torch.bool)
+        at = 0
+        for b, cols in enumerate(need):
+            for col in cols:
+                table[b, col] = perm[at]
+                for off in range(bs):
+                    live[perm[at], off] = col * bs + off in seen[b]
+                at += 1
+        shape = (self.num_blocks, hkv, bs, d)
+        k, v = torch.randn(shape, generator=g), torch.randn(shape, generator=g)
+        hidden = ~live[:, None, :, None]
+        if kv == "bf16":
+            self.k = k.masked_fill(hidden, float("nan")).to(torch.bfloat16)
+            self.v = v.masked_fill(hidden, float("nan")).to(torch.bfloat16)
+            self.ks = self.vs = None
+            self.k64, self.v64 = self.k.double().numpy(), self.v.double().numpy()
+        else:
+            self.k, self.v = ((x * 16).to(torch.float8_e4m3fn).view(torch.uint8)
+                              .masked_fill(hidden, E4M3_NAN) for x in (k, v))
+            self.ks, self.vs = (0.04 + 0.05 * torch.rand(hkv, generator=g) for _ in "kv")
+            self.k64, self.v64 = (x.view(torch.float8_e4m3fn).double().numpy() *
+                                  s.double().numpy()[:, None, None]
+                                  for x, s in ((self.k, self.ks), (self.v, self.vs)))
+        i32 = dict(dtype=torch.int32)
+        self.table = table
+        self.qsl = torch.tensor(np.concatenate([[0], np.cumsum([n for _, n in requests])]), **i32)
+        self.ctx = torch.tensor([c for c, _ in requests], **i32)
+        self.seq = torch.tensor([c + n for c, n in requests], **i32)
+        self.total = int(self.qsl[-1])
+        self.q = torch.randn((self.total + pad, hq, d), generator=g).to(torch.bfloat16)
+        self.scale = d ** -0.5
+        self.staging = sum(len(x) for x, (_, n) in zip(need, requests) if n * hq // hkv > 64)
+
+    def to_dev(self):
+        t = {x: getattr(self, x).to(DEV) for x in ("q", "k", "v", "table", "qsl", "ctx", "seq")}
+        t["ks"], t["vs"] = ((None, None) if self.ks is None
+                            else (self.ks.to(DEV), self.vs.to(DEV)))
+        t["out"] = torch.full_like(t["q"], 7.0)
+        t["lse"] = torch.full(t["q"].shape[:2], 7.0, device=DEV)
+        return t
+
+    def call(self, t, **kw):
+        kw.setdefault("staging_blocks", self.staging if self.kv == "e4m3" else 0)
+        return pk.pa_window_attention(t["q"], t["k"], t["v"], t["table"], t["qsl"], t["ctx"],
+                                      t["seq"], self.scale, self.window, self.sinks, t["out"],
+                                      t["lse"], k_scale=t["ks"], v_scale=t["vs"], **kw)
+
+    def check(self, t, what=""):
+        n = self.total
+        ref_o, ref_l, mag = ops.window_attention(
+            self.q.double().numpy()[:n], self.k64, self.v64, self.table.numpy(), self.qsl.numpy(),
+            self.ctx.numpy(), self.scale, self.window, self.sinks, self.bs)
+        out, lse = t["out"].double().cpu().numpy(), t["lse"].double().cpu().numpy()
+        assert np.all(out[n:] == 7.0) and np.all(lse[n:] == 7.0), "rows of no request written"
+        err, lerr = np.abs(out[:n] - ref_o), np.abs(lse[:n] - ref_l)
+        tol = 2.0 ** -8 * np.abs(ref_o) + (2.0 ** -8 + 2.0 ** -12) * mag
+        ltol = 2.0 ** -13 + 2.0 ** -22 * np.abs(ref_l)
+        assert np.all(np.isfinite(out[:n])) and np.all(np.isfinite(lse[:n])), what
+        assert np.all(err <= tol), f"{what}: {np.max(err / tol)} of the tolerance"
+        assert np.all(lerr <= ltol), f"{what}: lse {np.max(lerr / ltol)} of the tolerance"
+
+    def run_and_check(self, **kw):
+        t = self.to_dev()
+        self.call(t, **kw)
+        torch.cuda.synchronize()
+        self.check(t, f"{self.requests[:4]} W={self.window} S={self.sinks} bs={self.bs}")
+        assert_status_clean()
+        return t
+
+
+DECODE = [(0, 1), (1, 1), (15, 1), (16, 1), (63, 1), (64, 1), (100, 1), (333, 1), (700, 1)]
+VERIFY = [(0, 5), (3, 2), (60, 5), (130, 3), (411, 5), (15, 7)]
+CHUNKS = [(0, 150), (37, 70), (260, 129)]
+MIXED = [(0, 90), (500, 1), (77, 5), (211, 64), (1, 1), (300, 140), (0, 0), (40, 0)]
+WINDOWS = [(1, 0), (1, 3), (7, 0), (16, 4), (33, 17), (64, 1), (100, 130), (128, 0), (5000, 0),
+           (31, 5000)]
+
+
+@pytest.mark.parametrize("window,sinks", WINDOWS)
+@pytest.mark.parametrize("requests", [DECODE, VERIFY, CHUNKS, MIXED],
+                         ids=["decode", "verify", "chunks", "mixed"])
+def test_bf16_128(requests, window, sinks):
+    Step(requests, 8, 2, 128, 16, window, sinks, seed=window).run_and_check()
+
+
+@pytest.mark.parametrize("window,sinks", WINDOWS)
+@pytest.mark.parametrize("requests", [DECODE, MIXED], ids=["decode", "mixed"])
+def test_e4m3(requests, window, sinks):
+    Step(requests, 8, 2, 128, 16, window, sinks, kv="e4m3", seed=window).run_and_check()
+
+
+@pytest.mark.parametrize("staged", [0, 1, 12])
+def test_e4m3_long_requests_without_enough_staging_room(staged):
+    st = Step(MIXED, 16, 2, 128, 32, 90, 9, kv="e4m3", seed=5)
+    st.run_and_check(staging_blocks=staged)
+
+
+@pytest.mark.parametrize("hq,hkv,d,bs,kv", [
+    (4, 4, 64, 16, "bf16"), (14, 2, 64, 32, "bf16"), (16, 1, 128, 64, "bf16"),
+    (5, 1, 128, 256, "bf16"), (6, 3, 64, 48, "bf16"), (128, 1, 64, 16, "bf16"),
+    (14, 2, 128, 48, "e4m3"), (3, 3, 128, 16, "e4m3"), (32, 1, 128, 256, "e4m3")])
+@pytest.mark.parametrize("window,sinks", [(20, 3), (200, 40)])
+def test_heads_and_block_sizes(hq, hkv, d, bs, kv, window, sinks):
+    Step([(0, 1), (250, 1), (90, 4), (130, 35), (0, 0), (600, 1)], hq, hkv, d, bs, window, sinks,
+         kv=kv, seed=hq).run_and_check()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_long_contexts_split_over_the_window(kv):
+    """Few rows over long windows (the split and its fold), far into a context
+    whose other blocks are gone."""
+    Step([(20000, 1), (9000, 2)], 8, 2, 128, 16, 6000, 37, kv=kv, seed=3).run_and_check()
+
+
+def test_far_positions_have_a_table_of_gone_blocks():
+    """A position past 2^20 keys: table columns far out, all but the window's and
+    the sinks' blocks given back."""
+    Step([(1 << 20, 1), ((1 << 20) + 5, 3)], 4, 2, 64, 256, 300, 4, seed=4).run_and_check()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_padding_rows_are_left_alone(kv):
+    Step([(30, 3), (0, 0), (200, 70)], 8, 2, 128, 16, 40, 4, kv=kv, pad=9).run_and_check()
+
+
+def test_no_lse_and_a_kept_workspace():
+    st = Step(MIXED, 8, 2, 128, 16, 50, 4)
+    t = st.to_dev()
+    ws = st.call(t)
+    first = t["out"].clone()
+    t["out"].fill_(3.0)
+    assert st.call(t, workspace=ws) is ws
+    torch.cuda.synchronize()
+    assert torch.equal(t["out"], first)
+    t["lse"], lse = None, t["lse"]
+    st.call(t, workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(t["out"], first)
+    t["lse"] = lse
+    st.check(t)
+    assert_status_clean()
+
+
+def test_a_window_past_every_context_equals_pa_attention():
+    """The same keys as plain causal attention: both within the definition's
+    tolerance, and the plain call's own result unchanged by a windowed one."""
+    st = Step([(100, 1), (0, 90), (33, 5)], 8, 2, 128, 16, 10 ** 6, 0)
+    t = st.to_dev()
+    args = (t["q"], t["k"], t["v"], t["table"], t["qsl"], t["ctx"], t["seq"], st.scale)
+    pk.pa_attention(*args, t["out"], t["lse"])
+    torch.cuda.synchronize()
+    plain = t["out"].clone()
+    st.check(t, "pa_attention")
+    st.call(t)
+    torch.cuda.synchronize()
+    st.check(t, "pa_window_attention")
+    pk.pa_attention(*args, t["out"], t["lse"])
+    torch.cuda.synchronize()
+    assert torch.equal(t["out"], plain)
+    assert_status_clean()
+
+
+def test_other_stream_and_interleaved_calls():
+    a = Step(DECODE, 8, 2, 128, 16, 50, 4, seed=1)
+    b = Step(MIXED, 8, 2, 128, 16, 9, 0, kv="e4m3", seed=2)
+    ta, tb = a.to_dev(), b.to_dev()
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    wa = a.call(ta, stream=s1)
+    wb = b.call(tb, stream=s2)
+    for _ in range(4):
+        a.call(ta, workspace=wa, stream=s1)
+        b.call(tb, workspace=wb, stream=s2)
+    torch.cuda.synchronize()
+    a.check(ta)
+    b.check(tb)
+    assert_status_clean()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_graph_captured_once_serves_other_metadata(kv):
+    """Captured on one batch, replayed on another of the same sizes (other
+    contexts, another split of the tokens, one request empty)."""
+    first = Step([(40, 1), (300, 5), (7, 70), (90, 1)], 8, 2, 128, 16, 60, 4, kv=kv, seed=1)
+    other = Step([(511, 1), (0, 70), (13, 5), (480, 0)], 8, 2, 128, 16, 60, 4, kv=kv, seed=2, pad=1)
+    assert other.q.shape == first.q.shape
+    t, o = first.to_dev(), other.to_dev()
+    width = max(t["table"].shape[1], o["table"].shape[1])
+    n = max(t["k"].shape[0], o["k"].shape[0])
+
+    def grown(x, size, dim, value):
+        shape = list(x.shape)
+        shape[dim] = size - shape[dim]
+        return torch.cat([x, torch.full(shape, value, dtype=x.dtype, device=x.device)], dim)
+    for x in (t, o):
+        x["table"] = grown(x["table"], width, 1, -1).contiguous()
+        for c in "kv":
+            x[c] = grown(x[c], n, 0, E4M3_NAN if kv == "e4m3" else float("nan")).contiguous()
+    room = max(first.staging, other.staging) if kv == "e4m3" else 0
+    ws = first.call(t, staging_blocks=room)
+    torch.cuda.synchronize()
+    eager = t["out"].clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        first.call(t, workspace=ws, staging_blocks=room)
+    t["out"].fill_(7.0)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(t["out"], eager)
+    first.check(t)
+    for name in t:
+        if t[name] is not None:
+            t[name].copy_(o[name])
+    g.replay()
+    torch.cuda.synchronize()
+    other.check(t)
+    assert_status_clean()
+
+
+def test_bad_block_and_bad_metadata_are_flagged():
+    """A visible entry outside the pool is clamped and flagged; a request whose
+    lengths disagree is skipped and flagged; the others are right."""
+    st = Step([(40, 1), (50, 2), (60, 1)], 4, 2, 64, 16, 20, 2)
+    t = st.to_dev()
+    t["table"][0, 2] = st.num_blocks
+    t["seq"][1] += 1
+    st.call(t)
+    torch.cuda.synchronize()
+    assert pk.read_device_status() == pk.PA_DEV_BAD_BLOCK | pk.PA_DEV_BAD_METADATA
+    assert torch.all(t["out"][1:3] == 7.0)
+    ref, _, _ = ops.window_attention(st.q.double().numpy(), st.k64, st.v64, st.table.numpy(),
+                                     st.qsl.numpy(), st.ctx.numpy(), st.scale, 20, 2, 16)
+    assert np.abs(t["out"][3].double().cpu().numpy() - ref[3]).max() < 0.05
