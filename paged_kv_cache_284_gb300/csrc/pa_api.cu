@@ -38,7 +38,7 @@ constexpr int kMaxDevices = 64;
 struct DeviceInfo {
     bool ready = false;
     int sms = 0;
-    int short_ctas_per_sm[3] = {0, 0, 0};  // bf16 head_dim 64, bf16 128, fp8 128
+    int short_ctas_per_sm[2][3] = {};  // [windowed][bf16 head_dim 64, bf16 128, fp8 128]
     unsigned *status = nullptr;
 };
 DeviceInfo g_dev[kMaxDevices];
@@ -57,9 +57,11 @@ int device_info(DeviceInfo **out) {
         d.status = static_cast<unsigned *>(sym);
         if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return fail(PA_ERR_CUDA, "cannot query SM count");
-        d.short_ctas_per_sm[0] = short_max_ctas_per_sm(64, false);
-        d.short_ctas_per_sm[1] = short_max_ctas_per_sm(128, false);
-        d.short_ctas_per_sm[2] = short_max_ctas_per_sm(128, true);
+        for (int w = 0; w < 2; ++w) {
+            d.short_ctas_per_sm[w][0] = short_max_ctas_per_sm(64, false, w != 0);
+            d.short_ctas_per_sm[w][1] = short_max_ctas_per_sm(128, false, w != 0);
+            d.short_ctas_per_sm[w][2] = short_max_ctas_per_sm(128, true, w != 0);
+        }
         d.ready = true;
     }
     *out = &d;
@@ -454,13 +456,15 @@ int check_window(int32_t window, int32_t num_sinks, float scale) {
 // Runs the planner, the split-KV kernel and the tensor-core kernel of one
 // step on `s`.  With `casc` (cascade decode, all rows short) the step is
 // the unique-suffix pass, run side by side with the shared-prefix pass.
-// With `fresh`, the step's new rows are written into the cache first.
+// With `fresh`, the step's new rows are written into the cache first.  With
+// `win` the step is windowed (no cascade): the windowed forms of the plan and
+// of both kernels run.
 int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, int32_t max_blocks,
              const int32_t *qsl, const int32_t *ctx, const int32_t *seq_lens, int32_t num_seqs,
              int32_t T, int32_t Hq, float scale, void *out, float *lse, uint8_t *ws,
              const WsLayout &L, int short_max_rows, int split_keys, const CascadeArgs *casc,
              bool forbid_long, const StepMaps &maps, const Staging &stg, DeviceInfo *dev,
-             cudaStream_t s, const NewRows *fresh = nullptr) {
+             cudaStream_t s, const NewRows *fresh = nullptr, const WindowArgs *win = nullptr) {
     const int D = kv->head_dim;
     const int group = Hq / kv->num_kv_heads;
     const int tq = q_tile_tokens(group);
@@ -487,10 +491,16 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
     pp.fp8 = fp8 ? 1 : 0;
     pp.stage_cap = staged ? stg.cap : 0;
     pp.block_size = kv->block_size;
+    pp.windowed = win ? 1 : 0;
+    if (win) {
+        pp.win = *win;
+        pp.max_keys = max_blocks * kv->block_size;
+    }
     pp.stage_base = staged ? reinterpret_cast<int *>(ws + L.stage_base) : nullptr;
     pp.stage_list = staged ? reinterpret_cast<int *>(ws + L.stage_list) : nullptr;
     pp.split_stages = split_keys / kStageKeys;
-    const int short_grid = dev->sms * dev->short_ctas_per_sm[fp8 ? 2 : (D == 128 ? 1 : 0)];
+    const int short_grid =
+        dev->sms * dev->short_ctas_per_sm[win ? 1 : 0][fp8 ? 2 : (D == 128 ? 1 : 0)];
     pp.target_items = kSplitItemsPerCta * short_grid;
     pp.num_ctas = short_grid;
     pp.hdr = hdr;
@@ -521,7 +531,7 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
     if (rc != PA_OK) return fail(rc, "plan launch failed");
     if (staged) {
         rc = launch_stage_fp8(kv, block_tables, max_blocks, hdr, pp.stage_base, pp.stage_list,
-                              stg.k, stg.v, dev->status, 2 * dev->sms, s);
+                              stg.k, stg.v, dev->status, 2 * dev->sms, s, ctx, seq_lens, win);
         if (rc != PA_OK) return fail(rc, "fp8 staging copy launch failed");
     }
 
@@ -554,6 +564,7 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
     sp.num_q_tokens = T;
     sp.max_items = L.max_short;
     sp.claim_ahead = kClaimAheadStages;
+    if (win) sp.win = *win;
     const int stall = g_test_stall.load(std::memory_order_relaxed);
     sp.test_stall = stall == PA_TEST_STALL_SPLIT_KV ? 1 : 0;
 
@@ -594,20 +605,20 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         LongParams c1 = cp;
         c1.wait_start = 1;
         c1.first_ctas = -1;
-        rc = launch_long(c1, maps.q, *ptk, *ptv, D, g1, s);
+        rc = launch_long(c1, maps.q, *ptk, *ptv, D, false, g1, s);
         if (rc != PA_OK) return fail(rc, "prefix kernel launch failed: %s",
                                      cudaGetErrorString(cudaGetLastError()));
         sp.no_start_wait = 1;
         sp.test_stall = 0;
         sp.out_f32 = casc->suffix_o;
         sp.lse = casc->suffix_lse;
-        rc = launch_short(sp, maps.k, maps.v, D, fp8, short_grid, s);
+        rc = launch_short(sp, maps.k, maps.v, D, fp8, win != nullptr, short_grid, s);
         if (rc != PA_OK) return fail(rc, "split-KV kernel launch failed: %s",
                                      cudaGetErrorString(cudaGetLastError()));
         LongParams c2 = cp;
         c2.overlap_prev = 1;
         c2.first_ctas = g1;
-        rc = launch_long(c2, maps.q, *ptk, *ptv, D, n_prefix, s);
+        rc = launch_long(c2, maps.q, *ptk, *ptv, D, false, n_prefix, s);
         if (rc != PA_OK) return fail(rc, "prefix kernel launch failed: %s",
                                      cudaGetErrorString(cudaGetLastError()));
         PrefixFoldParams f{};
@@ -655,6 +666,7 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         lp.kv_rows = sp.kv_rows;
         lp.scale_log2 = sp.scale_log2;
         lp.prefix_mode = 0;
+        if (win) lp.win = *win;
         lp.hdr = hdr;
         lp.items = pp.long_items;
         lp.partial_o = sp.partial_o;
@@ -695,13 +707,13 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         // beside the fp8 one, whose rate follows its SM count (707.3 us, 710.1
         // with an eighth)
         const int g1 = std::min(std::max(1, fp8 ? dev->sms / 10 : dev->sms * 2 / 5), long_grid);
-        rc = launch_long(l1, maps.q, lk, lv, D, g1, s);
+        rc = launch_long(l1, maps.q, lk, lv, D, win != nullptr, g1, s);
         if (rc != PA_OK) return fail(rc, "tensor-core kernel launch failed: %s",
                                      cudaGetErrorString(cudaGetLastError()));
         sp.no_start_wait = 1;
         sp.claim_ahead = 0;
         sp.test_stall = 0;
-        rc = launch_short(sp, maps.k, maps.v, D, fp8, short_grid, s);
+        rc = launch_short(sp, maps.k, maps.v, D, fp8, win != nullptr, short_grid, s);
         if (rc != PA_OK) return fail(rc, "split-KV kernel launch failed: %s",
                                      cudaGetErrorString(cudaGetLastError()));
         LongParams l2 = lp;
@@ -710,7 +722,7 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         l2.first_done = &hdr->first_done;
         // the test hook waits for one CTA that the first grid never had
         l2.first_ctas = g1 + (stall == PA_TEST_STALL_LAST_GRID ? 1 : 0);
-        rc = launch_long(l2, maps.q, lk, lv, D, long_grid, s);
+        rc = launch_long(l2, maps.q, lk, lv, D, win != nullptr, long_grid, s);
         if (rc != PA_OK) return fail(rc, "tensor-core kernel launch failed: %s",
                                      cudaGetErrorString(cudaGetLastError()));
         return PA_OK;
@@ -718,7 +730,7 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
 
     {
         ProfScope prof(PA_KERNEL_SPLIT_KV, s);
-        rc = launch_short(sp, maps.k, maps.v, D, fp8, short_grid, s);
+        rc = launch_short(sp, maps.k, maps.v, D, fp8, win != nullptr, short_grid, s);
     }
     if (rc != PA_OK) return fail(rc, "split-KV kernel launch failed: %s",
                                  cudaGetErrorString(cudaGetLastError()));
@@ -728,7 +740,7 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         lp.overlap_prev = short_grid > 0 ? 1 : 0;
         {
             ProfScope prof(PA_KERNEL_TENSOR_CORE, s);
-            rc = launch_long(lp, maps.q, lk, lv, D, long_grid, s);
+            rc = launch_long(lp, maps.q, lk, lv, D, win != nullptr, long_grid, s);
         }
         if (rc != PA_OK) return fail(rc, "tensor-core kernel launch failed: %s",
                                      cudaGetErrorString(cudaGetLastError()));
@@ -773,7 +785,7 @@ int run_prefix(const void *q, const pa_kv_desc *kv, const int32_t *prefix_blocks
     int rc = stage_prefix(ps, kv, prefix_blocks, &lp, &tk, &tv, dev, s);
     if (rc != PA_OK) return rc;
     const int grid = kv->num_kv_heads * q_tiles * nsplit;
-    rc = launch_long(lp, maps.q, *tk, *tv, kv->head_dim, grid, s);
+    rc = launch_long(lp, maps.q, *tk, *tv, kv->head_dim, false, grid, s);
     if (rc != PA_OK) return fail(rc, "prefix kernel launch failed");
     if (nsplit > 1) {
         PrefixFoldParams f{};
@@ -914,13 +926,15 @@ size_t pa_attention_workspace_size(int32_t num_seqs, int32_t num_q_tokens, int32
 
 namespace {
 
-// pa_attention_ex, and with `fresh` the write of the step's new rows first.
+// pa_attention_ex, with `fresh` the write of the step's new rows first, or with
+// `win` a windowed step.
 int attention_entry(const void *q, const pa_kv_desc *kv, const int32_t *block_tables,
                     int32_t max_blocks_per_seq, const int32_t *query_start_loc,
                     const int32_t *context_lens, const int32_t *seq_lens, int32_t num_seqs,
                     int32_t num_q_tokens, int32_t num_q_heads, float scale, void *out, float *lse,
                     void *workspace, size_t workspace_bytes, int32_t short_q_max_rows,
-                    int32_t split_keys, cudaStream_t stream, const NewRows *fresh) {
+                    int32_t split_keys, cudaStream_t stream, const NewRows *fresh,
+                    const WindowArgs *win = nullptr) {
     g_err[0] = 0;
     int rc = common_checks(q, kv, num_q_tokens, num_q_heads, scale, out, workspace);
     if (rc != PA_OK) return rc;
@@ -943,6 +957,8 @@ int attention_entry(const void *q, const pa_kv_desc *kv, const int32_t *block_ta
     if (!block_tables || !query_start_loc || !context_lens || !seq_lens)
         return fail(PA_ERR_INVALID_ARG, "metadata pointer is NULL");
     if (max_blocks_per_seq <= 0) return fail(PA_ERR_INVALID_ARG, "max_blocks_per_seq <= 0");
+    if (win && static_cast<int64_t>(max_blocks_per_seq) * kv->block_size > kMaxWindowKeys)
+        return fail(PA_ERR_UNSUPPORTED, "block tables of more than 2^30 tokens per request");
     const WsLayout L = make_layout(num_seqs, num_q_tokens, num_q_heads, kv->num_kv_heads,
                                    kv->head_dim, 0, false);
     if (!workspace || workspace_bytes < L.total)
@@ -961,7 +977,7 @@ int attention_entry(const void *q, const pa_kv_desc *kv, const int32_t *block_ta
                     seq_lens, num_seqs, num_q_tokens, num_q_heads, scale, out, lse,
                     static_cast<uint8_t *>(workspace), L,
                     short_q_max_rows < 0 ? kShortMaxRows : short_q_max_rows, split_keys, nullptr,
-                    false, maps, stg, dev, stream, fresh);
+                    false, maps, stg, dev, stream, fresh, win);
 }
 
 }  // namespace
@@ -1020,50 +1036,15 @@ int pa_window_attention(const void *q, const pa_kv_desc *kv, const int32_t *bloc
                         int32_t num_sinks, void *out, float *lse, void *workspace,
                         size_t workspace_bytes, void *stream) {
     g_err[0] = 0;
-    int rc = common_checks(q, kv, num_q_tokens, num_q_heads, scale, out, workspace);
+    const int rc = check_window(window, num_sinks, scale);
     if (rc != PA_OK) return rc;
-    if ((rc = check_window(window, num_sinks, scale)) != PA_OK) return rc;
-    if (num_seqs < 0) return fail(PA_ERR_INVALID_ARG, "num_seqs < 0");
-    if (num_seqs == 0 || num_q_tokens == 0) return PA_OK;
-    if (!block_tables || !query_start_loc || !context_lens || !seq_lens)
-        return fail(PA_ERR_INVALID_ARG, "metadata pointer is NULL");
-    if (max_blocks_per_seq <= 0) return fail(PA_ERR_INVALID_ARG, "max_blocks_per_seq <= 0");
-    if (static_cast<int64_t>(max_blocks_per_seq) * kv->block_size > kMaxWindowKeys)
-        return fail(PA_ERR_UNSUPPORTED, "block tables of more than 2^30 tokens per request");
-    const WsLayout L = make_layout(num_seqs, num_q_tokens, num_q_heads, kv->num_kv_heads,
-                                   kv->head_dim, 0, false);
-    if (!workspace || workspace_bytes < L.total)
-        return fail(PA_ERR_WORKSPACE, "workspace needs %zu bytes, got %zu", L.total,
-                    workspace_bytes);
-    DeviceInfo *dev;
-    if ((rc = device_info(&dev)) != PA_OK) return rc;
-    const bool fp8 = kv->kv_dtype == PA_KV_FP8_E4M3;
-    WindowParams p{};
-    p.q = static_cast<const __nv_bfloat16 *>(q);
-    p.out = static_cast<__nv_bfloat16 *>(out);
-    p.lse = lse;
-    p.k_cache = kv->k_cache;
-    p.v_cache = kv->v_cache;
-    p.block_tables = block_tables;
-    p.bt_stride = max_blocks_per_seq;
-    p.qsl = query_start_loc;
-    p.ctx = context_lens;
-    p.seq_lens = seq_lens;
-    p.num_seqs = num_seqs;
-    p.num_q_tokens = num_q_tokens;
-    p.num_q_heads = num_q_heads;
-    p.num_kv_heads = kv->num_kv_heads;
-    p.group = num_q_heads / kv->num_kv_heads;
-    p.block_size = kv->block_size;
-    p.num_blocks = kv->num_blocks;
-    p.window = window;
-    p.sinks = num_sinks;
-    p.scale_log2 = scale * 1.4426950408889634f;
-    p.k_scale = kv->k_scale;
-    p.v_scale = kv->v_scale;
-    p.status = dev->status;
-    rc = launch_window(p, kv->head_dim, fp8, static_cast<cudaStream_t>(stream));
-    return rc == PA_OK ? PA_OK : fail(rc, "window attention launch failed");
+    // a request has at most 2^30 keys: more window or sinks see no more of it
+    const int32_t most = static_cast<int32_t>(kMaxWindowKeys);
+    const WindowArgs win{std::min(window, most), std::min(num_sinks, most)};
+    return attention_entry(q, kv, block_tables, max_blocks_per_seq, query_start_loc, context_lens,
+                           seq_lens, num_seqs, num_q_tokens, num_q_heads, scale, out, lse,
+                           workspace, workspace_bytes, -1, 0, static_cast<cudaStream_t>(stream),
+                           nullptr, &win);
 }
 
 int pa_rope_write_kv(const void *q, int64_t q_stride, const void *k, int64_t k_stride,

@@ -72,22 +72,70 @@ static_assert(sizeof(PlanHeader) == 64, "header size");
 // [stage_begin*64, min(stage_end*64, seq_len)).  Split s of kv head h writes
 // partial rows partial_base + h*nsplit*R + [0, R) (R = q_count * group) when
 // nsplit > 1, and counts its completion in counters[counter*Hkv + h].
+// A windowed step counts stages and keys over the piece's visible chunks alone
+// (see KeySpan): seq_len is then the packed end of its keys.
 struct alignas(16) ShortItem {
     int b, split, nsplit, stage_begin;
     int stage_end, partial_base, q_begin, q_count;
-    int counter, seq_len, pad1, pad2;  // seq_len: the request's, read once by the plan
+    int counter, seq_len;  // seq_len: the request's, read once by the plan
+    int sink_chunks, gap;  // windowed step: the piece's KeySpan
 };
 static_assert(sizeof(ShortItem) == 48, "item size");
 
 // Tensor-core record: query tile q_tile of request b (tile = 128/group tokens
-// x group heads), keys [key_begin, key_end).
+// x group heads), keys [key_begin, key_end) (packed keys in a windowed step).
 struct alignas(16) LongItem {
     int b, q_tile, key_begin, key_end;
-    int pad[4];
+    int sink_chunks, gap;  // windowed step: the tile's KeySpan
+    int pad[2];
 };
 static_assert(sizeof(LongItem) == 32, "item size");
 
+// Sliding window and sinks of a windowed step: the row at position p sees key
+// j <= p if j > p - window or j < sinks.  Positions, window and sinks are at
+// most 2^30 (the host clamps the last two), so that their differences fit int.
+struct WindowArgs {
+    int window, sinks;
+};
+
 #if defined(__CUDACC__)
+// The 16-key chunks of which some row at positions [first_pos, end) sees a
+// key: the sinks' chunks 0 .. sink_chunks - 1, then every chunk from the first
+// row's window up to the last row.  The kernels pack them: packed chunk c is
+// chunk c of the request below sink_chunks and chunk c + gap from there on, so
+// work, pipeline stages and key tiles hold visible chunks only, and a chunk's
+// place in the cache is looked up by its own block id anyway.  With gap > 0
+// every row's window lies behind the sinks' chunks, so in packed keys (key -
+// 16 gap) the mask keeps its form: j <= p - 16 gap and (j < sinks or j > p -
+// 16 gap - window).
+struct KeySpan {
+    int sink_chunks, gap, keys;  // keys: packed end, end - 16 * gap
+};
+__device__ __forceinline__ KeySpan key_span(const WindowArgs &w, int first_pos, int end) {
+    KeySpan s;
+    s.sink_chunks = (min(w.sinks, end) + kChunkKeys - 1) / kChunkKeys;
+    s.gap = max(0, max(0, first_pos - w.window + 1) / kChunkKeys - s.sink_chunks);
+    s.keys = end - s.gap * kChunkKeys;
+    return s;
+}
+// First key of the packed chunk that starts at packed key `key0`.
+__device__ __forceinline__ int unpacked_key(int key0, int sink_chunks, int gap) {
+    return key0 < sink_chunks * kChunkKeys ? key0 : key0 + gap * kChunkKeys;
+}
+// The same for whole blocks of a request whose rows start at `first_pos`: its
+// visible blocks are the sinks' blocks 0 .. sink_blocks - 1 and those from
+// sink_blocks + gap on.
+struct BlockSpan {
+    int sink_blocks, gap;
+};
+__device__ __forceinline__ BlockSpan block_span(const WindowArgs &w, int first_pos, int end,
+                                                int block_size) {
+    BlockSpan s;
+    s.sink_blocks = (min(w.sinks, end) + block_size - 1) / block_size;
+    s.gap = max(0, max(0, first_pos - w.window + 1) / block_size - s.sink_blocks);
+    return s;
+}
+
 // Records are read through L2 (the plan kernel that wrote them may have run
 // concurrently with this grid's launch).
 template <typename T>
@@ -142,6 +190,7 @@ struct ShortParams {
     int num_seqs, num_q_tokens;  // sizes of the metadata arrays and of q (L2 warm-up)
     int max_items;               // work-record capacity of the workspace (>= 1)
     int claim_ahead;  // ring stages before an item's end at which the next is claimed (0: at its start)
+    WindowArgs win;   // windowed step only
     int test_stall;   // test hook: CTA 0's producer stops after its first stage
 };
 
@@ -183,6 +232,7 @@ struct LongParams {
     // the step's inputs) before its last instruction, where it waits for the
     // split-KV grid so that its own completion still orders the stream.
     int overlap_prev;
+    WindowArgs win;  // windowed step only
 };
 
 struct PlanParams {
@@ -195,6 +245,9 @@ struct PlanParams {
     // last; stage_base[b] = first staging block or -1, stage_list = staged
     // requests in order.  stage_cap = 0: no staging (all rows split-KV).
     int fp8, stage_cap, block_size;
+    int windowed;  // a windowed step: only visible chunks (blocks) are counted,
+    int max_keys;  // and a request longer than its table is skipped
+    WindowArgs win;
     int *stage_base, *stage_list;
     int split_stages;    // 0 = automatic
     int target_items;    // automatic split aims at about this many split-KV items
@@ -219,22 +272,6 @@ struct PrefixFoldParams {
     __nv_bfloat16 *out;  // bf16 result, or
     float *out_f32;      // fp32 result (a state for the suffix pass)
     float *lse;          // may be NULL
-};
-
-// Windowed attention (one warp per row).
-struct WindowParams {
-    const __nv_bfloat16 *q;
-    __nv_bfloat16 *out;
-    float *lse;
-    const void *k_cache, *v_cache;
-    const int *block_tables;
-    int bt_stride;
-    const int *qsl, *ctx, *seq_lens;
-    int num_seqs, num_q_tokens, num_q_heads, num_kv_heads, group, block_size, num_blocks;
-    int window, sinks;
-    float scale_log2;
-    const float *k_scale, *v_scale;
-    unsigned *status;
 };
 
 // Rotary positions and cache write of a step's new rows.
@@ -318,7 +355,8 @@ int launch_write_kv(const void *k, const void *v, const int64_t *slots, int num_
 // bf16 staging pool; grid-stride over staging blocks.
 int launch_stage_fp8(const pa_kv_desc *kv, const int32_t *block_tables, int32_t bt_stride,
                      const PlanHeader *hdr, const int *stage_base, const int *stage_list,
-                     void *stage_k, void *stage_v, unsigned *status, int grid, cudaStream_t s);
+                     void *stage_k, void *stage_v, unsigned *status, int grid, cudaStream_t s,
+                     const int *ctx, const int *seq_lens, const WindowArgs *win);
 // The shared prefix's n e4m3 blocks decoded to bf16 staging blocks 0..n-1
 // (cascade decode on an e4m3 pool); ident[k] = k is the staged block list.
 int launch_stage_prefix_fp8(const pa_kv_desc *kv, const int32_t *prefix_blocks, int n,
@@ -327,13 +365,12 @@ int launch_stage_prefix_fp8(const pa_kv_desc *kv, const int32_t *prefix_blocks, 
 int launch_rope_write(const RopeParams &p, cudaStream_t s);
 int launch_copy_blocks(const pa_kv_desc *kv, int num_layers, const int32_t *pairs, int num_pairs,
                        int sms, unsigned *status, cudaStream_t s);
-int launch_window(const WindowParams &p, int head_dim, bool fp8, cudaStream_t s);
 int launch_plan(const PlanParams &p, cudaStream_t s);
 int launch_short(const ShortParams &p, const CUtensorMap &tk, const CUtensorMap &tv,
-                 int head_dim, bool fp8, int grid, cudaStream_t s);
-int short_max_ctas_per_sm(int head_dim, bool fp8);
+                 int head_dim, bool fp8, bool windowed, int grid, cudaStream_t s);
+int short_max_ctas_per_sm(int head_dim, bool fp8, bool windowed);
 int launch_long(const LongParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
-                const CUtensorMap &tv, int head_dim, int grid, cudaStream_t s);
+                const CUtensorMap &tv, int head_dim, bool windowed, int grid, cudaStream_t s);
 int launch_prefix_fold(const PrefixFoldParams &f, int head_dim, cudaStream_t s);
 int launch_merge(const void *oa, const float *la, const void *ob, const float *lb, int n,
                  int heads, int head_dim, void *out, float *lse_out, cudaStream_t s);

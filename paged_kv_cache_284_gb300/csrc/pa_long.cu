@@ -85,6 +85,11 @@ struct Bars {
     uint64_t o_free, drain, drain_pv;
 };
 
+// The lowest n bits set, n clamped to 0 .. 64.
+__device__ __forceinline__ uint64_t low_bits(int n) {
+    return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1;
+}
+
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
     return warp_mbar_wait(bar, parity, abort);
 }
@@ -121,8 +126,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 struct Item {
     int b, h, tok0, nvalid, pos0, key_begin, key_end, causal, nsplit, split;
     int pair, partial_base, nt;
+    int sink_chunks, gap;      // windowed step
+    int block_sinks, block_gap;  // windowed step on staged blocks (BlockSpan)
 };
 
+template <bool WIN>
 __device__ __forceinline__ Item decode_item(const LongParams &p, int idx) {
     Item it{};
     const int TQ = p.q_tile_tokens;
@@ -140,6 +148,18 @@ __device__ __forceinline__ Item decode_item(const LongParams &p, int idx) {
         it.key_end = li.key_end;
         it.causal = 1;
         it.nsplit = 1;
+        if constexpr (WIN) {
+            // positions in packed keys from here on
+            if (p.stage_base) {
+                const int ctx = it.pos0 - li.q_tile * TQ;
+                const BlockSpan bsp = block_span(p.win, ctx, ctx + n, p.block_size);
+                it.block_sinks = bsp.sink_blocks;
+                it.block_gap = bsp.gap;
+            }
+            it.sink_chunks = li.sink_chunks;
+            it.gap = li.gap;
+            it.pos0 -= li.gap * kChunkKeys;
+        }
     } else {
         it.split = idx % p.prefix_nsplit;
         const int qt = (idx / p.prefix_nsplit) % p.prefix_q_tiles;
@@ -232,7 +252,7 @@ __device__ __forceinline__ int num_items(const LongParams &p) {
 
 // Producer loop shared by the K warp (0, which also loads Q) and the V warp
 // (6): gathers one 128-key tile per step into its ring.
-template <int D, int NS>
+template <int D, int NS, bool WIN>
 __device__ void produce(const LongParams &p, const Sched &sc, const CUtensorMap *tm, uint8_t *ring,
                         uint64_t *full, uint64_t *empty, Bars *bars, bool load_q,
                         const CUtensorMap *tmq, uint8_t *sQ, volatile int *abort_flag) {
@@ -252,7 +272,7 @@ __device__ void produce(const LongParams &p, const Sched &sc, const CUtensorMap 
             ok = false;
             break;
         }
-        const Item it = decode_item(p, idx);
+        const Item it = decode_item<WIN>(p, idx);
         if (it.nt == 0) continue;
         if (load_q) {
             if (k_item > 0 && !warp_wait(&bars->q_empty, (k_item - 1) & 1, abort_flag)) break;
@@ -272,16 +292,25 @@ __device__ void produce(const LongParams &p, const Sched &sc, const CUtensorMap 
             if ((j & 3) == 0) {
                 // rows of the next 32 chunks (4 tiles), one per lane; chunks
                 // past key_end are read fully out of bounds -> zeros
-                const int key0 = it.key_begin + (j * 8 + lane) * kChunkKeys;
+                int key0 = it.key_begin + (j * 8 + lane) * kChunkKeys;
                 my_row = p.kv_rows;
                 if (key0 < it.key_end) {
+                    if constexpr (WIN) key0 = unpacked_key(key0, it.sink_chunks, it.gap);
                     int col = key0 / p.block_size;
                     if (p.bt_stride > 0 && col >= p.bt_stride) {
                         flag_status(p.status, PA_DEV_BAD_METADATA);
                         col = p.bt_stride - 1;
                     }
                     // fp8 pool: block col of a staged request is its staging block
-                    int blk = p.stage_base ? __ldcg(p.stage_base + it.b) + col : __ldg(bt + col);
+                    // (a windowed step stages its visible blocks)
+                    int blk;
+                    if (p.stage_base) {
+                        blk = __ldcg(p.stage_base + it.b) + col;
+                        if constexpr (WIN)
+                            if (col >= it.block_sinks) blk -= it.block_gap;
+                    } else {
+                        blk = __ldg(bt + col);
+                    }
                     if (blk < 0 || blk >= p.num_blocks) {
                         flag_status(p.status, PA_DEV_BAD_BLOCK);
                         blk = min(max(blk, 0), p.num_blocks - 1);
@@ -315,7 +344,7 @@ __device__ void produce(const LongParams &p, const Sched &sc, const CUtensorMap 
 
 }  // namespace
 
-template <int D>
+template <int D, bool WIN>
 __global__ void __launch_bounds__(32 * kLongWarps, 1)
     long_kernel(const LongParams p, const __grid_constant__ CUtensorMap tmq,
                 const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
@@ -390,12 +419,12 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
             tma_prefetch_desc(&tmq);
             tma_prefetch_desc(&tmk);
         }
-        produce<D, kKStages>(p, sched, &tmk, sK, bars->k_full, bars->k_empty, bars, true, &tmq, sQ,
+        produce<D, kKStages, WIN>(p, sched, &tmk, sK, bars->k_full, bars->k_empty, bars, true, &tmq, sQ,
                              abort_flag);
     } else if (warp == kWarpV) {
         // ============================ V loads ============================
         if (lane == 0) tma_prefetch_desc(&tmv);
-        produce<D, kVStages>(p, sched, &tmv, sV, bars->v_full, bars->v_empty, bars, false, nullptr,
+        produce<D, kVStages, WIN>(p, sched, &tmv, sV, bars->v_full, bars->v_empty, bars, false, nullptr,
                              nullptr, abort_flag);
     } else if (warp == 1) {
         // ============================ Q K^T issuer ============================
@@ -413,7 +442,7 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
                     ok = false;
                     break;
                 }
-                const Item it = decode_item(p, idx);
+                const Item it = decode_item<WIN>(p, idx);
                 if (it.nt == 0) continue;
                 if (!mbar_wait(&bars->q_full, k_item & 1, abort_flag)) { ok = false; break; }
                 int j = 0;
@@ -466,7 +495,7 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
                     ok = false;
                     break;
                 }
-                const Item it = decode_item(p, idx);
+                const Item it = decode_item<WIN>(p, idx);
                 if (it.nt == 0) continue;
                 for (int j = 0; j < it.nt; ++j) {
                     const uint32_t tt = t + j;
@@ -535,10 +564,12 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
                 ok = false;
                 break;
             }
-            const Item it = decode_item(p, idx);
+            const Item it = decode_item<WIN>(p, idx);
             const bool row_valid = ttok < it.nvalid && r < p.q_tile_tokens * p.group;
             const int row_limit = it.causal ? it.pos0 + ttok : 0x7fffffff;
             const int tile_limit_min = it.causal ? it.pos0 : 0x7fffffff;
+            // windowed: the first row's lowest key behind the sinks (packed)
+            const int low_first = WIN ? it.pos0 - p.win.window + 1 : 0;
             float m_used = -INFINITY, l = 0.f;
             // scores in log2 units; an fp8 pool's K scale folds in here
             const float sl2 = p.k_scale ? p.scale_log2 * __ldg(p.k_scale + it.h) : p.scale_log2;
@@ -556,9 +587,27 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->s_free[sb]);
                 const int kb = it.key_begin + j * kLongKeys;
-                const bool need_mask =
+                bool need_mask =
                     (kb + kLongKeys - 1 > tile_limit_min) || (kb + kLongKeys > it.key_end);
-                if (need_mask) {
+                if constexpr (WIN)
+                    // below the last row's window and not sinks alone
+                    need_mask = need_mask ||
+                                (kb < low_first + it.nvalid - 1 && kb + kLongKeys > p.win.sinks);
+                if (WIN && need_mask) {
+                    // bit i: key kb + c0 + i is visible to this row -- below
+                    // the causal limit and a sink or at or past the row's low
+                    const int at = kb + c0;
+                    const uint64_t seen = low_bits(min(row_limit, it.key_end - 1) + 1 - at) &
+                                          (low_bits(p.win.sinks - at) |
+                                           ~low_bits(row_limit - p.win.window + 1 - at));
+                    const uint32_t seen0 = static_cast<uint32_t>(seen);
+                    const uint32_t seen1 = static_cast<uint32_t>(seen >> 32);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        if (!(seen0 & (1u << i))) s0[i] = __float_as_uint(-INFINITY);
+                        if (!(seen1 & (1u << i))) s1[i] = __float_as_uint(-INFINITY);
+                    }
+                } else if (need_mask) {
                     // keys [0, lim) of this half are visible to this row
                     const int lim = min(row_limit, it.key_end - 1) - (kb + c0) + 1;
 #pragma unroll
@@ -644,6 +693,26 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
                     }
                     tmem_wait_st();
                 }
+                bool zeroed = kb + kLongKeys > it.key_end;
+                if constexpr (WIN) {
+                    // keys that no row sees between the sinks and the first
+                    // row's window share chunks with visible ones (at most 30 of
+                    // them): their V rows may hold anything too
+                    const int z0 = max(p.win.sinks - kb, 0), z1 = min(low_first - kb, kLongKeys);
+                    if (z0 < z1) {
+                        zeroed = true;
+                        const int vs = tt % kVStages;
+                        if (!warp_wait(&bars->v_full[vs], (tt / kVStages) & 1, abort_flag)) { ok = false; break; }
+                        const int pieces = (z1 - z0) * 8 * G::kHalves;
+                        for (int q = r + half * 128; q < pieces; q += 256) {
+                            const int hf = q / ((z1 - z0) * 8);
+                            const int rem = q - hf * (z1 - z0) * 8;
+                            *reinterpret_cast<uint4 *>(sV + vs * G::kKVBytes + hf * G::kHalfBytes +
+                                                       (z0 + rem / 8) * 128 + (rem % 8) * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                }
                 if (kb + kLongKeys > it.key_end) {
                     // the last loaded chunk may extend past the keys: zero those V
                     // rows so 0-probabilities never meet non-finite cache contents
@@ -661,7 +730,7 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
                     }
                 }
                 tmem_wait_st();
-                if (kb + kLongKeys > it.key_end) fence_proxy_async_smem();  // zeroed V rows
+                if (zeroed) fence_proxy_async_smem();  // zeroed V rows
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->p_full[sb]);
@@ -853,37 +922,40 @@ size_t long_smem_bytes(int head_dim) {
     return head_dim == 128 ? LongGeom<128>::kSmemBytes : LongGeom<64>::kSmemBytes;
 }
 
-template <int D>
+template <int D, bool WIN>
 static int configure_long() {
     static PerDeviceOnce once;
     return once_per_device(once, [] {
-        return cudaFuncSetAttribute(long_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(long_kernel<D, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     LongGeom<D>::kSmemBytes);
     });
+}
+
+template <int D, bool WIN>
+static int launch(const LongParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
+                  const CUtensorMap &tv, int grid, cudaStream_t s) {
+    if (configure_long<D, WIN>() != PA_OK) return PA_ERR_CUDA;
+    const bool pdl = p.overlap_prev != 0 || p.wait_start != 0;
+    PdlLaunch l(grid, 32 * kLongWarps, LongGeom<D>::kSmemBytes, s, pdl);
+    return launch_kernel(l, long_kernel<D, WIN>, p, tq, tk, tv) == cudaSuccess ? PA_OK
+                                                                               : PA_ERR_CUDA;
 }
 
 // grid: the caller passes an upper bound on the number of items; the kernel is
 // persistent, so at most one CTA per SM is launched.
 int launch_long(const LongParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
-                const CUtensorMap &tv, int head_dim, int grid, cudaStream_t s) {
+                const CUtensorMap &tv, int head_dim, bool windowed, int grid, cudaStream_t s) {
     if (grid <= 0) return PA_OK;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return PA_ERR_CUDA;
     grid = grid < sms ? grid : sms;
-    const bool pdl = p.overlap_prev != 0 || p.wait_start != 0;
-    if (head_dim == 128) {
-        if (configure_long<128>() != PA_OK) return PA_ERR_CUDA;
-        PdlLaunch l(grid, 32 * kLongWarps, LongGeom<128>::kSmemBytes, s, pdl);
-        return launch_kernel(l, long_kernel<128>, p, tq, tk, tv) == cudaSuccess
-                   ? PA_OK
-                   : PA_ERR_CUDA;
-    }
-    if (configure_long<64>() != PA_OK) return PA_ERR_CUDA;
-    PdlLaunch l(grid, 32 * kLongWarps, LongGeom<64>::kSmemBytes, s, pdl);
-    return launch_kernel(l, long_kernel<64>, p, tq, tk, tv) == cudaSuccess ? PA_OK
-                                                                                    : PA_ERR_CUDA;
+    if (windowed)
+        return head_dim == 128 ? launch<128, true>(p, tq, tk, tv, grid, s)
+                               : launch<64, true>(p, tq, tk, tv, grid, s);
+    return head_dim == 128 ? launch<128, false>(p, tq, tk, tv, grid, s)
+                           : launch<64, false>(p, tq, tk, tv, grid, s);
 }
 
 }  // namespace pa

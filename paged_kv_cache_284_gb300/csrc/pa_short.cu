@@ -115,6 +115,22 @@ struct Consumer {
     float sl2, vsc;  // score scale (log2 units) and value scale
     bool swapped;    // fp8 pool, R <= 8: S^T = K Q^T and O^T = V^T P^T
     bool active;
+    // Windowed step (packed keys): rows see keys below `sinks` and from their
+    // own low0 / low1 on; low_first and low_last are the first and the last
+    // row's.  A key in [sinks, low_first) is seen by no row.
+    int sinks, low0, low1, low_first, low_last;
+    // keys key .. key + 15 are below no row's window (or all are sinks)
+    __device__ __forceinline__ bool all_in_window(int key) const {
+        return key >= low_last || key + kChunkKeys <= sinks;
+    }
+    __device__ __forceinline__ bool in_window(int key, int low) const {
+        return key < sinks || key >= low;
+    }
+    // some row sees it, causal limits aside: V rows of other keys may hold
+    // anything and are zeroed
+    __device__ __forceinline__ bool live(int key) const {
+        return key < key_end && in_window(key, low_first);
+    }
     // per thread: rows g and g+8 of this warp's 16-row tile
     int limit0, limit1;
     uint32_t qa[KS][4];
@@ -127,13 +143,14 @@ struct Consumer {
 // item's keys.  The TMA row is computed from it by chunk_row_from, later, so
 // that the load's latency overlaps the stages issued in between.  An
 // out-of-range table column is clamped and flagged.
+template <bool WIN>
 __device__ __forceinline__ int chunk_blk_load(const ShortParams &p, const ShortItem &item, int L,
                                               int first_stage, int lane, bool &has) {
     const int key_end = min(item.stage_end * kStageKeys, L);
     const int key0 = (first_stage * kStageChunks + lane) * kChunkKeys;
     has = key0 < key_end;
     if (!has) return 0;
-    int col = key0 / p.block_size;
+    int col = (WIN ? unpacked_key(key0, item.sink_chunks, item.gap) : key0) / p.block_size;
     if (col >= p.bt_stride) {  // seq_len beyond the table row
         flag_status(p.status, PA_DEV_BAD_METADATA);
         col = p.bt_stride - 1;
@@ -142,14 +159,16 @@ __device__ __forceinline__ int chunk_blk_load(const ShortParams &p, const ShortI
 }
 // TMA row coordinate (cache row = (block, kv head h, offset)) of that chunk,
 // or -1 without one; an out-of-range block id is clamped and flagged.
-__device__ __forceinline__ int chunk_row_from(const ShortParams &p, int blk, bool has, int h,
-                                              int first_stage, int lane) {
+template <bool WIN>
+__device__ __forceinline__ int chunk_row_from(const ShortParams &p, const ShortItem &item, int blk,
+                                              bool has, int h, int first_stage, int lane) {
     if (!has) return -1;
     if (blk < 0 || blk >= p.num_blocks) {
         flag_status(p.status, PA_DEV_BAD_BLOCK);
         blk = min(max(blk, 0), p.num_blocks - 1);
     }
-    const int key0 = (first_stage * kStageChunks + lane) * kChunkKeys;
+    int key0 = (first_stage * kStageChunks + lane) * kChunkKeys;
+    if constexpr (WIN) key0 = unpacked_key(key0, item.sink_chunks, item.gap);
     return (blk * p.num_kv_heads + h) * p.block_size + key0 % p.block_size;
 }
 
@@ -186,7 +205,7 @@ __device__ __forceinline__ ShortItem short_work(const ShortParams &p, int idx, i
 // [2] = (2t, 16cc+2g+1), [3] = (2t+1, 16cc+2g+1).  CHECK = false: every
 // key of the chunks is below the item's end and visible to every row (the
 // caller checked), so the masks and the V-tail zeroing are compiled out.
-template <int D, int NC, bool CHECK>
+template <int D, int NC, bool CHECK, bool WIN>
 __device__ __forceinline__ void swapped_chunks(Consumer<D> &cs, const uint32_t (&kb)[NC],
                                                const uint32_t (&vb)[NC], const int (&key0)[NC],
                                                int lane) {
@@ -224,14 +243,17 @@ __device__ __forceinline__ void swapped_chunks(Consumer<D> &cs, const uint32_t (
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
         const bool need_mask =
-            CHECK && ((key0[n] + kChunkKeys - 1 > cs.ctx) || (key0[n] + kChunkKeys > cs.key_end));
+            CHECK && ((key0[n] + kChunkKeys - 1 > cs.ctx) || (key0[n] + kChunkKeys > cs.key_end) ||
+                      (WIN && !cs.all_in_window(key0[n])));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             s[n][e] = (st[n][0][e] + st[n][1][e]) * cs.sl2;
             if (need_mask) {
                 const int key = key0[n] + g + (e >> 1) * 8;
                 const int lim = (e & 1) ? cs.limit1 : cs.limit0;
-                if (key > lim || key >= cs.key_end) s[n][e] = -INFINITY;
+                if (key > lim || key >= cs.key_end ||
+                    (WIN && !cs.in_window(key, (e & 1) ? cs.low1 : cs.low0)))
+                    s[n][e] = -INFINITY;
             }
         }
     }
@@ -290,6 +312,13 @@ __device__ __forceinline__ void swapped_chunks(Consumer<D> &cs, const uint32_t (
         k1[n] = 2 * t + 1 < nvalid;
         k8[n] = 2 * t + 8 < nvalid;
         k9[n] = 2 * t + 9 < nvalid;
+        if constexpr (WIN && CHECK) {
+            tail[n] = tail[n] || !cs.all_in_window(key0[n]);
+            k0[n] = cs.live(key0[n] + 2 * t);
+            k1[n] = cs.live(key0[n] + 2 * t + 1);
+            k8[n] = cs.live(key0[n] + 2 * t + 8);
+            k9[n] = cs.live(key0[n] + 2 * t + 9);
+        }
     }
 #pragma unroll
     for (int c2 = 0; c2 < D / 32; ++c2) {
@@ -417,7 +446,7 @@ __device__ __forceinline__ void swapped_epilogue(Consumer<D> &cs, const ShortPar
 
 }  // namespace
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool WIN>
 __global__ void __launch_bounds__(kShortThreads, 2)
     short_kernel(const ShortParams p, const __grid_constant__ CUtensorMap tmk,
                  const __grid_constant__ CUtensorMap tmv) {
@@ -508,10 +537,10 @@ __global__ void __launch_bounds__(kShortThreads, 2)
         ShortItem cur = short_work(p, min(cur_idx, p.max_items - 1), cur_h);
         if (cur_idx < num_items) {
             bool has;
-            const int blk = chunk_blk_load(p, cur, cur.seq_len, cur.stage_begin, lane, has);
+            const int blk = chunk_blk_load<WIN>(p, cur, cur.seq_len, cur.stage_begin, lane, has);
             cur_q0 = __ldg(p.qsl + cur.b);
             cur_ctx = __ldg(p.ctx + cur.b);
-            cur_row = chunk_row_from(p, blk, has, cur_h, cur.stage_begin, lane);
+            cur_row = chunk_row_from<WIN>(p, cur, blk, has, cur_h, cur.stage_begin, lane);
         }
         while (!aborted) {
             if (cur_idx >= num_items) {
@@ -551,10 +580,11 @@ __global__ void __launch_bounds__(kShortThreads, 2)
                 if (rel % G::kRSB == 0) {
                     // this batch's rows from the block ids loaded a batch ago;
                     // then the next batch's ids, used only a batch from now
-                    if (rel > 0) batch_row = chunk_row_from(p, next_blk, next_has, cur_h, st, lane);
+                    if (rel > 0)
+                        batch_row = chunk_row_from<WIN>(p, cur, next_blk, next_has, cur_h, st, lane);
                     next_has = false;
                     if (rel + G::kRSB < nrs)
-                        next_blk = chunk_blk_load(p, cur, cur.seq_len, st + 8, lane, next_has);
+                        next_blk = chunk_blk_load<WIN>(p, cur, cur.seq_len, st + 8, lane, next_has);
                 }
                 if (rel == rel_claim && lane == 0)
                     nxt_idx = atomicAdd(&p.hdr->short_next, 1) + first_static;
@@ -569,8 +599,8 @@ __global__ void __launch_bounds__(kShortThreads, 2)
                         pf = 1;
                     } else {
                         if (nxt_idx < num_items) {
-                            nxt_blk = chunk_blk_load(p, nxt, nxt.seq_len, nxt.stage_begin, lane,
-                                                     nxt_has);
+                            nxt_blk = chunk_blk_load<WIN>(p, nxt, nxt.seq_len, nxt.stage_begin,
+                                                          lane, nxt_has);
                             nxt_q0 = __ldg(p.qsl + nxt.b);
                             nxt_ctx = __ldg(p.ctx + nxt.b);
                         }
@@ -614,7 +644,7 @@ __global__ void __launch_bounds__(kShortThreads, 2)
                         ii.seq_len = cur.seq_len;
                         ii.stage_end = cur.stage_end;
                         ii.tok0 = cur_q0;
-                        ii.ctx = cur_ctx;
+                        ii.ctx = WIN ? cur_ctx - cur.gap * kChunkKeys : cur_ctx;
                         info[slot] = ii;
                     }
                     mbar_arrive_expect_tx(&full[slot],
@@ -637,7 +667,8 @@ __global__ void __launch_bounds__(kShortThreads, 2)
             cur = nxt;
             cur_h = nxt_h;
             cur_row = cur_idx < num_items
-                          ? chunk_row_from(p, nxt_blk, nxt_has, nxt_h, nxt.stage_begin, lane)
+                          ? chunk_row_from<WIN>(p, nxt, nxt_blk, nxt_has, nxt_h, nxt.stage_begin,
+                                                lane)
                           : -1;
             cur_q0 = nxt_q0;
             cur_ctx = nxt_ctx;
@@ -705,6 +736,13 @@ __global__ void __launch_bounds__(kShortThreads, 2)
             const int r0 = cs.rt * 16 + g, r1 = r0 + 8;
             cs.limit0 = r0 < cs.R ? cs.ctx + r0 / p.group : -1;
             cs.limit1 = r1 < cs.R ? cs.ctx + r1 / p.group : -1;
+            if constexpr (WIN) {
+                cs.sinks = p.win.sinks;
+                cs.low_first = cs.ctx - p.win.window + 1;
+                cs.low_last = cs.low_first + n - 1;
+                cs.low0 = cs.low_first + r0 / p.group;
+                cs.low1 = cs.low_first + r1 / p.group;
+            }
             if (FP8 && cs.swapped) {
                 // lane: rows 2t and 2t+1 of the scores, q row g of Q^T; Q^T
                 // fragment of k-step ks = q row g, dims 16ks+4t .. +3 (the
@@ -712,6 +750,10 @@ __global__ void __launch_bounds__(kShortThreads, 2)
                 const int ra = 2 * t, rb = 2 * t + 1;
                 cs.limit0 = ra < cs.R ? cs.ctx + ra / p.group : -1;
                 cs.limit1 = rb < cs.R ? cs.ctx + rb / p.group : -1;
+                if constexpr (WIN) {
+                    cs.low0 = cs.low_first + ra / p.group;
+                    cs.low1 = cs.low_first + rb / p.group;
+                }
                 const __nv_bfloat16 *qg = nullptr;
                 if (g < cs.R)
                     qg = p.q + (static_cast<int64_t>(cs.tok0 + g / p.group) * p.num_q_heads +
@@ -788,15 +830,16 @@ __global__ void __launch_bounds__(kShortThreads, 2)
                         // key of either chunk needs a mask (one uniform
                         // branch instead of ten per stage)
                         const int last = kb2 + kChunkKeys - 1;
-                        if (last < cs.key_end && last <= cs.ctx)
-                            swapped_chunks<D, 2, false>(cs, kbs, vbs, ks0, lane);
+                        if (last < cs.key_end && last <= cs.ctx &&
+                            (!WIN || (cs.all_in_window(ka) && cs.all_in_window(kb2))))
+                            swapped_chunks<D, 2, false, WIN>(cs, kbs, vbs, ks0, lane);
                         else
-                            swapped_chunks<D, 2, true>(cs, kbs, vbs, ks0, lane);
+                            swapped_chunks<D, 2, true, WIN>(cs, kbs, vbs, ks0, lane);
                     } else {
                         const uint32_t kbs[1] = {smem_u32(k_box(slot, cs.kq, 0))};
                         const uint32_t vbs[1] = {smem_u32(v_box(slot, cs.kq, 0))};
                         const int ks0[1] = {ka};
-                        swapped_chunks<D, 1, true>(cs, kbs, vbs, ks0, lane);
+                        swapped_chunks<D, 1, true, WIN>(cs, kbs, vbs, ks0, lane);
                     }
                 }
             }
@@ -852,7 +895,8 @@ __global__ void __launch_bounds__(kShortThreads, 2)
                     }
                     // scale to log2 units and mask (causal limit per row, item key range)
                     const bool need_mask = CHECK && ((key0 + kChunkKeys - 1 > cs.ctx) ||
-                                                     (key0 + kChunkKeys > cs.key_end));
+                                                     (key0 + kChunkKeys > cs.key_end) ||
+                                                     (WIN && !cs.all_in_window(key0)));
 #pragma unroll
                     for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
@@ -861,7 +905,9 @@ __global__ void __launch_bounds__(kShortThreads, 2)
                             if (need_mask) {
                                 const int key = key0 + nt * 8 + 2 * t + (e & 1);
                                 const int lim = (e < 2) ? cs.limit0 : cs.limit1;
-                                if (key > lim || key >= cs.key_end) s = -INFINITY;
+                                if (key > lim || key >= cs.key_end ||
+                                    (WIN && !cs.in_window(key, (e < 2) ? cs.low0 : cs.low1)))
+                                    s = -INFINITY;
                             }
                             sacc[nt][e] = s;
                         }
@@ -907,9 +953,16 @@ __global__ void __launch_bounds__(kShortThreads, 2)
                     // V rows past the item's keys may hold anything (even NaN):
                     // zero them in the fragments of a partially valid chunk.
                     const int nvalid = cs.key_end - key0;
-                    const bool tail = CHECK && nvalid < kChunkKeys;
-                    const bool k0 = 2 * t < nvalid, k1 = 2 * t + 1 < nvalid;
-                    const bool k8 = 2 * t + 8 < nvalid, k9 = 2 * t + 9 < nvalid;
+                    bool tail = CHECK && nvalid < kChunkKeys;
+                    bool k0 = 2 * t < nvalid, k1 = 2 * t + 1 < nvalid;
+                    bool k8 = 2 * t + 8 < nvalid, k9 = 2 * t + 9 < nvalid;
+                    if constexpr (WIN && CHECK) {
+                        tail = tail || !cs.all_in_window(key0);
+                        k0 = cs.live(key0 + 2 * t);
+                        k1 = cs.live(key0 + 2 * t + 1);
+                        k8 = cs.live(key0 + 2 * t + 8);
+                        k9 = cs.live(key0 + 2 * t + 9);
+                    }
                     if constexpr (FP8) {
 #pragma unroll
                         for (int c2 = 0; c2 < D / 32; ++c2) {
@@ -957,7 +1010,8 @@ __global__ void __launch_bounds__(kShortThreads, 2)
                         }
                     }
                 };
-                if (key0 + kChunkKeys - 1 > cs.ctx || key0 + kChunkKeys > cs.key_end)
+                if (key0 + kChunkKeys - 1 > cs.ctx || key0 + kChunkKeys > cs.key_end ||
+                    (WIN && !cs.all_in_window(key0)))
                     chunk(std::true_type{});
                 else
                     chunk(std::false_type{});
@@ -1164,46 +1218,58 @@ size_t short_smem_bytes(int head_dim) {
     return head_dim == 128 ? ShortGeom<128, false>::kSmemBytes : ShortGeom<64, false>::kSmemBytes;
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool WIN>
 static int configure_short() {
     static PerDeviceOnce once;
     return once_per_device(once, [] {
-        return cudaFuncSetAttribute(short_kernel<D, FP8>,
+        return cudaFuncSetAttribute(short_kernel<D, FP8, WIN>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     ShortGeom<D, FP8>::kSmemBytes);
     });
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool WIN>
 static int max_ctas() {
     int n = 0;
-    if (configure_short<D, FP8>() != PA_OK) return 1;
-    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, short_kernel<D, FP8>, kShortThreads,
+    if (configure_short<D, FP8, WIN>() != PA_OK) return 1;
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, short_kernel<D, FP8, WIN>, kShortThreads,
                                                   ShortGeom<D, FP8>::kSmemBytes);
     return n > 0 ? n : 1;
 }
 
-int short_max_ctas_per_sm(int head_dim, bool fp8) {
-    if (fp8) return max_ctas<128, true>();
-    return head_dim == 128 ? max_ctas<128, false>() : max_ctas<64, false>();
+template <bool WIN>
+static int max_ctas_of(int head_dim, bool fp8) {
+    if (fp8) return max_ctas<128, true, WIN>();
+    return head_dim == 128 ? max_ctas<128, false, WIN>() : max_ctas<64, false, WIN>();
 }
 
-template <int D, bool FP8>
+int short_max_ctas_per_sm(int head_dim, bool fp8, bool windowed) {
+    return windowed ? max_ctas_of<true>(head_dim, fp8) : max_ctas_of<false>(head_dim, fp8);
+}
+
+template <int D, bool FP8, bool WIN>
 static int launch(const ShortParams &p, const CUtensorMap &tk, const CUtensorMap &tv, int grid,
                   cudaStream_t s) {
-    if (configure_short<D, FP8>() != PA_OK) return PA_ERR_CUDA;
+    if (configure_short<D, FP8, WIN>() != PA_OK) return PA_ERR_CUDA;
     PdlLaunch l(grid, kShortThreads, ShortGeom<D, FP8>::kSmemBytes, s);
-    return launch_kernel(l, short_kernel<D, FP8>, p, tk, tv) == cudaSuccess
-               ? PA_OK
-               : PA_ERR_CUDA;
+    return launch_kernel(l, short_kernel<D, FP8, WIN>, p, tk, tv) == cudaSuccess ? PA_OK
+                                                                                 : PA_ERR_CUDA;
+}
+
+template <bool WIN>
+static int launch_of(const ShortParams &p, const CUtensorMap &tk, const CUtensorMap &tv,
+                     int head_dim, bool fp8, int grid, cudaStream_t s) {
+    if (fp8)
+        return head_dim == 128 ? launch<128, true, WIN>(p, tk, tv, grid, s) : PA_ERR_UNSUPPORTED;
+    return head_dim == 128 ? launch<128, false, WIN>(p, tk, tv, grid, s)
+                           : launch<64, false, WIN>(p, tk, tv, grid, s);
 }
 
 int launch_short(const ShortParams &p, const CUtensorMap &tk, const CUtensorMap &tv,
-                 int head_dim, bool fp8, int grid, cudaStream_t s) {
+                 int head_dim, bool fp8, bool windowed, int grid, cudaStream_t s) {
     if (grid <= 0) return PA_OK;
-    if (fp8) return head_dim == 128 ? launch<128, true>(p, tk, tv, grid, s) : PA_ERR_UNSUPPORTED;
-    return head_dim == 128 ? launch<128, false>(p, tk, tv, grid, s)
-                           : launch<64, false>(p, tk, tv, grid, s);
+    return windowed ? launch_of<true>(p, tk, tv, head_dim, fp8, grid, s)
+                    : launch_of<false>(p, tk, tv, head_dim, fp8, grid, s);
 }
 
 }  // namespace pa

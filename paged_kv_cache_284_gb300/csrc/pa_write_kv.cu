@@ -174,12 +174,14 @@ __device__ __forceinline__ void decode_block(const uint4 *__restrict__ kc8,
 // kernel: staging block k of staged request b (k = stage_base[b] + j) holds
 // block j of b's table decoded to bf16.  Grid-stride over staging blocks;
 // thread 0 finds the request of a block by binary search over the staged
-// requests' first blocks.
+// requests' first blocks.  A windowed step stages the visible blocks alone.
+template <bool WIN>
 __global__ void __launch_bounds__(256) stage_fp8_kernel(
     const uint4 *__restrict__ kc8, const uint4 *__restrict__ vc8, int num_blocks,
     int pieces_per_block, const int32_t *__restrict__ bt, int bt_stride, const PlanHeader *hdr,
     const int *stage_base, const int *stage_list, uint4 *__restrict__ sk, uint4 *__restrict__ sv,
-    unsigned *status) {
+    unsigned *status, const int *__restrict__ ctx, const int *__restrict__ seq_lens,
+    const WindowArgs win, int block_size) {
     pdl_wait();  // the plan that chose the staged requests
     pdl_trigger();
     __shared__ int s_src;
@@ -193,7 +195,12 @@ __global__ void __launch_bounds__(256) stage_fp8_kernel(
                 if (__ldcg(stage_base + __ldcg(stage_list + mid)) <= k) lo = mid; else hi = mid - 1;
             }
             const int b = __ldcg(stage_list + lo);
-            const int j = k - __ldcg(stage_base + b);
+            int j = k - __ldcg(stage_base + b);
+            if constexpr (WIN) {
+                const BlockSpan bsp =
+                    block_span(win, __ldg(ctx + b), __ldg(seq_lens + b), block_size);
+                if (j >= bsp.sink_blocks) j += bsp.gap;
+            }
             int src = (j < bt_stride) ? __ldg(bt + static_cast<int64_t>(b) * bt_stride + j) : -1;
             if (src < 0 || src >= num_blocks) {
                 flag_status(status, PA_DEV_BAD_BLOCK);
@@ -209,16 +216,18 @@ __global__ void __launch_bounds__(256) stage_fp8_kernel(
 
 int launch_stage_fp8(const pa_kv_desc *kv, const int32_t *block_tables, int32_t bt_stride,
                      const PlanHeader *hdr, const int *stage_base, const int *stage_list,
-                     void *stage_k, void *stage_v, unsigned *status, int grid, cudaStream_t s) {
+                     void *stage_k, void *stage_v, unsigned *status, int grid, cudaStream_t s,
+                     const int *ctx, const int *seq_lens, const WindowArgs *win) {
     if (grid <= 0) return PA_OK;
     // 16 codes per piece; a block holds num_kv_heads * block_size * head_dim codes
     const int pieces = kv->num_kv_heads * kv->block_size * kv->head_dim / 16;
     PdlLaunch l(static_cast<unsigned>(grid), 256, 0, s);
     const cudaError_t e = launch_kernel(
-        l, stage_fp8_kernel, static_cast<const uint4 *>(kv->k_cache),
-        static_cast<const uint4 *>(kv->v_cache), kv->num_blocks, pieces, block_tables, bt_stride,
-        hdr, stage_base, stage_list, static_cast<uint4 *>(stage_k), static_cast<uint4 *>(stage_v),
-        status);
+        l, win ? stage_fp8_kernel<true> : stage_fp8_kernel<false>,
+        static_cast<const uint4 *>(kv->k_cache), static_cast<const uint4 *>(kv->v_cache),
+        kv->num_blocks, pieces, block_tables, bt_stride, hdr, stage_base, stage_list,
+        static_cast<uint4 *>(stage_k), static_cast<uint4 *>(stage_v), status, ctx, seq_lens,
+        win ? *win : WindowArgs{}, kv->block_size);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
