@@ -1110,13 +1110,13 @@ int pa_rope_write_kv(const void *q, int64_t q_stride, const void *k, int64_t k_s
     p.num_kv_heads = kv->num_kv_heads;
     p.head_dim = kv->head_dim;
     p.block_size = kv->block_size;
-    p.num_blocks = kv->num_blocks;
+    p.num_slots = static_cast<int64_t>(kv->num_blocks) * kv->block_size;
     p.rot_dim = rope->rot_dim;
     p.num_axes = rope->num_axes;
     p.adjacent = rope->adjacent;
     p.attn_factor = rope->attn_factor;
     p.status = dev->status;
-    rc = launch_rope_write(p, static_cast<cudaStream_t>(stream));
+    rc = launch_rope_write(p, dev->sms, static_cast<cudaStream_t>(stream));
     return rc == PA_OK ? PA_OK : fail(rc, "rope_write_kv launch failed");
 }
 

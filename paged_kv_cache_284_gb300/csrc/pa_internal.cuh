@@ -285,9 +285,11 @@ struct RopeParams {
     __nv_bfloat16 *q_out;
     void *k_cache, *v_cache;
     const float *k_scale, *v_scale;  // fp8 pool only
-    int num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks;
+    int num_tokens, num_q_heads, num_kv_heads, head_dim, block_size;
     int rot_dim, num_axes, adjacent, fp8;
     float attn_factor;
+    int64_t num_slots;      // num_blocks * block_size
+    int parts, part_heads;  // a token's heads (q, k, v in turn) in runs of part_heads
     unsigned *status;
 };
 
@@ -362,7 +364,7 @@ int launch_stage_fp8(const pa_kv_desc *kv, const int32_t *block_tables, int32_t 
 int launch_stage_prefix_fp8(const pa_kv_desc *kv, const int32_t *prefix_blocks, int n,
                             int32_t *ident, void *stage_k, void *stage_v, unsigned *status,
                             int grid, cudaStream_t s);
-int launch_rope_write(const RopeParams &p, cudaStream_t s);
+int launch_rope_write(RopeParams p, int sms, cudaStream_t s);
 int launch_copy_blocks(const pa_kv_desc *kv, int num_layers, const int32_t *pairs, int num_pairs,
                        int sms, unsigned *status, cudaStream_t s);
 int launch_plan(const PlanParams &p, cudaStream_t s);
