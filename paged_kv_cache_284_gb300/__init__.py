@@ -329,14 +329,35 @@ def pa_write_kv_attention(k, v, slot_mapping, q, k_cache, v_cache, block_tables,
     return workspace
 
 
-def _same_device(device: torch.device, tensors):
-    """The calls run on the current device: every tensor must live there."""
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, the current device is "
+def _explain(device: int, tensors):
+    """Raise for the first (name, tensor, dtype) that is not a contiguous tensor
+    of that type on the current device; dtype None: device alone."""
+    for name, t, dtype in tensors:
+        if t is None:
+            continue
+        if dtype is not None:
+            _need(t, name, dtype)
+        elif not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+    if device != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
-    for name, t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _raw_stream(stream, device: int) -> int:
+    # the current stream's handle without building a Stream object (1 us of a
+    # small step's host time)
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
+_BF16, _I32, _I64, _F32, _F64 = (torch.bfloat16, torch.int32, torch.int64, torch.float32,
+                                 torch.float64)
+
+
+def _off(t, dtype, device: int) -> bool:
+    return t.dtype is not dtype or t.get_device() != device or not t.is_contiguous()
 
 
 def pa_window_attention(q, k_cache, v_cache, block_tables, query_start_loc, context_lens, seq_lens,
@@ -347,51 +368,60 @@ def pa_window_attention(q, k_cache, v_cache, block_tables, query_start_loc, cont
     e4m3 pools as in pa_attention; blocks of which no row of their request
     sees a key may have any table entry (staging_blocks counts the visible
     blocks of the long requests).  Returns the workspace tensor used."""
-    _need(q, "q", torch.bfloat16)
-    _need(out, "out", torch.bfloat16)
-    for name, t in (("block_tables", block_tables), ("query_start_loc", query_start_loc),
-                    ("context_lens", context_lens), ("seq_lens", seq_lens)):
-        _need(t, name, torch.int32)
-    if lse is not None:
-        _need(lse, "lse", torch.float32)
+    dev = q.get_device()
+    if (_off(q, _BF16, dev) or _off(out, _BF16, dev) or _off(block_tables, _I32, dev) or
+            _off(query_start_loc, _I32, dev) or _off(context_lens, _I32, dev) or
+            _off(seq_lens, _I32, dev) or (lse is not None and _off(lse, _F32, dev)) or dev < 0 or
+            dev != torch._C._cuda_getDevice() or k_cache.get_device() != dev or
+            v_cache.get_device() != dev or
+            (workspace is not None and workspace.get_device() != dev) or
+            (k_scale is not None and (k_scale.get_device() != dev or v_scale.get_device() != dev))):
+        _explain(dev, (("q", q, _BF16), ("out", out, _BF16), ("block_tables", block_tables, _I32),
+                       ("query_start_loc", query_start_loc, _I32),
+                       ("context_lens", context_lens, _I32), ("seq_lens", seq_lens, _I32),
+                       ("lse", lse, _F32), ("k_cache", k_cache, None), ("v_cache", v_cache, None),
+                       ("workspace", workspace, None), ("k_scale", k_scale, None),
+                       ("v_scale", v_scale, None)))
     kv = kv_desc(k_cache, v_cache, k_scale, v_scale)
-    T, hq, d = q.shape
-    B = int(seq_lens.shape[0])
-    if d != kv.head_dim or out.shape != q.shape or (lse is not None and lse.shape != q.shape[:2]):
+    shape = q.shape
+    T, hq, d = shape
+    B = seq_lens.numel()
+    tables = block_tables.shape
+    if d != kv.head_dim or out.shape != shape or (lse is not None and lse.shape != shape[:2]):
         raise ValueError("q and out must be [T, Hq, head_dim], lse [T, Hq]")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape[0] != B or \
-            query_start_loc.shape[0] != B + 1:
+    if len(tables) != 2 or tables[0] != B or context_lens.numel() != B or \
+            query_start_loc.numel() != B + 1:
         raise ValueError("block_tables [B, N], query_start_loc [B + 1], context_lens [B] and "
                          "seq_lens [B] must agree")
-    _same_device(q.device, (("out", out), ("lse", lse), ("k_cache", k_cache),
-                            ("v_cache", v_cache), ("block_tables", block_tables),
-                            ("query_start_loc", query_start_loc), ("context_lens", context_lens),
-                            ("seq_lens", seq_lens), ("k_scale", k_scale), ("v_scale", v_scale),
-                            ("workspace", workspace)))
-    need = workspace_size(B, T, hq, kv.num_kv_heads, kv.head_dim)
-    if kv.kv_dtype == PA_KV_FP8_E4M3 and staging_blocks > 0:
-        need += fp8_staging_bytes(kv.num_kv_heads, kv.head_dim, kv.block_size, staging_blocks)
-    if workspace is None or workspace.numel() < need:
+    L = lib()
+    need = L.pa_attention_workspace_size(B, T, hq, kv.num_kv_heads, d)
+    if staging_blocks > 0 and kv.kv_dtype == PA_KV_FP8_E4M3:
+        need += L.pa_fp8_staging_bytes(kv.num_kv_heads, d, kv.block_size, int(staging_blocks))
+    room = 0 if workspace is None else workspace.nbytes
+    if room < need:
         workspace = alloc_workspace(need, q.device)
-    _check(lib().pa_window_attention(_ptr(q), ctypes.byref(kv), _ptr(block_tables),
-                                     int(block_tables.shape[1]), _ptr(query_start_loc),
-                                     _ptr(context_lens), _ptr(seq_lens), B, T, hq, float(scale),
-                                     int(window), int(num_sinks), _ptr(out), _ptr(lse),
-                                     _ptr(workspace), workspace.numel(), _stream(stream)),
-           "pa_window_attention")
+        room = workspace.nbytes
+    rc = L.pa_window_attention(q.data_ptr(), kv, block_tables.data_ptr(), tables[1],
+                               query_start_loc.data_ptr(), context_lens.data_ptr(),
+                               seq_lens.data_ptr(), B, T, hq, scale, int(window), int(num_sinks),
+                               out.data_ptr(), None if lse is None else lse.data_ptr(),
+                               workspace.data_ptr(), room, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "pa_window_attention")
     return workspace
 
 
-def _token_stride(t: torch.Tensor, name: str) -> int:
-    """Elements between the token rows of a [T, H, d] tensor whose rows are
-    contiguous (a slice of a fused projection, or a whole tensor)."""
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+def _token_rows(t: torch.Tensor, name: str, device: int):
+    """(elements between token rows, T, H, d) of a bf16 [T, H, d] tensor whose
+    rows are contiguous: a slice of a fused projection, or a whole tensor."""
+    if t.dtype is not _BF16:
+        raise TypeError(f"{name} must be {_BF16}, got {t.dtype}")
+    if device < 0 or t.get_device() != device:
+        _explain(device, ((name, t, None),))
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or stride[2] != 1 or (shape[1] > 1 and stride[1] != shape[2]):
         raise ValueError(f"{name} must be [T, H, d] with contiguous rows")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return (stride[0] if shape[0] > 1 else shape[1] * shape[2], *shape)
 
 
 def pa_rope_write_kv(q, k, v, positions, inv_freq, axis, slot_mapping, k_cache, v_cache, q_out,
@@ -402,41 +432,48 @@ def pa_rope_write_kv(q, k, v, positions, inv_freq, axis, slot_mapping, k_cache, 
     one axis); inv_freq float64 [rot_dim / 2]; axis int32 [rot_dim / 2], the
     axis of each frequency, or None for axis 0; q_out bf16 [T, Hq, d] (may be
     a contiguous q).  q and q_out may both be None."""
-    if positions.dim() == 1:
-        positions = positions[None]
-    T = int(k.shape[0])
-    ks, vs = _token_stride(k, "k"), _token_stride(v, "v")
-    hq, qs = 0, 0
+    dev = k.get_device()
+    ks, T, hkv, d = _token_rows(k, "k", dev)
+    vs, Tv, hv, dv = _token_rows(v, "v", dev)
+    qs = hq = 0
     if q is not None:
-        qs, hq = _token_stride(q, "q"), int(q.shape[1])
-        _need(q_out, "q_out", torch.bfloat16)
-        if q_out.shape != q.shape:
+        qs, Tq, hq, dq = _token_rows(q, "q", dev)
+        if Tq != T or dq != d:
+            raise ValueError("k and v must be [T, num_kv_heads, head_dim], q [T, Hq, head_dim]")
+        if q_out is None or q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _need(positions, "positions", torch.int32)
-    _need(slot_mapping, "slot_mapping", torch.int64)
-    _need(inv_freq, "inv_freq", torch.float64)
-    if axis is not None:
-        _need(axis, "axis", torch.int32)
-        if axis.numel() != inv_freq.numel():
-            raise ValueError("axis and inv_freq must have one entry per frequency")
+    if ((q_out is not None and _off(q_out, _BF16, dev)) or _off(positions, _I32, dev) or
+            _off(inv_freq, _F64, dev) or _off(slot_mapping, _I64, dev) or
+            (axis is not None and _off(axis, _I32, dev)) or k_cache.get_device() != dev or
+            v_cache.get_device() != dev or dev != torch._C._cuda_getDevice() or
+            (k_scale is not None and (k_scale.get_device() != dev or v_scale.get_device() != dev))):
+        _explain(dev, (("q_out", q_out, _BF16), ("positions", positions, _I32),
+                       ("inv_freq", inv_freq, _F64), ("slot_mapping", slot_mapping, _I64),
+                       ("axis", axis, _I32), ("k_cache", k_cache, None),
+                       ("v_cache", v_cache, None), ("k_scale", k_scale, None),
+                       ("v_scale", v_scale, None)))
     kv = kv_desc(k_cache, v_cache, k_scale, v_scale)
-    if k.shape != v.shape or k.shape[1] != kv.num_kv_heads or k.shape[2] != kv.head_dim or \
-            (q is not None and (q.shape[0] != T or q.shape[2] != kv.head_dim)):
+    if Tv != T or hv != hkv or dv != d or hkv != kv.num_kv_heads or d != kv.head_dim:
         raise ValueError("k and v must be [T, num_kv_heads, head_dim], q [T, Hq, head_dim]")
-    if positions.dim() != 2 or positions.shape[1] != T or slot_mapping.numel() != T:
+    axes = positions.shape
+    if len(axes) == 1:
+        axes = (1, axes[0])
+    if len(axes) != 2 or axes[1] != T or slot_mapping.numel() != T:
         raise ValueError("positions must be [axes, T], slot_mapping [T]")
-    _same_device(k.device, (("q", q), ("v", v), ("positions", positions), ("inv_freq", inv_freq),
-                            ("axis", axis), ("slot_mapping", slot_mapping), ("k_cache", k_cache),
-                            ("v_cache", v_cache), ("q_out", q_out), ("k_scale", k_scale),
-                            ("v_scale", v_scale)))
-    rope = RopeDesc(inv_freq.data_ptr(), None if axis is None else axis.data_ptr(),
-                    2 * inv_freq.numel(), int(positions.shape[0]), 1 if adjacent else 0,
-                    float(attn_factor))
-    _check(lib().pa_rope_write_kv(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(positions),
-                                  ctypes.byref(rope), _ptr(slot_mapping), T, hq, ctypes.byref(kv),
-                                  _ptr(q_out), _stream(stream)), "pa_rope_write_kv")
+    half = inv_freq.numel()
+    if axis is not None and axis.numel() != half:
+        raise ValueError("axis and inv_freq must have one entry per frequency")
+    rope = RopeDesc(inv_freq.data_ptr(), None if axis is None else axis.data_ptr(), 2 * half,
+                    axes[0], 1 if adjacent else 0, attn_factor)
+    rc = lib().pa_rope_write_kv(None if q is None else q.data_ptr(), qs, k.data_ptr(), ks,
+                                v.data_ptr(), vs, positions.data_ptr(), rope,
+                                slot_mapping.data_ptr(), T, hq, kv,
+                                None if q_out is None else q_out.data_ptr(),
+                                _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "pa_rope_write_kv")
 
 
 class KVLayers:
@@ -445,7 +482,7 @@ class KVLayers:
     def __init__(self, descs, tensors):
         self.descs = descs
         self.tensors = tensors  # keeps the pools alive
-        self.device = tensors[0].device if tensors else None
+        self.device = tensors[0].get_device() if tensors else -1
 
     def __len__(self):
         return len(self.descs)
@@ -479,14 +516,20 @@ def pa_copy_blocks(layers: KVLayers, pairs, stream=None):
     """Copy physical blocks in every layer: pairs int32 [n, 2] of (src, dst) on
     the device (BlockManager.schedule's copies, BlockManager.compact's moves).
     A dst appears once and is no other pair's src; negative ids are padding."""
-    _need(pairs, "pairs", torch.int32)
-    if pairs.dim() != 2 or pairs.shape[1] != 2:
+    if pairs.dtype is not _I32:
+        raise TypeError(f"pairs must be {_I32}, got {pairs.dtype}")
+    shape = pairs.shape
+    if len(shape) != 2 or shape[1] != 2:
         raise ValueError("pairs must be [n, 2]")
-    if len(layers) == 0:
+    if len(layers.descs) == 0:
         return
-    _same_device(layers.device, (("pairs", pairs),))
-    _check(lib().pa_copy_blocks(layers.descs, len(layers), _ptr(pairs), int(pairs.shape[0]),
-                                _stream(stream)), "pa_copy_blocks")
+    dev = layers.device
+    if _off(pairs, _I32, dev) or dev != torch._C._cuda_getDevice():
+        _explain(dev, (("pairs", pairs, _I32),))
+    rc = lib().pa_copy_blocks(layers.descs, len(layers.descs), pairs.data_ptr(), shape[0],
+                              _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "pa_copy_blocks")
 
 
 def pa_validate_copies(pairs, num_blocks):

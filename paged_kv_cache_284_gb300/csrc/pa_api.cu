@@ -491,11 +491,6 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
     pp.fp8 = fp8 ? 1 : 0;
     pp.stage_cap = staged ? stg.cap : 0;
     pp.block_size = kv->block_size;
-    pp.windowed = win ? 1 : 0;
-    if (win) {
-        pp.win = *win;
-        pp.max_keys = max_blocks * kv->block_size;
-    }
     pp.stage_base = staged ? reinterpret_cast<int *>(ws + L.stage_base) : nullptr;
     pp.stage_list = staged ? reinterpret_cast<int *>(ws + L.stage_list) : nullptr;
     pp.split_stages = split_keys / kStageKeys;
@@ -512,6 +507,24 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
     pp.cap_rows = L.cap_rows;
     pp.num_counters = L.num_counters;
     pp.status = dev->status;
+    // a long request has q_len * group > short_max_rows, so there are at
+    // most T / (short_max_rows / group + 1) of them
+    const int min_long_tokens = short_max_rows / group + 1;
+    const int max_long_reqs =
+        forbid_long ? 0 : std::min(num_seqs, T / std::max(1, min_long_tokens));
+    const bool side_by_side =
+        max_long_reqs > 0 && T >= kSideBySideMinTokens && !profiling_active();
+    if (win) {
+        // the windowed planner keeps its table at the end of the partial states
+        pp.win = *win;
+        pp.max_keys = max_blocks * kv->block_size;
+        pp.max_pieces = pieces_bound(num_seqs, T, group);
+        const size_t row = sizeof(float) * D;
+        const int piece_rows = static_cast<int>(
+            (sizeof(WindowPiece) * static_cast<size_t>(pp.max_pieces) + row - 1) / row);
+        pp.cap_rows -= piece_rows;
+        pp.pieces = reinterpret_cast<WindowPiece *>(ws + L.partial_o + row * pp.cap_rows);
+    }
     int rc;
     if (fresh && fresh->num_tokens > 0) {
         // The step's new rows first, as pa_write_kv does: its kernel runs as a
@@ -526,7 +539,7 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
     }
     {
         ProfScope prof(PA_KERNEL_PLAN, s);
-        rc = launch_plan(pp, s);
+        rc = win ? launch_plan_window(pp, s) : launch_plan(pp, s);
     }
     if (rc != PA_OK) return fail(rc, "plan launch failed");
     if (staged) {
@@ -605,7 +618,7 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         LongParams c1 = cp;
         c1.wait_start = 1;
         c1.first_ctas = -1;
-        rc = launch_long(c1, maps.q, *ptk, *ptv, D, false, g1, s);
+        rc = launch_long(c1, maps.q, *ptk, *ptv, D, g1, s);
         if (rc != PA_OK) return fail(rc, "prefix kernel launch failed: %s",
                                      cudaGetErrorString(cudaGetLastError()));
         sp.no_start_wait = 1;
@@ -618,7 +631,7 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         LongParams c2 = cp;
         c2.overlap_prev = 1;
         c2.first_ctas = g1;
-        rc = launch_long(c2, maps.q, *ptk, *ptv, D, false, n_prefix, s);
+        rc = launch_long(c2, maps.q, *ptk, *ptv, D, n_prefix, s);
         if (rc != PA_OK) return fail(rc, "prefix kernel launch failed: %s",
                                      cudaGetErrorString(cudaGetLastError()));
         PrefixFoldParams f{};
@@ -640,11 +653,6 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         return rc == PA_OK ? PA_OK : fail(rc, "cascade fold launch failed");
     }
 
-    // a long request has q_len * group > short_max_rows, so there are at
-    // most T / (short_max_rows / group + 1) of them
-    const int min_long_tokens = short_max_rows / group + 1;
-    const int max_long_reqs =
-        forbid_long ? 0 : std::min(num_seqs, T / std::max(1, min_long_tokens));
     LongParams lp{};
     int long_grid = 0;
     if (max_long_reqs > 0) {
@@ -685,8 +693,12 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
     }
     const CUtensorMap &lk = staged ? stg.tk : maps.k;
     const CUtensorMap &lv = staged ? stg.tv : maps.v;
+    auto tensor_core = [&](const LongParams &params, int grid) {
+        return win ? launch_long_window(params, maps.q, lk, lv, D, grid, dev->sms, s)
+                   : launch_long(params, maps.q, lk, lv, D, grid, s);
+    };
 
-    if (max_long_reqs > 0 && T >= kSideBySideMinTokens && !profiling_active()) {
+    if (side_by_side) {
         // The HBM-bound split-KV kernel and the tensor-core kernel run side by
         // side: a first tensor-core grid takes part of the SMs (it waits
         // for the plan, then lets the next grid in), the split-KV grid fills
@@ -707,7 +719,7 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         // beside the fp8 one, whose rate follows its SM count (707.3 us, 710.1
         // with an eighth)
         const int g1 = std::min(std::max(1, fp8 ? dev->sms / 10 : dev->sms * 2 / 5), long_grid);
-        rc = launch_long(l1, maps.q, lk, lv, D, win != nullptr, g1, s);
+        rc = tensor_core(l1, g1);
         if (rc != PA_OK) return fail(rc, "tensor-core kernel launch failed: %s",
                                      cudaGetErrorString(cudaGetLastError()));
         sp.no_start_wait = 1;
@@ -722,7 +734,7 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         l2.first_done = &hdr->first_done;
         // the test hook waits for one CTA that the first grid never had
         l2.first_ctas = g1 + (stall == PA_TEST_STALL_LAST_GRID ? 1 : 0);
-        rc = launch_long(l2, maps.q, lk, lv, D, win != nullptr, long_grid, s);
+        rc = tensor_core(l2, long_grid);
         if (rc != PA_OK) return fail(rc, "tensor-core kernel launch failed: %s",
                                      cudaGetErrorString(cudaGetLastError()));
         return PA_OK;
@@ -740,7 +752,7 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         lp.overlap_prev = short_grid > 0 ? 1 : 0;
         {
             ProfScope prof(PA_KERNEL_TENSOR_CORE, s);
-            rc = launch_long(lp, maps.q, lk, lv, D, win != nullptr, long_grid, s);
+            rc = tensor_core(lp, long_grid);
         }
         if (rc != PA_OK) return fail(rc, "tensor-core kernel launch failed: %s",
                                      cudaGetErrorString(cudaGetLastError()));
@@ -785,7 +797,7 @@ int run_prefix(const void *q, const pa_kv_desc *kv, const int32_t *prefix_blocks
     int rc = stage_prefix(ps, kv, prefix_blocks, &lp, &tk, &tv, dev, s);
     if (rc != PA_OK) return rc;
     const int grid = kv->num_kv_heads * q_tiles * nsplit;
-    rc = launch_long(lp, maps.q, *tk, *tv, kv->head_dim, false, grid, s);
+    rc = launch_long(lp, maps.q, *tk, *tv, kv->head_dim, grid, s);
     if (rc != PA_OK) return fail(rc, "prefix kernel launch failed");
     if (nsplit > 1) {
         PrefixFoldParams f{};

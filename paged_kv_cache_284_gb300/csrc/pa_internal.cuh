@@ -73,7 +73,9 @@ static_assert(sizeof(PlanHeader) == 64, "header size");
 // partial rows partial_base + h*nsplit*R + [0, R) (R = q_count * group) when
 // nsplit > 1, and counts its completion in counters[counter*Hkv + h].
 // A windowed step counts stages and keys over the piece's visible chunks alone
-// (see KeySpan): seq_len is then the packed end of its keys.
+// (see KeySpan): seq_len is then the packed end of its keys.  Its records are
+// per kv head: counter is the job, piece * Hkv + h, and partial_base the first
+// partial row of this very split.
 struct alignas(16) ShortItem {
     int b, split, nsplit, stage_begin;
     int stage_end, partial_base, q_begin, q_count;
@@ -81,6 +83,17 @@ struct alignas(16) ShortItem {
     int sink_chunks, gap;  // windowed step: the piece's KeySpan
 };
 static_assert(sizeof(ShortItem) == 48, "item size");
+
+// Windowed step: a piece as its planner keeps it (in the workspace).  A long
+// request's entry has q_count = its tokens, keys = its context and before =
+// the tiles before it.
+struct alignas(16) WindowPiece {
+    int b, q_begin, q_count, keys;
+    int sink_chunks, gap, stages, splits;
+    int rows, slot_hi, slot_lo, pad;  // first partial row; first records of its longer and shorter splits
+    long long before, pad2;           // stages (one head) before it, later splits (one head)
+};
+static_assert(sizeof(WindowPiece) == 64, "piece size");
 
 // Tensor-core record: query tile q_tile of request b (tile = 128/group tokens
 // x group heads), keys [key_begin, key_end) (packed keys in a windowed step).
@@ -245,9 +258,11 @@ struct PlanParams {
     // last; stage_base[b] = first staging block or -1, stage_list = staged
     // requests in order.  stage_cap = 0: no staging (all rows split-KV).
     int fp8, stage_cap, block_size;
-    int windowed;  // a windowed step: only visible chunks (blocks) are counted,
-    int max_keys;  // and a request longer than its table is skipped
+    // windowed step only (launch_plan_window)
     WindowArgs win;
+    int max_keys;  // a request longer than its table is skipped
+    WindowPiece *pieces;
+    int max_pieces;
     int *stage_base, *stage_list;
     int split_stages;    // 0 = automatic
     int target_items;    // automatic split aims at about this many split-KV items
@@ -368,11 +383,14 @@ int launch_rope_write(RopeParams p, int sms, cudaStream_t s);
 int launch_copy_blocks(const pa_kv_desc *kv, int num_layers, const int32_t *pairs, int num_pairs,
                        int sms, unsigned *status, cudaStream_t s);
 int launch_plan(const PlanParams &p, cudaStream_t s);
+int launch_plan_window(const PlanParams &p, cudaStream_t s);
 int launch_short(const ShortParams &p, const CUtensorMap &tk, const CUtensorMap &tv,
                  int head_dim, bool fp8, bool windowed, int grid, cudaStream_t s);
 int short_max_ctas_per_sm(int head_dim, bool fp8, bool windowed);
 int launch_long(const LongParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
-                const CUtensorMap &tv, int head_dim, bool windowed, int grid, cudaStream_t s);
+                const CUtensorMap &tv, int head_dim, int grid, cudaStream_t s);
+int launch_long_window(const LongParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
+                       const CUtensorMap &tv, int head_dim, int grid, int sms, cudaStream_t s);
 int launch_prefix_fold(const PrefixFoldParams &f, int head_dim, cudaStream_t s);
 int launch_merge(const void *oa, const float *la, const void *ob, const float *lb, int n,
                  int heads, int head_dim, void *out, float *lse_out, cudaStream_t s);

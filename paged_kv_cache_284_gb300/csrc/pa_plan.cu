@@ -152,7 +152,6 @@ struct ReqInfo {
     int qtiles;   // query tiles of a tensor-core request
 };
 
-template <bool WIN>
 __device__ __forceinline__ ReqInfo load_req(const PlanParams &p, int b) {
     ReqInfo r{};
     const int q0 = p.qsl[b], q1 = p.qsl[b + 1];
@@ -160,7 +159,7 @@ __device__ __forceinline__ ReqInfo load_req(const PlanParams &p, int b) {
     r.ctx = p.ctx[b];
     r.len = p.seq_lens[b];
     const bool bad = r.n < 0 || r.ctx < 0 || r.len != r.ctx + r.n || q0 < 0 ||
-                     q1 > p.num_q_tokens || (WIN && r.len > p.max_keys);
+                     q1 > p.num_q_tokens;
     if (bad) {
         flag_status(p.status, PA_DEV_BAD_METADATA);
         r.n = 0;
@@ -178,18 +177,15 @@ __device__ __forceinline__ ReqInfo load_req(const PlanParams &p, int b) {
 }
 
 // Piece i of a split-KV request: its query tokens and the 64-key stages up
-// to its last token's causal limit (windowed: of its visible chunks).
+// to its last token's causal limit.
 struct Piece {
     int q_begin, q_count, stages;
 };
-template <bool WIN>
 __device__ __forceinline__ Piece piece_of(const PlanParams &p, const ReqInfo &r, int i) {
     Piece pc;
     pc.q_begin = i * p.piece_tokens;
     pc.q_count = min(p.piece_tokens, r.n - pc.q_begin);
-    int end = r.ctx + pc.q_begin + pc.q_count;
-    if constexpr (WIN) end = key_span(p.win, r.ctx + pc.q_begin, end).keys;
-    pc.stages = (end + kStageKeys - 1) / kStageKeys;
+    pc.stages = (r.ctx + pc.q_begin + pc.q_count + kStageKeys - 1) / kStageKeys;
     return pc;
 }
 
@@ -203,11 +199,9 @@ __device__ __forceinline__ int bin_shift(int longest, int bins) {
 }
 
 // 128-key tiles of query tile qt of a long request.
-template <bool WIN>
 __device__ __forceinline__ int long_tiles(const PlanParams &p, const ReqInfo &r, int qt) {
     const int nvalid = min(p.q_tile_tokens, r.n - qt * p.q_tile_tokens);
-    int kend = min(r.len, r.ctx + qt * p.q_tile_tokens + nvalid);
-    if constexpr (WIN) kend = key_span(p.win, r.ctx + qt * p.q_tile_tokens, kend).keys;
+    const int kend = min(r.len, r.ctx + qt * p.q_tile_tokens + nvalid);
     return (kend + kLongKeys - 1) / kLongKeys;
 }
 
@@ -231,7 +225,7 @@ __device__ __forceinline__ SplitCut split_cut(int stages, int sp) {
 
 // kT threads: 1024 in general, one warp for steps of few requests (its
 // phases then cost shuffles instead of block barriers).
-template <int kT, bool WIN>
+template <int kT>
 __global__ void __launch_bounds__(kT) plan_kernel(PlanParams p) {
     constexpr int kSortBins = kT;
     __shared__ int tmp[66];
@@ -256,13 +250,8 @@ __global__ void __launch_bounds__(kT) plan_kernel(PlanParams p) {
             int cnt = 0;
             if (b < p.num_seqs) {
                 const int n = p.qsl[b + 1] - p.qsl[b], len = p.seq_lens[b];
-                // (a windowed step stages no request that the plan will skip)
-                const bool bad =
-                    WIN && (len > p.max_keys || len < n || p.ctx[b] != len - n);
-                if (!bad && n > 0 && len > 0 && static_cast<long long>(n) * p.group > p.short_max_rows) {
+                if (n > 0 && len > 0 && static_cast<long long>(n) * p.group > p.short_max_rows)
                     cnt = (len + p.block_size - 1) / p.block_size;
-                    if constexpr (WIN) cnt -= block_span(p.win, len - n, len, p.block_size).gap;
-                }
             }
             int tot_c, tot_s;
             const int base = cand_base + block_exclusive_scan<kT>(cnt, tmp, &tot_c);
@@ -278,8 +267,8 @@ __global__ void __launch_bounds__(kT) plan_kernel(PlanParams p) {
     }
     // Request tid's metadata is read once and kept in registers; only steps
     // with more than kT requests read the others again per pass.
-    const ReqInfo mine = tid < p.num_seqs ? load_req<WIN>(p, tid) : ReqInfo{};
-    auto req = [&](int b) { return b == tid ? mine : load_req<WIN>(p, b); };
+    const ReqInfo mine = tid < p.num_seqs ? load_req(p, tid) : ReqInfo{};
+    auto req = [&](int b) { return b == tid ? mine : load_req(p, b); };
     __syncthreads();
 
     // 1. totals: split-KV work (in stages), pieces, longest piece, query tiles
@@ -288,7 +277,7 @@ __global__ void __launch_bounds__(kT) plan_kernel(PlanParams p) {
     for (int b = tid; b < p.num_seqs; b += kT) {
         const ReqInfo r = req(b);
         for (int i = 0; i < r.pieces; ++i) {
-            const Piece pc = piece_of<WIN>(p, r, i);
+            const Piece pc = piece_of(p, r, i);
             tot[0] += pc.stages;
             max_stages = max(max_stages, pc.stages);
         }
@@ -340,7 +329,7 @@ __global__ void __launch_bounds__(kT) plan_kernel(PlanParams p) {
     for (int b = tid; b < p.num_seqs; b += kT) {
         const ReqInfo r = req(b);
         for (int i = 0; i < r.pieces; ++i) {
-            const Piece pc = piece_of<WIN>(p, r, i);
+            const Piece pc = piece_of(p, r, i);
             const int na = (pc.stages + sp_a - 1) / sp_a, nb = (pc.stages + sp_b - 1) / sp_b;
             cnt[0] += na;
             cnt[2] += nb;
@@ -363,7 +352,7 @@ __global__ void __launch_bounds__(kT) plan_kernel(PlanParams p) {
         for (int b = tid; b < p.num_seqs; b += kT) {
             const ReqInfo r = req(b);
             for (int i = 0; i < r.pieces; ++i) {
-                const Piece pc = piece_of<WIN>(p, r, i);
+                const Piece pc = piece_of(p, r, i);
                 const int ns = (pc.stages + sp - 1) / sp;
                 c2[0] += ns;
                 if (ns > 1) c2[1] += static_cast<long long>(ns) * pc.q_count * p.group;
@@ -388,7 +377,7 @@ __global__ void __launch_bounds__(kT) plan_kernel(PlanParams p) {
     for (int b = tid; b < p.num_seqs; b += kT) {
         const ReqInfo r = req(b);
         for (int i = 0; i < r.pieces; ++i) {
-            const SplitCut c = split_cut(piece_of<WIN>(p, r, i).stages, sp);
+            const SplitCut c = split_cut(piece_of(p, r, i).stages, sp);
             if (c.rem > 0) atomicAdd(&bins[len_bin(c.q + 1, shift_s, kSortBins)], c.rem);
             if (c.ns > c.rem) atomicAdd(&bins[len_bin(c.q, shift_s, kSortBins)], c.ns - c.rem);
         }
@@ -408,7 +397,7 @@ __global__ void __launch_bounds__(kT) plan_kernel(PlanParams p) {
         if (b < p.num_seqs) r = req(b);
         int n_rows = 0;
         for (int i = 0; i < r.pieces; ++i) {
-            const Piece pc = piece_of<WIN>(p, r, i);
+            const Piece pc = piece_of(p, r, i);
             const int ns = (pc.stages + sp - 1) / sp;
             if (ns > 1) n_rows += ns * pc.q_count * p.group * hkv;
         }
@@ -425,7 +414,7 @@ __global__ void __launch_bounds__(kT) plan_kernel(PlanParams p) {
         }
         int row = off_r;
         for (int i = 0; i < r.pieces; ++i) {
-            const Piece pc = piece_of<WIN>(p, r, i);
+            const Piece pc = piece_of(p, r, i);
             const SplitCut c = split_cut(pc.stages, sp);
             const int R = pc.q_count * p.group;
             const int slot_hi =
@@ -441,13 +430,6 @@ __global__ void __launch_bounds__(kT) plan_kernel(PlanParams p) {
             it.counter = off_p + i;
             it.seq_len = r.len;
             it.sink_chunks = it.gap = 0;
-            if constexpr (WIN) {
-                const KeySpan ks =
-                    key_span(p.win, r.ctx + pc.q_begin, r.ctx + pc.q_begin + pc.q_count);
-                it.seq_len = ks.keys;
-                it.sink_chunks = ks.sink_chunks;
-                it.gap = ks.gap;
-            }
             for (int s = 0; s < c.ns; ++s) {
                 const bool big = s < c.rem;
                 it.split = s;
@@ -470,7 +452,7 @@ __global__ void __launch_bounds__(kT) plan_kernel(PlanParams p) {
         int max_tiles = 0;
         for (int b = tid; b < p.num_seqs; b += kT) {
             const ReqInfo r = req(b);
-            if (r.qtiles > 0) max_tiles = max(max_tiles, long_tiles<WIN>(p, r, r.qtiles - 1));
+            if (r.qtiles > 0) max_tiles = max(max_tiles, long_tiles(p, r, r.qtiles - 1));
         }
         {
             long long unused[1] = {0};
@@ -480,7 +462,7 @@ __global__ void __launch_bounds__(kT) plan_kernel(PlanParams p) {
         for (int b = tid; b < p.num_seqs; b += kT) {
             const ReqInfo r = req(b);
             for (int qt = 0; qt < r.qtiles; ++qt)
-                atomicAdd(&bins[len_bin(long_tiles<WIN>(p, r, qt), shift_l, kSortBins)], 1);
+                atomicAdd(&bins[len_bin(long_tiles(p, r, qt), shift_l, kSortBins)], 1);
         }
         __syncthreads();
         {
@@ -504,15 +486,8 @@ __global__ void __launch_bounds__(kT) plan_kernel(PlanParams p) {
                     it.q_tile = qt;
                     it.key_begin = 0;
                     it.key_end = min(r.len, r.ctx + qt * p.q_tile_tokens + nvalid);
-                    if constexpr (WIN) {
-                        const KeySpan ks =
-                            key_span(p.win, r.ctx + qt * p.q_tile_tokens, it.key_end);
-                        it.key_end = ks.keys;
-                        it.sink_chunks = ks.sink_chunks;
-                        it.gap = ks.gap;
-                    }
                     store_record(p.long_items,
-                                 atomicAdd(&bins[len_bin(long_tiles<WIN>(p, r, qt), shift_l,
+                                 atomicAdd(&bins[len_bin(long_tiles(p, r, qt), shift_l,
                                                          kSortBins)], 1),
                                  it);
                 }
@@ -538,19 +513,13 @@ __global__ void __launch_bounds__(kT) plan_kernel(PlanParams p) {
     }
 }
 
-template <bool WIN>
-static int launch(const PlanParams &p, cudaStream_t s) {
+int launch_plan(const PlanParams &p, cudaStream_t s) {
     if (p.num_seqs <= kSmallPlanSeqs) {
         PdlLaunch l(1, 32, 0, s);
-        return launch_kernel(l, plan_kernel<32, WIN>, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+        return launch_kernel(l, plan_kernel<32>, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     }
     PdlLaunch l(1, kPlanThreads, 0, s);
-    return launch_kernel(l, plan_kernel<kPlanThreads, WIN>, p) == cudaSuccess ? PA_OK
-                                                                              : PA_ERR_CUDA;
-}
-
-int launch_plan(const PlanParams &p, cudaStream_t s) {
-    return p.windowed ? launch<true>(p, s) : launch<false>(p, s);
+    return launch_kernel(l, plan_kernel<kPlanThreads>, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace pa

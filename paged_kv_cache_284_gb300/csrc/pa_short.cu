@@ -190,8 +190,14 @@ __device__ __forceinline__ void prefetch_item_q(const ShortParams &p, int tok0, 
     }
 }
 
-// Work item idx: its record and kv head.
+// Work item idx: its record and kv head (a windowed step's records are per head).
+template <bool WIN>
 __device__ __forceinline__ ShortItem short_work(const ShortParams &p, int idx, int &h) {
+    if constexpr (WIN) {
+        const ShortItem it = load_record(p.items, idx);
+        h = it.counter % p.num_kv_heads;
+        return it;
+    }
     const int rec = idx / p.num_kv_heads;
     h = idx - rec * p.num_kv_heads;
     return load_record(p.items, rec);
@@ -534,7 +540,7 @@ __global__ void __launch_bounds__(kShortThreads, 2)
         int cur_h = 0, cur_row = -1, cur_q0 = 0, cur_ctx = 0;
         // the record is loaded together with the item count (records up to
         // max_items exist in the workspace, valid or not)
-        ShortItem cur = short_work(p, min(cur_idx, p.max_items - 1), cur_h);
+        ShortItem cur = short_work<WIN>(p, min(cur_idx, p.max_items - 1), cur_h);
         if (cur_idx < num_items) {
             bool has;
             const int blk = chunk_blk_load<WIN>(p, cur, cur.seq_len, cur.stage_begin, lane, has);
@@ -595,7 +601,7 @@ __global__ void __launch_bounds__(kShortThreads, 2)
                     if (pf >= 2 || !((it >= kStages && rel > rel_claim) || rel == nrs - 1)) break;
                     if (pf == 0) {
                         nxt_idx = __shfl_sync(0xffffffffu, nxt_idx, 0);
-                        nxt = short_work(p, min(nxt_idx, p.max_items - 1), nxt_h);
+                        nxt = short_work<WIN>(p, min(nxt_idx, p.max_items - 1), nxt_h);
                         pf = 1;
                     } else {
                         if (nxt_idx < num_items) {
@@ -709,7 +715,7 @@ __global__ void __launch_bounds__(kShortThreads, 2)
             cs.h = item_h;
             cs.split = item.split;
             cs.nsplit = item.nsplit;
-            cs.counter = item.counter * p.num_kv_heads + item_h;
+            cs.counter = WIN ? item.counter : item.counter * p.num_kv_heads + item_h;
             // a piece of a request: its tokens start q_begin tokens in, so its
             // rows' causal limits start q_begin keys further
             cs.tok0 = item.tok0 + item.q_begin;
@@ -718,7 +724,8 @@ __global__ void __launch_bounds__(kShortThreads, 2)
             const int L = item.seq_len;
             cs.key_end = min(item.stage_end * kStageKeys, L);
             cs.R = n * p.group;
-            cs.partial_base = item.partial_base + item_h * item.nsplit * cs.R;
+            cs.partial_base =
+                WIN ? item.partial_base : item.partial_base + item_h * item.nsplit * cs.R;
             if constexpr (FP8) {
                 cs.sl2 = p.scale_log2 * __ldg(p.k_scale + item_h);
                 cs.vsc = __ldg(p.v_scale + item_h);
