@@ -33,41 +33,271 @@ namespace {
 // issuer, 4-7 softmax of even tiles, 8-11 of odd ones
 constexpr int kWarpQK = 1, kWarpV = 2, kWarpPV = 3, kFirstSoftmax = 4;
 constexpr int kGroupWarps = 4;
-constexpr int kSTiles = 3;
+// Key tiles of K (and of V) in shared memory.  A K tile lands ~3000 cycles after
+// its copies are issued, under load.
+constexpr int kRing = 3;
+
+// A work item as every role needs it (positions and keys packed).
+struct alignas(16) WinItem {
+    int b, h, tok0, nvalid;         // query tokens [tok0, tok0 + nvalid), kv head h
+    int pos0, key_end, nt;          // first position, end of the keys, key tiles (0: no more items)
+    int sink_chunks, gap;           // KeySpan
+    int block_sinks, block_gap, pad;  // BlockSpan of the request (staged blocks)
+};
+static_assert(sizeof(WinItem) == 48, "queue entry");
+constexpr int kQueue = 8;
 
 template <int D>
-struct WinGeom : LongTiles<D> {
-    using T = LongTiles<D>;
+struct WinGeom {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kHalfBytes = 128 * 128;            // 128 rows x 128 B
+    static constexpr int kQBytes = kHalves * kHalfBytes;    // Q tile
+    static constexpr int kKVBytes = kHalves * kHalfBytes;   // one K (or V) tile of 128 keys
     static constexpr int kOffQ = 0;
-    static constexpr int kOffK = kOffQ + T::kQBytes;
-    static constexpr int kOffV = kOffK + kKStages * T::kKVBytes;
-    static constexpr int kOffBar = kOffV + kVStages * T::kKVBytes;
-    static constexpr int kOffCtl = kOffBar + 384;
-    // per row: references by tile parity [2][128], sums [item parity][group][128]
-    static constexpr int kOffRef = kOffCtl + 128;
+    static constexpr int kOffK = kOffQ + kQBytes;
+    static constexpr int kOffV = kOffK + kRing * kKVBytes;
+    static constexpr int kOffBar = kOffV + kRing * kKVBytes;
+    static constexpr int kOffCtl = kOffBar + 304;
+    // items published by the K producer, their count, and how many each warp has read
+    static constexpr int kOffQueue = kOffCtl + 32;
+    static constexpr int kOffRead = kOffQueue + kQueue * static_cast<int>(sizeof(WinItem));
+    // per row: references by tile parity [2][128], sums by group [2][128]
+    static constexpr int kOffRef = kOffRead + 64;
     static constexpr int kOffSum = kOffRef + 2 * 128 * 4;
-    static constexpr int kOffQueue = kOffSum + 2 * 2 * 128 * 4;
-    static constexpr int kSmemRaw = kOffQueue + 512 + 1024;
+    static constexpr int kSmemRaw = kOffSum + 2 * 128 * 4;
     // at least 116 KiB so that one CTA owns an SM (and its 512 TMEM columns)
     static constexpr int kSmemBytes = kSmemRaw > 116 * 1024 ? kSmemRaw : 116 * 1024;
-    // TMEM columns: S0 | S1 | S2 (fp32, P in the first half of each) | O (fp32)
+    static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+    // TMEM columns: S0 | S1 (fp32 scores) | O (fp32) | P0 | P1 (bf16 pairs)
     static constexpr uint32_t kTmemCols = 512;
-    static constexpr int kColO = kSTiles * kLongKeys;
-    static_assert(kColO + D <= 512, "TMEM");
+    static constexpr int kColO = 2 * kLongKeys, kColP = 3 * kLongKeys;
+    static_assert(kColO + D <= kColP, "TMEM");
 };
 
 struct Bars {
     uint64_t q_full, q_empty;
-    uint64_t k_full[kKStages], k_empty[kKStages];
-    uint64_t v_full[kVStages], v_empty[kVStages];
-    uint64_t s_full[kSTiles];   // scores of a tile written
-    uint64_t p_full[kSTiles];   // P of a tile written (4 warps)
-    uint64_t pv_done[kSTiles];  // P V of a tile finished: its S tile is free
+    uint64_t k_full[kRing], k_empty[kRing];
+    uint64_t v_full[kRing], v_empty[kRing];
+    // by tile parity, that is, by group
+    uint64_t s_full[2], s_free[2];  // scores of a tile written / read (4 warps)
+    uint64_t p_full[2], pv_done[2]; // P of a tile written (4 warps) / its P V finished
     uint64_t ref[4][2];         // reference of a tile published, by row quarter and tile parity
     uint64_t sums[4];           // both groups' sums of an item written, by row quarter
     uint64_t o_free, drain, drain_pv;
 };
-static_assert(sizeof(Bars) <= 384, "barrier area");
+static_assert(sizeof(Bars) <= 304, "barrier area");
+
+// Items in order, one reader per warp.  Warp 0, which runs ahead of every other
+// role, takes an item's index -- from the step's counter, shared by every
+// launch of the step (p.dynamic), so that a CTA that starts late takes fewer;
+// else in serpentine order over the CTAs -- decodes it once and publishes it, so
+// that no other role starts an item with a chain of global loads (measured:
+// ~1500 cycles of each softmax group's time per item).
+struct Queue {
+    WinItem *items;
+    volatile int *published;
+    volatile int *read;  // [kLongWarps]
+    volatile int *abort;
+};
+template <typename Ready>
+__device__ __forceinline__ bool queue_spin(const Queue &q, Ready ready) {
+    if (ready()) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (!ready()) {
+        if (*q.abort) return false;
+        if (global_timer_ns() - t0 > kWaitTimeoutNs) {
+            *q.abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+// Warp 0, all lanes: takes, publishes and returns item k.
+__device__ __forceinline__ WinItem queue_next(const LongParams &p, const Queue &q, int n_items,
+                                              int k) {
+    const int lane = threadIdx.x & 31;
+    int idx = 0;
+    if (lane == 0) {
+        if (p.dynamic) {
+            idx = atomicAdd(&p.hdr->long_next, 1);
+        } else {
+            const int g = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
+            idx = k * g + ((k & 1) ? g - 1 - c : c);
+        }
+    }
+    idx = __shfl_sync(0xffffffffu, idx, 0);
+    WinItem it{};
+    if (idx < n_items) {
+        const int rec = idx / p.num_kv_heads, TQ = p.q_tile_tokens;
+        const LongItem li = load_record(p.items, rec);
+        const int q0 = __ldg(p.qsl + li.b), n = __ldg(p.qsl + li.b + 1) - q0;
+        const int ctx = __ldg(p.ctx + li.b);
+        it.b = li.b;
+        it.h = idx - rec * p.num_kv_heads;
+        it.tok0 = q0 + li.q_tile * TQ;
+        it.nvalid = min(TQ, n - li.q_tile * TQ);
+        it.pos0 = ctx + li.q_tile * TQ - li.gap * kChunkKeys;
+        it.key_end = li.key_end;
+        it.nt = (li.key_end + kLongKeys - 1) / kLongKeys;
+        it.sink_chunks = li.sink_chunks;
+        it.gap = li.gap;
+        if (p.stage_base) {
+            const BlockSpan bsp = block_span(p.win, ctx, ctx + n, p.block_size);
+            it.block_sinks = bsp.sink_blocks;
+            it.block_gap = bsp.gap;
+        }
+    }
+    if (lane == 0) {
+        // entry k % kQueue is free once every warp has read item k - kQueue
+        const bool ok = k < kQueue || queue_spin(q, [&] {
+            for (int w = 1; w < kLongWarps; ++w)
+                if (q.read[w] <= k - kQueue) return false;
+            return true;
+        });
+        if (ok) {
+            q.items[k % kQueue] = it;
+            __threadfence_block();
+            *q.published = k + 1;
+        }
+    }
+    __syncwarp();
+    if (*q.abort) it.nt = 0;
+    return it;
+}
+// Any other warp, all lanes: item k (nt = 0: no more, or aborted).
+__device__ __forceinline__ WinItem queue_item(const Queue &q, int warp, int k) {
+    const int lane = threadIdx.x & 31;
+    int ok = 1;
+    if (lane == 0) ok = queue_spin(q, [&] { return *q.published > k; }) ? 1 : 0;
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    WinItem it{};
+    if (ok) {
+        __threadfence_block();
+        const volatile int *src = reinterpret_cast<const volatile int *>(q.items + k % kQueue);
+        int *dst = reinterpret_cast<int *>(&it);
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(WinItem) / sizeof(int)); ++i) dst[i] = src[i];
+    }
+    __syncwarp();
+    if (lane == 0) q.read[warp] = k + 1;
+    return it;
+}
+
+// Loads of the K warp (which also takes the items and loads Q) and of the V
+// warp: gathers one 128-key tile per step into its ring, eight 16-key chunks
+// through the block table.
+template <int D>
+__device__ void produce(const LongParams &p, const Queue &q, int n_items, const CUtensorMap *tm,
+                        uint8_t *ring, uint64_t *full, uint64_t *empty, Bars *bars,
+                        const CUtensorMap *tmq, uint8_t *sQ, int warp) {
+    using G = WinGeom<D>;
+    const int lane = threadIdx.x & 31;
+    uint32_t t = 0;  // tiles issued so far (all items)
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+        const WinItem it = tmq ? queue_next(p, q, n_items, k) : queue_item(q, warp, k);
+        if (it.nt == 0) break;
+        if (tmq) {
+            if (k > 0 && !warp_wait(&bars->q_empty, (k - 1) & 1, q.abort)) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bars->q_full, static_cast<uint32_t>(
+                                                         G::kHalves * 128 * p.group *
+                                                         p.q_tile_tokens));
+                for (int hf = 0; hf < G::kHalves; ++hf)
+                    tma_load_3d(sQ + hf * G::kHalfBytes, tmq, hf * 64, it.h * p.group, it.tok0,
+                                &bars->q_full);
+            }
+        }
+        const int *bt = p.block_tables + static_cast<int64_t>(it.b) * p.bt_stride;
+        int my_row = p.kv_rows;
+        for (int j = 0; j < it.nt; ++j, ++t) {
+            if ((j & 3) == 0) {
+                // rows of the next 32 chunks (4 tiles), one per lane; chunks
+                // past key_end are read fully out of bounds -> zeros
+                int key0 = (j * 8 + lane) * kChunkKeys;
+                my_row = p.kv_rows;
+                if (key0 < it.key_end) {
+                    key0 = unpacked_key(key0, it.sink_chunks, it.gap);
+                    int col = key0 / p.block_size;
+                    if (col >= p.bt_stride) {
+                        flag_status(p.status, PA_DEV_BAD_METADATA);
+                        col = p.bt_stride - 1;
+                    }
+                    // fp8 pool: a request's visible blocks in their order are
+                    // its staging blocks
+                    int blk = p.stage_base ? __ldcg(p.stage_base + it.b) + col -
+                                                 (col >= it.block_sinks ? it.block_gap : 0)
+                                           : __ldg(bt + col);
+                    if (blk < 0 || blk >= p.num_blocks) {
+                        flag_status(p.status, PA_DEV_BAD_BLOCK);
+                        blk = min(max(blk, 0), p.num_blocks - 1);
+                    }
+                    my_row = (blk * p.num_kv_heads + it.h) * p.block_size + key0 % p.block_size;
+                }
+            }
+            const int slot = t % kRing;
+            if (t >= kRing && !warp_wait(&empty[slot], (t / kRing - 1) & 1, q.abort)) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(G::kKVBytes));
+            __syncwarp();
+            const int c = lane & 7;
+            const int row = __shfl_sync(0xffffffffu, my_row, (j & 3) * 8 + c);
+            if (lane < 8) {
+#pragma unroll
+                for (int hf = 0; hf < G::kHalves; ++hf)
+                    tma_load_2d(ring + slot * G::kKVBytes + hf * G::kHalfBytes + c * 2048, tm,
+                                hf * 64, row, &full[slot]);
+            }
+            __syncwarp();
+        }
+    }
+    if (*q.abort && lane == 0) {
+        // let copies already in flight land before the CTA exits
+        for (uint32_t i = (t > kRing ? t - kRing : 0); i < t; ++i)
+            mbar_drain(&full[i % kRing], (i / kRing) & 1);
+    }
+}
+
+// MMA and commit issued by the elected lane of a warp whose lanes all run the
+// surrounding code: operands stay in uniform registers.  (Inside a branch of
+// one lane each MMA took ~80 cycles to issue, 645 for a tile's eight.)
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e;
+}
+__device__ __forceinline__ void mma_ss(uint32_t elected, uint32_t d_tmem, uint64_t adesc,
+                                       uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t elected, uint32_t d_tmem, uint32_t a_tmem,
+                                       uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t elected, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_u32(bar)),
+        "r"(elected)
+        : "memory");
+}
 
 }  // namespace
 
@@ -78,44 +308,44 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
                        const __grid_constant__ CUtensorMap tmv) {
     using G = WinGeom<D>;
     constexpr int KS = D / 16;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    // (swizzled tiles: the three rings leave no room to align them by hand)
+    extern __shared__ __align__(1024) uint8_t smem[];
     Bars *bars = reinterpret_cast<Bars *>(smem + G::kOffBar);
     int *ctl = reinterpret_cast<int *>(smem + G::kOffCtl);
     volatile int *abort_flag = ctl;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ctl + 4);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // (a shuffled warp index is uniform to the compiler, and so is what follows it)
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
+    const int lane = threadIdx.x & 31;
     if (p.wait_start) {
         pdl_wait();     // the plan (and any staging copy) first
         pdl_trigger();  // then the split-KV grid may take the other SMs
     }
-    const int n_items = num_items(p);
+    const int n_items = *reinterpret_cast<volatile int *>(&p.hdr->num_long_items);
     if (!p.dynamic && static_cast<int>(blockIdx.x) >= n_items) {
         pdl_wait();  // complete only after the grid this one overlaps
         return;
     }
-    int *qmem = reinterpret_cast<int *>(smem + G::kOffQueue);
-    Sched sched;
-    sched.idx = qmem;
-    sched.pub = qmem + kItemQueue;
-    sched.cons = qmem + kItemQueue + 1;
+    Queue queue;
+    queue.items = reinterpret_cast<WinItem *>(smem + G::kOffQueue);
+    queue.published = reinterpret_cast<int *>(smem + G::kOffRead);
+    queue.read = queue.published + 1;
+    queue.abort = abort_flag;
 
     // ---- setup ----------------------------------------------------------------
     if (threadIdx.x == 0) {
         mbar_init(&bars->q_full, 1);
         mbar_init(&bars->q_empty, 1);
-        for (int i = 0; i < kKStages; ++i) {
+        for (int i = 0; i < kRing; ++i) {
             mbar_init(&bars->k_full[i], 1);
             mbar_init(&bars->k_empty[i], 1);
-        }
-        for (int i = 0; i < kVStages; ++i) {
             mbar_init(&bars->v_full[i], 1);
             mbar_init(&bars->v_empty[i], 1);
         }
-        for (int i = 0; i < kSTiles; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->s_full[i], 1);
+            mbar_init(&bars->s_free[i], kGroupWarps);
             mbar_init(&bars->p_full[i], kGroupWarps);
             mbar_init(&bars->pv_done[i], 1);
         }
@@ -128,15 +358,15 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
         mbar_init(&bars->drain, 1);
         mbar_init(&bars->drain_pv, 1);
         ctl[0] = 0;
-        *sched.pub = 0;
-        for (int w = 0; w < kLongWarps; ++w) sched.cons[w] = 0;
+        *queue.published = 0;
+        for (int w = 0; w < kLongWarps; ++w) queue.read[w] = 0;
         fence_mbar_init();
     }
     if (warp == kWarpQK) tmem_alloc(tmem_slot, G::kTmemCols);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
     uint8_t *sQ = smem + G::kOffQ;
     uint8_t *sK = smem + G::kOffK;
@@ -148,116 +378,101 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
             tma_prefetch_desc(&tmq);
             tma_prefetch_desc(&tmk);
         }
-        produce<D, kKStages, true>(p, sched, &tmk, sK, bars->k_full, bars->k_empty, &bars->q_full,
-                                   &bars->q_empty, true, &tmq, sQ, abort_flag);
+        produce<D>(p, queue, n_items, &tmk, sK, bars->k_full, bars->k_empty, bars, &tmq, sQ, warp);
     } else if (warp == kWarpV) {
         // ============================ V loads ============================
         if (lane == 0) tma_prefetch_desc(&tmv);
-        produce<D, kVStages, true>(p, sched, &tmv, sV, bars->v_full, bars->v_empty, nullptr, nullptr,
-                                   false, nullptr, nullptr, abort_flag);
+        produce<D>(p, queue, n_items, &tmv, sV, bars->v_full, bars->v_empty, bars, nullptr, nullptr,
+                   warp);
     } else if (warp == kWarpQK) {
         // ============================ Q K^T issuer ============================
-        // A tile's scores wait for its K tile and for the P V three tiles back,
-        // which read P from the same S tile.
-        if (lane == 0) {
-            constexpr uint32_t idesc_qk = idesc_bf16_f32(kLongRows, kLongKeys, 0);
-            const uint32_t q_addr = smem_u32(sQ), k_addr = smem_u32(sK);
-            uint32_t t = 0, k_item = 0;
-            bool ok = true;
-            for (int round = 0; ok; ++round) {
-                const int idx = sched_take(p, sched, n_items, round, warp, abort_flag);
-                if (idx == kSchedDone) break;
-                if (idx == kSchedAbort) {
+        // A tile's scores wait for its K tile and for the scores two tiles back
+        // to have been read.
+        constexpr uint32_t idesc_qk = idesc_bf16_f32(kLongRows, kLongKeys, 0);
+        const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
+        const uint64_t k_desc = smem_desc_sw128(smem_u32(sK), 16, 1024);
+        const uint32_t elected = elect_one();
+        uint32_t t = 0, k_item = 0;
+        bool ok = true;
+        for (; ok; ++k_item) {
+            const int nt = __shfl_sync(0xffffffffu, queue_item(queue, warp, k_item).nt, 0);
+            if (nt == 0) break;
+            if (!mbar_wait(&bars->q_full, k_item & 1, abort_flag)) { ok = false; break; }
+            int j = 0;
+            for (; j < nt; ++j) {
+                const uint32_t tt = t + j;
+                const int ks = tt % kRing;
+                const int sb = tt & 1;
+                if (!mbar_wait(&bars->k_full[ks], (tt / kRing) & 1, abort_flag)) { ok = false; break; }
+                if (tt >= 2 && !mbar_wait(&bars->s_free[sb], ((tt - 2) >> 1) & 1, abort_flag)) {
                     ok = false;
                     break;
                 }
-                const Item it = decode_item<true>(p, idx);
-                if (it.nt == 0) continue;
-                if (!mbar_wait(&bars->q_full, k_item & 1, abort_flag)) { ok = false; break; }
-                int j = 0;
-                for (; j < it.nt; ++j) {
-                    const uint32_t tt = t + j;
-                    const int ks = tt % kKStages;
-                    const int sb = tt % kSTiles;
-                    if (!mbar_wait(&bars->k_full[ks], (tt / kKStages) & 1, abort_flag)) { ok = false; break; }
-                    if (tt >= kSTiles &&
-                        !mbar_wait(&bars->pv_done[sb], (tt / kSTiles - 1) & 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t kb = k_addr + ks * G::kKVBytes;
+                __syncwarp();
+                tc_fence_after();
+                const uint64_t kd = k_desc + static_cast<uint32_t>(ks * (G::kKVBytes >> 4));
 #pragma unroll
-                    for (int kk = 0; kk < KS; ++kk) {
-                        const uint64_t ad = smem_desc_sw128(
-                            q_addr + (kk >> 2) * G::kHalfBytes + (kk & 3) * 32, 16, 1024);
-                        const uint64_t bd = smem_desc_sw128(
-                            kb + (kk >> 2) * G::kHalfBytes + (kk & 3) * 32, 16, 1024);
-                        tc_mma(tmem + sb * kLongKeys, ad, bd, idesc_qk, kk > 0 ? 1u : 0u);
-                    }
-                    tc_commit(&bars->k_empty[ks]);
-                    tc_commit(&bars->s_full[sb]);
-                    if (j == it.nt - 1) tc_commit(&bars->q_empty);
+                for (int kk = 0; kk < KS; ++kk) {
+                    constexpr int kHalf16 = G::kHalfBytes >> 4;
+                    const int off = (kk >> 2) * kHalf16 + (kk & 3) * 2;  // 16-byte units
+                    mma_ss(elected, tmem + sb * kLongKeys, q_desc + off, kd + off, idesc_qk,
+                           kk > 0 ? 1u : 0u);
                 }
-                if (p.tile_counter) atomicAdd(p.tile_counter, static_cast<unsigned long long>(j));
-                t += it.nt;
-                ++k_item;
+                commit(elected, &bars->s_full[sb]);
+                commit(elected, &bars->k_empty[ks]);
+                if (j == nt - 1) commit(elected, &bars->q_empty);
             }
-            if (!ok) {
-                // let every MMA already issued finish before TMEM is released
-                tc_commit(&bars->drain);
-                mbar_drain(&bars->drain, 0);
-            }
+            if (p.tile_counter && lane == 0)
+                atomicAdd(p.tile_counter, static_cast<unsigned long long>(j));
+            t += nt;
+        }
+        if (!ok || *abort_flag) {
+            // let every MMA already issued finish before TMEM is released
+            __syncwarp();
+            commit(elected, &bars->drain);
+            mbar_drain(&bars->drain, 0);
         }
     } else if (warp == kWarpPV) {
         // ============================ P V issuer ============================
         // A tile's P V waits for its P, its V tile and, at the start of an item,
         // for the previous item's epilogue to read O.
-        if (lane == 0) {
-            constexpr uint32_t idesc_pv = idesc_bf16_f32(kLongRows, D, 1);
-            const uint32_t v_addr = smem_u32(sV);
-            uint32_t t = 0, k_item = 0;
-            bool ok = true;
-            for (int round = 0; ok; ++round) {
-                const int idx = sched_take(p, sched, n_items, round, warp, abort_flag);
-                if (idx == kSchedDone) break;
-                if (idx == kSchedAbort) {
+        constexpr uint32_t idesc_pv = idesc_bf16_f32(kLongRows, D, 1);
+        const uint64_t v_desc = smem_desc_sw128(smem_u32(sV), G::kHalfBytes, 1024);
+        const uint32_t elected = elect_one();
+        uint32_t t = 0, k_item = 0;
+        bool ok = true;
+        for (; ok; ++k_item) {
+            const int nt = __shfl_sync(0xffffffffu, queue_item(queue, warp, k_item).nt, 0);
+            if (nt == 0) break;
+            for (int j = 0; j < nt; ++j) {
+                const uint32_t tt = t + j;
+                const int sb = tt & 1;
+                if (j == 0 && k_item > 0 &&
+                    !mbar_wait(&bars->o_free, (k_item - 1) & 1, abort_flag)) {
                     ok = false;
                     break;
                 }
-                const Item it = decode_item<true>(p, idx);
-                if (it.nt == 0) continue;
-                for (int j = 0; j < it.nt; ++j) {
-                    const uint32_t tt = t + j;
-                    const int sb = tt % kSTiles;
-                    if (!mbar_wait(&bars->p_full[sb], (tt / kSTiles) & 1, abort_flag)) { ok = false; break; }
-                    if (j == 0 && k_item > 0 &&
-                        !mbar_wait(&bars->o_free, (k_item - 1) & 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    const int vs = tt % kVStages;
-                    if (!mbar_wait(&bars->v_full[vs], (tt / kVStages) & 1, abort_flag)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t vbase = v_addr + vs * G::kKVBytes;
-                    // P (bf16) of this tile: row r in TMEM lane r, key k in column k / 2
-                    const uint32_t pcol = tmem + sb * kLongKeys;
+                const int vs = tt % kRing;
+                if (!mbar_wait(&bars->v_full[vs], (tt / kRing) & 1, abort_flag)) { ok = false; break; }
+                if (!mbar_wait(&bars->p_full[sb], (tt >> 1) & 1, abort_flag)) { ok = false; break; }
+                __syncwarp();
+                tc_fence_after();
+                const uint64_t vd = v_desc + static_cast<uint32_t>(vs * (G::kKVBytes >> 4));
+                // P (bf16) of this tile: row r in TMEM lane r, key k in column k / 2
+                const uint32_t pcol = tmem + G::kColP + sb * (kLongKeys / 2);
 #pragma unroll
-                    for (int kk = 0; kk < kLongKeys / 16; ++kk) {
-                        const uint64_t bd = smem_desc_sw128(vbase + kk * 2048, G::kHalfBytes, 1024);
-                        tc_mma_ts(tmem + G::kColO, pcol + kk * 8, bd, idesc_pv,
-                                  (j > 0 || kk > 0) ? 1u : 0u);
-                    }
-                    tc_commit(&bars->v_empty[vs]);
-                    tc_commit(&bars->pv_done[sb]);
-                }
-                t += it.nt;
-                ++k_item;
+                for (int kk = 0; kk < kLongKeys / 16; ++kk)
+                    mma_ts(elected, tmem + G::kColO, pcol + kk * 8, vd + kk * (2048 >> 4), idesc_pv,
+                           (j > 0 || kk > 0) ? 1u : 0u);
+                commit(elected, &bars->pv_done[sb]);
+                commit(elected, &bars->v_empty[vs]);
             }
-            if (!ok) {
-                tc_commit(&bars->drain_pv);
-                mbar_drain(&bars->drain_pv, 0);
-            }
+            t += nt;
+        }
+        if (!ok || *abort_flag) {
+            __syncwarp();
+            commit(elected, &bars->drain_pv);
+            mbar_drain(&bars->drain_pv, 0);
         }
     } else {
         // ============================ softmax + epilogue ============================
@@ -268,20 +483,12 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
         const int ttok = r / p.group;
         const int jh = r - ttok * p.group;
         float *refs = reinterpret_cast<float *>(smem + G::kOffRef) + r;  // [parity * 128]
-        float *sums = reinterpret_cast<float *>(smem + G::kOffSum) + r;  // [(parity * 2 + grp) * 128]
+        float *sums = reinterpret_cast<float *>(smem + G::kOffSum) + r;  // [grp * 128]
         uint32_t t = 0, k_item = 0;
         bool ok = true;
-        for (int round = 0; ok; ++round) {
-            int idx = 0;
-            if (lane == 0) idx = sched_take(p, sched, n_items, round, warp, abort_flag);
-            idx = __shfl_sync(0xffffffffu, idx, 0);
-            if (idx == kSchedDone) break;
-            if (idx == kSchedAbort) {
-                ok = false;
-                break;
-            }
-            const Item it = decode_item<true>(p, idx);
-            if (it.nt == 0) continue;
+        for (; ok; ++k_item) {
+            const WinItem it = queue_item(queue, warp, k_item);
+            if (it.nt == 0) break;
             const bool row_valid = ttok < it.nvalid && r < p.q_tile_tokens * p.group;
             // (packed keys) this row's last key, and the first row's lowest key
             // behind the sinks
@@ -292,26 +499,23 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
             float ref = -INFINITY, l = 0.f;  // this group's sum, against `ref`
             for (int j = (t & 1) == static_cast<uint32_t>(grp) ? 0 : 1; j < it.nt; j += 2) {
                 const uint32_t tt = t + j;
-                const int sb = tt % kSTiles;
                 const int kb = j * kLongKeys;
-                // keys kb + i visible to this row, bit i: below the causal
-                // limit, and a sink or at or past the row's low.  Only tiles
-                // that hold a key some row does not see are masked.
-                const bool need_mask = kb + kLongKeys - 1 > it.pos0 || kb + kLongKeys > it.key_end ||
-                                       (kb < low_first + it.nvalid - 1 &&
-                                        kb + kLongKeys > p.win.sinks);
-                auto seen_from = [&](int at) {
-                    return low_bits(min(row_limit, it.key_end - 1) + 1 - at) &
-                           (low_bits(p.win.sinks - at) |
-                            ~low_bits(row_limit - p.win.window + 1 - at));
-                };
-                if (!warp_wait(&bars->s_full[sb], (tt / kSTiles) & 1, abort_flag)) { ok = false; break; }
+                if (!warp_mbar_wait_spin(&bars->s_full[grp], (tt >> 1) & 1, abort_flag)) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t sa = t_lane + sb * kLongKeys;
-                // the row's maximum: keys 64..127 first, keys 0..63 stay in registers
+                // The row's 128 scores, 64 at a time: keys 64..127 for their
+                // maximum, keys 0..63, and later keys 64..127 again.
                 uint32_t s0[32], s1[32];
-                float mx = -INFINITY;
-                auto mask = [&](uint64_t seen) {
+                const uint32_t sa = t_lane + grp * kLongKeys;
+                // Tiles that hold a key some row does not see are masked; bit i:
+                // key at + i is below the causal limit, and a sink or at or past
+                // this row's low.
+                const bool need_mask =
+                    kb + kLongKeys - 1 > it.pos0 || kb + kLongKeys > it.key_end ||
+                    (kb < low_first + it.nvalid - 1 && kb + kLongKeys > p.win.sinks);
+                auto mask = [&](int at) {
+                    const uint64_t seen = low_bits(min(row_limit, it.key_end - 1) + 1 - at) &
+                                          (low_bits(p.win.sinks - at) |
+                                           ~low_bits(row_limit - p.win.window + 1 - at));
                     const uint32_t lo = static_cast<uint32_t>(seen);
                     const uint32_t hi = static_cast<uint32_t>(seen >> 32);
 #pragma unroll
@@ -320,6 +524,7 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
                         if (!(hi & (1u << i))) s1[i] = __float_as_uint(-INFINITY);
                     }
                 };
+                float mx = -INFINITY;
                 auto row_max = [&]() {
                     float mx0 = mx, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
@@ -334,17 +539,17 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
                 tmem_ld32(sa + 64, s0);
                 tmem_ld32(sa + 96, s1);
                 tmem_wait_ld();
-                if (need_mask) mask(seen_from(kb + 64));
+                if (need_mask) mask(kb + 64);
                 row_max();
                 tmem_ld32(sa, s0);
                 tmem_ld32(sa + 32, s1);
                 tmem_wait_ld();
-                if (need_mask) mask(seen_from(kb));
+                if (need_mask) mask(kb);
                 row_max();
                 // the reference: the tile before's, unless this tile exceeds it
                 float before = -INFINITY;
                 if (tt > 0) {
-                    if (!warp_wait(&bars->ref[wq][(tt - 1) & 1], ((tt - 1) >> 1) & 1, abort_flag)) { ok = false; break; }
+                    if (!warp_mbar_wait_spin(&bars->ref[wq][(tt - 1) & 1], ((tt - 1) >> 1) & 1, abort_flag)) { ok = false; break; }
                     if (j > 0) before = *reinterpret_cast<volatile float *>(refs + ((tt - 1) & 1) * 128);
                 }
                 const float mxs = mx * sl2;  // scale > 0: max commutes with it
@@ -358,8 +563,11 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
                     ref = now;
                 }
                 const float neg_ref = now == -INFINITY ? 0.f : -now;
-                // P row r (bf16 pairs) over the S tile's first 64 columns: 32
-                // keys take 16 columns, so a piece only covers scores read before
+                // P row r (bf16 pairs), in four pieces so that a piece's store lies
+                // beside the next one's exponentials; the P V that used this
+                // buffer two tiles ago must be done
+                if (tt >= 2 && !warp_mbar_wait_spin(&bars->pv_done[grp], ((tt - 2) >> 1) & 1, abort_flag)) { ok = false; break; }
+                tc_fence_after();
                 const uint64_t sc2 = f2_pack(sl2, sl2);
                 const uint64_t nr2 = f2_pack(neg_ref, neg_ref);
                 uint64_t acc0 = f2_pack(0.f, 0.f), acc1 = acc0;
@@ -383,14 +591,18 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
                     }
                     tmem_st16(dst, pk);
                 };
-                exps(s0, sa);
-                exps(s1, sa + 16);
+                const uint32_t pdst = t_lane + G::kColP + grp * (kLongKeys / 2);
+                exps(s0, pdst);
                 tmem_ld32(sa + 64, s0);
+                exps(s1, pdst + 16);
                 tmem_ld32(sa + 96, s1);
                 tmem_wait_ld();
-                if (need_mask) mask(seen_from(kb + 64));
-                exps(s0, sa + 32);
-                exps(s1, sa + 48);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->s_free[grp]);
+                if (need_mask) mask(kb + 64);
+                exps(s0, pdst + 32);
+                exps(s1, pdst + 48);
                 float sum0, sum1, sum2, sum3;
                 f2_unpack(acc0, sum0, sum1);
                 f2_unpack(acc1, sum2, sum3);
@@ -399,8 +611,7 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
                 // tile's P V must be done, this tile's has not begun
                 const float alpha = up && before != -INFINITY ? fast_exp2(before - now) : 1.f;
                 if (j >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                    const uint32_t prev = tt - 1;
-                    if (!warp_wait(&bars->pv_done[prev % kSTiles], (prev / kSTiles) & 1, abort_flag)) { ok = false; break; }
+                    if (!warp_mbar_wait_spin(&bars->pv_done[(tt - 1) & 1], ((tt - 1) >> 1) & 1, abort_flag)) { ok = false; break; }
                     tc_fence_after();
 #pragma unroll
                     for (int qd = 0; qd < D / 32; ++qd) {
@@ -421,8 +632,8 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
                 auto zero_rows = [&](int z0, int z1) -> bool {
                     if (z0 >= z1) return true;
                     zeroed = true;
-                    const int vs = tt % kVStages;
-                    if (!warp_wait(&bars->v_full[vs], (tt / kVStages) & 1, abort_flag)) return false;
+                    const int vs = tt % kRing;
+                    if (!warp_mbar_wait_spin(&bars->v_full[vs], (tt / kRing) & 1, abort_flag)) return false;
                     const int pieces = (z1 - z0) * 8 * G::kHalves;  // 16-byte pieces
                     for (int q = r; q < pieces; q += 32 * kGroupWarps) {
                         const int hf = q / ((z1 - z0) * 8);
@@ -443,24 +654,25 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
                 if (zeroed) fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->p_full[sb]);
+                if (lane == 0) mbar_arrive(&bars->p_full[grp]);
             }
 
             // ---- epilogue: this group's half of the output columns ----
             const uint32_t last = t + it.nt - 1;
             float final_ref = -INFINITY;
-            if (ok) ok = warp_wait(&bars->ref[wq][last & 1], (last >> 1) & 1, abort_flag);
+            // (the last P V first: it implies that both groups have read the
+            // item before's sums, which are overwritten below)
+            if (ok) ok = warp_mbar_wait_spin(&bars->pv_done[last & 1], (last >> 1) & 1, abort_flag);
+            if (ok) ok = warp_mbar_wait_spin(&bars->ref[wq][last & 1], (last >> 1) & 1, abort_flag);
             if (ok) {
                 final_ref = *reinterpret_cast<volatile float *>(refs + (last & 1) * 128);
                 if (ref != final_ref) l = ref == -INFINITY ? 0.f : l * fast_exp2(ref - final_ref);
-                float *slot = sums + (k_item & 1) * 256;
-                *reinterpret_cast<volatile float *>(slot + grp * 128) = l;
+                *reinterpret_cast<volatile float *>(sums + grp * 128) = l;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->sums[wq]);
-                ok = warp_wait(&bars->sums[wq], k_item & 1, abort_flag);
-                if (ok) l += *reinterpret_cast<volatile float *>(slot + (1 - grp) * 128);
+                ok = warp_mbar_wait_spin(&bars->sums[wq], k_item & 1, abort_flag);
+                if (ok) l += *reinterpret_cast<volatile float *>(sums + (1 - grp) * 128);
             }
-            if (ok) ok = warp_wait(&bars->pv_done[last % kSTiles], (last / kSTiles) & 1, abort_flag);
             if (!ok) break;
             tc_fence_after();
             // an fp8 pool's V scale multiplies the output
@@ -493,7 +705,6 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
             if (row_valid && grp == 0 && p.lse)
                 p.lse[orow] = l > 0.f ? (final_ref + __log2f(l)) * kLn2 : -INFINITY;
             t += it.nt;
-            ++k_item;
         }
     }
 
