@@ -84,16 +84,17 @@ struct alignas(16) ShortItem {
 };
 static_assert(sizeof(ShortItem) == 48, "item size");
 
-// Windowed step: a piece as its planner keeps it (in the workspace).  A long
-// request's entry has q_count = its tokens, keys = its context and before =
-// the tiles before it.
+// Windowed step: a piece as its planner keeps it (in the workspace when there
+// are many).  A long request's entry has q_count = its tokens, keys = its
+// context and before = the tiles before it.
 struct alignas(16) WindowPiece {
     int b, q_begin, q_count, keys;
     int sink_chunks, gap, stages, splits;
-    int rows, slot_hi, slot_lo, pad;  // first partial row; first records of its longer and shorter splits
-    long long before, pad2;           // stages (one head) before it, later splits (one head)
+    // first partial row, first records of its longer and its shorter splits,
+    // splits (one head) before it
+    int rows, slot_hi, slot_lo, before;
 };
-static_assert(sizeof(WindowPiece) == 64, "piece size");
+static_assert(sizeof(WindowPiece) == 48, "piece size");
 
 // Tensor-core record: query tile q_tile of request b (tile = 128/group tokens
 // x group heads), keys [key_begin, key_end) (packed keys in a windowed step).

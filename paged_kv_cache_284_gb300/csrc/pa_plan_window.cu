@@ -2,17 +2,18 @@
 //
 // Like the plain planner (pa_plan.cu) it turns the step's metadata into the two
 // kernels' work lists without a host round trip, over the packed visible
-// chunks of each request (KeySpan), longest first.  Windows bound the lengths,
-// so with many requests most split-KV jobs (a piece, for one kv head) are
-// equally long, and taking whole jobs leaves CTAs idle in the last round.  So
-//  * with more jobs than CTAs, whole jobs go first and the pieces that make up
-//    the last kTailStages stages per CTA are cut into splits of kTailSplit
-//    stages, which the CTAs pull as they come free;
+// chunks of each request (KeySpan), longest first.  Windows bound the lengths:
+//  * with more split-KV jobs (a piece, for one kv head) than CTAs every job
+//    stays whole.  Cutting the last ones finer, or the whole line of work into
+//    equal runs of stages per CTA, balances better on paper and was slower
+//    (64-request decode step: 70.6 us whole, 71.9 / 76.9 / 87.3 us with the
+//    last 4 / 8 / 16 stages per CTA cut by 4, 74.9 us in equal runs): a split
+//    costs its CTA about three stages' time;
 //  * with fewer jobs than CTAs, every job is cut so that all splits run in one
 //    round.
 // One CTA; latency is all that counts.  Every list is written by one thread
 // per record (splits, tensor-core tiles), so that one long request is not
-// planned by one thread.
+// planned by one thread, and the tables stay in shared memory.
 #include "pa_internal.cuh"
 
 namespace pa {
@@ -21,62 +22,45 @@ namespace {
 
 constexpr int kT = 512;
 constexpr int kWarps = kT / 32;
-constexpr int kTableInSmem = 1024;
-#ifndef TAIL_STAGES
-#define TAIL_STAGES 0
-#define TAIL_SPLIT 4
-#endif
-constexpr int kTailStages = TAIL_STAGES;
-constexpr int kTailSplit = TAIL_SPLIT;
+constexpr int kTableInSmem = 768;
 
-// Exclusive prefix of v over the block; *total = the block's sum.
 struct Sums {
-    long long a, b;
-    int c, d;
+    int a, b, c;
 };
 __device__ __forceinline__ Sums operator+(const Sums &x, const Sums &y) {
-    return {x.a + y.a, x.b + y.b, x.c + y.c, x.d + y.d};
+    return {x.a + y.a, x.b + y.b, x.c + y.c};
 }
 __device__ __forceinline__ Sums operator-(const Sums &x, const Sums &y) {
-    return {x.a - y.a, x.b - y.b, x.c - y.c, x.d - y.d};
+    return {x.a - y.a, x.b - y.b, x.c - y.c};
 }
 __device__ __forceinline__ Sums warp_inclusive(Sums x) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const Sums n = {__shfl_up_sync(0xffffffffu, x.a, o), __shfl_up_sync(0xffffffffu, x.b, o),
-                        __shfl_up_sync(0xffffffffu, x.c, o), __shfl_up_sync(0xffffffffu, x.d, o)};
+                        __shfl_up_sync(0xffffffffu, x.c, o)};
         if (lane >= o) x = x + n;
     }
     return x;
 }
+// Exclusive prefix of v over the block; *total = the block's sum.  (Two
+// barriers; the caller has one between two uses of tmp.)
 __device__ Sums block_scan(const Sums &v, Sums *tmp, Sums *total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Sums incl = warp_inclusive(v);
     if (lane == 31) tmp[warp] = incl;
     __syncthreads();
     if (warp == 0) {
-        const Sums mine = lane < kWarps ? tmp[lane] : Sums{0, 0, 0, 0};
+        const Sums mine = lane < kWarps ? tmp[lane] : Sums{0, 0, 0};
         const Sums w = warp_inclusive(mine);
+        __syncwarp();
         if (lane < kWarps) tmp[lane] = w - mine;
         if (lane == kWarps - 1) tmp[kWarps] = w;
     }
     __syncthreads();
     const Sums base = tmp[warp];
     *total = tmp[kWarps];
-    __syncthreads();
     return base + incl - v;
-}
-
-__device__ int block_max(int v, int *tmp) {
-    const int m = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(v)));
-    if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = m;
-    __syncthreads();
-    int r = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) r = max(r, tmp[i]);
-    __syncthreads();
-    return r;
 }
 
 struct Req {
@@ -86,9 +70,9 @@ struct Req {
 
 __device__ __forceinline__ Req load_req(const PlanParams &p, int b) {
     Req r{};
-    const int q0 = p.qsl[b], q1 = p.qsl[b + 1], len = p.seq_lens[b];
+    const int q0 = __ldg(p.qsl + b), q1 = __ldg(p.qsl + b + 1), len = __ldg(p.seq_lens + b);
     r.n = q1 - q0;
-    r.ctx = p.ctx[b];
+    r.ctx = __ldg(p.ctx + b);
     if (r.n < 0 || r.ctx < 0 || len > p.max_keys || len != r.ctx + r.n || q0 < 0 ||
         q1 > p.num_q_tokens) {
         flag_status(p.status, PA_DEV_BAD_METADATA);
@@ -121,103 +105,116 @@ __device__ __forceinline__ WindowPiece piece_of(const PlanParams &p, const Req &
     return w;
 }
 
-__device__ __forceinline__ unsigned long long udiv(unsigned long long a, unsigned long long b) {
-    return ((a | b) >> 32) ? a / b
-                           : static_cast<unsigned>(a) / static_cast<unsigned>(b);
-}
-
 // Sort bin of an item of `len` stages or tiles: bin 0 holds the longest; a bin
 // holds 2^shift consecutive lengths.
 __device__ __forceinline__ int bin_shift(int longest) {
-    int shift = 0;
-    while ((longest >> shift) >= kT) ++shift;
-    return shift;
+    const int bits = 32 - __clz(longest / kT);  // longest >> bits < kT
+    return longest < kT ? 0 : bits;
 }
 __device__ __forceinline__ int len_bin(int len, int shift) {
     return kT - 1 - min(len >> shift, kT - 1);
 }
-// atomicAdd(&bins[bin], 1) by the active lanes of a warp, one atomic per bin.
-__device__ __forceinline__ int bin_slot(int *bins, int bin) {
+// atomicAdd(&bins[bin], n) by the active lanes of a warp, one atomic per bin;
+// returns where this lane's n start.
+__device__ __forceinline__ int bin_take(int *bins, int bin, int n) {
     const unsigned same = __match_any_sync(__activemask(), bin);
     const int leader = __ffs(same) - 1, lane = threadIdx.x & 31;
     int at = 0;
-    if (lane == leader) at = atomicAdd(&bins[bin], __popc(same));
-    return __shfl_sync(same, at, leader) + __popc(same & ((1u << lane) - 1));
+    if (lane == leader) at = atomicAdd(&bins[bin], __popc(same) * n);
+    return __shfl_sync(same, at, leader) + __popc(same & ((1u << lane) - 1)) * n;
 }
 
 }  // namespace
 
 __global__ void __launch_bounds__(kT) plan_window_kernel(const PlanParams p) {
-    __shared__ Sums tmps[kWarps + 1];
-    __shared__ int tmpi[kWarps];
-    __shared__ int bins[kT];
-    // splits (one head) before each piece; tiles before each long request
-    __shared__ int s_off[kTableInSmem], s_loff[kTableInSmem];
-    __shared__ int s_overflow;
+    __shared__ Sums tmp_a[kWarps + 1], tmp_b[kWarps + 1], tmp_c[kWarps + 1];
+    __shared__ int bins[kT], tile_bins[kT];
+    __shared__ int s_max_stages, s_max_tiles;
+    __shared__ float s_stages;
+    __shared__ long long s_blocks[kWarps];
+    __shared__ WindowPiece s_table[kTableInSmem];
     const int tid = threadIdx.x;
     const int hkv = p.num_kv_heads;
+    if (tid == 0) {
+        s_max_stages = s_max_tiles = 0;
+        s_stages = 0.f;
+    }
+    bins[tid] = tile_bins[tid] = 0;
+    // the pieces from the front, the long requests from the back
+    const int table_size = p.max_pieces;
+    WindowPiece *table = table_size <= kTableInSmem ? s_table : p.pieces;
     // the metadata (and the workspace) may belong to the previous kernel
     pdl_wait();
     pdl_trigger();
-    if (tid == 0) s_overflow = 0;
-    bins[tid] = 0;
     // request tid's metadata is read once; the others' again in each pass
     const Req mine = tid < p.num_seqs ? load_req(p, tid) : Req{};
     auto req = [&](int b) { return b == tid ? mine : b < p.num_seqs ? load_req(p, b) : Req{}; };
+    for (int i = tid; i < p.num_counters; i += kT) p.counters[i] = 0;
 
     // 0. fp8 pool with a staging area: long requests get consecutive bf16
     // staging blocks for their visible blocks, in request order while they fit
-    int staged = 0;
-    long long staged_blocks = 0;
+    int staged = 0, staged_blocks = 0;
     if (p.fp8 && p.stage_cap > 0) {
-        long long cand = 0;
+        int cand = 0;
+        bool full = false;
         for (int b0 = 0; b0 < p.num_seqs; b0 += kT) {
             const int b = b0 + tid;
             const Req r = req(b);
             int cnt = 0;
-            if (r.n > 0 && static_cast<long long>(r.n) * p.group > p.short_max_rows)
-                cnt = (r.ctx + r.n + p.block_size - 1) / p.block_size -
-                      block_span(p.win, r.ctx, r.ctx + r.n, p.block_size).gap;
-            Sums tot;
-            const long long base = cand + block_scan({cnt, 0, 0, 0}, tmps, &tot).a;
-            cand += tot.a;
+            if (!full && r.n > 0 && static_cast<long long>(r.n) * p.group > p.short_max_rows)
+                cnt = min(p.stage_cap + 1,
+                          (r.ctx + r.n + p.block_size - 1) / p.block_size -
+                              block_span(p.win, r.ctx, r.ctx + r.n, p.block_size).gap);
+            // blocks before this request, in 64 bits (2^28 blocks a request)
+            long long before = cnt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long n = __shfl_up_sync(0xffffffffu, before, o);
+                if ((tid & 31) >= o) before += n;
+            }
+            if ((tid & 31) == 31) s_blocks[tid >> 5] = before;
+            __syncthreads();
+            long long base = cand + before - cnt, all = cand;
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < (tid >> 5)) base += s_blocks[w];
+                all += s_blocks[w];
+            }
             const bool fits = cnt > 0 && base + cnt <= p.stage_cap;
-            const Sums at = block_scan({fits ? cnt : 0, 0, fits ? 1 : 0, 0}, tmps, &tot);
+            Sums tot;
+            const Sums at = block_scan({fits ? cnt : 0, fits ? 1 : 0, 0}, tmp_b, &tot);
             if (b < p.num_seqs) p.stage_base[b] = fits ? static_cast<int>(base) : -1;
-            if (fits) p.stage_list[staged + at.c] = b;
-            staged += tot.c;
+            if (fits) p.stage_list[staged + at.b] = b;
+            staged += tot.b;
             staged_blocks += tot.a;
+            full = all > p.stage_cap;  // no later request fits
+            cand = full ? 0 : static_cast<int>(all);
+            __syncthreads();
         }
     }
 
-    // 1. tables: the pieces, with the stages before each, from the front;
-    // the long requests, with the tiles before each, from the back
-    Sums base{0, 0, 0, 0};  // stages (one head), tiles, pieces, long requests
+    // 1. tables: the pieces from the front, the long requests (q_count = tokens,
+    // keys = context, before = tiles before it) from the back
+    Sums base{0, 0, 0};  // pieces, tiles, long requests
+    bool overflow = false;
     int max_stages = 0;
+    float stages = 0.f;
     for (int b0 = 0; b0 < p.num_seqs; b0 += kT) {
         const int b = b0 + tid;
         Req r = req(b);
         classify(p, r, b);
-        long long sum = 0;
-        for (int i = 0; i < r.pieces; ++i) {
-            const int st = piece_of(p, r, b, i).stages;
-            sum += st;
-            max_stages = max(max_stages, st);
-        }
+        if (b0 > 0) __syncthreads();
         Sums tot;
-        const Sums off =
-            base + block_scan({sum, r.qtiles, r.pieces, r.qtiles > 0 ? 1 : 0}, tmps, &tot);
+        const Sums off = base + block_scan({r.pieces, r.qtiles, r.qtiles > 0 ? 1 : 0}, tmp_a, &tot);
         base = base + tot;
-        if (base.c + base.d > p.max_pieces || base.b * hkv > p.max_long) {
-            if (tid == 0) s_overflow = 1;
-            break;  // uniform: the totals are block-wide
+        if (base.a + base.c > table_size || static_cast<long long>(base.b) * hkv > p.max_long) {
+            overflow = true;  // uniform: the totals are block-wide
+            break;
         }
-        long long at = off.a;
         for (int i = 0; i < r.pieces; ++i) {
-            WindowPiece w = piece_of(p, r, b, i);
-            w.before = at;
-            at += w.stages;
-            p.pieces[off.c + i] = w;
+            const WindowPiece w = piece_of(p, r, b, i);
+            stages += static_cast<float>(w.stages);
+            max_stages = max(max_stages, w.stages);
+            table[off.a + i] = w;
         }
         if (r.qtiles > 0) {
             WindowPiece w{};
@@ -225,54 +222,60 @@ __global__ void __launch_bounds__(kT) plan_window_kernel(const PlanParams p) {
             w.q_count = r.n;
             w.keys = r.ctx;
             w.before = off.b;
-            p.pieces[p.max_pieces - 1 - off.d] = w;
-            if (off.d < kTableInSmem) s_loff[off.d] = static_cast<int>(off.b);
+            table[table_size - 1 - off.c] = w;
         }
     }
-    max_stages = block_max(max_stages, tmpi);  // (its barriers publish the tables)
-    const int P = base.c, n_long = base.d;
-    const long long J = static_cast<long long>(P) * hkv;  // jobs
-    const long long total = base.a * hkv;                 // stages
-    const int n_tiles = static_cast<int>(base.b);
-    const long long C = max(1, p.num_ctas);
+    max_stages = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(max_stages)));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) stages += __shfl_xor_sync(0xffffffffu, stages, o);
+    if ((tid & 31) == 0 && max_stages > 0) {
+        atomicMax(&s_max_stages, max_stages);
+        atomicAdd(&s_stages, stages);
+    }
+    __syncthreads();  // the tables too
+    max_stages = s_max_stages;
+    const int P = base.a, n_long = base.c, n_tiles = base.b;
+    const int J = overflow ? 0 : P * hkv;  // jobs (at most num_counters, see below)
+    const int C = max(1, p.num_ctas);
 
-    // 2. splits per piece -------------------------------------------------------
-    // More jobs than CTAs: pieces whose work lies in the last kTailStages
-    // stages per CTA are cut by kTailSplit, the others stay whole.  Else all
-    // by sp: total / (C - J / 2) stages a split usually gives at most C splits
-    // (half a split of rounding per job), total / (C - J) always does.
-    // Partial states that do not fit double the split.
-    long long tail = J > C ? C * kTailStages : total;
-    int sp = kTailSplit;
-    if (J > 0 && J <= C)
-        sp = static_cast<int>(max(static_cast<long long>(kMinSplitStages),
-                                  static_cast<long long>(udiv(total + C - J / 2 - 1, C - J / 2))));
-    auto splits_of = [&](const WindowPiece &w, long long stages_before) {
-        return (base.a - stages_before) * hkv <= tail ? (w.stages + sp - 1) / sp : 1;
-    };
-    long long items = 0, rows = 0;
-    for (int tries = 0; !s_overflow && P > 0; ++tries) {
-        Sums sum{0, 0, 0, 0};
-        for (int i = tid; i < P; i += kT) {
-            const WindowPiece w = p.pieces[i];
-            const int ns = splits_of(w, w.before);
-            sum.a += ns;
-            if (ns > 1) sum.b += static_cast<long long>(ns) * w.q_count * p.group;
+    // 2. splits per piece: one, or with at most as many jobs as CTAs
+    // ceil(stages / sp).  total / (C - J / 2) stages a split usually gives at
+    // most C splits (half a split of rounding per job), total / (C - J) always
+    // does.  Partial states that do not fit double the split.  (The total in
+    // fp32: it only steers the cut.)
+    int sp = max(1, max_stages);
+    int items = J, rows = 0;
+    if (J > 0 && J <= C && max_stages > kMinSplitStages) {
+        const float total = s_stages * static_cast<float>(hkv);
+        auto size = [&](int d) {
+            return max(kMinSplitStages,
+                       static_cast<int>(fminf(ceilf(total / static_cast<float>(max(1, d))),
+                                              static_cast<float>(max_stages))));
+        };
+        sp = size(C - J / 2);
+        for (int tries = 0;; ++tries) {
+            Sums sum{0, 0, 0};
+            for (int i = tid; i < P; i += kT) {
+                const int ns = (table[i].stages + sp - 1) / sp;
+                sum.a += min(ns, C + 1);
+                if (ns > 1) sum.b += min(ns, C + 1) * table[i].q_count * p.group;
+            }
+            Sums tot;
+            (void)block_scan(sum, tmp_b, &tot);
+            __syncthreads();
+            items = tot.a * hkv;
+            rows = tot.b * hkv;
+            if (sp >= max_stages || (items <= C && items <= p.max_short && rows <= p.cap_rows)) break;
+            sp = tries == 0 && J < C ? max(sp, size(C - J)) : min(max_stages, 2 * sp);
         }
-        Sums tot;
-        (void)block_scan(sum, tmps, &tot);
-        items = tot.a * hkv;
-        rows = tot.b * hkv;
-        if (sp >= max_stages ||
-            (rows <= p.cap_rows && items <= p.max_short && (J > C || items <= C)))
-            break;
-        sp = tries == 0 && J < C
-                 ? max(sp, static_cast<int>(min(static_cast<long long>(max_stages),
-                                                static_cast<long long>(udiv(total + C - J - 1, C - J)))))
-                 : min(max_stages, 2 * sp);
     }
-    const bool fits = !s_overflow && J <= p.num_counters && items <= p.max_short &&
-                      rows <= p.cap_rows;
+    const bool split = sp < max_stages;
+    if (!split) {
+        items = J;
+        rows = 0;
+    }
+    const bool fits = !overflow && static_cast<long long>(P) * hkv <= p.num_counters &&
+                      items <= p.max_short;
 
     // 3. split-KV records, longest first (counting sort on the stages).  A
     // piece cuts its stages into splits that differ by at most one stage; its
@@ -280,60 +283,63 @@ __global__ void __launch_bounds__(kT) plan_window_kernel(const PlanParams p) {
     if (fits && P > 0) {
         const int shift = bin_shift(max_stages);
         for (int i = tid; i < P; i += kT) {
-            const WindowPiece w = p.pieces[i];
-            const int ns = splits_of(w, w.before);
-            const int q = w.stages / ns, extra = w.stages - q * ns;
+            const int st = table[i].stages, ns = split ? (st + sp - 1) / sp : 1;
+            const int q = st / ns, extra = st - q * ns;
             if (extra > 0) atomicAdd(&bins[len_bin(q + 1, shift)], extra * hkv);
             atomicAdd(&bins[len_bin(q, shift)], (ns - extra) * hkv);
         }
         __syncthreads();
         Sums tot;
-        const int bin_at = block_scan({0, 0, bins[tid], 0}, tmps, &tot).c;
+        const int bin_at = block_scan({bins[tid], 0, 0}, tmp_c, &tot).a;
         bins[tid] = bin_at;
         __syncthreads();
-        Sums run{0, 0, 0, 0};
+        Sums run{0, 0, 0};
         for (int i0 = 0; i0 < P; i0 += kT) {
             const int i = i0 + tid;
-            WindowPiece w{};
-            int ns = 0;
+            int ns = 0, q = 0, extra = 0, need = 0;
             if (i < P) {
-                w = p.pieces[i];
-                ns = splits_of(w, w.before);
+                const int st = table[i].stages;
+                ns = split ? (st + sp - 1) / sp : 1;
+                q = st / ns;
+                extra = st - q * ns;
+                need = ns > 1 ? ns * table[i].q_count * p.group : 0;
             }
-            const Sums at =
-                run + block_scan({ns > 1 ? static_cast<long long>(ns) * w.q_count * p.group : 0, 0,
-                                  ns, 0}, tmps, &tot);
-            run = run + tot;
+            Sums at{i, 0, 0};
+            if (split) {  // (one split each: the splits before piece i are i)
+                if (i0 > 0) __syncthreads();
+                at = run + block_scan({ns, need, 0}, tmp_a, &tot);
+                run = run + tot;
+            }
             if (i >= P) continue;
-            const int q = w.stages / ns, extra = w.stages - q * ns;
-            w.splits = ns;
-            w.rows = static_cast<int>(at.a) * hkv;
-            w.slot_hi = extra > 0 ? atomicAdd(&bins[len_bin(q + 1, shift)], extra * hkv) : 0;
-            w.slot_lo = atomicAdd(&bins[len_bin(q, shift)], (ns - extra) * hkv);
-            w.before = at.c;
-            p.pieces[i] = w;
-            if (i < kTableInSmem) s_off[i] = at.c;
+            table[i].splits = ns;
+            table[i].rows = at.b * hkv;
+            table[i].slot_hi =
+                extra > 0 ? atomicAdd(&bins[len_bin(q + 1, shift)], extra * hkv) : 0;
+            table[i].slot_lo = atomicAdd(&bins[len_bin(q, shift)], (ns - extra) * hkv);
+            table[i].before = at.a;
         }
         __syncthreads();
-        for (long long j = tid; j < items; j += kT) {
-            int lo = 0, hi = P - 1;  // the piece: the last that starts at or before j
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                const long long before = mid < kTableInSmem ? s_off[mid] : p.pieces[mid].before;
-                if (before * hkv <= j) lo = mid; else hi = mid - 1;
+        for (int j = tid; j < items; j += kT) {
+            int lo = j / hkv;  // the piece: the last that starts at or before j
+            if (split) {
+                lo = 0;
+                int hi = P - 1;
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (table[mid].before * hkv <= j) lo = mid; else hi = mid - 1;
+                }
             }
-            const WindowPiece w = p.pieces[lo];
-            const int in = static_cast<int>(j - w.before * hkv);
+            const WindowPiece w = table[lo];
+            const int in = j - w.before * hkv;
             const int h = in / w.splits, s = in - h * w.splits;
             const int q = w.stages / w.splits, extra = w.stages - q * w.splits;
-            const int R = w.q_count * p.group;
             ShortItem it;
             it.b = w.b;
             it.split = s;
             it.nsplit = w.splits;
             it.stage_begin = s * q + min(s, extra);
             it.stage_end = it.stage_begin + q + (s < extra ? 1 : 0);
-            it.partial_base = w.splits > 1 ? w.rows + in * R : 0;
+            it.partial_base = w.splits > 1 ? w.rows + in * w.q_count * p.group : 0;
             it.q_begin = w.q_begin;
             it.q_count = w.q_count;
             it.counter = lo * hkv + h;
@@ -353,14 +359,12 @@ __global__ void __launch_bounds__(kT) plan_window_kernel(const PlanParams p) {
             int lo = 0, hi = n_long - 1;
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
-                const long long before =
-                    mid < kTableInSmem ? s_loff[mid] : p.pieces[p.max_pieces - 1 - mid].before;
-                if (before <= t) lo = mid; else hi = mid - 1;
+                if (table[table_size - 1 - mid].before <= t) lo = mid; else hi = mid - 1;
             }
-            const WindowPiece w = p.pieces[p.max_pieces - 1 - lo];
+            const WindowPiece w = table[table_size - 1 - lo];
             it = LongItem{};
             it.b = w.b;
-            it.q_tile = t - static_cast<int>(w.before);
+            it.q_tile = t - w.before;
             const int first = w.keys + it.q_tile * p.q_tile_tokens;
             const KeySpan ks = key_span(p.win, first,
                                         min(w.keys + w.q_count, first + p.q_tile_tokens));
@@ -369,9 +373,7 @@ __global__ void __launch_bounds__(kT) plan_window_kernel(const PlanParams p) {
             it.gap = ks.gap;
             return (ks.keys + kLongKeys - 1) / kLongKeys;
         };
-        __syncthreads();
-        bins[tid] = 0;
-        LongItem first_item;
+        LongItem first_item{};
         int longest = 0, first_len = 0;
         for (int t = tid; t < n_tiles; t += kT) {
             LongItem it;
@@ -382,38 +384,38 @@ __global__ void __launch_bounds__(kT) plan_window_kernel(const PlanParams p) {
                 first_len = len;
             }
         }
-        const int shift = bin_shift(block_max(longest, tmpi));
+        longest = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(longest)));
+        if ((tid & 31) == 0 && longest > 0) atomicMax(&s_max_tiles, longest);
+        __syncthreads();
+        const int shift = bin_shift(s_max_tiles);
         for (int t = tid; t < n_tiles; t += kT) {
             LongItem it;
-            const int len = t == tid ? first_len : tile(t, it);
-            (void)bin_slot(bins, len_bin(len, shift));
+            (void)bin_take(tile_bins, len_bin(t == tid ? first_len : tile(t, it), shift), 1);
         }
         __syncthreads();
         Sums tot;
-        const int bin_at = block_scan({0, 0, bins[tid], 0}, tmps, &tot).c;
-        bins[tid] = bin_at;
+        const int bin_at = block_scan({tile_bins[tid], 0, 0}, tmp_b, &tot).a;
+        tile_bins[tid] = bin_at;
         __syncthreads();
         for (int t = tid; t < n_tiles; t += kT) {
             LongItem it = first_item;
             const int len = t == tid ? first_len : tile(t, it);
-            store_record(p.long_items, bin_slot(bins, len_bin(len, shift)), it);
+            store_record(p.long_items, bin_take(tile_bins, len_bin(len, shift), 1), it);
         }
     }
 
-    // 5. counters and header ----------------------------------------------------
-    for (int i = tid; i < p.num_counters && i < J; i += kT) p.counters[i] = 0;
-    __syncthreads();
+    // 5. header -----------------------------------------------------------------
     if (tid == 0) {
         // a work list that did not fit is never run partially: no items at all
         if (!fits) flag_status(p.status, PA_DEV_PLAN_OVERFLOW);
-        p.hdr->num_short_items = fits ? static_cast<int>(items) : 0;
+        p.hdr->num_short_items = fits ? items : 0;
         p.hdr->num_long_items = fits ? n_tiles * hkv : 0;
         p.hdr->short_next = 0;
         p.hdr->long_next = 0;
         p.hdr->split_stages = sp;
-        p.hdr->partial_rows = fits ? static_cast<int>(rows) : 0;
+        p.hdr->partial_rows = fits ? rows : 0;
         p.hdr->num_staged = fits ? staged : 0;
-        p.hdr->staged_blocks = fits ? static_cast<int>(staged_blocks) : 0;
+        p.hdr->staged_blocks = fits ? staged_blocks : 0;
         p.hdr->first_done = 0;
     }
 }

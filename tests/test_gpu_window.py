@@ -159,6 +159,22 @@ def test_far_positions_have_a_table_of_gone_blocks():
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_more_requests_than_a_plan_keeps_in_shared_memory(kv):
+    """Over a thousand requests, decode rows and chunks among them."""
+    rng = np.random.default_rng(5)
+    reqs = [(int(c), 1) for c in rng.integers(0, 90, 1100)]
+    reqs[7] = reqs[600] = (33, 40)
+    reqs[1099] = (5, 70)
+    Step(reqs, 4, 2, 128, 16, 30, 2, kv=kv, seed=6).run_and_check()
+
+
+def test_many_pieces_of_an_unstaged_prompt():
+    """An e4m3 prompt without staging room: one piece per 4 tokens, split-KV."""
+    Step([(100, 700), (20, 3)], 16, 1, 128, 16, 64, 5, kv="e4m3",
+         seed=7).run_and_check(staging_blocks=0)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 def test_padding_rows_are_left_alone(kv):
     Step([(30, 3), (0, 0), (200, 70)], 8, 2, 128, 16, 40, 4, kv=kv, pad=9).run_and_check()
 
