@@ -360,6 +360,21 @@ def _off(t, dtype, device: int) -> bool:
     return t.dtype is not dtype or t.get_device() != device or not t.is_contiguous()
 
 
+def _pool(k_cache, v_cache, k_scale, v_scale, device: int) -> KVDesc:
+    """kv_desc of a pool on `device`: a bf16 one checked in one go (kv_desc's
+    steps are half of a small call's host time)."""
+    shape = k_cache.shape
+    if (k_scale is not None or v_scale is not None or _off(k_cache, _BF16, device) or
+            _off(v_cache, _BF16, device) or len(shape) != 4 or v_cache.shape != shape):
+        for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale),
+                        ("v_scale", v_scale)):
+            if t is not None and t.get_device() != device:
+                _explain(device, ((name, t, None),))
+        return kv_desc(k_cache, v_cache, k_scale, v_scale)
+    nb, hkv, bs, d = shape
+    return KVDesc(k_cache.data_ptr(), v_cache.data_ptr(), nb, bs, hkv, d)
+
+
 def pa_window_attention(q, k_cache, v_cache, block_tables, query_start_loc, context_lens, seq_lens,
                         scale, window, num_sinks, out, lse=None, workspace=None, stream=None,
                         k_scale=None, v_scale=None, staging_blocks=0):
@@ -372,17 +387,13 @@ def pa_window_attention(q, k_cache, v_cache, block_tables, query_start_loc, cont
     if (_off(q, _BF16, dev) or _off(out, _BF16, dev) or _off(block_tables, _I32, dev) or
             _off(query_start_loc, _I32, dev) or _off(context_lens, _I32, dev) or
             _off(seq_lens, _I32, dev) or (lse is not None and _off(lse, _F32, dev)) or dev < 0 or
-            dev != torch._C._cuda_getDevice() or k_cache.get_device() != dev or
-            v_cache.get_device() != dev or
-            (workspace is not None and workspace.get_device() != dev) or
-            (k_scale is not None and (k_scale.get_device() != dev or v_scale.get_device() != dev))):
+            dev != torch._C._cuda_getDevice() or
+            (workspace is not None and workspace.get_device() != dev)):
         _explain(dev, (("q", q, _BF16), ("out", out, _BF16), ("block_tables", block_tables, _I32),
                        ("query_start_loc", query_start_loc, _I32),
                        ("context_lens", context_lens, _I32), ("seq_lens", seq_lens, _I32),
-                       ("lse", lse, _F32), ("k_cache", k_cache, None), ("v_cache", v_cache, None),
-                       ("workspace", workspace, None), ("k_scale", k_scale, None),
-                       ("v_scale", v_scale, None)))
-    kv = kv_desc(k_cache, v_cache, k_scale, v_scale)
+                       ("lse", lse, _F32), ("workspace", workspace, None)))
+    kv = _pool(k_cache, v_cache, k_scale, v_scale, dev)
     shape = q.shape
     T, hq, d = shape
     B = seq_lens.numel()
@@ -412,16 +423,16 @@ def pa_window_attention(q, k_cache, v_cache, block_tables, query_start_loc, cont
 
 
 def _token_rows(t: torch.Tensor, name: str, device: int):
-    """(elements between token rows, T, H, d) of a bf16 [T, H, d] tensor whose
-    rows are contiguous: a slice of a fused projection, or a whole tensor."""
+    """(elements between token rows, shape) of a bf16 [T, H, d] tensor whose rows
+    are contiguous: a slice of a fused projection, or a whole tensor."""
     if t.dtype is not _BF16:
         raise TypeError(f"{name} must be {_BF16}, got {t.dtype}")
     if device < 0 or t.get_device() != device:
         _explain(device, ((name, t, None),))
     shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or stride[2] != 1 or (shape[1] > 1 and stride[1] != shape[2]):
+    if len(stride) != 3 or stride[2] != 1 or (stride[1] != shape[2] and shape[1] > 1):
         raise ValueError(f"{name} must be [T, H, d] with contiguous rows")
-    return (stride[0] if shape[0] > 1 else shape[1] * shape[2], *shape)
+    return (stride[0] if shape[0] > 1 else shape[1] * shape[2]), shape
 
 
 def pa_rope_write_kv(q, k, v, positions, inv_freq, axis, slot_mapping, k_cache, v_cache, q_out,
@@ -433,29 +444,27 @@ def pa_rope_write_kv(q, k, v, positions, inv_freq, axis, slot_mapping, k_cache, 
     axis of each frequency, or None for axis 0; q_out bf16 [T, Hq, d] (may be
     a contiguous q).  q and q_out may both be None."""
     dev = k.get_device()
-    ks, T, hkv, d = _token_rows(k, "k", dev)
-    vs, Tv, hv, dv = _token_rows(v, "v", dev)
+    ks, rows = _token_rows(k, "k", dev)
+    vs, v_rows = _token_rows(v, "v", dev)
+    T, hkv, d = rows
     qs = hq = 0
     if q is not None:
-        qs, Tq, hq, dq = _token_rows(q, "q", dev)
+        qs, q_rows = _token_rows(q, "q", dev)
+        Tq, hq, dq = q_rows
         if Tq != T or dq != d:
             raise ValueError("k and v must be [T, num_kv_heads, head_dim], q [T, Hq, head_dim]")
-        if q_out is None or q_out.shape != q.shape:
+        if q_out is None or q_out.shape != q_rows:
             raise ValueError("q_out must have q's shape")
     elif q_out is not None:
         raise ValueError("q_out without q")
     if ((q_out is not None and _off(q_out, _BF16, dev)) or _off(positions, _I32, dev) or
             _off(inv_freq, _F64, dev) or _off(slot_mapping, _I64, dev) or
-            (axis is not None and _off(axis, _I32, dev)) or k_cache.get_device() != dev or
-            v_cache.get_device() != dev or dev != torch._C._cuda_getDevice() or
-            (k_scale is not None and (k_scale.get_device() != dev or v_scale.get_device() != dev))):
+            (axis is not None and _off(axis, _I32, dev)) or dev != torch._C._cuda_getDevice()):
         _explain(dev, (("q_out", q_out, _BF16), ("positions", positions, _I32),
                        ("inv_freq", inv_freq, _F64), ("slot_mapping", slot_mapping, _I64),
-                       ("axis", axis, _I32), ("k_cache", k_cache, None),
-                       ("v_cache", v_cache, None), ("k_scale", k_scale, None),
-                       ("v_scale", v_scale, None)))
-    kv = kv_desc(k_cache, v_cache, k_scale, v_scale)
-    if Tv != T or hv != hkv or dv != d or hkv != kv.num_kv_heads or d != kv.head_dim:
+                       ("axis", axis, _I32)))
+    kv = _pool(k_cache, v_cache, k_scale, v_scale, dev)
+    if v_rows != rows or hkv != kv.num_kv_heads or d != kv.head_dim:
         raise ValueError("k and v must be [T, num_kv_heads, head_dim], q [T, Hq, head_dim]")
     axes = positions.shape
     if len(axes) == 1:

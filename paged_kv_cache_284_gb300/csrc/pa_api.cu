@@ -356,12 +356,14 @@ int stage_prefix(const PrefixStage &ps, const pa_kv_desc *kv, const int32_t *pre
     return PA_OK;
 }
 
-int make_maps(StepMaps *m, const void *q, const pa_kv_desc *kv, int tokens, int heads) {
+// need_q: only the tensor-core kernel reads q through a map
+int make_maps(StepMaps *m, const void *q, const pa_kv_desc *kv, int tokens, int heads,
+              bool need_q = true) {
     const int group = heads / kv->num_kv_heads;
     const bool fp8 = kv->kv_dtype == PA_KV_FP8_E4M3;
     int rc = make_kv_map(&m->k, kv->k_cache, kv_rows(kv), kv->head_dim, fp8);
     if (rc == PA_OK) rc = make_kv_map(&m->v, kv->v_cache, kv_rows(kv), kv->head_dim, fp8);
-    if (rc == PA_OK)
+    if (rc == PA_OK && need_q)
         rc = make_q_map(&m->q, q, tokens, heads, kv->head_dim, group, q_tile_tokens(group));
     return rc;
 }
@@ -979,7 +981,10 @@ int attention_entry(const void *q, const pa_kv_desc *kv, const int32_t *block_ta
     DeviceInfo *dev;
     if ((rc = device_info(&dev)) != PA_OK) return rc;
     StepMaps maps;
-    if ((rc = make_maps(&maps, q, kv, num_q_tokens, num_q_heads)) != PA_OK) return rc;
+    // (a windowed step of few tokens has no long request: see run_step)
+    const bool any_long =
+        !win || num_q_tokens > kShortMaxRows / (num_q_heads / kv->num_kv_heads);
+    if ((rc = make_maps(&maps, q, kv, num_q_tokens, num_q_heads, any_long)) != PA_OK) return rc;
     // an fp8 pool stages long requests in the workspace beyond the layout
     Staging stg;
     if ((rc = make_staging(&stg, kv, static_cast<uint8_t *>(workspace), L.total, workspace_bytes)) !=

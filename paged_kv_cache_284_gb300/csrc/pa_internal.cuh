@@ -304,8 +304,7 @@ struct RopeParams {
     int num_tokens, num_q_heads, num_kv_heads, head_dim, block_size;
     int rot_dim, num_axes, adjacent, fp8;
     float attn_factor;
-    int64_t num_slots;      // num_blocks * block_size
-    int parts, part_heads;  // a token's heads (q, k, v in turn) in runs of part_heads
+    int64_t num_slots;  // num_blocks * block_size
     unsigned *status;
 };
 
@@ -380,7 +379,7 @@ int launch_stage_fp8(const pa_kv_desc *kv, const int32_t *block_tables, int32_t 
 int launch_stage_prefix_fp8(const pa_kv_desc *kv, const int32_t *prefix_blocks, int n,
                             int32_t *ident, void *stage_k, void *stage_v, unsigned *status,
                             int grid, cudaStream_t s);
-int launch_rope_write(RopeParams p, int sms, cudaStream_t s);
+int launch_rope_write(const RopeParams &p, int sms, cudaStream_t s);
 int launch_copy_blocks(const pa_kv_desc *kv, int num_layers, const int32_t *pairs, int num_pairs,
                        int sms, unsigned *status, cudaStream_t s);
 int launch_plan(const PlanParams &p, cudaStream_t s);
@@ -579,6 +578,20 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *tm, in
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
         "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+        : "memory");
+}
+// Untiled bulk copy: both addresses and the size in multiples of 16 bytes.
+__device__ __forceinline__ uint64_t evict_first_policy() {
+    uint64_t policy;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    return policy;
+}
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes,
+                                          uint64_t *bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1], %2, [%3], %4;" ::"r"(smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
 }
 // L2 prefetch of slice `part` of `parts` of [base, base + bytes) by the 32
