@@ -57,11 +57,11 @@ struct WinGeom {
     static constexpr int kOffK = kOffQ + kQBytes;
     static constexpr int kOffV = kOffK + kRing * kKVBytes;
     static constexpr int kOffBar = kOffV + kRing * kKVBytes;
-    static constexpr int kOffCtl = kOffBar + 304;
+    static constexpr int kOffCtl = kOffBar + 336;
     // items published by the K producer, their count, and how many each warp has read
     static constexpr int kOffQueue = kOffCtl + 32;
     static constexpr int kOffRead = kOffQueue + kQueue * static_cast<int>(sizeof(WinItem));
-    // per row: references by tile parity [2][128], sums by group [2][128]
+    // per row: references by tile parity [2][128], sums by item parity [2][128]
     static constexpr int kOffRef = kOffRead + 64;
     static constexpr int kOffSum = kOffRef + 2 * 128 * 4;
     static constexpr int kSmemRaw = kOffSum + 2 * 128 * 4;
@@ -82,10 +82,10 @@ struct Bars {
     uint64_t s_full[2], s_free[2];  // scores of a tile written / read (4 warps)
     uint64_t p_full[2], pv_done[2]; // P of a tile written (4 warps) / its P V finished
     uint64_t ref[4][2];         // reference of a tile published, by row quarter and tile parity
-    uint64_t sums[4];           // both groups' sums of an item written, by row quarter
+    uint64_t sums[2][4];        // the other group's sums of an item left, by item parity and quarter
     uint64_t o_free, drain, drain_pv;
 };
-static_assert(sizeof(Bars) <= 304, "barrier area");
+static_assert(sizeof(Bars) <= 336, "barrier area");
 
 // Items in order, one reader per warp.  Warp 0, which runs ahead of every other
 // role, takes an item's index -- from the step's counter, shared by every
@@ -352,9 +352,10 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
         for (int i = 0; i < 4; ++i) {
             mbar_init(&bars->ref[i][0], 1);
             mbar_init(&bars->ref[i][1], 1);
-            mbar_init(&bars->sums[i], 2);
+            mbar_init(&bars->sums[0][i], 1);
+            mbar_init(&bars->sums[1][i], 1);
         }
-        mbar_init(&bars->o_free, 2 * kGroupWarps);
+        mbar_init(&bars->o_free, kGroupWarps);
         mbar_init(&bars->drain, 1);
         mbar_init(&bars->drain_pv, 1);
         ctl[0] = 0;
@@ -483,7 +484,7 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
         const int ttok = r / p.group;
         const int jh = r - ttok * p.group;
         float *refs = reinterpret_cast<float *>(smem + G::kOffRef) + r;  // [parity * 128]
-        float *sums = reinterpret_cast<float *>(smem + G::kOffSum) + r;  // [grp * 128]
+        float *sums = reinterpret_cast<float *>(smem + G::kOffSum) + r;  // [item parity * 128]
         uint32_t t = 0, k_item = 0;
         bool ok = true;
         for (; ok; ++k_item) {
@@ -497,6 +498,7 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
             // scores in log2 units; an fp8 pool's K scale folds in here
             const float sl2 = p.k_scale ? p.scale_log2 * __ldg(p.k_scale + it.h) : p.scale_log2;
             float ref = -INFINITY, l = 0.f;  // this group's sum, against `ref`
+            float before = -INFINITY;        // the reference of the tile before the last one done
             for (int j = (t & 1) == static_cast<uint32_t>(grp) ? 0 : 1; j < it.nt; j += 2) {
                 const uint32_t tt = t + j;
                 const int kb = j * kLongKeys;
@@ -547,7 +549,7 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
                 if (need_mask) mask(kb);
                 row_max();
                 // the reference: the tile before's, unless this tile exceeds it
-                float before = -INFINITY;
+                before = -INFINITY;
                 if (tt > 0) {
                     if (!warp_mbar_wait_spin(&bars->ref[wq][(tt - 1) & 1], ((tt - 1) >> 1) & 1, abort_flag)) { ok = false; break; }
                     if (j > 0) before = *reinterpret_cast<volatile float *>(refs + ((tt - 1) & 1) * 128);
@@ -657,22 +659,25 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
                 if (lane == 0) mbar_arrive(&bars->p_full[grp]);
             }
 
-            // ---- epilogue: this group's half of the output columns ----
+            if (!ok) break;
+            // ---- epilogue ----
+            // The group of the item's last tile writes the output; the other
+            // leaves its sum (against the last tile's `before`) and goes on to
+            // the next item, whose first tile is its own.
             const uint32_t last = t + it.nt - 1;
-            float final_ref = -INFINITY;
-            // (the last P V first: it implies that both groups have read the
-            // item before's sums, which are overwritten below)
-            if (ok) ok = warp_mbar_wait_spin(&bars->pv_done[last & 1], (last >> 1) & 1, abort_flag);
-            if (ok) ok = warp_mbar_wait_spin(&bars->ref[wq][last & 1], (last >> 1) & 1, abort_flag);
-            if (ok) {
-                final_ref = *reinterpret_cast<volatile float *>(refs + (last & 1) * 128);
-                if (ref != final_ref) l = ref == -INFINITY ? 0.f : l * fast_exp2(ref - final_ref);
-                *reinterpret_cast<volatile float *>(sums + grp * 128) = l;
+            float *left = sums + (k_item & 1) * 128;
+            uint64_t *sums_bar = &bars->sums[k_item & 1][wq];
+            t += it.nt;
+            if ((last & 1) != static_cast<uint32_t>(grp)) {
+                *reinterpret_cast<volatile float *>(left) = l;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->sums[wq]);
-                ok = warp_mbar_wait_spin(&bars->sums[wq], k_item & 1, abort_flag);
-                if (ok) l += *reinterpret_cast<volatile float *>(sums + (1 - grp) * 128);
+                if (lane == 0) mbar_arrive(sums_bar);
+                continue;
             }
+            ok = warp_mbar_wait_spin(sums_bar, (k_item >> 1) & 1, abort_flag);
+            if (ok && before != -INFINITY)
+                l += *reinterpret_cast<volatile float *>(left) * fast_exp2(before - ref);
+            if (ok) ok = warp_mbar_wait_spin(&bars->pv_done[last & 1], (last >> 1) & 1, abort_flag);
             if (!ok) break;
             tc_fence_after();
             // an fp8 pool's V scale multiplies the output
@@ -680,14 +685,19 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
             const float inv = l > 0.f ? vsc / l : 0.f;
             const int64_t orow = static_cast<int64_t>(it.tok0 + ttok) * p.num_q_heads +
                                  it.h * p.group + jh;
+            uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * D);
 #pragma unroll
-            for (int qd = 0; qd < D / 64; ++qd) {
-                const int col = grp * (D / 2) + qd * 32;
+            for (int qd = 0; qd < D / 32; ++qd) {
                 uint32_t raw[32];
-                tmem_ld32(t_lane + G::kColO + col, raw);
+                tmem_ld32(t_lane + G::kColO + qd * 32, raw);
                 tmem_wait_ld();
+                if (qd == D / 32 - 1) {
+                    // O has been read: the next item's first P V may overwrite it
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->o_free);
+                }
                 if (!row_valid) continue;
-                uint4 *dst = reinterpret_cast<uint4 *>(p.out + orow * D + col);
 #pragma unroll
                 for (int v4 = 0; v4 < 4; ++v4) {
                     uint4 w;
@@ -695,16 +705,11 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
                     w.y = pack_bf16x2(__uint_as_float(raw[v4 * 8 + 2]) * inv, __uint_as_float(raw[v4 * 8 + 3]) * inv);
                     w.z = pack_bf16x2(__uint_as_float(raw[v4 * 8 + 4]) * inv, __uint_as_float(raw[v4 * 8 + 5]) * inv);
                     w.w = pack_bf16x2(__uint_as_float(raw[v4 * 8 + 6]) * inv, __uint_as_float(raw[v4 * 8 + 7]) * inv);
-                    dst[v4] = w;
+                    dst[qd * 4 + v4] = w;
                 }
             }
-            // O has been read: the next item's first P V may overwrite it
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->o_free);
-            if (row_valid && grp == 0 && p.lse)
-                p.lse[orow] = l > 0.f ? (final_ref + __log2f(l)) * kLn2 : -INFINITY;
-            t += it.nt;
+            if (row_valid && p.lse)
+                p.lse[orow] = l > 0.f ? (ref + __log2f(l)) * kLn2 : -INFINITY;
         }
     }
 
