@@ -398,27 +398,32 @@ def pa_window_attention(q, k_cache, v_cache, block_tables, query_start_loc, cont
     T, hq, d = shape
     B = seq_lens.numel()
     tables = block_tables.shape
-    if d != kv.head_dim or out.shape != shape or (lse is not None and lse.shape != shape[:2]):
+    if d != kv.head_dim or out.shape != shape or (lse is not None and lse.numel() != T * hq):
         raise ValueError("q and out must be [T, Hq, head_dim], lse [T, Hq]")
     if len(tables) != 2 or tables[0] != B or context_lens.numel() != B or \
             query_start_loc.numel() != B + 1:
         raise ValueError("block_tables [B, N], query_start_loc [B + 1], context_lens [B] and "
                          "seq_lens [B] must agree")
     L = lib()
+    args = (q.data_ptr(), kv, block_tables.data_ptr(), tables[1], query_start_loc.data_ptr(),
+            context_lens.data_ptr(), seq_lens.data_ptr(), B, T, hq, scale, int(window),
+            int(num_sinks), out.data_ptr(), None if lse is None else lse.data_ptr())
+    handle = _raw_stream(stream, dev)
+    staged = staging_blocks > 0 and kv.kv_dtype == PA_KV_FP8_E4M3
+    if workspace is not None and not staged:
+        # the call itself checks the size, before it launches anything
+        rc = L.pa_window_attention(*args, workspace.data_ptr(), workspace.nbytes, handle)
+        if rc == PA_OK:
+            return workspace
+        if rc != PA_ERR_WORKSPACE:
+            _check(rc, "pa_window_attention")
     need = L.pa_attention_workspace_size(B, T, hq, kv.num_kv_heads, d)
-    if staging_blocks > 0 and kv.kv_dtype == PA_KV_FP8_E4M3:
+    if staged:
         need += L.pa_fp8_staging_bytes(kv.num_kv_heads, d, kv.block_size, int(staging_blocks))
-    room = 0 if workspace is None else workspace.nbytes
-    if room < need:
+    if workspace is None or workspace.nbytes < need:
         workspace = alloc_workspace(need, q.device)
-        room = workspace.nbytes
-    rc = L.pa_window_attention(q.data_ptr(), kv, block_tables.data_ptr(), tables[1],
-                               query_start_loc.data_ptr(), context_lens.data_ptr(),
-                               seq_lens.data_ptr(), B, T, hq, scale, int(window), int(num_sinks),
-                               out.data_ptr(), None if lse is None else lse.data_ptr(),
-                               workspace.data_ptr(), room, _raw_stream(stream, dev))
-    if rc:
-        _check(rc, "pa_window_attention")
+    _check(L.pa_window_attention(*args, workspace.data_ptr(), workspace.nbytes, handle),
+           "pa_window_attention")
     return workspace
 
 

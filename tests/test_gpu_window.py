@@ -188,6 +188,10 @@ def test_no_lse_and_a_kept_workspace():
     assert st.call(t, workspace=ws) is ws
     torch.cuda.synchronize()
     assert torch.equal(t["out"], first)
+    small = pk.alloc_workspace(4096, DEV)          # too small: a fresh one is used
+    assert st.call(t, workspace=small) is not small
+    torch.cuda.synchronize()
+    assert torch.equal(t["out"], first)
     t["lse"], lse = None, t["lse"]
     st.call(t, workspace=ws)
     torch.cuda.synchronize()
