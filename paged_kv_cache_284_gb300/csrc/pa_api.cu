@@ -161,9 +161,11 @@ int q_tile_tokens(int group) { return group <= kLongRows ? kLongRows / group : 0
 
 // Query tokens per split-KV piece (a piece fills at most kShortMaxRows rows),
 // and a bound on the pieces of a step with these sizes.
-int piece_tokens_for(int group) { return std::max(1, kShortMaxRows / std::max(1, group)); }
-int pieces_bound(int num_seqs, int num_q_tokens, int group) {
-    const int pt = piece_tokens_for(group);
+int piece_tokens_for(int group, int rows = kShortMaxRows) {
+    return std::max(1, rows / std::max(1, group));
+}
+int pieces_bound(int num_seqs, int num_q_tokens, int group, int rows = kShortMaxRows) {
+    const int pt = piece_tokens_for(group, rows);
     return num_seqs + (num_q_tokens + pt - 1) / pt;
 }
 
@@ -516,16 +518,48 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         forbid_long ? 0 : std::min(num_seqs, T / std::max(1, min_long_tokens));
     const bool side_by_side =
         max_long_reqs > 0 && T >= kSideBySideMinTokens && !profiling_active();
+    // Side by side, the first tensor-core grid's share of the SMs, measured best
+    // on the mixed step: two fifths beside the HBM-bound bf16 split-KV kernel
+    // (60 of 152 SMs: 767.9 us per step, against 769.6 with 56, 773.4 with 64
+    // and 785.4 with 50); a tenth beside the fp8 one, whose rate follows its SM
+    // count (707.3 us, 710.1 with an eighth).
+    const int first_grid =
+        side_by_side ? std::max(1, fp8 ? dev->sms / 10 : dev->sms * 2 / 5) : 0;
+    bool rows_kernel = false;
     if (win) {
-        // the windowed planner keeps its table at the end of the partial states
+        // The windowed decode kernel (a warp per job) or the split-KV kernel (four
+        // warps per job, CTAs side by side)?  A request of more than kWindowRows
+        // rows would read its keys more than once in the former, so the step's
+        // average decides; and its warps want jobs of their own.  Decode, 8 kv
+        // heads, head_dim 128, window 1024: 48 requests 54 us against 67, 64
+        // 60.4 / 67.6, 128 98 / 119; but 32 requests 43 / 43 and 16 33 / 29.
+        // With 20 rows a request (128 of them beside prompt chunks) 202 / 188.
+        // e4m3 pools: the decoding of the codes bounds both (256 requests, window
+        // 4096: 294-300 / 296 us), the split-KV kernel alone serves them.
+        const int pieces16 = pieces_bound(num_seqs, T, group, kWindowRows);
+        rows_kernel = !fp8 && group <= kWindowRows &&
+                      static_cast<int64_t>(T) * group <=
+                          static_cast<int64_t>(num_seqs) * kWindowRows &&
+                      static_cast<int64_t>(num_seqs) * kv->num_kv_heads >= 2 * dev->sms &&
+                      static_cast<int64_t>(pieces16) * kv->num_kv_heads <= L.max_short;
         pp.win = *win;
         pp.max_keys = max_blocks * kv->block_size;
         pp.max_pieces = pieces_bound(num_seqs, T, group);
+        if (rows_kernel) {
+            pp.piece_tokens = piece_tokens_for(group, kWindowRows);
+            pp.num_ctas = (dev->sms - first_grid) * window_rows_workers_per_sm(D);
+            pp.max_pieces = pieces16;
+            pp.worker_warps = side_by_side ? 2 : 1;
+        }
+        // The windowed planner keeps its table and the splits' completion
+        // counters at the end of the partial states.
         const size_t row = sizeof(float) * D;
-        const int piece_rows = static_cast<int>(
-            (sizeof(WindowPiece) * static_cast<size_t>(pp.max_pieces) + row - 1) / row);
-        pp.cap_rows -= piece_rows;
+        pp.num_counters = pp.max_pieces * kv->num_kv_heads;
+        const size_t bytes = sizeof(WindowPiece) * static_cast<size_t>(pp.max_pieces) +
+                             sizeof(int) * static_cast<size_t>(pp.num_counters);
+        pp.cap_rows -= static_cast<int>((bytes + row - 1) / row);
         pp.pieces = reinterpret_cast<WindowPiece *>(ws + L.partial_o + row * pp.cap_rows);
+        pp.counters = reinterpret_cast<int *>(pp.pieces + pp.max_pieces);
     }
     int rc;
     if (fresh && fresh->num_tokens > 0) {
@@ -583,6 +617,15 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
     const int stall = g_test_stall.load(std::memory_order_relaxed);
     sp.test_stall = stall == PA_TEST_STALL_SPLIT_KV ? 1 : 0;
 
+    if (rows_kernel) {
+        sp.k_pool = static_cast<const uint8_t *>(kv->k_cache);
+        sp.v_pool = static_cast<const uint8_t *>(kv->v_cache);
+    }
+    auto split_kv = [&](const ShortParams &params) {
+        return rows_kernel
+                   ? launch_window_rows(params, maps.k, maps.v, D, dev->sms, s)
+                   : launch_short(params, maps.k, maps.v, D, fp8, win != nullptr, short_grid, s);
+    };
     if (casc) {
         // Cascade decode ([AI] §02.1): the shared-prefix pass (tensor cores,
         // compute-heavy, each prefix tile read once per 128 query rows) and
@@ -627,7 +670,7 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         sp.test_stall = 0;
         sp.out_f32 = casc->suffix_o;
         sp.lse = casc->suffix_lse;
-        rc = launch_short(sp, maps.k, maps.v, D, fp8, win != nullptr, short_grid, s);
+        rc = split_kv(sp);
         if (rc != PA_OK) return fail(rc, "split-KV kernel launch failed: %s",
                                      cudaGetErrorString(cudaGetLastError()));
         LongParams c2 = cp;
@@ -715,19 +758,14 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         l1.wait_start = 1;
         l1.first_done = &hdr->first_done;
         l1.first_ctas = -1;
-        // share of the SMs measured best on the mixed step: two fifths beside
-        // the HBM-bound bf16 split-KV kernel (60 of 152 SMs: 767.9 us per step,
-        // against 769.6 with 56, 773.4 with 64 and 785.4 with 50); a tenth
-        // beside the fp8 one, whose rate follows its SM count (707.3 us, 710.1
-        // with an eighth)
-        const int g1 = std::min(std::max(1, fp8 ? dev->sms / 10 : dev->sms * 2 / 5), long_grid);
+        const int g1 = std::min(first_grid, long_grid);
         rc = tensor_core(l1, g1);
         if (rc != PA_OK) return fail(rc, "tensor-core kernel launch failed: %s",
                                      cudaGetErrorString(cudaGetLastError()));
         sp.no_start_wait = 1;
         sp.claim_ahead = 0;
         sp.test_stall = 0;
-        rc = launch_short(sp, maps.k, maps.v, D, fp8, win != nullptr, short_grid, s);
+        rc = split_kv(sp);
         if (rc != PA_OK) return fail(rc, "split-KV kernel launch failed: %s",
                                      cudaGetErrorString(cudaGetLastError()));
         LongParams l2 = lp;
@@ -744,7 +782,7 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
 
     {
         ProfScope prof(PA_KERNEL_SPLIT_KV, s);
-        rc = launch_short(sp, maps.k, maps.v, D, fp8, win != nullptr, short_grid, s);
+        rc = split_kv(sp);
     }
     if (rc != PA_OK) return fail(rc, "split-KV kernel launch failed: %s",
                                  cudaGetErrorString(cudaGetLastError()));

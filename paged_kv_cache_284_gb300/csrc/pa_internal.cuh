@@ -28,6 +28,7 @@ constexpr int kShortStages = 3;       // split-KV kernel: pipeline depth
 constexpr int kShortMaxRows = 64;     // rows (q_len * group) a split-KV item may hold
 constexpr int kShortConsumerWarps = 4;
 constexpr int kShortThreads = 32 * (kShortConsumerWarps + 1);
+constexpr int kWindowRows = 16;       // windowed decode kernel: rows of a work item
 constexpr int kLongRows = 128;        // tcgen05 tile: M = 128 query rows
 constexpr int kLongKeys = 128;        // tcgen05 tile: N = 128 keys per KV tile
 constexpr int kLongThreads = 384;     // 12 warps: K+Q loads, QK^T, 8 x softmax, V loads, PV
@@ -205,6 +206,7 @@ struct ShortParams {
     int max_items;               // work-record capacity of the workspace (>= 1)
     int claim_ahead;  // ring stages before an item's end at which the next is claimed (0: at its start)
     WindowArgs win;   // windowed step only
+    const uint8_t *k_pool, *v_pool;  // windowed decode kernel: for its L2 prefetch
     int test_stall;   // test hook: CTA 0's producer stops after its first stage
 };
 
@@ -264,6 +266,7 @@ struct PlanParams {
     int max_keys;  // a request longer than its table is skipped
     WindowPiece *pieces;
     int max_pieces;
+    int worker_warps;  // num_ctas counts the windowed decode kernel's warps
     int *stage_base, *stage_list;
     int split_stages;    // 0 = automatic
     int target_items;    // automatic split aims at about this many split-KV items
@@ -387,6 +390,9 @@ int launch_plan_window(const PlanParams &p, cudaStream_t s);
 int launch_short(const ShortParams &p, const CUtensorMap &tk, const CUtensorMap &tv,
                  int head_dim, bool fp8, bool windowed, int grid, cudaStream_t s);
 int short_max_ctas_per_sm(int head_dim, bool fp8, bool windowed);
+int window_rows_workers_per_sm(int head_dim);
+int launch_window_rows(const ShortParams &p, const CUtensorMap &tk, const CUtensorMap &tv,
+                       int head_dim, int grid, cudaStream_t s);
 int launch_long(const LongParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
                 const CUtensorMap &tv, int head_dim, int grid, cudaStream_t s);
 int launch_long_window(const LongParams &p, const CUtensorMap &tq, const CUtensorMap &tk,

@@ -291,3 +291,89 @@ def test_bad_block_and_bad_metadata_are_flagged():
     ref, _, _ = ops.window_attention(st.q.double().numpy(), st.k64, st.v64, st.table.numpy(),
                                      st.qsl.numpy(), st.ctx.numpy(), st.scale, 20, 2, 16)
     assert np.abs(t["out"][3].double().cpu().numpy() - ref[3]).max() < 0.05
+
+
+# bf16 batches of at most 16 rows a request on average and two or more (request,
+# kv head) pairs per SM of a 152-SM GPU take the windowed decode kernel.
+def many(n, spread, rng, new=(1, 2)):
+    return [(int(c), int(m)) for c, m in zip(rng.integers(0, spread, n), rng.integers(*new, n))]
+
+
+@pytest.mark.parametrize("kv,d", [("bf16", 128), ("bf16", 64), ("e4m3", 128)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (16, 4), (33, 17), (100, 130), (700, 5)])
+def test_large_batches(kv, d, window, sinks):
+    rng = np.random.default_rng(window)
+    reqs = many(45, 900, rng, (1, 6)) + [(0, 1), (15, 1), (16, 1), (0, 0), (63, 4), (5, 0)]
+    Step(reqs, 28, 7, d, 16, window, sinks, kv=kv, seed=window, pad=3).run_and_check()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("group,bs,new", [(1, 64, 17), (5, 16, 5), (8, 48, 3), (16, 32, 3),
+                                          (17, 16, 2)])
+def test_large_batches_of_other_groups(kv, group, bs, new):
+    """Pieces of 16 / group tokens; a group of 17 stays with the other kernel."""
+    rng = np.random.default_rng(group)
+    reqs = many(80, 400, rng, (1, new)) + [(0, 0)] * 60
+    assert group == 17 or sum(n for _, n in reqs) * group <= 16 * len(reqs)
+    Step(reqs, 4 * group, 4, 128, bs, 130, 7, kv=kv, seed=group).run_and_check()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_large_batches_of_more_jobs_than_warps(kv):
+    """Over 2000 jobs: whole ones, several to a warp, a few of them long."""
+    rng = np.random.default_rng(8)
+    Step(many(260, 120, rng) + [(3000, 1), (2500, 2)], 16, 8, 128, 16, 2000, 20, kv=kv,
+         seed=8).run_and_check()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_large_batches_split_over_the_window(kv):
+    Step([(5000 - 37 * i, 1) for i in range(40)], 16, 8, 128, 16, 1500, 37, kv=kv,
+         seed=9).run_and_check()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_a_large_batch_beside_prompt_chunks(kv):
+    rng = np.random.default_rng(10)
+    reqs = many(330, 400, rng, (1, 3)) + [(100, 300), (0, 140), (411, 70)]
+    assert 512 <= sum(n for _, n in reqs) <= 4 * len(reqs)
+    st = Step(reqs, 8, 2, 128, 16, 150, 9, kv=kv, seed=10)
+    t = st.run_and_check()
+    first = t["out"].clone()
+    for _ in range(3):
+        st.call(t)
+    torch.cuda.synchronize()
+    assert torch.equal(t["out"], first)
+
+
+def test_a_large_batch_flags_a_bad_block_and_reads_inside_the_pool():
+    rng = np.random.default_rng(11)
+    st = Step(many(60, 300, rng), 16, 8, 128, 16, 100, 4, seed=11)
+    t = st.to_dev()
+    last = (int(st.ctx[5])) // 16
+    t["table"][5, last] = st.num_blocks + 7
+    st.call(t)
+    torch.cuda.synchronize()
+    assert pk.read_device_status(clear=True) & pk.PA_DEV_BAD_BLOCK
+    t["table"][5, last] = st.table[5, last].item()
+    st.call(t)
+    torch.cuda.synchronize()
+    st.check(t)
+    assert_status_clean()
+
+
+def test_a_large_batch_times_out_when_chunks_never_come():
+    rng = np.random.default_rng(12)
+    st = Step(many(60, 300, rng), 16, 8, 128, 16, 100, 4, seed=12)
+    t = st.to_dev()
+    pk.set_test_stall(pk.PA_TEST_STALL_SPLIT_KV)
+    try:
+        st.call(t)
+        torch.cuda.synchronize()
+    finally:
+        pk.set_test_stall(pk.PA_TEST_STALL_NONE)
+    assert pk.read_device_status(clear=True) & pk.PA_DEV_WAIT_TIMEOUT
+    st.call(t)
+    torch.cuda.synchronize()
+    st.check(t)
+    assert_status_clean()
