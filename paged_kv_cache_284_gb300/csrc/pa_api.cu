@@ -150,6 +150,26 @@ struct ProfScope {
 // kernels side by side (below it they run one after the other).
 constexpr int kSideBySideMinTokens = 512;
 
+// A windowed step of groups of at most 16 runs as one kernel (window_direct_kernel)
+// in place of the plan and the planned kernels
+//  * when its pieces (of 16 rows), kv heads and windows bound its work to
+//    kDirectAnyChunks chunks on at most kDirectJobsPerSm jobs per SM, whatever its
+//    requests are: a lone token at window 128 takes 5.7 us against 11.5, 24 verify
+//    requests 7.8 against 20.6, a prompt chunk of 64 tokens at window 128 10.2
+//    against 14.3; but one of 256 20.8 / 14.7;
+//  * beyond that when it has few rows, or no more than a piece's per request on
+//    average (a chunk of 64 tokens at window 4096: 33 us against 43; of 128, past
+//    the bound: 57 / 43).  Decode, 8 kv heads, d = 128: 16 requests at window 1024
+//    17.8 us against 28.5, 64 49.7 / 67.6, 256 126 / 155 at window 700 and 50 / 73
+//    at 128, 800 at window 128 149 / 179;
+//  * on e4m3 pools, where decoding the codes bounds both, only while there is
+//    little to decode: 32 requests at window 2048 36 us against 43, 64 at window
+//    4096 115 / 107.
+constexpr int64_t kDirectAnyChunks = 4096;
+constexpr int64_t kDirectJobsPerSm = 7;
+constexpr int64_t kDirectAnyRows = 256;
+constexpr int64_t kDirectE4m3Chunks = 65536;
+
 bool profiling_active() {
     std::lock_guard<std::mutex> lock(g_prof_mu);
     return g_prof[PA_KERNEL_SPLIT_KV][0] || g_prof[PA_KERNEL_TENSOR_CORE][0];
@@ -457,6 +477,45 @@ int check_window(int32_t window, int32_t num_sinks, float scale) {
     return PA_OK;
 }
 
+// Whether a windowed step is one for the one-kernel form, and its launch.
+bool direct_step(const WindowArgs &win, int num_seqs, int T, const pa_kv_desc *kv, int group,
+                 int max_blocks, int sms, DirectParams *dp) {
+    if (group > kDirectRows || num_seqs > kDirectMaxSeqs) return false;
+    dp->piece_tokens = piece_tokens_for(group, kDirectRows);
+    dp->max_pieces = std::min(T, pieces_bound(num_seqs, T, group, kDirectRows));
+    dp->max_keys = max_blocks * kv->block_size;
+    // chunks of a piece: its sinks', its rows' windows' (cut anywhere), at most
+    // its whole table's
+    const int64_t table = static_cast<int64_t>(max_blocks) * kv->block_size / kChunkKeys;
+    const int64_t seen = (static_cast<int64_t>(win.sinks) + kChunkKeys - 1) / kChunkKeys +
+                         (static_cast<int64_t>(win.window) + dp->piece_tokens) / kChunkKeys + 2;
+    const int64_t chunks = std::min(table, seen);
+    const int64_t jobs = static_cast<int64_t>(dp->max_pieces) * kv->num_kv_heads;
+    const int64_t rows = static_cast<int64_t>(T) * group;
+    if (jobs * chunks > kDirectAnyChunks || jobs > kDirectJobsPerSm * sms) {
+        if (rows > kDirectAnyRows && rows > static_cast<int64_t>(num_seqs) * kDirectRows)
+            return false;
+        if (kv->kv_dtype == PA_KV_FP8_E4M3 && jobs * chunks > kDirectE4m3Chunks) return false;
+    }
+    // CTAs per job and per SM: the fewest rounds times a CTA's time, in chunks of
+    // one warp at one CTA per SM (and what it costs besides, as much as twelve).
+    // Three CTAs per SM have shorter rings: 48 decode requests, 8 kv heads, window
+    // 1024: 36 us with three (one round), 47 with two; 64 requests 56 / 50.
+    int64_t best = -1;
+    for (int per = 2; per <= 3; ++per)
+        for (int c = 1; c <= kDirectMaxCluster; c *= 2) {
+            const int64_t per_warp = (chunks + kDirectWarps * c - 1) / (kDirectWarps * c);
+            const int64_t slots = static_cast<int64_t>(per) * sms;
+            const int64_t time = (jobs * c + slots - 1) / slots * (per_warp * per + 12);
+            if (best < 0 || time < best) {
+                best = time;
+                dp->cluster = c;
+                dp->per_sm = per;
+            }
+        }
+    return true;
+}
+
 // Runs the planner, the split-KV kernel and the tensor-core kernel of one
 // step on `s`.  With `casc` (cascade decode, all rows short) the step is
 // the unique-suffix pass, run side by side with the shared-prefix pass.
@@ -518,72 +577,17 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         forbid_long ? 0 : std::min(num_seqs, T / std::max(1, min_long_tokens));
     const bool side_by_side =
         max_long_reqs > 0 && T >= kSideBySideMinTokens && !profiling_active();
-    // Side by side, the first tensor-core grid's share of the SMs, measured best
-    // on the mixed step: two fifths beside the HBM-bound bf16 split-KV kernel
-    // (60 of 152 SMs: 767.9 us per step, against 769.6 with 56, 773.4 with 64
-    // and 785.4 with 50); a tenth beside the fp8 one, whose rate follows its SM
-    // count (707.3 us, 710.1 with an eighth).
-    const int first_grid =
-        side_by_side ? std::max(1, fp8 ? dev->sms / 10 : dev->sms * 2 / 5) : 0;
-    bool rows_kernel = false;
     if (win) {
-        // The windowed decode kernel (a warp per job) or the split-KV kernel (four
-        // warps per job, CTAs side by side)?  A request of more than kWindowRows
-        // rows would read its keys more than once in the former, so the step's
-        // average decides; and its warps want jobs of their own.  Decode, 8 kv
-        // heads, head_dim 128, window 1024: 48 requests 54 us against 67, 64
-        // 60.4 / 67.6, 128 98 / 119; but 32 requests 43 / 43 and 16 33 / 29.
-        // With 20 rows a request (128 of them beside prompt chunks) 202 / 188.
-        // e4m3 pools: the decoding of the codes bounds both (256 requests, window
-        // 4096: 294-300 / 296 us), the split-KV kernel alone serves them.
-        const int pieces16 = pieces_bound(num_seqs, T, group, kWindowRows);
-        rows_kernel = !fp8 && group <= kWindowRows &&
-                      static_cast<int64_t>(T) * group <=
-                          static_cast<int64_t>(num_seqs) * kWindowRows &&
-                      static_cast<int64_t>(num_seqs) * kv->num_kv_heads >= 2 * dev->sms &&
-                      static_cast<int64_t>(pieces16) * kv->num_kv_heads <= L.max_short;
+        // the windowed planner keeps its table at the end of the partial states
         pp.win = *win;
         pp.max_keys = max_blocks * kv->block_size;
         pp.max_pieces = pieces_bound(num_seqs, T, group);
-        if (rows_kernel) {
-            pp.piece_tokens = piece_tokens_for(group, kWindowRows);
-            pp.num_ctas = (dev->sms - first_grid) * window_rows_workers_per_sm(D);
-            pp.max_pieces = pieces16;
-            pp.worker_warps = side_by_side ? 2 : 1;
-        }
-        // The windowed planner keeps its table and the splits' completion
-        // counters at the end of the partial states.
         const size_t row = sizeof(float) * D;
-        pp.num_counters = pp.max_pieces * kv->num_kv_heads;
-        const size_t bytes = sizeof(WindowPiece) * static_cast<size_t>(pp.max_pieces) +
-                             sizeof(int) * static_cast<size_t>(pp.num_counters);
-        pp.cap_rows -= static_cast<int>((bytes + row - 1) / row);
+        const int piece_rows = static_cast<int>(
+            (sizeof(WindowPiece) * static_cast<size_t>(pp.max_pieces) + row - 1) / row);
+        pp.cap_rows -= piece_rows;
         pp.pieces = reinterpret_cast<WindowPiece *>(ws + L.partial_o + row * pp.cap_rows);
-        pp.counters = reinterpret_cast<int *>(pp.pieces + pp.max_pieces);
     }
-    int rc;
-    if (fresh && fresh->num_tokens > 0) {
-        // The step's new rows first, as pa_write_kv does: its kernel runs as a
-        // programmatic dependent ahead of the planner and is off the step's
-        // critical path.  (Writing them from copy blocks in the planner's
-        // grid measured no faster on an 8-request decode step and slower on
-        // large ones.)
-        ProfScope prof(PA_KERNEL_WRITE_KV, s);
-        rc = launch_write_kv(fresh->k, fresh->v, fresh->slots, fresh->num_tokens, kv, dev->status,
-                             s);
-        if (rc != PA_OK) return fail(rc, "write_kv launch failed");
-    }
-    {
-        ProfScope prof(PA_KERNEL_PLAN, s);
-        rc = win ? launch_plan_window(pp, s) : launch_plan(pp, s);
-    }
-    if (rc != PA_OK) return fail(rc, "plan launch failed");
-    if (staged) {
-        rc = launch_stage_fp8(kv, block_tables, max_blocks, hdr, pp.stage_base, pp.stage_list,
-                              stg.k, stg.v, dev->status, 2 * dev->sms, s, ctx, seq_lens, win);
-        if (rc != PA_OK) return fail(rc, "fp8 staging copy launch failed");
-    }
-
     ShortParams sp{};
     sp.q = static_cast<const __nv_bfloat16 *>(q);
     sp.out = static_cast<__nv_bfloat16 *>(out);
@@ -617,15 +621,36 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
     const int stall = g_test_stall.load(std::memory_order_relaxed);
     sp.test_stall = stall == PA_TEST_STALL_SPLIT_KV ? 1 : 0;
 
-    if (rows_kernel) {
-        sp.k_pool = static_cast<const uint8_t *>(kv->k_cache);
-        sp.v_pool = static_cast<const uint8_t *>(kv->v_cache);
+    DirectParams direct{};
+    if (win && direct_step(*win, num_seqs, T, kv, group, max_blocks, dev->sms, &direct)) {
+        ProfScope prof(PA_KERNEL_SPLIT_KV, s);
+        const int rc = launch_window_direct(sp, maps.k, maps.v, direct, D, fp8, s);
+        return rc == PA_OK ? PA_OK : fail(rc, "window kernel launch failed: %s",
+                                          cudaGetErrorString(cudaGetLastError()));
     }
-    auto split_kv = [&](const ShortParams &params) {
-        return rows_kernel
-                   ? launch_window_rows(params, maps.k, maps.v, D, dev->sms, s)
-                   : launch_short(params, maps.k, maps.v, D, fp8, win != nullptr, short_grid, s);
-    };
+    int rc;
+    if (fresh && fresh->num_tokens > 0) {
+        // The step's new rows first, as pa_write_kv does: its kernel runs as a
+        // programmatic dependent ahead of the planner and is off the step's
+        // critical path.  (Writing them from copy blocks in the planner's
+        // grid measured no faster on an 8-request decode step and slower on
+        // large ones.)
+        ProfScope prof(PA_KERNEL_WRITE_KV, s);
+        rc = launch_write_kv(fresh->k, fresh->v, fresh->slots, fresh->num_tokens, kv, dev->status,
+                             s);
+        if (rc != PA_OK) return fail(rc, "write_kv launch failed");
+    }
+    {
+        ProfScope prof(PA_KERNEL_PLAN, s);
+        rc = win ? launch_plan_window(pp, s) : launch_plan(pp, s);
+    }
+    if (rc != PA_OK) return fail(rc, "plan launch failed");
+    if (staged) {
+        rc = launch_stage_fp8(kv, block_tables, max_blocks, hdr, pp.stage_base, pp.stage_list,
+                              stg.k, stg.v, dev->status, 2 * dev->sms, s, ctx, seq_lens, win);
+        if (rc != PA_OK) return fail(rc, "fp8 staging copy launch failed");
+    }
+
     if (casc) {
         // Cascade decode ([AI] §02.1): the shared-prefix pass (tensor cores,
         // compute-heavy, each prefix tile read once per 128 query rows) and
@@ -670,7 +695,7 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         sp.test_stall = 0;
         sp.out_f32 = casc->suffix_o;
         sp.lse = casc->suffix_lse;
-        rc = split_kv(sp);
+        rc = launch_short(sp, maps.k, maps.v, D, fp8, win != nullptr, short_grid, s);
         if (rc != PA_OK) return fail(rc, "split-KV kernel launch failed: %s",
                                      cudaGetErrorString(cudaGetLastError()));
         LongParams c2 = cp;
@@ -758,14 +783,19 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         l1.wait_start = 1;
         l1.first_done = &hdr->first_done;
         l1.first_ctas = -1;
-        const int g1 = std::min(first_grid, long_grid);
+        // share of the SMs measured best on the mixed step: two fifths beside
+        // the HBM-bound bf16 split-KV kernel (60 of 152 SMs: 767.9 us per step,
+        // against 769.6 with 56, 773.4 with 64 and 785.4 with 50); a tenth
+        // beside the fp8 one, whose rate follows its SM count (707.3 us, 710.1
+        // with an eighth)
+        const int g1 = std::min(std::max(1, fp8 ? dev->sms / 10 : dev->sms * 2 / 5), long_grid);
         rc = tensor_core(l1, g1);
         if (rc != PA_OK) return fail(rc, "tensor-core kernel launch failed: %s",
                                      cudaGetErrorString(cudaGetLastError()));
         sp.no_start_wait = 1;
         sp.claim_ahead = 0;
         sp.test_stall = 0;
-        rc = split_kv(sp);
+        rc = launch_short(sp, maps.k, maps.v, D, fp8, win != nullptr, short_grid, s);
         if (rc != PA_OK) return fail(rc, "split-KV kernel launch failed: %s",
                                      cudaGetErrorString(cudaGetLastError()));
         LongParams l2 = lp;
@@ -782,7 +812,7 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
 
     {
         ProfScope prof(PA_KERNEL_SPLIT_KV, s);
-        rc = split_kv(sp);
+        rc = launch_short(sp, maps.k, maps.v, D, fp8, win != nullptr, short_grid, s);
     }
     if (rc != PA_OK) return fail(rc, "split-KV kernel launch failed: %s",
                                  cudaGetErrorString(cudaGetLastError()));

@@ -28,7 +28,7 @@ constexpr int kShortStages = 3;       // split-KV kernel: pipeline depth
 constexpr int kShortMaxRows = 64;     // rows (q_len * group) a split-KV item may hold
 constexpr int kShortConsumerWarps = 4;
 constexpr int kShortThreads = 32 * (kShortConsumerWarps + 1);
-constexpr int kWindowRows = 16;       // windowed decode kernel: rows of a work item
+constexpr int kDirectRows = 16;       // one-kernel windowed step: rows of a piece
 constexpr int kLongRows = 128;        // tcgen05 tile: M = 128 query rows
 constexpr int kLongKeys = 128;        // tcgen05 tile: N = 128 keys per KV tile
 constexpr int kLongThreads = 384;     // 12 warps: K+Q loads, QK^T, 8 x softmax, V loads, PV
@@ -206,9 +206,19 @@ struct ShortParams {
     int max_items;               // work-record capacity of the workspace (>= 1)
     int claim_ahead;  // ring stages before an item's end at which the next is claimed (0: at its start)
     WindowArgs win;   // windowed step only
-    const uint8_t *k_pool, *v_pool;  // windowed decode kernel: for its L2 prefetch
     int test_stall;   // test hook: CTA 0's producer stops after its first stage
 };
+
+// A windowed step in one kernel: clusters of `cluster` CTAs for each of
+// max_pieces pieces x kv heads.
+struct DirectParams {
+    int per_sm;  // CTAs per SM: 2 or 3
+    int cluster, max_pieces, piece_tokens;
+    int max_keys;  // a request longer than its table is skipped
+};
+constexpr int kDirectMaxSeqs = 1024;  // eight per thread
+constexpr int kDirectWarps = 4;       // per CTA
+constexpr int kDirectMaxCluster = 8;  // the portable cluster size
 
 struct LongParams {
     __nv_bfloat16 *out;
@@ -266,7 +276,6 @@ struct PlanParams {
     int max_keys;  // a request longer than its table is skipped
     WindowPiece *pieces;
     int max_pieces;
-    int worker_warps;  // num_ctas counts the windowed decode kernel's warps
     int *stage_base, *stage_list;
     int split_stages;    // 0 = automatic
     int target_items;    // automatic split aims at about this many split-KV items
@@ -324,7 +333,7 @@ struct CopyLayers {
 // before it touches anything that kernel (or an earlier one) produces.
 struct PdlLaunch {
     cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     PdlLaunch(dim3 grid, dim3 block, size_t smem, cudaStream_t s, bool pdl = true) {
         cfg.gridDim = grid;
         cfg.blockDim = block;
@@ -334,6 +343,12 @@ struct PdlLaunch {
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = pdl ? 1 : 0;
+    }
+    void set_cluster(int ctas) {
+        cudaLaunchAttribute &a = attr[cfg.numAttrs++];
+        a.id = cudaLaunchAttributeClusterDimension;
+        a.val.clusterDim.x = ctas;
+        a.val.clusterDim.y = a.val.clusterDim.z = 1;
     }
     PdlLaunch(const PdlLaunch &) = delete;
     PdlLaunch &operator=(const PdlLaunch &) = delete;
@@ -390,9 +405,8 @@ int launch_plan_window(const PlanParams &p, cudaStream_t s);
 int launch_short(const ShortParams &p, const CUtensorMap &tk, const CUtensorMap &tv,
                  int head_dim, bool fp8, bool windowed, int grid, cudaStream_t s);
 int short_max_ctas_per_sm(int head_dim, bool fp8, bool windowed);
-int window_rows_workers_per_sm(int head_dim);
-int launch_window_rows(const ShortParams &p, const CUtensorMap &tk, const CUtensorMap &tv,
-                       int head_dim, int grid, cudaStream_t s);
+int launch_window_direct(const ShortParams &p, const CUtensorMap &tk, const CUtensorMap &tv,
+                        const DirectParams &dp, int head_dim, bool fp8, cudaStream_t s);
 int launch_long(const LongParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
                 const CUtensorMap &tv, int head_dim, int grid, cudaStream_t s);
 int launch_long_window(const LongParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
@@ -564,6 +578,33 @@ __device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity) {
     while (!mbar_try_wait(bar, parity)) {
         if (global_timer_ns() - t0 > 100000000ull) break;
     }
+}
+
+// Clusters ---------------------------------------------------------------------
+// Barrier over the cluster's threads; what they wrote before it is seen after it.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Loads from the shared memory of CTA `rank` of the cluster, at the place that
+// `local` has in this CTA's.
+__device__ __forceinline__ uint32_t cluster_addr(const void *local, int rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float2 ld_cluster_f2(const void *local, int rank) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                 : "=f"(v.x), "=f"(v.y) : "r"(cluster_addr(local, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(const void *local, int rank) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_addr(local, rank)) : "memory");
+    return v;
 }
 
 // TMA --------------------------------------------------------------------------

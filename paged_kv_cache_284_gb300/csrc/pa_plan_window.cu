@@ -23,8 +23,6 @@ namespace {
 constexpr int kT = 512;
 constexpr int kWarps = kT / 32;
 constexpr int kTableInSmem = 768;
-constexpr int kCuts = 8;          // cuts of the longest job that are compared
-constexpr float kCutCost = 2.f;   // stages that an item costs its worker besides its own
 
 struct Sums {
     int a, b, c;
@@ -133,8 +131,6 @@ __global__ void __launch_bounds__(kT) plan_window_kernel(const PlanParams p) {
     __shared__ int bins[kT], tile_bins[kT];
     __shared__ int s_max_stages, s_max_tiles;
     __shared__ float s_stages;
-    __shared__ int s_cut_items[kCuts], s_cut_rows[kCuts];
-    __shared__ float s_cut_time[kCuts];
     __shared__ long long s_blocks[kWarps];
     __shared__ WindowPiece s_table[kTableInSmem];
     const int tid = threadIdx.x;
@@ -239,7 +235,7 @@ __global__ void __launch_bounds__(kT) plan_window_kernel(const PlanParams p) {
     __syncthreads();  // the tables too
     max_stages = s_max_stages;
     const int P = base.a, n_long = base.c, n_tiles = base.b;
-    const int J = overflow ? 0 : P * hkv;  // jobs
+    const int J = overflow ? 0 : P * hkv;  // jobs (at most num_counters, see below)
     const int C = max(1, p.num_ctas);
 
     // 2. splits per piece: one, or with at most as many jobs as CTAs
@@ -273,50 +269,13 @@ __global__ void __launch_bounds__(kT) plan_window_kernel(const PlanParams p) {
             sp = tries == 0 && J < C ? max(sp, size(C - J)) : min(max_stages, 2 * sp);
         }
     }
-    if (p.worker_warps && J > C && J < kCuts * C && max_stages > kMinSplitStages) {
-        // Cut k: jobs in pieces of at most ceil(longest / (k + 1)) stages, looked
-        // at by warp k.  Equal items take ceil(items / C) rounds (in a grid that
-        // has the GPU to itself); one long job counts by itself.
-        auto cut = [&](int k) { return max(kMinSplitStages, (max_stages + k) / (k + 1)); };
-        if (tid < 32 * kCuts) {
-            const int k = tid >> 5;
-            const unsigned len = k == 0 ? max_stages : cut(k);
-            unsigned n = 0, r = 0;
-            for (int i = tid & 31; i < P; i += 32) {
-                const unsigned ns = (table[i].stages + len - 1) / len;
-                n += ns;
-                if (ns > 1) r += ns * table[i].q_count;
-            }
-            n = __reduce_add_sync(0xffffffffu, n) * hkv;
-            r = __reduce_add_sync(0xffffffffu, r) * hkv * p.group;
-            if ((tid & 31) == 0) {
-                float rounds = static_cast<float>(n) / static_cast<float>(C);
-                if (p.worker_warps == 1) rounds = ceilf(rounds);
-                const float avg = s_stages * static_cast<float>(hkv) / static_cast<float>(n);
-                const bool room = n <= static_cast<unsigned>(p.max_short) &&
-                                  r <= static_cast<unsigned>(p.cap_rows);
-                s_cut_time[k] = k > 0 && !room
-                                    ? INFINITY
-                                    : fmaxf(rounds * (avg + kCutCost),
-                                            static_cast<float>(len) + kCutCost);
-                s_cut_items[k] = n;
-                s_cut_rows[k] = r;
-            }
-        }
-        __syncthreads();
-        int best = 0;
-        for (int k = 1; k < kCuts; ++k)
-            if (s_cut_time[k] < s_cut_time[best]) best = k;
-        sp = best == 0 ? max_stages : cut(best);
-        items = s_cut_items[best];
-        rows = s_cut_rows[best];
-    }
     const bool split = sp < max_stages;
     if (!split) {
         items = J;
         rows = 0;
     }
-    const bool fits = !overflow && items <= p.max_short && (!split || J <= p.num_counters);
+    const bool fits = !overflow && static_cast<long long>(P) * hkv <= p.num_counters &&
+                      items <= p.max_short;
 
     // 3. split-KV records, longest first (counting sort on the stages).  A
     // piece cuts its stages into splits that differ by at most one stage; its

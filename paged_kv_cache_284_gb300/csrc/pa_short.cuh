@@ -1,6 +1,6 @@
 // pa_short.cuh -- the arithmetic of the memory-bound attention kernels on one
 // 16-key chunk of K and V in shared memory, shared by the split-KV kernel
-// (pa_short.cu) and the windowed decode kernel (pa_window.cu).
+// (pa_short.cu) and the one-kernel windowed step (pa_window.cu).
 #pragma once
 
 #include "pa_internal.cuh"

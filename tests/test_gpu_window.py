@@ -293,8 +293,8 @@ def test_bad_block_and_bad_metadata_are_flagged():
     assert np.abs(t["out"][3].double().cpu().numpy() - ref[3]).max() < 0.05
 
 
-# bf16 batches of at most 16 rows a request on average and two or more (request,
-# kv head) pairs per SM of a 152-SM GPU take the windowed decode kernel.
+# Batches of at most 16 rows a request on average run as one kernel: clusters of
+# CTAs for each (piece of 16 rows, kv head), in several rounds when there are many.
 def many(n, spread, rng, new=(1, 2)):
     return [(int(c), int(m)) for c, m in zip(rng.integers(0, spread, n), rng.integers(*new, n))]
 
@@ -311,7 +311,7 @@ def test_large_batches(kv, d, window, sinks):
 @pytest.mark.parametrize("group,bs,new", [(1, 64, 17), (5, 16, 5), (8, 48, 3), (16, 32, 3),
                                           (17, 16, 2)])
 def test_large_batches_of_other_groups(kv, group, bs, new):
-    """Pieces of 16 / group tokens; a group of 17 stays with the other kernel."""
+    """Pieces of 16 / group tokens; a group of 17 stays with the planned kernels."""
     rng = np.random.default_rng(group)
     reqs = many(80, 400, rng, (1, new)) + [(0, 0)] * 60
     assert group == 17 or sum(n for _, n in reqs) * group <= 16 * len(reqs)
@@ -319,8 +319,8 @@ def test_large_batches_of_other_groups(kv, group, bs, new):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
-def test_large_batches_of_more_jobs_than_warps(kv):
-    """Over 2000 jobs: whole ones, several to a warp, a few of them long."""
+def test_large_batches_of_many_jobs(kv):
+    """Over 2000 jobs, a few of them long."""
     rng = np.random.default_rng(8)
     Step(many(260, 120, rng) + [(3000, 1), (2500, 2)], 16, 8, 128, 16, 2000, 20, kv=kv,
          seed=8).run_and_check()
@@ -377,3 +377,104 @@ def test_a_large_batch_times_out_when_chunks_never_come():
     torch.cuda.synchronize()
     st.check(t)
     assert_status_clean()
+
+
+# The same for steps whose pieces, kv heads and windows bound little work, whatever
+# their requests are.
+@pytest.mark.parametrize("kv,d", [("bf16", 128), ("bf16", 64), ("e4m3", 128)])
+@pytest.mark.parametrize("requests,window,sinks", [
+    ([(0, 1)], 1, 0), ([(700, 1)], 128, 4), ([(5000, 1)], 4000, 9), ([(300, 3)], 40, 0),
+    ([(31, 5), (0, 0), (64, 1), (15, 9)], 33, 17), ([(9, 40)], 7, 100),
+    ([(100 * i, 1 + i % 3) for i in range(30)], 90, 3),
+    ([(3 * i, i % 2) for i in range(128)], 20, 2)])
+def test_small_steps(kv, d, requests, window, sinks):
+    Step(requests, 8, 2, d, 16, window, sinks, kv=kv, seed=len(requests), pad=2).run_and_check()
+
+
+@pytest.mark.parametrize("hq,hkv,bs", [(1, 1, 32), (16, 1, 64), (15, 3, 256), (17, 1, 16)])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_small_steps_of_other_groups(hq, hkv, bs, kv):
+    Step([(250, 1), (90, 4), (130, 18), (0, 2)], hq, hkv, 128, bs, 150, 20, kv=kv,
+         seed=hq).run_and_check()
+
+
+def test_small_step_in_a_graph_beside_another_on_its_own_stream():
+    a = Step([(500, 1), (60, 2)], 8, 2, 128, 16, 300, 4, seed=1)
+    b = Step([(80, 1)], 4, 4, 64, 16, 50, 0, seed=2)
+    ta, tb = a.to_dev(), b.to_dev()
+    wa, wb = a.call(ta), b.call(tb)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(3):
+            a.call(ta, workspace=wa)
+    s = torch.cuda.Stream()
+    for _ in range(5):
+        g.replay()
+        b.call(tb, workspace=wb, stream=s)
+    torch.cuda.synchronize()
+    a.check(ta)
+    b.check(tb)
+    assert_status_clean()
+
+
+def test_small_step_flags_bad_blocks_bad_metadata_and_a_wait_that_runs_out():
+    st = Step([(40, 1), (50, 2), (900, 1)], 4, 2, 64, 16, 600, 2)
+    t = st.to_dev()
+    t["table"][0, 2] = st.num_blocks
+    t["seq"][1] += 1
+    st.call(t)
+    torch.cuda.synchronize()
+    assert pk.read_device_status(clear=True) == pk.PA_DEV_BAD_BLOCK | pk.PA_DEV_BAD_METADATA
+    assert torch.all(t["out"][1:3] == 7.0)
+    # overlapping requests want more pieces than the step's tokens allow
+    over = Step([(5, 9), (5, 9), (5, 9)], 4, 1, 64, 16, 600, 0)
+    t = over.to_dev()
+    t["qsl"] = torch.tensor([0, 27, 0, 27], dtype=torch.int32, device=DEV)
+    t["ctx"][0] = t["ctx"][2] = 0
+    t["seq"][0] = t["seq"][2] = 27
+    t["table"].clamp_(min=0)
+    t["table"] = t["table"].repeat(1, 4).contiguous()
+    over.call(t)
+    torch.cuda.synchronize()
+    status = pk.read_device_status(clear=True)
+    assert status & pk.PA_DEV_PLAN_OVERFLOW and torch.all(t["out"] == 7.0)
+    # request 0's first worker has two chunks, asks for one
+    late = Step([(1000, 1)], 32, 8, 128, 16, 900, 0)
+    t = late.to_dev()
+    pk.set_test_stall(pk.PA_TEST_STALL_SPLIT_KV)
+    try:
+        late.call(t)
+        torch.cuda.synchronize()
+    finally:
+        pk.set_test_stall(pk.PA_TEST_STALL_NONE)
+    assert pk.read_device_status(clear=True) & pk.PA_DEV_WAIT_TIMEOUT
+    late.run_and_check()
+
+
+# The planned kernels: steps with more work and more rows a request, in which they
+# run one after the other (under 512 tokens) or side by side.
+@pytest.mark.parametrize("window,sinks", WINDOWS)
+@pytest.mark.parametrize("kv,d,staged", [("bf16", 128, 0), ("bf16", 64, 0), ("e4m3", 128, 0),
+                                         ("e4m3", 128, 1), ("e4m3", 128, 12),
+                                         ("e4m3", 128, None)])
+def test_planned_steps(kv, d, staged, window, sinks):
+    kw = {} if staged is None else {"staging_blocks": staged}
+    Step(MIXED, 64, 8, d, 16, window, sinks, kv=kv, seed=window).run_and_check(**kw)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_planned_steps_split_over_the_window(kv):
+    Step([(9000 - 500 * i, 10) for i in range(8)], 8, 1, 128, 16, 3000, 37, kv=kv,
+         seed=3).run_and_check()
+
+
+def test_planned_step_at_far_positions():
+    Step(MIXED + [((1 << 20) + 5, 70)], 64, 8, 64, 256, 300, 4, seed=4).run_and_check()
+
+
+@pytest.mark.parametrize("window,sinks", WINDOWS)
+@pytest.mark.parametrize("kv,d", [("bf16", 128), ("bf16", 64), ("e4m3", 128)])
+def test_large_planned_steps(kv, d, window, sinks):
+    Step(MIXED * 2 + CHUNKS + VERIFY * 4 + DECODE * 4, 16, 4, d, 16, window, sinks, kv=kv,
+         seed=window).run_and_check()
