@@ -161,6 +161,25 @@ def lib():
     return _lib
 
 
+_direct = None
+
+
+def _load_direct():
+    """The binding of the small calls (csrc/pa_torch.cpp), bound to libpa.so."""
+    global _direct
+    try:
+        from . import _pa_torch
+    except ImportError as e:
+        raise ImportError("_pa_torch.so not built: run "
+                          "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+    L = lib()
+    _pa_torch.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                     for f in (L.pa_window_attention, L.pa_rope_write_kv,
+                               L.pa_copy_blocks)))
+    _direct = _pa_torch
+    return _direct
+
+
 def _check(rc: int, what: str):
     if rc != PA_OK:
         raise PaError(rc, what, lib().pa_last_error_message().decode())
@@ -383,6 +402,13 @@ def pa_window_attention(q, k_cache, v_cache, block_tables, query_start_loc, cont
     e4m3 pools as in pa_attention; blocks of which no row of their request
     sees a key may have any table entry (staging_blocks counts the visible
     blocks of the long requests).  Returns the workspace tensor used."""
+    # a plain call with a kept workspace goes straight to the library; what is
+    # wrong with any other (or needs a workspace) comes out below
+    if workspace is not None and staging_blocks == 0 and \
+            (_direct or _load_direct()).window_attention(
+                q, k_cache, v_cache, block_tables, query_start_loc, context_lens, seq_lens, scale,
+                window, num_sinks, out, lse, workspace, stream, k_scale, v_scale) == PA_OK:
+        return workspace
     dev = q.get_device()
     if (_off(q, _BF16, dev) or _off(out, _BF16, dev) or _off(block_tables, _I32, dev) or
             _off(query_start_loc, _I32, dev) or _off(context_lens, _I32, dev) or
@@ -448,6 +474,10 @@ def pa_rope_write_kv(q, k, v, positions, inv_freq, axis, slot_mapping, k_cache, 
     one axis); inv_freq float64 [rot_dim / 2]; axis int32 [rot_dim / 2], the
     axis of each frequency, or None for axis 0; q_out bf16 [T, Hq, d] (may be
     a contiguous q).  q and q_out may both be None."""
+    if (_direct or _load_direct()).rope_write_kv(
+            q, k, v, positions, inv_freq, axis, slot_mapping, k_cache, v_cache, q_out, adjacent,
+            attn_factor, stream, k_scale, v_scale) == PA_OK:
+        return
     dev = k.get_device()
     ks, rows = _token_rows(k, "k", dev)
     vs, v_rows = _token_rows(v, "v", dev)
@@ -495,6 +525,7 @@ class KVLayers:
 
     def __init__(self, descs, tensors):
         self.descs = descs
+        self.address = ctypes.addressof(descs)
         self.tensors = tensors  # keeps the pools alive
         self.device = tensors[0].get_device() if tensors else -1
 
@@ -530,6 +561,9 @@ def pa_copy_blocks(layers: KVLayers, pairs, stream=None):
     """Copy physical blocks in every layer: pairs int32 [n, 2] of (src, dst) on
     the device (BlockManager.schedule's copies, BlockManager.compact's moves).
     A dst appears once and is no other pair's src; negative ids are padding."""
+    if (_direct or _load_direct()).copy_blocks(layers.address, len(layers.descs), layers.device,
+                                               pairs, stream) == PA_OK:
+        return
     if pairs.dtype is not _I32:
         raise TypeError(f"pairs must be {_I32}, got {pairs.dtype}")
     shape = pairs.shape

@@ -115,3 +115,25 @@ def test_offsets_past_32_bits():
     for b in (0, 1, 2, 3, 4, nb - 3, nb - 2, nb - 1):
         assert torch.all(k[b] == want.get(b, 0.0)) and torch.all(v[b] == -want.get(b, 0.0))
     assert_status_clean()
+
+
+def test_binding_takes_plain_calls_and_leaves_the_others():
+    dev = torch.device("cuda:0")
+    k, v = (torch.randn(6, 2, 16, 64, device=dev).to(torch.bfloat16) for _ in "kv")
+    layers = pk.kv_layers([k], [v])
+    pairs = torch.tensor([[0, 3], [1, 4], [-1, -1]], dtype=torch.int32, device=dev)
+    call = pk._load_direct().copy_blocks
+    good = [layers.address, 1, layers.device, pairs, None]
+    assert call(*good) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(k[3], k[0]) and torch.equal(v[4], v[1])
+    before = pk.lib().pa_kernel_launches()
+    wrong = {0: [None, 1.5], 1: [0, None], 2: [-1, 99], 4: [3],
+             3: [pairs.long(), pairs.cpu(), pairs[0], pairs.t(), pairs[:, :1], None]}
+    for i, values in wrong.items():
+        for x in values:
+            assert call(*good[:i], x, *good[i + 1:]) == -1, (i, x)
+    assert call() == -1
+    assert pk.lib().pa_kernel_launches() == before
+    pk.pa_copy_blocks(layers, pairs[:0])  # nothing to copy
+    torch.cuda.synchronize()

@@ -222,3 +222,36 @@ def test_graph_and_stream():
         t[name].copy_(o[name])
     g.replay()
     check(other, t, q_out)
+
+
+def test_binding_takes_plain_calls_and_leaves_the_others():
+    """The direct binding launches a documented call and hands every other back
+    (-1) without a launch."""
+    dev, T, d = torch.device("cuda:0"), 5, 64
+    q = torch.randn(T, 4, d, device=dev).to(torch.bfloat16)
+    k, v = (torch.randn(T, 2, d, device=dev).to(torch.bfloat16) for _ in "kv")
+    kc, vc = (torch.zeros(3, 2, 16, d, device=dev, dtype=torch.bfloat16) for _ in "kv")
+    pos = torch.arange(T, device=dev, dtype=torch.int32)
+    freq = torch.ones(d // 2, device=dev, dtype=torch.float64)
+    axis = torch.zeros(d // 2, device=dev, dtype=torch.int32)
+    slots = torch.arange(T, device=dev, dtype=torch.int64)
+    out = torch.empty_like(q)
+    call = pk._load_direct().rope_write_kv
+    good = [q, k, v, pos, freq, axis, slots, kc, vc, out, False, 1.0, None, None, None]
+    assert call(*good) == 0
+    assert call(None, *good[1:9], None, *good[10:]) == 0
+    assert call(*good[:5], None, *good[6:]) == 0
+    torch.cuda.synchronize()
+    before = pk.lib().pa_kernel_launches()
+    wrong = {0: [q.float(), q[:3], None, q[..., ::2]], 1: [k.cpu(), k[:, :1], k[0]],
+             2: [v[1:], v.half()], 3: [pos.long(), pos[1:], pos.view(1, 1, T)],
+             4: [freq.float(), freq[1:]], 5: [axis[1:], axis.long()], 6: [slots.int(), slots[1:]],
+             7: [kc[0], kc.float(), vc.view(torch.uint8)], 8: [vc[1:]], 9: [None, out[1:]],
+             10: [0, None], 11: ["1", None], 12: [5], 13: [freq]}
+    for i, values in wrong.items():
+        for x in values:
+            assert call(*good[:i], x, *good[i + 1:]) == -1, (i, x)
+    assert call() == -1
+    assert pk.lib().pa_kernel_launches() == before
+    with pytest.raises((TypeError, ValueError)):
+        pk.pa_rope_write_kv(*good[:3], pos.long(), *good[4:10])

@@ -478,3 +478,34 @@ def test_planned_step_at_far_positions():
 def test_large_planned_steps(kv, d, window, sinks):
     Step(MIXED * 2 + CHUNKS + VERIFY * 4 + DECODE * 4, 16, 4, d, 16, window, sinks, kv=kv,
          seed=window).run_and_check()
+
+
+def test_binding_takes_plain_calls_and_leaves_the_others():
+    """The direct binding launches a documented call and hands every other back
+    (-1) without a launch."""
+    st = Step([(40, 1), (50, 2)], 4, 2, 64, 16, 20, 2)
+    t = st.to_dev()
+    ws = st.call(t)
+    torch.cuda.synchronize()
+    call = pk._load_direct().window_attention
+    good = [t["q"], t["k"], t["v"], t["table"], t["qsl"], t["ctx"], t["seq"], st.scale, 20, 2,
+            t["out"], t["lse"], ws, None, None, None]
+    t["out"].fill_(7.0)
+    assert call(*good) == 0 and call(*good[:13], torch.cuda.Stream(), None, None) == 0
+    torch.cuda.synchronize()
+    st.check(t)
+    before = pk.lib().pa_kernel_launches()
+    wrong = {0: [t["q"].float(), t["q"].cpu(), t["q"].transpose(0, 1), None, 3],
+             1: [t["k"].view(torch.uint8), t["k"][0], t["k"][:, :, ::2]],
+             2: [t["v"][1:]], 3: [t["table"].long(), t["table"][0], t["table"].t()],
+             4: [t["qsl"][1:]], 5: [t["ctx"].cpu()], 6: [t["seq"].float()],
+             7: ["1", t["ctx"]], 8: [20.5, 1 << 40, None], 9: ["2"],
+             10: [t["out"][:, :1], t["out"].half()], 11: [t["lse"][1:], t["lse"].double()],
+             12: [None, ws.cpu(), 5], 13: [7, "stream"], 14: [t["lse"]]}
+    for i, values in wrong.items():
+        for v in values:
+            assert call(*good[:i], v, *good[i + 1:]) == -1, (i, v)
+    assert call(*good[:15]) == -1 and call() == -1
+    assert call(*good[:12], ws[:256], *good[13:]) == pk.PA_ERR_WORKSPACE
+    assert call(*good[:8], 0, *good[9:]) == pk.PA_ERR_INVALID_ARG
+    assert pk.lib().pa_kernel_launches() == before
