@@ -295,6 +295,10 @@ int pa_attention_ex(const void *q, const pa_kv_desc *kv, const int32_t *block_ta
  * leaves -1), and keys that no row of the request sees may hold anything,
  * even NaN.  Keys that one row sees and another does not must be finite.
  * pa_fp8_staging_bytes counts a long request's visible blocks only.
+ *
+ * A step of little work, or of few rows a request, runs as one kernel (counted
+ * and timed as PA_KERNEL_SPLIT_KV); the workspace is asked for all the same,
+ * as the choice depends on sizes that need not stay the same between steps.
  */
 int pa_window_attention(const void *q, const pa_kv_desc *kv, const int32_t *block_tables,
                         int32_t max_blocks_per_seq, const int32_t *query_start_loc,
@@ -455,7 +459,9 @@ int pa_set_profile_events(int32_t which, void *start_event, void *end_event);
  *                             launch), CTA 0's producer stops after its
  *                             first stage: CTA 0's consumers wait for a
  *                             stage that never comes, time out and return.
- *                             The step's result is then incomplete.
+ *                             The step's result is then incomplete.  (A
+ *                             windowed step of one kernel: CTA 0's first warp
+ *                             waits for its second chunk.)
  *   PA_TEST_STALL_LAST_GRID   in every later side-by-side step (split-KV
  *                             and tensor-core kernels together), the last
  *                             tensor-core grid waits for one CTA more than

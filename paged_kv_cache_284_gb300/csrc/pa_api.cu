@@ -144,8 +144,6 @@ struct ProfScope {
     }
 };
 
-// True while per-kernel profiling events are set: the step then launches its
-// kernels one after the other so that each event pair times one kernel.
 // Fewest query tokens for which a step runs its split-KV and tensor-core
 // kernels side by side (below it they run one after the other).
 constexpr int kSideBySideMinTokens = 512;
@@ -170,6 +168,8 @@ constexpr int64_t kDirectJobsPerSm = 7;
 constexpr int64_t kDirectAnyRows = 256;
 constexpr int64_t kDirectE4m3Chunks = 65536;
 
+// True while per-kernel profiling events are set: the step then launches its
+// kernels one after the other so that each event pair times one kernel.
 bool profiling_active() {
     std::lock_guard<std::mutex> lock(g_prof_mu);
     return g_prof[PA_KERNEL_SPLIT_KV][0] || g_prof[PA_KERNEL_TENSOR_CORE][0];

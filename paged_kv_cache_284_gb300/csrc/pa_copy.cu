@@ -4,7 +4,11 @@
 //
 // A block is one contiguous run of num_kv_heads * block_size * head_dim
 // elements in each of a layer's two arrays, so a pair is two plain copies per
-// layer: nothing but HBM traffic, each byte read once and written once.
+// layer: nothing but HBM traffic, each byte read once and written once.  One
+// 16-byte piece per thread and step keeps enough loads in flight: 58 blocks in each
+// of 32 layers (243 MB read and written) take 37.5 us, 6.5 TB/s, 0.97 of the measured
+// copy bandwidth; 2048 blocks in 8 layers (2.1 GB) 328 us, 0.98; 4 blocks in one layer
+// 1.8 us, which is the launch.
 #include <algorithm>
 
 #include "pa_internal.cuh"

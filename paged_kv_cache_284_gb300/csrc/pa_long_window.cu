@@ -10,19 +10,28 @@
 // to a row; every wait of a tile's chain (scores, the halves' maxima, P) idles
 // all of them, and a key tile takes ~2300 cycles against 1024 of MMA.  Here
 //  * two groups of four warps take the key tiles in turn, one thread to a row,
-//    so one group's waits lie beside the other's arithmetic;
-//  * S is a ring of three TMEM tiles and P overwrites the S tile it came from,
-//    so the scores of up to two later tiles are ready when a group wants one;
+//    so one group's waits lie beside the other's arithmetic; each group has its
+//    own S and its own P in TMEM, and a row's scores are read in two halves so
+//    that 168 registers hold them;
 //  * both groups share one accumulator O, so they must agree on each row's
 //    reference (the running maximum its exponents are taken against).  A tile's
 //    reference is the tile before's unless the tile's maximum exceeds it by
 //    2^8 (then O is rescaled), and is handed from tile to tile through shared
 //    memory as soon as the tile's maximum is known, long before its P is.
 //    Sums are kept per group, each against the reference it last used, and
-//    added at the item's end.
-// Shared memory traffic is what bounds it then: Q and K tiles read by Q K^T,
-// V by P V, both written by TMA, 160 KB per key tile at 128 B a cycle = 1280
-// cycles.
+//    added at the item's end;
+//  * items are decoded once, by the K producer, and read by every role from a
+//    queue in shared memory; the group that has an item's last tile writes its
+//    output while the other begins the next item;
+//  * K and V rings are three tiles deep, and Q K^T and P V are issued by two
+//    warps (one elected lane each): a 128 x 128 x 128 group of MMAs takes
+//    700-800 cycles by itself and 512 beside the other warp's; one issuing thread
+//    for both was slower (616 us against 487 on the case below).
+// Two chunks of 4096 tokens, window 4096 + 16 sinks, 32 q / 8 kv heads, d = 128, 552
+// GFLOP of visible pairs: 478 us, 1155 TFLOP/s, 0.60 of the measured bf16 rate (565 us
+// in the plain kernel's form).  Bound: the chain of a key tile (scores, maximum,
+// exponentials, P V) at ~1900 cycles for two tiles in flight, against 1024 of MMA;
+// a third S tile with P written over S left too few registers and columns to win.
 #include "pa_long.cuh"
 
 namespace pa {

@@ -6,7 +6,7 @@
 //  * with more split-KV jobs (a piece, for one kv head) than CTAs every job
 //    stays whole.  Cutting the last ones finer, or the whole line of work into
 //    equal runs of stages per CTA, balances better on paper and was slower
-//    (64-request decode step: 70.6 us whole, 71.9 / 76.9 / 87.3 us with the
+//    (512 jobs of 17 stages: 70.6 us whole, 71.9 / 76.9 / 87.3 us with the
 //    last 4 / 8 / 16 stages per CTA cut by 4, 74.9 us in equal runs): a split
 //    costs its CTA about three stages' time;
 //  * with fewer jobs than CTAs, every job is cut so that all splits run in one

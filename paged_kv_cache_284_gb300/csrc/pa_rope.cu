@@ -20,6 +20,10 @@
 // turn each frequency once per item, two per lane, and share cos and sin
 // through shared memory; then each lane keeps the frequencies of its 16
 // elements of a head in registers while it walks over the heads.
+// 4096 tokens of 32 + 8 + 8 heads, three axes, bf16 (101 MB): 18.1 us, 5.6 TB/s,
+// 0.83 of the measured copy bandwidth; 16384 tokens into an e4m3 pool (369 MB)
+// 64.6 us, 0.85; 8 tokens 3.5 us, most of it the launch.  A block per token with
+// plain loads took 21-26 and 79-106 us.
 #include <algorithm>
 
 #include <cuda_fp8.h>

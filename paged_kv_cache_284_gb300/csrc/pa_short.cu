@@ -41,6 +41,10 @@
 //    the second MMA's B operand through movmatrix (8x8 transposes).  The
 //    row maximum is reduced across lanes only when some score exceeds the
 //    running maximum by more than 2^8 (the lazy rescale threshold).
+//  * windowed steps (WIN): items count packed visible chunks, so that the ring
+//    skips what no row sees, and each row has a lower limit besides its causal
+//    one.  Their records are per kv head.  256 e4m3 decode rows, window 4096 + 64
+//    sinks: 297 us for 1.7 GB, 0.86 of the measured copy bandwidth.
 #include "pa_short.cuh"
 
 namespace pa {
