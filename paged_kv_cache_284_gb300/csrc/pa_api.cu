@@ -147,6 +147,14 @@ struct ProfScope {
 // Fewest query tokens for which a step runs its split-KV and tensor-core
 // kernels side by side (below it they run one after the other).
 constexpr int kSideBySideMinTokens = 512;
+// In a windowed step the short rows' work is bounded too: with fewer chunks than
+// this, if every request were a decode row, there is nothing for the extra grids
+// to overlap.  32 q / 8 kv heads, side by side / one after the other: a chunk of
+// 1024 tokens at window 128 29 / 21 us, at window 4096 76 / 72; 4 chunks of 512 and
+// 72 decode and verify rows 50 / 46 us at window 16 (2.4 k chunks), 60 / 65 at 128
+// (6.7 k), 227 / 291 at 4096.  8 / 2 heads, the same rows: 43 / 38 us at window 512
+// (5.3 k), 94 / 99 at 4096 (39 k).
+constexpr int64_t kSideBySideMinChunks = 6144;
 
 // A windowed step of groups of at most 16 runs as one kernel (window_direct_kernel)
 // in place of the plan and the planned kernels
@@ -477,6 +485,15 @@ int check_window(int32_t window, int32_t num_sinks, float scale) {
     return PA_OK;
 }
 
+// Most chunks that `tokens` consecutive rows see: their sinks' and their windows' (cut
+// anywhere), at most a whole table's.
+int64_t seen_chunks(const WindowArgs &win, int tokens, int max_blocks, int block_size) {
+    const int64_t table = static_cast<int64_t>(max_blocks) * block_size / kChunkKeys;
+    const int64_t seen = (static_cast<int64_t>(win.sinks) + kChunkKeys - 1) / kChunkKeys +
+                         (static_cast<int64_t>(win.window) + tokens) / kChunkKeys + 2;
+    return std::min(table, seen);
+}
+
 // Whether a windowed step is one for the one-kernel form, and its launch.
 bool direct_step(const WindowArgs &win, int num_seqs, int T, const pa_kv_desc *kv, int group,
                  int max_blocks, int sms, DirectParams *dp) {
@@ -484,12 +501,7 @@ bool direct_step(const WindowArgs &win, int num_seqs, int T, const pa_kv_desc *k
     dp->piece_tokens = piece_tokens_for(group, kDirectRows);
     dp->max_pieces = std::min(T, pieces_bound(num_seqs, T, group, kDirectRows));
     dp->max_keys = max_blocks * kv->block_size;
-    // chunks of a piece: its sinks', its rows' windows' (cut anywhere), at most
-    // its whole table's
-    const int64_t table = static_cast<int64_t>(max_blocks) * kv->block_size / kChunkKeys;
-    const int64_t seen = (static_cast<int64_t>(win.sinks) + kChunkKeys - 1) / kChunkKeys +
-                         (static_cast<int64_t>(win.window) + dp->piece_tokens) / kChunkKeys + 2;
-    const int64_t chunks = std::min(table, seen);
+    const int64_t chunks = seen_chunks(win, dp->piece_tokens, max_blocks, kv->block_size);
     const int64_t jobs = static_cast<int64_t>(dp->max_pieces) * kv->num_kv_heads;
     const int64_t rows = static_cast<int64_t>(T) * group;
     if (jobs * chunks > kDirectAnyChunks || jobs > kDirectJobsPerSm * sms) {
@@ -497,16 +509,19 @@ bool direct_step(const WindowArgs &win, int num_seqs, int T, const pa_kv_desc *k
             return false;
         if (kv->kv_dtype == PA_KV_FP8_E4M3 && jobs * chunks > kDirectE4m3Chunks) return false;
     }
-    // CTAs per job and per SM: the fewest rounds times a CTA's time, in chunks of
-    // one warp at one CTA per SM (and what it costs besides, as much as twelve).
-    // Three CTAs per SM have shorter rings: 48 decode requests, 8 kv heads, window
-    // 1024: 36 us with three (one round), 47 with two; 64 requests 56 / 50.
+    // Warps per job (one, or all of 1, 2, 4 or 8 CTAs) and CTAs per SM: the fewest
+    // rounds times a CTA's time, in chunks of one warp at one CTA per SM (and what
+    // it costs besides, as much as twelve).  Three CTAs per SM have shorter rings: 48
+    // decode requests, 8 kv heads, window 1024: 36 us with three (one round), 47 with
+    // two; 64 requests 56 / 50.
     int64_t best = -1;
     for (int per = 2; per <= 3; ++per)
-        for (int c = 1; c <= kDirectMaxCluster; c *= 2) {
-            const int64_t per_warp = (chunks + kDirectWarps * c - 1) / (kDirectWarps * c);
+        for (int c = 0; c <= kDirectMaxCluster; c = c == 0 ? 1 : 2 * c) {
+            const int64_t warps = c == 0 ? 1 : kDirectWarps * c;
+            const int64_t per_warp = (chunks + warps - 1) / warps;
+            const int64_t ctas = (jobs * warps + kDirectWarps - 1) / kDirectWarps;
             const int64_t slots = static_cast<int64_t>(per) * sms;
-            const int64_t time = (jobs * c + slots - 1) / slots * (per_warp * per + 12);
+            const int64_t time = (ctas + slots - 1) / slots * (per_warp * per + 12);
             if (best < 0 || time < best) {
                 best = time;
                 dp->cluster = c;
@@ -575,8 +590,11 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
     const int min_long_tokens = short_max_rows / group + 1;
     const int max_long_reqs =
         forbid_long ? 0 : std::min(num_seqs, T / std::max(1, min_long_tokens));
-    const bool side_by_side =
-        max_long_reqs > 0 && T >= kSideBySideMinTokens && !profiling_active();
+    bool side_by_side = max_long_reqs > 0 && T >= kSideBySideMinTokens && !profiling_active();
+    if (win && static_cast<int64_t>(num_seqs) * kv->num_kv_heads *
+                       seen_chunks(*win, 1, max_blocks, kv->block_size) <
+                   kSideBySideMinChunks)
+        side_by_side = false;
     if (win) {
         // the windowed planner keeps its table at the end of the partial states
         pp.win = *win;
@@ -820,6 +838,8 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         // the split-KV kernel was launched just before: the tensor-core grid
         // may take over SMs as split-KV CTAs finish (its rows are disjoint)
         lp.overlap_prev = short_grid > 0 ? 1 : 0;
+        // (many windowed items: from the step's counter, see pa_long_window.cu)
+        lp.dynamic = win && long_grid > 2 * dev->sms ? 1 : 0;
         {
             ProfScope prof(PA_KERNEL_TENSOR_CORE, s);
             rc = tensor_core(lp, long_grid);

@@ -209,8 +209,8 @@ struct ShortParams {
     int test_stall;   // test hook: CTA 0's producer stops after its first stage
 };
 
-// A windowed step in one kernel: clusters of `cluster` CTAs for each of
-// max_pieces pieces x kv heads.
+// A windowed step in one kernel: a cluster of `cluster` CTAs, or (0) a warp, for each
+// of max_pieces pieces x kv heads.
 struct DirectParams {
     int per_sm;  // CTAs per SM: 2 or 3
     int cluster, max_pieces, piece_tokens;

@@ -2,8 +2,8 @@
 // grid.
 //
 // The host bounds the step's pieces (of at most 16 rows of a request) and launches a
-// cluster of 1 to 8 CTAs for each (piece, kv head).  Each CTA finds its piece by a
-// scan over the requests; the cluster's warps take the piece's visible 16-key chunks
+// cluster of 1 to 8 CTAs for each (piece, kv head), or, where there are many and they
+// are short, a warp.  Each CTA finds its piece by a scan over the requests; the cluster's warps take the piece's visible 16-key chunks
 // in turn, each through a TMA ring of its own that it refills the moment it has
 // consumed a slot (no producer, no block barrier in the loop); at the end every
 // warp leaves its rows' maximum, sum and unnormalised output in shared memory,
@@ -44,11 +44,11 @@ struct DirectGeom {
     static constexpr int kRingBytes = kSlots * kSlotBytes;
     static constexpr int kThreads = 32 * kDirectWarps;
     // after the rings: the barriers, maximum and sum of each warp's rows, the
-    // piece, the requests' scan
+    // piece (each warp's), the requests' scan
     static constexpr int kOffBar = kDirectWarps * kRingBytes;
     static constexpr int kOffRows = kOffBar + kDirectWarps * kSlots * 8;
     static constexpr int kOffWork = kOffRows + kDirectWarps * kDirectRows * 8;
-    static constexpr int kOffScan = kOffWork + static_cast<int>(sizeof(Work));
+    static constexpr int kOffScan = kOffWork + kDirectWarps * static_cast<int>(sizeof(Work));
     static constexpr int kSmemBytes = kOffScan + 4 * kDirectWarps;
     static_assert(kOffBar % 1024 == 0 && kOffRows % 8 == 0 && kOffWork % alignof(Work) == 0 &&
                       kOffScan % 4 == 0,
@@ -137,7 +137,8 @@ __device__ __forceinline__ void begin_item(Consumer<D> &cs, const ShortParams &p
 
 }  // namespace
 
-template <int D, bool FP8, int PER_SM>
+// ALONE: a warp per job, else a cluster of CTAs.
+template <int D, bool FP8, int PER_SM, bool ALONE>
 __global__ void __launch_bounds__(DirectGeom<D, FP8, PER_SM>::kThreads, PER_SM)
     window_direct_kernel(const ShortParams p, const __grid_constant__ CUtensorMap tmk,
                         const __grid_constant__ CUtensorMap tmv, const DirectParams dp) {
@@ -147,12 +148,12 @@ __global__ void __launch_bounds__(DirectGeom<D, FP8, PER_SM>::kThreads, PER_SM)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint8_t *ring = smem + warp * G::kRingBytes;
     float2 *rows = reinterpret_cast<float2 *>(smem + G::kOffRows);
-    Work *work = reinterpret_cast<Work *>(smem + G::kOffWork);
+    Work *works = reinterpret_cast<Work *>(smem + G::kOffWork);
     int *scan = reinterpret_cast<int *>(smem + G::kOffScan);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + G::kOffBar) + warp * NS;
-    const int size = dp.cluster, rank = static_cast<int>(blockIdx.x) % size;
-    const int job = static_cast<int>(blockIdx.x) / size;
-    const int piece = job / p.num_kv_heads;
+    // the CTA's jobs: the cluster's, or one for each warp
+    const int size = ALONE ? 1 : dp.cluster, rank = static_cast<int>(blockIdx.x) % size;
+    const int first_job = static_cast<int>(blockIdx.x) / size * (ALONE ? kDirectWarps : 1);
     if (lane == 0) {
         for (int i = 0; i < NS; ++i) mbar_init(&full[i], 1);
         fence_mbar_init();
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(DirectGeom<D, FP8, PER_SM>::kThreads, PER_SM)
             tma_prefetch_desc(&tmv);
         }
     }
-    if (tid == 0) *work = Work{};
+    if (tid < kDirectWarps) works[tid] = Work{};
     pdl_wait();
     pdl_trigger();
 
@@ -200,26 +201,26 @@ __global__ void __launch_bounds__(DirectGeom<D, FP8, PER_SM>::kThreads, PER_SM)
         if (blockIdx.x == 0 && tid == 0) flag_status(p.status, PA_DEV_PLAN_OVERFLOW);
         return;
     }
-    if (piece >= total) return;  // (all of a cluster's CTAs)
-    if (piece >= first && piece < first + pieces) {
-        int b = tid * each;
+    if (first_job / p.num_kv_heads >= total) return;  // (all of a cluster's CTAs)
+    for (int k = 0; k < (ALONE ? kDirectWarps : 1); ++k) {
+        const int piece = (first_job + k) / p.num_kv_heads;
+        if (piece < first || piece >= first + pieces) continue;  // none, or another thread's
+        int b = tid * each, at = first;
         if (each > 1)
-            for (int at = first;; ++b) {
-                const int k = pieces_of(b, q0, n, ctx);
-                if (piece < at + k) {
-                    first = at;
-                    break;
-                }
-                at += k;
+            for (;; ++b) {
+                const int of_b = pieces_of(b, q0, n, ctx);
+                if (piece < at + of_b) break;
+                at += of_b;
             }
-        const int begin = (piece - first) * dp.piece_tokens;
+        const int begin = (piece - at) * dp.piece_tokens;
         const int count = min(dp.piece_tokens, n - begin);
         const KeySpan ks = key_span(p.win, ctx + begin, ctx + begin + count);
+        Work *work = works + k;
         work->b = b;
         work->q_count = count;
         work->sink_chunks = ks.sink_chunks;
         work->gap = ks.gap;
-        work->h = job - piece * p.num_kv_heads;
+        work->h = (first_job + k) - piece * p.num_kv_heads;
         work->key_end = ks.keys;
         work->chunks = (ks.keys + kChunkKeys - 1) / kChunkKeys;
         work->tok0 = q0 + begin;
@@ -229,8 +230,9 @@ __global__ void __launch_bounds__(DirectGeom<D, FP8, PER_SM>::kThreads, PER_SM)
 
     // this warp's chunks: worker, worker + workers, ...; lane l holds the TMA
     // row of the (base + l)-th, and the raw block id of the 32 after those
-    const Work &w = *work;
-    const int workers = size * kDirectWarps, worker = rank * kDirectWarps + warp;
+    const Work &w = works[ALONE ? warp : 0];
+    const int workers = ALONE ? 1 : size * kDirectWarps;
+    const int worker = ALONE ? 0 : rank * kDirectWarps + warp;
     const int mine = w.chunks > worker ? (w.chunks - worker + workers - 1) / workers : 0;
     auto nth = [&](int i) { return i < mine ? worker + i * workers : w.chunks; };
     int row_of = chunk_row(p, w, nth(lane), chunk_block(p, w, nth(lane)));
@@ -300,10 +302,15 @@ __global__ void __launch_bounds__(DirectGeom<D, FP8, PER_SM>::kThreads, PER_SM)
             }
         }
     }
-    cluster_sync();
-    // Fold: four columns of a row per thread, the CTAs of the cluster in turn
+    if (ALONE)
+        __syncwarp();
+    else
+        cluster_sync();
+    // Fold: four columns of a row per thread, the CTAs of the cluster in turn (a warp
+    // alone: its own state)
     const float vsc = FP8 ? __ldg(p.v_scale + w.h) : 1.f;
-    for (int i = rank * G::kThreads + tid; i < cs.R * (D / 4); i += size * G::kThreads) {
+    const int stride = ALONE ? 32 : size * G::kThreads;
+    for (int i = ALONE ? lane : rank * G::kThreads + tid; i < cs.R * (D / 4); i += stride) {
         const int r = i / (D / 4), e4 = i - r * (D / 4);
         float M = -INFINITY, sum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -313,8 +320,11 @@ __global__ void __launch_bounds__(DirectGeom<D, FP8, PER_SM>::kThreads, PER_SM)
             float most = M;
 #pragma unroll
             for (int k = 0; k < kDirectWarps; ++k) {
-                ml[k] = ld_cluster_f2(&rows[k * kDirectRows + r], c);
-                v[k] = ld_cluster_f4(smem + k * G::kRingBytes + (r * D + 4 * e4) * 4, c);
+                const bool with = !ALONE || k == warp;
+                ml[k] = with ? ld_cluster_f2(&rows[k * kDirectRows + r], c)
+                             : make_float2(-INFINITY, 0.f);
+                v[k] = with ? ld_cluster_f4(smem + k * G::kRingBytes + (r * D + 4 * e4) * 4, c)
+                            : make_float4(0.f, 0.f, 0.f, 0.f);
                 most = fmaxf(most, ml[k].x);
             }
             if (most == -INFINITY) continue;
@@ -344,42 +354,48 @@ __global__ void __launch_bounds__(DirectGeom<D, FP8, PER_SM>::kThreads, PER_SM)
         reinterpret_cast<uint2 *>(p.out + row * D)[e4] = out;
         if (e4 == 0 && p.lse) p.lse[row] = sum > 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
     }
-    cluster_sync();  // the others have read this CTA's states
+    if (!ALONE) cluster_sync();  // the others have read this CTA's states
 }
 
 namespace {
 
-template <int D, bool FP8, int PER_SM>
+template <int D, bool FP8, int PER_SM, bool ALONE>
 int launch_direct(const ShortParams &p, const CUtensorMap &tk, const CUtensorMap &tv,
                  const DirectParams &dp, cudaStream_t s) {
     using G = DirectGeom<D, FP8, PER_SM>;
     static PerDeviceOnce once;
     if (once_per_device(once, [] {
-            return cudaFuncSetAttribute(window_direct_kernel<D, FP8, PER_SM>,
+            return cudaFuncSetAttribute(window_direct_kernel<D, FP8, PER_SM, ALONE>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         G::kSmemBytes);
         }) != PA_OK)
         return PA_ERR_CUDA;
-    PdlLaunch l(dp.max_pieces * p.num_kv_heads * dp.cluster, G::kThreads, G::kSmemBytes, s);
-    l.set_cluster(dp.cluster);
-    return launch_kernel(l, window_direct_kernel<D, FP8, PER_SM>, p, tk, tv, dp) == cudaSuccess
+    const int jobs = dp.max_pieces * p.num_kv_heads;
+    const int grid = ALONE ? (jobs + kDirectWarps - 1) / kDirectWarps : jobs * dp.cluster;
+    PdlLaunch l(grid, G::kThreads, G::kSmemBytes, s);
+    if (dp.cluster > 1) l.set_cluster(dp.cluster);
+    return launch_kernel(l, window_direct_kernel<D, FP8, PER_SM, ALONE>, p, tk, tv, dp) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
+}
+
+template <int D, bool FP8>
+int launch_direct(const ShortParams &p, const CUtensorMap &tk, const CUtensorMap &tv,
+                  const DirectParams &dp, cudaStream_t s) {
+    if (dp.cluster == 0)
+        return dp.per_sm == 2 ? launch_direct<D, FP8, 2, true>(p, tk, tv, dp, s)
+                              : launch_direct<D, FP8, 3, true>(p, tk, tv, dp, s);
+    return dp.per_sm == 2 ? launch_direct<D, FP8, 2, false>(p, tk, tv, dp, s)
+                          : launch_direct<D, FP8, 3, false>(p, tk, tv, dp, s);
 }
 
 }  // namespace
 
 int launch_window_direct(const ShortParams &p, const CUtensorMap &tk, const CUtensorMap &tv,
                         const DirectParams &dp, int head_dim, bool fp8, cudaStream_t s) {
-    const bool two = dp.per_sm == 2;
-    if (fp8)
-        return two ? launch_direct<128, true, 2>(p, tk, tv, dp, s)
-                   : launch_direct<128, true, 3>(p, tk, tv, dp, s);
-    if (head_dim == 128)
-        return two ? launch_direct<128, false, 2>(p, tk, tv, dp, s)
-                   : launch_direct<128, false, 3>(p, tk, tv, dp, s);
-    return two ? launch_direct<64, false, 2>(p, tk, tv, dp, s)
-               : launch_direct<64, false, 3>(p, tk, tv, dp, s);
+    if (fp8) return launch_direct<128, true>(p, tk, tv, dp, s);
+    return head_dim == 128 ? launch_direct<128, false>(p, tk, tv, dp, s)
+                           : launch_direct<64, false>(p, tk, tv, dp, s);
 }
 
 }  // namespace pa
