@@ -510,18 +510,24 @@ bool direct_step(const WindowArgs &win, int num_seqs, int T, const pa_kv_desc *k
         if (kv->kv_dtype == PA_KV_FP8_E4M3 && jobs * chunks > kDirectE4m3Chunks) return false;
     }
     // Warps per job (one, or all of 1, 2, 4 or 8 CTAs) and CTAs per SM: the fewest
-    // rounds times a CTA's time, in chunks of one warp at one CTA per SM (and what
-    // it costs besides, as much as twelve).  Three CTAs per SM have shorter rings: 48
-    // decode requests, 8 kv heads, window 1024: 36 us with three (one round), 47 with
-    // two; 64 requests 56 / 50.
+    // rounds times a CTA's time, from what was measured in units of a chunk of one
+    // warp (0.67 us): 7 for its start and fold, half a unit more per CTA of a cluster
+    // and 10 for warps on their own, and a chunk half as long again for each
+    // further CTA on the SM.  (8 jobs at window 1024: 15.9, 11.8, 9.7 and 9.3 us with 1, 2,
+    // 4 and 8 CTAs; at window 64 6.1, 5.9, 6.6 and 7.6; 384 jobs at window 1024 36 us
+    // with three CTAs per SM, one round, and 47 with two; 1024 jobs at window 128 21 us
+    // with a warp each, 29 with a CTA.)
     int64_t best = -1;
     for (int per = 2; per <= 3; ++per)
-        for (int c = 0; c <= kDirectMaxCluster; c = c == 0 ? 1 : 2 * c) {
+        for (int c = 0; c <= (per == 2 ? kDirectMaxCluster : kDirectMaxCluster / 2);
+             c = c == 0 ? 1 : 2 * c) {
             const int64_t warps = c == 0 ? 1 : kDirectWarps * c;
             const int64_t per_warp = (chunks + warps - 1) / warps;
             const int64_t ctas = (jobs * warps + kDirectWarps - 1) / kDirectWarps;
             const int64_t slots = static_cast<int64_t>(per) * sms;
-            const int64_t time = (ctas + slots - 1) / slots * (per_warp * per + 12);
+            const int64_t on_sm = std::min<int64_t>(per, (ctas + sms - 1) / sms);
+            const int64_t start = c == 0 ? 20 : c == 1 ? 14 : 14 + c;  // half units
+            const int64_t time = (ctas + slots - 1) / slots * (per_warp * (on_sm + 1) + start);
             if (best < 0 || time < best) {
                 best = time;
                 dp->cluster = c;
