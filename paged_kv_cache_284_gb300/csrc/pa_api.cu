@@ -157,22 +157,27 @@ constexpr int kSideBySideMinTokens = 512;
 constexpr int64_t kSideBySideMinChunks = 6144;
 
 // A windowed step of groups of at most 16 runs as one kernel (window_direct_kernel)
-// in place of the plan and the planned kernels
-//  * when its pieces (of 16 rows), kv heads and windows bound its work to
-//    kDirectAnyChunks chunks on at most kDirectJobsPerSm jobs per SM, whatever its
-//    requests are: a lone token at window 128 takes 5.7 us against 11.5, 24 verify
-//    requests 7.8 against 20.6, a prompt chunk of 64 tokens at window 128 10.2
-//    against 14.3; but one of 256 20.8 / 14.7;
-//  * beyond that when it has few rows, or no more than a piece's per request on
-//    average (a chunk of 64 tokens at window 4096: 33 us against 43; of 128, past
-//    the bound: 57 / 43).  Decode, 8 kv heads, d = 128: 16 requests at window 1024
-//    17.8 us against 28.5, 64 49.7 / 67.6, 256 126 / 155 at window 700 and 50 / 73
-//    at 128, 800 at window 128 149 / 179;
-//  * on e4m3 pools, where decoding the codes bounds both, only while there is
-//    little to decode: 32 requests at window 2048 36 us against 43, 64 at window
-//    4096 115 / 107.
+// in place of the plan and the planned kernels (times: one kernel / planned)
+//  * whatever its requests are, when its pieces (of 16 rows), kv heads and windows
+//    bound its work to kDirectAnyChunks chunks on at most kDirectJobsPerSm jobs per
+//    SM, or its jobs fill one round and its work kDirectRoundChunks: a lone token at
+//    window 128 5.7 / 11.5 us, 24 verify requests 7.8 / 20.6, a prompt chunk of 128
+//    tokens of 32 q / 8 kv heads (264 jobs) at window 128 10.5 / 14.0, at 512 15.3 /
+//    17.5, at 1024 (past the bound) 21.2 / 20.6; of 256 tokens (520 jobs) at window 128
+//    (past it) 19.8 / 14.4.  e4m3 pools, whose prompts are staged as bf16 first: 128
+//    tokens at window 512 14.1 / 23.3, 512 tokens of 8 / 2 heads at window 1024 20.5 /
+//    25.6;
+//  * beyond that when it has few rows, or on average no more than a piece's per
+//    request (or two pieces', of little work): a chunk of 64 tokens at window 4096
+//    33 / 43 us, but of 128 57 / 43; 16 verify requests of 20 rows at window 1024 16 /
+//    23.  Decode, 8 kv heads, d = 128: 16 requests at window 1024 18 / 28 us, 64 50 /
+//    68, 256 at window 700 126 / 155 and at 128 40 / 73;
+//  * on e4m3 pools, where decoding the codes bounds both, the latter only while there
+//    is little to decode: 32 requests at window 2048 36 / 43 us, 64 at 4096 115 / 107.
 constexpr int64_t kDirectAnyChunks = 4096;
+constexpr int64_t kDirectAnyChunksE4m3 = 6144;
 constexpr int64_t kDirectJobsPerSm = 7;
+constexpr int64_t kDirectRoundChunks = 16384;
 constexpr int64_t kDirectAnyRows = 256;
 constexpr int64_t kDirectE4m3Chunks = 65536;
 
@@ -504,11 +509,15 @@ bool direct_step(const WindowArgs &win, int num_seqs, int T, const pa_kv_desc *k
     const int64_t chunks = seen_chunks(win, dp->piece_tokens, max_blocks, kv->block_size);
     const int64_t jobs = static_cast<int64_t>(dp->max_pieces) * kv->num_kv_heads;
     const int64_t rows = static_cast<int64_t>(T) * group;
-    if (jobs * chunks > kDirectAnyChunks || jobs > kDirectJobsPerSm * sms) {
-        if (rows > kDirectAnyRows && rows > static_cast<int64_t>(num_seqs) * kDirectRows)
-            return false;
-        if (kv->kv_dtype == PA_KV_FP8_E4M3 && jobs * chunks > kDirectE4m3Chunks) return false;
-    }
+    const bool e4m3 = kv->kv_dtype == PA_KV_FP8_E4M3;
+    const int64_t work = jobs * chunks;
+    const bool any = work <= (e4m3 ? kDirectAnyChunksE4m3 : kDirectAnyChunks)
+                         ? jobs <= kDirectJobsPerSm * sms
+                         : jobs <= 2 * sms && work <= (e4m3 ? 2 : 1) * kDirectRoundChunks;
+    const bool few = rows <= kDirectAnyRows || rows <= static_cast<int64_t>(num_seqs) * kDirectRows ||
+                     (rows <= 2 * static_cast<int64_t>(num_seqs) * kDirectRows &&
+                      work <= 2 * kDirectRoundChunks);
+    if (!any && !(few && (!e4m3 || work <= kDirectE4m3Chunks))) return false;
     // Warps per job (one, or all of 1, 2, 4 or 8 CTAs) and CTAs per SM: the fewest
     // rounds times a CTA's time, from what was measured in units of a chunk of one
     // warp (0.67 us): 7 for its start and fold, half a unit more per CTA of a cluster

@@ -465,7 +465,7 @@ def test_planned_steps(kv, d, staged, window, sinks):
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 def test_planned_steps_split_over_the_window(kv):
-    Step([(9000 - 500 * i, 10) for i in range(8)], 8, 1, 128, 16, 3000, 37, kv=kv,
+    Step([(16000 - 300 * i, 8) for i in range(8)], 8, 1, 128, 16, 14000, 37, kv=kv,
          seed=3).run_and_check()
 
 
