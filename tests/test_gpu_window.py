@@ -509,3 +509,46 @@ def test_binding_takes_plain_calls_and_leaves_the_others():
     assert call(*good[:12], ws[:256], *good[13:]) == pk.PA_ERR_WORKSPACE
     assert call(*good[:8], 0, *good[9:]) == pk.PA_ERR_INVALID_ARG
     assert pk.lib().pa_kernel_launches() == before
+
+
+@pytest.mark.parametrize("kv,d", [("bf16", 128), ("bf16", 64), ("e4m3", 128)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (16, 4), (33, 17), (90, 0)])
+def test_many_short_jobs_of_a_warp_each(kv, d, window, sinks):
+    rng = np.random.default_rng(window)
+    reqs = many(150, 500, rng, (1, 4)) + [(0, 0)] * 40 + many(3, 40, rng, (9, 10))
+    Step(reqs, 32, 8, d, 16, window, sinks, kv=kv, seed=window, pad=2).run_and_check()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,window", [(129, 200), (300, 40), (1024, 20)])
+def test_more_requests_than_threads_of_a_cta(kv, n, window):
+    """Each thread scans several requests; few jobs, so clusters share them."""
+    rng = np.random.default_rng(n)
+    reqs = many(n, 300, rng)
+    for i in range(0, n, 7):
+        reqs[i] = (0, 0)
+    reqs[n // 2] = (77, 9)
+    Step(reqs, 4, 1, 128, 32, window, 5, kv=kv, seed=n).run_and_check()
+
+
+@pytest.mark.parametrize("kv,d,n", [("bf16", 64, 300), ("bf16", 128, 300), ("e4m3", 128, 200)])
+def test_many_requests_over_one_long_prefix(kv, d, n):
+    """Every request has the same blocks, position and query, so each warp walks
+    dozens of chunks (several batches of block ids) and all rows are equal."""
+    one = Step([(4400, 1)], 4, 1, d, 16, 4300, 20, kv=kv, seed=n)
+    t = one.to_dev()
+    one.call(t)
+    torch.cuda.synchronize()
+    one.check(t)
+    t["q"] = t["q"].repeat(n, 1, 1).contiguous()
+    t["table"] = t["table"].repeat(n, 1).contiguous()
+    t["qsl"] = torch.arange(n + 1, dtype=torch.int32, device=DEV)
+    t["ctx"], t["seq"] = t["ctx"].repeat(n), t["seq"].repeat(n)
+    t["out"] = torch.full_like(t["q"], 7.0)
+    t["lse"] = torch.full((n, 4), 7.0, device=DEV)
+    one.call(t)
+    torch.cuda.synchronize()
+    assert torch.equal(t["out"], t["out"][:1].expand_as(t["out"]))
+    assert torch.equal(t["lse"], t["lse"][:1].expand_as(t["lse"]))
+    one.check({"out": t["out"][:1], "lse": t["lse"][:1]})
+    assert_status_clean()
