@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
         pdl_trigger();  // then the split-KV grid may take the other SMs
     }
     const int n_items = *reinterpret_cast<volatile int *>(&p.hdr->num_long_items);
-    if (!p.dynamic && static_cast<int>(blockIdx.x) >= n_items) {
+    if (!p.first_done && static_cast<int>(blockIdx.x) >= n_items) {
         pdl_wait();  // complete only after the grid this one overlaps
         return;
     }
