@@ -156,20 +156,33 @@ constexpr int kSideBySideMinTokens = 512;
 // (5.3 k), 94 / 99 at 4096 (39 k).
 constexpr int64_t kSideBySideMinChunks = 6144;
 
+// A windowed bf16 step of at most this many requests needs no plan (see run_step): the
+// tensor-core kernel finds the tiles itself (a lane per request), and CTAs are launched
+// for all pieces that its requests might have as short rows.  32 q / 8 kv heads, without
+// / with a plan: one chunk of 256 tokens at window 128 11.0 / 14.4 us, of 1024 at window
+// 1024 31.8 / 34.3.  With 32 requests, most of them verify rows, the CTAs without a piece
+// cost more than the plan (29.6 / 25.4).
+constexpr int kOwnPlanMaxSeqs = 8;
+static_assert(kOwnPlanMaxSeqs <= 32, "a lane per request");
+// More tiles gain more from the plan's counter: 3 chunks of 2048 tokens, 8 kv heads, window
+// 512 (1536 tiles) 104 us without a plan, 100 with; one of 1024 (256 tiles) 25 / 28.
+constexpr int kOwnPlanTilesPerSm = 6;
+
 // A windowed step of groups of at most 16 runs as one kernel (window_direct_kernel)
 // in place of the plan and the planned kernels (times: one kernel / planned)
 //  * whatever its requests are, when its pieces (of 16 rows), kv heads and windows
 //    bound its work to kDirectAnyChunks chunks on at most kDirectJobsPerSm jobs per
 //    SM, or its jobs fill one round and its work kDirectRoundChunks: a lone token at
-//    window 128 5.7 / 11.5 us, 24 verify requests 7.8 / 20.6, a prompt chunk of 128
-//    tokens of 32 q / 8 kv heads (264 jobs) at window 128 10.5 / 14.0, at 512 15.3 /
-//    17.5, at 1024 (past the bound) 21.2 / 20.6; of 256 tokens (520 jobs) at window 128
-//    (past it) 19.8 / 14.4.  e4m3 pools, whose prompts are staged as bf16 first: 128
-//    tokens at window 512 14.1 / 23.3, 512 tokens of 8 / 2 heads at window 1024 20.5 /
-//    25.6;
+//    window 128 5.7 / 11.5 us, 24 verify requests 7.8 / 20.6.  e4m3 pools, whose
+//    prompts are staged as bf16 first: 128 tokens of 32 q / 8 kv heads at window 512
+//    14.1 / 23.3, 512 tokens of 8 / 2 heads at window 1024 20.5 / 25.6.  In bf16
+//    steps of few requests the other form has no plan either (see run_step) and the
+//    bounds are closer: 64 tokens (136 jobs) at window 1024 16.2 / 17.6, 128 (264 jobs)
+//    at window 128 10.6 / 10.9 and at 512 15.4 / 14.1, 256 (520 jobs) at window 16
+//    14.8 / 10.5; at head_dim 64 128 tokens at window 512 11.3 / 12.5;
 //  * beyond that when it has few rows, or on average no more than a piece's per
 //    request (or two pieces', of little work): a chunk of 64 tokens at window 4096
-//    33 / 43 us, but of 128 57 / 43; 16 verify requests of 20 rows at window 1024 16 /
+//    33 / 40 us, but of 128 57 / 41; 16 verify requests of 20 rows at window 1024 16 /
 //    23.  Decode, 8 kv heads, d = 128: 16 requests at window 1024 18 / 28 us, 64 50 /
 //    68, 256 at window 700 126 / 155 and at 128 40 / 73;
 //  * on e4m3 pools, where decoding the codes bounds both, the latter only while there
@@ -499,33 +512,15 @@ int64_t seen_chunks(const WindowArgs &win, int tokens, int max_blocks, int block
     return std::min(table, seen);
 }
 
-// Whether a windowed step is one for the one-kernel form, and its launch.
-bool direct_step(const WindowArgs &win, int num_seqs, int T, const pa_kv_desc *kv, int group,
-                 int max_blocks, int sms, DirectParams *dp) {
-    if (group > kDirectRows || num_seqs > kDirectMaxSeqs) return false;
-    dp->piece_tokens = piece_tokens_for(group, kDirectRows);
-    dp->max_pieces = std::min(T, pieces_bound(num_seqs, T, group, kDirectRows));
-    dp->max_keys = max_blocks * kv->block_size;
-    const int64_t chunks = seen_chunks(win, dp->piece_tokens, max_blocks, kv->block_size);
-    const int64_t jobs = static_cast<int64_t>(dp->max_pieces) * kv->num_kv_heads;
-    const int64_t rows = static_cast<int64_t>(T) * group;
-    const bool e4m3 = kv->kv_dtype == PA_KV_FP8_E4M3;
-    const int64_t work = jobs * chunks;
-    const bool any = work <= (e4m3 ? kDirectAnyChunksE4m3 : kDirectAnyChunks)
-                         ? jobs <= kDirectJobsPerSm * sms
-                         : jobs <= 2 * sms && work <= (e4m3 ? 2 : 1) * kDirectRoundChunks;
-    const bool few = rows <= kDirectAnyRows || rows <= static_cast<int64_t>(num_seqs) * kDirectRows ||
-                     (rows <= 2 * static_cast<int64_t>(num_seqs) * kDirectRows &&
-                      work <= 2 * kDirectRoundChunks);
-    if (!any && !(few && (!e4m3 || work <= kDirectE4m3Chunks))) return false;
-    // Warps per job (one, or all of 1, 2, 4 or 8 CTAs) and CTAs per SM: the fewest
-    // rounds times a CTA's time, from what was measured in units of a chunk of one
-    // warp (0.67 us): 7 for its start and fold, half a unit more per CTA of a cluster
-    // and 10 for warps on their own, and a chunk half as long again for each
-    // further CTA on the SM.  (8 jobs at window 1024: 15.9, 11.8, 9.7 and 9.3 us with 1, 2,
-    // 4 and 8 CTAs; at window 64 6.1, 5.9, 6.6 and 7.6; 384 jobs at window 1024 36 us
-    // with three CTAs per SM, one round, and 47 with two; 1024 jobs at window 128 21 us
-    // with a warp each, 29 with a CTA.)
+// The one-kernel form's warps per job (one, or all of 1, 2, 4 or 8 CTAs) and CTAs per SM:
+// the fewest rounds times a CTA's time, from what was measured in units of a chunk of
+// one warp (0.67 us): 7 for its start and fold, half a unit more per CTA of a cluster
+// and 10 for warps on their own, and a chunk half as long again for each further CTA on
+// the SM.  (8 jobs at window 1024: 15.9, 11.8, 9.7 and 9.3 us with 1, 2, 4 and 8 CTAs; at
+// window 64 6.1, 5.9, 6.6 and 7.6; 384 jobs at window 1024 36 us with three CTAs per SM,
+// one round, and 47 with two; 1024 jobs at window 128 21 us with a warp each, 29 with a
+// CTA.)
+void direct_shape(int64_t jobs, int64_t chunks, int sms, DirectParams *dp) {
     int64_t best = -1;
     for (int per = 2; per <= 3; ++per)
         for (int c = 0; c <= (per == 2 ? kDirectMaxCluster : kDirectMaxCluster / 2);
@@ -543,6 +538,35 @@ bool direct_step(const WindowArgs &win, int num_seqs, int T, const pa_kv_desc *k
                 dp->per_sm = per;
             }
         }
+}
+
+// Whether a windowed step is one for the one-kernel form, and its launch.
+bool direct_step(const WindowArgs &win, int num_seqs, int T, const pa_kv_desc *kv, int group,
+                 int max_blocks, int sms, DirectParams *dp) {
+    if (group > kDirectRows || num_seqs > kDirectMaxSeqs) return false;
+    dp->piece_tokens = piece_tokens_for(group, kDirectRows);
+    dp->max_pieces = std::min(T, pieces_bound(num_seqs, T, group, kDirectRows));
+    dp->max_keys = max_blocks * kv->block_size;
+    const int64_t chunks = seen_chunks(win, dp->piece_tokens, max_blocks, kv->block_size);
+    const int64_t jobs = static_cast<int64_t>(dp->max_pieces) * kv->num_kv_heads;
+    const int64_t rows = static_cast<int64_t>(T) * group;
+    const bool e4m3 = kv->kv_dtype == PA_KV_FP8_E4M3;
+    const int64_t work = jobs * chunks;
+    bool any;
+    if (!e4m3 && num_seqs <= kOwnPlanMaxSeqs)
+        any = jobs <= sms ? work <= kDirectRoundChunks
+                          : kv->head_dim == 64 ? jobs <= 3 * sms && work <= 2 * kDirectAnyChunks
+                                               : jobs <= 2 * sms && 4 * work <= 3 * kDirectAnyChunks;
+    else if (work <= (e4m3 ? kDirectAnyChunksE4m3 : kDirectAnyChunks))
+        any = jobs <= kDirectJobsPerSm * sms;
+    else
+        any = jobs <= 2 * sms && work <= (e4m3 ? 2 : 1) * kDirectRoundChunks;
+    const bool few = rows <= kDirectAnyRows || rows <= static_cast<int64_t>(num_seqs) * kDirectRows ||
+                     (rows <= 2 * static_cast<int64_t>(num_seqs) * kDirectRows &&
+                      work <= 2 * kDirectRoundChunks);
+    if (!any && !(few && (!e4m3 || work <= kDirectE4m3Chunks))) return false;
+    dp->max_rows = 0x7fffffff;
+    direct_shape(jobs, chunks, sms, dp);
     return true;
 }
 
@@ -661,7 +685,25 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         return rc == PA_OK ? PA_OK : fail(rc, "window kernel launch failed: %s",
                                           cudaGetErrorString(cudaGetLastError()));
     }
-    int rc;
+    // A windowed step of few requests whose kernels run one after the other needs no
+    // plan either: its short rows run in the one-kernel form, and the tensor-core
+    // kernel finds the long requests' tiles itself.
+    const bool own_plans = win && !fp8 && group <= kDirectRows && num_seqs <= kOwnPlanMaxSeqs &&
+                           max_long_reqs > 0 && !side_by_side &&
+                           kv->num_kv_heads * ((T + tq - 1) / tq) <= kOwnPlanTilesPerSm * dev->sms;
+    if (own_plans) {
+        const int per_request = (kShortMaxRows / group + direct.piece_tokens - 1) / direct.piece_tokens;
+        direct.max_pieces = std::min(direct.max_pieces, num_seqs * per_request);
+        direct.max_rows = kShortMaxRows;
+        direct_shape(static_cast<int64_t>(num_seqs) * kv->num_kv_heads,
+                     seen_chunks(*win, direct.piece_tokens, max_blocks, kv->block_size), dev->sms,
+                     &direct);
+        ProfScope prof(PA_KERNEL_SPLIT_KV, s);
+        const int rc = launch_window_direct(sp, maps.k, maps.v, direct, D, fp8, s);
+        if (rc != PA_OK)
+            return fail(rc, "window kernel launch failed: %s", cudaGetErrorString(cudaGetLastError()));
+    }
+    int rc = PA_OK;
     if (fresh && fresh->num_tokens > 0) {
         // The step's new rows first, as pa_write_kv does: its kernel runs as a
         // programmatic dependent ahead of the planner and is off the step's
@@ -673,7 +715,7 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
                              s);
         if (rc != PA_OK) return fail(rc, "write_kv launch failed");
     }
-    {
+    if (!own_plans) {
         ProfScope prof(PA_KERNEL_PLAN, s);
         rc = win ? launch_plan_window(pp, s) : launch_plan(pp, s);
     }
@@ -778,6 +820,10 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         lp.scale_log2 = sp.scale_log2;
         lp.prefix_mode = 0;
         if (win) lp.win = *win;
+        if (own_plans) {
+            lp.own_seqs = num_seqs;
+            lp.own_max_keys = direct.max_keys;
+        }
         lp.hdr = hdr;
         lp.items = pp.long_items;
         lp.partial_o = sp.partial_o;
@@ -843,7 +889,7 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         return PA_OK;
     }
 
-    {
+    if (!own_plans) {
         ProfScope prof(PA_KERNEL_SPLIT_KV, s);
         rc = launch_short(sp, maps.k, maps.v, D, fp8, win != nullptr, short_grid, s);
     }
@@ -854,7 +900,7 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         // may take over SMs as split-KV CTAs finish (its rows are disjoint)
         lp.overlap_prev = short_grid > 0 ? 1 : 0;
         // (many windowed items: from the step's counter, see pa_long_window.cu)
-        lp.dynamic = win && long_grid > 2 * dev->sms ? 1 : 0;
+        lp.dynamic = win && !own_plans && long_grid > 2 * dev->sms ? 1 : 0;
         {
             ProfScope prof(PA_KERNEL_TENSOR_CORE, s);
             rc = tensor_core(lp, long_grid);

@@ -215,6 +215,7 @@ struct DirectParams {
     int per_sm;  // CTAs per SM: 2 or 3
     int cluster, max_pieces, piece_tokens;
     int max_keys;  // a request longer than its table is skipped
+    int max_rows;  // of a request; one with more is left to the tensor-core kernel
 };
 constexpr int kDirectMaxSeqs = 1024;  // eight per thread
 constexpr int kDirectWarps = 4;       // per CTA
@@ -258,6 +259,8 @@ struct LongParams {
     // the step's inputs) before its last instruction, where it waits for the
     // split-KV grid so that its own completion still orders the stream.
     int overlap_prev;
+    // windowed step without a plan: its requests, and the longest that a table holds
+    int own_seqs, own_max_keys;
     WindowArgs win;  // windowed step only
 };
 

@@ -96,6 +96,63 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 336, "barrier area");
 
+// A step without a plan (p.own_seqs > 0, at most a warp's lanes of requests): lane b
+// holds request b and the tiles up to and with it; a short request has none.
+struct OwnPlan {
+    int q0, n, ctx, tiles, incl, total;
+};
+__device__ __forceinline__ OwnPlan own_plan(const LongParams &p) {
+    const int lane = threadIdx.x & 31;
+    OwnPlan o{};
+    if (lane < p.own_seqs) {
+        o.q0 = __ldg(p.qsl + lane);
+        o.ctx = __ldg(p.ctx + lane);
+        const int q1 = __ldg(p.qsl + lane + 1), len = __ldg(p.seq_lens + lane);
+        o.n = q1 - o.q0;
+        // (a request that the short rows' kernel flags is skipped here too)
+        const bool bad = o.n < 0 || o.ctx < 0 || len > p.own_max_keys || len != o.ctx + o.n ||
+                         o.q0 < 0 || q1 > p.num_q_tokens;
+        if (bad) o.n = 0;
+        if (o.n * p.group > kShortMaxRows)
+            o.tiles = (o.n + p.q_tile_tokens - 1) / p.q_tile_tokens;
+    }
+    // requests that overlap: none runs
+    long long tokens = o.n;
+#pragma unroll
+    for (int i = 1; i < 32; i <<= 1) tokens += __shfl_xor_sync(0xffffffffu, tokens, i);
+    if (tokens > p.num_q_tokens) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) flag_status(p.status, PA_DEV_PLAN_OVERFLOW);
+        o.tiles = 0;
+    }
+    o.incl = o.tiles;
+#pragma unroll
+    for (int i = 1; i < 32; i <<= 1) {
+        const int before = __shfl_up_sync(0xffffffffu, o.incl, i);
+        if (lane >= i) o.incl += before;
+    }
+    o.total = __shfl_sync(0xffffffffu, o.incl, 31);
+    return o;
+}
+// Its tile `t`, with the request's first row, tokens and context.
+__device__ __forceinline__ LongItem own_tile(const LongParams &p, const OwnPlan &o, int t, int &q0,
+                                             int &n, int &ctx) {
+    const int excl = o.incl - o.tiles;
+    const unsigned owner = __ballot_sync(0xffffffffu, excl <= t && t < o.incl);
+    const int src = __ffs(owner) - 1;
+    q0 = __shfl_sync(0xffffffffu, o.q0, src);
+    n = __shfl_sync(0xffffffffu, o.n, src);
+    ctx = __shfl_sync(0xffffffffu, o.ctx, src);
+    LongItem it{};
+    it.b = src;
+    it.q_tile = t - __shfl_sync(0xffffffffu, excl, src);
+    const int first = it.q_tile * p.q_tile_tokens;
+    const KeySpan ks = key_span(p.win, ctx + first, ctx + min(n, first + p.q_tile_tokens));
+    it.key_end = ks.keys;
+    it.sink_chunks = ks.sink_chunks;
+    it.gap = ks.gap;
+    return it;
+}
+
 // Items in order, one reader per warp.  Warp 0, which runs ahead of every other
 // role, takes an item's index -- from the step's counter, shared by every
 // launch of the step (p.dynamic), so that a CTA that starts late takes fewer;
@@ -123,7 +180,7 @@ __device__ __forceinline__ bool queue_spin(const Queue &q, Ready ready) {
 }
 // Warp 0, all lanes: takes, publishes and returns item k.
 __device__ __forceinline__ WinItem queue_next(const LongParams &p, const Queue &q, int n_items,
-                                              int k) {
+                                              const OwnPlan &own, int k) {
     const int lane = threadIdx.x & 31;
     int idx = 0;
     if (lane == 0) {
@@ -138,9 +195,16 @@ __device__ __forceinline__ WinItem queue_next(const LongParams &p, const Queue &
     WinItem it{};
     if (idx < n_items) {
         const int rec = idx / p.num_kv_heads, TQ = p.q_tile_tokens;
-        const LongItem li = load_record(p.items, rec);
-        const int q0 = __ldg(p.qsl + li.b), n = __ldg(p.qsl + li.b + 1) - q0;
-        const int ctx = __ldg(p.ctx + li.b);
+        LongItem li;
+        int q0, n, ctx;
+        if (p.own_seqs > 0) {  // a request's last tiles, which may see more, first
+            li = own_tile(p, own, own.total - 1 - rec, q0, n, ctx);
+        } else {
+            li = load_record(p.items, rec);
+            q0 = __ldg(p.qsl + li.b);
+            n = __ldg(p.qsl + li.b + 1) - q0;
+            ctx = __ldg(p.ctx + li.b);
+        }
         it.b = li.b;
         it.h = idx - rec * p.num_kv_heads;
         it.tok0 = q0 + li.q_tile * TQ;
@@ -196,15 +260,15 @@ __device__ __forceinline__ WinItem queue_item(const Queue &q, int warp, int k) {
 // warp: gathers one 128-key tile per step into its ring, eight 16-key chunks
 // through the block table.
 template <int D>
-__device__ void produce(const LongParams &p, const Queue &q, int n_items, const CUtensorMap *tm,
-                        uint8_t *ring, uint64_t *full, uint64_t *empty, Bars *bars,
+__device__ void produce(const LongParams &p, const Queue &q, int n_items, const OwnPlan &own,
+                        const CUtensorMap *tm, uint8_t *ring, uint64_t *full, uint64_t *empty, Bars *bars,
                         const CUtensorMap *tmq, uint8_t *sQ, int warp) {
     using G = WinGeom<D>;
     const int lane = threadIdx.x & 31;
     uint32_t t = 0;  // tiles issued so far (all items)
     bool ok = true;
     for (int k = 0; ok; ++k) {
-        const WinItem it = tmq ? queue_next(p, q, n_items, k) : queue_item(q, warp, k);
+        const WinItem it = tmq ? queue_next(p, q, n_items, own, k) : queue_item(q, warp, k);
         if (it.nt == 0) break;
         if (tmq) {
             if (k > 0 && !warp_wait(&bars->q_empty, (k - 1) & 1, q.abort)) break;
@@ -331,7 +395,13 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
         pdl_wait();     // the plan (and any staging copy) first
         pdl_trigger();  // then the split-KV grid may take the other SMs
     }
-    const int n_items = *reinterpret_cast<volatile int *>(&p.hdr->num_long_items);
+    // (without a plan: the short rows' grid, which lets this one start, waited for
+    // whatever wrote the metadata)
+    OwnPlan own{};
+    if (p.own_seqs > 0) own = own_plan(p);
+    const int n_items = p.own_seqs > 0
+                            ? own.total * p.num_kv_heads
+                            : *reinterpret_cast<volatile int *>(&p.hdr->num_long_items);
     if (!p.first_done && static_cast<int>(blockIdx.x) >= n_items) {
         pdl_wait();  // complete only after the grid this one overlaps
         return;
@@ -388,11 +458,11 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
             tma_prefetch_desc(&tmq);
             tma_prefetch_desc(&tmk);
         }
-        produce<D>(p, queue, n_items, &tmk, sK, bars->k_full, bars->k_empty, bars, &tmq, sQ, warp);
+        produce<D>(p, queue, n_items, own, &tmk, sK, bars->k_full, bars->k_empty, bars, &tmq, sQ, warp);
     } else if (warp == kWarpV) {
         // ============================ V loads ============================
         if (lane == 0) tma_prefetch_desc(&tmv);
-        produce<D>(p, queue, n_items, &tmv, sV, bars->v_full, bars->v_empty, bars, nullptr, nullptr,
+        produce<D>(p, queue, n_items, own, &tmv, sV, bars->v_full, bars->v_empty, bars, nullptr, nullptr,
                    warp);
     } else if (warp == kWarpQK) {
         // ============================ Q K^T issuer ============================

@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(DirectGeom<D, FP8, PER_SM>::kThreads, PER_SM)
             if (blockIdx.x == 0) flag_status(p.status, PA_DEV_BAD_METADATA);
             n = 0;
         }
+        if (static_cast<int64_t>(n) * p.group > dp.max_rows) return 0;
         return (n + dp.piece_tokens - 1) / dp.piece_tokens;
     };
     int pieces = 0, q0 = 0, n = 0, ctx = 0;

@@ -552,3 +552,37 @@ def test_many_requests_over_one_long_prefix(kv, d, n):
     assert torch.equal(t["lse"], t["lse"][:1].expand_as(t["lse"]))
     one.check({"out": t["out"][:1], "lse": t["lse"][:1]})
     assert_status_clean()
+
+
+@pytest.mark.parametrize("window,sinks", WINDOWS)
+@pytest.mark.parametrize("hq,hkv,d", [(16, 4, 128), (32, 8, 64), (16, 1, 128)])
+def test_prompts_and_short_rows_without_a_plan(hq, hkv, d, window, sinks):
+    """bf16 steps of at most 8 requests: short rows in the one-kernel form, long
+    requests' tiles found by the tensor-core kernel itself."""
+    reqs = CHUNKS + [(0, 0), (100, 1), (40, 16), (64, 17), (300, 300)]
+    Step(reqs, hq, hkv, d, 16, window, sinks, seed=window, pad=3).run_and_check()
+
+
+def test_a_step_without_a_plan_skips_bad_and_overlapping_requests():
+    st = Step([(40, 200), (50, 300), (60, 1), (700, 150)], 32, 8, 128, 16, 600, 2)
+    t = st.to_dev()
+    t["seq"][1] += 1
+    st.call(t)
+    torch.cuda.synchronize()
+    assert pk.read_device_status(clear=True) == pk.PA_DEV_BAD_METADATA
+    assert torch.all(t["out"][200:500] == 7.0)
+    ref, _, mag = ops.window_attention(st.q.double().numpy(), st.k64, st.v64, st.table.numpy(),
+                                       st.qsl.numpy(), st.ctx.numpy(), st.scale, 600, 2, 16)
+    err = np.abs(t["out"].double().cpu().numpy() - ref)
+    ok = err <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -12) * mag
+    assert ok[:200].all() and ok[500:].all()
+    t = st.to_dev()
+    t["qsl"][:] = torch.tensor([0, 200, 0, 651, 651], dtype=torch.int32, device=DEV)
+    t["qsl"][1:4] = torch.tensor([651, 0, 651], dtype=torch.int32, device=DEV)
+    t["ctx"][:] = 0
+    t["seq"][:] = torch.tensor([651, 1, 651, 0], dtype=torch.int32, device=DEV)
+    t["table"] = t["table"].clamp_(min=0).repeat(1, 4).contiguous()
+    st.call(t)
+    torch.cuda.synchronize()
+    assert pk.read_device_status(clear=True) & pk.PA_DEV_PLAN_OVERFLOW
+    assert torch.all(t["out"] == 7.0)
