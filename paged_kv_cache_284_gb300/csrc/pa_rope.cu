@@ -87,6 +87,14 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
     return d;
 }
 
+// a b + c rounded down.  A remainder is exact in any rounding; rounded down, an
+// exact zero is -0, and -0 added to a zero leaves that zero its sign.
+__device__ __forceinline__ uint64_t f2_fma_down(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rm.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 // A cache row's scale s and r = 1 / s (rounded to nearest).
 struct Scale {
     float s, r;
@@ -102,7 +110,7 @@ __device__ __forceinline__ Scale make_scale(float s) {
 // rounded quotient when r is the rounded reciprocal and the quotient before is
 // within one unit in the last place.  Quotients past 512 (infinities, whose
 // remainder is no number) go the plain way; those whose remainder is subnormal
-// have the code of zero; NaN stays NaN.
+// have the code of zero, signed as x is; so has -0 (f2_fma_down); NaN stays NaN.
 __device__ __forceinline__ uint2 pack8_e4m3(const uint64_t (&x)[4], const Scale &sc) {
     const uint64_t r2 = f2_pack(sc.r, sc.r), s2 = f2_pack(-sc.s, -sc.s);
     uint64_t q[4];
@@ -116,8 +124,8 @@ __device__ __forceinline__ uint2 pack8_e4m3(const uint64_t (&x)[4], const Scale 
     if (sc.plain && most < 512.f) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            q[i] = f2_fma(f2_fma(q[i], s2, x[i]), r2, q[i]);
-            q[i] = f2_fma(f2_fma(q[i], s2, x[i]), r2, q[i]);
+            q[i] = f2_fma(f2_fma_down(q[i], s2, x[i]), r2, q[i]);
+            q[i] = f2_fma(f2_fma_down(q[i], s2, x[i]), r2, q[i]);
             f2_unpack(q[i], lo[i], hi[i]);
         }
     } else {

@@ -255,3 +255,43 @@ def test_binding_takes_plain_calls_and_leaves_the_others():
     assert pk.lib().pa_kernel_launches() == before
     with pytest.raises((TypeError, ValueError)):
         pk.pa_rope_write_kv(*good[:3], pos.long(), *good[4:10])
+
+
+# Scales: ordinary, both sides of 2^-60 and 2^60, where the quotient is taken another
+# way, and the ends of fp32.
+@pytest.mark.parametrize("scales", [(1.0, 0.0371), (2.0 ** -59, 1.7 * 2.0 ** 59),
+                                    (2.0 ** -61, 1.3 * 2.0 ** 61), (0.3, 7.0 / 3.0),
+                                    (2.0 ** -126, 3.0e38), (1.1e-5, 450.7)])
+@pytest.mark.parametrize("adjacent", [False, True])
+def test_every_bf16_value_gets_the_code_of_pa_write_kv(scales, adjacent):
+    """All 65536 bit patterns (zeros of both signs, subnormals, infinities, NaN) as
+    values and as unrotated key elements, at two scales: the same codes, bit for bit."""
+    T, hkv, d, bs, rot = 592, 2, 128, 16, 16
+    every = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    # 112 unrotated elements a head: 592 tokens hold every pattern
+    rows = torch.zeros(T * (d - rot), dtype=torch.bfloat16)
+    rows[:65536] = every
+    x = torch.zeros(T, hkv, d, dtype=torch.bfloat16)
+    x[:, :, rot:] = rows.view(T, 1, d - rot)
+    x[:, :, :rot] = x[:, :, rot:2 * rot]
+    k, v = x.clone(), x
+    k[:, :, :rot] = 0.5
+    slots = torch.randperm(T, generator=torch.Generator().manual_seed(1))
+    k, v, slots = k.to(DEV), v.to(DEV), slots.to(DEV)
+    ks = torch.tensor(scales, dtype=torch.float32, device=DEV)
+    vs = ks.flip(0).contiguous()
+    new, want = ([torch.full((T // bs, hkv, bs, d), 0x11, dtype=torch.uint8, device=DEV)
+                  for _ in "kv"] for _ in range(2))
+    pos = torch.zeros(T, dtype=torch.int32, device=DEV)
+    freq = torch.ones(rot // 2, dtype=torch.float64, device=DEV)
+    pk.pa_rope_write_kv(None, k, v, pos, freq, None, slots, *new, None, adjacent=adjacent,
+                        k_scale=ks, v_scale=vs)
+    pk.pa_write_kv(k, v, slots, *want, k_scale=ks, v_scale=vs)
+    torch.cuda.synchronize()
+    for name, a, b in (("k", new[0], want[0]), ("v", new[1], want[1])):
+        wrong = (a != b).nonzero()
+        assert len(wrong) == 0, (name, len(wrong), wrong[:4].tolist(), a[a != b][:4].tolist(),
+                                 b[a != b][:4].tolist())
+    # (an e4m3 zero keeps its sign: both codes appear)
+    assert (want[1] == 0x80).any() and (want[1] == 0x00).any()
+    assert_status_clean()
