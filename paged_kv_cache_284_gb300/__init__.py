@@ -195,6 +195,13 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _int32(x) -> int:
+    """x as an int32 of the C ABI, where ctypes would wrap it: a window or a count
+    past the range keeps its meaning (more than any request has), a negative one
+    is refused as -1 is."""
+    return max(-1, min(int(x), 2**31 - 1))
+
+
 def _need(t: torch.Tensor, name: str, dtype, device=True):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -432,8 +439,8 @@ def pa_window_attention(q, k_cache, v_cache, block_tables, query_start_loc, cont
                          "seq_lens [B] must agree")
     L = lib()
     args = (q.data_ptr(), kv, block_tables.data_ptr(), tables[1], query_start_loc.data_ptr(),
-            context_lens.data_ptr(), seq_lens.data_ptr(), B, T, hq, scale, int(window),
-            int(num_sinks), out.data_ptr(), None if lse is None else lse.data_ptr())
+            context_lens.data_ptr(), seq_lens.data_ptr(), B, T, hq, scale, _int32(window),
+            _int32(num_sinks), out.data_ptr(), None if lse is None else lse.data_ptr())
     handle = _raw_stream(stream, dev)
     staged = staging_blocks > 0 and kv.kv_dtype == PA_KV_FP8_E4M3
     if workspace is not None and not staged:
@@ -657,7 +664,7 @@ def pa_validate_metadata(block_tables, query_start_loc, context_lens, seq_lens, 
     if window is not None:
         _check(lib().pa_validate_window_metadata(
             _ptr(bt), int(bt.shape[1]), _ptr(qsl), _ptr(ctx), _ptr(sl), int(sl.shape[0]), T,
-            int(window), int(num_sinks), _ptr(sm), int(num_blocks), int(block_size)),
+            _int32(window), _int32(num_sinks), _ptr(sm), int(num_blocks), int(block_size)),
             "pa_validate_window_metadata")
         return
     _check(lib().pa_validate_metadata(_ptr(bt), int(bt.shape[1]), _ptr(qsl), _ptr(ctx), _ptr(sl),

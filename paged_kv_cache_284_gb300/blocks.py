@@ -7,7 +7,7 @@ from typing import Dict, List, Optional, Sequence
 
 import numpy as np
 
-from . import PaError, _STATUS, PA_OK, lib
+from . import PaError, _STATUS, PA_OK, _int32 as _c_int32, lib
 
 
 def _i32(a) -> np.ndarray:
@@ -65,18 +65,18 @@ class BlockManager:
         """Give back the blocks no later row of the request can see under
         pa_window_attention(window, num_sinks); returns how many."""
         n = ctypes.c_int32(0)
-        self._check(lib().pa_bm_release_window(self._h, int(req_id), int(window), int(num_sinks),
-                                               ctypes.byref(n)), "pa_bm_release_window")
+        self._check(lib().pa_bm_release_window(self._h, int(req_id), _c_int32(window),
+                                               _c_int32(num_sinks), ctypes.byref(n)), "pa_bm_release_window")
         return n.value
 
     def compact(self, max_moves: Optional[int] = None) -> np.ndarray:
         """Move the used blocks to the pool's lower end; returns the (src, dst)
         moves, which pa_copy_blocks has to make before the next step."""
-        if max_moves is None:
-            max_moves = self.num_blocks
-        moves = np.empty((max(int(max_moves), 1), 2), np.int32)
+        # (there are never more moves than blocks)
+        most = self.num_blocks if max_moves is None else _c_int32(min(max_moves, self.num_blocks))
+        moves = np.empty((max(most, 1), 2), np.int32)
         n = ctypes.c_int32(0)
-        self._check(lib().pa_bm_compact(self._h, int(max_moves), _ptr(moves), ctypes.byref(n)),
+        self._check(lib().pa_bm_compact(self._h, most, _ptr(moves), ctypes.byref(n)),
                     "pa_bm_compact")
         return moves[:n.value].copy()
 

@@ -586,3 +586,17 @@ def test_a_step_without_a_plan_skips_bad_and_overlapping_requests():
     torch.cuda.synchronize()
     assert pk.read_device_status(clear=True) & pk.PA_DEV_PLAN_OVERFLOW
     assert torch.all(t["out"] == 7.0)
+
+
+@pytest.mark.parametrize("window,sinks", [(2**32 + 3, 0), (2**70, 2**32), (1, 2**32 + 1),
+                                          (2**31 - 1, 2**31 - 1)])
+def test_windows_and_sinks_past_int32_see_every_key(window, sinks):
+    st = Step(DECODE + [(33, 5)], 8, 2, 128, 16, 10 ** 6, 0)
+    t = st.to_dev()
+    st.window, st.sinks = window, sinks
+    st.call(t)
+    st.call(t, workspace=pk.alloc_workspace(1 << 26, DEV))   # (a kept one)
+    torch.cuda.synchronize()
+    st.window, st.sinks = 10 ** 6, 0
+    st.check(t)
+    assert_status_clean()

@@ -312,3 +312,61 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         pk.pa_copy_blocks(pk.kv_layers([], []), i.long())
     with pytest.raises(ValueError):
         pk.pa_copy_blocks(pk.kv_layers([], []), i)
+
+
+# ---- numbers past int32 ------------------------------------------------------------
+
+@pytest.mark.parametrize("window,sinks,gone", [
+    (2**32 + 1, 0, 0), (2**40, 0, 0), (2**63, 0, 0), (1, 2**32, 0), (1, 2**70, 0), (1, 0, 9)])
+def test_release_window_with_numbers_past_int32(window, sinks, gone):
+    """A window or sinks past any request's keys hide nothing, whatever their low 32
+    bits are."""
+    bm = BlockManager(16, 4)
+    bm.add_request(1, [5])
+    bm.append_tokens(1, [1] * 37)
+    bm.schedule([1], [38], 64)
+    assert bm.release_window(1, window, sinks) == gone
+    assert bm.blocks_of(1).count(-1) == gone
+
+
+@pytest.mark.parametrize("window,sinks", [(-2**32 + 5, 0), (5, -2**32 + 5), (-2**70, 0), (2**32, -1)])
+def test_negative_numbers_past_int32_are_refused(window, sinks):
+    bm = BlockManager(16, 4)
+    bm.add_request(1, [5])
+    with pytest.raises(pk.PaError) as e:
+        bm.release_window(1, window, sinks)
+    assert e.value.code == pk.PA_ERR_INVALID_ARG
+    t = [torch.tensor(x, dtype=torch.int32) for x in ([[0]], [0, 1], [0], [1])]
+    with pytest.raises(pk.PaError) as e:
+        pk.pa_validate_metadata(*t, num_blocks=4, block_size=16, window=window, num_sinks=sinks)
+    assert e.value.code == pk.PA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("window,sinks", [(2**32 + 1, 0), (2**40, 0), (1, 2**32 + 16), (1, 2**70)])
+def test_window_metadata_with_numbers_past_int32(window, sinks):
+    """Every block of a request of 51 tokens is visible then, -1 entries are not."""
+    kw = dict(num_blocks=4, block_size=16, window=window, num_sinks=sinks)
+    rest = [torch.tensor(x, dtype=torch.int32) for x in ([0, 1], [50], [51])]
+    pk.pa_validate_metadata(torch.tensor([[0, 1, 2, 3]], dtype=torch.int32), *rest, **kw)
+    with pytest.raises(pk.PaError) as e:
+        pk.pa_validate_metadata(torch.tensor([[0, -1, 2, 3]], dtype=torch.int32), *rest, **kw)
+    assert e.value.code == pk.PA_ERR_BAD_METADATA
+
+
+def test_compact_with_numbers_past_int32():
+    def pool():
+        bm = BlockManager(8, 4)
+        for rid in (1, 2):
+            bm.add_request(rid, [rid] * 4)
+            bm.schedule([rid], [4], 8)
+        bm.append_tokens(2, [7] * 4)
+        bm.schedule([2], [4], 8)
+        bm.free_request(1)
+        bm.add_request(3, [9] * 4)
+        return bm
+    for most in (2**32 + 3, 2**70):
+        assert pool().compact(most).tolist() == pool().compact().tolist()
+    for most in (-2**32 + 3, -2**70, -1):
+        with pytest.raises(pk.PaError) as e:
+            pool().compact(most)
+        assert e.value.code == pk.PA_ERR_INVALID_ARG
