@@ -588,8 +588,10 @@ def pa_copy_blocks(layers: KVLayers, pairs, stream=None):
 
 
 def pa_validate_copies(pairs, num_blocks):
-    """Host-side check of pa_copy_blocks' pairs.  Raises PaError on a problem."""
+    """Host-side check of pa_copy_blocks' pairs [n, 2].  Raises PaError on a problem."""
     p = torch.as_tensor(pairs, dtype=torch.int32).detach().cpu().contiguous()
+    if p.numel() and (p.dim() != 2 or p.shape[1] != 2):
+        raise ValueError("pairs must be [n, 2]")
     _check(lib().pa_validate_copies(_ptr(p) if p.numel() else None, int(p.shape[0]),
                                     int(num_blocks)), "pa_validate_copies")
 

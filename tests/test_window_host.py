@@ -370,3 +370,18 @@ def test_compact_with_numbers_past_int32():
         with pytest.raises(pk.PaError) as e:
             pool().compact(most)
         assert e.value.code == pk.PA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("pairs", [torch.tensor([1, 2, 3, 4]), torch.tensor([[1], [2], [3]]),
+                                   torch.tensor([[1, 2, 0], [3, 4, 0]]), torch.zeros(1, 2, 2),
+                                   torch.tensor(3), [5, 6]])
+def test_validate_copies_refuses_what_is_no_list_of_pairs(pairs):
+    """(A flat list or one column holds fewer than two numbers a row.)"""
+    with pytest.raises(ValueError, match="pairs"):
+        pk.pa_validate_copies(pairs, 10)
+
+
+@pytest.mark.parametrize("pairs", [[], torch.empty(0, 2, dtype=torch.int32), [[1, 2], [3, 4]],
+                                   np.array([[0, 9]], np.int64)])
+def test_validate_copies_takes_pairs(pairs):
+    pk.pa_validate_copies(pairs, 10)
