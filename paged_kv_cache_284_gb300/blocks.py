@@ -122,10 +122,13 @@ class BlockManager:
         return int(lib().pa_bm_block_ref_count(self._h, int(block)))
 
     def blocks_of(self, req_id: int) -> Optional[List[int]]:
-        cap = self.num_blocks
-        out = np.empty(cap, np.int32)
-        k = int(lib().pa_bm_request_blocks(self._h, int(req_id), _ptr(out), cap))
-        return None if k < 0 else out[:k].tolist()
+        # (a table whose blocks were given back may be longer than the pool)
+        k = int(lib().pa_bm_request_blocks(self._h, int(req_id), None, 0))
+        if k < 0:
+            return None
+        out = np.empty(max(k, 1), np.int32)
+        lib().pa_bm_request_blocks(self._h, int(req_id), _ptr(out), k)
+        return out[:k].tolist()
 
     def num_computed(self, req_id: int) -> int:
         return int(lib().pa_bm_num_computed(self._h, int(req_id)))

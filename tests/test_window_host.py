@@ -385,3 +385,20 @@ def test_validate_copies_refuses_what_is_no_list_of_pairs(pairs):
                                    np.array([[0, 9]], np.int64)])
 def test_validate_copies_takes_pairs(pairs):
     pk.pa_validate_copies(pairs, 10)
+
+
+def test_blocks_of_a_stream_longer_than_the_pool():
+    """200 tokens through a pool of 6 blocks of 4: the whole table, given back
+    entries and the last blocks alike."""
+    m, bm = BlockManagerModel(6, 4), BlockManager(6, 4)
+    for x in (m, bm):
+        x.add_request(1, [5])
+    for i in range(50):
+        advance(m, bm, 1, 4 if i else 3)
+        assert bm.release_window(1, 7, 2) == m.release_window(1, 7, 2)[1]
+        same(m, bm)
+    table = bm.blocks_of(1)
+    assert len(table) == 50 and table[0] >= 0 and table[-1] >= 0 and table.count(-1) == 47
+    assert bm.blocks_of(2) is None
+    bm.add_request(2, [1])
+    assert bm.blocks_of(2) == []
