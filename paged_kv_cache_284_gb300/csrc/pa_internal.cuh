@@ -585,7 +585,9 @@ __device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity) {
 
 // Clusters ---------------------------------------------------------------------
 // Barrier over the cluster's threads; what they wrote before it is seen after it.
+// (.aligned: a warp's lanes execute it together, so they meet first.)
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }

@@ -731,6 +731,7 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
                     ok = false;
                     break;
                 }
+                __syncwarp();  // (lanes zero different numbers of pieces)
                 tmem_wait_st();
                 if (zeroed) fence_proxy_async_smem();
                 tc_fence_before();
@@ -768,6 +769,7 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
 #pragma unroll
             for (int qd = 0; qd < D / 32; ++qd) {
                 uint32_t raw[32];
+                __syncwarp();  // (lanes without a row have not written the piece before)
                 tmem_ld32(t_lane + G::kColO + qd * 32, raw);
                 tmem_wait_ld();
                 if (qd == D / 32 - 1) {

@@ -600,3 +600,19 @@ def test_windows_and_sinks_past_int32_see_every_key(window, sinks):
     st.window, st.sinks = 10 ** 6, 0
     st.check(t)
     assert_status_clean()
+
+
+@pytest.mark.parametrize("group,n", [(1, 1), (1, 3), (3, 1), (5, 3), (7, 1), (15, 1)])
+@pytest.mark.parametrize("window,sinks", [(40, 1), (700, 5), (3000, 0)])
+def test_clusters_fold_an_odd_number_of_rows(group, n, window, sinks):
+    """At head_dim 64 an odd number of rows leaves a warp of the fold half idle; few jobs,
+    so that clusters of 2, 4 and 8 CTAs share them."""
+    assert group * n % 2 == 1
+    st = Step([(3500, n), (90, n), (2100, n)], group, 1, 64, 16, window, sinks, seed=group)
+    t = st.run_and_check()
+    first = t["out"].clone()
+    for _ in range(5):
+        st.call(t)
+    torch.cuda.synchronize()
+    assert torch.equal(t["out"], first)
+    assert_status_clean()
