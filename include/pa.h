@@ -468,10 +468,15 @@ int pa_set_profile_events(int32_t which, void *start_event, void *end_event);
  *                             the first grid launched.  All work is done
  *                             and the result is right; only the wait times
  *                             out.
+ *   PA_TEST_STALL_TENSOR_CORE in every later tensor-core launch of a windowed
+ *                             step, CTA 0 loads one tile of keys: whoever
+ *                             waits for the next one times out.  The step's
+ *                             result is then incomplete.
  * Process-wide, read at launch time; set it from one thread, with no call
  * of this library in flight on the host.
  */
-enum { PA_TEST_STALL_NONE = 0, PA_TEST_STALL_SPLIT_KV = 1, PA_TEST_STALL_LAST_GRID = 2 };
+enum { PA_TEST_STALL_NONE = 0, PA_TEST_STALL_SPLIT_KV = 1, PA_TEST_STALL_LAST_GRID = 2,
+       PA_TEST_STALL_TENSOR_CORE = 3 };
 int pa_set_test_stall(int32_t which);
 
 /*

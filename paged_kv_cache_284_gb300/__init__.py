@@ -689,7 +689,8 @@ def partition_requests(seq_lens, num_ranks: int):
     return rank_of.tolist(), loads[:int(num_ranks)].tolist()
 
 
-PA_TEST_STALL_NONE, PA_TEST_STALL_SPLIT_KV, PA_TEST_STALL_LAST_GRID = 0, 1, 2
+(PA_TEST_STALL_NONE, PA_TEST_STALL_SPLIT_KV, PA_TEST_STALL_LAST_GRID,
+ PA_TEST_STALL_TENSOR_CORE) = range(4)
 
 
 def set_test_stall(which: int):

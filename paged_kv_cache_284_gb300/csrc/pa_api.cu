@@ -820,6 +820,7 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
         lp.scale_log2 = sp.scale_log2;
         lp.prefix_mode = 0;
         if (win) lp.win = *win;
+        lp.test_stall = stall == PA_TEST_STALL_TENSOR_CORE ? 1 : 0;
         if (own_plans) {
             lp.own_seqs = num_seqs;
             lp.own_max_keys = direct.max_keys;
@@ -1551,8 +1552,7 @@ int pa_set_tile_counter(uint64_t *counter) {
 
 int pa_set_test_stall(int32_t which) {
     g_err[0] = 0;
-    if (which != PA_TEST_STALL_NONE && which != PA_TEST_STALL_SPLIT_KV &&
-        which != PA_TEST_STALL_LAST_GRID)
+    if (which < PA_TEST_STALL_NONE || which > PA_TEST_STALL_TENSOR_CORE)
         return fail(PA_ERR_INVALID_ARG, "unknown test stall %d", which);
     g_test_stall.store(which, std::memory_order_relaxed);
     return PA_OK;

@@ -261,6 +261,7 @@ struct LongParams {
     int overlap_prev;
     // windowed step without a plan: its requests, and the longest that a table holds
     int own_seqs, own_max_keys;
+    int test_stall;  // test hook, windowed step only: CTA 0's K loads stop after one tile
     WindowArgs win;  // windowed step only
 };
 

@@ -233,8 +233,7 @@ __device__ __forceinline__ WinItem queue_next(const LongParams &p, const Queue &
             *q.published = k + 1;
         }
     }
-    __syncwarp();
-    if (*q.abort) it.nt = 0;
+    if (__any_sync(0xffffffffu, *q.abort)) it.nt = 0;
     return it;
 }
 // Any other warp, all lanes: item k (nt = 0: no more, or aborted).
@@ -310,6 +309,12 @@ __device__ void produce(const LongParams &p, const Queue &q, int n_items, const 
             }
             const int slot = t % kRing;
             if (t >= kRing && !warp_wait(&empty[slot], (t / kRing - 1) & 1, q.abort)) {
+                ok = false;
+                break;
+            }
+            // test hook: stop after the first tile, as a producer would whose wait
+            // had run out
+            if (p.test_stall && tmq && blockIdx.x == 0 && t == 1) {
                 ok = false;
                 break;
             }
@@ -477,18 +482,21 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
         for (; ok; ++k_item) {
             const int nt = __shfl_sync(0xffffffffu, queue_item(queue, warp, k_item).nt, 0);
             if (nt == 0) break;
-            if (!mbar_wait(&bars->q_full, k_item & 1, abort_flag)) { ok = false; break; }
+            // Every lane polls for itself, with no broadcast between a barrier and the
+            // MMAs.  One lane may find the barrier complete and another that the CTA has
+            // given up, so the warp votes: all go on or none does, or they would wait for
+            // each other at the next point where a warp meets.
+            const bool q_here = mbar_wait(&bars->q_full, k_item & 1, abort_flag);
             int j = 0;
             for (; j < nt; ++j) {
                 const uint32_t tt = t + j;
                 const int ks = tt % kRing;
                 const int sb = tt & 1;
-                if (!mbar_wait(&bars->k_full[ks], (tt / kRing) & 1, abort_flag)) { ok = false; break; }
-                if (tt >= 2 && !mbar_wait(&bars->s_free[sb], ((tt - 2) >> 1) & 1, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                __syncwarp();
+                const bool here =
+                    q_here && mbar_wait(&bars->k_full[ks], (tt / kRing) & 1, abort_flag) &&
+                    (tt < 2 || mbar_wait(&bars->s_free[sb], ((tt - 2) >> 1) & 1, abort_flag));
+                ok = __all_sync(0xffffffffu, here);
+                if (!ok) break;
                 tc_fence_after();
                 const uint64_t kd = k_desc + static_cast<uint32_t>(ks * (G::kKVBytes >> 4));
 #pragma unroll
@@ -506,9 +514,8 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
                 atomicAdd(p.tile_counter, static_cast<unsigned long long>(j));
             t += nt;
         }
-        if (!ok || *abort_flag) {
+        if (__any_sync(0xffffffffu, !ok || *abort_flag)) {
             // let every MMA already issued finish before TMEM is released
-            __syncwarp();
             commit(elected, &bars->drain);
             mbar_drain(&bars->drain, 0);
         }
@@ -527,15 +534,14 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
             for (int j = 0; j < nt; ++j) {
                 const uint32_t tt = t + j;
                 const int sb = tt & 1;
-                if (j == 0 && k_item > 0 &&
-                    !mbar_wait(&bars->o_free, (k_item - 1) & 1, abort_flag)) {
-                    ok = false;
-                    break;
-                }
                 const int vs = tt % kRing;
-                if (!mbar_wait(&bars->v_full[vs], (tt / kRing) & 1, abort_flag)) { ok = false; break; }
-                if (!mbar_wait(&bars->p_full[sb], (tt >> 1) & 1, abort_flag)) { ok = false; break; }
-                __syncwarp();
+                const bool here =
+                    (j > 0 || k_item == 0 ||
+                     mbar_wait(&bars->o_free, (k_item - 1) & 1, abort_flag)) &&
+                    mbar_wait(&bars->v_full[vs], (tt / kRing) & 1, abort_flag) &&
+                    mbar_wait(&bars->p_full[sb], (tt >> 1) & 1, abort_flag);
+                ok = __all_sync(0xffffffffu, here);  // (see the other issuer)
+                if (!ok) break;
                 tc_fence_after();
                 const uint64_t vd = v_desc + static_cast<uint32_t>(vs * (G::kKVBytes >> 4));
                 // P (bf16) of this tile: row r in TMEM lane r, key k in column k / 2
@@ -549,8 +555,7 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
             }
             t += nt;
         }
-        if (!ok || *abort_flag) {
-            __syncwarp();
+        if (__any_sync(0xffffffffu, !ok || *abort_flag)) {
             commit(elected, &bars->drain_pv);
             mbar_drain(&bars->drain_pv, 0);
         }

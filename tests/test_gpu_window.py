@@ -8,6 +8,8 @@ out by at most 2^-8 sum_j p_j |v_j|; scores and sums in fp32 add less than
 2^-12 of that sum (a score of 128 products has an error below
 128 * 2^-24 * scale * sum |q k| < 2^-13 for the inputs here; the normaliser as
 much).  lse inherits the scores' error, 2^-13, and fp32's own 2^-22 of it."""
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -615,4 +617,41 @@ def test_clusters_fold_an_odd_number_of_rows(group, n, window, sinks):
         st.call(t)
     torch.cuda.synchronize()
     assert torch.equal(t["out"], first)
+    assert_status_clean()
+
+
+def stalled(st):
+    """The step with keys that never come: its tensors, seconds and status."""
+    t = st.to_dev()
+    torch.cuda.synchronize()
+    pk.set_test_stall(pk.PA_TEST_STALL_TENSOR_CORE)
+    try:
+        t0 = time.perf_counter()
+        st.call(t)
+        torch.cuda.synchronize()
+        seconds = time.perf_counter() - t0
+    finally:
+        pk.set_test_stall(pk.PA_TEST_STALL_NONE)
+    return t, seconds, pk.read_device_status(clear=True)
+
+
+STALLED = [("bf16", 128, [(300, 400), (5, 1), (700, 200)]),              # no plan
+           ("bf16", 64, [(300, 400), (5, 1), (700, 200)]),
+           ("bf16", 128, [(300, 400), (700, 60)] + [(50, 9)] * 8),       # planned
+           ("bf16", 64, [(900, 1000), (700, 60)] + [(2900, 9)] * 10),    # side by side
+           ("e4m3", 128, [(300, 400), (700, 60), (5, 1)])]               # staged
+
+
+@pytest.mark.parametrize("kv,d,requests", STALLED)
+def test_a_prompt_kernel_whose_keys_never_come_returns(kv, d, requests):
+    """The wait for CTA 0's second tile of keys runs out (2 s a grid): every role gives
+    up, and the next call is right."""
+    st = Step(requests, 32, 8, d, 16, 2500, 4, kv=kv, seed=d)
+    t, seconds, _ = stalled(st)
+    assert 1.5 < seconds < 60.0, seconds
+    t["out"].fill_(7.0)
+    t["lse"].fill_(7.0)
+    st.call(t)
+    torch.cuda.synchronize()
+    st.check(t)
     assert_status_clean()
