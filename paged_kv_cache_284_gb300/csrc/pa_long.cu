@@ -697,10 +697,11 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
         }
     }
 
-    if (*abort_flag && threadIdx.x == 0) flag_status(p.status, PA_DEV_WAIT_TIMEOUT);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // (after the barrier: thread 0's warp may be done long before another's wait runs out)
+    if (*abort_flag && threadIdx.x == 0) flag_status(p.status, PA_DEV_WAIT_TIMEOUT);
     if (warp == 1) tmem_dealloc(tmem, G::kTmemCols);
     // with overlap_prev: this grid completes only after the split-KV grid it
     // overlapped, so later work on the stream is still ordered after both

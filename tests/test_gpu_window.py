@@ -655,3 +655,11 @@ def test_a_prompt_kernel_whose_keys_never_come_returns(kv, d, requests):
     torch.cuda.synchronize()
     st.check(t)
     assert_status_clean()
+
+
+@pytest.mark.parametrize("kv,d,requests", STALLED)
+def test_a_prompt_kernel_whose_keys_never_come_flags_it(kv, d, requests):
+    """The warp that loads keys has left when the others' waits run out: the status says
+    so all the same."""
+    _, _, status = stalled(Step(requests, 32, 8, d, 16, 2500, 4, kv=kv, seed=d))
+    assert status == pk.PA_DEV_WAIT_TIMEOUT
