@@ -1282,6 +1282,7 @@ int pa_rope_write_kv(const void *q, int64_t q_stride, const void *k, int64_t k_s
     p.num_axes = rope->num_axes;
     p.adjacent = rope->adjacent;
     p.attn_factor = rope->attn_factor;
+    p.test_stall = g_test_stall.load(std::memory_order_relaxed) == PA_TEST_STALL_ROPE ? 1 : 0;
     p.status = dev->status;
     rc = launch_rope_write(p, dev->sms, static_cast<cudaStream_t>(stream));
     return rc == PA_OK ? PA_OK : fail(rc, "rope_write_kv launch failed");
@@ -1552,7 +1553,7 @@ int pa_set_tile_counter(uint64_t *counter) {
 
 int pa_set_test_stall(int32_t which) {
     g_err[0] = 0;
-    if (which < PA_TEST_STALL_NONE || which > PA_TEST_STALL_TENSOR_CORE)
+    if (which < PA_TEST_STALL_NONE || which > PA_TEST_STALL_ROPE)
         return fail(PA_ERR_INVALID_ARG, "unknown test stall %d", which);
     g_test_stall.store(which, std::memory_order_relaxed);
     return PA_OK;

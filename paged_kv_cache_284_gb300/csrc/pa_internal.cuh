@@ -321,6 +321,7 @@ struct RopeParams {
     int rot_dim, num_axes, adjacent, fp8;
     float attn_factor;
     int64_t num_slots;  // num_blocks * block_size
+    int test_stall;  // test hook: CTA 0's first warp does not fetch its second item
     unsigned *status;
 };
 

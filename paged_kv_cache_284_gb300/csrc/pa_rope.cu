@@ -231,7 +231,9 @@ __global__ void __launch_bounds__(32 * kRopeWarps, kRopeCtas)
     const uint64_t policy = evict_first_policy();
     // Brings an item's rows into ring entry `e` (lane 0): up to three runs of
     // heads; a token that is not stored needs q alone.
+    const bool stall = p.test_stall && me == 0;
     auto fetch = [&](const Cursor &c, int n, int e) {
+        if (stall && e > 0) return;
         const int h0 = c.step * per_step, h1 = min(heads, h0 + n * per_step);
         const int64_t sl = h1 > first_k ? __ldg(p.slots + c.t) : 0;
         const bool stored = sl >= 0 && sl < p.num_slots;

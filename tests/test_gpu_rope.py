@@ -4,6 +4,8 @@ Tolerances: one rounding to bf16 (2^-8 of the value), or to e4m3 (2^-4 of the
 code's value, half the subnormal step 2^-10 below that); the fp32 rotation
 adds at most |f| (|a| + |b|) 2^-21 (cos and sin good to 2^-22, three fp32
 roundings of 2^-24 each).  v and the unrotated elements are exact in bf16."""
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -295,3 +297,27 @@ def test_every_bf16_value_gets_the_code_of_pa_write_kv(scales, adjacent):
     # (an e4m3 zero keeps its sign: both codes appear)
     assert (want[1] == 0x80).any() and (want[1] == 0x00).any()
     assert_status_clean()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_rows_that_never_come_time_out(kv):
+    """The first warp's second item is not fetched: its wait runs out (2 s), the status
+    says so, the rows before it are written, and the next call is right."""
+    s = make(2500, 32, 8, 128, 128, 16, axes=3, kv=kv, seed=10)
+    t = to_dev(s)
+    torch.cuda.synchronize()
+    pk.set_test_stall(pk.PA_TEST_STALL_ROPE)
+    try:
+        t0 = time.perf_counter()
+        q_out = call(s, t)
+        torch.cuda.synchronize()
+        seconds = time.perf_counter() - t0
+    finally:
+        pk.set_test_stall(pk.PA_TEST_STALL_NONE)
+    assert 1.5 < seconds < 60.0, seconds
+    assert pk.read_device_status(clear=True) == pk.PA_DEV_WAIT_TIMEOUT
+    whole = call(s, to_dev(s))
+    lost = (q_out != whole).flatten(1).any(1).nonzero().flatten().tolist()
+    assert lost and max(lost) < 20, lost
+    assert torch.equal(q_out[0, 0], whole[0, 0]) and torch.all(q_out[0, -1] == 7.0)
+    check(s, t, call(s, t))
