@@ -678,10 +678,23 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
     const int stall = g_test_stall.load(std::memory_order_relaxed);
     sp.test_stall = stall == PA_TEST_STALL_SPLIT_KV ? 1 : 0;
 
+    int rc = PA_OK;
+    if (fresh && fresh->num_tokens > 0) {
+        // The step's new rows first, as pa_write_kv does: its kernel runs as a
+        // programmatic dependent ahead of the planner and is off the step's
+        // critical path.  (Writing them from copy blocks in the planner's
+        // grid measured no faster on an 8-request decode step and slower on
+        // large ones.)
+        ProfScope prof(PA_KERNEL_WRITE_KV, s);
+        rc = launch_write_kv(fresh->k, fresh->v, fresh->slots, fresh->num_tokens, kv, dev->status,
+                             s);
+        if (rc != PA_OK) return fail(rc, "write_kv launch failed");
+    }
+
     DirectParams direct{};
     if (win && direct_step(*win, num_seqs, T, kv, group, max_blocks, dev->sms, &direct)) {
         ProfScope prof(PA_KERNEL_SPLIT_KV, s);
-        const int rc = launch_window_direct(sp, maps.k, maps.v, direct, D, fp8, s);
+        rc = launch_window_direct(sp, maps.k, maps.v, direct, D, fp8, s);
         return rc == PA_OK ? PA_OK : fail(rc, "window kernel launch failed: %s",
                                           cudaGetErrorString(cudaGetLastError()));
     }
@@ -699,21 +712,9 @@ int run_step(const void *q, const pa_kv_desc *kv, const int32_t *block_tables, i
                      seen_chunks(*win, direct.piece_tokens, max_blocks, kv->block_size), dev->sms,
                      &direct);
         ProfScope prof(PA_KERNEL_SPLIT_KV, s);
-        const int rc = launch_window_direct(sp, maps.k, maps.v, direct, D, fp8, s);
+        rc = launch_window_direct(sp, maps.k, maps.v, direct, D, fp8, s);
         if (rc != PA_OK)
             return fail(rc, "window kernel launch failed: %s", cudaGetErrorString(cudaGetLastError()));
-    }
-    int rc = PA_OK;
-    if (fresh && fresh->num_tokens > 0) {
-        // The step's new rows first, as pa_write_kv does: its kernel runs as a
-        // programmatic dependent ahead of the planner and is off the step's
-        // critical path.  (Writing them from copy blocks in the planner's
-        // grid measured no faster on an 8-request decode step and slower on
-        // large ones.)
-        ProfScope prof(PA_KERNEL_WRITE_KV, s);
-        rc = launch_write_kv(fresh->k, fresh->v, fresh->slots, fresh->num_tokens, kv, dev->status,
-                             s);
-        if (rc != PA_OK) return fail(rc, "write_kv launch failed");
     }
     if (!own_plans) {
         ProfScope prof(PA_KERNEL_PLAN, s);
@@ -1090,7 +1091,7 @@ size_t pa_attention_workspace_size(int32_t num_seqs, int32_t num_q_tokens, int32
 
 namespace {
 
-// pa_attention_ex, with `fresh` the write of the step's new rows first, or with
+// pa_attention_ex, with `fresh` the write of the step's new rows first, with
 // `win` a windowed step.
 int attention_entry(const void *q, const pa_kv_desc *kv, const int32_t *block_tables,
                     int32_t max_blocks_per_seq, const int32_t *query_start_loc,
