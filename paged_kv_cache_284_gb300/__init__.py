@@ -372,6 +372,9 @@ def _explain(device: int, tensors):
                          f"cuda:{torch.cuda.current_device()}")
 
 
+_NOT_PLAIN = -1  # the direct binding: not a plain call, nothing was launched
+
+
 def _raw_stream(stream, device: int) -> int:
     # the current stream's handle without building a Stream object (1 us of a
     # small step's host time)
@@ -411,11 +414,14 @@ def pa_window_attention(q, k_cache, v_cache, block_tables, query_start_loc, cont
     blocks of the long requests).  Returns the workspace tensor used."""
     # a plain call with a kept workspace goes straight to the library; what is
     # wrong with any other (or needs a workspace) comes out below
-    if workspace is not None and staging_blocks == 0 and \
-            (_direct or _load_direct()).window_attention(
-                q, k_cache, v_cache, block_tables, query_start_loc, context_lens, seq_lens, scale,
-                window, num_sinks, out, lse, workspace, stream, k_scale, v_scale) == PA_OK:
-        return workspace
+    if workspace is not None and staging_blocks == 0:
+        rc = (_direct or _load_direct()).window_attention(
+            q, k_cache, v_cache, block_tables, query_start_loc, context_lens, seq_lens, scale,
+            window, num_sinks, out, lse, workspace, stream, k_scale, v_scale)
+        if rc == PA_OK:
+            return workspace
+        if rc != _NOT_PLAIN and rc != PA_ERR_WORKSPACE:
+            _check(rc, "pa_window_attention")
     dev = q.get_device()
     if (_off(q, _BF16, dev) or _off(out, _BF16, dev) or _off(block_tables, _I32, dev) or
             _off(query_start_loc, _I32, dev) or _off(context_lens, _I32, dev) or
@@ -481,9 +487,12 @@ def pa_rope_write_kv(q, k, v, positions, inv_freq, axis, slot_mapping, k_cache, 
     one axis); inv_freq float64 [rot_dim / 2]; axis int32 [rot_dim / 2], the
     axis of each frequency, or None for axis 0; q_out bf16 [T, Hq, d] (may be
     a contiguous q).  q and q_out may both be None."""
-    if (_direct or _load_direct()).rope_write_kv(
-            q, k, v, positions, inv_freq, axis, slot_mapping, k_cache, v_cache, q_out, adjacent,
-            attn_factor, stream, k_scale, v_scale) == PA_OK:
+    rc = (_direct or _load_direct()).rope_write_kv(
+        q, k, v, positions, inv_freq, axis, slot_mapping, k_cache, v_cache, q_out, adjacent,
+        attn_factor, stream, k_scale, v_scale)
+    if rc != _NOT_PLAIN:
+        if rc:
+            _check(rc, "pa_rope_write_kv")
         return
     dev = k.get_device()
     ks, rows = _token_rows(k, "k", dev)
@@ -568,8 +577,11 @@ def pa_copy_blocks(layers: KVLayers, pairs, stream=None):
     """Copy physical blocks in every layer: pairs int32 [n, 2] of (src, dst) on
     the device (BlockManager.schedule's copies, BlockManager.compact's moves).
     A dst appears once and is no other pair's src; negative ids are padding."""
-    if (_direct or _load_direct()).copy_blocks(layers.address, len(layers.descs), layers.device,
-                                               pairs, stream) == PA_OK:
+    rc = (_direct or _load_direct()).copy_blocks(layers.address, len(layers.descs), layers.device,
+                                                 pairs, stream)
+    if rc != _NOT_PLAIN:
+        if rc:
+            _check(rc, "pa_copy_blocks")
         return
     if pairs.dtype is not _I32:
         raise TypeError(f"pairs must be {_I32}, got {pairs.dtype}")

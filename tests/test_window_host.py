@@ -402,3 +402,46 @@ def test_blocks_of_a_stream_longer_than_the_pool():
     assert bm.blocks_of(2) is None
     bm.add_request(2, [1])
     assert bm.blocks_of(2) == []
+
+
+# ---- the direct binding's answers ---------------------------------------------------
+
+class Answers:
+    """Stands in for the direct binding: every call gives `code`."""
+
+    def __init__(self, code):
+        self.code, self.calls = code, 0
+
+    def window_attention(self, *args):
+        self.calls += 1
+        return self.code
+    rope_write_kv = copy_blocks = window_attention
+
+
+def direct_calls():
+    x = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    n = torch.zeros(3, dtype=torch.int32)
+    layers = pk.KVLayers((pk.KVDesc * 1)(), [x])
+    return {
+        "pa_window_attention": lambda: pk.pa_window_attention(
+            x, x, x, n, n, n, n, 1.0, 4, 0, x, workspace=torch.zeros(8, dtype=torch.uint8)),
+        "pa_rope_write_kv": lambda: pk.pa_rope_write_kv(x, x, x, n, n, None, n, x, x, x),
+        "pa_copy_blocks": lambda: pk.pa_copy_blocks(layers, torch.zeros(1, 2, dtype=torch.int64))}
+
+
+@pytest.mark.parametrize("name", ["pa_window_attention", "pa_rope_write_kv", "pa_copy_blocks"])
+@pytest.mark.parametrize("code", [pk.PA_ERR_INVALID_ARG, pk.PA_ERR_UNSUPPORTED, pk.PA_ERR_CUDA])
+def test_a_failed_call_is_not_made_again(monkeypatch, name, code):
+    """What the library refuses, or what fails on the device, is raised as it came."""
+    answers = Answers(code)
+    monkeypatch.setattr(pk, "_direct", answers)
+    with pytest.raises(pk.PaError) as e:
+        direct_calls()[name]()
+    assert e.value.code == code and answers.calls == 1 and name in str(e.value)
+
+
+@pytest.mark.parametrize("name", ["pa_window_attention", "pa_rope_write_kv", "pa_copy_blocks"])
+def test_calls_that_are_not_plain_reach_the_checks(monkeypatch, name):
+    monkeypatch.setattr(pk, "_direct", Answers(-1))
+    with pytest.raises((TypeError, ValueError)):     # (CPU tensors, int64 pairs)
+        direct_calls()[name]()
