@@ -279,9 +279,14 @@ def _cascade_need(kv, num_seqs, T, hq, prefix_len) -> int:
     return need
 
 
-def alloc_workspace(nbytes: int, device=None) -> torch.Tensor:
-    """Device workspace owned by torch (256-byte aligned by the allocator)."""
-    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device or "cuda")
+def alloc_workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
+    """Device workspace owned by torch (256-byte aligned by the allocator), for
+    use on `stream` (None: the current one): a caller that drops it while that
+    stream still works on it does not free it for others."""
+    workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device or "cuda")
+    if stream is not None:
+        workspace.record_stream(torch.cuda.ExternalStream(stream.cuda_stream, workspace.device))
+    return workspace
 
 
 def fp8_staging_bytes(num_kv_heads, head_dim, block_size, num_blocks) -> int:
@@ -310,7 +315,7 @@ def pa_attention(q, k_cache, v_cache, block_tables, query_start_loc, context_len
     if kv.kv_dtype == PA_KV_FP8_E4M3 and staging_blocks > 0:
         need += fp8_staging_bytes(kv.num_kv_heads, kv.head_dim, kv.block_size, staging_blocks)
     if workspace is None or workspace.numel() < need:
-        workspace = alloc_workspace(need, q.device)
+        workspace = alloc_workspace(need, q.device, stream)
     _check(lib().pa_attention_ex(_ptr(q), ctypes.byref(kv), _ptr(block_tables),
                                  int(block_tables.shape[1]), _ptr(query_start_loc),
                                  _ptr(context_lens), _ptr(seq_lens), B, T, hq, float(scale),
@@ -344,7 +349,7 @@ def pa_write_kv_attention(k, v, slot_mapping, q, k_cache, v_cache, block_tables,
     if kv.kv_dtype == PA_KV_FP8_E4M3 and staging_blocks > 0:
         need += fp8_staging_bytes(kv.num_kv_heads, kv.head_dim, kv.block_size, staging_blocks)
     if workspace is None or workspace.numel() < need:
-        workspace = alloc_workspace(need, q.device)
+        workspace = alloc_workspace(need, q.device, stream)
     _check(lib().pa_write_kv_attention(_ptr(k), _ptr(v), _ptr(slot_mapping), int(k.shape[0]),
                                        _ptr(q), ctypes.byref(kv), _ptr(block_tables),
                                        int(block_tables.shape[1]), _ptr(query_start_loc),
@@ -460,7 +465,7 @@ def pa_window_attention(q, k_cache, v_cache, block_tables, query_start_loc, cont
     if staged:
         need += L.pa_fp8_staging_bytes(kv.num_kv_heads, d, kv.block_size, int(staging_blocks))
     if workspace is None or workspace.nbytes < need:
-        workspace = alloc_workspace(need, q.device)
+        workspace = alloc_workspace(need, q.device, stream)
     _check(L.pa_window_attention(*args, workspace.data_ptr(), workspace.nbytes, handle),
            "pa_window_attention")
     return workspace
@@ -631,7 +636,7 @@ def pa_prefix_attention(q, k_cache, v_cache, prefix_blocks, prefix_len, scale, o
     T, hq, _ = q.shape
     need = _cascade_need(kv, 1, T, hq, prefix_len)
     if workspace is None or workspace.numel() < need:
-        workspace = alloc_workspace(need, q.device)
+        workspace = alloc_workspace(need, q.device, stream)
     _check(lib().pa_prefix_attention(_ptr(q), ctypes.byref(kv), _ptr(prefix_blocks),
                                      int(prefix_len), T, hq, float(scale), _ptr(out), _ptr(lse),
                                      _ptr(workspace), workspace.numel(), _stream(stream)),
@@ -655,7 +660,7 @@ def pa_cascade_decode(q, k_cache, v_cache, prefix_blocks, prefix_len, block_tabl
     B = int(seq_lens.shape[0])
     need = _cascade_need(kv, B, T, hq, prefix_len)
     if workspace is None or workspace.numel() < need:
-        workspace = alloc_workspace(need, q.device)
+        workspace = alloc_workspace(need, q.device, stream)
     _check(lib().pa_cascade_decode(_ptr(q), ctypes.byref(kv), _ptr(prefix_blocks),
                                    int(prefix_len), _ptr(block_tables), int(block_tables.shape[1]),
                                    _ptr(query_start_loc), _ptr(context_lens), _ptr(seq_lens), B,

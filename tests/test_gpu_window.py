@@ -663,3 +663,30 @@ def test_a_prompt_kernel_whose_keys_never_come_flags_it(kv, d, requests):
     so all the same."""
     _, _, status = stalled(Step(requests, 32, 8, d, 16, 2500, 4, kv=kv, seed=d))
     assert status == pk.PA_DEV_WAIT_TIMEOUT
+
+
+@pytest.mark.parametrize("call", ["pa_window_attention", "pa_attention"])
+def test_a_workspace_made_for_another_stream_is_not_handed_out_while_in_use(call):
+    """A call on a busy stream makes its workspace, and the caller drops it: the
+    allocator keeps it until that stream is done."""
+    st = Step(MIXED, 16, 4, 128, 16, 10 ** 6, 0)
+    t = st.to_dev()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    args = (t["q"], t["k"], t["v"], t["table"], t["qsl"], t["ctx"], t["seq"], st.scale)
+    if call == "pa_window_attention":
+        args += (st.window, st.sinks)
+    getattr(pk, call)(*args, t["out"], t["lse"])    # (loading a kernel waits for the device)
+    torch.cuda._sleep(1)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(int(1e9))     # about half a second
+    ws = getattr(pk, call)(*args, t["out"], t["lse"], stream=side)
+    at, size = ws.data_ptr(), ws.numel()
+    del ws
+    other = torch.empty(size, dtype=torch.uint8, device=DEV)
+    busy, other_at = not side.query(), other.data_ptr()
+    torch.cuda.synchronize()
+    assert busy and other_at != at
+    st.check(t)
+    assert_status_clean()
