@@ -194,6 +194,20 @@ constexpr int64_t kDirectRoundChunks = 16384;
 constexpr int64_t kDirectAnyRows = 256;
 constexpr int64_t kDirectE4m3Chunks = 65536;
 
+// ... and short rows alone (no request can be long) leave it when their windows are long
+// and they are few: a job gets 8 CTAs at most, while the plan's splits take every SM, with a
+// fold that grows with the rows.  More chunks a job than kDirectLongPerRow times a request's
+// rows, and than kDirectLongPerJob times the jobs, go there.  d = 128, one kernel / planned,
+// bf16: one job of 4 rows at 8192 keys 19 / 21 us, 16384 30 / 27, 32768 51 / 37, 131072 179 /
+// 71; 8 jobs at 16384 31 / 32, 32768 53 / 44, 131072 181 / 99; 16 jobs at 32768 57 / 60, 65536
+// 105 / 99; 32 at 65536 165 / 169.  One job of 8 rows at 32768 52 / 60, 131072 180 / 108; two of
+// 16 at 65536 96 / 111, 131072 182 / 121.  e4m3: one job of 4 rows at 16384 29 / 27, 131072 178 /
+// 66; 16 jobs at 16384 34 / 33, 65536 114 / 68; 32 at 32768 64 / 67.  (A table wider than its
+// requests' contexts counts in full: the host does not know the lengths.)
+constexpr int64_t kDirectLongPerRow = 256;
+constexpr int64_t kDirectLongPerJob = 192;
+constexpr int64_t kDirectLongPerJobE4m3 = 64;
+
 // True while per-kernel profiling events are set: the step then launches its
 // kernels one after the other so that each event pair times one kernel.
 bool profiling_active() {
@@ -552,6 +566,11 @@ bool direct_step(const WindowArgs &win, int num_seqs, int T, const pa_kv_desc *k
     const int64_t rows = static_cast<int64_t>(T) * group;
     const bool e4m3 = kv->kv_dtype == PA_KV_FP8_E4M3;
     const int64_t work = jobs * chunks;
+    if (rows <= kShortMaxRows &&
+        chunks > std::max(kDirectLongPerRow * ((rows + num_seqs - 1) / num_seqs),
+                          (e4m3 ? kDirectLongPerJobE4m3 : kDirectLongPerJob) * num_seqs *
+                              kv->num_kv_heads))
+        return false;
     bool any;
     if (!e4m3 && num_seqs <= kOwnPlanMaxSeqs)
         any = jobs <= sms ? work <= kDirectRoundChunks

@@ -690,3 +690,37 @@ def test_a_workspace_made_for_another_stream_is_not_handed_out_while_in_use(call
     assert busy and other_at != at
     st.check(t)
     assert_status_clean()
+
+
+def launches(st, t, **kw):
+    """Kernels that the step launches (one: the one-kernel form)."""
+    ws = st.call(t, **kw)
+    torch.cuda.synchronize()
+    before = pk.lib().pa_kernel_launches()
+    st.call(t, workspace=ws, **kw)
+    torch.cuda.synchronize()
+    return pk.lib().pa_kernel_launches() - before
+
+
+@pytest.mark.parametrize("kv,d", [("bf16", 128), ("bf16", 64), ("e4m3", 128)])
+@pytest.mark.parametrize("requests,hq,hkv,kernels", [
+    ([(17000, 1)], 4, 1, 2), ([(16000, 1)], 4, 1, 1),      # 4 rows: from 1024 chunks on
+    ([(17000, 1), (300, 1)], 8, 2, 2), ([(17000, 2)], 4, 1, 1),
+    ([(33500, 2), (20000, 2)], 4, 1, 2)])
+def test_a_few_long_jobs_are_split_over_the_whole_device(kv, d, requests, hq, hkv, kernels):
+    """Decode and verify rows that see all of a long context: plan and split-KV kernel."""
+    st = Step(requests, hq, hkv, d, 16, 10 ** 6, 0, kv=kv, seed=hkv)
+    t = st.to_dev()
+    assert launches(st, t) == kernels
+    st.check(t)
+    assert_status_clean()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_a_few_long_jobs_behind_a_gap(kv):
+    """The same with blocks between the sinks and the window given back."""
+    st = Step([(26000, 1), (25000, 1)], 4, 1, 128, 16, 18000, 37, kv=kv, seed=5)
+    t = st.to_dev()
+    assert launches(st, t) == 2
+    st.check(t)
+    assert_status_clean()
