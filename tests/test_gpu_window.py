@@ -15,7 +15,7 @@ import pytest
 import torch
 
 import paged_kv_cache_284_gb300 as pk
-from gpu_helpers import DEV, assert_status_clean
+from gpu_helpers import DEV, assert_status_clean, plan_header
 from oracle import ops
 
 pytestmark = pytest.mark.gpu
@@ -722,5 +722,115 @@ def test_a_few_long_jobs_behind_a_gap(kv):
     st = Step([(26000, 1), (25000, 1)], 4, 1, 128, 16, 18000, 37, kv=kv, seed=5)
     t = st.to_dev()
     assert launches(st, t) == 2
+    st.check(t)
+    assert_status_clean()
+
+
+# Steps whose path is asserted by what they launch: the planned kernels one after the
+# other (plan, [staging,] split-KV, tensor core) and side by side (one more tensor-core
+# grid), with blocks given back between sinks and windows.
+PROMPTS = [(2000, 150), (3100, 200), (0, 130), (1500, 90)]
+
+
+def beside(n, seed):
+    """n decode and verify rows of contexts past the windows."""
+    rng = np.random.default_rng(seed)
+    return [(int(c), int(m)) for c, m in zip(rng.integers(1300, 4000, n), rng.integers(1, 6, n))]
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (33, 17), (100, 130), (700, 5), (31, 5000)])
+@pytest.mark.parametrize("kv,d,staged", [("bf16", 128, 0), ("bf16", 64, 0), ("e4m3", 128, None)])
+def test_planned_steps_of_many_requests(kv, d, staged, window, sinks):
+    st = Step(MIXED + CHUNKS[1:] + [(900, 3), (1400, 5)], 64, 8, d, 16, window, sinks, kv=kv,
+              seed=window, pad=2)
+    assert len(st.requests) > 8 and st.total < 512
+    t = st.to_dev()
+    kw = {} if staged is None else {"staging_blocks": staged}
+    assert launches(st, t, **kw) == (3 if kv == "bf16" else 4)
+    st.check(t)
+    assert_status_clean()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("window,sinks", [(14000, 37), (9000, 0)])
+def test_planned_steps_of_many_requests_split_over_the_window(kv, window, sinks):
+    """Split-KV items cut over the packed chunks, and their fold: 64 rows at 12 requests."""
+    st = Step([(16000 - 300 * i, 8) for i in range(12)], 8, 1, 128, 16, window, sinks, kv=kv, seed=3)
+    t = st.to_dev()
+    ws = st.call(t)
+    torch.cuda.synchronize()
+    header = plan_header(ws)
+    assert header["short_items"] > 12 and header["long_items"] == 0
+    st.check(t)
+    first = t["out"].clone()
+    for _ in range(3):
+        st.call(t, workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(t["out"], first)
+    assert_status_clean()
+
+
+@pytest.mark.parametrize("window,sinks", [(1024, 5), (1200, 300), (1100, 0)])
+@pytest.mark.parametrize("kv,d,staged", [("bf16", 128, 0), ("bf16", 64, 0), ("e4m3", 128, None),
+                                         ("e4m3", 128, 90)])
+def test_side_by_side_behind_a_gap(kv, d, staged, window, sinks):
+    st = Step(PROMPTS + beside(22, window), 16, 4, d, 16, window, sinks, kv=kv, seed=window, pad=1)
+    assert st.total >= 512
+    t = st.to_dev()
+    kw = {} if staged is None else {"staging_blocks": staged}
+    assert launches(st, t, **kw) == (4 if kv == "bf16" else 5)
+    st.check(t)
+    first = t["out"].clone()
+    for _ in range(3):
+        st.call(t, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(t["out"], first)
+    assert_status_clean()
+
+
+def test_side_by_side_in_a_graph():
+    """Captured on one batch, replayed on it while its outputs are cleared, with the
+    workspace's counters as the replay before left them."""
+    st = Step(PROMPTS + beside(22, 7), 16, 4, 128, 16, 1024, 5, seed=7)
+    t = st.to_dev()
+    ws = st.call(t)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        st.call(t, workspace=ws)
+    for _ in range(3):
+        t["out"].fill_(7.0)
+        g.replay()
+    torch.cuda.synchronize()
+    st.check(t)
+    assert_status_clean()
+
+
+def test_the_last_grid_of_a_windowed_step_times_out_waiting_for_a_missing_cta():
+    st = Step(PROMPTS + beside(22, 8), 16, 4, 64, 16, 1024, 5, seed=8)
+    t = st.to_dev()
+    assert launches(st, t) == 4
+    t["out"].fill_(7.0)
+    pk.set_test_stall(pk.PA_TEST_STALL_LAST_GRID)
+    try:
+        st.call(t)
+        torch.cuda.synchronize()
+    finally:
+        pk.set_test_stall(pk.PA_TEST_STALL_NONE)
+    assert pk.read_device_status(clear=True) == pk.PA_DEV_WAIT_TIMEOUT
+    st.check(t)     # every item ran before the wait
+    assert_status_clean()
+
+
+@pytest.mark.parametrize("requests,hq,hkv,kernels", [
+    ([(500, 1)] * 3, 8, 2, 1),                                    # one kernel
+    (CHUNKS + [(300, 300)], 32, 8, 2),                            # no plan
+    ([(500, 1)] * 1025, 4, 1, 4),                                 # over 1024 requests
+    ([(500, 1)] * 3, 34, 2, 2),                                   # a group of 17
+    ([(500, 1)] * 20, 34, 2, 3)])
+def test_what_a_step_launches(requests, hq, hkv, kernels):
+    st = Step(requests, hq, hkv, 128, 16, 90, 3, seed=len(requests))
+    t = st.to_dev()
+    assert launches(st, t) == kernels
     st.check(t)
     assert_status_clean()
