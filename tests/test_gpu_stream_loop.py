@@ -141,3 +141,135 @@ def test_loop(kv, window, sinks):
     assert copied >= 1 and moved >= 1
     assert released >= 1 or window == 200
     assert_status_clean()
+
+
+@pytest.mark.parametrize("kv,window,sinks", [("bf16", 37, 4), ("e4m3", 37, 4), ("bf16", 16, 0),
+                                             ("e4m3", 200, 20), ("e4m3", 3, 1)])
+def test_loop_against_the_rows_written(kv, window, sinks):
+    """The same run of calls, with the rounding of q, k and v taken out of the comparison:
+    every new row is read back from its slot and checked against the rotation, and kept
+    with its request; attention over the kept rows, with the rotated q that the call itself
+    used, has the windowed attention's own tolerance.  A lost sink, a window off by one, a
+    block copied too late or to the wrong place changes far more than that."""
+    rng = random.Random(window + 1)
+    bm = BlockManager(NB, BS)
+    shape = (NB, HKV, BS, D)
+    fp8 = kv == "e4m3"
+    kc, vc = ([torch.full(shape, 0x7F, dtype=torch.uint8, device=DEV) if fp8 else
+               torch.full(shape, float("nan"), dtype=torch.bfloat16, device=DEV)
+               for _ in range(LAYERS)] for _ in "kv")
+    ks = vs = None
+    step_of = np.ones((HKV, 1))
+    if fp8:
+        ks, vs = (torch.tensor([0.02, 0.05], device=DEV) for _ in "kv")
+        step_of = ks.cpu().double().numpy()[:, None]
+    layers = pk.kv_layers(kc, vc)
+    inv = 1e4 ** (-torch.arange(ROT // 2, dtype=torch.float64) / (ROT // 2))
+    axis = (torch.arange(ROT // 2) % 3).to(torch.int32)
+    inv_d, axis_d = inv.to(DEV), axis.to(DEV)
+    scale = D ** -0.5
+    seqs, kept, pos_of = {}, {}, lambda p: (p, p // 7, p % 7)
+    copied = moved = released = 0
+
+    def values(pool, slots):
+        rows = pool.cpu()[slots // BS, :, slots % BS]
+        return (rows.view(torch.float8_e4m3fn) if fp8 else rows).double().numpy() * step_of
+
+    def admit(rid, n):
+        seqs[rid] = [rng.randrange(50) for _ in range(n)]
+        hits = bm.add_request(rid, seqs[rid])
+        assert hits == 0
+        kept[rid] = [([], []) for _ in range(LAYERS)]
+
+    admit(0, 75)
+    admit(1, 6)
+    admit(8, 20)
+    for step in range(24):
+        for at, src, dst in ((4, 0, 2), (4, 1, 3), (11, 2, 5)):
+            if step == at:
+                bm.fork(src, dst)
+                seqs[dst] = list(seqs[src])
+                kept[dst] = [(list(k), list(v)) for k, v in kept[src]]
+        if step in (9, 17):
+            for rid in ((8, 1) if step == 9 else (0,)):
+                bm.free_request(rid)
+                del seqs[rid], kept[rid]
+        if step == 13:
+            admit(6, 52)
+        if step in (9, 17):
+            moves = bm.compact(5)
+            pk.pa_validate_copies(moves, NB)
+            pk.pa_copy_blocks(layers, torch.from_numpy(moves).to(DEV))
+            moved += len(moves)
+        rids, new = sorted(seqs), []
+        for rid in rids:
+            done = bm.num_computed(rid)
+            if done == len(seqs[rid]):
+                t = [rng.randrange(50) for _ in range(rng.choice([1, 1, 3]))]
+                seqs[rid] += t
+                bm.append_tokens(rid, t)
+            new.append(min(len(seqs[rid]) - done, 40))
+        meta = bm.schedule(rids, new, 32)
+        if len(meta["copies"]):
+            pk.pa_copy_blocks(layers, torch.from_numpy(meta["copies"]).to(DEV))
+            copied += len(meta["copies"])
+        dev = {k: torch.from_numpy(np.ascontiguousarray(v)).to(DEV) for k, v in meta.items()}
+        place = [(rid, p) for i, rid in enumerate(rids)
+                 for p in range(meta["context_lens"][i], meta["seq_lens"][i])]
+        T = len(place)
+        positions = torch.tensor([pos_of(p) for _, p in place], dtype=torch.int32).T.contiguous()
+        how = (positions.numpy(), inv.numpy(), axis.numpy(), ROT, False)
+        slots = torch.from_numpy(meta["slot_mapping"])
+        for layer in range(LAYERS):
+            qkv = torch.stack([rows_of(seqs[r][:p + 1], layer) for r, p in place]).to(DEV)
+            q, k, v = (x.view(T, -1, D) for x in qkv.split([HQ * D, HKV * D, HKV * D], dim=1))
+            q_rot = torch.empty((T, HQ, D), dtype=torch.bfloat16, device=DEV)
+            out, lse = torch.empty_like(q_rot), torch.empty((T, HQ), device=DEV)
+            pk.pa_rope_write_kv(q, k, v, positions.to(DEV), inv_d, axis_d, dev["slot_mapping"],
+                                kc[layer], vc[layer], q_rot, k_scale=ks, v_scale=vs)
+            pk.pa_window_attention(q_rot, kc[layer], vc[layer], dev["block_tables"],
+                                   dev["query_start_loc"], dev["context_lens"], dev["seq_lens"],
+                                   scale, window, sinks, out, lse, k_scale=ks, v_scale=vs,
+                                   staging_blocks=20)
+            q64, k64, v64 = (x.double().cpu().numpy() for x in (q, k, v))
+            # one rounding to bf16, or to e4m3 of value / scale (half a step: 2^-4 of the
+            # value, 2^-10 below the normal range), and the fp32 rotation's (|a| + |b|) 2^-21
+            for name, got, want, rounds in (
+                    ("q", q_rot.double().cpu().numpy(), ops.rope(q64, *how), False),
+                    ("k", values(kc[layer], slots), ops.rope(k64, *how), fp8),
+                    ("v", values(vc[layer], slots), v64, fp8)):
+                pair = np.zeros_like(want)
+                src = {"q": q64, "k": k64}.get(name)
+                if src is not None:
+                    a, b = np.abs(src[..., :ROT // 2]), np.abs(src[..., ROT // 2:ROT])
+                    pair[..., :ROT // 2] = pair[..., ROT // 2:ROT] = (a + b) * 2.0 ** -21
+                tol = 2.0 ** -8 * np.abs(want) + pair
+                if rounds:
+                    want = np.clip(want, -448 * step_of, 448 * step_of)
+                    tol = 2.0 ** -4 * np.abs(want) + 2.0 ** -10 * step_of + pair
+                assert np.all(np.abs(got - want) <= tol), (step, layer, name)
+            k_new, v_new = values(kc[layer], slots), values(vc[layer], slots)
+            for t, (rid, p) in enumerate(place):
+                rows_k, rows_v = kept[rid][layer]
+                assert len(rows_k) == p
+                rows_k.append(k_new[t])
+                rows_v.append(v_new[t])
+            got, got_lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+            q64 = q_rot.double().cpu().numpy()
+            for i, rid in enumerate(rids):
+                L, n, at = int(meta["seq_lens"][i]), new[i], int(meta["query_start_loc"][i])
+                kd, vd = (np.concatenate([np.stack(y), np.zeros((-L % BS, HKV, D))])
+                          .reshape(-1, BS, HKV, D).transpose(0, 2, 1, 3) for y in kept[rid][layer])
+                ref, ref_l, mag = ops.window_attention(q64[at:at + n], kd, vd,
+                                                       np.arange(kd.shape[0])[None], [0, n],
+                                                       [L - n], scale, window, sinks, BS)
+                err = np.abs(got[at:at + n] - ref)
+                tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -12) * mag
+                assert np.all(err <= tol), (step, layer, rid, np.max(err / tol))
+                lerr = np.abs(got_lse[at:at + n] - ref_l)
+                assert np.all(lerr <= 2.0 ** -13 + 2.0 ** -22 * np.abs(ref_l)), (step, layer, rid)
+        for rid in rids:
+            released += bm.release_window(rid, window, sinks)
+    assert copied >= 1 and moved >= 1
+    assert released >= 1 or window == 200
+    assert_status_clean()
