@@ -135,8 +135,9 @@ int pa_write_kv(const void *k, const void *v, const int64_t *slot_mapping, int32
  * embedding of text; three (time, height, width) serve images and video,
  * with any assignment of frequencies to axes.
  *
- * The angle is reduced exactly: position and inv_freq / 2 pi meet in 64-bit
- * integer arithmetic, so far positions lose nothing.  The rotation runs in
+ * The angle is reduced modulo one turn in 64-bit integers: inv_freq / 2 pi is
+ * held to 2^-64 max(1, inv_freq) turns, so that with inv_freq of at most 1 even
+ * position 2^31 is off by no more than 2^-33 turns.  The rotation runs in
  * fp32 and is rounded once: to bf16 for q_out and a bf16 pool, and for an
  * e4m3 pool straight to the code of (rotated x) / k_scale[h], as pa_write_kv
  * rounds, without a bf16 step in between.
@@ -296,8 +297,9 @@ int pa_attention_ex(const void *q, const pa_kv_desc *kv, const int32_t *block_ta
  * even NaN.  Keys that one row sees and another does not must be finite.
  * pa_fp8_staging_bytes counts a long request's visible blocks only.
  *
- * A step of little work, or of few rows a request, runs as one kernel (counted
- * and timed as PA_KERNEL_SPLIT_KV); the workspace is asked for all the same,
+ * A step of little work, or of few rows a request (unless these are few and
+ * their windows long), runs as one kernel (counted and timed as
+ * PA_KERNEL_SPLIT_KV); the workspace is asked for all the same,
  * as the choice depends on sizes that need not stay the same between steps.
  */
 int pa_window_attention(const void *q, const pa_kv_desc *kv, const int32_t *block_tables,

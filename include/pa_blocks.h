@@ -120,7 +120,10 @@ int pa_bm_release_window(pa_block_manager *bm, int64_t req_id, int32_t window,
  * are 0 .. used - 1 or max_moves moves are made.  moves (int32
  * [max_moves][2], (src, dst)) are for pa_copy_blocks, before the next step
  * reads the pool; *num_moves receives their count.  Tables, reference counts
- * and the prefix cache follow at once.  No dst is another move's src.
+ * and the prefix cache follow at once, but not what pa_bm_schedule has already
+ * given out: a scheduled step, its copies first, is launched before the moves,
+ * and two calls' moves are copied one after the other.  Within a call no dst is
+ * another move's src.
  * PA_ERR_WORKSPACE: out of host memory.
  */
 int pa_bm_compact(pa_block_manager *bm, int32_t max_moves, int32_t *moves, int32_t *num_moves);

@@ -187,6 +187,10 @@ constexpr int kOwnPlanTilesPerSm = 6;
 //    68, 256 at window 700 126 / 155 and at 128 40 / 73;
 //  * on e4m3 pools, where decoding the codes bounds both, the latter only while there
 //    is little to decode: 32 requests at window 2048 36 / 43 us, 64 at 4096 115 / 107.
+// The averages are over all requests, empty ones too, so that a long chunk among many
+// decode rows or empty slots goes along, in pieces of 16 rows: 192 decode rows and a chunk
+// of 512 at window 128 51 / 67 us, at 1024 177 / 161, at 4096 576 / 498; a chunk of 4096
+// tokens in a batch padded to 1024 requests 125 / 59, 358 / 95 and 1150 / 248.
 constexpr int64_t kDirectAnyChunks = 4096;
 constexpr int64_t kDirectAnyChunksE4m3 = 6144;
 constexpr int64_t kDirectJobsPerSm = 7;

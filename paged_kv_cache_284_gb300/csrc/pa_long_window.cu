@@ -28,7 +28,7 @@
 //    700-800 cycles by itself and 512 beside the other warp's; one issuing thread
 //    for both was slower (616 us against 487 on the case below).
 // Two chunks of 4096 tokens, window 4096 + 16 sinks, 32 q / 8 kv heads, d = 128, 552
-// GFLOP of visible pairs: 478 us, 1155 TFLOP/s, 0.60 of the measured bf16 rate (565 us
+// GFLOP of visible pairs: 488 us, 1130 TFLOP/s, 0.58 of the measured bf16 rate (565 us
 // in the plain kernel's form).  Bound: the chain of a key tile (scores, maximum,
 // exponentials, P V) at ~1900 cycles for two tiles in flight, against 1024 of MMA;
 // a third S tile with P written over S left too few registers and columns to win.
@@ -649,7 +649,8 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
                     ref = now;
                 }
                 const float neg_ref = now == -INFINITY ? 0.f : -now;
-                // P row r (bf16 pairs), in four pieces so that a piece's store lies
+                // P row r (bf16 pairs: an MMA's operands have one type, and V is bf16; the
+                // sums above take the unrounded values), in four pieces so that a piece's store lies
                 // beside the next one's exponentials; the P V that used this
                 // buffer two tiles ago must be done
                 if (tt >= 2 && !warp_mbar_wait_spin(&bars->pv_done[grp], ((tt - 2) >> 1) & 1, abort_flag)) { ok = false; break; }

@@ -6,9 +6,9 @@
 //   a' = f (a cos t - b sin t),  b' = f (b cos t + a sin t).
 // The angle is only wanted modulo one turn.  inv_freq / 2 pi is held as a
 // 64-bit binary fraction of a turn, and position * fraction in wrapping 64-bit
-// integers IS that product modulo one turn: exact for every int32 position,
-// negative ones too, with a step of 2^-64 turns (2^-33 after the largest
-// position).  Its top 32 bits, as a signed fraction x in [-1/2, 1/2) of a
+// integers IS that product modulo one turn, for every int32 position, negative
+// ones too; the fraction itself is good to 2^-64 max(1, inv_freq) turns, the
+// product to 2^31 times that for the farthest position.  Its top 32 bits, as a signed fraction x in [-1/2, 1/2) of a
 // turn, give cos and sin through sincospif(2 x).
 //
 // The work is HBM traffic: q, k and v read once, q_out and the cache rows
@@ -20,9 +20,9 @@
 // turn each frequency once per item, two per lane, and share cos and sin
 // through shared memory; then each lane keeps the frequencies of its 16
 // elements of a head in registers while it walks over the heads.
-// 4096 tokens of 32 + 8 + 8 heads, three axes, bf16 (101 MB): 18.1 us, 5.6 TB/s,
-// 0.83 of the measured copy bandwidth; 16384 tokens into an e4m3 pool (369 MB)
-// 64.6 us, 0.85; 8 tokens 3.5 us, most of it the launch.  A block per token with
+// 4096 tokens of 32 + 8 + 8 heads, three axes, bf16 (101 MB): 18.3 us, 5.5 TB/s,
+// 0.82 of the measured copy bandwidth; 16384 tokens into an e4m3 pool (369 MB)
+// 66.2 us, 0.83; 8 tokens 3.5 us, most of it the launch.  A block per token with
 // plain loads took 21-26 and 79-106 us.
 #include <algorithm>
 
