@@ -58,6 +58,7 @@ enum {
 #define PA_DEV_BAD_SLOT      0x4u  /* a slot outside the pool: that row was not written    */
 #define PA_DEV_WAIT_TIMEOUT  0x8u  /* a pipeline wait ran out; the kernel stopped early    */
 #define PA_DEV_PLAN_OVERFLOW 0x10u /* work did not fit the workspace's item capacity       */
+#define PA_DEV_NO_BLOCKS     0x20u /* pa_build_step: the free list is too short for the step */
 
 /* Element type of a KV pool (pa_kv_desc.kv_dtype). */
 enum { PA_KV_BF16 = 0, PA_KV_FP8_E4M3 = 1 };
@@ -192,6 +193,58 @@ int pa_copy_blocks(const pa_kv_desc *kv, int32_t num_layers, const int32_t *pair
 int pa_validate_copies(const int32_t *pairs, int32_t num_pairs, int32_t num_blocks);
 
 /*
+ * A step's metadata from the requests' lengths, on the GPU: what pa_bm_schedule
+ * (pa_blocks.h) makes on the host for requests whose blocks are shared and hashed, for a
+ * persistent batch whose rows own their blocks.  Nothing is read back, so a captured step
+ * runs on by itself.
+ *
+ * Row b has cached_lens[b] tokens in the blocks of its table row.  query_lens[b] says what
+ * the step does with it:
+ *   n > 0  n new tokens behind the cached ones; the blocks that they need beyond the row's
+ *          ceil(cached / block_size) are taken from the free list, row by row, and entered
+ *          in block_tables
+ *   0      nothing: it stays in the batch
+ *   < 0    the row is done: the blocks of its first ceil(cached / block_size) entries go
+ *          back to the free list (negative entries, as pa_bm_release_window leaves them, are
+ *          passed over) and the row is empty from now on.  Blocks given back are first taken
+ *          by a later call.
+ * Outputs, in the form that the other calls take:
+ *   query_start_loc  int32 [num_seqs + 1]
+ *   context_lens     int32 [num_seqs]  cached tokens before the step (0 for a row that is done)
+ *   seq_lens         int32 [num_seqs]  context + new; may be cached_lens itself, which then
+ *                    holds the next step's
+ *   slot_mapping     int64 [num_tokens]  from the last row's tokens on: -1
+ *   positions        int32 [num_tokens]  of each token in its request, then 0
+ * The free list is a ring of block ids: free_state holds its head and its count (int32 [4],
+ * two more words are the library's); blocks are taken at the head and given back behind the
+ * tail.  free_state_out (int32 [4]) receives head and count after the step and, third, how
+ * many blocks were missing (0 for a step that was made); it may be free_state itself.
+ * Every block is in the list or in one row's table, once.
+ *
+ * All or nothing: with too few blocks in the list (PA_DEV_NO_BLOCKS), more tokens than
+ * num_tokens, a row longer than its table, a negative cached length, or a head or count out
+ * of range (PA_DEV_BAD_METADATA) the call changes neither table nor list, takes no row out,
+ * and makes a step without tokens: every query start 0, every slot -1, context and seq_lens
+ * the cached lengths.
+ * A table entry outside the pool that a token's slot needs gives slot -1 and
+ * PA_DEV_BAD_BLOCK, such an id in the list too (the table gets it clamped).
+ * query_lens, cached_lens and free_state may not overlap any output but those named.
+ * num_seqs is at most 8192; max_blocks_per_seq * block_size at most 2^30.
+ */
+typedef struct pa_free_list {
+    int32_t *blocks;          /* device int32 [capacity]; capacity >= blocks it can ever hold */
+    const int32_t *state;     /* device int32 [4]: head, count */
+    int32_t *state_out;       /* device int32 [4]: head, count, missing */
+    int32_t capacity;
+    int32_t reserved;         /* must be 0 */
+} pa_free_list;
+int pa_build_step(const int32_t *query_lens, const int32_t *cached_lens, int32_t num_seqs,
+                  int32_t *block_tables, int32_t max_blocks_per_seq, const pa_free_list *free_list,
+                  int32_t num_blocks, int32_t block_size, int32_t num_tokens,
+                  int32_t *query_start_loc, int32_t *context_lens, int32_t *seq_lens,
+                  int64_t *slot_mapping, int32_t *positions, void *stream);
+
+/*
  * Workspace bytes pa_attention / pa_attention_ex need for a step with these
  * sizes (independent of the lengths in the metadata).  The workspace holds
  * the device-built work list, split-KV partial states and completion
@@ -308,6 +361,68 @@ int pa_window_attention(const void *q, const pa_kv_desc *kv, const int32_t *bloc
                         int32_t num_q_tokens, int32_t num_q_heads, float scale, int32_t window,
                         int32_t num_sinks, void *out, float *lse, void *workspace,
                         size_t workspace_bytes, void *stream);
+
+/*
+ * Cross attention of a step's rows to an encoder's states in a paged pool: every query row of
+ * request b attends all of its encoder_lens[b] keys, held in order by the blocks of its table
+ * row, with no mask.  encoder_lens[b] = 0 gives out 0 and lse -inf.  The encoder's k and v
+ * are written once with pa_write_kv (pa_build_step makes their table and slots); rows that
+ * share an encoder's states (beams) may be one request of several query tokens, which reads
+ * the states once.
+ * Arguments, padded batches, workspace size, e4m3 pools (pa_fp8_staging_bytes counts the
+ * blocks of requests with q_len * group > 64) and errors are those of pa_attention, with
+ * encoder_lens (int32 [num_seqs]) in the place of both lengths.  scale > 0;
+ * max_blocks_per_seq * block_size and num_q_tokens must not exceed 2^30.  Table entries past
+ * ceil(encoder_len / block_size) are not read, keys past encoder_len may hold anything.
+ */
+int pa_cross_attention(const void *q, const pa_kv_desc *kv, const int32_t *block_tables,
+                       int32_t max_blocks_per_seq, const int32_t *query_start_loc,
+                       const int32_t *encoder_lens, int32_t num_seqs, int32_t num_q_tokens,
+                       int32_t num_q_heads, float scale, void *out, float *lse, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+/*
+ * Linear attention with a decay per head, for the layers of a hybrid model that keep a state
+ * instead of a cache.  Request b owns query tokens [qsl[b], qsl[b+1]) as in pa_attention; for
+ * each of its kv heads, with a state S of head_dim x head_dim (k by v),
+ *   S_t = e^(g_t) S_(t-1) + k_t v_t^T,    out_t = scale * q_t S_t
+ * for the query heads of the group.  S starts as the state in slot state_in[b], or as zero
+ * where that is negative, and is left in slot state_out[b], or dropped where that is negative.
+ * The two may be the same slot (a decode loop) or not (a copy to fork from, or to go back to
+ * after rejected tokens); a request without tokens copies its state from one to the other.
+ * A slot that a request writes is no other request's, to read or to write.
+ *   q, k, v       bf16 [num_tokens][heads][head_dim], token rows q_stride, k_stride, v_stride
+ *                 elements apart (multiples of 8, so that the three may be slices of one
+ *                 fused projection), 16-B aligned
+ *   log_decay     fp32 natural logarithms g, at most 0 (a greater one or a NaN counts as 0,
+ *                 -inf clears the state): [num_tokens][num_kv_heads], or [num_kv_heads] for
+ *                 all tokens with decay_per_token = 0
+ *   state         fp32 [num_slots][num_kv_heads][head_dim][head_dim], 16-B aligned, finite
+ *   state_in, state_out  int32 [num_seqs]; one beyond the pool counts as negative and flags
+ *                 PA_DEV_BAD_SLOT
+ *   out           bf16 [num_tokens][num_q_heads][head_dim], 16-B aligned; rows that belong to
+ *                 no request are left untouched; may not overlap an input
+ * States and all sums are fp32.  head_dim 64 or 128; num_q_heads a multiple of num_kv_heads,
+ * at most 128 heads to a group.  A decreasing query start, or one past num_tokens, skips the
+ * request and flags PA_DEV_BAD_METADATA.
+ */
+typedef struct pa_linear_desc {
+    float *state;
+    int32_t num_slots;
+    int32_t num_q_heads, num_kv_heads, head_dim;
+    int32_t decay_per_token;  /* 0 or 1 */
+    float scale;              /* finite */
+} pa_linear_desc;
+int pa_linear_attention(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                        const void *v, int64_t v_stride, const int32_t *query_start_loc,
+                        int32_t num_seqs, int32_t num_tokens, const float *log_decay,
+                        const pa_linear_desc *desc, const int32_t *state_in,
+                        const int32_t *state_out, void *out, void *workspace,
+                        size_t workspace_bytes, void *stream);
+/* Workspace bytes of pa_linear_attention (256-byte aligned, untouched while the call's kernels
+ * run).  Returns 0 for invalid sizes. */
+size_t pa_linear_workspace_size(int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads,
+                                int32_t num_kv_heads, int32_t head_dim);
 
 /*
  * Merge operator of cascade inference ([AI] §02.1): combine two attention

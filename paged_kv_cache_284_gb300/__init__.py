@@ -18,6 +18,9 @@ Calls (same names as the C ABI):
   pa_rope_write_kv     rotary positions (several axes) on q and k, and the
                        cache write, in one pass
   pa_copy_blocks       block copies (copy-on-write, compaction) in all layers
+  pa_build_step        a step's metadata made on the GPU from request lengths
+  pa_cross_attention   attention to an encoder's states in the paged pool
+  pa_linear_attention  linear attention with a decay per head over a pool of states
 """
 from __future__ import annotations
 
@@ -33,7 +36,7 @@ LIB_PATH = os.path.join(_PKG, "libpa.so")
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_WORKSPACE, PA_ERR_CUDA, \
     PA_ERR_BAD_METADATA = range(6)
 PA_DEV_BAD_METADATA, PA_DEV_BAD_BLOCK, PA_DEV_BAD_SLOT, PA_DEV_WAIT_TIMEOUT, \
-    PA_DEV_PLAN_OVERFLOW = 0x1, 0x2, 0x4, 0x8, 0x10
+    PA_DEV_PLAN_OVERFLOW, PA_DEV_NO_BLOCKS = 0x1, 0x2, 0x4, 0x8, 0x10, 0x20
 
 EXPORTED = ["pa_write_kv", "pa_attention_workspace_size", "pa_attention", "pa_attention_ex",
             "pa_write_kv_attention", "pa_cascade_fp8_staging_bytes",
@@ -50,6 +53,8 @@ EXPORTED = ["pa_write_kv", "pa_attention_workspace_size", "pa_attention", "pa_at
             "pa_set_test_stall", "pa_set_tile_counter",
             "pa_window_attention", "pa_validate_window_metadata", "pa_rope_write_kv",
             "pa_copy_blocks", "pa_validate_copies",
+            "pa_build_step", "pa_cross_attention", "pa_linear_attention",
+            "pa_linear_workspace_size",
             # request router for sharded replicas (include/pa_shard.h)
             "pa_partition_requests"]
 PA_KERNEL_WRITE_KV, PA_KERNEL_PLAN, PA_KERNEL_SPLIT_KV, PA_KERNEL_TENSOR_CORE = range(4)
@@ -80,6 +85,19 @@ class RopeDesc(ctypes.Structure):
     _fields_ = [("inv_freq", ctypes.c_void_p), ("axis", ctypes.c_void_p),
                 ("rot_dim", ctypes.c_int32), ("num_axes", ctypes.c_int32),
                 ("adjacent", ctypes.c_int32), ("attn_factor", ctypes.c_float)]
+
+
+class FreeList(ctypes.Structure):
+    _fields_ = [("blocks", ctypes.c_void_p), ("state", ctypes.c_void_p),
+                ("state_out", ctypes.c_void_p), ("capacity", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class LinearDesc(ctypes.Structure):
+    _fields_ = [("state", ctypes.c_void_p), ("num_slots", ctypes.c_int32),
+                ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("decay_per_token", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
 
 
 def _declare(lib):
@@ -134,6 +152,13 @@ def _declare(lib):
                               P, P], ctypes.c_int),
         "pa_copy_blocks": ([KV, i32, P, i32, P], ctypes.c_int),
         "pa_validate_copies": ([P, i32, i32], ctypes.c_int),
+        "pa_build_step": ([P, P, i32, P, i32, ctypes.POINTER(FreeList), i32, i32, i32, P, P, P, P,
+                           P, P], ctypes.c_int),
+        "pa_cross_attention": ([P, KV, P, i32, P, P, i32, i32, i32, f32, P, P, P, sz, P],
+                               ctypes.c_int),
+        "pa_linear_attention": ([P, i64, P, i64, P, i64, P, i32, i32, P,
+                                 ctypes.POINTER(LinearDesc), P, P, P, P, sz, P], ctypes.c_int),
+        "pa_linear_workspace_size": ([i32, i32, i32, i32, i32], sz),
         "pa_set_test_stall": ([i32], ctypes.c_int),
         "pa_set_tile_counter": ([P], ctypes.c_int),
     }
@@ -174,8 +199,8 @@ def _load_direct():
                           "`python -c 'import __graft_entry__ as g; g.build()'`") from e
     L = lib()
     _pa_torch.bind(*(ctypes.cast(f, ctypes.c_void_p).value
-                     for f in (L.pa_window_attention, L.pa_rope_write_kv,
-                               L.pa_copy_blocks)))
+                     for f in (L.pa_window_attention, L.pa_rope_write_kv, L.pa_copy_blocks,
+                               L.pa_cross_attention, L.pa_linear_attention, L.pa_build_step)))
     _direct = _pa_torch
     return _direct
 
@@ -469,6 +494,147 @@ def pa_window_attention(q, k_cache, v_cache, block_tables, query_start_loc, cont
     _check(L.pa_window_attention(*args, workspace.data_ptr(), workspace.nbytes, handle),
            "pa_window_attention")
     return workspace
+
+
+def pa_cross_attention(q, k_cache, v_cache, block_tables, query_start_loc, encoder_lens, scale,
+                       out, lse=None, workspace=None, stream=None, k_scale=None, v_scale=None,
+                       staging_blocks=0):
+    """Every query row of request b attends all encoder_lens[b] (int32 [B]) keys of its
+    table row, without a mask; no keys give out 0 and lse -inf.  Other arguments,
+    workspace and e4m3 pools as in pa_attention.  Returns the workspace tensor used."""
+    # (plain calls as in pa_window_attention)
+    if workspace is not None and staging_blocks == 0:
+        rc = (_direct or _load_direct()).cross_attention(
+            q, k_cache, v_cache, block_tables, query_start_loc, encoder_lens, scale, out, lse,
+            workspace, stream, k_scale, v_scale)
+        if rc == PA_OK:
+            return workspace
+        if rc != _NOT_PLAIN and rc != PA_ERR_WORKSPACE:
+            _check(rc, "pa_cross_attention")
+    dev = q.get_device()
+    _explain(dev, (("q", q, _BF16), ("out", out, _BF16), ("block_tables", block_tables, _I32),
+                   ("query_start_loc", query_start_loc, _I32),
+                   ("encoder_lens", encoder_lens, _I32), ("lse", lse, _F32),
+                   ("workspace", workspace, None)))
+    kv = _pool(k_cache, v_cache, k_scale, v_scale, dev)
+    if q.dim() != 3 or q.shape[2] != kv.head_dim or out.shape != q.shape or \
+            (lse is not None and lse.numel() != q.shape[0] * q.shape[1]):
+        raise ValueError("q and out must be [T, Hq, head_dim], lse [T, Hq]")
+    T, hq, d = q.shape
+    B = encoder_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or query_start_loc.numel() != B + 1:
+        raise ValueError("block_tables [B, N], query_start_loc [B + 1] and encoder_lens [B] must "
+                         "agree")
+    L = lib()
+    need = L.pa_attention_workspace_size(B, T, hq, kv.num_kv_heads, d)
+    if staging_blocks > 0 and kv.kv_dtype == PA_KV_FP8_E4M3:
+        need += L.pa_fp8_staging_bytes(kv.num_kv_heads, d, kv.block_size, int(staging_blocks))
+    if workspace is None or workspace.nbytes < need:
+        workspace = alloc_workspace(need, q.device, stream)
+    _check(L.pa_cross_attention(q.data_ptr(), kv, block_tables.data_ptr(), block_tables.shape[1],
+                                query_start_loc.data_ptr(), encoder_lens.data_ptr(), B, T, hq,
+                                scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
+                                workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev)),
+           "pa_cross_attention")
+    return workspace
+
+
+def linear_workspace_size(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim) -> int:
+    return int(lib().pa_linear_workspace_size(num_seqs, num_tokens, num_q_heads, num_kv_heads,
+                                              head_dim))
+
+
+def pa_linear_attention(q, k, v, query_start_loc, log_decay, state, state_in, state_out, scale,
+                        out, workspace=None, stream=None):
+    """Linear attention with a decay per head: S_t = e^g_t S_(t-1) + k_t v_t^T, out_t = scale
+    q_t S_t for the tokens of each request.  q [T, Hq, d], k and v [T, Hkv, d] bf16, token
+    rows at any stride that is a multiple of 8; log_decay float32 [Hkv] or [T, Hkv], at most
+    0; state float32 [slots, Hkv, d, d]; state_in and state_out int32 [B], the slot a request
+    starts from (negative: zero) and the one it leaves its state in (negative: none); out
+    bf16 [T, Hq, d].  Returns the workspace tensor used."""
+    if workspace is not None:
+        rc = (_direct or _load_direct()).linear_attention(
+            q, k, v, query_start_loc, log_decay, state, state_in, state_out, scale, out,
+            workspace, stream)
+        if rc == PA_OK:
+            return workspace
+        if rc != _NOT_PLAIN and rc != PA_ERR_WORKSPACE:
+            _check(rc, "pa_linear_attention")
+    dev = q.get_device()
+    (qs, q_rows), (ks, k_rows), (vs, v_rows) = (_token_rows(t, name, dev) for t, name in
+                                                ((q, "q"), (k, "k"), (v, "v")))
+    _explain(dev, (("query_start_loc", query_start_loc, _I32), ("log_decay", log_decay, _F32),
+                   ("state", state, _F32), ("state_in", state_in, _I32),
+                   ("state_out", state_out, _I32), ("out", out, _BF16),
+                   ("workspace", workspace, None)))
+    T, hq, d = q_rows
+    hkv = k_rows[1]
+    if k_rows != (T, hkv, d) or v_rows != k_rows or out.shape != q_rows:
+        raise ValueError("q and out must be [T, Hq, d], k and v [T, Hkv, d]")
+    if state.dim() != 4 or state.shape[1:] != (hkv, d, d):
+        raise ValueError("state must be [slots, Hkv, d, d]")
+    if log_decay.shape not in ((hkv,), (T, hkv)):
+        raise ValueError("log_decay must be [Hkv] or [T, Hkv]")
+    B = state_in.numel()
+    if state_out.numel() != B or query_start_loc.numel() != B + 1:
+        raise ValueError("state_in [B], state_out [B] and query_start_loc [B + 1] must agree")
+    L = lib()
+    need = L.pa_linear_workspace_size(B, T, hq, hkv, d)
+    if workspace is None or workspace.nbytes < need:
+        workspace = alloc_workspace(need, q.device, stream)
+    desc = LinearDesc(state.data_ptr(), state.shape[0], hq, hkv, d,
+                      1 if log_decay.dim() == 2 else 0, scale)
+    _check(L.pa_linear_attention(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                                 query_start_loc.data_ptr(), B, T, log_decay.data_ptr(), desc,
+                                 state_in.data_ptr(), state_out.data_ptr(), out.data_ptr(),
+                                 workspace.data_ptr(), workspace.nbytes,
+                                 _raw_stream(stream, dev)), "pa_linear_attention")
+    return workspace
+
+
+def pa_build_step(query_lens, cached_lens, block_tables, free_blocks, free_state, num_blocks,
+                  block_size, query_start_loc, context_lens, seq_lens, slot_mapping, positions,
+                  free_state_out=None, stream=None):
+    """A step's metadata from the rows' lengths, with blocks taken from and given back to a
+    free list, all on the GPU.  query_lens int32 [B]: new tokens of each row (negative: the
+    row is done); cached_lens int32 [B]; block_tables int32 [B, N], which gets the new
+    blocks; free_blocks int32 [capacity], a ring; free_state int32 [4], its head and count.
+    Outputs: query_start_loc [B + 1], context_lens [B], seq_lens [B] (may be cached_lens),
+    slot_mapping int64 [T], positions int32 [T], free_state_out int32 [4]: head, count and
+    missing blocks after the step (None: free_state itself)."""
+    if free_state_out is None:
+        free_state_out = free_state
+    rc = (_direct or _load_direct()).build_step(
+        query_lens, cached_lens, block_tables, free_blocks, free_state, num_blocks, block_size,
+        query_start_loc, context_lens, seq_lens, slot_mapping, positions, free_state_out, stream)
+    if rc != _NOT_PLAIN:
+        if rc:
+            _check(rc, "pa_build_step")
+        return
+    dev = query_lens.get_device()
+    _explain(dev, (("query_lens", query_lens, _I32), ("cached_lens", cached_lens, _I32),
+                   ("block_tables", block_tables, _I32), ("free_blocks", free_blocks, _I32),
+                   ("free_state", free_state, _I32), ("query_start_loc", query_start_loc, _I32),
+                   ("context_lens", context_lens, _I32), ("seq_lens", seq_lens, _I32),
+                   ("slot_mapping", slot_mapping, _I64), ("positions", positions, _I32),
+                   ("free_state_out", free_state_out, _I32)))
+    B, T = query_lens.numel(), slot_mapping.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or cached_lens.numel() != B or \
+            context_lens.numel() != B or seq_lens.numel() != B or query_start_loc.numel() != B + 1:
+        raise ValueError("query_lens, cached_lens, context_lens and seq_lens [B], block_tables "
+                         "[B, N] and query_start_loc [B + 1] must agree")
+    if positions.numel() != T:
+        raise ValueError("slot_mapping and positions must be [T]")
+    if free_state.numel() != 4 or free_state_out.numel() != 4:
+        raise ValueError("free_state and free_state_out must hold 4 values")
+    free = FreeList(free_blocks.data_ptr(), free_state.data_ptr(), free_state_out.data_ptr(),
+                    free_blocks.numel(), 0)
+    _check(lib().pa_build_step(query_lens.data_ptr(), cached_lens.data_ptr(), B,
+                               block_tables.data_ptr(), block_tables.shape[1], free,
+                               _int32(num_blocks), _int32(block_size), T,
+                               query_start_loc.data_ptr(), context_lens.data_ptr(),
+                               seq_lens.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(),
+                               _raw_stream(stream, dev)), "pa_build_step")
 
 
 def _token_rows(t: torch.Tensor, name: str, device: int):

@@ -1115,14 +1115,15 @@ size_t pa_attention_workspace_size(int32_t num_seqs, int32_t num_q_tokens, int32
 namespace {
 
 // pa_attention_ex, with `fresh` the write of the step's new rows first, with
-// `win` a windowed step.
+// `win` a windowed step, with `cross` (and a window past every key) cross attention:
+// context_lens is NULL, in the kernels too.
 int attention_entry(const void *q, const pa_kv_desc *kv, const int32_t *block_tables,
                     int32_t max_blocks_per_seq, const int32_t *query_start_loc,
                     const int32_t *context_lens, const int32_t *seq_lens, int32_t num_seqs,
                     int32_t num_q_tokens, int32_t num_q_heads, float scale, void *out, float *lse,
                     void *workspace, size_t workspace_bytes, int32_t short_q_max_rows,
                     int32_t split_keys, cudaStream_t stream, const NewRows *fresh,
-                    const WindowArgs *win = nullptr) {
+                    const WindowArgs *win = nullptr, bool cross = false) {
     g_err[0] = 0;
     int rc = common_checks(q, kv, num_q_tokens, num_q_heads, scale, out, workspace);
     if (rc != PA_OK) return rc;
@@ -1142,7 +1143,7 @@ int attention_entry(const void *q, const pa_kv_desc *kv, const int32_t *block_ta
                              stream);
         return rc == PA_OK ? PA_OK : fail(rc, "write_kv launch failed");
     }
-    if (!block_tables || !query_start_loc || !context_lens || !seq_lens)
+    if (!block_tables || !query_start_loc || (!context_lens && !cross) || !seq_lens)
         return fail(PA_ERR_INVALID_ARG, "metadata pointer is NULL");
     if (max_blocks_per_seq <= 0) return fail(PA_ERR_INVALID_ARG, "max_blocks_per_seq <= 0");
     if (win && static_cast<int64_t>(max_blocks_per_seq) * kv->block_size > kMaxWindowKeys)
@@ -1236,6 +1237,165 @@ int pa_window_attention(const void *q, const pa_kv_desc *kv, const int32_t *bloc
                            seq_lens, num_seqs, num_q_tokens, num_q_heads, scale, out, lse,
                            workspace, workspace_bytes, -1, 0, static_cast<cudaStream_t>(stream),
                            nullptr, &win);
+}
+
+int pa_cross_attention(const void *q, const pa_kv_desc *kv, const int32_t *block_tables,
+                       int32_t max_blocks_per_seq, const int32_t *query_start_loc,
+                       const int32_t *encoder_lens, int32_t num_seqs, int32_t num_q_tokens,
+                       int32_t num_q_heads, float scale, void *out, float *lse, void *workspace,
+                       size_t workspace_bytes, void *stream) {
+    g_err[0] = 0;
+    // the windowed kernels without a window: each row stands behind its request's last key
+    const WindowArgs all{static_cast<int32_t>(kMaxWindowKeys), 0};
+    const int rc = check_window(all.window, all.sinks, scale);
+    if (rc != PA_OK) return rc;
+    if (num_q_tokens > kMaxWindowKeys)
+        return fail(PA_ERR_UNSUPPORTED, "more than 2^30 query tokens");
+    return attention_entry(q, kv, block_tables, max_blocks_per_seq, query_start_loc, nullptr,
+                           encoder_lens, num_seqs, num_q_tokens, num_q_heads, scale, out, lse,
+                           workspace, workspace_bytes, -1, 0, static_cast<cudaStream_t>(stream),
+                           nullptr, &all, true);
+}
+
+int pa_build_step(const int32_t *query_lens, const int32_t *cached_lens, int32_t num_seqs,
+                  int32_t *block_tables, int32_t max_blocks_per_seq, const pa_free_list *free_list,
+                  int32_t num_blocks, int32_t block_size, int32_t num_tokens,
+                  int32_t *query_start_loc, int32_t *context_lens, int32_t *seq_lens,
+                  int64_t *slot_mapping, int32_t *positions, void *stream) {
+    g_err[0] = 0;
+    if (num_seqs < 0 || num_tokens < 0)
+        return fail(PA_ERR_INVALID_ARG, "num_seqs or num_tokens < 0");
+    if (num_seqs > kBuildMaxSeqs)
+        return fail(PA_ERR_UNSUPPORTED, "num_seqs %d: at most %d", num_seqs, kBuildMaxSeqs);
+    if (num_blocks <= 0 || max_blocks_per_seq <= 0)
+        return fail(PA_ERR_INVALID_ARG, "num_blocks and max_blocks_per_seq must be positive");
+    if (block_size <= 0 || block_size % 16 != 0 || block_size > 256)
+        return fail(PA_ERR_UNSUPPORTED, "block_size %d: need a multiple of 16, at most 256",
+                    block_size);
+    if (static_cast<int64_t>(max_blocks_per_seq) * block_size > kMaxWindowKeys)
+        return fail(PA_ERR_UNSUPPORTED, "block tables of more than 2^30 tokens per request");
+    if (!free_list || !free_list->blocks || !free_list->state || !free_list->state_out)
+        return fail(PA_ERR_INVALID_ARG, "free list pointer is NULL");
+    if (free_list->reserved != 0) return fail(PA_ERR_INVALID_ARG, "pa_free_list.reserved must be 0");
+    if (free_list->capacity <= 0) return fail(PA_ERR_INVALID_ARG, "free list capacity must be positive");
+    if (!query_start_loc || (num_tokens > 0 && (!slot_mapping || !positions)) ||
+        (num_seqs > 0 && (!query_lens || !cached_lens || !block_tables || !context_lens || !seq_lens)))
+        return fail(PA_ERR_INVALID_ARG, "metadata pointer is NULL");
+    const void *words[] = {query_lens, cached_lens, block_tables, free_list->blocks,
+                           free_list->state, free_list->state_out, query_start_loc, context_lens,
+                           seq_lens, positions};
+    for (const void *w : words)
+        if (!aligned(w, 4)) return fail(PA_ERR_INVALID_ARG, "an int32 array is misaligned");
+    if (!aligned(slot_mapping, 8)) return fail(PA_ERR_INVALID_ARG, "slot_mapping is misaligned");
+    DeviceInfo *dev;
+    int rc = device_info(&dev);
+    if (rc != PA_OK) return rc;
+    BuildParams p{};
+    p.query_lens = query_lens;
+    p.cached_lens = cached_lens;
+    p.block_tables = block_tables;
+    p.num_seqs = num_seqs;
+    p.max_blocks = max_blocks_per_seq;
+    p.max_keys = max_blocks_per_seq * block_size;
+    p.free_blocks = free_list->blocks;
+    p.free_state = free_list->state;
+    p.free_state_out = free_list->state_out;
+    p.capacity = free_list->capacity;
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    p.num_tokens = num_tokens;
+    p.query_start_loc = query_start_loc;
+    p.context_lens = context_lens;
+    p.seq_lens = seq_lens;
+    p.positions = positions;
+    p.slot_mapping = slot_mapping;
+    p.status = dev->status;
+    rc = launch_build_step(p, static_cast<cudaStream_t>(stream));
+    return rc == PA_OK ? PA_OK : fail(rc, "build_step launch failed: %s",
+                                      cudaGetErrorString(cudaGetLastError()));
+}
+
+size_t pa_linear_workspace_size(int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads,
+                                int32_t num_kv_heads, int32_t head_dim) {
+    if (num_seqs < 0 || num_tokens < 0 || num_kv_heads <= 0 || num_q_heads <= 0 ||
+        num_q_heads % num_kv_heads != 0 || (head_dim != 64 && head_dim != 128))
+        return 0;
+    return 256;
+}
+
+int pa_linear_attention(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                        const void *v, int64_t v_stride, const int32_t *query_start_loc,
+                        int32_t num_seqs, int32_t num_tokens, const float *log_decay,
+                        const pa_linear_desc *desc, const int32_t *state_in,
+                        const int32_t *state_out, void *out, void *workspace,
+                        size_t workspace_bytes, void *stream) {
+    g_err[0] = 0;
+    if (!desc) return fail(PA_ERR_INVALID_ARG, "linear descriptor is NULL");
+    const int hq = desc->num_q_heads, hkv = desc->num_kv_heads, d = desc->head_dim;
+    if (num_seqs < 0 || num_tokens < 0)
+        return fail(PA_ERR_INVALID_ARG, "num_seqs or num_tokens < 0");
+    if (desc->num_slots < 0) return fail(PA_ERR_INVALID_ARG, "num_slots < 0");
+    if (hkv <= 0 || hq <= 0 || hq % hkv != 0)
+        return fail(PA_ERR_INVALID_ARG, "num_q_heads %d is not a multiple of num_kv_heads %d", hq, hkv);
+    if (d != 64 && d != 128) return fail(PA_ERR_UNSUPPORTED, "head_dim %d not built (64 or 128)", d);
+    if (hq / hkv > kLongRows)
+        return fail(PA_ERR_UNSUPPORTED, "group size %d too large", hq / hkv);
+    if (desc->decay_per_token != 0 && desc->decay_per_token != 1)
+        return fail(PA_ERR_INVALID_ARG, "pa_linear_desc.decay_per_token must be 0 or 1");
+    if (!std::isfinite(desc->scale)) return fail(PA_ERR_INVALID_ARG, "scale is not finite");
+    if (static_cast<int64_t>(num_seqs) * hkv > (static_cast<int64_t>(1) << 28))
+        return fail(PA_ERR_UNSUPPORTED, "more than 2^28 states in a step");
+    if (num_seqs == 0) return PA_OK;
+    if (!query_start_loc || !state_in || !state_out || !desc->state || !log_decay)
+        return fail(PA_ERR_INVALID_ARG, "state, decay or metadata pointer is NULL");
+    if (num_tokens > 0 && (!q || !k || !v || !out))
+        return fail(PA_ERR_INVALID_ARG, "q, k, v or out is NULL");
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
+        !aligned(desc->state, 16))
+        return fail(PA_ERR_INVALID_ARG, "q, k, v, out and state must be 16-byte aligned");
+    if (!aligned(query_start_loc, 4) || !aligned(state_in, 4) || !aligned(state_out, 4) ||
+        !aligned(log_decay, 4))
+        return fail(PA_ERR_INVALID_ARG, "metadata or log_decay is misaligned");
+    const int64_t stride[3] = {q_stride, k_stride, v_stride};
+    const int64_t least[3] = {static_cast<int64_t>(hq) * d, static_cast<int64_t>(hkv) * d,
+                              static_cast<int64_t>(hkv) * d};
+    for (int i = 0; i < 3; ++i)
+        if (stride[i] % 8 != 0 || (num_tokens > 1 && stride[i] < least[i]))
+            return fail(PA_ERR_INVALID_ARG,
+                        "%c_stride %lld: need a multiple of 8 that holds a token's heads", "qkv"[i],
+                        (long long)stride[i]);
+    const size_t need = pa_linear_workspace_size(num_seqs, num_tokens, hq, hkv, d);
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < need)
+        return fail(PA_ERR_WORKSPACE, "workspace needs %zu bytes, 256-byte aligned, got %zu", need,
+                    workspace_bytes);
+    DeviceInfo *dev;
+    int rc = device_info(&dev);
+    if (rc != PA_OK) return rc;
+    LinearParams p{};
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.k = static_cast<const __nv_bfloat16 *>(k);
+    p.v = static_cast<const __nv_bfloat16 *>(v);
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.qsl = query_start_loc;
+    p.decay = log_decay;
+    p.decay_stride = desc->decay_per_token ? hkv : 0;
+    p.state = desc->state;
+    p.state_in = state_in;
+    p.state_out = state_out;
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.num_seqs = num_seqs;
+    p.num_tokens = num_tokens;
+    p.num_q_heads = hq;
+    p.num_kv_heads = hkv;
+    p.group = hq / hkv;
+    p.num_slots = desc->num_slots;
+    p.scale = desc->scale;
+    p.status = dev->status;
+    rc = launch_linear_step(p, d, static_cast<cudaStream_t>(stream));
+    return rc == PA_OK ? PA_OK : fail(rc, "linear attention launch failed: %s",
+                                      cudaGetErrorString(cudaGetLastError()));
 }
 
 int pa_rope_write_kv(const void *q, int64_t q_stride, const void *k, int64_t k_stride,

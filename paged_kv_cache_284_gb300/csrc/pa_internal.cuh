@@ -329,6 +329,36 @@ struct RopeParams {
     unsigned *status;
 };
 
+// A step's metadata from its requests' lengths (pa_build_step).
+constexpr int kBuildMaxSeqs = 8192;  // three ints of shared memory each
+struct BuildParams {
+    const int32_t *query_lens, *cached_lens;
+    int32_t *block_tables;
+    int num_seqs, max_blocks, max_keys;  // max_keys: what a table row holds
+    int32_t *free_blocks;
+    const int32_t *free_state;
+    int32_t *free_state_out;
+    int capacity, num_blocks, block_size, num_tokens;
+    int32_t *query_start_loc, *context_lens, *seq_lens, *positions;
+    int64_t *slot_mapping;
+    unsigned *status;
+};
+
+// Linear attention with decay over a pool of states.
+struct LinearParams {
+    const __nv_bfloat16 *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // elements between tokens
+    const int *qsl;
+    const float *decay;  // natural logs, [T][Hkv] (decay_stride = Hkv) or [Hkv] (0)
+    int decay_stride;
+    float *state;  // [num_slots][Hkv][D][D]
+    const int *state_in, *state_out;
+    __nv_bfloat16 *out;
+    int num_seqs, num_tokens, num_q_heads, num_kv_heads, group, num_slots;
+    float scale;
+    unsigned *status;
+};
+
 // The cache arrays of one pa_copy_blocks launch: K and V of up to
 // kCopyLayers layers.
 constexpr int kCopyLayers = 64;
@@ -409,6 +439,8 @@ int launch_stage_prefix_fp8(const pa_kv_desc *kv, const int32_t *prefix_blocks, 
 int launch_rope_write(const RopeParams &p, int sms, cudaStream_t s);
 int launch_copy_blocks(const pa_kv_desc *kv, int num_layers, const int32_t *pairs, int num_pairs,
                        int sms, unsigned *status, cudaStream_t s);
+int launch_build_step(const BuildParams &p, cudaStream_t s);
+int launch_linear_step(const LinearParams &p, int head_dim, cudaStream_t s);
 int launch_plan(const PlanParams &p, cudaStream_t s);
 int launch_plan_window(const PlanParams &p, cudaStream_t s);
 int launch_short(const ShortParams &p, const CUtensorMap &tk, const CUtensorMap &tv,

@@ -106,12 +106,12 @@ __device__ __forceinline__ OwnPlan own_plan(const LongParams &p) {
     OwnPlan o{};
     if (lane < p.own_seqs) {
         o.q0 = __ldg(p.qsl + lane);
-        o.ctx = __ldg(p.ctx + lane);
         const int q1 = __ldg(p.qsl + lane + 1), len = __ldg(p.seq_lens + lane);
+        o.ctx = p.ctx ? __ldg(p.ctx + lane) : len;  // (cross attention)
         o.n = q1 - o.q0;
         // (a request that the short rows' kernel flags is skipped here too)
-        const bool bad = o.n < 0 || o.ctx < 0 || len > p.own_max_keys || len != o.ctx + o.n ||
-                         o.q0 < 0 || q1 > p.num_q_tokens;
+        const bool bad = o.n < 0 || o.ctx < 0 || len > p.own_max_keys ||
+                         (p.ctx && len != o.ctx + o.n) || o.q0 < 0 || q1 > p.num_q_tokens;
         if (bad) o.n = 0;
         if (o.n * p.group > kShortMaxRows)
             o.tiles = (o.n + p.q_tile_tokens - 1) / p.q_tile_tokens;
@@ -146,7 +146,9 @@ __device__ __forceinline__ LongItem own_tile(const LongParams &p, const OwnPlan 
     it.b = src;
     it.q_tile = t - __shfl_sync(0xffffffffu, excl, src);
     const int first = it.q_tile * p.q_tile_tokens;
-    const KeySpan ks = key_span(p.win, ctx + first, ctx + min(n, first + p.q_tile_tokens));
+    const KeySpan ks = p.ctx
+                           ? key_span(p.win, ctx + first, ctx + min(n, first + p.q_tile_tokens))
+                           : key_span(p.win, ctx, ctx);
     it.key_end = ks.keys;
     it.sink_chunks = ks.sink_chunks;
     it.gap = ks.gap;
@@ -203,19 +205,20 @@ __device__ __forceinline__ WinItem queue_next(const LongParams &p, const Queue &
             li = load_record(p.items, rec);
             q0 = __ldg(p.qsl + li.b);
             n = __ldg(p.qsl + li.b + 1) - q0;
-            ctx = __ldg(p.ctx + li.b);
+            ctx = p.ctx ? __ldg(p.ctx + li.b) : __ldg(p.seq_lens + li.b);
         }
         it.b = li.b;
         it.h = idx - rec * p.num_kv_heads;
         it.tok0 = q0 + li.q_tile * TQ;
         it.nvalid = min(TQ, n - li.q_tile * TQ);
-        it.pos0 = ctx + li.q_tile * TQ - li.gap * kChunkKeys;
+        // (cross attention: behind all keys, which may be none: then one tile of zeros)
+        it.pos0 = p.ctx ? ctx + li.q_tile * TQ - li.gap * kChunkKeys : ctx;
         it.key_end = li.key_end;
-        it.nt = (li.key_end + kLongKeys - 1) / kLongKeys;
+        it.nt = max(1, (li.key_end + kLongKeys - 1) / kLongKeys);
         it.sink_chunks = li.sink_chunks;
         it.gap = li.gap;
         if (p.stage_base) {
-            const BlockSpan bsp = block_span(p.win, ctx, ctx + n, p.block_size);
+            const BlockSpan bsp = block_span(p.win, ctx, p.ctx ? ctx + n : ctx, p.block_size);
             it.block_sinks = bsp.sink_blocks;
             it.block_gap = bsp.gap;
         }

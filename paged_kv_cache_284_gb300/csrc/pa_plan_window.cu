@@ -63,8 +63,10 @@ __device__ Sums block_scan(const Sums &v, Sums *tmp, Sums *total) {
     return base + incl - v;
 }
 
+// Cross attention (no ctx array) is a step whose rows all stand behind the request's
+// `end` keys.
 struct Req {
-    int n, ctx;
+    int n, ctx, end;
     int pieces, qtiles;  // split-KV pieces or tensor-core tiles
 };
 
@@ -72,8 +74,9 @@ __device__ __forceinline__ Req load_req(const PlanParams &p, int b) {
     Req r{};
     const int q0 = __ldg(p.qsl + b), q1 = __ldg(p.qsl + b + 1), len = __ldg(p.seq_lens + b);
     r.n = q1 - q0;
-    r.ctx = __ldg(p.ctx + b);
-    if (r.n < 0 || r.ctx < 0 || len > p.max_keys || len != r.ctx + r.n || q0 < 0 ||
+    r.ctx = p.ctx ? __ldg(p.ctx + b) : len;
+    r.end = len;
+    if (r.n < 0 || r.ctx < 0 || len > p.max_keys || (p.ctx && len != r.ctx + r.n) || q0 < 0 ||
         q1 > p.num_q_tokens) {
         flag_status(p.status, PA_DEV_BAD_METADATA);
         r.n = 0;
@@ -97,11 +100,13 @@ __device__ __forceinline__ WindowPiece piece_of(const PlanParams &p, const Req &
     w.b = b;
     w.q_begin = i * p.piece_tokens;
     w.q_count = min(p.piece_tokens, r.n - w.q_begin);
-    const KeySpan ks = key_span(p.win, r.ctx + w.q_begin, r.ctx + w.q_begin + w.q_count);
+    const int pos = p.ctx ? r.ctx + w.q_begin : r.ctx;
+    const KeySpan ks = key_span(p.win, pos, p.ctx ? pos + w.q_count : r.end);
     w.keys = ks.keys;
     w.sink_chunks = ks.sink_chunks;
     w.gap = ks.gap;
-    w.stages = (ks.keys + kStageKeys - 1) / kStageKeys;
+    // (rows without a key have a stage too: it holds no chunk, and their output is written)
+    w.stages = max(1, (ks.keys + kStageKeys - 1) / kStageKeys);
     return w;
 }
 
@@ -163,8 +168,8 @@ __global__ void __launch_bounds__(kT) plan_window_kernel(const PlanParams p) {
             int cnt = 0;
             if (!full && r.n > 0 && static_cast<long long>(r.n) * p.group > p.short_max_rows)
                 cnt = min(p.stage_cap + 1,
-                          (r.ctx + r.n + p.block_size - 1) / p.block_size -
-                              block_span(p.win, r.ctx, r.ctx + r.n, p.block_size).gap);
+                          (r.end + p.block_size - 1) / p.block_size -
+                              block_span(p.win, r.ctx, r.end, p.block_size).gap);
             // blocks before this request, in 64 bits (2^28 blocks a request)
             long long before = cnt;
 #pragma unroll
@@ -376,8 +381,9 @@ __global__ void __launch_bounds__(kT) plan_window_kernel(const PlanParams p) {
             it.b = w.b;
             it.q_tile = t - w.before;
             const int first = w.keys + it.q_tile * p.q_tile_tokens;
-            const KeySpan ks = key_span(p.win, first,
-                                        min(w.keys + w.q_count, first + p.q_tile_tokens));
+            const KeySpan ks =
+                p.ctx ? key_span(p.win, first, min(w.keys + w.q_count, first + p.q_tile_tokens))
+                      : key_span(p.win, w.keys, w.keys);
             it.key_end = ks.keys;
             it.sink_chunks = ks.sink_chunks;
             it.gap = ks.gap;

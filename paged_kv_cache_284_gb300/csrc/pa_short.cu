@@ -124,6 +124,14 @@ __device__ __forceinline__ int chunk_row_from(const ShortParams &p, const ShortI
     return (blk * p.num_kv_heads + h) * p.block_size + key0 % p.block_size;
 }
 
+// The request's context.  Cross attention (a windowed step without a context array) has every
+// row behind the request's keys, none of which is hidden.
+template <bool WIN>
+__device__ __forceinline__ int context_of(const ShortParams &p, const ShortItem &item) {
+    if (WIN && !p.ctx) return item.seq_len;
+    return __ldg(p.ctx + item.b);
+}
+
 // Work item idx: its record and kv head (a windowed step's records are per head).
 template <bool WIN>
 __device__ __forceinline__ ShortItem short_work(const ShortParams &p, int idx, int &h) {
@@ -280,7 +288,7 @@ __global__ void __launch_bounds__(kShortThreads, 2)
         if (q_bytes <= kPrefetchQMaxBytes) l2_prefetch_slice(p.q, q_bytes, part, parts, lane);
         if (part == 0) {
             l2_prefetch_slice(p.qsl, (p.num_seqs + 1) * sizeof(int), 0, 1, lane);
-            l2_prefetch_slice(p.ctx, p.num_seqs * sizeof(int), 0, 1, lane);
+            l2_prefetch_slice(p.ctx, p.num_seqs * sizeof(int), 0, 1, lane);  // (none: cross attention)
         }
     }
     __syncthreads();
@@ -326,7 +334,7 @@ __global__ void __launch_bounds__(kShortThreads, 2)
             bool has;
             const int blk = chunk_blk_load<WIN>(p, cur, cur.seq_len, cur.stage_begin, lane, has);
             cur_q0 = __ldg(p.qsl + cur.b);
-            cur_ctx = __ldg(p.ctx + cur.b);
+            cur_ctx = context_of<WIN>(p, cur);
             cur_row = chunk_row_from<WIN>(p, cur, blk, has, cur_h, cur.stage_begin, lane);
         }
         while (!aborted) {
@@ -389,7 +397,7 @@ __global__ void __launch_bounds__(kShortThreads, 2)
                             nxt_blk = chunk_blk_load<WIN>(p, nxt, nxt.seq_len, nxt.stage_begin,
                                                           lane, nxt_has);
                             nxt_q0 = __ldg(p.qsl + nxt.b);
-                            nxt_ctx = __ldg(p.ctx + nxt.b);
+                            nxt_ctx = context_of<WIN>(p, nxt);
                         }
                         pf = 2;
                     }

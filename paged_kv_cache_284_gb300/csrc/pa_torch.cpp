@@ -1,5 +1,6 @@
-// pa_torch.cpp -- the plain calls of pa_window_attention, pa_rope_write_kv and
-// pa_copy_blocks from Python straight into libpa.so.
+// pa_torch.cpp -- the plain calls of pa_window_attention, pa_cross_attention,
+// pa_linear_attention, pa_rope_write_kv, pa_copy_blocks and pa_build_step from Python
+// straight into libpa.so.
 //
 // A small step's kernels take 2 to 8 us; reading fifteen tensors' types, devices,
 // shapes and pointers through Python attributes took 6 us and ctypes one more (a call
@@ -24,6 +25,9 @@ namespace {
 decltype(&pa_window_attention) g_window = nullptr;
 decltype(&pa_rope_write_kv) g_rope = nullptr;
 decltype(&pa_copy_blocks) g_copy = nullptr;
+decltype(&pa_cross_attention) g_cross = nullptr;
+decltype(&pa_linear_attention) g_linear = nullptr;
+decltype(&pa_build_step) g_build = nullptr;
 
 // The arguments of a call; `plain` turns false at the first that is not as
 // documented.
@@ -183,6 +187,143 @@ PyObject *window_attention(PyObject *, PyObject *const *args, Py_ssize_t n) {
     }
 }
 
+// q, k_cache, v_cache, block_tables, query_start_loc, encoder_lens, scale, out, lse,
+// workspace, stream, k_scale, v_scale
+PyObject *cross_attention(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 13 || !g_cross) return finish(-1);
+    try {
+        Args a{args};
+        pa_kv_desc kv{};
+        const at::Tensor *q = a.dense(0, at::kBFloat16);
+        a.pool(1, 11, &kv);
+        const at::Tensor *tables = a.dense(3, at::kInt), *qsl = a.dense(4, at::kInt),
+                         *lens = a.dense(5, at::kInt);
+        const double scale = a.number(6);
+        const at::Tensor *out = a.dense(7, at::kBFloat16);
+        const at::Tensor *lse = a.none(8) ? nullptr : a.dense(8, at::kFloat);
+        const at::Tensor *ws = a.tensor(9);
+        if (!a.plain) return finish(-1);
+        a.need(q->dim() == 3 && out->sizes() == q->sizes() && tables->dim() == 2 &&
+               ws->is_cuda() && ws->get_device() == a.device && ws->is_contiguous());
+        if (!a.plain) return finish(-1);
+        const int64_t T = q->size(0), hq = q->size(1), B = lens->numel();
+        a.need(q->size(2) == kv.head_dim && tables->size(0) == B && qsl->numel() == B + 1 &&
+               (!lse || lse->numel() == T * hq) && T <= INT32_MAX && hq <= INT32_MAX &&
+               B <= INT32_MAX && tables->size(1) <= INT32_MAX);
+        void *stream = a.stream(10);
+        if (!a.plain) return finish(-1);
+        void *qp = q->data_ptr(), *op = out->data_ptr(), *wp = ws->data_ptr();
+        const int32_t *tp = data<int32_t>(tables), *qslp = data<int32_t>(qsl),
+                      *lp = data<int32_t>(lens);
+        float *lsep = data<float>(lse);
+        const int64_t width = tables->size(1);
+        const size_t bytes = ws->nbytes();
+        return launch([&] {
+            return g_cross(qp, &kv, tp, static_cast<int32_t>(width), qslp, lp,
+                           static_cast<int32_t>(B), static_cast<int32_t>(T),
+                           static_cast<int32_t>(hq), static_cast<float>(scale), op, lsep, wp, bytes,
+                           stream);
+        });
+    } catch (...) {
+        PyErr_Clear();
+        return finish(-1);
+    }
+}
+
+// q, k, v, query_start_loc, log_decay, state, state_in, state_out, scale, out, workspace,
+// stream
+PyObject *linear_attention(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 12 || !g_linear) return finish(-1);
+    try {
+        Args a{args};
+        int64_t ks = 0, vs = 0, qs = 0;
+        const at::Tensor *q = a.token_rows(0, &qs), *k = a.token_rows(1, &ks),
+                         *v = a.token_rows(2, &vs);
+        const at::Tensor *qsl = a.dense(3, at::kInt), *decay = a.dense(4, at::kFloat),
+                         *state = a.dense(5, at::kFloat), *in = a.dense(6, at::kInt),
+                         *to = a.dense(7, at::kInt);
+        const double scale = a.number(8);
+        const at::Tensor *out = a.dense(9, at::kBFloat16);
+        const at::Tensor *ws = a.tensor(10);
+        if (!a.plain) return finish(-1);
+        const int64_t T = q->size(0), hq = q->size(1), hkv = k->size(1), d = q->size(2);
+        const int64_t B = in->numel();
+        a.need(k->size(0) == T && k->size(2) == d && v->sizes() == k->sizes() &&
+               out->sizes() == q->sizes() && state->dim() == 4 && state->size(1) == hkv &&
+               state->size(2) == d && state->size(3) == d && to->numel() == B &&
+               qsl->numel() == B + 1 && ws->is_cuda() && ws->get_device() == a.device &&
+               ws->is_contiguous() && T <= INT32_MAX && hq <= INT32_MAX && hkv <= INT32_MAX &&
+               B <= INT32_MAX && d <= INT32_MAX && state->size(0) <= INT32_MAX);
+        a.need((decay->dim() == 1 && decay->size(0) == hkv) ||
+               (decay->dim() == 2 && decay->size(0) == T && decay->size(1) == hkv));
+        void *stream = a.stream(11);
+        if (!a.plain) return finish(-1);
+        pa_linear_desc desc{};
+        desc.state = data<float>(state);
+        desc.num_slots = static_cast<int32_t>(state->size(0));
+        desc.num_q_heads = static_cast<int32_t>(hq);
+        desc.num_kv_heads = static_cast<int32_t>(hkv);
+        desc.head_dim = static_cast<int32_t>(d);
+        desc.decay_per_token = decay->dim() == 2;
+        desc.scale = static_cast<float>(scale);
+        void *qp = q->data_ptr(), *kp = k->data_ptr(), *vp = v->data_ptr(), *op = out->data_ptr(),
+             *wp = ws->data_ptr();
+        const int32_t *qslp = data<int32_t>(qsl), *ip = data<int32_t>(in), *tp = data<int32_t>(to);
+        const float *gp = data<float>(decay);
+        const size_t bytes = ws->nbytes();
+        return launch([&] {
+            return g_linear(qp, qs, kp, ks, vp, vs, qslp, static_cast<int32_t>(B),
+                            static_cast<int32_t>(T), gp, &desc, ip, tp, op, wp, bytes, stream);
+        });
+    } catch (...) {
+        PyErr_Clear();
+        return finish(-1);
+    }
+}
+
+// query_lens, cached_lens, block_tables, free_blocks, free_state, num_blocks, block_size,
+// query_start_loc, context_lens, seq_lens, slot_mapping, positions, free_state_out, stream
+PyObject *build_step(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 14 || !g_build) return finish(-1);
+    try {
+        Args a{args};
+        const at::Tensor *q = a.dense(0, at::kInt), *cached = a.dense(1, at::kInt),
+                         *tables = a.dense(2, at::kInt), *blocks = a.dense(3, at::kInt),
+                         *state = a.dense(4, at::kInt);
+        const int64_t num_blocks = a.integer(5), block_size = a.integer(6);
+        const at::Tensor *qsl = a.dense(7, at::kInt), *ctx = a.dense(8, at::kInt),
+                         *seq = a.dense(9, at::kInt), *slots = a.dense(10, at::kLong),
+                         *positions = a.dense(11, at::kInt), *state_out = a.dense(12, at::kInt);
+        if (!a.plain) return finish(-1);
+        const int64_t B = q->numel(), T = slots->numel();
+        a.need(cached->numel() == B && tables->dim() == 2 && tables->size(0) == B &&
+               qsl->numel() == B + 1 && ctx->numel() == B && seq->numel() == B &&
+               positions->numel() == T && state->numel() == 4 && state_out->numel() == 4 &&
+               B <= INT32_MAX && T <= INT32_MAX && tables->size(1) <= INT32_MAX &&
+               blocks->numel() <= INT32_MAX);
+        void *stream = a.stream(13);
+        if (!a.plain) return finish(-1);
+        pa_free_list list{};
+        list.blocks = data<int32_t>(blocks);
+        list.state = data<int32_t>(state);
+        list.state_out = data<int32_t>(state_out);
+        list.capacity = static_cast<int32_t>(blocks->numel());
+        const int32_t *qp = data<int32_t>(q), *cp = data<int32_t>(cached);
+        int32_t *tp = data<int32_t>(tables), *qslp = data<int32_t>(qsl), *xp = data<int32_t>(ctx),
+                *sp = data<int32_t>(seq), *pp = data<int32_t>(positions);
+        int64_t *slp = data<int64_t>(slots);
+        const int64_t width = tables->size(1);
+        return launch([&] {
+            return g_build(qp, cp, static_cast<int32_t>(B), tp, static_cast<int32_t>(width), &list,
+                           static_cast<int32_t>(num_blocks), static_cast<int32_t>(block_size),
+                           static_cast<int32_t>(T), qslp, xp, sp, slp, pp, stream);
+        });
+    } catch (...) {
+        PyErr_Clear();
+        return finish(-1);
+    }
+}
+
 // q, k, v, positions, inv_freq, axis, slot_mapping, k_cache, v_cache, q_out, adjacent,
 // attn_factor, stream, k_scale, v_scale
 PyObject *rope_write_kv(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -259,19 +400,23 @@ PyObject *copy_blocks(PyObject *, PyObject *const *args, Py_ssize_t n) {
     }
 }
 
-// bind(addresses of pa_window_attention, pa_rope_write_kv and pa_copy_blocks of the loaded
-// libpa.so)
+// bind(addresses of pa_window_attention, pa_rope_write_kv, pa_copy_blocks,
+// pa_cross_attention, pa_linear_attention and pa_build_step of the loaded libpa.so)
 PyObject *bind(PyObject *, PyObject *const *args, Py_ssize_t n) {
-    if (n != 3) {
-        PyErr_SetString(PyExc_TypeError, "bind(window_attention, rope_write_kv, copy_blocks)");
+    void *f[6];
+    if (n != 6) {
+        PyErr_SetString(PyExc_TypeError, "bind(window_attention, rope_write_kv, copy_blocks, "
+                                         "cross_attention, linear_attention, build_step)");
         return nullptr;
     }
-    void *w = PyLong_AsVoidPtr(args[0]), *r = PyLong_AsVoidPtr(args[1]),
-         *c = PyLong_AsVoidPtr(args[2]);
+    for (int i = 0; i < 6; ++i) f[i] = PyLong_AsVoidPtr(args[i]);
     if (PyErr_Occurred()) return nullptr;
-    g_window = reinterpret_cast<decltype(g_window)>(w);
-    g_rope = reinterpret_cast<decltype(g_rope)>(r);
-    g_copy = reinterpret_cast<decltype(g_copy)>(c);
+    g_window = reinterpret_cast<decltype(g_window)>(f[0]);
+    g_rope = reinterpret_cast<decltype(g_rope)>(f[1]);
+    g_copy = reinterpret_cast<decltype(g_copy)>(f[2]);
+    g_cross = reinterpret_cast<decltype(g_cross)>(f[3]);
+    g_linear = reinterpret_cast<decltype(g_linear)>(f[4]);
+    g_build = reinterpret_cast<decltype(g_build)>(f[5]);
     Py_RETURN_NONE;
 }
 
@@ -286,6 +431,9 @@ PyMethodDef methods[] = {
     {"window_attention", fast<window_attention>(), METH_FASTCALL, nullptr},
     {"rope_write_kv", fast<rope_write_kv>(), METH_FASTCALL, nullptr},
     {"copy_blocks", fast<copy_blocks>(), METH_FASTCALL, nullptr},
+    {"cross_attention", fast<cross_attention>(), METH_FASTCALL, nullptr},
+    {"linear_attention", fast<linear_attention>(), METH_FASTCALL, nullptr},
+    {"build_step", fast<build_step>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pa_torch", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

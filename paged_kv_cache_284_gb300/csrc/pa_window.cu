@@ -171,10 +171,10 @@ __global__ void __launch_bounds__(DirectGeom<D, FP8, PER_SM>::kThreads, PER_SM)
     const int b_end = min(p.num_seqs, (tid + 1) * each);
     auto pieces_of = [&](int b, int &q0, int &n, int &ctx) {
         q0 = __ldg(p.qsl + b);
-        ctx = __ldg(p.ctx + b);
         const int q1 = __ldg(p.qsl + b + 1), len = __ldg(p.seq_lens + b);
+        ctx = p.ctx ? __ldg(p.ctx + b) : len;  // (cross attention: every row behind all keys)
         n = q1 - q0;
-        if (n < 0 || ctx < 0 || len > dp.max_keys || len != ctx + n || q0 < 0 ||
+        if (n < 0 || ctx < 0 || len > dp.max_keys || (p.ctx && len != ctx + n) || q0 < 0 ||
             q1 > p.num_q_tokens) {
             if (blockIdx.x == 0) flag_status(p.status, PA_DEV_BAD_METADATA);
             n = 0;
@@ -215,7 +215,8 @@ __global__ void __launch_bounds__(DirectGeom<D, FP8, PER_SM>::kThreads, PER_SM)
             }
         const int begin = (piece - at) * dp.piece_tokens;
         const int count = min(dp.piece_tokens, n - begin);
-        const KeySpan ks = key_span(p.win, ctx + begin, ctx + begin + count);
+        const int pos = p.ctx ? ctx + begin : ctx;
+        const KeySpan ks = key_span(p.win, pos, p.ctx ? pos + count : ctx);
         Work *work = works + k;
         work->b = b;
         work->q_count = count;
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(DirectGeom<D, FP8, PER_SM>::kThreads, PER_SM)
         work->key_end = ks.keys;
         work->chunks = (ks.keys + kChunkKeys - 1) / kChunkKeys;
         work->tok0 = q0 + begin;
-        work->ctx = ctx + begin - ks.gap * kChunkKeys;
+        work->ctx = pos - ks.gap * kChunkKeys;
     }
     __syncthreads();
 

@@ -198,7 +198,8 @@ __global__ void __launch_bounds__(256) stage_fp8_kernel(
             int j = k - __ldcg(stage_base + b);
             if constexpr (WIN) {
                 const BlockSpan bsp =
-                    block_span(win, __ldg(ctx + b), __ldg(seq_lens + b), block_size);
+                    block_span(win, ctx ? __ldg(ctx + b) : __ldg(seq_lens + b),
+                               __ldg(seq_lens + b), block_size);
                 if (j >= bsp.sink_blocks) j += bsp.gap;
             }
             int src = (j < bt_stride) ? __ldg(bt + static_cast<int64_t>(b) * bt_stride + j) : -1;
