@@ -592,11 +592,14 @@ int pa_set_profile_events(int32_t which, void *start_event, void *end_event);
  *   PA_TEST_STALL_ROPE        in every later pa_rope_write_kv, CTA 0's first
  *                             warp does not fetch the second of its items: it
  *                             writes the first, times out and returns.
+ *   PA_TEST_STALL_LINEAR      in every later prompt launch of pa_linear_attention, CTA 0
+ *                             loads one chunk: whoever waits for the next one
+ *                             times out.  The step's result is then incomplete.
  * Process-wide, read at launch time; set it from one thread, with no call
  * of this library in flight on the host.
  */
 enum { PA_TEST_STALL_NONE = 0, PA_TEST_STALL_SPLIT_KV = 1, PA_TEST_STALL_LAST_GRID = 2,
-       PA_TEST_STALL_TENSOR_CORE = 3, PA_TEST_STALL_ROPE = 4 };
+       PA_TEST_STALL_TENSOR_CORE = 3, PA_TEST_STALL_ROPE = 4, PA_TEST_STALL_LINEAR = 5 };
 int pa_set_test_stall(int32_t which);
 
 /*

@@ -873,7 +873,7 @@ def partition_requests(seq_lens, num_ranks: int):
 
 
 (PA_TEST_STALL_NONE, PA_TEST_STALL_SPLIT_KV, PA_TEST_STALL_LAST_GRID,
- PA_TEST_STALL_TENSOR_CORE, PA_TEST_STALL_ROPE) = range(5)
+ PA_TEST_STALL_TENSOR_CORE, PA_TEST_STALL_ROPE, PA_TEST_STALL_LINEAR) = range(6)
 
 
 def set_test_stall(which: int):

@@ -18,7 +18,8 @@ LIB = os.path.join(PKG, "libpa.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 SOURCES = ["pa_api.cu", "pa_write_kv.cu", "pa_plan.cu", "pa_plan_window.cu", "pa_short.cu",
            "pa_long.cu", "pa_long_window.cu", "pa_window.cu", "pa_merge.cu", "pa_static.cu",
-           "pa_rope.cu", "pa_copy.cu", "pa_build.cu", "pa_linear.cu", "pa_blocks.cpp", "pa_shard.cpp"]
+           "pa_rope.cu", "pa_copy.cu", "pa_build.cu", "pa_linear.cu",
+           "pa_linear_prompt.cu", "pa_blocks.cpp", "pa_shard.cpp"]
 BINDING = "pa_torch.cpp"  # -> _pa_torch.so, host code that reads torch's tensors
 BINDING_LIB = os.path.join(PKG, "_pa_torch.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

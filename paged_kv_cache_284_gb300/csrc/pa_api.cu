@@ -118,6 +118,24 @@ int make_q_map(CUtensorMap *m, const void *q, int tokens, int heads, int head_di
     return r == CUDA_SUCCESS ? PA_OK : fail(PA_ERR_CUDA, "Q tensor map encode failed (%d)", (int)r);
 }
 
+// 3-D view of bf16 rows [tokens][heads][head_dim], tokens `stride` elements apart; a box is 64
+// dims x box_heads heads x kLinearChunk tokens.
+int make_rows_map(CUtensorMap *m, const void *base, int tokens, int heads, int head_dim,
+                  int64_t stride, int box_heads) {
+    auto fn = encode_fn();
+    if (!fn) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(heads),
+                          static_cast<cuuint64_t>(tokens)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2,
+                             static_cast<cuuint64_t>(stride) * 2};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), kLinearChunk};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PA_OK : fail(PA_ERR_CUDA, "row tensor map encode failed (%d)", (int)r);
+}
+
 std::atomic<unsigned long long> g_launches{0};
 std::atomic<int> g_test_stall{PA_TEST_STALL_NONE};  // pa_set_test_stall
 std::atomic<uint64_t *> g_tile_counter{nullptr};     // pa_set_tile_counter
@@ -1393,7 +1411,23 @@ int pa_linear_attention(const void *q, int64_t q_stride, const void *k, int64_t 
     p.num_slots = desc->num_slots;
     p.scale = desc->scale;
     p.status = dev->status;
-    rc = launch_linear_step(p, d, static_cast<cudaStream_t>(stream));
+    p.max_rows = kLinearStepRows;
+    p.heads_per_tile = std::min(2, p.group);
+    p.test_stall = g_test_stall.load(std::memory_order_relaxed) == PA_TEST_STALL_LINEAR ? 1 : 0;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (num_tokens > kLinearStepRows) {
+        // a request may be long: the prompt kernel first, the recurrent form beside it
+        CUtensorMap tq, tk, tv;
+        if ((rc = make_rows_map(&tq, q, num_tokens, hq, d, q_stride, p.heads_per_tile)) != PA_OK ||
+            (rc = make_rows_map(&tk, k, num_tokens, hkv, d, k_stride, 1)) != PA_OK ||
+            (rc = make_rows_map(&tv, v, num_tokens, hkv, d, v_stride, 1)) != PA_OK)
+            return rc;
+        rc = launch_linear_prompt(p, tq, tk, tv, d, dev->sms, s);
+        if (rc != PA_OK) return fail(rc, "linear prompt launch failed: %s",
+                                     cudaGetErrorString(cudaGetLastError()));
+        p.overlap = 1;
+    }
+    rc = launch_linear_step(p, d, s);
     return rc == PA_OK ? PA_OK : fail(rc, "linear attention launch failed: %s",
                                       cudaGetErrorString(cudaGetLastError()));
 }
@@ -1737,7 +1771,7 @@ int pa_set_tile_counter(uint64_t *counter) {
 
 int pa_set_test_stall(int32_t which) {
     g_err[0] = 0;
-    if (which < PA_TEST_STALL_NONE || which > PA_TEST_STALL_ROPE)
+    if (which < PA_TEST_STALL_NONE || which > PA_TEST_STALL_LINEAR)
         return fail(PA_ERR_INVALID_ARG, "unknown test stall %d", which);
     g_test_stall.store(which, std::memory_order_relaxed);
     return PA_OK;

@@ -357,7 +357,16 @@ struct LinearParams {
     int num_seqs, num_tokens, num_q_heads, num_kv_heads, group, num_slots;
     float scale;
     unsigned *status;
+    // requests of more than max_rows tokens are the prompt kernel's; overlap: launched beside
+    // it, which has waited for whatever wrote the inputs
+    int max_rows, overlap;
+    int heads_per_tile;  // prompt kernel: query heads of a tile (1 or 2)
+    int test_stall;      // test hook: CTA 0's loads stop after one chunk
 };
+// Requests of up to this many tokens take the recurrent form.
+constexpr int kLinearStepRows = 16;
+// Tokens of a chunk of the prompt kernel, and rows (tokens x heads) of its query tiles.
+constexpr int kLinearChunk = 64;
 
 // The cache arrays of one pa_copy_blocks launch: K and V of up to
 // kCopyLayers layers.
@@ -441,6 +450,8 @@ int launch_copy_blocks(const pa_kv_desc *kv, int num_layers, const int32_t *pair
                        int sms, unsigned *status, cudaStream_t s);
 int launch_build_step(const BuildParams &p, cudaStream_t s);
 int launch_linear_step(const LinearParams &p, int head_dim, cudaStream_t s);
+int launch_linear_prompt(const LinearParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
+                         const CUtensorMap &tv, int head_dim, int sms, cudaStream_t s);
 int launch_plan(const PlanParams &p, cudaStream_t s);
 int launch_plan_window(const PlanParams &p, cudaStream_t s);
 int launch_short(const ShortParams &p, const CUtensorMap &tk, const CUtensorMap &tv,
@@ -636,6 +647,12 @@ __device__ __forceinline__ uint32_t cluster_addr(const void *local, int rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
     return a;
 }
+__device__ __forceinline__ float ld_cluster_f1(const void *local, int rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                 : "=f"(v) : "r"(cluster_addr(local, rank)) : "memory");
+    return v;
+}
 __device__ __forceinline__ float2 ld_cluster_f2(const void *local, int rank) {
     float2 v;
     asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
@@ -809,11 +826,14 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr, uint32_t lbo,
     return d;
 }
 // Instruction descriptor for kind::f16 with bf16 A/B and fp32 accumulate.
-// b_mn_major: B operand stored N-contiguous (e.g. V rows for P*V).
-__host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int b_mn_major) {
+// b_mn_major: B operand stored N-contiguous (e.g. V rows for P*V); a_mn_major: A stored
+// M-contiguous (K rows for K^T V).
+__host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int b_mn_major,
+                                                      int a_mn_major = 0) {
     return (1u << 4)                                  // D format: f32
            | (1u << 7)                                // A format: bf16
            | (1u << 10)                               // B format: bf16
+           | (static_cast<uint32_t>(a_mn_major) << 15)  // A major-ness
            | (static_cast<uint32_t>(b_mn_major) << 16)  // B major-ness
            | (static_cast<uint32_t>(N >> 3) << 17)    // N / 8
            | (static_cast<uint32_t>(M >> 4) << 24);   // M / 16
@@ -861,6 +881,45 @@ __device__ __forceinline__ void tmem_wait_ld() {
 __device__ __forceinline__ void tmem_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
+// MMA and commit issued by the elected lane of a warp whose lanes all run the
+// surrounding code: operands stay in uniform registers.  (Inside a branch of
+// one lane each MMA took ~80 cycles to issue, 645 for a tile's eight.)
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e;
+}
+__device__ __forceinline__ void mma_ss(uint32_t elected, uint32_t d_tmem, uint64_t adesc,
+                                       uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t elected, uint32_t d_tmem, uint32_t a_tmem,
+                                       uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t elected, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_u32(bar)),
+        "r"(elected)
+        : "memory");
+}
+
 // 32 lanes x 32 columns of 32-bit TMEM cells: thread i gets lane (base+i),
 // columns col..col+31.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {

@@ -30,7 +30,7 @@ struct StepGeom {
 }  // namespace
 
 template <int D, int COLS>
-__global__ void __launch_bounds__(kThreads) linear_step_kernel(const LinearParams p) {
+__device__ __forceinline__ void step_job(const LinearParams &p) {
     using G = StepGeom<D, COLS>;
     constexpr int R = G::kRows, kSlices = D / COLS;
     __shared__ float s_q[kHeadBatch][D], s_k[D], s_v[COLS];
@@ -39,15 +39,14 @@ __global__ void __launch_bounds__(kThreads) linear_step_kernel(const LinearParam
     const int slice = blockIdx.x % kSlices, job = blockIdx.x / kSlices;
     const int b = job / p.num_kv_heads, h = job - b * p.num_kv_heads;
     const int col = (lane % G::kLanes) * 4, row0 = (warp * G::kSub + lane / G::kLanes) * R;
-    pdl_wait();
-    pdl_trigger();
     const int t0 = __ldg(p.qsl + b), n = __ldg(p.qsl + b + 1) - t0;
     int in = __ldg(p.state_in + b), to = __ldg(p.state_out + b);
-    unsigned flags = 0;
     if (n < 0 || t0 < 0 || t0 > p.num_tokens - n) {
         if (tid == 0) flag_status(p.status, PA_DEV_BAD_METADATA);
         return;
     }
+    if (n > p.max_rows) return;
+    unsigned flags = 0;
     if (in >= p.num_slots) flags |= PA_DEV_BAD_SLOT, in = -1;
     if (to >= p.num_slots) flags |= PA_DEV_BAD_SLOT, to = -1;
     if (flags && tid == 0) flag_status(p.status, flags);
@@ -123,6 +122,18 @@ __global__ void __launch_bounds__(kThreads) linear_step_kernel(const LinearParam
 #pragma unroll
     for (int i = 0; i < R; ++i) *reinterpret_cast<float4 *>(dst + i * D) = s[i];
 }
+
+template <int D, int COLS>
+__global__ void __launch_bounds__(kThreads) linear_step_kernel(const LinearParams p) {
+    // Beside the prompt kernel, which has waited for whatever wrote the inputs, there is nothing
+    // to wait for: its rows and slots are others.  This grid then ends after that one, so that
+    // what follows comes after both.
+    if (!p.overlap) pdl_wait();
+    pdl_trigger();
+    step_job<D, COLS>(p);
+    if (p.overlap) pdl_wait();
+}
+
 
 namespace {
 

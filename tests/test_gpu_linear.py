@@ -265,3 +265,23 @@ def test_refusals():
             s.call(t, **kw)
         s.scale = 0.125
     assert_status_clean()
+
+
+def test_a_wait_that_runs_out():
+    """CTA 0 loads one chunk: its waits give up after 2 s, the status says so, and the next call
+    is right again.  One CTA to a request, and a cluster (whose barriers are met all the same)."""
+    for lens in ([200] * 90, [900]):
+        s = Step(lens, 4, 2, 128, seed=1)
+        t = s.to_dev()
+        pk.set_test_stall(pk.PA_TEST_STALL_LINEAR)
+        try:
+            s.call(t)
+        finally:
+            pk.set_test_stall(pk.PA_TEST_STALL_NONE)
+        torch.cuda.synchronize()
+        assert pk.read_device_status(clear=True) == pk.PA_DEV_WAIT_TIMEOUT
+        assert pk.read_device_status() == 0
+        t = s.to_dev()
+        s.call(t)
+        s.check(t)
+        assert_status_clean()
