@@ -1411,11 +1411,14 @@ int pa_linear_attention(const void *q, int64_t q_stride, const void *k, int64_t 
     p.num_slots = desc->num_slots;
     p.scale = desc->scale;
     p.status = dev->status;
-    p.max_rows = kLinearStepRows;
+    // a step of few tokens a request is taken to have no prompt: the recurrent form has them all
+    const bool prompts = num_tokens > kLinearStepRows &&
+                         num_tokens > kLinearStepMeanRows * static_cast<int64_t>(num_seqs);
+    p.max_rows = prompts ? kLinearStepRows : 0x7fffffff;
     p.heads_per_tile = std::min(2, p.group);
     p.test_stall = g_test_stall.load(std::memory_order_relaxed) == PA_TEST_STALL_LINEAR ? 1 : 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (num_tokens > kLinearStepRows) {
+    if (prompts) {
         // a request may be long: the prompt kernel first, the recurrent form beside it
         CUtensorMap tq, tk, tv;
         if ((rc = make_rows_map(&tq, q, num_tokens, hq, d, q_stride, p.heads_per_tile)) != PA_OK ||

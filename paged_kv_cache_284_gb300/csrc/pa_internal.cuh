@@ -365,6 +365,8 @@ struct LinearParams {
 };
 // Requests of up to this many tokens take the recurrent form.
 constexpr int kLinearStepRows = 16;
+// ... and all requests of a step of at most this many tokens on average.
+constexpr int kLinearStepMeanRows = 6;
 // Tokens of a chunk of the prompt kernel, and rows (tokens x heads) of its query tiles.
 constexpr int kLinearChunk = 64;
 
@@ -624,6 +626,42 @@ __device__ __forceinline__ bool warp_mbar_wait_spin(uint64_t *bar, uint32_t pari
     __syncwarp();
     return ok != 0;
 }
+// mbar_try_wait that suspends the thread for up to `ns`, so that a waiting warp leaves the others
+// its issue slots.
+__device__ __forceinline__ bool mbar_try_wait_for(uint64_t *bar, uint32_t parity, uint32_t ns) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
+        : "memory");
+    return ok != 0;
+}
+// mbar_wait and warp_mbar_wait in few instructions, for kernels with many waits and many waiting
+// warps.  The bound is 2 s at 2.1 GHz, by the SM's clock.
+__device__ __forceinline__ bool mbar_wait_small(uint64_t *bar, uint32_t parity,
+                                                volatile int *abort) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    bool ok = false;
+#pragma unroll 1
+    while (!ok && !*abort) {
+        ok = mbar_try_wait_for(bar, parity, 20000);
+        if (clock64() - t0 > 4200000000ll) *abort = 1;
+    }
+    return ok;
+}
+__device__ __forceinline__ bool warp_mbar_wait_small(uint64_t *bar, uint32_t parity,
+                                                     volatile int *abort) {
+    int ok = 1;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait_small(bar, parity, abort) ? 1 : 0;
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (ok) (void)mbar_try_wait(bar, parity);
+    __syncwarp();
+    return ok != 0;
+}
 // Short bounded wait used only while draining after an abort.
 __device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity) {
     const uint64_t t0 = global_timer_ns();
@@ -647,11 +685,13 @@ __device__ __forceinline__ uint32_t cluster_addr(const void *local, int rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
     return a;
 }
-__device__ __forceinline__ float ld_cluster_f1(const void *local, int rank) {
+__device__ __forceinline__ float ld_cluster_at(uint32_t addr) {
     float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                 : "=f"(v) : "r"(cluster_addr(local, rank)) : "memory");
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
+}
+__device__ __forceinline__ float ld_cluster_f1(const void *local, int rank) {
+    return ld_cluster_at(cluster_addr(local, rank));
 }
 __device__ __forceinline__ float2 ld_cluster_f2(const void *local, int rank) {
     float2 v;
@@ -935,6 +975,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
           "=r"(r[31])
         : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -955,6 +1004,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
         "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
         : "memory");
 }
 // One 32-bit TMEM cell per thread (lane = thread, one column).

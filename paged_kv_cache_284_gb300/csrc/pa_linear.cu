@@ -4,8 +4,9 @@
 // query heads read the same one.
 //
 // A CTA holds COLS columns of one state in registers (columns do not depend on each other)
-// and takes the request's tokens in turn: k and q of a token in shared memory, each thread
-// four columns of R rows, then a sum over the rows through shared memory.
+// and takes the request's tokens in turn, a block of them at a time in shared memory: each
+// thread has four columns of R rows, and a sum over the rows goes through shared memory, with one
+// barrier for four query heads of a token.
 // Bound for single tokens: HBM, each state read and written once.
 #include <algorithm>
 
@@ -18,6 +19,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kHeadBatch = 4;  // query heads summed at once
+constexpr int kQRows = 32;     // query rows (tokens x heads) in shared memory
+constexpr int kTokens = 8;     // tokens of a block
 
 template <int D, int COLS>
 struct StepGeom {
@@ -33,8 +36,9 @@ template <int D, int COLS>
 __device__ __forceinline__ void step_job(const LinearParams &p) {
     using G = StepGeom<D, COLS>;
     constexpr int R = G::kRows, kSlices = D / COLS;
-    __shared__ float s_q[kHeadBatch][D], s_k[D], s_v[COLS];
-    __shared__ float s_part[kWarps][kHeadBatch][COLS];
+    __shared__ __align__(16) __nv_bfloat16 s_q[kQRows][D], s_k[kTokens][D], s_v[kTokens][COLS];
+    __shared__ float s_keep[kTokens];
+    __shared__ __align__(16) float s_part[2][kWarps][kHeadBatch][COLS];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int slice = blockIdx.x % kSlices, job = blockIdx.x / kSlices;
     const int b = job / p.num_kv_heads, h = job - b * p.num_kv_heads;
@@ -62,58 +66,87 @@ __device__ __forceinline__ void step_job(const LinearParams &p) {
         s[i] = in >= 0 ? *reinterpret_cast<const float4 *>(src + i * D)
                        : make_float4(0.f, 0.f, 0.f, 0.f);
 
-    for (int t = t0; t < t0 + n; ++t) {
-        const __nv_bfloat16 *kt = p.k + t * p.k_stride + h * D;
-        const __nv_bfloat16 *vt = p.v + t * p.v_stride + h * D + slice * COLS;
-        for (int i = tid; i < D; i += kThreads) s_k[i] = __bfloat162float(kt[i]);
-        for (int i = tid; i < COLS; i += kThreads) s_v[i] = __bfloat162float(vt[i]);
-        // a positive or NaN logarithm counts as 0, so that no state grows by its decay
-        const float g = __ldg(p.decay + static_cast<int64_t>(t) * p.decay_stride + h);
-        const float keep = expf(g < 0.f ? g : 0.f);
-        for (int g0 = 0; g0 < p.group; g0 += kHeadBatch) {
-            const int heads = min(kHeadBatch, p.group - g0);
-            const __nv_bfloat16 *qt = p.q + t * p.q_stride + (h * p.group + g0) * D;
-            for (int i = tid; i < heads * D; i += kThreads)
-                s_q[i / D][i % D] = __bfloat162float(qt[i]);
+    // 16-byte pieces of `rows` rows of `len` elements
+    auto fetch = [&](__nv_bfloat16 *dst, const __nv_bfloat16 *src, int64_t stride, int rows, int len) {
+        const int pieces = len / 8;
+        for (int i = tid; i < rows * pieces; i += kThreads) {
+            const int r = i / pieces, c = i - r * pieces;
+            *reinterpret_cast<uint4 *>(dst + r * len + c * 8) =
+                *reinterpret_cast<const uint4 *>(src + r * stride + c * 8);
+        }
+    };
+    const int block = max(1, min(kTokens, kQRows / p.group));
+    int buf = 0;
+    for (int t = t0; t < t0 + n; t += block) {
+        const int m = min(block, t0 + n - t);
+        if (t > t0) __syncthreads();
+        fetch(&s_k[0][0], p.k + t * p.k_stride + h * D, p.k_stride, m, D);
+        fetch(&s_v[0][0], p.v + t * p.v_stride + h * D + slice * COLS, p.v_stride, m, COLS);
+        if (tid < m) {
+            // a positive or NaN logarithm counts as 0, so that no state grows by its decay
+            const float g = __ldg(p.decay + static_cast<int64_t>(t + tid) * p.decay_stride + h);
+            s_keep[tid] = expf(g < 0.f ? g : 0.f);
+        }
+        // (groups of more than kQRows heads: one token, several turns)
+        for (int g0 = 0; g0 < p.group; g0 += kQRows) {
+            const int heads = min(kQRows, p.group - g0);
+            if (g0 > 0) __syncthreads();
+            for (int i = 0; i < m; ++i)
+                fetch(&s_q[i * heads][0], p.q + (t + i) * p.q_stride + (h * p.group + g0) * D, D,
+                      heads, D);
             __syncthreads();
-            if (g0 == 0) {
-                const float4 v = *reinterpret_cast<const float4 *>(s_v + col);
+            for (int i = 0; i < m; ++i) {
+                if (g0 == 0) {
+                    const float keep = s_keep[i];
+                    const uint2 raw = *reinterpret_cast<const uint2 *>(&s_v[i][col]);
+                    const float4 v = make_float4(
+                        __uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u),
+                        __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xFFFF0000u));
 #pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    const float k = s_k[row0 + i];
-                    s[i].x = fmaf(keep, s[i].x, k * v.x);
-                    s[i].y = fmaf(keep, s[i].y, k * v.y);
-                    s[i].z = fmaf(keep, s[i].z, k * v.z);
-                    s[i].w = fmaf(keep, s[i].w, k * v.w);
+                    for (int x = 0; x < R; ++x) {
+                        const float k = __bfloat162float(s_k[i][row0 + x]);
+                        s[x].x = fmaf(keep, s[x].x, k * v.x);
+                        s[x].y = fmaf(keep, s[x].y, k * v.y);
+                        s[x].z = fmaf(keep, s[x].z, k * v.z);
+                        s[x].w = fmaf(keep, s[x].w, k * v.w);
+                    }
                 }
-            }
-            for (int j = 0; j < heads; ++j) {
-                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int j0 = 0; j0 < heads; j0 += kHeadBatch) {
+                    const int some = min(kHeadBatch, heads - j0);
+                    for (int j = 0; j < some; ++j) {
+                        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                        const __nv_bfloat16 *q = &s_q[i * heads + j0 + j][row0];
 #pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    const float q = s_q[j][row0 + i];
-                    o.x = fmaf(q, s[i].x, o.x);
-                    o.y = fmaf(q, s[i].y, o.y);
-                    o.z = fmaf(q, s[i].z, o.z);
-                    o.w = fmaf(q, s[i].w, o.w);
+                        for (int x = 0; x < R; ++x) {
+                            const float y = __bfloat162float(q[x]);
+                            o.x = fmaf(y, s[x].x, o.x);
+                            o.y = fmaf(y, s[x].y, o.y);
+                            o.z = fmaf(y, s[x].z, o.z);
+                            o.w = fmaf(y, s[x].w, o.w);
+                        }
+#pragma unroll
+                        for (int x = G::kLanes; x < 32; x <<= 1) {
+                            o.x += __shfl_xor_sync(0xffffffffu, o.x, x);
+                            o.y += __shfl_xor_sync(0xffffffffu, o.y, x);
+                            o.z += __shfl_xor_sync(0xffffffffu, o.z, x);
+                            o.w += __shfl_xor_sync(0xffffffffu, o.w, x);
+                        }
+                        if (lane < G::kLanes)
+                            *reinterpret_cast<float4 *>(&s_part[buf][warp][j][col]) = o;
+                    }
+                    __syncthreads();
+                    // (the next sums go to the other buffer, and meet this one's readers at its
+                    // barrier)
+                    for (int y = tid; y < some * COLS; y += kThreads) {
+                        const int j = y / COLS, c = y % COLS;
+                        float o = 0.f;
+#pragma unroll
+                        for (int w = 0; w < kWarps; ++w) o += s_part[buf][w][j][c];
+                        p.out[(static_cast<int64_t>(t + i) * p.num_q_heads + h * p.group + g0 + j0 +
+                               j) * D + slice * COLS + c] = __float2bfloat16(o * p.scale);
+                    }
+                    buf ^= 1;
                 }
-#pragma unroll
-                for (int x = G::kLanes; x < 32; x <<= 1) {
-                    o.x += __shfl_xor_sync(0xffffffffu, o.x, x);
-                    o.y += __shfl_xor_sync(0xffffffffu, o.y, x);
-                    o.z += __shfl_xor_sync(0xffffffffu, o.z, x);
-                    o.w += __shfl_xor_sync(0xffffffffu, o.w, x);
-                }
-                if (lane < G::kLanes) *reinterpret_cast<float4 *>(&s_part[warp][j][col]) = o;
-            }
-            __syncthreads();
-            for (int i = tid; i < heads * COLS; i += kThreads) {
-                const int j = i / COLS, c = i % COLS;
-                float o = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) o += s_part[w][j][c];
-                p.out[(static_cast<int64_t>(t) * p.num_q_heads + h * p.group + g0 + j) * D +
-                      slice * COLS + c] = __float2bfloat16(o * p.scale);
             }
         }
     }

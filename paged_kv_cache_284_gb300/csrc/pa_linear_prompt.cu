@@ -4,21 +4,26 @@
 // With G_i the sum of the logarithms of a chunk's decays up to and with token i, S the state
 // before the chunk and L the chunk's last token,
 //   o_i  = scale (e^(G_i) q_i S + sum_(j <= i) e^(G_i - G_j) (q_i k_j) v_j)
-//   S'   = e^(G_L) S + sum_j (e^(G_L - G_j) k_j) v_j^T
+//   S'   = e^(G_L) S + sum_j k_j (e^(G_L - G_j) v_j)^T
 // Every exponent is at most 0.  Columns of S and of o do not depend on each other, so a CTA
 // has 64 of them (a slice), for one request and kv head, and walks along the request:
 //   scores  Q K^T            M = 64 tokens x 2 query heads of the group (1: half the rows idle)
 //   inside  P V              P = the scores times e^(G_i - G_j), masked, over them in TMEM
 //   before  Q S              S in bf16, in shared memory
-//   update  (K e^(G_L - G))^T V, M = the state's rows
-// Roles: warp 0 loads, warp 1 issues the MMAs, warps 4-7 make P and write the outputs (one
-// thread a row), warps 8-15 weigh K and keep the state: 32 fp32 values of a thread.
+//   update  K^T (e^(G_L - G) V), M = the state's rows
+// Roles: warp 0 loads; warps 1-3 issue the MMAs; warps 4-11, two groups that take
+// the tiles in turn, make P and write the outputs (one thread a row); warps 12-15 weigh V; warps
+// 16-23 keep the state, 32 fp32 values of a thread.  So the chain from one chunk's state to the
+// next (update, sum, rounding) and the chain of the weighed V run beside each other and beside
+// the outputs.  Loops over 16 columns stay loops: with six kinds of warps on a scheduler,
+// straight-line code spends its time waiting for instructions.
+// P's weights: within 16 tokens exponentials, from one run of 16 to a later one products of a
+// factor of the row's and one of the column's.
 //
 // Roundings.  P and the S that Q meets are rounded to bf16, as an MMA's operands must be; both
 // go into an output of bf16.  The state itself is a result in fp32 that later chunks build on,
-// so the weighed K is taken as a sum of two bf16 numbers (rest below 2^-16 of it) and the
-// update's products accumulate in fp32.  With head_dim 64 the two parts are the two halves of
-// an M = 128 MMA, and their states are kept apart until the end.
+// so the weighed V is taken as a sum of three bf16 numbers, which holds all its digits, and the
+// update's products accumulate in fp32.
 //
 // A cluster of up to 8 CTAs shares a request when there are fewer of them than SMs: each rank
 // takes a run of chunks, first makes its run's own update from K and V alone, then the ranks
@@ -35,13 +40,23 @@ namespace {
 constexpr int kC = kLinearChunk;
 constexpr int kSlice = 64;   // state columns of a CTA
 constexpr int kRows = 128;   // rows of a query tile, and of a state's MMA
-constexpr int kThreads = 512;
-constexpr int kWarpMma = 1, kFirstOut = 4, kFirstState = 8;
-constexpr int kOutWarps = 4, kStateWarps = 8;
+constexpr int kWarpQK = 1, kWarpPV = 2, kWarpQS = 3, kFirstOut = 4, kFirstWeigh = 12,
+              kFirstState = 16;
+constexpr int kMmaWarps = 3, kGroupWarps = 4, kWeighWarps = 4, kStateWarps = 8;
+constexpr int kWarps = kFirstState + kStateWarps, kThreads = 32 * kWarps;
 constexpr int kRing = 3;     // chunks of K and V in shared memory
 constexpr int kQueue = 4;
+constexpr int kTables = 4;   // chunks whose sums of logarithms are kept
+constexpr int kParts = 3;    // bf16 numbers whose sum is a weighed element of V
 // Logarithms (base 2) below this are as good as none: what they multiply is 0 in fp32.
 constexpr float kLeastLog = -150.f;
+
+// Of a chunk's tokens: the logarithms' sums up to each (base 2), e^ of what lies between a token
+// and the end of its run of 16, and the whole sum.
+struct alignas(16) Table {
+    float sum[kC], tail[kC];
+    float all, pad[3];
+};
 
 template <int D>
 struct Geom {
@@ -53,32 +68,34 @@ struct Geom {
     static constexpr int kSBytes = kRows * 128;  // bf16 state: 128 rows x 64 columns
     static constexpr int kOffQ = 0;              // [2]
     static constexpr int kOffKV = kOffQ + 2 * kQBytes;
-    static constexpr int kOffKt = kOffKV + kRing * kStageBytes;  // weighed K: first parts, rests
-    static constexpr int kOffS = kOffKt + 2 * kKBytes;           // [2]
+    static constexpr int kOffVt = kOffKV + kRing * kStageBytes;  // weighed V, part after part
+    static constexpr int kOffS = kOffVt + kParts * kVBytes;      // [2]
     static constexpr int kOffBar = kOffS + 2 * kSBytes;
-    static constexpr int kOffG = kOffBar + 256;                  // [2][kC] sums of logarithms
-    static constexpr int kOffCtl = kOffG + 2 * kC * 4;
+    static constexpr int kOffTab = kOffBar + 320;                // [kTables]
+    static constexpr int kOffCtl = kOffTab + kTables * static_cast<int>(sizeof(Table));
     static constexpr int kSmemRaw = kOffCtl + 512 + (kThreads + 1) * 4;
     // one CTA per SM: its TMEM columns are all taken
     static constexpr int kSmemBytes = kSmemRaw > 116 * 1024 ? kSmemRaw : 116 * 1024;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
     static_assert(kOffBar % 1024 == 0, "alignment");
-    // TMEM columns: scores [2], outputs (before | inside) [2], update
+    // TMEM columns: scores [2], outputs (before | inside) [2], updates [2]
     static constexpr uint32_t kTmemCols = 512;
     static constexpr int kColO = 2 * kC, kColU = kColO + 2 * 2 * kSlice;
-    static_assert(kColU + kSlice <= 512, "TMEM");
+    static_assert(kColU + 2 * kSlice <= 512, "TMEM");
 };
 
 struct Bars {
     uint64_t kv_full[kRing], kv_empty[kRing];
     uint64_t q_full[2], q_empty[2];
-    uint64_t kt_full[2], u_full;       // weighed K of a chunk there / its update done
+    // weighed V (and table) of a chunk there; its update done (which frees the weighed V) /
+    // read.  The weighing warps may be two chunks ahead of who looks at their barrier.
+    uint64_t vt_full[kTables], u_full[2], u_empty[2];
     uint64_t s_full[2], s_empty[2];    // state before a chunk in shared memory / read
     uint64_t sc_full[2], p_full[2];    // scores of a tile / its P
     uint64_t o_full[2], o_empty[2];
-    uint64_t drain;
+    uint64_t drain[kMmaWarps];
 };
-static_assert(sizeof(Bars) <= 256, "barrier area");
+static_assert(sizeof(Bars) <= 320, "barrier area");
 
 // One request, kv head and slice, and this rank's run of chunks.
 struct alignas(16) Item {
@@ -89,9 +106,8 @@ struct alignas(16) Item {
 static_assert(sizeof(Item) == 48, "queue entry");
 
 struct Ctl {
-    int abort, published, read[kThreads / 32];
-    uint32_t tmem;
-    int pad;
+    int abort, published, read[kWarps];
+    uint32_t tmem, pad;
     Item items[kQueue];
     float decay;  // of this rank's run, log2 (read by the cluster)
 };
@@ -135,7 +151,8 @@ __device__ Item find_item(const LinearParams &p, const int *count, int k, int ra
     // the thread whose requests hold it: count[owner] <= want < count[owner + 1]
     unsigned m = __ballot_sync(0xffffffffu, count[lane * (kThreads / 32)] <= want);
     const int group = (31 - __clz(m)) * (kThreads / 32);
-    m = __ballot_sync(0xffffffffu, lane < kThreads / 32 && count[group + lane % (kThreads / 32)] <= want);
+    m = __ballot_sync(0xffffffffu,
+                      lane < kThreads / 32 && count[group + lane % (kThreads / 32)] <= want);
     const int owner = group + 31 - __clz(m);
     const int each = (p.num_seqs + kThreads - 1) / kThreads;
     int left = want - count[owner];
@@ -188,6 +205,7 @@ __device__ __forceinline__ Item queue_item(Ctl *ctl, int warp, int k) {
     }
     __syncwarp();
     if (lane == 0) *reinterpret_cast<volatile int *>(&ctl->read[warp]) = k + 1;
+    __syncwarp();
     return it;
 }
 
@@ -201,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     using G = Geom<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     Bars *bars = reinterpret_cast<Bars *>(smem + G::kOffBar);
-    float *s_g = reinterpret_cast<float *>(smem + G::kOffG);
+    Table *tables = reinterpret_cast<Table *>(smem + G::kOffTab);
     Ctl *ctl = reinterpret_cast<Ctl *>(smem + G::kOffCtl);
     int *count = reinterpret_cast<int *>(smem + G::kOffCtl + 512);
     volatile int *abort_flag = &ctl->abort;
@@ -213,30 +231,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&bars->kv_full[i], 1);
-            mbar_init(&bars->kv_empty[i], 1);
+            mbar_init(&bars->kv_empty[i], kMmaWarps);
         }
+        for (int i = 0; i < kMmaWarps; ++i) mbar_init(&bars->drain[i], 1);
+        for (int i = 0; i < kTables; ++i) mbar_init(&bars->vt_full[i], kWeighWarps);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->q_full[i], 1);
-            mbar_init(&bars->q_empty[i], 1);
-            mbar_init(&bars->kt_full[i], kStateWarps);
+            mbar_init(&bars->q_empty[i], 2);  // by Q K^T and Q S
+            mbar_init(&bars->u_full[i], 1);
+            mbar_init(&bars->u_empty[i], kStateWarps);
             mbar_init(&bars->s_full[i], kStateWarps);
             mbar_init(&bars->s_empty[i], 1);
             mbar_init(&bars->sc_full[i], 1);
-            mbar_init(&bars->p_full[i], kOutWarps);
-            mbar_init(&bars->o_full[i], 1);
-            mbar_init(&bars->o_empty[i], kOutWarps);
+            mbar_init(&bars->p_full[i], kGroupWarps);
+            mbar_init(&bars->o_full[i], 2);  // by Q S and P V
+            mbar_init(&bars->o_empty[i], kGroupWarps);
         }
-        mbar_init(&bars->u_full, 1);
-        mbar_init(&bars->drain, 1);
         ctl->abort = 0;
         ctl->published = 0;
-        for (int w = 0; w < kThreads / 32; ++w) ctl->read[w] = 0;
+        for (int w = 0; w < kWarps; ++w) ctl->read[w] = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tmq);
         tma_prefetch_desc(&tmk);
         tma_prefetch_desc(&tmv);
     }
-    if (warp == kWarpMma) tmem_alloc(&ctl->tmem, G::kTmemCols);
+    if (warp == kWarpQK) tmem_alloc(&ctl->tmem, G::kTmemCols);
     tc_fence_before();
     pdl_wait();
     pdl_trigger();
@@ -252,17 +271,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int before = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += before;
         }
-        if (lane == 31) reinterpret_cast<int *>(s_g)[warp] = incl;
+        if (lane == 31) reinterpret_cast<int *>(tables)[warp] = incl;
         __syncthreads();
         int base = 0;
-        for (int w = 0; w < warp; ++w) base += reinterpret_cast<int *>(s_g)[w];
+        for (int w = 0; w < warp; ++w) base += reinterpret_cast<int *>(tables)[w];
         count[tid + 1] = base + incl;
         if (tid == 0) count[0] = 0;
     }
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem, 0);
-    uint8_t *sQ = smem + G::kOffQ, *sKV = smem + G::kOffKV, *sKt = smem + G::kOffKt,
+    uint8_t *sQ = smem + G::kOffQ, *sKV = smem + G::kOffKV, *sVt = smem + G::kOffVt,
             *sS = smem + G::kOffS;
 
     if (warp == 0) {
@@ -271,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         auto load_kv = [&](const Item &it, int i) {
             const int st = c % kRing;
-            if (ok && c >= kRing) ok = warp_mbar_wait(&bars->kv_empty[st], (c / kRing - 1) & 1, abort_flag);
+            if (ok && c >= kRing) ok = warp_mbar_wait_small(&bars->kv_empty[st], (c / kRing - 1) & 1, abort_flag);
             // test hook: stop after the first chunk, as if a wait had run out
             if (p.test_stall && blockIdx.x == 0 && c == 1) ok = false;
             if (!ok) return;
@@ -291,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Item it = find_item<D>(p, count, k, rank, size);
             if (lane == 0) {
                 const bool free = k < kQueue || spin(&ctl->abort, [&] {
-                                      for (int w = 1; w < kThreads / 32; ++w)
+                                      for (int w = 1; w < kWarps; ++w)
                                           if (*reinterpret_cast<volatile int *>(&ctl->read[w]) <= k - kQueue)
                                               return false;
                                       return true;
@@ -304,27 +323,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             if (it.n == 0) break;
-            if (size > 1) {
-                if (it.c_end < it.chunks)
-                    for (int i = it.c_begin; ok && i < it.c_end; ++i) load_kv(it, i);
-                cluster_sync();
-                cluster_sync();
-            }
-            for (int i = it.c_begin; ok && i < it.c_end; ++i) {
-                load_kv(it, i);
-                for (int j = 0; ok && j < tiles; ++j, ++t) {
-                    const int st = t & 1;
-                    if (t >= 2) ok = warp_mbar_wait(&bars->q_empty[st], ((t >> 1) - 1) & 1, abort_flag);
-                    if (!ok) break;
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&bars->q_full[st],
-                                              G::kHalves * kC * p.heads_per_tile * 128);
-                        for (int hf = 0; hf < G::kHalves; ++hf)
-                            tma_load_3d(sQ + st * G::kQBytes + hf * G::kQHalf, &tmq, hf * 64,
-                                        it.h * p.group + j * p.heads_per_tile, it.t0 + i * kC,
-                                        &bars->q_full[st]);
+#pragma unroll 1
+            for (int outputs = size > 1 ? 0 : 1; outputs < 2; ++outputs) {
+                const int end = outputs || it.c_end < it.chunks ? it.c_end : it.c_begin;
+#pragma unroll 1
+                for (int i = it.c_begin; ok && i < end; ++i) {
+                    load_kv(it, i);
+                    if (!outputs) continue;
+#pragma unroll 1
+                    for (int j = 0; ok && j < tiles; ++j, ++t) {
+                        const int st = t & 1;
+                        if (t >= 2)
+                            ok = warp_mbar_wait_small(&bars->q_empty[st], ((t >> 1) - 1) & 1, abort_flag);
+                        if (!ok) break;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(&bars->q_full[st],
+                                                  G::kHalves * kC * p.heads_per_tile * 128);
+                            for (int hf = 0; hf < G::kHalves; ++hf)
+                                tma_load_3d(sQ + st * G::kQBytes + hf * G::kQHalf, &tmq, hf * 64,
+                                            it.h * p.group + j * p.heads_per_tile, it.t0 + i * kC,
+                                            &bars->q_full[st]);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                }
+                if (!outputs) {
+                    cluster_sync();
+                    cluster_sync();
                 }
             }
         }
@@ -334,134 +359,147 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_drain(&bars->kv_full[i % kRing], (i / kRing) & 1);
             for (uint32_t i = t > 2 ? t - 2 : 0; i < t; ++i) mbar_drain(&bars->q_full[i & 1], (i >> 1) & 1);
         }
-    } else if (warp == kWarpMma) {
+    } else if (warp < kFirstOut) {
         // ============================ MMAs ============================
+        // A thread of three warps each, so that none stands behind another's wait: one the
+        // scores, one the updates and P V, one Q S.  (One thread, not a warp with an elected
+        // lane's predicate: operands in a warp's uniform registers are no longer its own when
+        // a wait has taken the lanes apart.  A commit was seen to arrive twice, and worse.)
         constexpr uint32_t idesc_qk = idesc_bf16_f32(kRows, kC, 0);
         constexpr uint32_t idesc_v = idesc_bf16_f32(kRows, kSlice, 1);
         constexpr uint32_t idesc_kv = idesc_bf16_f32(kRows, kSlice, 1, 1);
         const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
         const uint64_t k_desc = smem_desc_sw128(smem_u32(sKV), 16, 1024);
+        // K with its tokens as the summed dimension (head_dim 64: the second half of M is V, and
+        // those rows of the update are not read)
+        const uint64_t kt_desc = smem_desc_sw128(smem_u32(sKV), G::kKHalf, 1024);
         const uint64_t v_desc = smem_desc_sw128(smem_u32(sKV) + G::kKBytes, G::kKHalf, 1024);
-        const uint64_t kt_desc = smem_desc_sw128(smem_u32(sKt), G::kKHalf, 1024);
+        const uint64_t vt_desc = smem_desc_sw128(smem_u32(sVt), G::kKHalf, 1024);
         const uint64_t s_desc = smem_desc_sw128(smem_u32(sS), G::kKHalf, 1024);
-        const uint32_t elected = elect_one();
         uint32_t c = 0, u = 0, s = 0, t = 0;  // chunks of the ring, updates, states, tiles
         bool ok = true;
-        // (one lane may find a barrier complete and another that the CTA has given up)
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            ok = __all_sync(0xffffffffu, ok && mbar_wait(bar, parity, abort_flag));
+            ok = ok && mbar_wait_small(bar, parity, abort_flag);
             return ok;
         };
-        auto update = [&](uint32_t chunk) {
-            if (!wait(&bars->kt_full[u & 1], (u >> 1) & 1)) return;
+        auto wait_chunk = [&]() { return wait(&bars->kv_full[c % kRing], (c / kRing) & 1); };
+        auto update = [&]() {
+            if (!wait(&bars->vt_full[u % kTables], (u / kTables) & 1) ||
+                (u >= 2 && !wait(&bars->u_empty[u & 1], ((u >> 1) - 1) & 1)))
+                return;
             tc_fence_after();
-            const uint32_t st = (chunk % kRing) * (G::kStageBytes >> 4);
-            // head_dim 128: first parts, then rests; 64: both at once, as the halves of M
-            if (elected) {
-#pragma unroll
-            for (int part = 0; part < G::kHalves; ++part)
-#pragma unroll
-                for (int kk = 0; kk < kC / 16; ++kk)
-                    tc_mma(tmem + G::kColU,
-                           kt_desc + ((part * G::kKBytes + kk * 2048) >> 4),
-                           v_desc + st + (kk * 2048 >> 4), idesc_kv, part + kk > 0 ? 1u : 0u);
-            tc_commit(&bars->u_full);
-            }
-            __syncwarp();
+            const uint64_t kd = kt_desc + (c % kRing) * (G::kStageBytes >> 4);
+            const uint32_t d = tmem + G::kColU + (u & 1) * kSlice;
+            static_assert(G::kVBytes == kC * 128, "parts follow each other");
+#pragma unroll 1
+            for (int kk = 0; kk < kParts * (kC / 16); ++kk)
+                tc_mma(d, kd + kk % (kC / 16) * (2048 >> 4), vt_desc + kk * (2048 >> 4), idesc_kv,
+                       kk > 0 ? 1u : 0u);
+            tc_commit(&bars->u_full[u & 1]);
             ++u;
+        };
+        // one chunk of the outputs, and what it issues of each of its tiles
+        auto scores = [&]() {
+#pragma unroll 1
+            for (int j = 0; j < tiles; ++j, ++t) {
+                const uint32_t b = t & 1, turn = (t >> 1) & 1;
+                // (the columns hold P of two tiles ago until its P V is done)
+                if (!wait(&bars->q_full[b], turn) || (t >= 2 && !wait(&bars->o_full[b], turn ^ 1)))
+                    return;
+                tc_fence_after();
+                const uint64_t qd = q_desc + b * (G::kQBytes >> 4);
+                const uint64_t kd = k_desc + (c % kRing) * (G::kStageBytes >> 4);
+#pragma unroll 1
+                for (int kk = 0; kk < D / 16; ++kk)
+                    tc_mma(tmem + b * kC, qd + (kk >> 2) * (G::kQHalf >> 4) + (kk & 3) * 2,
+                           kd + (kk >> 2) * (G::kKHalf >> 4) + (kk & 3) * 2, idesc_qk,
+                           kk > 0 ? 1u : 0u);
+                tc_commit(&bars->sc_full[b]);
+                tc_commit(&bars->q_empty[b]);
+            }
+        };
+        auto before = [&]() {
+            if (!wait(&bars->s_full[s & 1], (s >> 1) & 1)) return;
+#pragma unroll 1
+            for (int j = 0; j < tiles; ++j, ++t) {
+                const uint32_t b = t & 1, turn = (t >> 1) & 1;
+                if (!wait(&bars->q_full[b], turn) || (t >= 2 && !wait(&bars->o_empty[b], turn ^ 1)))
+                    return;
+                tc_fence_after();
+                const uint64_t qd = q_desc + b * (G::kQBytes >> 4);
+                const uint64_t sd = s_desc + (s & 1) * (G::kSBytes >> 4);
+#pragma unroll 1
+                for (int kk = 0; kk < D / 16; ++kk)
+                    tc_mma(tmem + G::kColO + b * (2 * kSlice),
+                           qd + (kk >> 2) * (G::kQHalf >> 4) + (kk & 3) * 2,
+                           sd + (kk * 2048 >> 4), idesc_v, kk > 0 ? 1u : 0u);
+                tc_commit(&bars->o_full[b]);
+                tc_commit(&bars->q_empty[b]);
+            }
+            tc_commit(&bars->s_empty[s & 1]);
+            ++s;
+        };
+        auto inside = [&]() {
+#pragma unroll 1
+            for (int j = 0; j < tiles; ++j, ++t) {
+                const uint32_t b = t & 1, turn = (t >> 1) & 1;
+                // (P is there after the outputs of two tiles ago have been read)
+                if (!wait(&bars->p_full[b], turn)) return;
+                tc_fence_after();
+                const uint64_t vd = v_desc + (c % kRing) * (G::kStageBytes >> 4);
+#pragma unroll 1
+                for (int kk = 0; kk < kC / 16; ++kk)
+                    tc_mma_ts(tmem + G::kColO + b * (2 * kSlice) + kSlice, tmem + b * kC + kk * 8,
+                              vd + (kk * 2048 >> 4), idesc_v, kk > 0 ? 1u : 0u);
+                tc_commit(&bars->o_full[b]);
+            }
         };
         for (int k = 0;; ++k) {
             const Item it = queue_item(ctl, warp, k);
-            const int n = __shfl_sync(0xffffffffu, it.n, 0);
-            if (n == 0) break;
-            const int c_begin = __shfl_sync(0xffffffffu, it.c_begin, 0);
-            const int c_end = __shfl_sync(0xffffffffu, it.c_end, 0);
-            if (size > 1) {
-                if (c_end < __shfl_sync(0xffffffffu, it.chunks, 0))
-                    for (int i = c_begin; ok && i < c_end; ++i, ++c) {
-                        if (!wait(&bars->kv_full[c % kRing], (c / kRing) & 1)) break;
-                        update(c);
-                        if (ok && elected) tc_commit(&bars->kv_empty[c % kRing]);
-                        __syncwarp();
+            if (it.n == 0) break;
+            // the rank's chunks, first for their updates alone where others build on them
+#pragma unroll 1
+            for (int outputs = size > 1 ? 0 : 1; outputs < 2; ++outputs) {
+                if (lane == 0 && (outputs || it.c_end < it.chunks))
+#pragma unroll 1
+                    for (int i = it.c_begin; ok && i < it.c_end && wait_chunk(); ++i, ++c) {
+                        if (warp == kWarpPV) update();
+                        if (ok && outputs) {
+                            if (warp == kWarpQK)
+                                scores();
+                            else if (warp == kWarpQS)
+                                before();
+                            else
+                                inside();
+                        }
+                        if (ok) tc_commit(&bars->kv_empty[c % kRing]);
                     }
-                cluster_sync();
-                cluster_sync();
-            }
-            // scores of a tile: the first of a chunk waits for the chunk too
-            auto scores = [&](uint32_t chunk, uint32_t tile, bool first) {
-                if (first && !wait(&bars->kv_full[chunk % kRing], (chunk / kRing) & 1)) return;
-                if (!wait(&bars->q_full[tile & 1], (tile >> 1) & 1)) return;
-                tc_fence_after();
-                const uint64_t qd = q_desc + (tile & 1) * (G::kQBytes >> 4);
-                const uint64_t kd = k_desc + (chunk % kRing) * (G::kStageBytes >> 4);
-                if (elected) {
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    tc_mma(tmem + (tile & 1) * kC,
-                           qd + (kk >> 2) * (G::kQHalf >> 4) + (kk & 3) * 2,
-                           kd + (kk >> 2) * (G::kKHalf >> 4) + (kk & 3) * 2, idesc_qk,
-                           kk > 0 ? 1u : 0u);
-                tc_commit(&bars->sc_full[tile & 1]);
-                }
                 __syncwarp();
-            };
-            const int total = (c_end - c_begin) * tiles;
-            int j = 0;  // tile of the chunk
-            if (ok && total > 0) scores(c, t, true);
-            for (int i = 0; ok && i < total; ++i, ++t) {
-                if (j == 0) {
-                    update(c);
-                    if (!ok || !wait(&bars->s_full[s & 1], (s >> 1) & 1)) break;
-                }
-                if (t >= 2 && !wait(&bars->o_empty[t & 1], ((t >> 1) - 1) & 1)) break;
-                tc_fence_after();
-                const uint32_t o = tmem + G::kColO + (t & 1) * (2 * kSlice);
-                const uint64_t qd = q_desc + (t & 1) * (G::kQBytes >> 4);
-                const uint64_t sd = s_desc + (s & 1) * (G::kSBytes >> 4);
-                const bool last = j == tiles - 1;
-                if (elected) {
-#pragma unroll
-                for (int kk = 0; kk < kRows / 16; ++kk) {
-                    const int qk = kk % (D / 16);
-                    tc_mma(o, qd + (qk >> 2) * (G::kQHalf >> 4) + (qk & 3) * 2,
-                           sd + (kk * 2048 >> 4), idesc_v, kk > 0 ? 1u : 0u);
-                }
-                tc_commit(&bars->q_empty[t & 1]);
-                if (last) tc_commit(&bars->s_empty[s & 1]);
-                }
-                __syncwarp();
-                if (i + 1 < total) scores(last ? c + 1 : c, t + 1, last);
-                if (!ok || !wait(&bars->p_full[t & 1], (t >> 1) & 1)) break;
-                tc_fence_after();
-                const uint64_t vd = v_desc + (c % kRing) * (G::kStageBytes >> 4);
-                if (elected) {
-#pragma unroll
-                for (int kk = 0; kk < kC / 16; ++kk)
-                    tc_mma_ts(o + kSlice, tmem + (t & 1) * kC + kk * 8,
-                           vd + (kk * 2048 >> 4), idesc_v, kk > 0 ? 1u : 0u);
-                tc_commit(&bars->o_full[t & 1]);
-                if (last) tc_commit(&bars->kv_empty[c % kRing]);
-                }
-                __syncwarp();
-                j = last ? 0 : j + 1;
-                if (last) {
-                    ++c;
-                    ++s;
+                if (!outputs) {
+                    cluster_sync();
+                    cluster_sync();
                 }
             }
         }
-        if (__any_sync(0xffffffffu, !ok || *abort_flag)) {
+        if (lane == 0 && (!ok || *abort_flag)) {
             // MMAs already issued finish before TMEM is released
-            if (elected) tc_commit(&bars->drain);
-            __syncwarp();
-            mbar_drain(&bars->drain, 0);
+            tc_commit(&bars->drain[warp - kWarpQK]);
+            mbar_drain(&bars->drain[warp - kWarpQK], 0);
         }
-    } else if (warp >= kFirstOut && warp < kFirstOut + kOutWarps) {
+        __syncwarp();
+    } else if (warp < kFirstWeigh) {
         // ============================ P and outputs ============================
         const int wq = warp & 3, r = wq * 32 + lane;
+        const uint32_t grp = (warp - kFirstOut) / kGroupWarps;  // takes tiles of this parity
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
+        const uint32_t sa = t_lane + grp * kC, oa = t_lane + G::kColO + grp * (2 * kSlice);
         const int tok = r / p.heads_per_tile, head = r - tok * p.heads_per_tile;
-        uint32_t t = 0, u = 0;  // tiles, updates seen
+        // the runs of 16 tokens that the warp's rows lie in; a tile of one head fills half of the
+        // rows, and the warps of the others have nothing to do
+        const int first_run = wq * 32 / p.heads_per_tile / 16;
+        const int last_run = (wq * 32 + 31) / p.heads_per_tile / 16;
+        const bool idle = first_run * 16 >= kC;
+        uint32_t t = 0, u = 0;  // tiles, updates up to this item
         bool ok = true;
         for (int k = 0;; ++k) {
             const Item it = queue_item(ctl, warp, k);
@@ -472,110 +510,225 @@ __global__ void __launch_bounds__(kThreads, 1)
                 cluster_sync();
             }
             const int total = (it.c_end - it.c_begin) * tiles;
-            float grow = 0.f, grow_before = 0.f;  // e^(G_i) of this tile's row, and the last one's
-            int i = it.c_begin, j = 0, i_before = 0, j_before = 0;
-            for (int m = 0; ok && m <= total; ++m) {
-                if (m < total) {
-                    const uint32_t tt = t + m;
-                    // (the chunk's sums of logarithms are there with its weighed K)
-                    if (j == 0) {
-                        ok = warp_mbar_wait_spin(&bars->kt_full[u & 1], (u >> 1) & 1, abort_flag);
-                        ++u;
-                    }
-                    ok = ok && warp_mbar_wait_spin(&bars->sc_full[tt & 1], (tt >> 1) & 1, abort_flag);
+            int i = it.c_begin, j = 0;  // chunk, tile of the chunk
+#pragma unroll 1
+            for (int m = 0; ok && m < total; ++m) {
+                const uint32_t tt = t + m;
+                if ((tt & 1) == grp) {
+                    const uint32_t turn = (tt >> 1) & 1, uu = u + (i - it.c_begin);
+                    ok = warp_mbar_wait_small(&bars->vt_full[uu % kTables], (uu / kTables) & 1, abort_flag) &&
+                         warp_mbar_wait_small(&bars->sc_full[grp], turn, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
-                    const float *g = s_g + ((u - 1) & 1) * kC;
-                    const float gi = tok < kC ? g[tok] : 0.f;
-                    const uint32_t sa = t_lane + (tt & 1) * kC;
-                    uint32_t s0[32], s1[32], pk[32];
-                    tmem_ld32(sa, s0);
-                    tmem_ld32(sa + 32, s1);
-                    tmem_wait_ld();
-                    auto weigh = [&](const uint32_t (&sv)[32], int at, uint32_t *dst) {
+                    const Table &tab = tables[uu % kTables];
+                    const float gi = idle ? 0.f : tab.sum[tok];
+                    if (!idle) {
+#pragma unroll 1
+                        for (int run = 0; run < kC / 16; ++run) {
+                            uint32_t pk[8];
 #pragma unroll
-                        for (int x = 0; x < 32; x += 4) {
-                            const float4 gj = *reinterpret_cast<const float4 *>(g + at + x);
-                            const float e0 = fast_exp2(gi - gj.x), e1 = fast_exp2(gi - gj.y),
-                                        e2 = fast_exp2(gi - gj.z), e3 = fast_exp2(gi - gj.w);
-                            const int lim = tok - at - x;  // last visible token of the four
-                            const float a = lim >= 0 ? __uint_as_float(sv[x]) * e0 : 0.f;
-                            const float b = lim >= 1 ? __uint_as_float(sv[x + 1]) * e1 : 0.f;
-                            const float c = lim >= 2 ? __uint_as_float(sv[x + 2]) * e2 : 0.f;
-                            const float d = lim >= 3 ? __uint_as_float(sv[x + 3]) * e3 : 0.f;
-                            dst[x / 2] = pack_bf16x2(a, b);
-                            dst[x / 2 + 1] = pack_bf16x2(c, d);
+                            for (int x = 0; x < 8; ++x) pk[x] = 0u;
+                            if (run <= last_run) {
+                                uint32_t v[16];
+                                tmem_ld16(sa + run * 16, v);
+                                if (run < first_run) {
+                                    // e^(G_i - G_j) by way of the run's last token
+                                    const float row = fast_exp2(gi - tab.sum[run * 16 + 15]);
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int x = 0; x < 16; x += 4) {
+                                        const float4 f =
+                                            *reinterpret_cast<const float4 *>(tab.tail + run * 16 + x);
+                                        pk[x / 2] = pack_bf16x2(__uint_as_float(v[x]) * row * f.x,
+                                                                __uint_as_float(v[x + 1]) * row * f.y);
+                                        pk[x / 2 + 1] =
+                                            pack_bf16x2(__uint_as_float(v[x + 2]) * row * f.z,
+                                                        __uint_as_float(v[x + 3]) * row * f.w);
+                                    }
+                                } else {
+                                    const int lim = tok - run * 16;  // its last visible column
+                                    tmem_wait_ld();
+#pragma unroll
+                                    for (int x = 0; x < 16; x += 4) {
+                                        const float4 g =
+                                            *reinterpret_cast<const float4 *>(tab.sum + run * 16 + x);
+                                        auto w = [&](int e, float gj) {
+                                            const float y =
+                                                __uint_as_float(v[x + e]) * fast_exp2(gi - gj);
+                                            return x + e <= lim ? y : 0.f;
+                                        };
+                                        pk[x / 2] = pack_bf16x2(w(0, g.x), w(1, g.y));
+                                        pk[x / 2 + 1] = pack_bf16x2(w(2, g.z), w(3, g.w));
+                                    }
+                                }
+                            }
+                            // (over scores that have been read: a run's P takes half their columns)
+                            tmem_st8(sa + run * 8, pk);
                         }
-                    };
-                    weigh(s0, 0, pk);
-                    weigh(s1, 32, pk + 16);
-                    tmem_st32(sa, pk);
-                    tmem_wait_st();
-                    tc_fence_before();
+                        tmem_wait_st();
+                        tc_fence_before();
+                    }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->p_full[tt & 1]);
-                    grow_before = grow;
-                    grow = fast_exp2(gi);
-                }
-                if (m > 0) {
-                    const uint32_t tt = t + m - 1;
-                    ok = warp_mbar_wait_spin(&bars->o_full[tt & 1], (tt >> 1) & 1, abort_flag);
+                    if (lane == 0) mbar_arrive(&bars->p_full[grp]);
+
+                    ok = warp_mbar_wait_small(&bars->o_full[grp], turn, abort_flag);
                     if (!ok) break;
-                    tc_fence_after();
-                    const float before = (m < total ? grow_before : grow) * p.scale;
-                    const int token = i_before * kC + tok, hq = j_before * p.heads_per_tile + head;
-                    const bool valid = tok < kC && token < it.n && hq < p.group;
-                    uint4 *dst = reinterpret_cast<uint4 *>(
-                        p.out + (static_cast<int64_t>(it.t0 + token) * p.num_q_heads +
-                                 it.h * p.group + hq) * D + it.slice * kSlice);
-                    const uint32_t oa = t_lane + G::kColO + (tt & 1) * (2 * kSlice);
-#pragma unroll
-                    for (int half = 0; half < kSlice / 32; ++half) {
-                        uint32_t a[32], b[32];
-                        __syncwarp();
-                        tmem_ld32(oa + half * 32, a);
-                        tmem_ld32(oa + kSlice + half * 32, b);
-                        tmem_wait_ld();
-                        if (half == kSlice / 32 - 1) {
-                            tc_fence_before();
+                    if (!idle) {
+                        tc_fence_after();
+                        const float before = fast_exp2(gi) * p.scale;
+                        const int token = i * kC + tok, hq = j * p.heads_per_tile + head;
+                        const bool valid = token < it.n && hq < p.group;
+                        uint4 *dst = reinterpret_cast<uint4 *>(
+                            p.out + (static_cast<int64_t>(it.t0 + token) * p.num_q_heads +
+                                     it.h * p.group + hq) * D + it.slice * kSlice);
+#pragma unroll 1
+                        for (int part = 0; part < kSlice / 16; ++part) {
+                            uint32_t a[16], b[16];
                             __syncwarp();
-                            if (lane == 0) mbar_arrive(&bars->o_empty[tt & 1]);
+                            tmem_ld16(oa + part * 16, a);
+                            tmem_ld16(oa + kSlice + part * 16, b);
+                            tmem_wait_ld();
+                            auto sum = [&](int x) {
+                                return pack_bf16x2(
+                                    fmaf(before, __uint_as_float(a[x]), p.scale * __uint_as_float(b[x])),
+                                    fmaf(before, __uint_as_float(a[x + 1]),
+                                         p.scale * __uint_as_float(b[x + 1])));
+                            };
+                            if (valid) {
+                                dst[part * 2] = make_uint4(sum(0), sum(2), sum(4), sum(6));
+                                dst[part * 2 + 1] = make_uint4(sum(8), sum(10), sum(12), sum(14));
+                            }
                         }
-                        if (!valid) continue;
-                        auto sum = [&](int x) {
-                            return pack_bf16x2(
-                                fmaf(before, __uint_as_float(a[x]), p.scale * __uint_as_float(b[x])),
-                                fmaf(before, __uint_as_float(a[x + 1]),
-                                     p.scale * __uint_as_float(b[x + 1])));
-                        };
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            dst[half * 4 + x] = make_uint4(sum(x * 8), sum(x * 8 + 2), sum(x * 8 + 4),
-                                                           sum(x * 8 + 6));
+                        tc_fence_before();
                     }
                     __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->o_empty[grp]);
                 }
-                i_before = i;
-                j_before = j;
                 if (++j == tiles) j = 0, ++i;
             }
             t += total;
+            u += it.c_end - it.c_begin;
         }
-    } else if (warp >= kFirstState) {
-        // ============================ K's weights, the state ============================
+    } else if (warp < kFirstState) {
+        // ============================ V's weights ============================
+        const int vw = warp - kFirstWeigh;
+        uint32_t c = 0, u = 0;  // chunks of the ring, updates
+        bool ok = true;
+        // logarithm (base 2) of the decay of token i of the request
+        auto log_of = [&](const Item &it, int i) {
+            if (i >= it.n) return 0.f;
+            const float g = __ldg(p.decay + static_cast<int64_t>(it.t0 + i) * p.decay_stride + it.h);
+            return g < 0.f ? fmaxf(g * 1.4426950408889634f, kLeastLog) : 0.f;
+        };
+        for (int k = 0;; ++k) {
+            const Item it = queue_item(ctl, warp, k);
+            if (it.n == 0) break;
+#pragma unroll 1
+            for (int outputs = size > 1 ? 0 : 1; outputs < 2; ++outputs) {
+            const int c_last = outputs || it.c_end < it.chunks ? it.c_end : it.c_begin;
+            float g0 = log_of(it, it.c_begin * kC + 2 * lane);
+            float g1 = log_of(it, it.c_begin * kC + 2 * lane + 1);
+#pragma unroll 1
+            for (int i = it.c_begin; ok && i < c_last; ++i, ++c, ++u) {
+                // sums up to each token (lane: tokens 2 lane and 2 lane + 1), and of those behind
+                // it (each without a difference, so that a small one keeps its digits beside
+                // large ones)
+                float up = g0 + g1, down = up;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const float a = __shfl_up_sync(0xffffffffu, up, o);
+                    const float b = __shfl_down_sync(0xffffffffu, down, o);
+                    if (lane >= o) up += a;
+                    if (lane + o < 32) down += b;
+                }
+                const float all = __shfl_sync(0xffffffffu, up, 31);
+                float up0 = __shfl_up_sync(0xffffffffu, up, 1);
+                float down1 = __shfl_down_sync(0xffffffffu, down, 1);
+                if (lane == 0) up0 = 0.f;
+                if (lane == 31) down1 = 0.f;
+                up0 += g0;
+                const float w0 = exp2f(down1 + g1), w1 = exp2f(down1);
+                if (vw == 0) {
+                    Table &tab = tables[u % kTables];
+                    const float end = __shfl_sync(0xffffffffu, up, lane | 7);  // of the run of 16
+                    *reinterpret_cast<float2 *>(tab.sum + 2 * lane) = make_float2(up0, up);
+                    *reinterpret_cast<float2 *>(tab.tail + 2 * lane) =
+                        make_float2(fast_exp2(end - up0), fast_exp2(end - up));
+                    if (lane == 0) tab.all = all;
+                }
+                if (i + 1 < it.c_end) {
+                    g0 = log_of(it, (i + 1) * kC + 2 * lane);
+                    g1 = log_of(it, (i + 1) * kC + 2 * lane + 1);
+                }
+                const int st = c % kRing;
+                // the chunk is here, and the last one's update has read its weighed V
+                ok = warp_mbar_wait_small(&bars->kv_full[st], (c / kRing) & 1, abort_flag) &&
+                     (u == 0 || warp_mbar_wait_small(&bars->u_full[(u - 1) & 1], ((u - 1) >> 1) & 1, abort_flag));
+                if (!ok) break;
+                uint8_t *k = sKV + st * G::kStageBytes, *v = k + G::kKBytes;
+                const int valid = min(kC, it.n - i * kC);
+                // eight lanes to a row of 64 elements
+#pragma unroll 1
+                for (int x = 0; x < kC / (4 * kWeighWarps); ++x) {
+                    const int row = vw * (kC / kWeighWarps) + x * 4 + lane / 8;
+                    const float wa = __shfl_sync(0xffffffffu, w0, row >> 1);
+                    const float wb = __shfl_sync(0xffffffffu, w1, row >> 1);
+                    const float wt = row & 1 ? wb : wa;
+                    const uint32_t off = sw128_offset(row, lane % 8);
+                    const uint4 z = make_uint4(0, 0, 0, 0);
+                    uint4 in = *reinterpret_cast<const uint4 *>(v + off);
+                    // rows behind the request are another's, or padding: whatever stands there
+                    // does not reach a sum
+                    if (row >= valid) {
+                        in = z;
+                        *reinterpret_cast<uint4 *>(v + off) = z;
+#pragma unroll
+                        for (int hf = 0; hf < G::kHalves; ++hf)
+                            *reinterpret_cast<uint4 *>(k + hf * G::kKHalf + off) = z;
+                    }
+                    uint4 part[kParts];
+                    auto split = [&](uint32_t pair, uint32_t &p0, uint32_t &p1, uint32_t &p2) {
+                        float lo = __uint_as_float(pair << 16) * wt;
+                        float hi = __uint_as_float(pair & 0xFFFF0000u) * wt;
+                        p0 = pack_bf16x2(lo, hi);
+                        lo -= __uint_as_float(p0 << 16);
+                        hi -= __uint_as_float(p0 & 0xFFFF0000u);
+                        p1 = pack_bf16x2(lo, hi);
+                        p2 = pack_bf16x2(lo - __uint_as_float(p1 << 16),
+                                         hi - __uint_as_float(p1 & 0xFFFF0000u));
+                    };
+                    split(in.x, part[0].x, part[1].x, part[2].x);
+                    split(in.y, part[0].y, part[1].y, part[2].y);
+                    split(in.z, part[0].z, part[1].z, part[2].z);
+                    split(in.w, part[0].w, part[1].w, part[2].w);
+#pragma unroll
+                    for (int n = 0; n < kParts; ++n)
+                        *reinterpret_cast<uint4 *>(sVt + n * G::kVBytes + off) = part[n];
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->vt_full[u % kTables]);
+            }
+            if (!outputs) {
+                cluster_sync();
+                cluster_sync();
+            }
+            }
+        }
+    } else {
+        // ============================ the state ============================
         const int sw = warp - kFirstState, wq = warp & 3, half = sw >> 2;
         const int r = wq * 32 + lane;       // row of the update's MMA, 32 of its columns
-        const int dk = D == 128 ? r : r % 64;
-        const bool rest = D == 64 && r >= 64;  // the state of the rests of K
+        const bool real = r < D;  // (head_dim 64: the MMA's other rows go along unread)
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
         float s[32];
-        uint32_t c = 0, u = 0, w = 0;  // chunks of the ring, updates, states written
+        uint32_t u = 0, w = 0;  // updates, states written
         bool ok = true;
         float total = 0.f;  // log2 decay of the chunks gone through
 
         // the state in bf16, for the MMA that follows
         auto give_state = [&]() {
-            if (ok && w >= 2) ok = warp_mbar_wait_spin(&bars->s_empty[w & 1], ((w >> 1) - 1) & 1, abort_flag);
+            if (w >= 2) ok = warp_mbar_wait_small(&bars->s_empty[w & 1], ((w >> 1) - 1) & 1, abort_flag);
             if (!ok) return;
             uint8_t *dst = sS + (w & 1) * G::kSBytes;
 #pragma unroll
@@ -588,192 +741,97 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mbar_arrive(&bars->s_full[w & 1]);
             ++w;
         };
-        // logarithm (base 2) of the decay of token i of the request
-        auto log_of = [&](const Item &it, int i) {
-            if (i >= it.n) return 0.f;
-            const float g = __ldg(p.decay + static_cast<int64_t>(it.t0 + i) * p.decay_stride + it.h);
-            return g < 0.f ? fmaxf(g * 1.4426950408889634f, kLeastLog) : 0.f;
-        };
-        // One chunk: weighs K, then takes the update in.  g0, g1: the logarithms of tokens
-        // 2 lane and 2 lane + 1, and the next chunk's afterwards.
-        auto chunk = [&](const Item &it, int i, float &g0, float &g1, bool more) {
-            // sums up to each token, and of those behind it (each without a difference, so
-            // that a small one keeps its digits beside large ones)
-            float up = g0 + g1, down = up;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float a = __shfl_up_sync(0xffffffffu, up, o);
-                const float b = __shfl_down_sync(0xffffffffu, down, o);
-                if (lane >= o) up += a;
-                if (lane + o < 32) down += b;
-            }
-            const float all = __shfl_sync(0xffffffffu, up, 31);
-            float up0 = __shfl_up_sync(0xffffffffu, up, 1), down1 = __shfl_down_sync(0xffffffffu, down, 1);
-            if (lane == 0) up0 = 0.f;
-            if (lane == 31) down1 = 0.f;
-            up0 += g0;
-            const float w0 = exp2f(down1 + g1), w1 = exp2f(down1);
-            if (p.decay_stride == 0 && (i + 1) * kC <= it.n) {
-                // (one logarithm for all: exact multiples)
-                up0 = (2 * lane + 1) * g0;
-                up = (2 * lane + 2) * g0;
-            }
-            if (sw == 0)
-                *reinterpret_cast<float2 *>(s_g + (u & 1) * kC + 2 * lane) = make_float2(up0, up);
-            const float keep = exp2f(all);
-            total += all;
-            const int at = (i + 1) * kC + 2 * lane;
-            if (more) {
-                g0 = log_of(it, at);
-                g1 = log_of(it, at + 1);
-            }
-            const int st = c % kRing;
-            ok = ok && warp_mbar_wait_spin(&bars->kv_full[st], (c / kRing) & 1, abort_flag);
-            if (!ok) return;
-            const uint8_t *k = sKV + st * G::kStageBytes;
-            const int valid = min(kC, it.n - i * kC);
-            // eight lanes to a row of 64 elements
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int row = sw * 8 + x * 4 + lane / 8;
-                const int src = row >> 1;  // the lane that has its weight
-                const float wa = __shfl_sync(0xffffffffu, w0, src), wb = __shfl_sync(0xffffffffu, w1, src);
-                const float wt = row & 1 ? wb : wa;
-#pragma unroll
-                for (int hf = 0; hf < G::kHalves; ++hf) {
-                    const uint32_t off = hf * G::kKHalf + sw128_offset(row, lane % 8);
-                    const uint4 in = *reinterpret_cast<const uint4 *>(k + off);
-                    uint4 a = make_uint4(0, 0, 0, 0), b = a;
-                    auto part = [&](uint32_t pair, uint32_t &first, uint32_t &more_) {
-                        const float lo = __uint_as_float(pair << 16) * wt;
-                        const float hi = __uint_as_float(pair & 0xFFFF0000u) * wt;
-                        first = pack_bf16x2(lo, hi);
-                        more_ = pack_bf16x2(lo - __uint_as_float(first << 16),
-                                            hi - __uint_as_float(first & 0xFFFF0000u));
-                    };
-                    if (row < valid) {
-                        part(in.x, a.x, b.x);
-                        part(in.y, a.y, b.y);
-                        part(in.z, a.z, b.z);
-                        part(in.w, a.w, b.w);
-                    }
-                    *reinterpret_cast<uint4 *>(sKt + off) = a;
-                    *reinterpret_cast<uint4 *>(sKt + G::kKBytes + off) = b;
-                }
-                // rows behind the request are another's, or padding: whatever stands there,
-                // it does not reach a sum
-                if (row >= valid)
-                    *reinterpret_cast<uint4 *>(sKV + st * G::kStageBytes + G::kKBytes +
-                                               sw128_offset(row, lane % 8)) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->kt_full[u & 1]);
-            ++c;
-            ok = warp_mbar_wait_spin(&bars->u_full, u & 1, abort_flag);
-            ++u;
+        // takes a chunk's update in
+        auto update = [&]() {
+            ok = warp_mbar_wait_small(&bars->u_full[u & 1], (u >> 1) & 1, abort_flag) &&
+                 warp_mbar_wait_small(&bars->vt_full[u % kTables], (u / kTables) & 1, abort_flag);
             if (!ok) return;
             tc_fence_after();
-            uint32_t up_[32];
-            tmem_ld32(t_lane + G::kColU + half * 32, up_);
+            const float all = tables[u % kTables].all, keep = exp2f(all);
+            uint32_t up[32];
+            tmem_ld32(t_lane + G::kColU + (u & 1) * kSlice + half * 32, up);
             tmem_wait_ld();
             tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->u_empty[u & 1]);
+            ++u;
+            total += all;
 #pragma unroll
-            for (int x = 0; x < 32; ++x) s[x] = fmaf(keep, s[x], __uint_as_float(up_[x]));
+            for (int x = 0; x < 32; ++x) s[x] = fmaf(keep, s[x], __uint_as_float(up[x]));
         };
         for (int k = 0;; ++k) {
             const Item it = queue_item(ctl, warp, k);
             if (it.n == 0) break;
-            const int64_t place = static_cast<int64_t>(it.h) * D * D + static_cast<int64_t>(dk) * D +
+            const int64_t place = static_cast<int64_t>(it.h) * D * D + static_cast<int64_t>(r) * D +
                                   it.slice * kSlice + half * 32;
             const int64_t state_size = static_cast<int64_t>(p.num_kv_heads) * D * D;
-            const int at0 = it.c_begin * kC + 2 * lane;
-            float g0, g1;
-            if (size > 1) {
+            float *exchange = reinterpret_cast<float *>(sS) + (half * 32) * kRows + r;
+#pragma unroll 1
+            for (int outputs = size > 1 ? 0 : 1; outputs < 2; ++outputs) {
+                // the state before the run: the request's, and the ranks' before this one; for
+                // the updates alone none
                 total = 0.f;
+                const float4 *src =
+                    reinterpret_cast<const float4 *>(p.state + it.in * state_size + place);
 #pragma unroll
-                for (int x = 0; x < 32; ++x) s[x] = 0.f;
-                if (it.c_end < it.chunks) {
-                    g0 = log_of(it, at0);
-                    g1 = log_of(it, at0 + 1);
-                    for (int i = it.c_begin; ok && i < it.c_end; ++i)
-                        chunk(it, i, g0, g1, i + 1 < it.c_end);
-                    // (the MMAs of the item before have read both states)
-                    for (int x = 0; ok && x < 2; ++x)
-                        if (w > static_cast<uint32_t>(x)) {
-                            const uint32_t last = w - 1 - x;
-                            ok = warp_mbar_wait_spin(&bars->s_empty[last & 1], (last >> 1) & 1, abort_flag);
-                        }
-                    float *mine = reinterpret_cast<float *>(sS) + (half * 32) * kRows + r;
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) mine[x * kRows] = s[x];
-                    if (sw == 0 && lane == 0) ctl->decay = total;
+                for (int x = 0; x < 8; ++x) {
+                    const float4 v = outputs && it.in >= 0 && real ? src[x]
+                                                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+                    s[4 * x] = v.x;
+                    s[4 * x + 1] = v.y;
+                    s[4 * x + 2] = v.z;
+                    s[4 * x + 3] = v.w;
                 }
-                cluster_sync();
-            }
-            g0 = log_of(it, at0);
-            g1 = log_of(it, at0 + 1);
-            const float4 *src = reinterpret_cast<const float4 *>(p.state + it.in * state_size + place);
+                if (outputs && size > 1) {
+                    if (it.c_begin < it.c_end)
+#pragma unroll 1
+                        for (int other = 0; other < rank; ++other) {
+                            const float keep = exp2f(ld_cluster_f1(&ctl->decay, other));
+                            const uint32_t theirs = cluster_addr(exchange, other);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const float4 v = it.in >= 0 && !rest ? src[x] : make_float4(0.f, 0.f, 0.f, 0.f);
-                s[4 * x] = v.x;
-                s[4 * x + 1] = v.y;
-                s[4 * x + 2] = v.z;
-                s[4 * x + 3] = v.w;
-            }
-            if (size > 1) {
-                if (it.c_begin < it.c_end)
-                    for (int other = 0; other < rank; ++other) {
-                        const float keep = exp2f(ld_cluster_f1(&ctl->decay, other));
-                        const float *theirs = reinterpret_cast<float *>(sS) + (half * 32) * kRows + r;
+                            for (int x = 0; x < 32; ++x)
+                                s[x] = fmaf(keep, s[x], ld_cluster_at(theirs + x * kRows * 4));
+                        }
+                    cluster_sync();
+                }
+                const int c_last = outputs || it.c_end < it.chunks ? it.c_end : it.c_begin;
+#pragma unroll 1
+                for (int i = it.c_begin; ok && i < c_last; ++i) {
+                    if (outputs) give_state();
+                    if (ok) update();
+                }
+                if (!outputs) {
+                    if (c_last > it.c_begin) {
+                        // (the MMAs of the item before have read both states)
+                        for (uint32_t x = 0; ok && x < 2; ++x)
+                            if (w > x) {
+                                const uint32_t last = w - 1 - x;
+                                ok = warp_mbar_wait_small(&bars->s_empty[last & 1], (last >> 1) & 1,
+                                                          abort_flag);
+                            }
 #pragma unroll
-                        for (int x = 0; x < 32; ++x)
-                            s[x] = fmaf(keep, s[x], ld_cluster_f1(theirs + x * kRows, other));
+                        for (int x = 0; x < 32; ++x) exchange[x * kRows] = s[x];
+                        if (sw == 0 && lane == 0) ctl->decay = total;
                     }
-                cluster_sync();
+                    cluster_sync();
+                }
             }
-            if (it.c_begin < it.c_end) give_state();
-            for (int i = it.c_begin; ok && i < it.c_end; ++i) {
-                chunk(it, i, g0, g1, i + 1 < it.c_end);
-                if (i + 1 < it.c_end) give_state();
-            }
-            if (D == 64) {
-                // the rests' state joins the first parts'
-                float *other = reinterpret_cast<float *>(sKt) + (half * 32) * 64 + dk;
-                named_bar_sync(1, 32 * kStateWarps);
-                if (rest)
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) other[x * 64] = s[x];
-                named_bar_sync(1, 32 * kStateWarps);
-                if (!rest)
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) s[x] += other[x * 64];
-                named_bar_sync(1, 32 * kStateWarps);
-            }
-            if (ok && !rest && it.to >= 0 && it.c_begin < it.c_end && it.c_end == it.chunks) {
+            if (it.c_begin == it.c_end || it.c_end < it.chunks) continue;
+            // the last rank has the state behind the request
+            if (ok && real && it.to >= 0) {
                 float4 *dst = reinterpret_cast<float4 *>(p.state + it.to * state_size + place);
 #pragma unroll
                 for (int x = 0; x < 8; ++x)
                     dst[x] = make_float4(s[4 * x], s[4 * x + 1], s[4 * x + 2], s[4 * x + 3]);
             }
         }
-    } else if (size > 1) {
-        // (warps without a part in it: the cluster's barriers take every thread)
-        for (int k = 0;; ++k) {
-            if (queue_item(ctl, warp, k).n == 0) break;
-            cluster_sync();
-            cluster_sync();
-        }
-    } else {
-        for (int k = 0; queue_item(ctl, warp, k).n != 0; ++k) {}
     }
 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (*abort_flag && tid == 0) flag_status(p.status, PA_DEV_WAIT_TIMEOUT);
-    if (warp == kWarpMma) tmem_dealloc(tmem, G::kTmemCols);
+    if (warp == kWarpQK) tmem_dealloc(tmem, G::kTmemCols);
 }
 
 namespace {
@@ -792,8 +850,11 @@ int launch(const LinearParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
     const int64_t longs = std::min<int64_t>(p.num_seqs, p.num_tokens / (p.max_rows + 1));
     const int64_t items = longs * p.num_kv_heads * (D / kSlice);
     if (items == 0) return PA_OK;
+    // the largest cluster whose ranks have two chunks and whose items run at once (152 SMs hold 76
+    // clusters of 2, 36 of 4 and 15 of 8: a ninth of the SMs belongs to none of 8)
     int size = 1;
-    while (size < kDirectMaxCluster && 2 * size * items <= sms && 2 * size * 2 * kC <= p.num_tokens)
+    while (size < kDirectMaxCluster && 2 * size * 2 * kC <= p.num_tokens &&
+           2 * size * items <= (size < 4 ? sms * 18 / 19 : sms * 15 / 19))
         size *= 2;
     const int clusters = static_cast<int>(std::min<int64_t>(items, sms / size));
     PdlLaunch l(clusters * size, kThreads, Geom<D>::kSmemBytes, s);
