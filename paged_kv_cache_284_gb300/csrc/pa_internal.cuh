@@ -639,28 +639,28 @@ __device__ __forceinline__ bool mbar_try_wait_for(uint64_t *bar, uint32_t parity
         : "memory");
     return ok != 0;
 }
-// mbar_wait and warp_mbar_wait in few instructions, for kernels with many waits and many waiting
-// warps.  The bound is 2 s at 2.1 GHz, by the SM's clock.
+// mbar_wait in few instructions, for kernels with many waits and many waiting warps (20 such
+// waits of the other kind are 14 KB of code, and kernels of many roles run out of instruction
+// cache).  Any number of a warp's lanes may call it.  The bound is a number of tries of up to 2 us:
+// 2 s.
+constexpr int kSmallWaitTries = 1 << 20;
 __device__ __forceinline__ bool mbar_wait_small(uint64_t *bar, uint32_t parity,
                                                 volatile int *abort) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    bool ok = false;
+    bool ok = mbar_try_wait(bar, parity);
 #pragma unroll 1
-    while (!ok && !*abort) {
-        ok = mbar_try_wait_for(bar, parity, 20000);
-        if (clock64() - t0 > 4200000000ll) *abort = 1;
+    for (int n = 0; !ok && !*abort; ++n) {
+        ok = mbar_try_wait_for(bar, parity, 2000);
+        if (n > kSmallWaitTries) *abort = 1;
     }
     return ok;
 }
+// By all of a warp's lanes, which have all acquired the barrier and meet behind it.  (One may find
+// the phase complete and another that the CTA has given up: then none goes on.)
 __device__ __forceinline__ bool warp_mbar_wait_small(uint64_t *bar, uint32_t parity,
                                                      volatile int *abort) {
-    int ok = 1;
-    if ((threadIdx.x & 31) == 0) ok = mbar_wait_small(bar, parity, abort) ? 1 : 0;
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    if (ok) (void)mbar_try_wait(bar, parity);
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_small(bar, parity, abort));
     __syncwarp();
-    return ok != 0;
+    return ok;
 }
 // Short bounded wait used only while draining after an abort.
 __device__ __forceinline__ void mbar_drain(uint64_t *bar, uint32_t parity) {

@@ -30,6 +30,52 @@ struct StepGeom {
     static_assert(kRows >= 1, "rows");
 };
 
+// Two fp32 values in one 64-bit register pair, which one instruction multiplies and adds.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// R consecutive bf16 values of shared memory
+template <int R>
+__device__ __forceinline__ void load_row(const __nv_bfloat16 *src, float (&v)[R]) {
+    static_assert(R == 2 || R % 8 == 0 || R == 4, "vector loads");
+    constexpr int W = R / 2;  // words
+    uint32_t w[W];
+    if constexpr (R == 2) {
+        w[0] = *reinterpret_cast<const uint32_t *>(src);
+    } else if constexpr (R == 4) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(src);
+        w[0] = x.x, w[1] = x.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; i += 4) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(src + 2 * i);
+            w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
 }  // namespace
 
 template <int D, int COLS>
@@ -59,12 +105,15 @@ __device__ __forceinline__ void step_job(const LinearParams &p) {
     const int64_t state_size = static_cast<int64_t>(p.num_kv_heads) * D * D;
     const int64_t place = static_cast<int64_t>(h) * D * D + static_cast<int64_t>(row0) * D +
                           slice * COLS + col;
-    float4 s[R];
+    uint64_t s[R][2];  // four columns of a row
     const float *src = p.state + in * state_size + place;
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-        s[i] = in >= 0 ? *reinterpret_cast<const float4 *>(src + i * D)
-                       : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < R; ++i) {
+        const float4 x = in >= 0 ? __ldcs(reinterpret_cast<const float4 *>(src + i * D))
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+        s[i][0] = pair(x.x, x.y);
+        s[i][1] = pair(x.z, x.w);
+    }
 
     // 16-byte pieces of `rows` rows of `len` elements
     auto fetch = [&](__nv_bfloat16 *dst, const __nv_bfloat16 *src, int64_t stride, int rows, int len) {
@@ -97,33 +146,35 @@ __device__ __forceinline__ void step_job(const LinearParams &p) {
             __syncthreads();
             for (int i = 0; i < m; ++i) {
                 if (g0 == 0) {
-                    const float keep = s_keep[i];
+                    const uint64_t keep = pair(s_keep[i], s_keep[i]);
                     const uint2 raw = *reinterpret_cast<const uint2 *>(&s_v[i][col]);
-                    const float4 v = make_float4(
-                        __uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xFFFF0000u),
-                        __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xFFFF0000u));
+                    const uint64_t v0 = pair(__uint_as_float(raw.x << 16),
+                                             __uint_as_float(raw.x & 0xFFFF0000u));
+                    const uint64_t v1 = pair(__uint_as_float(raw.y << 16),
+                                             __uint_as_float(raw.y & 0xFFFF0000u));
+                    float k[R];
+                    load_row<R>(&s_k[i][row0], k);
 #pragma unroll
                     for (int x = 0; x < R; ++x) {
-                        const float k = __bfloat162float(s_k[i][row0 + x]);
-                        s[x].x = fmaf(keep, s[x].x, k * v.x);
-                        s[x].y = fmaf(keep, s[x].y, k * v.y);
-                        s[x].z = fmaf(keep, s[x].z, k * v.z);
-                        s[x].w = fmaf(keep, s[x].w, k * v.w);
+                        const uint64_t kk = pair(k[x], k[x]);
+                        s[x][0] = fma2(keep, s[x][0], mul2(kk, v0));
+                        s[x][1] = fma2(keep, s[x][1], mul2(kk, v1));
                     }
                 }
                 for (int j0 = 0; j0 < heads; j0 += kHeadBatch) {
                     const int some = min(kHeadBatch, heads - j0);
                     for (int j = 0; j < some; ++j) {
-                        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                        const __nv_bfloat16 *q = &s_q[i * heads + j0 + j][row0];
+                        uint64_t o0 = pair(0.f, 0.f), o1 = o0;
+                        float q[R];
+                        load_row<R>(&s_q[i * heads + j0 + j][row0], q);
 #pragma unroll
                         for (int x = 0; x < R; ++x) {
-                            const float y = __bfloat162float(q[x]);
-                            o.x = fmaf(y, s[x].x, o.x);
-                            o.y = fmaf(y, s[x].y, o.y);
-                            o.z = fmaf(y, s[x].z, o.z);
-                            o.w = fmaf(y, s[x].w, o.w);
+                            const uint64_t y = pair(q[x], q[x]);
+                            o0 = fma2(y, s[x][0], o0);
+                            o1 = fma2(y, s[x][1], o1);
                         }
+                        const float2 a = unpair(o0), b = unpair(o1);
+                        float4 o = make_float4(a.x, a.y, b.x, b.y);
 #pragma unroll
                         for (int x = G::kLanes; x < 32; x <<= 1) {
                             o.x += __shfl_xor_sync(0xffffffffu, o.x, x);
@@ -137,13 +188,19 @@ __device__ __forceinline__ void step_job(const LinearParams &p) {
                     __syncthreads();
                     // (the next sums go to the other buffer, and meet this one's readers at its
                     // barrier)
-                    for (int y = tid; y < some * COLS; y += kThreads) {
-                        const int j = y / COLS, c = y % COLS;
-                        float o = 0.f;
+                    for (int y = tid; y < some * (COLS / 2); y += kThreads) {
+                        const int j = y / (COLS / 2), c = y % (COLS / 2) * 2;
+                        float2 o = make_float2(0.f, 0.f);
 #pragma unroll
-                        for (int w = 0; w < kWarps; ++w) o += s_part[buf][w][j][c];
-                        p.out[(static_cast<int64_t>(t + i) * p.num_q_heads + h * p.group + g0 + j0 +
-                               j) * D + slice * COLS + c] = __float2bfloat16(o * p.scale);
+                        for (int w = 0; w < kWarps; ++w) {
+                            const float2 x = *reinterpret_cast<const float2 *>(&s_part[buf][w][j][c]);
+                            o.x += x.x;
+                            o.y += x.y;
+                        }
+                        *reinterpret_cast<uint32_t *>(
+                            p.out + (static_cast<int64_t>(t + i) * p.num_q_heads + h * p.group + g0 +
+                                     j0 + j) * D + slice * COLS + c) =
+                            pack_bf16x2(o.x * p.scale, o.y * p.scale);
                     }
                     buf ^= 1;
                 }
@@ -153,7 +210,10 @@ __device__ __forceinline__ void step_job(const LinearParams &p) {
     if (to < 0) return;
     float *dst = p.state + to * state_size + place;
 #pragma unroll
-    for (int i = 0; i < R; ++i) *reinterpret_cast<float4 *>(dst + i * D) = s[i];
+    for (int i = 0; i < R; ++i) {
+        const float2 a = unpair(s[i][0]), b = unpair(s[i][1]);
+        __stcs(reinterpret_cast<float4 *>(dst + i * D), make_float4(a.x, a.y, b.x, b.y));
+    }
 }
 
 template <int D, int COLS>

@@ -398,46 +398,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_commit(&bars->u_full[u & 1]);
             ++u;
         };
-        // one chunk of the outputs, and what it issues of each of its tiles
-        auto scores = [&]() {
+        // Q by K or by S for the tiles of a chunk (one code for both): B's descriptor, and its
+        // steps from 16 of the summed dimension to the next and from 64 to the next
+        auto by_q = [&](uint64_t b_desc, uint32_t step, uint32_t step64, uint32_t d, uint32_t d_next,
+                        uint32_t idesc, uint64_t *before, uint64_t *after) {
 #pragma unroll 1
             for (int j = 0; j < tiles; ++j, ++t) {
                 const uint32_t b = t & 1, turn = (t >> 1) & 1;
-                // (the columns hold P of two tiles ago until its P V is done)
-                if (!wait(&bars->q_full[b], turn) || (t >= 2 && !wait(&bars->o_full[b], turn ^ 1)))
-                    return;
+                if (!wait(&bars->q_full[b], turn) || (t >= 2 && !wait(&before[b], turn ^ 1))) return;
                 tc_fence_after();
                 const uint64_t qd = q_desc + b * (G::kQBytes >> 4);
-                const uint64_t kd = k_desc + (c % kRing) * (G::kStageBytes >> 4);
 #pragma unroll 1
                 for (int kk = 0; kk < D / 16; ++kk)
-                    tc_mma(tmem + b * kC, qd + (kk >> 2) * (G::kQHalf >> 4) + (kk & 3) * 2,
-                           kd + (kk >> 2) * (G::kKHalf >> 4) + (kk & 3) * 2, idesc_qk,
-                           kk > 0 ? 1u : 0u);
-                tc_commit(&bars->sc_full[b]);
+                    tc_mma(d + b * d_next, qd + (kk >> 2) * (G::kQHalf >> 4) + (kk & 3) * 2,
+                           b_desc + (kk >> 2) * step64 + (kk & 3) * step, idesc, kk > 0 ? 1u : 0u);
+                tc_commit(&after[b]);
                 tc_commit(&bars->q_empty[b]);
             }
-        };
-        auto before = [&]() {
-            if (!wait(&bars->s_full[s & 1], (s >> 1) & 1)) return;
-#pragma unroll 1
-            for (int j = 0; j < tiles; ++j, ++t) {
-                const uint32_t b = t & 1, turn = (t >> 1) & 1;
-                if (!wait(&bars->q_full[b], turn) || (t >= 2 && !wait(&bars->o_empty[b], turn ^ 1)))
-                    return;
-                tc_fence_after();
-                const uint64_t qd = q_desc + b * (G::kQBytes >> 4);
-                const uint64_t sd = s_desc + (s & 1) * (G::kSBytes >> 4);
-#pragma unroll 1
-                for (int kk = 0; kk < D / 16; ++kk)
-                    tc_mma(tmem + G::kColO + b * (2 * kSlice),
-                           qd + (kk >> 2) * (G::kQHalf >> 4) + (kk & 3) * 2,
-                           sd + (kk * 2048 >> 4), idesc_v, kk > 0 ? 1u : 0u);
-                tc_commit(&bars->o_full[b]);
-                tc_commit(&bars->q_empty[b]);
-            }
-            tc_commit(&bars->s_empty[s & 1]);
-            ++s;
         };
         auto inside = [&]() {
 #pragma unroll 1
@@ -465,12 +442,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = it.c_begin; ok && i < it.c_end && wait_chunk(); ++i, ++c) {
                         if (warp == kWarpPV) update();
                         if (ok && outputs) {
-                            if (warp == kWarpQK)
-                                scores();
-                            else if (warp == kWarpQS)
-                                before();
-                            else
+                            const bool qs = warp == kWarpQS;
+                            if (qs) wait(&bars->s_full[s & 1], (s >> 1) & 1);
+                            if (warp == kWarpPV)
                                 inside();
+                            else if (ok)
+                                // (Q K^T: the columns hold P of two tiles ago until its P V is done)
+                                by_q(qs ? s_desc + (s & 1) * (G::kSBytes >> 4)
+                                        : k_desc + (c % kRing) * (G::kStageBytes >> 4),
+                                     qs ? 2048 >> 4 : 2, qs ? 8192 >> 4 : G::kKHalf >> 4,
+                                     tmem + (qs ? G::kColO : 0), qs ? 2 * kSlice : kC,
+                                     qs ? idesc_v : idesc_qk, qs ? bars->o_empty : bars->o_full,
+                                     qs ? bars->o_full : bars->sc_full);
+                            if (qs && ok) {
+                                tc_commit(&bars->s_empty[s & 1]);
+                                ++s;
+                            }
                         }
                         if (ok) tc_commit(&bars->kv_empty[c % kRing]);
                     }
