@@ -30,27 +30,6 @@ struct StepGeom {
     static_assert(kRows >= 1, "rows");
 };
 
-// Two fp32 values in one 64-bit register pair, which one instruction multiplies and adds.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 // R consecutive bf16 values of shared memory
 template <int R>
 __device__ __forceinline__ void load_row(const __nv_bfloat16 *src, float (&v)[R]) {
@@ -111,8 +90,8 @@ __device__ __forceinline__ void step_job(const LinearParams &p) {
     for (int i = 0; i < R; ++i) {
         const float4 x = in >= 0 ? __ldcs(reinterpret_cast<const float4 *>(src + i * D))
                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-        s[i][0] = pair(x.x, x.y);
-        s[i][1] = pair(x.z, x.w);
+        s[i][0] = f2_pack(x.x, x.y);
+        s[i][1] = f2_pack(x.z, x.w);
     }
 
     // 16-byte pieces of `rows` rows of `len` elements
@@ -146,35 +125,36 @@ __device__ __forceinline__ void step_job(const LinearParams &p) {
             __syncthreads();
             for (int i = 0; i < m; ++i) {
                 if (g0 == 0) {
-                    const uint64_t keep = pair(s_keep[i], s_keep[i]);
+                    const uint64_t keep = f2_pack(s_keep[i], s_keep[i]);
                     const uint2 raw = *reinterpret_cast<const uint2 *>(&s_v[i][col]);
-                    const uint64_t v0 = pair(__uint_as_float(raw.x << 16),
+                    const uint64_t v0 = f2_pack(__uint_as_float(raw.x << 16),
                                              __uint_as_float(raw.x & 0xFFFF0000u));
-                    const uint64_t v1 = pair(__uint_as_float(raw.y << 16),
+                    const uint64_t v1 = f2_pack(__uint_as_float(raw.y << 16),
                                              __uint_as_float(raw.y & 0xFFFF0000u));
                     float k[R];
                     load_row<R>(&s_k[i][row0], k);
 #pragma unroll
                     for (int x = 0; x < R; ++x) {
-                        const uint64_t kk = pair(k[x], k[x]);
-                        s[x][0] = fma2(keep, s[x][0], mul2(kk, v0));
-                        s[x][1] = fma2(keep, s[x][1], mul2(kk, v1));
+                        const uint64_t kk = f2_pack(k[x], k[x]);
+                        s[x][0] = f2_fma(keep, s[x][0], f2_mul(kk, v0));
+                        s[x][1] = f2_fma(keep, s[x][1], f2_mul(kk, v1));
                     }
                 }
                 for (int j0 = 0; j0 < heads; j0 += kHeadBatch) {
                     const int some = min(kHeadBatch, heads - j0);
                     for (int j = 0; j < some; ++j) {
-                        uint64_t o0 = pair(0.f, 0.f), o1 = o0;
+                        uint64_t o0 = f2_pack(0.f, 0.f), o1 = o0;
                         float q[R];
                         load_row<R>(&s_q[i * heads + j0 + j][row0], q);
 #pragma unroll
                         for (int x = 0; x < R; ++x) {
-                            const uint64_t y = pair(q[x], q[x]);
-                            o0 = fma2(y, s[x][0], o0);
-                            o1 = fma2(y, s[x][1], o1);
+                            const uint64_t y = f2_pack(q[x], q[x]);
+                            o0 = f2_fma(y, s[x][0], o0);
+                            o1 = f2_fma(y, s[x][1], o1);
                         }
-                        const float2 a = unpair(o0), b = unpair(o1);
-                        float4 o = make_float4(a.x, a.y, b.x, b.y);
+                        float4 o;
+                        f2_unpack(o0, o.x, o.y);
+                        f2_unpack(o1, o.z, o.w);
 #pragma unroll
                         for (int x = G::kLanes; x < 32; x <<= 1) {
                             o.x += __shfl_xor_sync(0xffffffffu, o.x, x);
@@ -211,8 +191,10 @@ __device__ __forceinline__ void step_job(const LinearParams &p) {
     float *dst = p.state + to * state_size + place;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        const float2 a = unpair(s[i][0]), b = unpair(s[i][1]);
-        __stcs(reinterpret_cast<float4 *>(dst + i * D), make_float4(a.x, a.y, b.x, b.y));
+        float4 x;
+        f2_unpack(s[i][0], x.x, x.y);
+        f2_unpack(s[i][1], x.z, x.w);
+        __stcs(reinterpret_cast<float4 *>(dst + i * D), x);
     }
 }
 

@@ -40,21 +40,25 @@ namespace {
 constexpr int kC = kLinearChunk;
 constexpr int kSlice = 64;   // state columns of a CTA
 constexpr int kRows = 128;   // rows of a query tile, and of a state's MMA
-constexpr int kWarpQK = 1, kWarpPV = 2, kWarpQS = 3, kFirstOut = 4, kFirstWeigh = 12,
+constexpr int kWarpQK = 1, kWarpKV = 2, kWarpQS = 3, kFirstOut = 4, kFirstWeigh = 12,
               kFirstState = 16;
-constexpr int kMmaWarps = 3, kGroupWarps = 4, kWeighWarps = 4, kStateWarps = 8;
-constexpr int kWarps = kFirstState + kStateWarps, kThreads = 32 * kWarps;
+constexpr int kMmaWarps = 4, kGroupWarps = 4, kWeighWarps = 4, kStateWarps = 8;
+constexpr int kWarpPV = kFirstState + kStateWarps;
+constexpr int kWarpScan = kWarpPV + 1;
+constexpr int kWarps = kWarpScan + 1, kThreads = 32 * kWarps;
+static_assert(kWarpPV % kMmaWarps == 0, "a barrier of drain[] each");
 constexpr int kRing = 3;     // chunks of K and V in shared memory
 constexpr int kQueue = 4;
-constexpr int kTables = 4;   // chunks whose sums of logarithms are kept
+constexpr int kTables = 8;   // chunks whose sums of logarithms are kept
+constexpr int kVtBars = 4;   // chunks ahead of whoever looks at their weighed V's barrier
 constexpr int kParts = 3;    // bf16 numbers whose sum is a weighed element of V
 // Logarithms (base 2) below this are as good as none: what they multiply is 0 in fp32.
 constexpr float kLeastLog = -150.f;
 
 // Of a chunk's tokens: the logarithms' sums up to each (base 2), e^ of what lies between a token
-// and the end of its run of 16, and the whole sum.
+// and the end of its run of 16, of what lies behind it in the chunk, and the whole sum.
 struct alignas(16) Table {
-    float sum[kC], tail[kC];
+    float sum[kC], tail[kC], weight[kC];
     float all, pad[3];
 };
 
@@ -68,8 +72,8 @@ struct Geom {
     static constexpr int kSBytes = kRows * 128;  // bf16 state: 128 rows x 64 columns
     static constexpr int kOffQ = 0;              // [2]
     static constexpr int kOffKV = kOffQ + 2 * kQBytes;
-    static constexpr int kOffVt = kOffKV + kRing * kStageBytes;  // weighed V, part after part
-    static constexpr int kOffS = kOffVt + kParts * kVBytes;      // [2]
+    static constexpr int kOffVt = kOffKV + kRing * kStageBytes;  // weighed V, part after part [2]
+    static constexpr int kOffS = kOffVt + 2 * kParts * kVBytes;  // [2]
     static constexpr int kOffBar = kOffS + 2 * kSBytes;
     static constexpr int kOffTab = kOffBar + 320;                // [kTables]
     static constexpr int kOffCtl = kOffTab + kTables * static_cast<int>(sizeof(Table));
@@ -89,7 +93,7 @@ struct Bars {
     uint64_t q_full[2], q_empty[2];
     // weighed V (and table) of a chunk there; its update done (which frees the weighed V) /
     // read.  The weighing warps may be two chunks ahead of who looks at their barrier.
-    uint64_t vt_full[kTables], u_full[2], u_empty[2];
+    uint64_t tab_full[kVtBars], vt_full[kVtBars], u_full[2], u_empty[2];
     uint64_t s_full[2], s_empty[2];    // state before a chunk in shared memory / read
     uint64_t sc_full[2], p_full[2];    // scores of a tile / its P
     uint64_t o_full[2], o_empty[2];
@@ -234,7 +238,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars->kv_empty[i], kMmaWarps);
         }
         for (int i = 0; i < kMmaWarps; ++i) mbar_init(&bars->drain[i], 1);
-        for (int i = 0; i < kTables; ++i) mbar_init(&bars->vt_full[i], kWeighWarps);
+        for (int i = 0; i < kVtBars; ++i) {
+            mbar_init(&bars->tab_full[i], 1);
+            mbar_init(&bars->vt_full[i], kWeighWarps);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->q_full[i], 1);
             mbar_init(&bars->q_empty[i], 2);  // by Q K^T and Q S
@@ -359,10 +366,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_drain(&bars->kv_full[i % kRing], (i / kRing) & 1);
             for (uint32_t i = t > 2 ? t - 2 : 0; i < t; ++i) mbar_drain(&bars->q_full[i & 1], (i >> 1) & 1);
         }
-    } else if (warp < kFirstOut) {
+    } else if (warp < kFirstOut || warp == kWarpPV) {
         // ============================ MMAs ============================
-        // A thread of three warps each, so that none stands behind another's wait: one the
-        // scores, one the updates and P V, one Q S.  (One thread, not a warp with an elected
+        // A thread of four warps each, so that none stands behind another's wait or issue (an MMA
+        // takes its thread 120 to 260 cycles, and a chunk has 32): the scores, the updates, Q S,
+        // and P V.  (One thread, not a warp with an elected
         // lane's predicate: operands in a warp's uniform registers are no longer its own when
         // a wait has taken the lanes apart.  A commit was seen to arrive twice, and worse.)
         constexpr uint32_t idesc_qk = idesc_bf16_f32(kRows, kC, 0);
@@ -384,16 +392,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto wait_chunk = [&]() { return wait(&bars->kv_full[c % kRing], (c / kRing) & 1); };
         auto update = [&]() {
-            if (!wait(&bars->vt_full[u % kTables], (u / kTables) & 1) ||
+            if (!wait(&bars->vt_full[u % kVtBars], (u / kVtBars) & 1) ||
                 (u >= 2 && !wait(&bars->u_empty[u & 1], ((u >> 1) - 1) & 1)))
                 return;
             tc_fence_after();
             const uint64_t kd = kt_desc + (c % kRing) * (G::kStageBytes >> 4);
+            const uint64_t vd = vt_desc + (u & 1) * (kParts * G::kVBytes >> 4);
             const uint32_t d = tmem + G::kColU + (u & 1) * kSlice;
             static_assert(G::kVBytes == kC * 128, "parts follow each other");
 #pragma unroll 1
             for (int kk = 0; kk < kParts * (kC / 16); ++kk)
-                tc_mma(d, kd + kk % (kC / 16) * (2048 >> 4), vt_desc + kk * (2048 >> 4), idesc_kv,
+                tc_mma(d, kd + kk % (kC / 16) * (2048 >> 4), vd + kk * (2048 >> 4), idesc_kv,
                        kk > 0 ? 1u : 0u);
             tc_commit(&bars->u_full[u & 1]);
             ++u;
@@ -440,8 +449,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0 && (outputs || it.c_end < it.chunks))
 #pragma unroll 1
                     for (int i = it.c_begin; ok && i < it.c_end && wait_chunk(); ++i, ++c) {
-                        if (warp == kWarpPV) update();
-                        if (ok && outputs) {
+                        if (warp == kWarpKV) update();
+                        // (V's rows behind the request are zeroed with its weighing)
+                        if (warp == kWarpPV) {
+                            wait(&bars->vt_full[u % kVtBars], (u / kVtBars) & 1);
+                            ++u;
+                        }
+                        if (ok && outputs && warp != kWarpKV) {
                             const bool qs = warp == kWarpQS;
                             if (qs) wait(&bars->s_full[s & 1], (s >> 1) & 1);
                             if (warp == kWarpPV)
@@ -470,8 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0 && (!ok || *abort_flag)) {
             // MMAs already issued finish before TMEM is released
-            tc_commit(&bars->drain[warp - kWarpQK]);
-            mbar_drain(&bars->drain[warp - kWarpQK], 0);
+            tc_commit(&bars->drain[warp & (kMmaWarps - 1)]);
+            mbar_drain(&bars->drain[warp & (kMmaWarps - 1)], 0);
         }
         __syncwarp();
     } else if (warp < kFirstWeigh) {
@@ -503,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t tt = t + m;
                 if ((tt & 1) == grp) {
                     const uint32_t turn = (tt >> 1) & 1, uu = u + (i - it.c_begin);
-                    ok = warp_mbar_wait_small(&bars->vt_full[uu % kTables], (uu / kTables) & 1, abort_flag) &&
+                    ok = warp_mbar_wait_small(&bars->vt_full[uu % kVtBars], (uu / kVtBars) & 1, abort_flag) &&
                          warp_mbar_wait_small(&bars->sc_full[grp], turn, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
@@ -601,6 +615,80 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int vw = warp - kFirstWeigh;
         uint32_t c = 0, u = 0;  // chunks of the ring, updates
         bool ok = true;
+        for (int k = 0;; ++k) {
+            const Item it = queue_item(ctl, warp, k);
+            if (it.n == 0) break;
+#pragma unroll 1
+            for (int outputs = size > 1 ? 0 : 1; outputs < 2; ++outputs) {
+                const int c_last = outputs || it.c_end < it.chunks ? it.c_end : it.c_begin;
+#pragma unroll 1
+                for (int i = it.c_begin; ok && i < c_last; ++i, ++c, ++u) {
+                    const int st = c % kRing;
+                    // the chunk is here, and the update of two chunks ago has read its weighed V
+                    ok = warp_mbar_wait_small(&bars->kv_full[st], (c / kRing) & 1, abort_flag) &&
+                         warp_mbar_wait_small(&bars->tab_full[u % kVtBars], (u / kVtBars) & 1, abort_flag) &&
+                         (u < 2 || warp_mbar_wait_small(&bars->u_full[u & 1], ((u >> 1) - 1) & 1, abort_flag));
+                    if (!ok) break;
+                    uint8_t *k_tile = sKV + st * G::kStageBytes, *v = k_tile + G::kKBytes;
+                    uint8_t *vt = sVt + (u & 1) * (kParts * G::kVBytes);
+                    const float *weight = tables[u % kTables].weight;
+                    const int valid = min(kC, it.n - i * kC);
+                    // eight lanes to a row of 64 elements
+#pragma unroll 2
+                    for (int x = 0; x < kC / (4 * kWeighWarps); ++x) {
+                        const int row = vw * (kC / kWeighWarps) + x * 4 + lane / 8;
+                        const uint32_t off = sw128_offset(row, lane % 8);
+                        const uint64_t wt = f2_pack(weight[row], weight[row]);
+                        uint4 in = *reinterpret_cast<const uint4 *>(v + off);
+                        // rows behind the request are another's, or padding: whatever stands
+                        // there does not reach a sum
+                        if (row >= valid) {
+                            in = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4 *>(v + off) = in;
+#pragma unroll
+                            for (int hf = 0; hf < G::kHalves; ++hf)
+                                *reinterpret_cast<uint4 *>(k_tile + hf * G::kKHalf + off) = in;
+                        }
+                        uint4 part[kParts];
+                        const uint64_t minus = f2_pack(-1.f, -1.f);
+                        auto two = [](uint32_t pair) {
+                            return f2_pack(__uint_as_float(pair << 16),
+                                           __uint_as_float(pair & 0xFFFF0000u));
+                        };
+                        auto round = [](uint64_t v2) {
+                            float lo, hi;
+                            f2_unpack(v2, lo, hi);
+                            return pack_bf16x2(lo, hi);
+                        };
+                        auto split = [&](uint32_t pair, uint32_t &p0, uint32_t &p1, uint32_t &p2) {
+                            uint64_t y = f2_mul(two(pair), wt);
+                            p0 = round(y);
+                            y = f2_fma(two(p0), minus, y);
+                            p1 = round(y);
+                            p2 = round(f2_fma(two(p1), minus, y));
+                        };
+                        split(in.x, part[0].x, part[1].x, part[2].x);
+                        split(in.y, part[0].y, part[1].y, part[2].y);
+                        split(in.z, part[0].z, part[1].z, part[2].z);
+                        split(in.w, part[0].w, part[1].w, part[2].w);
+#pragma unroll
+                        for (int n = 0; n < kParts; ++n)
+                            *reinterpret_cast<uint4 *>(vt + n * G::kVBytes + off) = part[n];
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->vt_full[u % kVtBars]);
+                }
+                if (!outputs) {
+                    cluster_sync();
+                    cluster_sync();
+                }
+            }
+        }
+    } else if (warp == kWarpScan) {
+        // ============================ sums of logarithms ============================
+        uint32_t c = 0;
+        bool ok = true;
         // logarithm (base 2) of the decay of token i of the request
         auto log_of = [&](const Item &it, int i) {
             if (i >= it.n) return 0.f;
@@ -612,94 +700,54 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (it.n == 0) break;
 #pragma unroll 1
             for (int outputs = size > 1 ? 0 : 1; outputs < 2; ++outputs) {
-            const int c_last = outputs || it.c_end < it.chunks ? it.c_end : it.c_begin;
-            float g0 = log_of(it, it.c_begin * kC + 2 * lane);
-            float g1 = log_of(it, it.c_begin * kC + 2 * lane + 1);
+                const int c_last = outputs || it.c_end < it.chunks ? it.c_end : it.c_begin;
+                float g0 = 0.f, g1 = 0.f, n0 = 0.f, n1 = 0.f;
 #pragma unroll 1
-            for (int i = it.c_begin; ok && i < c_last; ++i, ++c, ++u) {
-                // sums up to each token (lane: tokens 2 lane and 2 lane + 1), and of those behind
-                // it (each without a difference, so that a small one keeps its digits beside
-                // large ones)
-                float up = g0 + g1, down = up;
+                for (int i = it.c_begin - 1; ok && i < c_last; ++i) {
+                    g0 = n0;
+                    g1 = n1;
+                    if (i + 1 < c_last) {  // the next chunk's, a chunk ahead
+                        n0 = log_of(it, (i + 1) * kC + 2 * lane);
+                        n1 = log_of(it, (i + 1) * kC + 2 * lane + 1);
+                    }
+                    if (i < it.c_begin) continue;
+                    // sums up to each token (lane: tokens 2 lane and 2 lane + 1), and of those
+                    // behind it (each without a difference, so that a small one keeps its digits
+                    // beside large ones)
+                    float up = g0 + g1, down = up;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const float a = __shfl_up_sync(0xffffffffu, up, o);
-                    const float b = __shfl_down_sync(0xffffffffu, down, o);
-                    if (lane >= o) up += a;
-                    if (lane + o < 32) down += b;
-                }
-                const float all = __shfl_sync(0xffffffffu, up, 31);
-                float up0 = __shfl_up_sync(0xffffffffu, up, 1);
-                float down1 = __shfl_down_sync(0xffffffffu, down, 1);
-                if (lane == 0) up0 = 0.f;
-                if (lane == 31) down1 = 0.f;
-                up0 += g0;
-                const float w0 = exp2f(down1 + g1), w1 = exp2f(down1);
-                if (vw == 0) {
-                    Table &tab = tables[u % kTables];
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const float a = __shfl_up_sync(0xffffffffu, up, o);
+                        const float b = __shfl_down_sync(0xffffffffu, down, o);
+                        if (lane >= o) up += a;
+                        if (lane + o < 32) down += b;
+                    }
                     const float end = __shfl_sync(0xffffffffu, up, lane | 7);  // of the run of 16
+                    float up0 = __shfl_up_sync(0xffffffffu, up, 1);
+                    float down1 = __shfl_down_sync(0xffffffffu, down, 1);
+                    if (lane == 0) up0 = 0.f;
+                    if (lane == 31) down1 = 0.f;
+                    up0 += g0;
+                    // (the chunk of three ago is through its MMAs: who still reads a table is no
+                    // further behind than the one of five ago)
+                    ok = c < kRing ||
+                         warp_mbar_wait_small(&bars->kv_empty[c % kRing], (c / kRing - 1) & 1, abort_flag);
+                    if (!ok) break;
+                    Table &tab = tables[c % kTables];
                     *reinterpret_cast<float2 *>(tab.sum + 2 * lane) = make_float2(up0, up);
                     *reinterpret_cast<float2 *>(tab.tail + 2 * lane) =
                         make_float2(fast_exp2(end - up0), fast_exp2(end - up));
-                    if (lane == 0) tab.all = all;
+                    *reinterpret_cast<float2 *>(tab.weight + 2 * lane) =
+                        make_float2(exp2f(down1 + g1), exp2f(down1));
+                    if (lane == 31) tab.all = up;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->tab_full[c % kVtBars]);
+                    ++c;
                 }
-                if (i + 1 < it.c_end) {
-                    g0 = log_of(it, (i + 1) * kC + 2 * lane);
-                    g1 = log_of(it, (i + 1) * kC + 2 * lane + 1);
+                if (!outputs) {
+                    cluster_sync();
+                    cluster_sync();
                 }
-                const int st = c % kRing;
-                // the chunk is here, and the last one's update has read its weighed V
-                ok = warp_mbar_wait_small(&bars->kv_full[st], (c / kRing) & 1, abort_flag) &&
-                     (u == 0 || warp_mbar_wait_small(&bars->u_full[(u - 1) & 1], ((u - 1) >> 1) & 1, abort_flag));
-                if (!ok) break;
-                uint8_t *k = sKV + st * G::kStageBytes, *v = k + G::kKBytes;
-                const int valid = min(kC, it.n - i * kC);
-                // eight lanes to a row of 64 elements
-#pragma unroll 1
-                for (int x = 0; x < kC / (4 * kWeighWarps); ++x) {
-                    const int row = vw * (kC / kWeighWarps) + x * 4 + lane / 8;
-                    const float wa = __shfl_sync(0xffffffffu, w0, row >> 1);
-                    const float wb = __shfl_sync(0xffffffffu, w1, row >> 1);
-                    const float wt = row & 1 ? wb : wa;
-                    const uint32_t off = sw128_offset(row, lane % 8);
-                    const uint4 z = make_uint4(0, 0, 0, 0);
-                    uint4 in = *reinterpret_cast<const uint4 *>(v + off);
-                    // rows behind the request are another's, or padding: whatever stands there
-                    // does not reach a sum
-                    if (row >= valid) {
-                        in = z;
-                        *reinterpret_cast<uint4 *>(v + off) = z;
-#pragma unroll
-                        for (int hf = 0; hf < G::kHalves; ++hf)
-                            *reinterpret_cast<uint4 *>(k + hf * G::kKHalf + off) = z;
-                    }
-                    uint4 part[kParts];
-                    auto split = [&](uint32_t pair, uint32_t &p0, uint32_t &p1, uint32_t &p2) {
-                        float lo = __uint_as_float(pair << 16) * wt;
-                        float hi = __uint_as_float(pair & 0xFFFF0000u) * wt;
-                        p0 = pack_bf16x2(lo, hi);
-                        lo -= __uint_as_float(p0 << 16);
-                        hi -= __uint_as_float(p0 & 0xFFFF0000u);
-                        p1 = pack_bf16x2(lo, hi);
-                        p2 = pack_bf16x2(lo - __uint_as_float(p1 << 16),
-                                         hi - __uint_as_float(p1 & 0xFFFF0000u));
-                    };
-                    split(in.x, part[0].x, part[1].x, part[2].x);
-                    split(in.y, part[0].y, part[1].y, part[2].y);
-                    split(in.z, part[0].z, part[1].z, part[2].z);
-                    split(in.w, part[0].w, part[1].w, part[2].w);
-#pragma unroll
-                    for (int n = 0; n < kParts; ++n)
-                        *reinterpret_cast<uint4 *>(sVt + n * G::kVBytes + off) = part[n];
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->vt_full[u % kTables]);
-            }
-            if (!outputs) {
-                cluster_sync();
-                cluster_sync();
-            }
             }
         }
     } else {
@@ -731,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // takes a chunk's update in
         auto update = [&]() {
             ok = warp_mbar_wait_small(&bars->u_full[u & 1], (u >> 1) & 1, abort_flag) &&
-                 warp_mbar_wait_small(&bars->vt_full[u % kTables], (u / kTables) & 1, abort_flag);
+                 warp_mbar_wait_small(&bars->vt_full[u % kVtBars], (u / kVtBars) & 1, abort_flag);
             if (!ok) return;
             tc_fence_after();
             const float all = tables[u % kTables].all, keep = exp2f(all);

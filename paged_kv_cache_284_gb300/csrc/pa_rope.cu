@@ -81,11 +81,6 @@ __device__ __forceinline__ uint4 pack8_bf16(const uint64_t (&x)[4]) {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 
 // a b + c rounded down.  A remainder is exact in any rounding; rounded down, an
 // exact zero is -0, and -0 added to a zero leaves that zero its sign.
