@@ -1322,6 +1322,7 @@ int pa_build_step(const int32_t *query_lens, const int32_t *cached_lens, int32_t
     p.num_blocks = num_blocks;
     p.block_size = block_size;
     p.num_tokens = num_tokens;
+    p.sms = dev->sms;
     p.query_start_loc = query_start_loc;
     p.context_lens = context_lens;
     p.seq_lens = seq_lens;

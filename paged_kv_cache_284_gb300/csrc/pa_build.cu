@@ -11,9 +11,14 @@
 // table column, and the block -- an old one from the table, a new one from the list.
 //
 // Bound: latency (launch, lengths, scan, table entry; the bytes of 65536 tokens are 0.2 us of
-// HBM time).  One cluster of 1 to 8 CTAs: each scans all rows for itself, so that no sum
-// crosses CTAs, takes its share of the tokens, and a cluster barrier stands before what the
-// call may change in place (lengths, the list's state).
+// HBM time).  Every CTA scans all rows for itself, so that no sum crosses CTAs.  Up to
+// kWholeTokens one CTA does the whole step (64 decode rows: 3.4 us).  Above, the tokens have a
+// grid of their own, a token to a thread, and a cluster of 8 beside it has the rows: it counts
+// the entries of finished rows, a warp to a row, passes the counts round through distributed
+// shared memory, gives the blocks back, and after the tokens' kernel has ended writes what the
+// call may change in place (lengths, the list's state).  4500 tokens of 256 rows, 12 of them
+// done: 7.9 us, 9.0 as one kernel of 8 CTAs; 140000 tokens of 1024 rows, 64 done: 10.3 us, 32.6
+// so.  Decode rows: 300 take 3.9 us whole and 5.3 split, 1000 8.8 and 8.7, 2000 11.7 and 9.7.
 #include <algorithm>
 
 #include "pa_internal.cuh"
@@ -24,15 +29,18 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
+constexpr int kWholeTokens = kThreads;
 
 struct Sums {
     long long tokens, blocks;
+    int done;  // rows
 };
 __device__ __forceinline__ Sums operator+(const Sums &a, const Sums &b) {
-    return {a.tokens + b.tokens, a.blocks + b.blocks};
+    return {a.tokens + b.tokens, a.blocks + b.blocks, a.done + b.done};
 }
 __device__ __forceinline__ Sums shfl_up(const Sums &s, int o) {
-    return {__shfl_up_sync(0xffffffffu, s.tokens, o), __shfl_up_sync(0xffffffffu, s.blocks, o)};
+    return {__shfl_up_sync(0xffffffffu, s.tokens, o), __shfl_up_sync(0xffffffffu, s.blocks, o),
+            __shfl_up_sync(0xffffffffu, s.done, o)};
 }
 
 // A row of the batch as the call found it.
@@ -65,29 +73,57 @@ __device__ __forceinline__ int row_of(const int *start, int rows, int t) {
     return lo;
 }
 
+// Calls f with a table row's first n entries, 32 at a time (-1 behind the last), by a whole
+// warp; eight loads in flight, whose latency is what a row costs.
+template <typename F>
+__device__ __forceinline__ void for_entries(const int32_t *row, int n, F f) {
+    const int lane = threadIdx.x & 31;
+    for (int col0 = 0; col0 < n; col0 += 256) {
+        int entry[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int col = col0 + 32 * i + lane;
+            entry[i] = col < n ? row[col] : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f(entry[i]);
+    }
+}
+
+// What a launch does: the whole step (one CTA), its tokens (any grid), or the rest (one cluster).
+enum Part { kWhole, kTokens, kRows };
+
 }  // namespace
 
+template <Part PART>
 __global__ void __launch_bounds__(kThreads) build_step_kernel(const BuildParams p) {
-    extern __shared__ int row_info[];  // [3][num_seqs]: first token, cached tokens, first new block
+    // [5][num_seqs]: first token, cached tokens, first new block; the rows that are done and
+    // how many blocks each gives back
+    extern __shared__ int row_info[];
     __shared__ Sums warp_sums[kWarps];
     __shared__ int warp_given[kWarps];
-    int *start = row_info, *ctx_of = row_info + p.num_seqs, *block_of = ctx_of + p.num_seqs;
+    int *start = row_info, *ctx_of = row_info + p.num_seqs, *block_of = ctx_of + p.num_seqs,
+        *done_rows = block_of + p.num_seqs, *gives = done_rows + p.num_seqs;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rank = blockIdx.x, size = gridDim.x;  // the grid is one cluster
-    pdl_wait();
-    pdl_trigger();
+    const int rank = blockIdx.x, size = gridDim.x;
+    if (PART == kRows) cluster_arrive_relaxed();
+    // kRows: the tokens' kernel has let this one start after its own wait, so what came before
+    // is there; only the outputs that may be inputs wait for its end
+    if (PART != kRows) {
+        pdl_wait();
+        pdl_trigger();
+    }
     const int head = p.free_state[0], count = p.free_state[1];
 
     // 1. sums over the rows: thread t has rows t * each ..
     const int each = (p.num_seqs + kThreads - 1) / kThreads;
     const int b0 = min(p.num_seqs, tid * each), b1 = min(p.num_seqs, b0 + each);
-    Sums mine{0, 0};
-    bool bad = false, any_done = false;
+    Sums mine{0, 0, 0};
+    bool bad = false;
     for (int b = b0; b < b1; ++b) {
         const Row r = load_row(p, b);
         bad |= r.bad;
-        any_done |= r.done;
-        mine = mine + Sums{r.n, r.need};
+        mine = mine + Sums{r.n, r.need, r.done};
     }
     Sums incl = mine;
 #pragma unroll
@@ -98,9 +134,8 @@ __global__ void __launch_bounds__(kThreads) build_step_kernel(const BuildParams 
     if (lane == 31) warp_sums[warp] = incl;
     bad = head < 0 || head >= p.capacity || count < 0 || count > p.capacity || bad;
     bad = __syncthreads_or(bad);
-    any_done = __syncthreads_or(any_done);
     if (warp == 0) {
-        Sums w = lane < kWarps ? warp_sums[lane] : Sums{0, 0};
+        Sums w = lane < kWarps ? warp_sums[lane] : Sums{0, 0, 0};
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const Sums before = shfl_up(w, o);
@@ -110,23 +145,25 @@ __global__ void __launch_bounds__(kThreads) build_step_kernel(const BuildParams 
     }
     __syncthreads();
     const Sums total = warp_sums[kWarps - 1];
-    const Sums base = warp > 0 ? warp_sums[warp - 1] : Sums{0, 0};
+    const Sums base = warp > 0 ? warp_sums[warp - 1] : Sums{0, 0, 0};
     // all or nothing: a step that does not fit leaves the rows, the tables and the list as
     // they are, and its metadata holds no token
     bad |= total.tokens > p.num_tokens;
     const long long missing = bad ? 0 : max(0ll, total.blocks - count);
     const bool good = !bad && missing == 0;
-    if (rank == 0 && tid == 0 && !good)
+    if (PART != kTokens && rank == 0 && tid == 0 && !good)
         flag_status(p.status, bad ? PA_DEV_BAD_METADATA : PA_DEV_NO_BLOCKS);
     {
         // (sums of a step that does not fit may pass 32 bits and are not used)
-        Sums at = base + Sums{incl.tokens - mine.tokens, incl.blocks - mine.blocks};
+        Sums at = base + Sums{incl.tokens - mine.tokens, incl.blocks - mine.blocks,
+                              incl.done - mine.done};
         for (int b = b0; b < b1; ++b) {
             const Row r = load_row(p, b);
             start[b] = good ? static_cast<int>(at.tokens) : 0;
             ctx_of[b] = r.ctx;
             block_of[b] = good ? static_cast<int>(at.blocks) : 0;
-            at = at + Sums{r.n, r.need};
+            if (r.done) done_rows[at.done] = b;
+            at = at + Sums{r.n, r.need, r.done};
         }
     }
     __syncthreads();
@@ -134,7 +171,7 @@ __global__ void __launch_bounds__(kThreads) build_step_kernel(const BuildParams 
     const int taken = good ? static_cast<int>(total.blocks) : 0;
 
     // 2. slots and positions; the first token of a new block enters it in the table
-    for (int64_t i = static_cast<int64_t>(rank) * kThreads + tid; i < p.num_tokens;
+    for (int64_t i = static_cast<int64_t>(rank) * kThreads + tid; PART != kRows && i < p.num_tokens;
          i += static_cast<int64_t>(size) * kThreads) {
         const int t = static_cast<int>(i);
         int64_t slot = -1;
@@ -166,24 +203,32 @@ __global__ void __launch_bounds__(kThreads) build_step_kernel(const BuildParams 
     // 3. the blocks of finished rows to the list's tail, rows and columns in order; entries
     // that were given back before (negative) are passed over.  The tail lies behind all that
     // was free, so nothing taken above is overwritten.
+    if (PART == kTokens) return;
     int given = 0;
-    if (any_done && good) {
-        // entries of a row, one warp each; the counts take the place of block_of
-        __syncthreads();
-        for (int b = warp; b < p.num_seqs; b += kWarps) {
-            const Row r = load_row(p, b);
+    if (PART == kRows) cluster_wait();  // every CTA runs: its shared memory may be written
+    if (total.done > 0 && good) {
+        // entries of a row, one warp of the cluster each
+        for (int d = rank * kWarps + warp; d < total.done; d += size * kWarps) {
+            const int b = done_rows[d];
             int live = 0;
-            if (r.done)
-                for (int col = lane; col < r.have; col += 32) {
-                    const int blk = p.block_tables[static_cast<int64_t>(b) * p.max_blocks + col];
-                    live += blk >= 0 && blk < p.num_blocks;
-                }
+            for_entries(p.block_tables + static_cast<int64_t>(b) * p.max_blocks,
+                        (ctx_of[b] + p.block_size - 1) / p.block_size,
+                        [&](int blk) { live += blk >= 0 && blk < p.num_blocks; });
             live = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(live)));
-            if (lane == 0) block_of[b] = live;
+            if (PART == kRows) {
+                if (lane < size) st_cluster(gives + d, lane, live);
+            } else if (lane == 0) {
+                gives[d] = live;
+            }
         }
-        __syncthreads();
+        if (PART == kRows)
+            cluster_sync();
+        else
+            __syncthreads();
+        const int d_each = (total.done + kThreads - 1) / kThreads;
+        const int d0 = min(total.done, tid * d_each), d1 = min(total.done, d0 + d_each);
         int sum = 0;
-        for (int b = b0; b < b1; ++b) sum += block_of[b];
+        for (int d = d0; d < d1; ++d) sum += gives[d];
         int run = sum;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -197,33 +242,29 @@ __global__ void __launch_bounds__(kThreads) build_step_kernel(const BuildParams 
             if (w < warp) at += warp_given[w];
             given += warp_given[w];
         }
-        for (int b = b0; b < b1; ++b) {
-            const int n = block_of[b];
-            block_of[b] = at;
+        for (int d = d0; d < d1; ++d) {
+            const int n = gives[d];
+            gives[d] = at;
             at += n;
         }
         __syncthreads();
         const int room = p.capacity - count;
-        for (int b = rank * kWarps + warp; b < p.num_seqs; b += size * kWarps) {
-            const Row r = load_row(p, b);
-            if (!r.done) continue;
-            int next = block_of[b];
-            for (int col0 = 0; col0 < r.have; col0 += 32) {
-                const int col = col0 + lane;
-                const int blk = col < r.have
-                                    ? p.block_tables[static_cast<int64_t>(b) * p.max_blocks + col]
-                                    : -1;
-                if (blk >= p.num_blocks) flag_status(p.status, PA_DEV_BAD_BLOCK);
-                const bool live = blk >= 0 && blk < p.num_blocks;
-                const unsigned lives = __ballot_sync(0xffffffffu, live);
-                const int place = next + __popc(lives & ((1u << lane) - 1));
-                if (live && place < room) {
-                    int64_t to = static_cast<int64_t>(head) + count + place;
-                    if (to >= p.capacity) to -= p.capacity;
-                    p.free_blocks[to] = blk;
-                }
-                next += __popc(lives);
-            }
+        for (int d = rank * kWarps + warp; d < total.done; d += size * kWarps) {
+            const int b = done_rows[d];
+            int next = gives[d];
+            for_entries(p.block_tables + static_cast<int64_t>(b) * p.max_blocks,
+                        (ctx_of[b] + p.block_size - 1) / p.block_size, [&](int blk) {
+                            if (blk >= p.num_blocks) flag_status(p.status, PA_DEV_BAD_BLOCK);
+                            const bool live = blk >= 0 && blk < p.num_blocks;
+                            const unsigned lives = __ballot_sync(0xffffffffu, live);
+                            const int place = next + __popc(lives & ((1u << lane) - 1));
+                            if (live && place < room) {
+                                int64_t to = static_cast<int64_t>(head) + count + place;
+                                if (to >= p.capacity) to -= p.capacity;
+                                p.free_blocks[to] = blk;
+                            }
+                            next += __popc(lives);
+                        });
         }
         if (given > room) {  // more blocks than the list holds: one was in it twice
             if (rank == 0 && tid == 0) flag_status(p.status, PA_DEV_BAD_METADATA);
@@ -233,7 +274,11 @@ __global__ void __launch_bounds__(kThreads) build_step_kernel(const BuildParams 
 
     // 4. the rows' lengths and the list's state, which may be the call's inputs: after every
     // CTA has read them
-    if (size > 1)
+    if (PART == kRows) {
+        pdl_wait();
+        pdl_trigger();
+    }
+    if (PART == kRows)
         cluster_sync();
     else
         __syncthreads();
@@ -257,19 +302,27 @@ __global__ void __launch_bounds__(kThreads) build_step_kernel(const BuildParams 
     }
 }
 
-int launch_build_step(const BuildParams &p, cudaStream_t s) {
+namespace {
+template <Part PART>
+int launch(const BuildParams &p, int ctas, cudaStream_t s) {
     static PerDeviceOnce once;
     if (once_per_device(once, [] {
-            return cudaFuncSetAttribute(build_step_kernel,
+            return cudaFuncSetAttribute(build_step_kernel<PART>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        3 * 4 * kBuildMaxSeqs);
+                                        5 * 4 * kBuildMaxSeqs);
         }) != PA_OK)
         return PA_ERR_CUDA;
-    int size = 1;
-    while (size < kDirectMaxCluster && static_cast<int64_t>(size) * kThreads < p.num_tokens) size *= 2;
-    PdlLaunch l(size, kThreads, 3 * sizeof(int) * p.num_seqs, s);
-    if (size > 1) l.set_cluster(size);
-    return launch_kernel(l, build_step_kernel, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    PdlLaunch l(ctas, kThreads, 5 * sizeof(int) * p.num_seqs, s);
+    if (PART == kRows) l.set_cluster(ctas);
+    return launch_kernel(l, build_step_kernel<PART>, p) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+}  // namespace
+
+int launch_build_step(const BuildParams &p, cudaStream_t s) {
+    if (p.num_tokens <= kWholeTokens) return launch<kWhole>(p, 1, s);
+    const int64_t ctas = (static_cast<int64_t>(p.num_tokens) + kThreads - 1) / kThreads;
+    const int rc = launch<kTokens>(p, static_cast<int>(std::min<int64_t>(p.sms, ctas)), s);
+    return rc != PA_OK ? rc : launch<kRows>(p, kDirectMaxCluster, s);
 }
 
 }  // namespace pa

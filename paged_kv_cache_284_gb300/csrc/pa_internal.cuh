@@ -330,7 +330,7 @@ struct RopeParams {
 };
 
 // A step's metadata from its requests' lengths (pa_build_step).
-constexpr int kBuildMaxSeqs = 8192;  // three ints of shared memory each
+constexpr int kBuildMaxSeqs = 8192;  // five ints of shared memory each
 struct BuildParams {
     const int32_t *query_lens, *cached_lens;
     int32_t *block_tables;
@@ -338,7 +338,7 @@ struct BuildParams {
     int32_t *free_blocks;
     const int32_t *free_state;
     int32_t *free_state_out;
-    int capacity, num_blocks, block_size, num_tokens;
+    int capacity, num_blocks, block_size, num_tokens, sms;
     int32_t *query_start_loc, *context_lens, *seq_lens, *positions;
     int64_t *slot_mapping;
     unsigned *status;
@@ -704,12 +704,26 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same barrier in two halves, without what was written: that every CTA has started.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
 // Loads from the shared memory of CTA `rank` of the cluster, at the place that
 // `local` has in this CTA's.
 __device__ __forceinline__ uint32_t cluster_addr(const void *local, int rank) {
     uint32_t a;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
     return a;
+}
+// (a store: after a cluster barrier, so that the other CTA has started)
+__device__ __forceinline__ void st_cluster(int *local, int rank, int value) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(local, rank)), "r"(value)
+                 : "memory");
 }
 __device__ __forceinline__ float ld_cluster_at(uint32_t addr) {
     float v;
