@@ -11,12 +11,25 @@
 //   inside  P V              P = the scores times e^(G_i - G_j), masked, over them in TMEM
 //   before  Q S              S in bf16, in shared memory
 //   update  K^T (e^(G_L - G) V), M = the state's rows
-// Roles: warp 0 loads; warps 1-3 issue the MMAs; warps 4-11, two groups that take
-// the tiles in turn, make P and write the outputs (one thread a row); warps 12-15 weigh V; warps
-// 16-23 keep the state, 32 fp32 values of a thread.  So the chain from one chunk's state to the
-// next (update, sum, rounding) and the chain of the weighed V run beside each other and beside
-// the outputs.  Loops over 16 columns stay loops: with six kinds of warps on a scheduler,
-// straight-line code spends its time waiting for instructions.
+// Roles: warp 0 loads; a thread each of warps 1-3 and 25 issues updates, scores, "before" and
+// "inside"; warps 4-11, two groups that take the tiles in turn, make P and write the outputs
+// (one thread a row); warps 12-15 weigh V; warps 16-23 keep the state, 32 fp32 values of a
+// thread; warp 24 sums the logarithms.  So the chain from one chunk's state to the next (update,
+// sum, rounding) and the chain of the weighed V run beside each other and beside the outputs.
+//
+// Bound: what the SM's four schedulers issue and the steps from role to role, not HBM or the
+// tensor cores.  2 x 8192 tokens of 32 kv heads of 128 take 202 us: HBM alone would need 80
+// (95 on the 128 SMs that have a slice), the MMAs' shared memory reads 0.4 of it, and the
+// busiest scheduler issues in 0.6 of its cycles.  What that led to:
+//  - loops over 16 columns stay loops, and only the MMAs of 64 of a dimension are unrolled: the
+//    code of all roles has to fit the instruction cache (109 KB of it: 349 us; 72 KB: 202; the
+//    MMAs unrolled in full, 76 KB: 268)
+//  - the roles' warps are dealt to the schedulers by what they issue, and tiles of one head take
+//    the lower and the upper rows in turn, so that P falls to all four (202 us; always the lower
+//    rows 216; the sums of logarithms beside the scores 229)
+//  - waits sleep on the barrier instead of polling it; packed fp32 arithmetic
+//  - a deeper ring of K and V (5) at one buffer of weighed V: 248; two buffers, rings of 3 and
+//    4: the same
 // P's weights: within 16 tokens exponentials, from one run of 16 to a later one products of a
 // factor of the row's and one of the column's.
 //
@@ -40,13 +53,12 @@ namespace {
 constexpr int kC = kLinearChunk;
 constexpr int kSlice = 64;   // state columns of a CTA
 constexpr int kRows = 128;   // rows of a query tile, and of a state's MMA
-constexpr int kWarpQK = 1, kWarpKV = 2, kWarpQS = 3, kFirstOut = 4, kFirstWeigh = 12,
+constexpr int kWarpKV = 1, kWarpQK = 2, kWarpQS = 3, kFirstOut = 4, kFirstWeigh = 12,
               kFirstState = 16;
 constexpr int kMmaWarps = 4, kGroupWarps = 4, kWeighWarps = 4, kStateWarps = 8;
-constexpr int kWarpPV = kFirstState + kStateWarps;
-constexpr int kWarpScan = kWarpPV + 1;
-constexpr int kWarps = kWarpScan + 1, kThreads = 32 * kWarps;
-static_assert(kWarpPV % kMmaWarps == 0, "a barrier of drain[] each");
+// (a warp is on the SM's quarter of its number modulo 4: each has as much to issue)
+constexpr int kWarpScan = kFirstState + kStateWarps, kWarpPV = kWarpScan + 1;
+constexpr int kWarps = kWarpPV + 1, kThreads = 32 * kWarps;
 constexpr int kRing = 3;     // chunks of K and V in shared memory
 constexpr int kQueue = 4;
 constexpr int kTables = 8;   // chunks whose sums of logarithms are kept
@@ -61,6 +73,17 @@ struct alignas(16) Table {
     float sum[kC], tail[kC], weight[kC];
     float all, pad[3];
 };
+
+// Pairs of fp32, in packed arithmetic.
+__device__ __forceinline__ uint64_t f2_twice(float v) { return f2_pack(v, v); }
+__device__ __forceinline__ uint64_t f2_words(uint32_t lo, uint32_t hi) {
+    return f2_pack(__uint_as_float(lo), __uint_as_float(hi));
+}
+__device__ __forceinline__ uint32_t f2_bf16x2(uint64_t v) {
+    float lo, hi;
+    f2_unpack(v, lo, hi);
+    return pack_bf16x2(lo, hi);
+}
 
 template <int D>
 struct Geom {
@@ -100,6 +123,7 @@ struct Bars {
     uint64_t drain[kMmaWarps];
 };
 static_assert(sizeof(Bars) <= 320, "barrier area");
+static_assert(kWarpKV < kMmaWarps && kWarpQK < kMmaWarps && kWarpQS < kMmaWarps, "drain[]");
 
 // One request, kv head and slice, and this rank's run of chunks.
 struct alignas(16) Item {
@@ -294,6 +318,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         // ============================ loads ============================
         uint32_t c = 0, t = 0;  // chunks and tiles loaded
+        // tiles of one head: every other one in the upper half of the rows, which are other warps'
+        const int upper = p.heads_per_tile == 1 ? kC * 128 : 0;
         bool ok = true;
         auto load_kv = [&](const Item &it, int i) {
             const int st = c % kRing;
@@ -347,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mbar_arrive_expect_tx(&bars->q_full[st],
                                                   G::kHalves * kC * p.heads_per_tile * 128);
                             for (int hf = 0; hf < G::kHalves; ++hf)
-                                tma_load_3d(sQ + st * G::kQBytes + hf * G::kQHalf, &tmq, hf * 64,
+                                tma_load_3d(sQ + st * G::kQBytes + hf * G::kQHalf + upper * st, &tmq, hf * 64,
                                             it.h * p.group + j * p.heads_per_tile, it.t0 + i * kC,
                                             &bars->q_full[st]);
                         }
@@ -401,9 +427,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t d = tmem + G::kColU + (u & 1) * kSlice;
             static_assert(G::kVBytes == kC * 128, "parts follow each other");
 #pragma unroll 1
-            for (int kk = 0; kk < kParts * (kC / 16); ++kk)
-                tc_mma(d, kd + kk % (kC / 16) * (2048 >> 4), vd + kk * (2048 >> 4), idesc_kv,
-                       kk > 0 ? 1u : 0u);
+            for (int part = 0; part < kParts; ++part)
+#pragma unroll
+                for (int kk = 0; kk < kC / 16; ++kk)
+                    tc_mma(d, kd + kk * (2048 >> 4),
+                           vd + part * (G::kVBytes >> 4) + kk * (2048 >> 4), idesc_kv,
+                           part + kk > 0 ? 1u : 0u);
             tc_commit(&bars->u_full[u & 1]);
             ++u;
         };
@@ -418,9 +447,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const uint64_t qd = q_desc + b * (G::kQBytes >> 4);
 #pragma unroll 1
-                for (int kk = 0; kk < D / 16; ++kk)
-                    tc_mma(d + b * d_next, qd + (kk >> 2) * (G::kQHalf >> 4) + (kk & 3) * 2,
-                           b_desc + (kk >> 2) * step64 + (kk & 3) * step, idesc, kk > 0 ? 1u : 0u);
+                for (int hf = 0; hf < G::kHalves; ++hf)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc_mma(d + b * d_next, qd + hf * (G::kQHalf >> 4) + kk * 2,
+                               b_desc + hf * step64 + kk * step, idesc, hf + kk > 0 ? 1u : 0u);
                 tc_commit(&after[b]);
                 tc_commit(&bars->q_empty[b]);
             }
@@ -433,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait(&bars->p_full[b], turn)) return;
                 tc_fence_after();
                 const uint64_t vd = v_desc + (c % kRing) * (G::kStageBytes >> 4);
-#pragma unroll 1
+#pragma unroll
                 for (int kk = 0; kk < kC / 16; ++kk)
                     tc_mma_ts(tmem + G::kColO + b * (2 * kSlice) + kSlice, tmem + b * kC + kk * 8,
                               vd + (kk * 2048 >> 4), idesc_v, kk > 0 ? 1u : 0u);
@@ -484,22 +515,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0 && (!ok || *abort_flag)) {
             // MMAs already issued finish before TMEM is released
-            tc_commit(&bars->drain[warp & (kMmaWarps - 1)]);
-            mbar_drain(&bars->drain[warp & (kMmaWarps - 1)], 0);
+            uint64_t *drain = &bars->drain[warp == kWarpPV ? 0 : warp];
+            tc_commit(drain);
+            mbar_drain(drain, 0);
         }
         __syncwarp();
     } else if (warp < kFirstWeigh) {
         // ============================ P and outputs ============================
-        const int wq = warp & 3, r = wq * 32 + lane;
+        const int wq = warp & 3;
         const uint32_t grp = (warp - kFirstOut) / kGroupWarps;  // takes tiles of this parity
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
         const uint32_t sa = t_lane + grp * kC, oa = t_lane + G::kColO + grp * (2 * kSlice);
-        const int tok = r / p.heads_per_tile, head = r - tok * p.heads_per_tile;
-        // the runs of 16 tokens that the warp's rows lie in; a tile of one head fills half of the
-        // rows, and the warps of the others have nothing to do
-        const int first_run = wq * 32 / p.heads_per_tile / 16;
-        const int last_run = (wq * 32 + 31) / p.heads_per_tile / 16;
-        const bool idle = first_run * 16 >= kC;
+        // a tile of one head fills half of the rows, the lower or the upper one; the warps of the
+        // others have nothing to do
+        const int row0 = p.heads_per_tile == 1 ? wq * 32 - static_cast<int>(grp) * kC : wq * 32;
+        const bool idle = row0 < 0 || row0 >= kC * p.heads_per_tile;
+        const int tok = (row0 + lane) / p.heads_per_tile;
+        const int head = row0 + lane - tok * p.heads_per_tile;
+        // the runs of 16 tokens that the warp's rows lie in
+        const int first_run = row0 / p.heads_per_tile / 16;
+        const int last_run = (row0 + 31) / p.heads_per_tile / 16;
         uint32_t t = 0, u = 0;  // tiles, updates up to this item
         bool ok = true;
         for (int k = 0;; ++k) {
@@ -534,32 +569,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tmem_ld16(sa + run * 16, v);
                                 if (run < first_run) {
                                     // e^(G_i - G_j) by way of the run's last token
-                                    const float row = fast_exp2(gi - tab.sum[run * 16 + 15]);
+                                    const uint64_t row = f2_twice(fast_exp2(gi - tab.sum[run * 16 + 15]));
                                     tmem_wait_ld();
 #pragma unroll
                                     for (int x = 0; x < 16; x += 4) {
                                         const float4 f =
                                             *reinterpret_cast<const float4 *>(tab.tail + run * 16 + x);
-                                        pk[x / 2] = pack_bf16x2(__uint_as_float(v[x]) * row * f.x,
-                                                                __uint_as_float(v[x + 1]) * row * f.y);
-                                        pk[x / 2 + 1] =
-                                            pack_bf16x2(__uint_as_float(v[x + 2]) * row * f.z,
-                                                        __uint_as_float(v[x + 3]) * row * f.w);
+                                        auto w = [&](int e, float f0, float f1) {
+                                            return f2_bf16x2(f2_mul(f2_mul(f2_words(v[x + e], v[x + e + 1]), row),
+                                                                    f2_pack(f0, f1)));
+                                        };
+                                        pk[x / 2] = w(0, f.x, f.y);
+                                        pk[x / 2 + 1] = w(2, f.z, f.w);
                                     }
                                 } else {
                                     const int lim = tok - run * 16;  // its last visible column
+                                    const uint64_t minus = f2_twice(-1.f);
                                     tmem_wait_ld();
 #pragma unroll
                                     for (int x = 0; x < 16; x += 4) {
                                         const float4 g =
                                             *reinterpret_cast<const float4 *>(tab.sum + run * 16 + x);
-                                        auto w = [&](int e, float gj) {
-                                            const float y =
-                                                __uint_as_float(v[x + e]) * fast_exp2(gi - gj);
-                                            return x + e <= lim ? y : 0.f;
+                                        auto w = [&](int e, float g0, float g1) {
+                                            float a, b;
+                                            f2_unpack(f2_fma(f2_pack(g0, g1), minus, f2_twice(gi)), a, b);
+                                            f2_unpack(f2_mul(f2_words(v[x + e], v[x + e + 1]),
+                                                             f2_pack(fast_exp2(a), fast_exp2(b))), a, b);
+                                            return pack_bf16x2(x + e <= lim ? a : 0.f,
+                                                               x + e + 1 <= lim ? b : 0.f);
                                         };
-                                        pk[x / 2] = pack_bf16x2(w(0, g.x), w(1, g.y));
-                                        pk[x / 2 + 1] = pack_bf16x2(w(2, g.z), w(3, g.w));
+                                        pk[x / 2] = w(0, g.x, g.y);
+                                        pk[x / 2 + 1] = w(2, g.z, g.w);
                                     }
                                 }
                             }
@@ -576,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     if (!idle) {
                         tc_fence_after();
-                        const float before = fast_exp2(gi) * p.scale;
+                        const uint64_t before = f2_twice(fast_exp2(gi) * p.scale), scale = f2_twice(p.scale);
                         const int token = i * kC + tok, hq = j * p.heads_per_tile + head;
                         const bool valid = token < it.n && hq < p.group;
                         uint4 *dst = reinterpret_cast<uint4 *>(
@@ -590,10 +630,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tmem_ld16(oa + kSlice + part * 16, b);
                             tmem_wait_ld();
                             auto sum = [&](int x) {
-                                return pack_bf16x2(
-                                    fmaf(before, __uint_as_float(a[x]), p.scale * __uint_as_float(b[x])),
-                                    fmaf(before, __uint_as_float(a[x + 1]),
-                                         p.scale * __uint_as_float(b[x + 1])));
+                                return f2_bf16x2(f2_fma(before, f2_words(a[x], a[x + 1]),
+                                                        f2_mul(scale, f2_words(b[x], b[x + 1]))));
                             };
                             if (valid) {
                                 dst[part * 2] = make_uint4(sum(0), sum(2), sum(4), sum(6));
@@ -638,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int x = 0; x < kC / (4 * kWeighWarps); ++x) {
                         const int row = vw * (kC / kWeighWarps) + x * 4 + lane / 8;
                         const uint32_t off = sw128_offset(row, lane % 8);
-                        const uint64_t wt = f2_pack(weight[row], weight[row]);
+                        const uint64_t wt = f2_twice(weight[row]);
                         uint4 in = *reinterpret_cast<const uint4 *>(v + off);
                         // rows behind the request are another's, or padding: whatever stands
                         // there does not reach a sum
@@ -650,22 +688,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 *reinterpret_cast<uint4 *>(k_tile + hf * G::kKHalf + off) = in;
                         }
                         uint4 part[kParts];
-                        const uint64_t minus = f2_pack(-1.f, -1.f);
+                        const uint64_t minus = f2_twice(-1.f);
                         auto two = [](uint32_t pair) {
                             return f2_pack(__uint_as_float(pair << 16),
                                            __uint_as_float(pair & 0xFFFF0000u));
                         };
-                        auto round = [](uint64_t v2) {
-                            float lo, hi;
-                            f2_unpack(v2, lo, hi);
-                            return pack_bf16x2(lo, hi);
-                        };
                         auto split = [&](uint32_t pair, uint32_t &p0, uint32_t &p1, uint32_t &p2) {
                             uint64_t y = f2_mul(two(pair), wt);
-                            p0 = round(y);
+                            p0 = f2_bf16x2(y);
                             y = f2_fma(two(p0), minus, y);
-                            p1 = round(y);
-                            p2 = round(f2_fma(two(p1), minus, y));
+                            p1 = f2_bf16x2(y);
+                            p2 = f2_bf16x2(f2_fma(two(p1), minus, y));
                         };
                         split(in.x, part[0].x, part[1].x, part[2].x);
                         split(in.y, part[0].y, part[1].y, part[2].y);
@@ -756,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = wq * 32 + lane;       // row of the update's MMA, 32 of its columns
         const bool real = r < D;  // (head_dim 64: the MMA's other rows go along unread)
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-        float s[32];
+        uint64_t s[16];  // pairs of columns
         uint32_t u = 0, w = 0;  // updates, states written
         bool ok = true;
         float total = 0.f;  // log2 decay of the chunks gone through
@@ -768,9 +801,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t *dst = sS + (w & 1) * G::kSBytes;
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-                *reinterpret_cast<uint4 *>(dst + sw128_offset(r, half * 4 + x)) = make_uint4(
-                    pack_bf16x2(s[8 * x], s[8 * x + 1]), pack_bf16x2(s[8 * x + 2], s[8 * x + 3]),
-                    pack_bf16x2(s[8 * x + 4], s[8 * x + 5]), pack_bf16x2(s[8 * x + 6], s[8 * x + 7]));
+                *reinterpret_cast<uint4 *>(dst + sw128_offset(r, half * 4 + x)) =
+                    make_uint4(f2_bf16x2(s[4 * x]), f2_bf16x2(s[4 * x + 1]),
+                               f2_bf16x2(s[4 * x + 2]), f2_bf16x2(s[4 * x + 3]));
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->s_full[w & 1]);
@@ -782,7 +815,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                  warp_mbar_wait_small(&bars->vt_full[u % kVtBars], (u / kVtBars) & 1, abort_flag);
             if (!ok) return;
             tc_fence_after();
-            const float all = tables[u % kTables].all, keep = exp2f(all);
+            const float all = tables[u % kTables].all;
+            const uint64_t keep = f2_twice(exp2f(all));
             uint32_t up[32];
             tmem_ld32(t_lane + G::kColU + (u & 1) * kSlice + half * 32, up);
             tmem_wait_ld();
@@ -792,7 +826,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++u;
             total += all;
 #pragma unroll
-            for (int x = 0; x < 32; ++x) s[x] = fmaf(keep, s[x], __uint_as_float(up[x]));
+            for (int x = 0; x < 16; ++x)
+                s[x] = f2_fma(keep, s[x], f2_words(up[2 * x], up[2 * x + 1]));
         };
         for (int k = 0;; ++k) {
             const Item it = queue_item(ctl, warp, k);
@@ -812,20 +847,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int x = 0; x < 8; ++x) {
                     const float4 v = outputs && it.in >= 0 && real ? src[x]
                                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
-                    s[4 * x] = v.x;
-                    s[4 * x + 1] = v.y;
-                    s[4 * x + 2] = v.z;
-                    s[4 * x + 3] = v.w;
+                    s[2 * x] = f2_pack(v.x, v.y);
+                    s[2 * x + 1] = f2_pack(v.z, v.w);
                 }
                 if (outputs && size > 1) {
                     if (it.c_begin < it.c_end)
 #pragma unroll 1
                         for (int other = 0; other < rank; ++other) {
-                            const float keep = exp2f(ld_cluster_f1(&ctl->decay, other));
+                            const uint64_t keep = f2_twice(exp2f(ld_cluster_f1(&ctl->decay, other)));
                             const uint32_t theirs = cluster_addr(exchange, other);
 #pragma unroll
-                            for (int x = 0; x < 32; ++x)
-                                s[x] = fmaf(keep, s[x], ld_cluster_at(theirs + x * kRows * 4));
+                            for (int x = 0; x < 16; ++x)
+                                s[x] = f2_fma(keep, s[x],
+                                              f2_pack(ld_cluster_at(theirs + 2 * x * kRows * 4),
+                                                      ld_cluster_at(theirs + (2 * x + 1) * kRows * 4)));
                         }
                     cluster_sync();
                 }
@@ -845,7 +880,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                           abort_flag);
                             }
 #pragma unroll
-                        for (int x = 0; x < 32; ++x) exchange[x * kRows] = s[x];
+                        for (int x = 0; x < 16; ++x)
+                            f2_unpack(s[x], exchange[2 * x * kRows], exchange[(2 * x + 1) * kRows]);
                         if (sw == 0 && lane == 0) ctl->decay = total;
                     }
                     cluster_sync();
@@ -856,8 +892,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && real && it.to >= 0) {
                 float4 *dst = reinterpret_cast<float4 *>(p.state + it.to * state_size + place);
 #pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    dst[x] = make_float4(s[4 * x], s[4 * x + 1], s[4 * x + 2], s[4 * x + 3]);
+                for (int x = 0; x < 8; ++x) {
+                    float4 v;
+                    f2_unpack(s[2 * x], v.x, v.y);
+                    f2_unpack(s[2 * x + 1], v.z, v.w);
+                    dst[x] = v;
+                }
             }
         }
     }
