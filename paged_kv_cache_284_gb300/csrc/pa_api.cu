@@ -1412,9 +1412,7 @@ int pa_linear_attention(const void *q, int64_t q_stride, const void *k, int64_t 
     p.num_slots = desc->num_slots;
     p.scale = desc->scale;
     p.status = dev->status;
-    // a step of few tokens a request is taken to have no prompt: the recurrent form has them all
-    const bool prompts = num_tokens > kLinearStepRows &&
-                         num_tokens > kLinearStepMeanRows * static_cast<int64_t>(num_seqs);
+    const bool prompts = num_tokens > kLinearStepRows;
     p.max_rows = prompts ? kLinearStepRows : 0x7fffffff;
     p.heads_per_tile = std::min(2, p.group);
     p.test_stall = g_test_stall.load(std::memory_order_relaxed) == PA_TEST_STALL_LINEAR ? 1 : 0;

@@ -363,10 +363,11 @@ struct LinearParams {
     int heads_per_tile;  // prompt kernel: query heads of a tile (1 or 2)
     int test_stall;      // test hook: CTA 0's loads stop after one chunk
 };
-// Requests of up to this many tokens take the recurrent form.
-constexpr int kLinearStepRows = 16;
-// ... and all requests of a step of at most this many tokens on average.
-constexpr int kLinearStepMeanRows = 6;
+// Requests of up to this many tokens take the recurrent form, whose time grows with a request's
+// tokens; the chunks' is that of 64 from the first on.  head_dim 128, 32 / 8 heads, recurrent and
+// in chunks: one request of 8 tokens 10.7 and 10.5 us, of 16 18.9 and 10.7; 64 requests of 8
+// 36 and 47 us, of 10 46 and 47, of 16 68 and 48; 128 of 8 in head_dim 64 15 and 13.
+constexpr int kLinearStepRows = 8;
 // Tokens of a chunk of the prompt kernel, and rows (tokens x heads) of its query tiles.
 constexpr int kLinearChunk = 64;
 

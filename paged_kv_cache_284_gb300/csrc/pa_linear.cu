@@ -206,8 +206,8 @@ __global__ void __launch_bounds__(kThreads) linear_step_kernel(const LinearParam
     // Beside the prompt kernel, which has waited for whatever wrote the inputs, there is nothing
     // to wait for: its rows and slots are others.  This grid still ends after that one, so that
     // what follows comes after both: its last block waits (waiting blocks would hold the SMs
-    // that the prompts leave free: 8 x 512 prompt tokens, 192 single ones and 32 x 5 take 89 us,
-    // 93 with a wait in each).
+    // that the prompts leave free: 8 x 512 prompt tokens, 192 single ones and 32 x 5 then take
+    // 4 us more).
     if (!p.overlap) pdl_wait();
     pdl_trigger();
     step_job<D, COLS>(p);

@@ -931,7 +931,15 @@ int launch(const LinearParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
     while (size < kDirectMaxCluster && 2 * size * 2 * kC <= p.num_tokens &&
            2 * size * items <= (size < 4 ? sms * 18 / 19 : sms * 15 / 19))
         size *= 2;
-    const int clusters = static_cast<int>(std::min<int64_t>(items, sms / size));
+    // Which requests are long is known on the GPU only, so the two forms' SMs are shared out by
+    // what T tokens and B states would take: reading and writing a state takes an SM about as
+    // long as 24 tokens of a prompt (head_dim 128, four heads a group: 28 us and 1.1 us for 8 kv
+    // heads).  8 x 512 tokens among 224 requests of 1 and 5 take 83.5 us, 89 with a prompt CTA on
+    // every SM; 256 single tokens, without any prompt, 47.6 and 60.
+    constexpr int64_t kStateTokens = 24;
+    const int share = static_cast<int>(sms * static_cast<int64_t>(p.num_tokens) /
+                                       (p.num_tokens + kStateTokens * p.num_seqs));
+    const int clusters = static_cast<int>(std::min<int64_t>(items, std::max(1, share / size)));
     PdlLaunch l(clusters * size, kThreads, Geom<D>::kSmemBytes, s);
     if (size > 1) l.set_cluster(size);
     return launch_kernel(l, linear_prompt_kernel<D>, p, tq, tk, tv, size) == cudaSuccess
