@@ -19,8 +19,8 @@
 //
 // Bound: what the SM's four schedulers issue and the steps from role to role, not HBM or the
 // tensor cores.  2 x 8192 tokens of 32 kv heads of 128 take 202 us: HBM alone would need 80
-// (95 on the 128 SMs that have a slice), the MMAs' shared memory reads 0.4 of it, and the
-// busiest scheduler issues in 0.6 of its cycles.  What that led to:
+// (95 on the 128 SMs that have a slice); on those the MMAs keep their operand reads busy 0.58 of
+// the time, the tensor pipe 0.29, and the busiest scheduler issues in 0.69 of its cycles.  What that led to:
 //  - loops over 16 columns stay loops, and only the MMAs of 64 of a dimension are unrolled: the
 //    code of all roles has to fit the instruction cache (109 KB of it: 349 us; 72 KB: 202; the
 //    MMAs unrolled in full, 76 KB: 268)
