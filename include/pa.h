@@ -402,9 +402,10 @@ int pa_cross_attention(const void *q, const pa_kv_desc *kv, const int32_t *block
  *                 PA_DEV_BAD_SLOT
  *   out           bf16 [num_tokens][num_q_heads][head_dim], 16-B aligned; rows that belong to
  *                 no request are left untouched; may not overlap an input
- * States and all sums are fp32.  head_dim 64 or 128; num_q_heads a multiple of num_kv_heads,
- * at most 128 heads to a group.  A decreasing query start, or one past num_tokens, skips the
- * request and flags PA_DEV_BAD_METADATA.
+ * States and all sums are fp32.  An infinity or a NaN in a request's q, k or v reaches its own
+ * state and outputs only, those up to 63 tokens earlier among them.  head_dim 64 or 128;
+ * num_q_heads a multiple of num_kv_heads, at most 128 heads to a group.  A decreasing query
+ * start, or one past num_tokens, skips the request and flags PA_DEV_BAD_METADATA.
  */
 typedef struct pa_linear_desc {
     float *state;
@@ -419,8 +420,8 @@ int pa_linear_attention(const void *q, int64_t q_stride, const void *k, int64_t 
                         const pa_linear_desc *desc, const int32_t *state_in,
                         const int32_t *state_out, void *out, void *workspace,
                         size_t workspace_bytes, void *stream);
-/* Workspace bytes of pa_linear_attention (256-byte aligned, untouched while the call's kernels
- * run).  Returns 0 for invalid sizes. */
+/* Workspace bytes of pa_linear_attention (256-byte aligned), as for the other attention calls; the
+ * kernels of this version keep nothing in it, so calls may share one.  0 for invalid sizes. */
 size_t pa_linear_workspace_size(int32_t num_seqs, int32_t num_tokens, int32_t num_q_heads,
                                 int32_t num_kv_heads, int32_t head_dim);
 

@@ -213,6 +213,38 @@ def test_captured_loop_runs_by_itself():
     assert_status_clean()
 
 
+def test_captured_loop_of_large_steps():
+    """As above with prompts of thousands of tokens: in place, one replay behind the other."""
+    rng = np.random.default_rng(5)
+    b = Batch([(900, 0), (1, 30), (0, 0), (1, 15), (700, 100)], 32, 200, spare=600, pad=1500)
+    t = b.on_gpu()
+    plan = np.where(rng.random((12, 5)) < 0.25, -1, rng.choice([0, 1, 5, 333, 600], (12, 5)))
+    plan = torch.from_numpy(plan.astype(np.int32)).to(DEV)
+    graph = torch.cuda.CUDAGraph()
+    saved = {x: t[x].clone() for x in ("cached", "table", "ring", "state_in")}
+    with torch.cuda.graph(graph):
+        pk.pa_build_step(t["q"], t["cached"], t["table"], t["ring"], t["state_in"], b.num_blocks,
+                         b.bs, t["qsl"], t["ctx"], t["cached"], t["slots"], t["positions"])
+    for x in saved:
+        t[x].copy_(saved[x])
+    for step in plan:   # (nothing waits for the one before)
+        t["q"].copy_(step)
+        graph.replay()
+    for step in plan.cpu().numpy():
+        b.q = step
+        want = b.expected()
+        assert not want["bad"] and want["state"][2] == 0
+        b.cached, b.table, b.ring = want["seq"], want["table"], want["ring"]
+        b.head, b.count = int(want["state"][0]), int(want["state"][1])
+    t["seq"], t["state"] = t["cached"], t["state_in"]
+    same(t, want)
+    assert_status_clean()
+
+
+def test_more_tokens_than_one_round():
+    check(Batch([(7, 100), (170000, 3), (1, 8), (-1, 5000)], 256, 700, pad=41))
+
+
 def test_other_stream_and_slices():
     b = Batch(random_rows(40, 8), 16, 30)
     t, want = b.on_gpu(), b.expected()

@@ -219,6 +219,22 @@ def test_other_stream_and_repeat():
     assert_status_clean()
 
 
+@pytest.mark.parametrize("requests", [[(300, 1), (17, 2)], [(300, 70), (40, 1)]])
+def test_pool_past_32_bits(requests):
+    """Blocks more than 2^31 elements into the pool."""
+    s = Step(requests, 16, 8, 128, 16, seed=4)
+    t = s.to_dev()
+    at = 131100   # 16384 elements a block
+    for x in "kv":
+        pool = torch.empty((at + s.num_blocks, 8, 16, 128), dtype=torch.bfloat16, device=DEV)
+        pool[at:] = t[x]
+        t[x] = pool
+    t["table"][t["table"] >= 0] += at
+    s.call(t)
+    s.check(t)
+    assert_status_clean()
+
+
 def test_refusals():
     s = Step([(50, 1), (60, 2)], 4, 2, 64, 16)
     t = s.to_dev()

@@ -245,6 +245,79 @@ def test_other_stream_and_repeat():
     assert_status_clean()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_other_rows_stay_other_rows(bad, d):
+    """What stands in the next request's rows, or behind the last, reaches no sum."""
+    lens = [70, 33, 1, 100, 5, 64, 9]
+    s = Step(lens, 6, 2, d, seed=8, pad=50)
+    t, u = s.to_dev(), s.to_dev()
+    s.call(t)
+    starts = s.qsl.tolist()
+    spoilt = (1, 4)
+    for x in "qkv":
+        for b in spoilt:
+            u[x][starts[b]:starts[b + 1]] = bad
+        u[x][s.total:] = bad
+    u["g"][s.total:] = bad
+    s.call(u)
+    torch.cuda.synchronize()
+    for b in set(range(len(lens))) - set(spoilt):
+        rows = slice(starts[b], starts[b + 1])
+        assert torch.equal(t["out"][rows], u["out"][rows]), b
+        slot = s.state_out[b]
+        assert torch.equal(t["state"][slot], u["state"][slot]), b
+    assert torch.all(u["out"][s.total:] == 7)
+    assert_status_clean()
+
+
+def test_steps_behind_each_other_and_beside():
+    """Steps of prompts and short rows in place, one behind the other without a wait, and the
+    same on two streams at once, give what they give one by one."""
+    lens = [300, 1, 1, 5, 90, 1, 8, 9] + [1] * 40
+    s = Step(lens, 4, 2, 128, seed=9, in_place=True)
+    one = s.to_dev()
+    for _ in range(4):
+        s.call(one)
+        torch.cuda.synchronize()
+    s.g = s.g.clone()
+    steps = [s.to_dev() for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for t, side in zip(steps, streams):
+            s.call(t, stream=side)
+    torch.cuda.synchronize()
+    for t in steps:
+        assert torch.equal(t["out"], one["out"]) and torch.equal(t["state"], one["state"])
+    assert_status_clean()
+
+
+@pytest.mark.parametrize("n", [5, 70])
+def test_offsets_past_32_bits(n):
+    """A pool of more than 2^32 bytes of states, and token rows 2^29 elements apart."""
+    s = Step([n, 1], 4, 2, 64, seed=n)
+    t = s.to_dev()
+    pool = torch.empty((264000, 2, 64, 64), device=DEV)   # 8192 elements a slot, 8.6 GB
+    slots = [263999, 262145, 131073, 5]
+    t["state_in"].copy_(torch.tensor(slots[:2]))
+    t["state_out"].copy_(torch.tensor(slots[2:]))
+    pool[slots[:2]] = t["state"][s.state_in.long().to(DEV)]
+    rows = torch.empty(((s.total - 1) << 29) + 1024, dtype=torch.bfloat16, device=DEV) \
+        if n == 5 else None
+    if rows is not None:
+        far = rows.as_strided((s.total, 4, 64), (1 << 29, 64, 1))
+        far.copy_(t["q"])
+        t["q"] = far
+    small = t["state"]
+    t["state"] = pool
+    s.call(t)
+    small[s.state_out.long().to(DEV)] = pool[slots[2:]]
+    t["state"] = small
+    s.check(t)
+    assert_status_clean()
+
+
 def test_refusals():
     s = Step([3, 2], 4, 2, 64)
     t = s.to_dev()
