@@ -18,18 +18,22 @@
 // sum, rounding) and the chain of the weighed V run beside each other and beside the outputs.
 //
 // Bound: what the SM's four schedulers issue and the steps from role to role, not HBM or the
-// tensor cores.  2 x 8192 tokens of 32 kv heads of 128 take 202 us: HBM alone would need 80
+// tensor cores.  2 x 8192 tokens of 32 kv heads of 128 take 193 us: HBM alone would need 80
 // (95 on the 128 SMs that have a slice); on those the MMAs keep their operand reads busy 0.58 of
-// the time, the tensor pipe 0.29, and the busiest scheduler issues in 0.69 of its cycles.  What that led to:
+// the time, the tensor pipe 0.29, and the busiest scheduler issues in 0.69 of its cycles.  An MMA
+// of 128 x 64 x 16 takes the pipe 47 cycles from any number of threads, 32 of them 1500 of a
+// chunk's 3500; but every step of a role is instructions that the others' code pushes out of the
+// instruction cache, about six cycles each.  What that led to:
 //  - loops over 16 columns stay loops, and only the MMAs of 64 of a dimension are unrolled: the
-//    code of all roles has to fit the instruction cache (109 KB of it: 349 us; 72 KB: 202; the
-//    MMAs unrolled in full, 76 KB: 268)
+//    code of all roles has to fit the instruction cache (109 KB of it: 349 us; 72 KB: 202), and
+//    a burst of one thread's MMAs holds up the others' (all unrolled: 240 to 268)
+//  - without a cluster a kernel of its own, that has no exchange (63 KB: 193)
 //  - the roles' warps are dealt to the schedulers by what they issue, and tiles of one head take
-//    the lower and the upper rows in turn, so that P falls to all four (202 us; always the lower
-//    rows 216; the sums of logarithms beside the scores 229)
+//    the lower and the upper rows in turn, so that P falls to all four (202 us then; always the
+//    lower rows 216; the sums of logarithms beside the scores 229)
 //  - waits sleep on the barrier instead of polling it; packed fp32 arithmetic
-//  - a deeper ring of K and V (5) at one buffer of weighed V: 248; two buffers, rings of 3 and
-//    4: the same
+//  - left out: a deeper ring of K and V (5) at one buffer of weighed V 248, rings of 3 and 4 at
+//    two the same; four query tiles ahead 195; two threads for the updates and for Q S 217
 // P's weights: within 16 tokens exponentials, from one run of 16 to a later one products of a
 // factor of the row's and one of the column's.
 //
@@ -239,11 +243,11 @@ __device__ __forceinline__ Item queue_item(Ctl *ctl, int warp, int k) {
 
 }  // namespace
 
-template <int D>
+template <int D, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_prompt_kernel(const LinearParams p, const __grid_constant__ CUtensorMap tmq,
                          const __grid_constant__ CUtensorMap tmk,
-                         const __grid_constant__ CUtensorMap tmv, int size) {
+                         const __grid_constant__ CUtensorMap tmv, int ranks) {
     using G = Geom<D>;
     extern __shared__ __align__(1024) uint8_t smem[];
     Bars *bars = reinterpret_cast<Bars *>(smem + G::kOffBar);
@@ -253,7 +257,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = &ctl->abort;
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31, tid = threadIdx.x;
-    const int rank = static_cast<int>(blockIdx.x) % size;
+    const int size = CLUSTER ? ranks : 1;
+    const int rank = CLUSTER ? static_cast<int>(blockIdx.x) % size : 0;
     const int tiles = (p.group + p.heads_per_tile - 1) / p.heads_per_tile;
 
     if (tid == 0) {
@@ -911,16 +916,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 namespace {
 
-template <int D>
+template <int D, bool CLUSTER>
 int launch(const LinearParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
-           const CUtensorMap &tv, int sms, cudaStream_t s) {
+           const CUtensorMap &tv, int clusters, int size, cudaStream_t s) {
     static PerDeviceOnce once;
     if (once_per_device(once, [] {
-            return cudaFuncSetAttribute(linear_prompt_kernel<D>,
+            return cudaFuncSetAttribute(linear_prompt_kernel<D, CLUSTER>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         Geom<D>::kSmemBytes);
         }) != PA_OK)
         return PA_ERR_CUDA;
+    PdlLaunch l(clusters * size, kThreads, Geom<D>::kSmemBytes, s);
+    if (CLUSTER) l.set_cluster(size);
+    return launch_kernel(l, linear_prompt_kernel<D, CLUSTER>, p, tq, tk, tv, size) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+template <int D>
+int launch(const LinearParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
+           const CUtensorMap &tv, int sms, cudaStream_t s) {
     // the most requests that can be long, and their items
     const int64_t longs = std::min<int64_t>(p.num_seqs, p.num_tokens / (p.max_rows + 1));
     const int64_t items = longs * p.num_kv_heads * (D / kSlice);
@@ -940,11 +955,8 @@ int launch(const LinearParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
     const int share = static_cast<int>(sms * static_cast<int64_t>(p.num_tokens) /
                                        (p.num_tokens + kStateTokens * p.num_seqs));
     const int clusters = static_cast<int>(std::min<int64_t>(items, std::max(1, share / size)));
-    PdlLaunch l(clusters * size, kThreads, Geom<D>::kSmemBytes, s);
-    if (size > 1) l.set_cluster(size);
-    return launch_kernel(l, linear_prompt_kernel<D>, p, tq, tk, tv, size) == cudaSuccess
-               ? PA_OK
-               : PA_ERR_CUDA;
+    return size > 1 ? launch<D, true>(p, tq, tk, tv, clusters, size, s)
+                    : launch<D, false>(p, tq, tk, tv, clusters, 1, s);
 }
 
 }  // namespace
