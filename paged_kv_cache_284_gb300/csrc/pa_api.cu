@@ -119,16 +119,16 @@ int make_q_map(CUtensorMap *m, const void *q, int tokens, int heads, int head_di
 }
 
 // 3-D view of bf16 rows [tokens][heads][head_dim], tokens `stride` elements apart; a box is 64
-// dims x box_heads heads x kLinearChunk tokens.
+// dims x box_heads heads x box_tokens tokens.
 int make_rows_map(CUtensorMap *m, const void *base, int tokens, int heads, int head_dim,
-                  int64_t stride, int box_heads) {
+                  int64_t stride, int box_heads, int box_tokens) {
     auto fn = encode_fn();
     if (!fn) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(heads),
                           static_cast<cuuint64_t>(tokens)};
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2,
                              static_cast<cuuint64_t>(stride) * 2};
-    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), kLinearChunk};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_tokens)};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
                     box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -1414,15 +1414,16 @@ int pa_linear_attention(const void *q, int64_t q_stride, const void *k, int64_t 
     p.status = dev->status;
     const bool prompts = num_tokens > kLinearStepRows;
     p.max_rows = prompts ? kLinearStepRows : 0x7fffffff;
-    p.heads_per_tile = std::min(2, p.group);
+    p.chunk = p.group == 1 ? kLinearTileRows : kLinearTileRows / 2;
     p.test_stall = g_test_stall.load(std::memory_order_relaxed) == PA_TEST_STALL_LINEAR ? 1 : 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (prompts) {
         // a request may be long: the prompt kernel first, the recurrent form beside it
         CUtensorMap tq, tk, tv;
-        if ((rc = make_rows_map(&tq, q, num_tokens, hq, d, q_stride, p.heads_per_tile)) != PA_OK ||
-            (rc = make_rows_map(&tk, k, num_tokens, hkv, d, k_stride, 1)) != PA_OK ||
-            (rc = make_rows_map(&tv, v, num_tokens, hkv, d, v_stride, 1)) != PA_OK)
+        if ((rc = make_rows_map(&tq, q, num_tokens, hq, d, q_stride, kLinearTileRows / p.chunk,
+                                p.chunk)) != PA_OK ||
+            (rc = make_rows_map(&tk, k, num_tokens, hkv, d, k_stride, 1, p.chunk)) != PA_OK ||
+            (rc = make_rows_map(&tv, v, num_tokens, hkv, d, v_stride, 1, p.chunk)) != PA_OK)
             return rc;
         rc = launch_linear_prompt(p, tq, tk, tv, d, dev->sms, s);
         if (rc != PA_OK) return fail(rc, "linear prompt launch failed: %s",

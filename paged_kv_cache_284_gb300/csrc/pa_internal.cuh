@@ -360,7 +360,7 @@ struct LinearParams {
     // requests of more than max_rows tokens are the prompt kernel's; overlap: launched beside
     // it, which has waited for whatever wrote the inputs
     int max_rows, overlap;
-    int heads_per_tile;  // prompt kernel: query heads of a tile (1 or 2)
+    int chunk;           // prompt kernel: tokens of a chunk, 64 or 128
     int test_stall;      // test hook: CTA 0's loads stop after one chunk
 };
 // Requests of up to this many tokens take the recurrent form, whose time grows with a request's
@@ -368,8 +368,9 @@ struct LinearParams {
 // in chunks: one request of 8 tokens 10.7 and 10.5 us, of 16 18.9 and 10.7; 64 requests of 8
 // 36 and 47 us, of 10 46 and 47, of 16 68 and 48; 128 of 8 in head_dim 64 15 and 13.
 constexpr int kLinearStepRows = 8;
-// Tokens of a chunk of the prompt kernel, and rows (tokens x heads) of its query tiles.
-constexpr int kLinearChunk = 64;
+// Rows (tokens x heads) of the prompt kernel's query tiles: chunks of 64 tokens and two heads of
+// a group, or of 128 tokens where a group is one head.
+constexpr int kLinearTileRows = 128;
 
 // The cache arrays of one pa_copy_blocks launch: K and V of up to
 // kCopyLayers layers.

@@ -1,4 +1,4 @@
-// pa_linear_prompt.cu -- linear attention with a decay per head: prompts, in chunks of 64
+// pa_linear_prompt.cu -- linear attention with a decay per head: prompts, in chunks of 64 or 128
 // tokens on tcgen05.
 //
 // With G_i the sum of the logarithms of a chunk's decays up to and with token i, S the state
@@ -7,7 +7,7 @@
 //   S'   = e^(G_L) S + sum_j k_j (e^(G_L - G_j) v_j)^T
 // Every exponent is at most 0.  Columns of S and of o do not depend on each other, so a CTA
 // has 64 of them (a slice), for one request and kv head, and walks along the request:
-//   scores  Q K^T            M = 64 tokens x 2 query heads of the group (1: half the rows idle)
+//   scores  Q K^T            M = 64 tokens x 2 query heads of the group, or 128 x 1
 //   inside  P V              P = the scores times e^(G_i - G_j), masked, over them in TMEM
 //   before  Q S              S in bf16, in shared memory
 //   update  K^T (e^(G_L - G) V), M = the state's rows
@@ -17,23 +17,25 @@
 // thread; warp 24 sums the logarithms.  So the chain from one chunk's state to the next (update,
 // sum, rounding) and the chain of the weighed V run beside each other and beside the outputs.
 //
-// Bound: what the SM's four schedulers issue and the steps from role to role, not HBM or the
-// tensor cores.  2 x 8192 tokens of 32 kv heads of 128 take 193 us: HBM alone would need 80
-// (95 on the 128 SMs that have a slice); on those the MMAs keep their operand reads busy 0.58 of
-// the time, the tensor pipe 0.29, and the busiest scheduler issues in 0.69 of its cycles.  An MMA
-// of 128 x 64 x 16 takes the pipe 47 cycles from any number of threads, 32 of them 1500 of a
-// chunk's 3500; but every step of a role is instructions that the others' code pushes out of the
-// instruction cache, about six cycles each.  What that led to:
+// Bound: the path between shared memory, the tensor cores' operands and L1 (128 bytes a cycle),
+// and what the schedulers issue; not HBM or the tensor pipe.  2 x 8192 tokens of 32 kv heads of
+// 128 take 179 us, where HBM alone would need 80 (95 on the 128 SMs that have a slice).  Of the
+// 5500 cycles of 128 tokens, that path carries the MMAs' operands for 2200, copies, weighed V and
+// states for 1300, and the stores, a sector from each row, for 500.  Leaving a role's work out
+// saves about its share, whichever it is: no stores 20 us, no weights and a third of the updates'
+// MMAs 30, no states 20.  What that led to:
+//  - where a group is one head, chunks of 128 tokens, whose tiles fill the MMA's 128 rows: 193 us
+//    with chunks of 64 and half the rows idle (216 before the idle rows took turns)
+//  - outputs by 32 bytes of a lane: 190 us by 16
+//  - packed fp32 arithmetic, waits that sleep on the barrier, roles dealt to the schedulers by
+//    what they issue
 //  - loops over 16 columns stay loops, and only the MMAs of 64 of a dimension are unrolled: the
-//    code of all roles has to fit the instruction cache (109 KB of it: 349 us; 72 KB: 202), and
-//    a burst of one thread's MMAs holds up the others' (all unrolled: 240 to 268)
-//  - without a cluster a kernel of its own, that has no exchange (63 KB: 193)
-//  - the roles' warps are dealt to the schedulers by what they issue, and tiles of one head take
-//    the lower and the upper rows in turn, so that P falls to all four (202 us then; always the
-//    lower rows 216; the sums of logarithms beside the scores 229)
-//  - waits sleep on the barrier instead of polling it; packed fp32 arithmetic
-//  - left out: a deeper ring of K and V (5) at one buffer of weighed V 248, rings of 3 and 4 at
-//    two the same; four query tiles ahead 195; two threads for the updates and for Q S 217
+//    code of all roles has to fit the instruction cache (109 KB of it: 349 us when 72 KB took
+//    215), and a burst of one thread's MMAs holds up the others' (all unrolled: 20 % more).  An MMA
+//    of 128 x 64 x 16 takes the pipe 47 cycles, from one thread or from four
+//  - without a cluster a kernel of its own, that has no exchange: 8 us less
+//  - left out: more chunks of K and V or more query tiles in shared memory, K and V given back one
+//    by one, eight warps for the weights, two threads for the updates: none gained
 // P's weights: within 16 tokens exponentials, from one run of 16 to a later one products of a
 // factor of the row's and one of the column's.
 //
@@ -54,7 +56,6 @@ namespace pa {
 
 namespace {
 
-constexpr int kC = kLinearChunk;
 constexpr int kSlice = 64;   // state columns of a CTA
 constexpr int kRows = 128;   // rows of a query tile, and of a state's MMA
 constexpr int kWarpKV = 1, kWarpQK = 2, kWarpQS = 3, kFirstOut = 4, kFirstWeigh = 12,
@@ -63,18 +64,19 @@ constexpr int kMmaWarps = 4, kGroupWarps = 4, kWeighWarps = 4, kStateWarps = 8;
 // (a warp is on the SM's quarter of its number modulo 4: each has as much to issue)
 constexpr int kWarpScan = kFirstState + kStateWarps, kWarpPV = kWarpScan + 1;
 constexpr int kWarps = kWarpPV + 1, kThreads = 32 * kWarps;
-constexpr int kRing = 3;     // chunks of K and V in shared memory
 constexpr int kQueue = 4;
 constexpr int kTables = 8;   // chunks whose sums of logarithms are kept
-constexpr int kVtBars = 4;   // chunks ahead of whoever looks at their weighed V's barrier
+constexpr int kVtBars = 8;   // more than weighed V can be ahead of whoever looks at its barrier
+constexpr int kPart = 64;    // tokens of a buffer of weighed V
 constexpr int kParts = 3;    // bf16 numbers whose sum is a weighed element of V
 // Logarithms (base 2) below this are as good as none: what they multiply is 0 in fp32.
 constexpr float kLeastLog = -150.f;
 
 // Of a chunk's tokens: the logarithms' sums up to each (base 2), e^ of what lies between a token
 // and the end of its run of 16, of what lies behind it in the chunk, and the whole sum.
+template <int C>
 struct alignas(16) Table {
-    float sum[kC], tail[kC], weight[kC];
+    float sum[C], tail[C], weight[C];
     float all, pad[3];
 };
 
@@ -89,44 +91,57 @@ __device__ __forceinline__ uint32_t f2_bf16x2(uint64_t v) {
     return pack_bf16x2(lo, hi);
 }
 
-template <int D>
+// 32 aligned bytes: a whole sector from each lane
+__device__ __forceinline__ void store32(uint4 *dst, const uint4 &lo, const uint4 &hi) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(lo.x),
+                 "r"(lo.y), "r"(lo.z), "r"(lo.w), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
+                 : "memory");
+}
+
+// A chunk is 64 tokens beside tiles of two heads, 128 beside tiles of one.
+template <int D, int C>
 struct Geom {
+    static constexpr int kHeads = kRows / C;  // of a tile
+    static constexpr int kRing = C == 64 ? 3 : 2;   // chunks of K and V in shared memory
+    static constexpr int kQBufs = C == 64 ? 2 : 1;  // query tiles
+    static constexpr int kOBufs = C == 64 ? 2 : 1;  // outputs in TMEM
+    static constexpr int kFills = C / kPart;        // buffers of weighed V that a chunk fills
     static constexpr int kHalves = D / 64;
-    static constexpr int kQHalf = kRows * 128, kKHalf = kC * 128;
+    static constexpr int kQHalf = kRows * 128, kKHalf = C * 128;
     static constexpr int kQBytes = kHalves * kQHalf;
     static constexpr int kKBytes = kHalves * kKHalf, kVBytes = kKHalf;
     static constexpr int kStageBytes = kKBytes + kVBytes;
     static constexpr int kSBytes = kRows * 128;  // bf16 state: 128 rows x 64 columns
-    static constexpr int kOffQ = 0;              // [2]
-    static constexpr int kOffKV = kOffQ + 2 * kQBytes;
+    static constexpr int kOffQ = 0;              // [kQBufs]
+    static constexpr int kOffKV = kOffQ + kQBufs * kQBytes;
     static constexpr int kOffVt = kOffKV + kRing * kStageBytes;  // weighed V, part after part [2]
-    static constexpr int kOffS = kOffVt + 2 * kParts * kVBytes;  // [2]
+    static constexpr int kVtBytes = kPart * 128;
+    static constexpr int kOffS = kOffVt + 2 * kParts * kVtBytes;  // [2]
     static constexpr int kOffBar = kOffS + 2 * kSBytes;
-    static constexpr int kOffTab = kOffBar + 320;                // [kTables]
-    static constexpr int kOffCtl = kOffTab + kTables * static_cast<int>(sizeof(Table));
+    static constexpr int kOffTab = kOffBar + 416;                // [kTables]
+    static constexpr int kOffCtl = kOffTab + kTables * static_cast<int>(sizeof(Table<C>));
     static constexpr int kSmemRaw = kOffCtl + 512 + (kThreads + 1) * 4;
     // one CTA per SM: its TMEM columns are all taken
     static constexpr int kSmemBytes = kSmemRaw > 116 * 1024 ? kSmemRaw : 116 * 1024;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
     static_assert(kOffBar % 1024 == 0, "alignment");
-    // TMEM columns: scores [2], outputs (before | inside) [2], updates [2]
+    // TMEM columns: scores [2], outputs (before | inside) [kOBufs], updates [2]
     static constexpr uint32_t kTmemCols = 512;
-    static constexpr int kColO = 2 * kC, kColU = kColO + 2 * 2 * kSlice;
+    static constexpr int kColO = 2 * C, kColU = kColO + kOBufs * 2 * kSlice;
     static_assert(kColU + 2 * kSlice <= 512, "TMEM");
 };
 
 struct Bars {
-    uint64_t kv_full[kRing], kv_empty[kRing];
+    uint64_t kv_full[3], kv_empty[3];
     uint64_t q_full[2], q_empty[2];
-    // weighed V (and table) of a chunk there; its update done (which frees the weighed V) /
-    // read.  The weighing warps may be two chunks ahead of who looks at their barrier.
-    uint64_t tab_full[kVtBars], vt_full[kVtBars], u_full[2], u_empty[2];
+    // table of a chunk there, weighed V of 64 tokens there / read; an update done / read
+    uint64_t tab_full[kVtBars], vt_full[kVtBars], vt_empty[2], u_full[2], u_empty[2];
     uint64_t s_full[2], s_empty[2];    // state before a chunk in shared memory / read
     uint64_t sc_full[2], p_full[2];    // scores of a tile / its P
     uint64_t o_full[2], o_empty[2];
     uint64_t drain[kMmaWarps];
 };
-static_assert(sizeof(Bars) <= 320, "barrier area");
+static_assert(sizeof(Bars) <= 416, "barrier area");
 static_assert(kWarpKV < kMmaWarps && kWarpQK < kMmaWarps && kWarpQS < kMmaWarps, "drain[]");
 
 // One request, kv head and slice, and this rank's run of chunks.
@@ -171,7 +186,7 @@ __device__ __forceinline__ int long_tokens(const LinearParams &p, int b, int &t0
 
 // The k-th item of this cluster, by all lanes of warp 0: long request number idx / (heads *
 // slices), found from the threads' counts of long requests before theirs (count[]).
-template <int D>
+template <int D, int C>
 __device__ Item find_item(const LinearParams &p, const int *count, int k, int rank, int size) {
     const int lane = threadIdx.x & 31;
     const int per = p.num_kv_heads * (D / kSlice);
@@ -213,7 +228,7 @@ __device__ Item find_item(const LinearParams &p, const int *count, int k, int ra
     if (it.in >= p.num_slots) it.in = -1, flags = PA_DEV_BAD_SLOT;
     if (it.to >= p.num_slots) it.to = -1, flags = PA_DEV_BAD_SLOT;
     if (flags && lane == 0) flag_status(p.status, flags);
-    it.chunks = (it.n + kC - 1) / kC;
+    it.chunks = (it.n + C - 1) / C;
     const int run = (it.chunks + size - 1) / size;
     it.c_begin = min(it.chunks, rank * run);
     it.c_end = min(it.chunks, it.c_begin + run);
@@ -243,15 +258,16 @@ __device__ __forceinline__ Item queue_item(Ctl *ctl, int warp, int k) {
 
 }  // namespace
 
-template <int D, bool CLUSTER>
+template <int D, int C, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_prompt_kernel(const LinearParams p, const __grid_constant__ CUtensorMap tmq,
                          const __grid_constant__ CUtensorMap tmk,
                          const __grid_constant__ CUtensorMap tmv, int ranks) {
-    using G = Geom<D>;
+    using G = Geom<D, C>;
+    constexpr int kRing = G::kRing;
     extern __shared__ __align__(1024) uint8_t smem[];
     Bars *bars = reinterpret_cast<Bars *>(smem + G::kOffBar);
-    Table *tables = reinterpret_cast<Table *>(smem + G::kOffTab);
+    Table<C> *tables = reinterpret_cast<Table<C> *>(smem + G::kOffTab);
     Ctl *ctl = reinterpret_cast<Ctl *>(smem + G::kOffCtl);
     int *count = reinterpret_cast<int *>(smem + G::kOffCtl + 512);
     volatile int *abort_flag = &ctl->abort;
@@ -259,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lane = threadIdx.x & 31, tid = threadIdx.x;
     const int size = CLUSTER ? ranks : 1;
     const int rank = CLUSTER ? static_cast<int>(blockIdx.x) % size : 0;
-    const int tiles = (p.group + p.heads_per_tile - 1) / p.heads_per_tile;
+    const int tiles = (p.group + G::kHeads - 1) / G::kHeads;
 
     if (tid == 0) {
         for (int i = 0; i < kRing; ++i) {
@@ -274,6 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->q_full[i], 1);
             mbar_init(&bars->q_empty[i], 2);  // by Q K^T and Q S
+            mbar_init(&bars->vt_empty[i], 1);
             mbar_init(&bars->u_full[i], 1);
             mbar_init(&bars->u_empty[i], kStateWarps);
             mbar_init(&bars->s_full[i], kStateWarps);
@@ -323,8 +340,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         // ============================ loads ============================
         uint32_t c = 0, t = 0;  // chunks and tiles loaded
-        // tiles of one head: every other one in the upper half of the rows, which are other warps'
-        const int upper = p.heads_per_tile == 1 ? kC * 128 : 0;
         bool ok = true;
         auto load_kv = [&](const Item &it, int i) {
             const int st = c % kRing;
@@ -336,16 +351,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint8_t *dst = sKV + st * G::kStageBytes;
                 mbar_arrive_expect_tx(&bars->kv_full[st], G::kStageBytes);
                 for (int hf = 0; hf < G::kHalves; ++hf)
-                    tma_load_3d(dst + hf * G::kKHalf, &tmk, hf * 64, it.h, it.t0 + i * kC,
+                    tma_load_3d(dst + hf * G::kKHalf, &tmk, hf * 64, it.h, it.t0 + i * C,
                                 &bars->kv_full[st]);
-                tma_load_3d(dst + G::kKBytes, &tmv, it.slice * kSlice, it.h, it.t0 + i * kC,
+                tma_load_3d(dst + G::kKBytes, &tmv, it.slice * kSlice, it.h, it.t0 + i * C,
                             &bars->kv_full[st]);
             }
             __syncwarp();
             ++c;
         };
         for (int k = 0;; ++k) {
-            Item it = find_item<D>(p, count, k, rank, size);
+            Item it = find_item<D, C>(p, count, k, rank, size);
             if (lane == 0) {
                 const bool free = k < kQueue || spin(&ctl->abort, [&] {
                                       for (int w = 1; w < kWarps; ++w)
@@ -370,16 +385,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!outputs) continue;
 #pragma unroll 1
                     for (int j = 0; ok && j < tiles; ++j, ++t) {
-                        const int st = t & 1;
-                        if (t >= 2)
-                            ok = warp_mbar_wait_small(&bars->q_empty[st], ((t >> 1) - 1) & 1, abort_flag);
+                        const int st = t % G::kQBufs;
+                        if (t >= G::kQBufs)
+                            ok = warp_mbar_wait_small(&bars->q_empty[st], (t / G::kQBufs - 1) & 1, abort_flag);
                         if (!ok) break;
                         if (lane == 0) {
-                            mbar_arrive_expect_tx(&bars->q_full[st],
-                                                  G::kHalves * kC * p.heads_per_tile * 128);
+                            mbar_arrive_expect_tx(&bars->q_full[st], G::kQBytes);
                             for (int hf = 0; hf < G::kHalves; ++hf)
-                                tma_load_3d(sQ + st * G::kQBytes + hf * G::kQHalf + upper * st, &tmq, hf * 64,
-                                            it.h * p.group + j * p.heads_per_tile, it.t0 + i * kC,
+                                tma_load_3d(sQ + st * G::kQBytes + hf * G::kQHalf, &tmq, hf * 64,
+                                            it.h * p.group + j * G::kHeads, it.t0 + i * C,
                                             &bars->q_full[st]);
                         }
                         __syncwarp();
@@ -395,7 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // copies in flight land before the CTA exits
             for (uint32_t i = c > kRing ? c - kRing : 0; i < c; ++i)
                 mbar_drain(&bars->kv_full[i % kRing], (i / kRing) & 1);
-            for (uint32_t i = t > 2 ? t - 2 : 0; i < t; ++i) mbar_drain(&bars->q_full[i & 1], (i >> 1) & 1);
+            for (uint32_t i = t > G::kQBufs ? t - G::kQBufs : 0; i < t; ++i)
+                mbar_drain(&bars->q_full[i % G::kQBufs], (i / G::kQBufs) & 1);
         }
     } else if (warp < kFirstOut || warp == kWarpPV) {
         // ============================ MMAs ============================
@@ -404,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // and P V.  (One thread, not a warp with an elected
         // lane's predicate: operands in a warp's uniform registers are no longer its own when
         // a wait has taken the lanes apart.  A commit was seen to arrive twice, and worse.)
-        constexpr uint32_t idesc_qk = idesc_bf16_f32(kRows, kC, 0);
+        constexpr uint32_t idesc_qk = idesc_bf16_f32(kRows, C, 0);
         constexpr uint32_t idesc_v = idesc_bf16_f32(kRows, kSlice, 1);
         constexpr uint32_t idesc_kv = idesc_bf16_f32(kRows, kSlice, 1, 1);
         const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
@@ -413,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // those rows of the update are not read)
         const uint64_t kt_desc = smem_desc_sw128(smem_u32(sKV), G::kKHalf, 1024);
         const uint64_t v_desc = smem_desc_sw128(smem_u32(sKV) + G::kKBytes, G::kKHalf, 1024);
-        const uint64_t vt_desc = smem_desc_sw128(smem_u32(sVt), G::kKHalf, 1024);
+        const uint64_t vt_desc = smem_desc_sw128(smem_u32(sVt), G::kVtBytes, 1024);
         const uint64_t s_desc = smem_desc_sw128(smem_u32(sS), G::kKHalf, 1024);
         uint32_t c = 0, u = 0, s = 0, t = 0;  // chunks of the ring, updates, states, tiles
         bool ok = true;
@@ -422,35 +437,45 @@ __global__ void __launch_bounds__(kThreads, 1)
             return ok;
         };
         auto wait_chunk = [&]() { return wait(&bars->kv_full[c % kRing], (c / kRing) & 1); };
+        // the last of a chunk's weighed V (and with it its table, and zeros behind the request)
+        auto wait_weighed = [&](uint32_t u) {
+            const uint32_t w = u * G::kFills + G::kFills - 1;
+            return wait(&bars->vt_full[w % kVtBars], (w / kVtBars) & 1);
+        };
         auto update = [&]() {
-            if (!wait(&bars->vt_full[u % kVtBars], (u / kVtBars) & 1) ||
-                (u >= 2 && !wait(&bars->u_empty[u & 1], ((u >> 1) - 1) & 1)))
-                return;
-            tc_fence_after();
-            const uint64_t kd = kt_desc + (c % kRing) * (G::kStageBytes >> 4);
-            const uint64_t vd = vt_desc + (u & 1) * (kParts * G::kVBytes >> 4);
+            if (u >= 2 && !wait(&bars->u_empty[u & 1], ((u >> 1) - 1) & 1)) return;
             const uint32_t d = tmem + G::kColU + (u & 1) * kSlice;
-            static_assert(G::kVBytes == kC * 128, "parts follow each other");
+            uint64_t kd = kt_desc + (c % kRing) * (G::kStageBytes >> 4);
 #pragma unroll 1
-            for (int part = 0; part < kParts; ++part)
+            for (uint32_t w = u * G::kFills; w < (u + 1) * G::kFills; ++w) {
+                if (!wait(&bars->vt_full[w % kVtBars], (w / kVtBars) & 1)) return;
+                tc_fence_after();
+                uint64_t vd = vt_desc + (w & 1) * (kParts * G::kVtBytes >> 4);
+#pragma unroll 1
+                for (int part = 0; part < kParts; ++part, vd += G::kVtBytes >> 4)
 #pragma unroll
-                for (int kk = 0; kk < kC / 16; ++kk)
-                    tc_mma(d, kd + kk * (2048 >> 4),
-                           vd + part * (G::kVBytes >> 4) + kk * (2048 >> 4), idesc_kv,
-                           part + kk > 0 ? 1u : 0u);
+                    for (int kk = 0; kk < kPart / 16; ++kk)
+                        tc_mma(d, kd + kk * (2048 >> 4), vd + kk * (2048 >> 4), idesc_kv,
+                               part + kk > 0 || w > u * G::kFills ? 1u : 0u);
+                kd += kPart * 128 >> 4;
+                tc_commit(&bars->vt_empty[w & 1]);
+            }
             tc_commit(&bars->u_full[u & 1]);
             ++u;
         };
         // Q by K or by S for the tiles of a chunk (one code for both): B's descriptor, and its
-        // steps from 16 of the summed dimension to the next and from 64 to the next
+        // steps from 16 of the summed dimension to the next and from 64 to the next; the barrier
+        // of the tile `lag` ago says that D's columns are free
         auto by_q = [&](uint64_t b_desc, uint32_t step, uint32_t step64, uint32_t d, uint32_t d_next,
-                        uint32_t idesc, uint64_t *before, uint64_t *after) {
+                        uint32_t idesc, uint32_t lag, uint64_t *before, uint64_t *after) {
 #pragma unroll 1
             for (int j = 0; j < tiles; ++j, ++t) {
-                const uint32_t b = t & 1, turn = (t >> 1) & 1;
-                if (!wait(&bars->q_full[b], turn) || (t >= 2 && !wait(&before[b], turn ^ 1))) return;
+                const uint32_t b = t & 1, slot = t % G::kQBufs, last = t - lag;
+                if (!wait(&bars->q_full[slot], (t / G::kQBufs) & 1) ||
+                    (t >= lag && !wait(&before[last & 1], (last >> 1) & 1)))
+                    return;
                 tc_fence_after();
-                const uint64_t qd = q_desc + b * (G::kQBytes >> 4);
+                const uint64_t qd = q_desc + slot * (G::kQBytes >> 4);
 #pragma unroll 1
                 for (int hf = 0; hf < G::kHalves; ++hf)
 #pragma unroll
@@ -458,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tc_mma(d + b * d_next, qd + hf * (G::kQHalf >> 4) + kk * 2,
                                b_desc + hf * step64 + kk * step, idesc, hf + kk > 0 ? 1u : 0u);
                 tc_commit(&after[b]);
-                tc_commit(&bars->q_empty[b]);
+                tc_commit(&bars->q_empty[slot]);
             }
         };
         auto inside = [&]() {
@@ -466,12 +491,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < tiles; ++j, ++t) {
                 const uint32_t b = t & 1, turn = (t >> 1) & 1;
                 // (P is there after the outputs of two tiles ago have been read)
-                if (!wait(&bars->p_full[b], turn)) return;
+                if (!wait(&bars->p_full[b], turn) ||
+                    (G::kOBufs == 1 && t >= 1 && !wait(&bars->o_empty[b ^ 1], ((t - 1) >> 1) & 1)))
+                    return;
                 tc_fence_after();
                 const uint64_t vd = v_desc + (c % kRing) * (G::kStageBytes >> 4);
 #pragma unroll
-                for (int kk = 0; kk < kC / 16; ++kk)
-                    tc_mma_ts(tmem + G::kColO + b * (2 * kSlice) + kSlice, tmem + b * kC + kk * 8,
+                for (int kk = 0; kk < C / 16; ++kk)
+                    tc_mma_ts(tmem + G::kColO + b % G::kOBufs * (2 * kSlice) + kSlice, tmem + b * C + kk * 8,
                               vd + (kk * 2048 >> 4), idesc_v, kk > 0 ? 1u : 0u);
                 tc_commit(&bars->o_full[b]);
             }
@@ -488,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (warp == kWarpKV) update();
                         // (V's rows behind the request are zeroed with its weighing)
                         if (warp == kWarpPV) {
-                            wait(&bars->vt_full[u % kVtBars], (u / kVtBars) & 1);
+                            wait_weighed(u);
                             ++u;
                         }
                         if (ok && outputs && warp != kWarpKV) {
@@ -501,8 +528,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 by_q(qs ? s_desc + (s & 1) * (G::kSBytes >> 4)
                                         : k_desc + (c % kRing) * (G::kStageBytes >> 4),
                                      qs ? 2048 >> 4 : 2, qs ? 8192 >> 4 : G::kKHalf >> 4,
-                                     tmem + (qs ? G::kColO : 0), qs ? 2 * kSlice : kC,
-                                     qs ? idesc_v : idesc_qk, qs ? bars->o_empty : bars->o_full,
+                                     tmem + (qs ? G::kColO : 0), qs ? (G::kOBufs - 1) * 2 * kSlice : C,
+                                     qs ? idesc_v : idesc_qk, qs ? G::kOBufs : 2, qs ? bars->o_empty : bars->o_full,
                                      qs ? bars->o_full : bars->sc_full);
                             if (qs && ok) {
                                 tc_commit(&bars->s_empty[s & 1]);
@@ -530,16 +557,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int wq = warp & 3;
         const uint32_t grp = (warp - kFirstOut) / kGroupWarps;  // takes tiles of this parity
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-        const uint32_t sa = t_lane + grp * kC, oa = t_lane + G::kColO + grp * (2 * kSlice);
-        // a tile of one head fills half of the rows, the lower or the upper one; the warps of the
-        // others have nothing to do
-        const int row0 = p.heads_per_tile == 1 ? wq * 32 - static_cast<int>(grp) * kC : wq * 32;
-        const bool idle = row0 < 0 || row0 >= kC * p.heads_per_tile;
-        const int tok = (row0 + lane) / p.heads_per_tile;
-        const int head = row0 + lane - tok * p.heads_per_tile;
+        const uint32_t sa = t_lane + grp * C, oa = t_lane + G::kColO + grp % G::kOBufs * (2 * kSlice);
+        const int tok = (wq * 32 + lane) / G::kHeads, head = (wq * 32 + lane) % G::kHeads;
         // the runs of 16 tokens that the warp's rows lie in
-        const int first_run = row0 / p.heads_per_tile / 16;
-        const int last_run = (row0 + 31) / p.heads_per_tile / 16;
+        const int first_run = wq * 32 / G::kHeads / 16, last_run = (wq * 32 + 31) / G::kHeads / 16;
+        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
         uint32_t t = 0, u = 0;  // tiles, updates up to this item
         bool ok = true;
         for (int k = 0;; ++k) {
@@ -557,94 +579,97 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t tt = t + m;
                 if ((tt & 1) == grp) {
                     const uint32_t turn = (tt >> 1) & 1, uu = u + (i - it.c_begin);
-                    ok = warp_mbar_wait_small(&bars->vt_full[uu % kVtBars], (uu / kVtBars) & 1, abort_flag) &&
+                    const uint32_t w = uu * G::kFills + G::kFills - 1;
+                    ok = warp_mbar_wait_small(&bars->vt_full[w % kVtBars], (w / kVtBars) & 1, abort_flag) &&
                          warp_mbar_wait_small(&bars->sc_full[grp], turn, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
-                    const Table &tab = tables[uu % kTables];
-                    const float gi = idle ? 0.f : tab.sum[tok];
-                    if (!idle) {
+                    const Table<C> &tab = tables[uu % kTables];
+                    const float gi = tab.sum[tok];
 #pragma unroll 1
-                        for (int run = 0; run < kC / 16; ++run) {
-                            uint32_t pk[8];
+                    for (int run = 0; run < C / 16; ++run) {
+                        uint32_t pk[8];
 #pragma unroll
-                            for (int x = 0; x < 8; ++x) pk[x] = 0u;
-                            if (run <= last_run) {
-                                uint32_t v[16];
-                                tmem_ld16(sa + run * 16, v);
-                                if (run < first_run) {
-                                    // e^(G_i - G_j) by way of the run's last token
-                                    const uint64_t row = f2_twice(fast_exp2(gi - tab.sum[run * 16 + 15]));
-                                    tmem_wait_ld();
+                        for (int x = 0; x < 8; ++x) pk[x] = 0u;
+                        if (run <= last_run) {
+                            uint32_t v[16];
+                            tmem_ld16(sa + run * 16, v);
+                            if (run < first_run) {
+                                // e^(G_i - G_j) by way of the run's last token
+                                const uint64_t row = f2_twice(fast_exp2(gi - tab.sum[run * 16 + 15]));
+                                tmem_wait_ld();
 #pragma unroll
-                                    for (int x = 0; x < 16; x += 4) {
-                                        const float4 f =
-                                            *reinterpret_cast<const float4 *>(tab.tail + run * 16 + x);
-                                        auto w = [&](int e, float f0, float f1) {
-                                            return f2_bf16x2(f2_mul(f2_mul(f2_words(v[x + e], v[x + e + 1]), row),
-                                                                    f2_pack(f0, f1)));
-                                        };
-                                        pk[x / 2] = w(0, f.x, f.y);
-                                        pk[x / 2 + 1] = w(2, f.z, f.w);
-                                    }
-                                } else {
-                                    const int lim = tok - run * 16;  // its last visible column
-                                    const uint64_t minus = f2_twice(-1.f);
-                                    tmem_wait_ld();
+                                for (int x = 0; x < 16; x += 4) {
+                                    const float4 f =
+                                        *reinterpret_cast<const float4 *>(tab.tail + run * 16 + x);
+                                    auto w = [&](int e, float f0, float f1) {
+                                        return f2_bf16x2(f2_mul(f2_mul(f2_words(v[x + e], v[x + e + 1]), row),
+                                                                f2_pack(f0, f1)));
+                                    };
+                                    pk[x / 2] = w(0, f.x, f.y);
+                                    pk[x / 2 + 1] = w(2, f.z, f.w);
+                                }
+                            } else {
+                                const int lim = tok - run * 16;  // its last visible column
+                                const uint64_t minus = f2_twice(-1.f);
+                                tmem_wait_ld();
 #pragma unroll
-                                    for (int x = 0; x < 16; x += 4) {
-                                        const float4 g =
-                                            *reinterpret_cast<const float4 *>(tab.sum + run * 16 + x);
-                                        auto w = [&](int e, float g0, float g1) {
-                                            float a, b;
-                                            f2_unpack(f2_fma(f2_pack(g0, g1), minus, f2_twice(gi)), a, b);
-                                            f2_unpack(f2_mul(f2_words(v[x + e], v[x + e + 1]),
-                                                             f2_pack(fast_exp2(a), fast_exp2(b))), a, b);
-                                            return pack_bf16x2(x + e <= lim ? a : 0.f,
-                                                               x + e + 1 <= lim ? b : 0.f);
-                                        };
-                                        pk[x / 2] = w(0, g.x, g.y);
-                                        pk[x / 2 + 1] = w(2, g.z, g.w);
-                                    }
+                                for (int x = 0; x < 16; x += 4) {
+                                    const float4 g =
+                                        *reinterpret_cast<const float4 *>(tab.sum + run * 16 + x);
+                                    auto w = [&](int e, float g0, float g1) {
+                                        float a, b;
+                                        f2_unpack(f2_fma(f2_pack(g0, g1), minus, f2_twice(gi)), a, b);
+                                        f2_unpack(f2_mul(f2_words(v[x + e], v[x + e + 1]),
+                                                         f2_pack(fast_exp2(a), fast_exp2(b))), a, b);
+                                        return pack_bf16x2(x + e <= lim ? a : 0.f,
+                                                           x + e + 1 <= lim ? b : 0.f);
+                                    };
+                                    pk[x / 2] = w(0, g.x, g.y);
+                                    pk[x / 2 + 1] = w(2, g.z, g.w);
                                 }
                             }
-                            // (over scores that have been read: a run's P takes half their columns)
-                            tmem_st8(sa + run * 8, pk);
                         }
-                        tmem_wait_st();
-                        tc_fence_before();
+                        // (over scores that have been read: a run's P takes half their columns)
+                        tmem_st8(sa + run * 8, pk);
                     }
+                    tmem_wait_st();
+                    tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars->p_full[grp]);
 
                     ok = warp_mbar_wait_small(&bars->o_full[grp], turn, abort_flag);
                     if (!ok) break;
-                    if (!idle) {
-                        tc_fence_after();
-                        const uint64_t before = f2_twice(fast_exp2(gi) * p.scale), scale = f2_twice(p.scale);
-                        const int token = i * kC + tok, hq = j * p.heads_per_tile + head;
-                        const bool valid = token < it.n && hq < p.group;
-                        uint4 *dst = reinterpret_cast<uint4 *>(
-                            p.out + (static_cast<int64_t>(it.t0 + token) * p.num_q_heads +
-                                     it.h * p.group + hq) * D + it.slice * kSlice);
+                    tc_fence_after();
+                    const uint64_t before = f2_twice(fast_exp2(gi) * p.scale), scale = f2_twice(p.scale);
+                    const int token = i * C + tok, hq = j * G::kHeads + head;
+                    const bool valid = token < it.n && hq < p.group;
+                    uint4 *dst = reinterpret_cast<uint4 *>(
+                        p.out + (static_cast<int64_t>(it.t0 + token) * p.num_q_heads +
+                                 it.h * p.group + hq) * D + it.slice * kSlice);
 #pragma unroll 1
-                        for (int part = 0; part < kSlice / 16; ++part) {
-                            uint32_t a[16], b[16];
-                            __syncwarp();
-                            tmem_ld16(oa + part * 16, a);
-                            tmem_ld16(oa + kSlice + part * 16, b);
-                            tmem_wait_ld();
-                            auto sum = [&](int x) {
-                                return f2_bf16x2(f2_fma(before, f2_words(a[x], a[x + 1]),
-                                                        f2_mul(scale, f2_words(b[x], b[x + 1]))));
-                            };
-                            if (valid) {
-                                dst[part * 2] = make_uint4(sum(0), sum(2), sum(4), sum(6));
-                                dst[part * 2 + 1] = make_uint4(sum(8), sum(10), sum(12), sum(14));
+                    for (int part = 0; part < kSlice / 16; ++part) {
+                        uint32_t a[16], b[16];
+                        __syncwarp();
+                        tmem_ld16(oa + part * 16, a);
+                        tmem_ld16(oa + kSlice + part * 16, b);
+                        tmem_wait_ld();
+                        auto sum = [&](int x) {
+                            return f2_bf16x2(f2_fma(before, f2_words(a[x], a[x + 1]),
+                                                    f2_mul(scale, f2_words(b[x], b[x + 1]))));
+                        };
+                        if (valid) {
+                            const uint4 lo = make_uint4(sum(0), sum(2), sum(4), sum(6));
+                            const uint4 hi = make_uint4(sum(8), sum(10), sum(12), sum(14));
+                            if (wide) {
+                                store32(dst + part * 2, lo, hi);
+                            } else {
+                                dst[part * 2] = lo;
+                                dst[part * 2 + 1] = hi;
                             }
                         }
-                        tc_fence_before();
                     }
+                    tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars->o_empty[grp]);
                 }
@@ -656,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < kFirstState) {
         // ============================ V's weights ============================
         const int vw = warp - kFirstWeigh;
-        uint32_t c = 0, u = 0;  // chunks of the ring, updates
+        uint32_t w = 0;  // buffers filled
         bool ok = true;
         for (int k = 0;; ++k) {
             const Item it = queue_item(ctl, warp, k);
@@ -665,21 +690,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int outputs = size > 1 ? 0 : 1; outputs < 2; ++outputs) {
                 const int c_last = outputs || it.c_end < it.chunks ? it.c_end : it.c_begin;
 #pragma unroll 1
-                for (int i = it.c_begin; ok && i < c_last; ++i, ++c, ++u) {
-                    const int st = c % kRing;
-                    // the chunk is here, and the update of two chunks ago has read its weighed V
-                    ok = warp_mbar_wait_small(&bars->kv_full[st], (c / kRing) & 1, abort_flag) &&
+                for (uint32_t f = 0; ok && f < (c_last - it.c_begin) * G::kFills; ++f, ++w) {
+                    const uint32_t u = w / G::kFills;
+                    const int st = u % kRing, i = it.c_begin + f / G::kFills;
+                    // the chunk is here, and the MMAs of two fills ago have read theirs
+                    ok = warp_mbar_wait_small(&bars->kv_full[st], (u / kRing) & 1, abort_flag) &&
                          warp_mbar_wait_small(&bars->tab_full[u % kVtBars], (u / kVtBars) & 1, abort_flag) &&
-                         (u < 2 || warp_mbar_wait_small(&bars->u_full[u & 1], ((u >> 1) - 1) & 1, abort_flag));
+                         (w < 2 || warp_mbar_wait_small(&bars->vt_empty[w & 1], ((w >> 1) - 1) & 1, abort_flag));
                     if (!ok) break;
-                    uint8_t *k_tile = sKV + st * G::kStageBytes, *v = k_tile + G::kKBytes;
-                    uint8_t *vt = sVt + (u & 1) * (kParts * G::kVBytes);
-                    const float *weight = tables[u % kTables].weight;
-                    const int valid = min(kC, it.n - i * kC);
+                    const uint32_t half = w % G::kFills * (kPart * 128);
+                    uint8_t *k_tile = sKV + st * G::kStageBytes + half, *v = k_tile + G::kKBytes;
+                    uint8_t *vt = sVt + (w & 1) * (kParts * G::kVtBytes);
+                    const float *weight = tables[u % kTables].weight + w % G::kFills * kPart;
+                    const int valid = it.n - i * C - w % G::kFills * kPart;
                     // eight lanes to a row of 64 elements
 #pragma unroll 2
-                    for (int x = 0; x < kC / (4 * kWeighWarps); ++x) {
-                        const int row = vw * (kC / kWeighWarps) + x * 4 + lane / 8;
+                    for (int x = 0; x < kPart / (4 * kWeighWarps); ++x) {
+                        const int row = vw * (kPart / kWeighWarps) + x * 4 + lane / 8;
                         const uint32_t off = sw128_offset(row, lane % 8);
                         const uint64_t wt = f2_twice(weight[row]);
                         uint4 in = *reinterpret_cast<const uint4 *>(v + off);
@@ -711,11 +738,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         split(in.w, part[0].w, part[1].w, part[2].w);
 #pragma unroll
                         for (int n = 0; n < kParts; ++n)
-                            *reinterpret_cast<uint4 *>(vt + n * G::kVBytes + off) = part[n];
+                            *reinterpret_cast<uint4 *>(vt + n * G::kVtBytes + off) = part[n];
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->vt_full[u % kVtBars]);
+                    if (lane == 0) mbar_arrive(&bars->vt_full[w % kVtBars]);
                 }
                 if (!outputs) {
                     cluster_sync();
@@ -725,6 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kWarpScan) {
         // ============================ sums of logarithms ============================
+        constexpr int T = C / 32;  // tokens of a lane
         uint32_t c = 0;
         bool ok = true;
         // logarithm (base 2) of the decay of token i of the request
@@ -739,20 +767,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int outputs = size > 1 ? 0 : 1; outputs < 2; ++outputs) {
                 const int c_last = outputs || it.c_end < it.chunks ? it.c_end : it.c_begin;
-                float g0 = 0.f, g1 = 0.f, n0 = 0.f, n1 = 0.f;
+                float g[T] = {}, next[T] = {};
 #pragma unroll 1
                 for (int i = it.c_begin - 1; ok && i < c_last; ++i) {
-                    g0 = n0;
-                    g1 = n1;
-                    if (i + 1 < c_last) {  // the next chunk's, a chunk ahead
-                        n0 = log_of(it, (i + 1) * kC + 2 * lane);
-                        n1 = log_of(it, (i + 1) * kC + 2 * lane + 1);
+#pragma unroll
+                    for (int x = 0; x < T; ++x) {
+                        g[x] = next[x];
+                        if (i + 1 < c_last) next[x] = log_of(it, (i + 1) * C + T * lane + x);  // a chunk ahead
                     }
                     if (i < it.c_begin) continue;
-                    // sums up to each token (lane: tokens 2 lane and 2 lane + 1), and of those
-                    // behind it (each without a difference, so that a small one keeps its digits
-                    // beside large ones)
-                    float up = g0 + g1, down = up;
+                    // sums up to each token (T to a lane), and of those behind it (each without a
+                    // difference, so that a small one keeps its digits beside large ones)
+                    float up = g[0];
+#pragma unroll
+                    for (int x = 1; x < T; ++x) up += g[x];
+                    float down = up;
 #pragma unroll
                     for (int o = 1; o < 32; o <<= 1) {
                         const float a = __shfl_up_sync(0xffffffffu, up, o);
@@ -760,23 +789,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (lane >= o) up += a;
                         if (lane + o < 32) down += b;
                     }
-                    const float end = __shfl_sync(0xffffffffu, up, lane | 7);  // of the run of 16
-                    float up0 = __shfl_up_sync(0xffffffffu, up, 1);
-                    float down1 = __shfl_down_sync(0xffffffffu, down, 1);
-                    if (lane == 0) up0 = 0.f;
-                    if (lane == 31) down1 = 0.f;
-                    up0 += g0;
-                    // (the chunk of three ago is through its MMAs: who still reads a table is no
-                    // further behind than the one of five ago)
+                    const float end = __shfl_sync(0xffffffffu, up, lane | (16 / T - 1));  // of the run of 16
+                    float sum[T], behind[T];
+                    sum[0] = __shfl_up_sync(0xffffffffu, up, 1);
+                    behind[T - 1] = __shfl_down_sync(0xffffffffu, down, 1);
+                    if (lane == 0) sum[0] = 0.f;
+                    if (lane == 31) behind[T - 1] = 0.f;
+                    sum[0] += g[0];
+#pragma unroll
+                    for (int x = 1; x < T; ++x) {
+                        sum[x] = x == T - 1 ? up : sum[x - 1] + g[x];
+                        behind[T - 1 - x] = behind[T - x] + g[T - x];
+                    }
+                    // (the chunk that had this place in the ring is through its MMAs: who still reads
+                    // a table is at most two further behind)
                     ok = c < kRing ||
                          warp_mbar_wait_small(&bars->kv_empty[c % kRing], (c / kRing - 1) & 1, abort_flag);
                     if (!ok) break;
-                    Table &tab = tables[c % kTables];
-                    *reinterpret_cast<float2 *>(tab.sum + 2 * lane) = make_float2(up0, up);
-                    *reinterpret_cast<float2 *>(tab.tail + 2 * lane) =
-                        make_float2(fast_exp2(end - up0), fast_exp2(end - up));
-                    *reinterpret_cast<float2 *>(tab.weight + 2 * lane) =
-                        make_float2(exp2f(down1 + g1), exp2f(down1));
+                    Table<C> &tab = tables[c % kTables];
+#pragma unroll
+                    for (int x = 0; x < T; x += 2) {
+                        const int t = T * lane + x;
+                        *reinterpret_cast<float2 *>(tab.sum + t) = make_float2(sum[x], sum[x + 1]);
+                        *reinterpret_cast<float2 *>(tab.tail + t) =
+                            make_float2(fast_exp2(end - sum[x]), fast_exp2(end - sum[x + 1]));
+                        *reinterpret_cast<float2 *>(tab.weight + t) =
+                            make_float2(exp2f(behind[x]), exp2f(behind[x + 1]));
+                    }
                     if (lane == 31) tab.all = up;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars->tab_full[c % kVtBars]);
@@ -816,8 +855,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // takes a chunk's update in
         auto update = [&]() {
+            const uint32_t last = u * G::kFills + G::kFills - 1;
             ok = warp_mbar_wait_small(&bars->u_full[u & 1], (u >> 1) & 1, abort_flag) &&
-                 warp_mbar_wait_small(&bars->vt_full[u % kVtBars], (u / kVtBars) & 1, abort_flag);
+                 warp_mbar_wait_small(&bars->vt_full[last % kVtBars], (last / kVtBars) & 1, abort_flag);
             if (!ok) return;
             tc_fence_after();
             const float all = tables[u % kTables].all;
@@ -916,24 +956,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 namespace {
 
-template <int D, bool CLUSTER>
+template <int D, int C, bool CLUSTER>
 int launch(const LinearParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
            const CUtensorMap &tv, int clusters, int size, cudaStream_t s) {
     static PerDeviceOnce once;
     if (once_per_device(once, [] {
-            return cudaFuncSetAttribute(linear_prompt_kernel<D, CLUSTER>,
+            return cudaFuncSetAttribute(linear_prompt_kernel<D, C, CLUSTER>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        Geom<D>::kSmemBytes);
+                                        Geom<D, C>::kSmemBytes);
         }) != PA_OK)
         return PA_ERR_CUDA;
-    PdlLaunch l(clusters * size, kThreads, Geom<D>::kSmemBytes, s);
+    PdlLaunch l(clusters * size, kThreads, Geom<D, C>::kSmemBytes, s);
     if (CLUSTER) l.set_cluster(size);
-    return launch_kernel(l, linear_prompt_kernel<D, CLUSTER>, p, tq, tk, tv, size) == cudaSuccess
+    return launch_kernel(l, linear_prompt_kernel<D, C, CLUSTER>, p, tq, tk, tv, size) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
 }
 
-template <int D>
+template <int D, int C>
 int launch(const LinearParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
            const CUtensorMap &tv, int sms, cudaStream_t s) {
     // the most requests that can be long, and their items
@@ -943,7 +983,7 @@ int launch(const LinearParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
     // the largest cluster whose ranks have two chunks and whose items run at once (152 SMs hold 76
     // clusters of 2, 36 of 4 and 15 of 8: a ninth of the SMs belongs to none of 8)
     int size = 1;
-    while (size < kDirectMaxCluster && 2 * size * 2 * kC <= p.num_tokens &&
+    while (size < kDirectMaxCluster && 2 * size * 2 * C <= p.num_tokens &&
            2 * size * items <= (size < 4 ? sms * 18 / 19 : sms * 15 / 19))
         size *= 2;
     // Which requests are long is known on the GPU only, so the two forms' SMs are shared out by
@@ -955,15 +995,19 @@ int launch(const LinearParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
     const int share = static_cast<int>(sms * static_cast<int64_t>(p.num_tokens) /
                                        (p.num_tokens + kStateTokens * p.num_seqs));
     const int clusters = static_cast<int>(std::min<int64_t>(items, std::max(1, share / size)));
-    return size > 1 ? launch<D, true>(p, tq, tk, tv, clusters, size, s)
-                    : launch<D, false>(p, tq, tk, tv, clusters, 1, s);
+    return size > 1 ? launch<D, C, true>(p, tq, tk, tv, clusters, size, s)
+                    : launch<D, C, false>(p, tq, tk, tv, clusters, 1, s);
 }
 
 }  // namespace
 
 int launch_linear_prompt(const LinearParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
                          const CUtensorMap &tv, int head_dim, int sms, cudaStream_t s) {
-    return head_dim == 128 ? launch<128>(p, tq, tk, tv, sms, s) : launch<64>(p, tq, tk, tv, sms, s);
+    if (p.chunk == 64)
+        return head_dim == 128 ? launch<128, 64>(p, tq, tk, tv, sms, s)
+                               : launch<64, 64>(p, tq, tk, tv, sms, s);
+    return head_dim == 128 ? launch<128, 128>(p, tq, tk, tv, sms, s)
+                           : launch<64, 128>(p, tq, tk, tv, sms, s);
 }
 
 }  // namespace pa

@@ -142,6 +142,30 @@ def test_decays(d):
     assert_status_clean()
 
 
+@pytest.mark.parametrize("decay", ["head", "token"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [8, 9, 16, 33, 63, 64, 65, 127, 128, 129, 191, 192, 193, 255, 257, 300, 640])
+def test_groups_of_one_head(n, d, decay):
+    """Tiles of one head: other chunks than a group's."""
+    run([n], 2, 2, d, decay=decay, seed=n)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_groups_of_one_head_side_by_side(d):
+    run([700, 1, 300, 5, 1, 513, 128, 0, 129], 3, 3, d, seed=1, pad=5, fresh=(0,), drop=(2,))
+    run([800], 1, 1, d, seed=2, decay="head", in_place=True)
+    run([(1, 0, 5, 140, 40)[i % 5] for i in range(200)], 2, 2, d, seed=4)
+    s = Step([90, 260, 4], 2, 2, d, seed=5, fused=False)
+    pick = torch.randint(4, s.g.shape, generator=torch.Generator().manual_seed(1))
+    s.g = torch.tensor([float("-inf"), -0.1, -0.2, -0.05])[pick]
+    t = s.to_dev()
+    t["out"] = torch.full(((t["out"].numel() + 8),), 7.0, dtype=torch.bfloat16,
+                          device=DEV)[8:].view(t["out"].shape)   # 16 bytes off the 32
+    s.call(t)
+    s.check(t)
+    assert_status_clean()
+
+
 def test_many_requests():
     run([1] * 300, 4, 2, 64, seed=3)
     run([(1, 0, 5, 1, 40)[i % 5] for i in range(1300)], 2, 1, 64, seed=4)
@@ -246,11 +270,12 @@ def test_other_stream_and_repeat():
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq", [2, 6])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-def test_other_rows_stay_other_rows(bad, d):
+def test_other_rows_stay_other_rows(bad, hq, d):
     """What stands in the next request's rows, or behind the last, reaches no sum."""
-    lens = [70, 33, 1, 100, 5, 64, 9]
-    s = Step(lens, 6, 2, d, seed=8, pad=50)
+    lens = [70, 33, 1, 100, 5, 64, 9, 200]
+    s = Step(lens, hq, 2, d, seed=8, pad=150)
     t, u = s.to_dev(), s.to_dev()
     s.call(t)
     starts = s.qsl.tolist()
