@@ -19,14 +19,16 @@
 //
 // Bound: the path between shared memory, the tensor cores' operands and L1 (128 bytes a cycle),
 // and what the schedulers issue; not HBM or the tensor pipe.  2 x 8192 tokens of 32 kv heads of
-// 128 take 179 us, where HBM alone would need 80 (95 on the 128 SMs that have a slice).  Of the
-// 5500 cycles of 128 tokens, that path carries the MMAs' operands for 2200, copies, weighed V and
+// 128 take 181 us, where HBM alone would need 80 (95 on the 128 SMs that have a slice).  Of the
+// 5500 cycles of 128 tokens, that path carries the MMAs' operands for 2000, copies, weighed V and
 // states for 1300, and the stores, a sector from each row, for 500.  Leaving a role's work out
 // saves about its share, whichever it is: no stores 20 us, no weights and a third of the updates'
 // MMAs 30, no states 20.  What that led to:
 //  - where a group is one head, chunks of 128 tokens, whose tiles fill the MMA's 128 rows: 193 us
 //    with chunks of 64 and half the rows idle (216 before the idle rows took turns)
 //  - outputs by 32 bytes of a lane: 190 us by 16
+//  - two of the three parts of the weighed V in one MMA, into columns of their own: 2 x 8192 of
+//    64 / 32 heads 200 us, 207 with an MMA to each (and one buffer for the update instead of two)
 //  - packed fp32 arithmetic, waits that sleep on the barrier, roles dealt to the schedulers by
 //    what they issue
 //  - loops over 16 columns stay loops, and only the MMAs of 64 of a dimension are unrolled: the
@@ -125,7 +127,8 @@ struct Geom {
     static constexpr int kSmemBytes = kSmemRaw > 116 * 1024 ? kSmemRaw : 116 * 1024;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
     static_assert(kOffBar % 1024 == 0, "alignment");
-    // TMEM columns: scores [2], outputs (before | inside) [kOBufs], updates [2]
+    // TMEM columns: scores [2], outputs (before | inside) [kOBufs], update (of the first part of
+    // the weighed V | of the others)
     static constexpr uint32_t kTmemCols = 512;
     static constexpr int kColO = 2 * C, kColU = kColO + kOBufs * 2 * kSlice;
     static_assert(kColU + 2 * kSlice <= 512, "TMEM");
@@ -135,7 +138,7 @@ struct Bars {
     uint64_t kv_full[3], kv_empty[3];
     uint64_t q_full[2], q_empty[2];
     // table of a chunk there, weighed V of 64 tokens there / read; an update done / read
-    uint64_t tab_full[kVtBars], vt_full[kVtBars], vt_empty[2], u_full[2], u_empty[2];
+    uint64_t tab_full[kVtBars], vt_full[kVtBars], vt_empty[2], u_full, u_empty;
     uint64_t s_full[2], s_empty[2];    // state before a chunk in shared memory / read
     uint64_t sc_full[2], p_full[2];    // scores of a tile / its P
     uint64_t o_full[2], o_empty[2];
@@ -282,6 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars->kv_full[i], 1);
             mbar_init(&bars->kv_empty[i], kMmaWarps);
         }
+        mbar_init(&bars->u_full, 1);
+        mbar_init(&bars->u_empty, kStateWarps);
         for (int i = 0; i < kMmaWarps; ++i) mbar_init(&bars->drain[i], 1);
         for (int i = 0; i < kVtBars; ++i) {
             mbar_init(&bars->tab_full[i], 1);
@@ -291,8 +296,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars->q_full[i], 1);
             mbar_init(&bars->q_empty[i], 2);  // by Q K^T and Q S
             mbar_init(&bars->vt_empty[i], 1);
-            mbar_init(&bars->u_full[i], 1);
-            mbar_init(&bars->u_empty[i], kStateWarps);
             mbar_init(&bars->s_full[i], kStateWarps);
             mbar_init(&bars->s_empty[i], 1);
             mbar_init(&bars->sc_full[i], 1);
@@ -422,6 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t idesc_qk = idesc_bf16_f32(kRows, C, 0);
         constexpr uint32_t idesc_v = idesc_bf16_f32(kRows, kSlice, 1);
         constexpr uint32_t idesc_kv = idesc_bf16_f32(kRows, kSlice, 1, 1);
+        constexpr uint32_t idesc_kv2 = idesc_bf16_f32(kRows, 2 * kSlice, 1, 1);
         const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
         const uint64_t k_desc = smem_desc_sw128(smem_u32(sKV), 16, 1024);
         // K with its tokens as the summed dimension (head_dim 64: the second half of M is V, and
@@ -443,24 +447,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             return wait(&bars->vt_full[w % kVtBars], (w / kVtBars) & 1);
         };
         auto update = [&]() {
-            if (u >= 2 && !wait(&bars->u_empty[u & 1], ((u >> 1) - 1) & 1)) return;
-            const uint32_t d = tmem + G::kColU + (u & 1) * kSlice;
+            if (u >= 1 && !wait(&bars->u_empty, (u - 1) & 1)) return;
+            const uint32_t d = tmem + G::kColU;
             uint64_t kd = kt_desc + (c % kRing) * (G::kStageBytes >> 4);
 #pragma unroll 1
             for (uint32_t w = u * G::kFills; w < (u + 1) * G::kFills; ++w) {
                 if (!wait(&bars->vt_full[w % kVtBars], (w / kVtBars) & 1)) return;
                 tc_fence_after();
-                uint64_t vd = vt_desc + (w & 1) * (kParts * G::kVtBytes >> 4);
-#pragma unroll 1
-                for (int part = 0; part < kParts; ++part, vd += G::kVtBytes >> 4)
+                const uint64_t vd = vt_desc + (w & 1) * (kParts * G::kVtBytes >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < kPart / 16; ++kk)
-                        tc_mma(d, kd + kk * (2048 >> 4), vd + kk * (2048 >> 4), idesc_kv,
-                               part + kk > 0 || w > u * G::kFills ? 1u : 0u);
+                for (int kk = 0; kk < kPart / 16; ++kk) {
+                    tc_mma(d, kd + kk * (2048 >> 4), vd + kk * (2048 >> 4), idesc_kv2,
+                           kk > 0 || w > u * G::kFills ? 1u : 0u);
+                    tc_mma(d + kSlice, kd + kk * (2048 >> 4),
+                           vd + (2 * G::kVtBytes >> 4) + kk * (2048 >> 4), idesc_kv, 1u);
+                }
                 kd += kPart * 128 >> 4;
                 tc_commit(&bars->vt_empty[w & 1]);
             }
-            tc_commit(&bars->u_full[u & 1]);
+            tc_commit(&bars->u_full);
             ++u;
         };
         // Q by K or by S for the tiles of a chunk (one code for both): B's descriptor, and its
@@ -856,23 +861,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         // takes a chunk's update in
         auto update = [&]() {
             const uint32_t last = u * G::kFills + G::kFills - 1;
-            ok = warp_mbar_wait_small(&bars->u_full[u & 1], (u >> 1) & 1, abort_flag) &&
+            ok = warp_mbar_wait_small(&bars->u_full, u & 1, abort_flag) &&
                  warp_mbar_wait_small(&bars->vt_full[last % kVtBars], (last / kVtBars) & 1, abort_flag);
             if (!ok) return;
             tc_fence_after();
             const float all = tables[u % kTables].all;
             const uint64_t keep = f2_twice(exp2f(all));
-            uint32_t up[32];
-            tmem_ld32(t_lane + G::kColU + (u & 1) * kSlice + half * 32, up);
-            tmem_wait_ld();
+#pragma unroll
+            for (int part = 0; part < 4; ++part) {
+                uint32_t up[16];
+                tmem_ld16(t_lane + G::kColU + (part & 1) * kSlice + half * 32 + part / 2 * 16, up);
+                tmem_wait_ld();
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    uint64_t &y = s[part / 2 * 8 + x];
+                    const uint64_t z = f2_words(up[2 * x], up[2 * x + 1]);
+                    y = part & 1 ? f2_add(y, z) : f2_fma(keep, y, z);
+                }
+            }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->u_empty[u & 1]);
+            if (lane == 0) mbar_arrive(&bars->u_empty);
             ++u;
             total += all;
-#pragma unroll
-            for (int x = 0; x < 16; ++x)
-                s[x] = f2_fma(keep, s[x], f2_words(up[2 * x], up[2 * x + 1]));
         };
         for (int k = 0;; ++k) {
             const Item it = queue_item(ctl, warp, k);
