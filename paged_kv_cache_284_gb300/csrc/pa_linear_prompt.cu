@@ -106,7 +106,6 @@ struct Geom {
     static constexpr int kHeads = kRows / C;  // of a tile
     static constexpr int kRing = C == 64 ? 3 : 2;   // chunks of K and V in shared memory
     static constexpr int kQBufs = C == 64 ? 2 : 1;  // query tiles
-    static constexpr int kOBufs = C == 64 ? 2 : 1;  // outputs in TMEM
     static constexpr int kFills = C / kPart;        // buffers of weighed V that a chunk fills
     static constexpr int kHalves = D / 64;
     static constexpr int kQHalf = kRows * 128, kKHalf = C * 128;
@@ -127,11 +126,12 @@ struct Geom {
     static constexpr int kSmemBytes = kSmemRaw > 116 * 1024 ? kSmemRaw : 116 * 1024;
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
     static_assert(kOffBar % 1024 == 0, "alignment");
-    // TMEM columns: scores [2], outputs (before | inside) [kOBufs], update (of the first part of
+    // TMEM columns: scores [2], "before" [2], "inside" [kInsides], update (64: of the first part of
     // the weighed V | of the others)
     static constexpr uint32_t kTmemCols = 512;
-    static constexpr int kColO = 2 * C, kColU = kColO + kOBufs * 2 * kSlice;
-    static_assert(kColU + 2 * kSlice <= 512, "TMEM");
+    static constexpr int kInsides = C == 64 ? 2 : 1, kUpdates = C == 64 ? 2 : 1;
+    static constexpr int kColB = 2 * C, kColI = kColB + 2 * kSlice, kColU = kColI + kInsides * kSlice;
+    static_assert(kColU + kUpdates * kSlice <= 512, "TMEM");
 };
 
 struct Bars {
@@ -455,12 +455,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait(&bars->vt_full[w % kVtBars], (w / kVtBars) & 1)) return;
                 tc_fence_after();
                 const uint64_t vd = vt_desc + (w & 1) * (kParts * G::kVtBytes >> 4);
+                const uint32_t more = w > u * G::kFills ? 1u : 0u;
+                if constexpr (G::kUpdates == 2) {
 #pragma unroll
-                for (int kk = 0; kk < kPart / 16; ++kk) {
-                    tc_mma(d, kd + kk * (2048 >> 4), vd + kk * (2048 >> 4), idesc_kv2,
-                           kk > 0 || w > u * G::kFills ? 1u : 0u);
-                    tc_mma(d + kSlice, kd + kk * (2048 >> 4),
-                           vd + (2 * G::kVtBytes >> 4) + kk * (2048 >> 4), idesc_kv, 1u);
+                    for (int kk = 0; kk < kPart / 16; ++kk) {
+                        tc_mma(d, kd + kk * (2048 >> 4), vd + kk * (2048 >> 4), idesc_kv2,
+                               kk > 0 ? 1u : more);
+                        tc_mma(d + kSlice, kd + kk * (2048 >> 4),
+                               vd + (2 * G::kVtBytes >> 4) + kk * (2048 >> 4), idesc_kv, 1u);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int part = 0; part < kParts; ++part)
+#pragma unroll
+                        for (int kk = 0; kk < kPart / 16; ++kk)
+                            tc_mma(d, kd + kk * (2048 >> 4),
+                                   vd + part * (G::kVtBytes >> 4) + kk * (2048 >> 4), idesc_kv,
+                                   part + kk > 0 ? 1u : more);
                 }
                 kd += kPart * 128 >> 4;
                 tc_commit(&bars->vt_empty[w & 1]);
@@ -470,14 +481,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // Q by K or by S for the tiles of a chunk (one code for both): B's descriptor, and its
         // steps from 16 of the summed dimension to the next and from 64 to the next; the barrier
-        // of the tile `lag` ago says that D's columns are free
+        // of two tiles ago says that D's columns are free
         auto by_q = [&](uint64_t b_desc, uint32_t step, uint32_t step64, uint32_t d, uint32_t d_next,
-                        uint32_t idesc, uint32_t lag, uint64_t *before, uint64_t *after) {
+                        uint32_t idesc, uint64_t *before, uint64_t *after) {
 #pragma unroll 1
             for (int j = 0; j < tiles; ++j, ++t) {
-                const uint32_t b = t & 1, slot = t % G::kQBufs, last = t - lag;
+                const uint32_t b = t & 1, slot = t % G::kQBufs;
                 if (!wait(&bars->q_full[slot], (t / G::kQBufs) & 1) ||
-                    (t >= lag && !wait(&before[last & 1], (last >> 1) & 1)))
+                    (t >= 2 && !wait(&before[b], ((t >> 1) - 1) & 1)))
                     return;
                 tc_fence_after();
                 const uint64_t qd = q_desc + slot * (G::kQBytes >> 4);
@@ -497,13 +508,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t b = t & 1, turn = (t >> 1) & 1;
                 // (P is there after the outputs of two tiles ago have been read)
                 if (!wait(&bars->p_full[b], turn) ||
-                    (G::kOBufs == 1 && t >= 1 && !wait(&bars->o_empty[b ^ 1], ((t - 1) >> 1) & 1)))
+                    (G::kInsides == 1 && t >= 1 && !wait(&bars->o_empty[b ^ 1], ((t - 1) >> 1) & 1)))
                     return;
                 tc_fence_after();
                 const uint64_t vd = v_desc + (c % kRing) * (G::kStageBytes >> 4);
 #pragma unroll
                 for (int kk = 0; kk < C / 16; ++kk)
-                    tc_mma_ts(tmem + G::kColO + b % G::kOBufs * (2 * kSlice) + kSlice, tmem + b * C + kk * 8,
+                    tc_mma_ts(tmem + G::kColI + b % G::kInsides * kSlice, tmem + b * C + kk * 8,
                               vd + (kk * 2048 >> 4), idesc_v, kk > 0 ? 1u : 0u);
                 tc_commit(&bars->o_full[b]);
             }
@@ -533,8 +544,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 by_q(qs ? s_desc + (s & 1) * (G::kSBytes >> 4)
                                         : k_desc + (c % kRing) * (G::kStageBytes >> 4),
                                      qs ? 2048 >> 4 : 2, qs ? 8192 >> 4 : G::kKHalf >> 4,
-                                     tmem + (qs ? G::kColO : 0), qs ? (G::kOBufs - 1) * 2 * kSlice : C,
-                                     qs ? idesc_v : idesc_qk, qs ? G::kOBufs : 2, qs ? bars->o_empty : bars->o_full,
+                                     tmem + (qs ? G::kColB : 0), qs ? kSlice : C,
+                                     qs ? idesc_v : idesc_qk, qs ? bars->o_empty : bars->o_full,
                                      qs ? bars->o_full : bars->sc_full);
                             if (qs && ok) {
                                 tc_commit(&bars->s_empty[s & 1]);
@@ -562,7 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int wq = warp & 3;
         const uint32_t grp = (warp - kFirstOut) / kGroupWarps;  // takes tiles of this parity
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(wq * 32) << 16);
-        const uint32_t sa = t_lane + grp * C, oa = t_lane + G::kColO + grp % G::kOBufs * (2 * kSlice);
+        const uint32_t sa = t_lane + grp * C, oa = t_lane + G::kColB + grp * kSlice,
+                       ia = t_lane + G::kColI + grp % G::kInsides * kSlice;
         const int tok = (wq * 32 + lane) / G::kHeads, head = (wq * 32 + lane) % G::kHeads;
         // the runs of 16 tokens that the warp's rows lie in
         const int first_run = wq * 32 / G::kHeads / 16, last_run = (wq * 32 + 31) / G::kHeads / 16;
@@ -657,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t a[16], b[16];
                         __syncwarp();
                         tmem_ld16(oa + part * 16, a);
-                        tmem_ld16(oa + kSlice + part * 16, b);
+                        tmem_ld16(ia + part * 16, b);
                         tmem_wait_ld();
                         auto sum = [&](int x) {
                             return f2_bf16x2(f2_fma(before, f2_words(a[x], a[x + 1]),
@@ -868,15 +880,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float all = tables[u % kTables].all;
             const uint64_t keep = f2_twice(exp2f(all));
 #pragma unroll
-            for (int part = 0; part < 4; ++part) {
+            for (int part = 0; part < 2 * G::kUpdates; ++part) {
+                constexpr int K = G::kUpdates;
                 uint32_t up[16];
-                tmem_ld16(t_lane + G::kColU + (part & 1) * kSlice + half * 32 + part / 2 * 16, up);
+                tmem_ld16(t_lane + G::kColU + part % K * kSlice + half * 32 + part / K * 16, up);
                 tmem_wait_ld();
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
-                    uint64_t &y = s[part / 2 * 8 + x];
+                    uint64_t &y = s[part / K * 8 + x];
                     const uint64_t z = f2_words(up[2 * x], up[2 * x + 1]);
-                    y = part & 1 ? f2_add(y, z) : f2_fma(keep, y, z);
+                    y = part % K ? f2_add(y, z) : f2_fma(keep, y, z);
                 }
             }
             tc_fence_before();
