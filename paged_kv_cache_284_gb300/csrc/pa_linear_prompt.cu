@@ -19,16 +19,18 @@
 //
 // Bound: the path between shared memory, the tensor cores' operands and L1 (128 bytes a cycle),
 // and what the schedulers issue; not HBM or the tensor pipe.  2 x 8192 tokens of 32 kv heads of
-// 128 take 181 us, where HBM alone would need 80 (95 on the 128 SMs that have a slice).  Of the
-// 5500 cycles of 128 tokens, that path carries the MMAs' operands for 2000, copies, weighed V and
+// 128 take 170 us, where HBM alone would need 80 (95 on the 128 SMs that have a slice).  Of the
+// 5200 cycles of 128 tokens, that path carries the MMAs' operands for 2000, copies, weighed V and
 // states for 1300, and the stores, a sector from each row, for 500.  Leaving a role's work out
 // saves about its share, whichever it is: no stores 20 us, no weights and a third of the updates'
 // MMAs 30, no states 20.  What that led to:
 //  - where a group is one head, chunks of 128 tokens, whose tiles fill the MMA's 128 rows: 193 us
 //    with chunks of 64 and half the rows idle (216 before the idle rows took turns)
 //  - outputs by 32 bytes of a lane: 190 us by 16
-//  - two of the three parts of the weighed V in one MMA, into columns of their own: 2 x 8192 of
-//    64 / 32 heads 200 us, 207 with an MMA to each (and one buffer for the update instead of two)
+//  - chunks of 64: two of the three parts of the weighed V in one MMA, into columns of their own
+//    (2 x 8192 of 64 / 32 heads 200 us, 207 with an MMA to each and two buffers for the update);
+//    chunks of 128 have these columns for a second "before" (173 us, 181)
+//  - nobody waits for the weighed V who needs the table only (170 us, 173)
 //  - packed fp32 arithmetic, waits that sleep on the barrier, roles dealt to the schedulers by
 //    what they issue
 //  - loops over 16 columns stay loops, and only the MMAs of 64 of a dimension are unrolled: the
@@ -441,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return ok;
         };
         auto wait_chunk = [&]() { return wait(&bars->kv_full[c % kRing], (c / kRing) & 1); };
-        // the last of a chunk's weighed V (and with it its table, and zeros behind the request)
+        // the last of a chunk's weighed V (and with it zeros behind the request)
         auto wait_weighed = [&](uint32_t u) {
             const uint32_t w = u * G::kFills + G::kFills - 1;
             return wait(&bars->vt_full[w % kVtBars], (w / kVtBars) & 1);
@@ -529,9 +531,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int i = it.c_begin; ok && i < it.c_end && wait_chunk(); ++i, ++c) {
                         if (warp == kWarpKV) update();
-                        // (V's rows behind the request are zeroed with its weighing)
+                        // (rows behind the request are zeroed with V's weighing)
                         if (warp == kWarpPV) {
-                            wait_weighed(u);
+                            if ((i + 1) * C > it.n) wait_weighed(u);
                             ++u;
                         }
                         if (ok && outputs && warp != kWarpKV) {
@@ -596,8 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t tt = t + m;
                 if ((tt & 1) == grp) {
                     const uint32_t turn = (tt >> 1) & 1, uu = u + (i - it.c_begin);
-                    const uint32_t w = uu * G::kFills + G::kFills - 1;
-                    ok = warp_mbar_wait_small(&bars->vt_full[w % kVtBars], (w / kVtBars) & 1, abort_flag) &&
+                    ok = warp_mbar_wait_small(&bars->tab_full[uu % kVtBars], (uu / kVtBars) & 1, abort_flag) &&
                          warp_mbar_wait_small(&bars->sc_full[grp], turn, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
@@ -872,9 +873,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // takes a chunk's update in
         auto update = [&]() {
-            const uint32_t last = u * G::kFills + G::kFills - 1;
             ok = warp_mbar_wait_small(&bars->u_full, u & 1, abort_flag) &&
-                 warp_mbar_wait_small(&bars->vt_full[last % kVtBars], (last / kVtBars) & 1, abort_flag);
+                 warp_mbar_wait_small(&bars->tab_full[u % kVtBars], (u / kVtBars) & 1, abort_flag);
             if (!ok) return;
             tc_fence_after();
             const float all = tables[u % kTables].all;
