@@ -171,6 +171,58 @@ def test_a_list_that_would_overflow():
     assert pk.read_device_status(clear=True) == pk.PA_DEV_BAD_METADATA
 
 
+@pytest.mark.parametrize("what", ["tokens", "table", "negative", "head", "count", "huge", "short"])
+def test_refused_large_steps(what):
+    rows = [(700, 10), (-1, 50), (1500, 97), (0, 3), (-1, 2000), (9, 40)]
+    b = Batch(rows, 16, 130, pad=5, spare=-1 if what == "short" else 8)
+    if what == "tokens":
+        b.tokens -= 6
+    elif what == "table":
+        b.q[2] = 130 * 16 - 96
+    elif what == "negative":
+        b.cached[3] = -1
+    elif what == "head":
+        b.head = -1
+    elif what == "count":
+        b.count = -1
+    elif what == "huge":
+        b.q[:] = 2**31 - 1
+    want = check(b, pk.PA_DEV_NO_BLOCKS if what == "short" else pk.PA_DEV_BAD_METADATA)
+    assert want["qsl"][-1] == 0 and np.array_equal(want["table"], b.table)
+
+
+def test_ids_outside_the_pool_in_a_large_step():
+    b = Batch([(1, 16), (1500, 20), (-1, 70)], 16, 100)
+    b.ring[b.head] = -5                    # row 0's new block
+    b.table[1, 1] = b.num_blocks           # row 1's open block
+    b.table[2, 3] = b.num_blocks + 9       # a block to be given back
+    want, t = b.expected(), b.on_gpu()
+    b.call(t)
+    torch.cuda.synchronize()
+    slots = t["slots"].cpu().numpy()
+    assert np.all(slots[:1 + 12] == -1) and np.array_equal(slots[13:], want["slots"][13:])
+    assert t["table"][0, 1].item() == 0 and t["table"][1, 1].item() == b.num_blocks
+    back = b.table[2, [0, 1, 2, 4]]
+    at = (b.head + b.count + np.arange(4)) % len(b.ring)
+    assert np.array_equal(t["ring"].cpu().numpy()[at], back)
+    assert t["state"][1].item() == b.count - 94 + 4
+    assert pk.read_device_status(clear=True) == pk.PA_DEV_BAD_BLOCK
+
+
+def test_a_list_that_would_overflow_in_a_large_step():
+    """As above, by the cluster: given back by many rows, no further than the ring goes."""
+    b = Batch([(-1, 64)] * 40 + [(1100, 0)], 16, 80, spare=0)
+    t = b.on_gpu()
+    cap, taken = len(b.ring), 69
+    t["state_in"][1] = cap - 100
+    b.call(t)
+    torch.cuda.synchronize()
+    assert t["state"].tolist() == [(b.head + taken) % cap, cap - 100 - taken + 100, 0, 0]
+    at = (b.head + cap - 100 + np.arange(100)) % cap
+    assert np.array_equal(t["ring"].cpu().numpy()[at], b.table[:25, :4].reshape(-1))
+    assert pk.read_device_status(clear=True) == pk.PA_DEV_BAD_METADATA
+
+
 @pytest.mark.parametrize("rows", [5, 3000])
 def test_in_place(rows):
     """seq_lens over cached_lens and the list's state over itself."""
