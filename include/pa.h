@@ -218,7 +218,8 @@ int pa_validate_copies(const int32_t *pairs, int32_t num_pairs, int32_t num_bloc
  * The free list is a ring of block ids: free_state holds its head and its count (int32 [4],
  * two more words are the library's); blocks are taken at the head and given back behind the
  * tail.  free_state_out (int32 [4]) receives head and count after the step and, third, how
- * many blocks were missing (0 for a step that was made); it may be free_state itself.
+ * many blocks were missing (0 for a step that was made, and for bad metadata); it may be
+ * free_state itself.
  * Every block is in the list or in one row's table, once.
  *
  * All or nothing: with too few blocks in the list (PA_DEV_NO_BLOCKS), more tokens than

@@ -132,7 +132,7 @@ def build_step(query_lens, cached, table, ring, head, count, num_tokens, block_s
     bad = any(c < 0 or c + n > width * block_size for n, c in lens) or \
         sum(n for n, _ in lens) > num_tokens or not (0 <= head < cap and 0 <= count <= cap)
     need = 0 if bad else sum(up(c + n) - up(c) for n, c in lens)
-    missing = max(0, need - count)
+    missing = 0 if bad else max(0, need - count)  # (a bad count counts nothing)
     slots, positions = np.full(num_tokens, -1, np.int64), np.zeros(num_tokens, np.int32)
     qsl, ctx, seq, given, taken = [0], [], [], [], 0
     for b in range(B):
