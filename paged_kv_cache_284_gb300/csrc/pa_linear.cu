@@ -68,7 +68,11 @@ __device__ __forceinline__ void step_job(const LinearParams &p) {
     __shared__ float s_keep[kTokens];
     __shared__ __align__(16) float s_part[2][kWarps][kHeadBatch][COLS];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int slice = blockIdx.x % kSlices, job = blockIdx.x / kSlices;
+    // From the last request to the first: batches commonly have their single tokens first, and
+    // what takes longer had better not start last (192 requests of 1 token and 32 of 5 in this
+    // order 46.7 us, from the first 49.5; 32 of 5 and 192 of 1 50.1 and 46.6).
+    const int index = static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x);
+    const int slice = index % kSlices, job = index / kSlices;
     const int b = job / p.num_kv_heads, h = job - b * p.num_kv_heads;
     const int col = (lane % G::kLanes) * 4, row0 = (warp * G::kSub + lane / G::kLanes) * R;
     const int t0 = __ldg(p.qsl + b), n = __ldg(p.qsl + b + 1) - t0;
