@@ -348,7 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         auto load_kv = [&](const Item &it, int i) {
             const int st = c % kRing;
-            if (ok && c >= kRing) ok = warp_mbar_wait_small(&bars->kv_empty[st], (c / kRing - 1) & 1, abort_flag);
+            if (ok && c >= kRing)
+                ok = warp_mbar_wait_small(&bars->kv_empty[st], (c / kRing - 1) & 1, abort_flag);
             // test hook: stop after the first chunk, as if a wait had run out
             if (p.test_stall && blockIdx.x == 0 && c == 1) ok = false;
             if (!ok) return;
@@ -420,10 +421,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp < kFirstOut || warp == kWarpPV) {
         // ============================ MMAs ============================
         // A thread of four warps each, so that none stands behind another's wait or issue (an MMA
-        // takes its thread 120 to 260 cycles, and a chunk has 32): the scores, the updates, Q S,
-        // and P V.  (One thread, not a warp with an elected
-        // lane's predicate: operands in a warp's uniform registers are no longer its own when
-        // a wait has taken the lanes apart.  A commit was seen to arrive twice, and worse.)
+        // takes its thread 100 to 200 cycles, four at a time): the scores, the updates, Q S, and
+        // P V.  (One thread, not a warp with an elected lane's predicate: operands in a warp's
+        // uniform registers are no longer its own when a wait has taken the lanes apart.  A commit
+        // was seen to arrive twice, and worse.)
         constexpr uint32_t idesc_qk = idesc_bf16_f32(kRows, C, 0);
         constexpr uint32_t idesc_v = idesc_bf16_f32(kRows, kSlice, 1);
         constexpr uint32_t idesc_kv = idesc_bf16_f32(kRows, kSlice, 1, 1);
@@ -714,7 +715,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // the chunk is here, and the MMAs of two fills ago have read theirs
                     ok = warp_mbar_wait_small(&bars->kv_full[st], (u / kRing) & 1, abort_flag) &&
                          warp_mbar_wait_small(&bars->tab_full[u % kVtBars], (u / kVtBars) & 1, abort_flag) &&
-                         (w < 2 || warp_mbar_wait_small(&bars->vt_empty[w & 1], ((w >> 1) - 1) & 1, abort_flag));
+                         (w < 2 ||
+                          warp_mbar_wait_small(&bars->vt_empty[w & 1], ((w >> 1) - 1) & 1, abort_flag));
                     if (!ok) break;
                     const uint32_t half = w % G::kFills * (kPart * 128);
                     uint8_t *k_tile = sKV + st * G::kStageBytes + half, *v = k_tile + G::kKBytes;
