@@ -365,8 +365,9 @@ struct LinearParams {
 };
 // Requests of up to this many tokens take the recurrent form, whose time grows with a request's
 // tokens; the chunks' is that of 64 from the first on.  head_dim 128, 32 / 8 heads, recurrent and
-// in chunks: one request of 8 tokens 10.7 and 10.5 us, of 16 18.9 and 10.7; 64 requests of 8
-// 36 and 47 us, of 10 46 and 47, of 16 68 and 48; 128 of 8 in head_dim 64 15 and 13.
+// in chunks: one request of 8 tokens 10.4 and 9.8 us, of 16 18.3 and 9.9; 64 requests of 8
+// 37 and 47 us, of 10 47 and 47, of 16 69 and 49 (the chunks on every SM); 128 of 8 in head_dim
+// 64 15 and 13.
 constexpr int kLinearStepRows = 8;
 // Rows (tokens x heads) of the prompt kernel's query tiles: chunks of 64 tokens and two heads of
 // a group, or of 128 tokens where a group is one head.

@@ -1015,11 +1015,14 @@ int launch(const LinearParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
     // Which requests are long is known on the GPU only, so the two forms' SMs are shared out by
     // what T tokens and B states would take: reading and writing a state takes an SM about as
     // long as 24 tokens of a prompt (head_dim 128, four heads a group: 28 us and 1.1 us for 8 kv
-    // heads).  8 x 512 tokens among 224 requests of 1 and 5 take 83.5 us, 89 with a prompt CTA on
-    // every SM; 256 single tokens, without any prompt, 47.6 and 60.
+    // heads).  256 single tokens, without any prompt: 47.6 us, 60 with a prompt CTA on every SM.
+    // Above kLinearStepRows tokens on average some request is long, and all may be, of one short
+    // chunk each, which takes as long as a full one: tokens count four times then.  8 x 512 tokens
+    // among 224 requests of 1 and 5 take 75.7 / 79.2 / 80.5 us with tokens counted once, four and
+    // eight times, 64 requests of 16 96 / 58 / 49, 128 of 32 137 / 96 / 91.
     constexpr int64_t kStateTokens = 24;
-    const int share = static_cast<int>(sms * static_cast<int64_t>(p.num_tokens) /
-                                       (p.num_tokens + kStateTokens * p.num_seqs));
+    const int64_t work = p.num_tokens * (p.num_tokens > int64_t{kLinearStepRows} * p.num_seqs ? 4 : 1);
+    const int share = static_cast<int>(sms * work / (work + kStateTokens * p.num_seqs));
     const int clusters = static_cast<int>(std::min<int64_t>(items, std::max(1, share / size)));
     return size > 1 ? launch<D, C, true>(p, tq, tk, tv, clusters, size, s)
                     : launch<D, C, false>(p, tq, tk, tv, clusters, 1, s);
