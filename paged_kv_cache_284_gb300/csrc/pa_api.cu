@@ -1263,8 +1263,10 @@ int pa_cross_attention(const void *q, const pa_kv_desc *kv, const int32_t *block
                        int32_t num_q_heads, float scale, void *out, float *lse, void *workspace,
                        size_t workspace_bytes, void *stream) {
     g_err[0] = 0;
-    // the windowed kernels without a window: each row stands behind its request's last key
-    const WindowArgs all{static_cast<int32_t>(kMaxWindowKeys), 0};
+    // the windowed kernels without a window: each row stands behind its request's last key, the
+    // rows of a tile or a piece (at most kLongRows) one behind the other, so at key
+    // kMaxWindowKeys + kLongRows - 1 at most; a window of one more shows that row key 0 too
+    const WindowArgs all{static_cast<int32_t>(kMaxWindowKeys) + kLongRows, 0};
     const int rc = check_window(all.window, all.sinks, scale);
     if (rc != PA_OK) return rc;
     if (num_q_tokens > kMaxWindowKeys)

@@ -124,11 +124,12 @@ __device__ __forceinline__ int chunk_row_from(const ShortParams &p, const ShortI
     return (blk * p.num_kv_heads + h) * p.block_size + key0 % p.block_size;
 }
 
-// The request's context.  Cross attention (a windowed step without a context array) has every
-// row behind the request's keys, none of which is hidden.
+// The request's context, to which the piece's first row is added.  Cross attention (a windowed
+// step without a context array) has each piece's rows right behind the request's keys, none of
+// which is hidden.
 template <bool WIN>
 __device__ __forceinline__ int context_of(const ShortParams &p, const ShortItem &item) {
-    if (WIN && !p.ctx) return item.seq_len;
+    if (WIN && !p.ctx) return item.seq_len - item.q_begin;
     return __ldg(p.ctx + item.b);
 }
 
