@@ -228,7 +228,9 @@ int pa_validate_copies(const int32_t *pairs, int32_t num_pairs, int32_t num_bloc
  * and makes a step without tokens: every query start 0, every slot -1, context and seq_lens
  * the cached lengths.
  * A table entry outside the pool that a token's slot needs gives slot -1 and
- * PA_DEV_BAD_BLOCK, such an id in the list too (the table gets it clamped).
+ * PA_DEV_BAD_BLOCK.  So does such an id taken from the list; the table gets it clamped, which
+ * is some other owner's block, and the head after the step is -1 - head: calls are refused
+ * (PA_DEV_BAD_METADATA) until the caller has put the entry, the list and its head right.
  * query_lens, cached_lens and free_state may not overlap any output but those named.
  * num_seqs is at most 8192; max_blocks_per_seq * block_size at most 2^30.
  */

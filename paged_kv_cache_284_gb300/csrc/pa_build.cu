@@ -19,6 +19,7 @@
 // call may change in place (lengths, the list's state).  4500 tokens of 256 rows, 12 of them
 // done: 7.9 us, 9.0 as one kernel of 8 CTAs; 140000 tokens of 1024 rows, 64 done: 10.3 us, 32.6
 // so.  Decode rows: 300 take 3.9 us whole and 5.3 split, 1000 8.8 and 8.7, 2000 11.7 and 9.7.
+// (The look at each id that is taken came after these: 0.2 us whole, 0.3 and 0.9 split.)
 #include <algorithm>
 
 #include "pa_internal.cuh"
@@ -102,6 +103,7 @@ __global__ void __launch_bounds__(kThreads) build_step_kernel(const BuildParams 
     extern __shared__ int row_info[];
     __shared__ Sums warp_sums[kWarps];
     __shared__ int warp_given[kWarps];
+    __shared__ int list_is_bad;  // an id that is none of the pool's was taken from it
     int *start = row_info, *ctx_of = row_info + p.num_seqs, *block_of = ctx_of + p.num_seqs,
         *done_rows = block_of + p.num_seqs, *gives = done_rows + p.num_seqs;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -114,6 +116,7 @@ __global__ void __launch_bounds__(kThreads) build_step_kernel(const BuildParams 
         pdl_trigger();
     }
     const int head = p.free_state[0], count = p.free_state[1];
+    if (tid == 0) list_is_bad = 0;
 
     // 1. sums over the rows: thread t has rows t * each ..
     const int each = (p.num_seqs + kThreads - 1) / kThreads;
@@ -191,7 +194,10 @@ __global__ void __launch_bounds__(kThreads) build_step_kernel(const BuildParams 
                 blk = p.free_blocks[at];
             }
             const bool ok = blk >= 0 && blk < p.num_blocks;
-            if (!ok) flag_status(p.status, PA_DEV_BAD_BLOCK);
+            if (!ok) {
+                flag_status(p.status, PA_DEV_BAD_BLOCK);
+                if (col >= have) list_is_bad = 1;
+            }
             if (col >= have && pos % p.block_size == 0)
                 *entry = ok ? blk : min(max(blk, 0), p.num_blocks - 1);
             slot = ok ? static_cast<int64_t>(blk) * p.block_size + pos % p.block_size : -1;
@@ -205,7 +211,18 @@ __global__ void __launch_bounds__(kThreads) build_step_kernel(const BuildParams 
     // was free, so nothing taken above is overwritten.
     if (PART == kTokens) return;
     int given = 0;
-    if (PART == kRows) cluster_wait();  // every CTA runs: its shared memory may be written
+    if (PART == kRows) {
+        // (the tokens' grid looks at the ids that it takes, but has nobody to tell)
+        bool bad_id = false;
+#pragma unroll 4
+        for (int64_t i = tid; rank == 0 && i < taken; i += kThreads) {
+            const int64_t at = head + i;
+            const int blk = p.free_blocks[at >= p.capacity ? at - p.capacity : at];
+            bad_id |= blk < 0 || blk >= p.num_blocks;
+        }
+        if (bad_id) list_is_bad = 1;
+        cluster_wait();  // every CTA runs: its shared memory may be written
+    }
     if (total.done > 0 && good) {
         // entries of a row, one warp of the cluster each
         for (int d = rank * kWarps + warp; d < total.done; d += size * kWarps) {
@@ -277,11 +294,10 @@ __global__ void __launch_bounds__(kThreads) build_step_kernel(const BuildParams 
     if (PART == kRows) {
         pdl_wait();
         pdl_trigger();
-    }
-    if (PART == kRows)
         cluster_sync();
-    else
+    } else {
         __syncthreads();
+    }
     if (rank != 0) return;
     for (int b = b0; b < b1; ++b) {
         const Row r = load_row(p, b);
@@ -295,7 +311,9 @@ __global__ void __launch_bounds__(kThreads) build_step_kernel(const BuildParams 
         p.query_start_loc[p.num_seqs] = tokens;
         int64_t h = static_cast<int64_t>(head) + taken;
         if (h >= p.capacity) h -= p.capacity;
-        p.free_state_out[0] = good ? static_cast<int>(h) : head;
+        // The row's table has a block of another row's or of the list's from now on, and would
+        // write there with its next token: a head out of range has later calls refused.
+        p.free_state_out[0] = !good ? head : static_cast<int>(list_is_bad ? -1 - h : h);
         p.free_state_out[1] = count - taken + given;
         p.free_state_out[2] = static_cast<int>(min(missing, 0x7fffffffll));
         p.free_state_out[3] = 0;
