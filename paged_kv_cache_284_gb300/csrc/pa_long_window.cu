@@ -24,11 +24,11 @@
 //    queue in shared memory; the group that has an item's last tile writes its
 //    output while the other begins the next item;
 //  * K and V rings are three tiles deep, and Q K^T and P V are issued by two
-//    warps (one elected lane each): a 128 x 128 x 128 group of MMAs takes
+//    warps (an elected lane of each): a 128 x 128 x 128 group of MMAs takes
 //    700-800 cycles by itself and 512 beside the other warp's; one issuing thread
 //    for both was slower (616 us against 487 on the case below).
 // Two chunks of 4096 tokens, window 4096 + 16 sinks, 32 q / 8 kv heads, d = 128, 552
-// GFLOP of visible pairs: 488 us, 1130 TFLOP/s, 0.58 of the measured bf16 rate (565 us
+// GFLOP of visible pairs: 473 us, 1167 TFLOP/s, 0.61 of the measured bf16 rate (565 us
 // in the plain kernel's form).  Bound: the chain of a key tile (scores, maximum,
 // exponentials, P V) at ~1900 cycles for two tiles in flight, against 1024 of MMA;
 // a third S tile with P written over S left too few registers and columns to win.
@@ -341,43 +341,19 @@ __device__ void produce(const LongParams &p, const Queue &q, int n_items, const 
     }
 }
 
-// MMA and commit issued by the elected lane of a warp whose lanes all run the
-// surrounding code: operands stay in uniform registers.  (Inside a branch of
-// one lane each MMA took ~80 cycles to issue, 645 for a tile's eight.)
-__device__ __forceinline__ uint32_t elect_one() {
+// True for one lane of the warp, whose lanes all call this together.  That lane issues the MMAs:
+// it waits, issues and commits in a branch of its own, and the others wait for it at the vote
+// behind an item.  So no lane but the issuing one runs between a barrier and the MMAs, and no
+// operand depends on lanes having met again after each has polled a barrier for itself (as they
+// had to when all lanes ran the loop and the MMAs were predicated; that took 488 us on the case
+// above).  With `lane == 0` in the place of the election it takes 547: the compiler then looks for
+// the operands of more than one lane.
+__device__ __forceinline__ bool elect_one() {
     uint32_t e;
     asm volatile(
         "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(e));
-    return e;
-}
-__device__ __forceinline__ void mma_ss(uint32_t elected, uint32_t d_tmem, uint64_t adesc,
-                                       uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 e, %5, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected)
-        : "memory");
-}
-__device__ __forceinline__ void mma_ts(uint32_t elected, uint32_t d_tmem, uint32_t a_tmem,
-                                       uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 e, %5, 0;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected)
-        : "memory");
-}
-__device__ __forceinline__ void commit(uint32_t elected, uint64_t *bar) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
-            smem_u32(bar)),
-        "r"(elected)
-        : "memory");
+    return e != 0;
 }
 
 }  // namespace
@@ -479,89 +455,88 @@ __global__ void __launch_bounds__(32 * kLongWarps, 1)
         constexpr uint32_t idesc_qk = idesc_bf16_f32(kLongRows, kLongKeys, 0);
         const uint64_t q_desc = smem_desc_sw128(smem_u32(sQ), 16, 1024);
         const uint64_t k_desc = smem_desc_sw128(smem_u32(sK), 16, 1024);
-        const uint32_t elected = elect_one();
+        const bool mine = elect_one();
         uint32_t t = 0, k_item = 0;
         bool ok = true;
         for (; ok; ++k_item) {
             const int nt = __shfl_sync(0xffffffffu, queue_item(queue, warp, k_item).nt, 0);
             if (nt == 0) break;
-            // Every lane polls for itself, with no broadcast between a barrier and the
-            // MMAs.  One lane may find the barrier complete and another that the CTA has
-            // given up, so the warp votes: all go on or none does, or they would wait for
-            // each other at the next point where a warp meets.
-            const bool q_here = mbar_wait(&bars->q_full, k_item & 1, abort_flag);
-            int j = 0;
-            for (; j < nt; ++j) {
-                const uint32_t tt = t + j;
-                const int ks = tt % kRing;
-                const int sb = tt & 1;
-                const bool here =
-                    q_here && mbar_wait(&bars->k_full[ks], (tt / kRing) & 1, abort_flag) &&
-                    (tt < 2 || mbar_wait(&bars->s_free[sb], ((tt - 2) >> 1) & 1, abort_flag));
-                ok = __all_sync(0xffffffffu, here);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t kd = k_desc + static_cast<uint32_t>(ks * (G::kKVBytes >> 4));
+            if (mine) {
+                ok = mbar_wait(&bars->q_full, k_item & 1, abort_flag);
+                int j = 0;
+                for (; ok && j < nt; ++j) {
+                    const uint32_t tt = t + j;
+                    const int ks = tt % kRing;
+                    const int sb = tt & 1;
+                    ok = mbar_wait(&bars->k_full[ks], (tt / kRing) & 1, abort_flag) &&
+                         (tt < 2 || mbar_wait(&bars->s_free[sb], ((tt - 2) >> 1) & 1, abort_flag));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t kd = k_desc + static_cast<uint32_t>(ks * (G::kKVBytes >> 4));
 #pragma unroll
-                for (int kk = 0; kk < KS; ++kk) {
-                    constexpr int kHalf16 = G::kHalfBytes >> 4;
-                    const int off = (kk >> 2) * kHalf16 + (kk & 3) * 2;  // 16-byte units
-                    mma_ss(elected, tmem + sb * kLongKeys, q_desc + off, kd + off, idesc_qk,
-                           kk > 0 ? 1u : 0u);
+                    for (int kk = 0; kk < KS; ++kk) {
+                        constexpr int kHalf16 = G::kHalfBytes >> 4;
+                        const int off = (kk >> 2) * kHalf16 + (kk & 3) * 2;  // 16-byte units
+                        tc_mma(tmem + sb * kLongKeys, q_desc + off, kd + off, idesc_qk,
+                               kk > 0 ? 1u : 0u);
+                    }
+                    tc_commit(&bars->s_full[sb]);
+                    tc_commit(&bars->k_empty[ks]);
+                    if (j == nt - 1) tc_commit(&bars->q_empty);
                 }
-                commit(elected, &bars->s_full[sb]);
-                commit(elected, &bars->k_empty[ks]);
-                if (j == nt - 1) commit(elected, &bars->q_empty);
+                if (p.tile_counter) atomicAdd(p.tile_counter, static_cast<unsigned long long>(j));
             }
-            if (p.tile_counter && lane == 0)
-                atomicAdd(p.tile_counter, static_cast<unsigned long long>(j));
+            ok = __all_sync(0xffffffffu, ok);
             t += nt;
         }
-        if (__any_sync(0xffffffffu, !ok || *abort_flag)) {
+        if (mine && (!ok || *abort_flag)) {
             // let every MMA already issued finish before TMEM is released
-            commit(elected, &bars->drain);
+            tc_commit(&bars->drain);
             mbar_drain(&bars->drain, 0);
         }
+        __syncwarp();
     } else if (warp == kWarpPV) {
         // ============================ P V issuer ============================
         // A tile's P V waits for its P, its V tile and, at the start of an item,
         // for the previous item's epilogue to read O.
         constexpr uint32_t idesc_pv = idesc_bf16_f32(kLongRows, D, 1);
         const uint64_t v_desc = smem_desc_sw128(smem_u32(sV), G::kHalfBytes, 1024);
-        const uint32_t elected = elect_one();
+        const bool mine = elect_one();
         uint32_t t = 0, k_item = 0;
         bool ok = true;
         for (; ok; ++k_item) {
             const int nt = __shfl_sync(0xffffffffu, queue_item(queue, warp, k_item).nt, 0);
             if (nt == 0) break;
-            for (int j = 0; j < nt; ++j) {
-                const uint32_t tt = t + j;
-                const int sb = tt & 1;
-                const int vs = tt % kRing;
-                const bool here =
-                    (j > 0 || k_item == 0 ||
-                     mbar_wait(&bars->o_free, (k_item - 1) & 1, abort_flag)) &&
-                    mbar_wait(&bars->v_full[vs], (tt / kRing) & 1, abort_flag) &&
-                    mbar_wait(&bars->p_full[sb], (tt >> 1) & 1, abort_flag);
-                ok = __all_sync(0xffffffffu, here);  // (see the other issuer)
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t vd = v_desc + static_cast<uint32_t>(vs * (G::kKVBytes >> 4));
-                // P (bf16) of this tile: row r in TMEM lane r, key k in column k / 2
-                const uint32_t pcol = tmem + G::kColP + sb * (kLongKeys / 2);
+            if (mine) {
+                for (int j = 0; j < nt; ++j) {
+                    const uint32_t tt = t + j;
+                    const int sb = tt & 1;
+                    const int vs = tt % kRing;
+                    ok = (j > 0 || k_item == 0 ||
+                          mbar_wait(&bars->o_free, (k_item - 1) & 1, abort_flag)) &&
+                         mbar_wait(&bars->v_full[vs], (tt / kRing) & 1, abort_flag) &&
+                         mbar_wait(&bars->p_full[sb], (tt >> 1) & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t vd = v_desc + static_cast<uint32_t>(vs * (G::kKVBytes >> 4));
+                    // P (bf16) of this tile: row r in TMEM lane r, key k in column k / 2
+                    const uint32_t pcol = tmem + G::kColP + sb * (kLongKeys / 2);
 #pragma unroll
-                for (int kk = 0; kk < kLongKeys / 16; ++kk)
-                    mma_ts(elected, tmem + G::kColO, pcol + kk * 8, vd + kk * (2048 >> 4), idesc_pv,
-                           (j > 0 || kk > 0) ? 1u : 0u);
-                commit(elected, &bars->pv_done[sb]);
-                commit(elected, &bars->v_empty[vs]);
+                    for (int kk = 0; kk < kLongKeys / 16; ++kk)
+                        tc_mma_ts(tmem + G::kColO, pcol + kk * 8, vd + kk * (2048 >> 4), idesc_pv,
+                                  (j > 0 || kk > 0) ? 1u : 0u);
+                    tc_commit(&bars->pv_done[sb]);
+                    tc_commit(&bars->v_empty[vs]);
+                }
             }
+            ok = __all_sync(0xffffffffu, ok);
             t += nt;
         }
-        if (__any_sync(0xffffffffu, !ok || *abort_flag)) {
-            commit(elected, &bars->drain_pv);
+        if (mine && (!ok || *abort_flag)) {
+            tc_commit(&bars->drain_pv);
             mbar_drain(&bars->drain_pv, 0);
         }
+        __syncwarp();
     } else {
         // ============================ softmax + epilogue ============================
         const int wq = warp & 3;  // TMEM lane quarter of this warp
