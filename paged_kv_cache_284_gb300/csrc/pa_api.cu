@@ -530,6 +530,7 @@ int check_new_rows(const NewRows &nr) {
 // then never overflows), and most axes of a rotary embedding.
 constexpr int64_t kMaxWindowKeys = static_cast<int64_t>(1) << 30;
 constexpr int kMaxRopeAxes = 8;
+constexpr int kMaxLinearTokens = 1 << 30;
 
 int check_window(int32_t window, int32_t num_sinks, float scale) {
     if (window < 1) return fail(PA_ERR_INVALID_ARG, "window %d: need at least 1", window);
@@ -1366,6 +1367,9 @@ int pa_linear_attention(const void *q, int64_t q_stride, const void *k, int64_t 
     if (!std::isfinite(desc->scale)) return fail(PA_ERR_INVALID_ARG, "scale is not finite");
     if (static_cast<int64_t>(num_seqs) * hkv > (static_cast<int64_t>(1) << 28))
         return fail(PA_ERR_UNSUPPORTED, "more than 2^28 states in a step");
+    // (places of a chunk behind the last token are still 32-bit)
+    if (num_tokens > kMaxLinearTokens)
+        return fail(PA_ERR_UNSUPPORTED, "more than 2^30 tokens in a step");
     if (num_seqs == 0) return PA_OK;
     if (!query_start_loc || !state_in || !state_out || !desc->state || !log_decay)
         return fail(PA_ERR_INVALID_ARG, "state, decay or metadata pointer is NULL");

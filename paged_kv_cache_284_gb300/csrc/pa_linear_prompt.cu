@@ -1042,14 +1042,15 @@ int launch(const LinearParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
 template <int D, int C>
 int launch(const LinearParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
            const CUtensorMap &tv, int sms, cudaStream_t s) {
-    // the most requests that can be long, and their items
-    const int64_t longs = std::min<int64_t>(p.num_seqs, p.num_tokens / (p.max_rows + 1));
+    // the most requests that can be long, and their items (at least one of each: the caller has
+    // more than max_rows tokens and a request)
+    const int64_t tokens = p.num_tokens;
+    const int64_t longs = std::min<int64_t>(p.num_seqs, tokens / (p.max_rows + 1));
     const int64_t items = longs * p.num_kv_heads * (D / kSlice);
-    if (items == 0) return PA_OK;
     // the largest cluster whose ranks have two chunks and whose items run at once (152 SMs hold 76
     // clusters of 2, 36 of 4 and 15 of 8: a ninth of the SMs belongs to none of 8)
     int size = 1;
-    while (size < kDirectMaxCluster && 2 * size * 2 * C <= p.num_tokens &&
+    while (size < kDirectMaxCluster && 2 * size * 2 * C <= tokens &&
            2 * size * items <= (size < 4 ? sms * 18 / 19 : sms * 15 / 19))
         size *= 2;
     // Which requests are long is known on the GPU only, so the two forms' SMs are shared out by
@@ -1061,7 +1062,7 @@ int launch(const LinearParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
     // among 224 requests of 1 and 5 take 75.7 / 79.2 / 80.5 us with tokens counted once, four and
     // eight times, 64 requests of 16 96 / 58 / 49, 128 of 32 137 / 96 / 91.
     constexpr int64_t kStateTokens = 24;
-    const int64_t work = p.num_tokens * (p.num_tokens > int64_t{kLinearStepRows} * p.num_seqs ? 4 : 1);
+    const int64_t work = tokens > int64_t{kLinearStepRows} * p.num_seqs ? 4 * tokens : tokens;
     const int share = static_cast<int>(sms * work / (work + kStateTokens * p.num_seqs));
     const int clusters = static_cast<int>(std::min<int64_t>(items, std::max(1, share / size)));
     return size > 1 ? launch<D, C, true>(p, tq, tk, tv, clusters, size, s)
