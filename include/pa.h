@@ -406,7 +406,8 @@ int pa_cross_attention(const void *q, const pa_kv_desc *kv, const int32_t *block
  *   out           bf16 [num_tokens][num_q_heads][head_dim], 16-B aligned; rows that belong to
  *                 no request are left untouched; may not overlap an input
  * States and all sums are fp32.  An infinity or a NaN in a request's q, k or v reaches its own
- * state and outputs only, those up to 127 tokens earlier among them.  head_dim 64 or 128;
+ * state and its outputs from that token on (an infinity in v may reach them as a NaN), one in v
+ * those of its column; earlier outputs and other requests' never.  head_dim 64 or 128;
  * num_q_heads a multiple of num_kv_heads, at most 128 heads to a group; num_tokens at most
  * 2^30.  A decreasing query start, or one past num_tokens, skips the request and flags
  * PA_DEV_BAD_METADATA.

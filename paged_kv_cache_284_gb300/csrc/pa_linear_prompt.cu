@@ -31,13 +31,15 @@
 //  - chunks of 64: two of the three parts of the weighed V in one MMA, into columns of their own
 //    (2 x 8192 of 64 / 32 heads 200 us, 207 with an MMA to each and two buffers for the update);
 //    chunks of 128 have these columns for a second "before" (173 us, 181)
-//  - nobody waits for the weighed V who needs the table only (170 us, 173)
+//  - the warps of the states and outputs wait for the table, not for the weighed V (P V does: V is
+//    weighed by then, and holds nothing any more that is no number)
 //  - packed fp32 arithmetic, waits that sleep on the barrier, roles dealt to the schedulers by
 //    what they issue
 //  - loops over 16 columns stay loops, and only the MMAs of 64 of a dimension are unrolled: the
 //    code of all roles has to fit the instruction cache (109 KB of it: 349 us when 72 KB took
-//    215), and a burst of one thread's MMAs holds up the others' (all unrolled: 20 % more).  An MMA
-//    of 128 x 64 x 16 takes the pipe 47 cycles, from one thread or from four
+//    215; the weighing by two rows of a lane instead of one: 172 us, and 229 instead of 209 with
+//    64 / 32 heads), and a burst of one thread's MMAs holds up the others' (all unrolled: 20 %
+//    more).  An MMA of 128 x 64 x 16 takes the pipe 47 cycles, from one thread or from four
 //  - without a cluster a kernel of its own, that has no exchange: 8 us less
 //  - left out: more chunks of K and V or more query tiles in shared memory, K and V given back one
 //    by one, eight warps for the weights, two threads for the updates: none gained
@@ -82,8 +84,8 @@ constexpr float kLeastLog = -150.f;
 // chunk; between[r][x], the sum of the runs x .. r - 1 (0 from x = r on); the chunk's sum.  Only
 // tokens of one run meet in a difference of sums, which keeps the digits that 16 logarithms leave:
 // in sums from the chunk's start a cleared token (-150) takes digits from all weights behind it,
-// 64 of them up to 0.002 of a weight (this form is 1.8 % slower for 2 x 8192 tokens of 32 heads,
-// 3.5 % for 64 / 32 heads, 0 to 0.5 % for the other cases).
+// 64 of them up to 0.002 of a weight (2 x 8192 tokens of 32 heads took 168.5 us so and take 169,
+// 64 / 32 heads 203 and 209).
 template <int C>
 struct alignas(16) Table {
     static constexpr int kRuns = C / 16;
@@ -100,6 +102,12 @@ __device__ __forceinline__ uint32_t f2_bf16x2(uint64_t v) {
     float lo, hi;
     f2_unpack(v, lo, hi);
     return pack_bf16x2(lo, hi);
+}
+
+// Two of bf16, with 0 for what is no finite number.
+__device__ __forceinline__ uint32_t finite2(uint32_t v) {
+    return ((v & 0x7F80u) == 0x7F80u ? 0u : v & 0xFFFFu) |
+           ((v & 0x7F800000u) == 0x7F800000u ? 0u : v & 0xFFFF0000u);
 }
 
 // 32 aligned bytes: a whole sector from each lane
@@ -166,7 +174,8 @@ static_assert(sizeof(Item) == 48, "queue entry");
 
 struct Ctl {
     int abort, published, read[kWarps];
-    uint32_t tmem, pad;
+    int odd;      // V held an infinity or a NaN
+    uint32_t tmem;
     Item items[kQueue];
     float decay;  // of this rank's run, log2 (read by the cluster)
 };
@@ -247,6 +256,52 @@ __device__ Item find_item(const LinearParams &p, const int *count, int k, int ra
     return it;
 }
 
+// Outputs behind an infinity or a NaN of V in the same chunk, by all warps of a CTA that has seen
+// one, when all its outputs are written.  P has zeros for earlier tokens, which P V would turn into
+// NaN; so V's element is 0 there, and here its column's outputs become NaN from its token on to the
+// end of the chunk.  (Later chunks have it from the state, whose update meets V as it is.)  At the
+// kernel's end it costs the roles neither registers nor instruction cache: among the outputs, or as
+// a function that is called, it cost 6 to 13 %.
+template <int D, int C>
+__device__ __forceinline__ void late_columns(const LinearParams &p, int rank, int size) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per = p.num_kv_heads * (D / kSlice);
+    // this cluster's items, as find_item has them
+    int64_t longs = 0, idx = blockIdx.x / size;  // long requests before b, next item
+#pragma unroll 1
+    for (int b = 0; b < p.num_seqs; ++b) {
+        int t0;
+        const int n = long_tokens(p, b, t0);
+        if (n == 0) continue;
+        const int chunks = (n + C - 1) / C, run = (chunks + size - 1) / size;
+        ++longs;
+#pragma unroll 1
+        for (; idx < longs * per; idx += gridDim.x / size) {
+            const int in = static_cast<int>(idx % per), h = in / (D / kSlice);
+            const int col = in % (D / kSlice) * kSlice + 2 * lane;  // and the next one
+#pragma unroll 1
+            for (int i = rank * run + warp; i < min(chunks, (rank + 1) * run); i += kWarps) {
+                bool lo = false, hi = false;
+#pragma unroll 1
+                for (int t = i * C; t < min(n, (i + 1) * C); ++t) {
+                    const uint32_t v = *reinterpret_cast<const uint32_t *>(
+                        p.v + (t0 + t) * p.v_stride + h * D + col);
+                    lo |= (v & 0x7F80u) == 0x7F80u;
+                    hi |= (v & 0x7F800000u) == 0x7F800000u;
+                    if (!lo && !hi) continue;
+                    unsigned short *out = reinterpret_cast<unsigned short *>(p.out) +
+                        (static_cast<int64_t>(t0 + t) * p.num_q_heads + h * p.group) * D + col;
+#pragma unroll 1
+                    for (int j = 0; j < p.group; ++j, out += D) {
+                        if (lo) out[0] = 0x7FFF;
+                        if (hi) out[1] = 0x7FFF;
+                    }
+                }
+            }
+        }
+    }
+}
+
 // Any other warp, all lanes: item k.
 __device__ __forceinline__ Item queue_item(Ctl *ctl, int warp, int k) {
     const int lane = threadIdx.x & 31;
@@ -313,6 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&bars->o_empty[i], kGroupWarps);
         }
         ctl->abort = 0;
+        ctl->odd = 0;
         ctl->published = 0;
         for (int w = 0; w < kWarps; ++w) ctl->read[w] = 0;
         fence_mbar_init();
@@ -539,9 +595,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int i = it.c_begin; ok && i < it.c_end && wait_chunk(); ++i, ++c) {
                         if (warp == kWarpKV) update();
-                        // (rows behind the request are zeroed with V's weighing)
+                        // (V's weighing zeroes rows behind the request, and what is no number)
                         if (warp == kWarpPV) {
-                            if ((i + 1) * C > it.n) wait_weighed(u);
+                            wait_weighed(u);
                             ++u;
                         }
                         if (ok && outputs && warp != kWarpKV) {
@@ -735,8 +791,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint8_t *vt = sVt + (w & 1) * (kParts * G::kVtBytes);
                     const float *weight = tables[u % kTables].weight + w % G::kFills * kPart;
                     const int valid = it.n - i * C - w % G::kFills * kPart;
+                    uint32_t rests = 0;
                     // eight lanes to a row of 64 elements
-#pragma unroll 2
+#pragma unroll 1
                     for (int x = 0; x < kPart / (4 * kWeighWarps); ++x) {
                         const int row = vw * (kPart / kWeighWarps) + x * 4 + lane / 8;
                         const uint32_t off = sw128_offset(row, lane % 8);
@@ -768,9 +825,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                         split(in.y, part[0].y, part[1].y, part[2].y);
                         split(in.z, part[0].z, part[1].z, part[2].z);
                         split(in.w, part[0].w, part[1].w, part[2].w);
+                        // (the rest of an infinity or a NaN is a NaN)
+                        rests |= part[2].x | part[2].y;
+                        rests |= part[2].z | part[2].w;
 #pragma unroll
                         for (int n = 0; n < kParts; ++n)
                             *reinterpret_cast<uint4 *>(vt + n * G::kVtBytes + off) = part[n];
+                    }
+                    if (__builtin_expect(finite2(rests) != rests, 0)) {
+                        // There may be one (the rests of values from 2^17 on, or-ed, can look like
+                        // it too): P V meets a 0 in its place, see late_columns.
+#pragma unroll 1
+                        for (int x = 0; x < kPart / (4 * kWeighWarps); ++x) {
+                            const int row = vw * (kPart / kWeighWarps) + x * 4 + lane / 8;
+                            uint32_t *at = reinterpret_cast<uint32_t *>(v + sw128_offset(row, lane % 8));
+#pragma unroll 1
+                            for (int e = 0; e < 4; ++e)
+                                if (finite2(at[e]) != at[e]) {
+                                    at[e] = finite2(at[e]);
+                                    ctl->odd = 1;
+                                }
+                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -1018,6 +1093,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     if (*abort_flag && tid == 0) flag_status(p.status, PA_DEV_WAIT_TIMEOUT);
     if (warp == kWarpQK) tmem_dealloc(tmem, G::kTmemCols);
+    if (ctl->odd && !*abort_flag) late_columns<D, C>(p, rank, size);
 }
 
 namespace {
