@@ -1418,8 +1418,10 @@ int pa_linear_attention(const void *q, int64_t q_stride, const void *k, int64_t 
     p.num_slots = desc->num_slots;
     p.scale = desc->scale;
     p.status = dev->status;
-    const bool prompts = num_tokens > kLinearStepRows;
-    p.max_rows = prompts ? kLinearStepRows : 0x7fffffff;
+    const int step_rows = linear_step_rows(
+        d, p.group, static_cast<int64_t>(num_seqs) * hkv * (d / 64), dev->sms);
+    const bool prompts = num_tokens > step_rows;
+    p.max_rows = prompts ? step_rows : 0x7fffffff;
     p.chunk = p.group == 1 ? kLinearTileRows : kLinearTileRows / 2;
     p.test_stall = g_test_stall.load(std::memory_order_relaxed) == PA_TEST_STALL_LINEAR ? 1 : 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

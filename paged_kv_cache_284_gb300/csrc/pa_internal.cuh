@@ -364,11 +364,24 @@ struct LinearParams {
     int test_stall;      // test hook: CTA 0's loads stop after one chunk
 };
 // Requests of up to this many tokens take the recurrent form, whose time grows with a request's
-// tokens; the chunks' is that of 64 from the first on.  head_dim 128, 32 / 8 heads, recurrent and
-// in chunks: one request of 8 tokens 10.4 and 9.8 us, of 16 18.3 and 9.9; 64 requests of 8
-// 37 and 47 us, of 10 47 and 47, of 16 69 and 49 (the chunks on every SM); 128 of 8 in head_dim
-// 64 15 and 13.
-constexpr int kLinearStepRows = 8;
+// tokens and with its heads to a group; a chunk takes as long with 9 tokens as with 64, but has
+// its operands' shared memory and the tensor cores to itself.  So few requests go to the chunks from
+// 9 tokens on, and those that fill the SMs more than once (a state's 64 columns to a CTA) later.
+// As launched, the same requests in the recurrent form / in chunks, us:
+//   head_dim 128, 8 kv heads  groups of 2        of 4               of 8
+//     8 requests of 9                            15.9 / 14.5
+//     64 of 12                38.3 / 54.2        50.8 / 58.1        78.4 / 77.9
+//     64 of 16                46.6 / 50.8        63.1 / 54.8        103.6 / 72.5
+//     200 (256) of 12         108 / 165          (194 / 225)        240 / 234
+//   groups of 16, 1 kv head: 128 requests of 6 34, of 8 44, in chunks 35; 256 of 8 58 and 65
+//   head_dim 64, 200 requests, 16 / 16 heads: of 12 96 / 140, of 16 120 / 128;
+//     16 / 8: of 9 49 / 68, of 12 60 / 61; 8 / 2 (128 requests): of 9 18.2 / 15.2
+constexpr int kLinearFewRows = 8;
+inline int linear_step_rows(int head_dim, int group, int64_t slices, int sms) {
+    if (slices <= sms) return kLinearFewRows;
+    if (head_dim == 128) return group <= 2 ? 16 : group <= 8 ? 12 : kLinearFewRows;
+    return group == 1 ? 12 : kLinearFewRows;
+}
 // Rows (tokens x heads) of the prompt kernel's query tiles: chunks of 64 tokens and two heads of
 // a group, or of 128 tokens where a group is one head.
 constexpr int kLinearTileRows = 128;

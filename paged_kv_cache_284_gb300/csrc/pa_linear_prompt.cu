@@ -1130,15 +1130,19 @@ int launch(const LinearParams &p, const CUtensorMap &tq, const CUtensorMap &tk,
            2 * size * items <= (size < 4 ? sms * 18 / 19 : sms * 15 / 19))
         size *= 2;
     // Which requests are long is known on the GPU only, so the two forms' SMs are shared out by
-    // what T tokens and B states would take: reading and writing a state takes an SM about as
-    // long as 24 tokens of a prompt (head_dim 128, four heads a group: 28 us and 1.1 us for 8 kv
-    // heads).  256 single tokens, without any prompt: 47.6 us, 60 with a prompt CTA on every SM.
-    // Above kLinearStepRows tokens on average some request is long, and all may be, of one short
-    // chunk each, which takes as long as a full one: tokens count four times then.  8 x 512 tokens
-    // among 224 requests of 1 and 5 take 75.7 / 79.2 / 80.5 us with tokens counted once, four and
-    // eight times, 64 requests of 16 96 / 58 / 49, 128 of 32 137 / 96 / 91.
+    // what T tokens and B states would take: reading and writing a state counts as 24 tokens of a
+    // prompt.  (Measured apart an SM takes 35 to 46 times a token's time for it, with 32 kv heads,
+    // either head_dim and groups of 1, 2 and 4 heads, so neither enters.  Counted as 24 / 40, us: 8 x
+    // 512 tokens beside 224 short rows of 32 / 8 heads 78.9 / 77.6, of 16 / 16 126 / 124, of 32 / 8
+    // heads of 64 34.2 / 33.8; 32 x 40 beside 80, of 32 / 8 41.3 / 42.3, of 16 / 16 76 / 80, of 6 / 6 of
+    // 64 15.7 / 16.7.)  256 single tokens, without any prompt: 47.6 us, 60 with a prompt CTA on
+    // every SM.
+    // Above kLinearFewRows tokens on average some request is likely to be long, and all may be, of
+    // one short chunk each, which takes as long as a full one: tokens count four times then.  8 x 512
+    // tokens among 224 requests of 1 and 5 take 75.7 / 79.2 / 80.5 us with tokens counted once, four
+    // and eight times, 64 requests of 16 96 / 58 / 49, 128 of 32 137 / 96 / 91.
     constexpr int64_t kStateTokens = 24;
-    const int64_t work = tokens > int64_t{kLinearStepRows} * p.num_seqs ? 4 * tokens : tokens;
+    const int64_t work = tokens > int64_t{kLinearFewRows} * p.num_seqs ? 4 * tokens : tokens;
     const int share = static_cast<int>(sms * work / (work + kStateTokens * p.num_seqs));
     const int clusters = static_cast<int>(std::min<int64_t>(items, std::max(1, share / size)));
     return size > 1 ? launch<D, C, true>(p, tq, tk, tv, clusters, size, s)
