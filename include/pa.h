@@ -222,7 +222,8 @@ int pa_validate_copies(const int32_t *pairs, int32_t num_pairs, int32_t num_bloc
  * free_state itself.
  * Every block is in the list or in one row's table, once.
  *
- * All or nothing: with too few blocks in the list (PA_DEV_NO_BLOCKS), more tokens than
+ * All or nothing: with too few blocks in the list (PA_DEV_NO_BLOCKS; what finished rows would
+ * give back in the same step does not count), more tokens than
  * num_tokens, a row longer than its table, a negative cached length, or a head or count out
  * of range (PA_DEV_BAD_METADATA) the call changes neither table nor list, takes no row out,
  * and makes a step without tokens: every query start 0, every slot -1, context and seq_lens
@@ -377,6 +378,9 @@ int pa_window_attention(const void *q, const pa_kv_desc *kv, const int32_t *bloc
  * encoder_lens (int32 [num_seqs]) in the place of both lengths.  scale > 0;
  * max_blocks_per_seq * block_size and num_q_tokens must not exceed 2^30.  Table entries past
  * ceil(encoder_len / block_size) are not read, keys past encoder_len may hold anything.
+ * Scores, maxima and sums are fp32.  Before they multiply v, the probabilities are rounded once:
+ * to bf16 over a bf16 pool (and an e4m3 pool's staging copy), to f16 in the split-KV form of an
+ * e4m3 pool; out is rounded to bf16.
  */
 int pa_cross_attention(const void *q, const pa_kv_desc *kv, const int32_t *block_tables,
                        int32_t max_blocks_per_seq, const int32_t *query_start_loc,
@@ -405,12 +409,17 @@ int pa_cross_attention(const void *q, const pa_kv_desc *kv, const int32_t *block
  *                 PA_DEV_BAD_SLOT
  *   out           bf16 [num_tokens][num_q_heads][head_dim], 16-B aligned; rows that belong to
  *                 no request are left untouched; may not overlap an input
- * States and all sums are fp32.  An infinity or a NaN in a request's q, k or v reaches its own
- * state and its outputs from that token on (an infinity in v may reach them as a NaN), one in v
- * those of its column; earlier outputs and other requests' never.  head_dim 64 or 128;
- * num_q_heads a multiple of num_kv_heads, at most 128 heads to a group; num_tokens at most
- * 2^30.  A decreasing query start, or one past num_tokens, skips the request and flags
- * PA_DEV_BAD_METADATA.
+ * States, decays and all sums are fp32, and a state that is left is never rounded to less.
+ * Requests of a few tokens (8; up to 16 where a step's states fill the SMs more than once) are
+ * computed token by token, with one rounding, of out to bf16.  Longer ones go by chunks of 64
+ * or 128 tokens, whose decayed products q k and whose copy of the state before the chunk, which
+ * q meets, are rounded to bf16 once each before they are multiplied and summed.
+ * An infinity or a NaN in a request's q, k or v reaches its own state and its outputs from that
+ * token on (an infinity in v may reach them as a NaN), one in v those of its column; earlier
+ * outputs and other requests' never.
+ * head_dim 64 or 128; num_q_heads a multiple of num_kv_heads, at most 128 heads to a group;
+ * num_tokens at most 2^30.  A decreasing query start, or one past num_tokens, skips the request
+ * and flags PA_DEV_BAD_METADATA.
  */
 typedef struct pa_linear_desc {
     float *state;

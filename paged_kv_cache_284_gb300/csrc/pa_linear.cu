@@ -8,9 +8,10 @@
 // thread has four columns of R rows, and a sum over the rows goes through shared memory, with one
 // barrier for four query heads of a token.
 // Bound for single tokens: HBM, each state read and written once.  256 requests of 8 kv heads of
-// 128: 47 us for 270 MB, 5.7 TB/s.  A warp to eight columns, with the sums over the rows in it
-// and no barrier: 58 us, since its 32-byte pieces of rows take HBM's pages badly; and 64 x 5
-// tokens 31 us instead of 27, where the sums' steps, not the barriers, are what is waited for.
+// 128: 48.5 us a call for 270 MB, 5.6 TB/s, of which the prompts' grid beside it, which finds none,
+// is one.  A warp to eight columns, with the sums over the rows in it and no barrier, took 58 us
+// where this form took 47, since its 32-byte pieces of rows take HBM's pages badly; and 64 x 5 tokens
+// 31 us instead of 27, where the sums' steps, not the barriers, are what is waited for.
 #include <algorithm>
 
 #include "pa_internal.cuh"
