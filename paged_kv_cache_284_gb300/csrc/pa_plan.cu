@@ -243,21 +243,27 @@ __global__ void __launch_bounds__(kT) plan_kernel(PlanParams p) {
     // staging blocks in request order while they fit (a request that does
     // not fit, and every later one, runs as split-KV pieces instead).
     int staged = 0, staged_blocks = 0;
+    // (Lengths are not checked yet, so blocks are counted in 64 bits and no further than the area
+    // goes: a sum that wrapped would give places outside it.)
     if (p.fp8 && p.stage_cap > 0) {
-        int cand_base = 0;
+        long long cand_base = 0;
         for (int b0 = 0; b0 < p.num_seqs; b0 += kT) {
             const int b = b0 + tid;
             int cnt = 0;
             if (b < p.num_seqs) {
                 const int n = p.qsl[b + 1] - p.qsl[b], len = p.seq_lens[b];
                 if (n > 0 && len > 0 && static_cast<long long>(n) * p.group > p.short_max_rows)
-                    cnt = (len + p.block_size - 1) / p.block_size;
+                    cnt = min((len - 1) / p.block_size, p.stage_cap) + 1;
             }
-            int tot_c, tot_s;
-            const int base = cand_base + block_exclusive_scan<kT>(cnt, tmp, &tot_c);
+            // in halves, whose sums over a block's threads fit an int (cnt <= 2^28 + 1)
+            constexpr int kHalf = 14;
+            int lo, hi, tot_lo, tot_hi, tot_s;
+            block_exclusive_scan2<kT>(cnt & ((1 << kHalf) - 1), cnt >> kHalf, tmp, lo, hi, tot_lo, tot_hi);
+            const long long base = cand_base + (static_cast<long long>(hi) << kHalf) + lo;
+            const long long tot_c = (static_cast<long long>(tot_hi) << kHalf) + tot_lo;
             const bool fits = cnt > 0 && base + cnt <= p.stage_cap;
             const int idx = staged + block_exclusive_scan<kT>(fits ? 1 : 0, tmp, &tot_s);
-            if (b < p.num_seqs) p.stage_base[b] = fits ? base : -1;
+            if (b < p.num_seqs) p.stage_base[b] = fits ? static_cast<int>(base) : -1;
             if (fits) p.stage_list[idx] = b;
             staged_blocks += static_cast<int>(block_sum_ll<kT>(fits ? cnt : 0, tmpl));
             cand_base += tot_c;
